@@ -329,6 +329,91 @@ moe_status moe_debug_inject(moe_layer* layer, uint32_t faults);
 moe_status moe_profile_enable(moe_layer* layer, int32_t enable);
 moe_status moe_profile_read(moe_layer* layer, float* stage_ms, int32_t n_stages);
 
+/* ---------------------------------------------------------------- dense operators
+ * What a transformer block runs next to the expert layer: the residual norm
+ * that opens it, and the projections of a dense (non-expert) FFN on the same
+ * number formats.  None of them needs a workspace or allocates, all may be
+ * captured into a CUDA graph, and all sizes may be ragged: no count has to be
+ * a multiple of anything.
+ *
+ * E4M3 activations: codes q[row][col] with a row stride of ldq bytes (a
+ * multiple of 16; q 16-byte aligned), and one scale per row and 128 columns,
+ * K-block-major: s[col / 128][row] with a stride of lds scales between blocks.
+ * Value = E4M3(q) * s.  Scales are fp32, or powers of two in eight bits
+ * (E8M0: 2^(b - 127), 255 is NaN).  A producer writes s = amax/448 of the 128
+ * columns (E8M0: the smallest power of two not below that), or 1 where
+ * amax/448 is below 2^-126; NaN and infinity are not hidden: they make the
+ * group's scale NaN or infinite and its codes NaN. */
+typedef enum { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
+typedef enum { MOE_SCALE_F32 = 0, MOE_SCALE_E8M0 = 1 } moe_scale_type;
+
+typedef struct {
+    uint8_t* q;                  /* [rows][ldq] E4M3FN                          */
+    void* s;                     /* [ceil(cols / 128)][lds] fp32 or E8M0        */
+    int64_t ldq;
+    int64_t lds;
+    int32_t scale_type;          /* moe_scale_type                              */
+    int32_t reserved;
+} moe_fp8_matrix;
+
+/* v = x + res (fp32, not rounded); res_out = v rounded to res_type;
+ * n = v * rsqrt(mean(v^2) + eps) * weight; y = n rounded to x_type;
+ * out = n quantised (from fp32 n, not from y).  res may be NULL (no addition;
+ * then no res_out); each output may be NULL (out: q and s NULL), one at least
+ * is given.  res_out may be res, and y may be x (same strides).  Types: x
+ * bf16 with res bf16 or fp32, or both fp32.  Strides ld* count elements.
+ * Rows whose operands all lie on 16-byte boundaries are moved 16 bytes at a
+ * time, others element by element. */
+#define MOE_RMSNORM_MAX_COLS 32768
+typedef struct {
+    int32_t rows, cols;
+    int32_t x_type, res_type;    /* moe_dtype                                   */
+    const void* x;    int64_t ldx;
+    const void* res;  int64_t ld_res;
+    const float* weight;         /* [cols] fp32                                 */
+    void* res_out;    int64_t ld_res_out;
+    void* y;          int64_t ldy;
+    moe_fp8_matrix out;
+    float eps;
+    int32_t reserved;
+} moe_rmsnorm_args;
+moe_status moe_add_rmsnorm(const moe_rmsnorm_args* args, void* stream);
+
+/* Weights of a dense FP8 projection, copied into the library's tile layout
+ * once; the caller may free its buffers afterwards.  Row-major E4M3FN
+ * [out_features][in_features] with one scale per 128 x 128 block,
+ * [ceil(out / 128)][ceil(in / 128)].  gated: w, s are the gate matrix and
+ * w_up, s_up the up matrix of the same shape. */
+#define MOE_LINEAR_MAX_FEATURES (1 << 20)
+typedef struct moe_linear moe_linear;    /* opaque; owned by the library */
+typedef struct {
+    int32_t in_features, out_features;
+    int32_t gated;               /* 0 or 1                                      */
+    int32_t scale_type;          /* of the weights and of every activation      */
+} moe_linear_desc;
+typedef struct {
+    const uint8_t* w;
+    const void* s;
+    const uint8_t* w_up;         /* gated only                                  */
+    const void* s_up;
+} moe_linear_weights;
+moe_status moe_linear_create(const moe_linear_desc* desc, const moe_linear_weights* w, void* stream, moe_linear** out);
+moe_status moe_linear_destroy(moe_linear* linear);   /* synchronises the device first */
+
+/* y[m][n] = sum over K blocks of s_a * s_w * (sum over 128 channels of the
+ * codes' products), fp32, rounded once to y_type (moe_dtype).  a: [rows][in].
+ * y: row stride ldy elements.  rows = 0 is a valid no-op. */
+moe_status moe_linear_forward(moe_linear* linear, const moe_fp8_matrix* a, int32_t rows, void* y, int64_t ldy,
+                              int32_t y_type, void* stream);
+
+/* h = SiLU(a Wg^T) * (a Wu^T), quantised to E4M3 per 128 features as it is
+ * produced.  h must not overlap a. */
+moe_status moe_gated_linear_forward(moe_linear* linear, const moe_fp8_matrix* a, int32_t rows, const moe_fp8_matrix* h,
+                                    void* stream);
+
+/* As moe_get_device_status, for a projection's kernels. */
+moe_status moe_linear_device_status(moe_linear* linear, void* stream, uint32_t* flags);
+
 const char* moe_status_string(moe_status s);
 const char* moe_last_error(void);   /* thread-local; "" when none */
 int32_t moe_abi_version(void);

@@ -25,11 +25,16 @@ __all__ = [
     "moe_abi_version", "moe_forward_smallep", "moe_forward_deferred", "moe_layers_workspace_bytes",
     "moe_forward_layers", "smallep_groups", "moe_create_ex", "moe_tiles_bytes", "moe_tiles_load", "moe_forward_tiles",
     "CREATE_HOST_TILES", "library_path", "load", "Layer", "LayerStackGraph", "StreamedStack",
+    "MoeFp8Matrix", "MoeRmsnormArgs", "MoeLinearDesc", "MoeLinearWeights", "BF16", "F32", "SCALE_F32", "SCALE_E8M0",
+    "moe_add_rmsnorm", "moe_linear_create", "moe_linear_destroy", "moe_linear_forward", "moe_gated_linear_forward",
+    "moe_linear_device_status", "Fp8Tensor", "RmsNorm", "Fp8Linear", "Fp8GatedLinear", "DenseFfn",
 ]
 
 MODE_ROUTE, MODE_PREFILL, MODE_DECODE = 0, 1, 2
 CREATE_HOST_TILES = 1
 DECODE_MAX_T = 64
+BF16, F32 = 0, 1
+SCALE_F32, SCALE_E8M0 = 0, 1
 MOE_OK = 0
 DEV_BAD_EXPERT_ID, DEV_BAD_ROW, DEV_WAIT_TIMEOUT = 0x1, 0x2, 0x4
 
@@ -53,6 +58,27 @@ class MoeWeights(ctypes.Structure):
 class MoeRouteOut(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "logits", "topk_ids", "topk_w", "expert_offsets", "sorted_token", "inv_row", "xq", "sx", "hq", "sh")]
+
+
+class MoeFp8Matrix(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("lds", ctypes.c_int64),
+                ("scale_type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class MoeRmsnormArgs(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("x_type", ctypes.c_int32),
+                ("res_type", ctypes.c_int32), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("res", ctypes.c_void_p), ("ld_res", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("res_out", ctypes.c_void_p), ("ld_res_out", ctypes.c_int64), ("y", ctypes.c_void_p),
+                ("ldy", ctypes.c_int64), ("out", MoeFp8Matrix), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class MoeLinearDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("in_features", "out_features", "gated", "scale_type")]
+
+
+class MoeLinearWeights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w", "s", "w_up", "s_up")]
 
 
 _lock = threading.Lock()
@@ -105,6 +131,13 @@ def load(build_if_missing: bool = False):
             "moe_forward_layers": ([ctypes.POINTER(vp), i32, i32, vp, i32, vp, vp, sz, vp], st),
             "moe_profile_enable": ([vp, i32], st),
             "moe_profile_read": ([vp, ctypes.POINTER(ctypes.c_float), i32], st),
+            "moe_add_rmsnorm": ([ctypes.POINTER(MoeRmsnormArgs), vp], st),
+            "moe_linear_create": ([ctypes.POINTER(MoeLinearDesc), ctypes.POINTER(MoeLinearWeights), vp,
+                                   ctypes.POINTER(vp)], st),
+            "moe_linear_destroy": ([vp], st),
+            "moe_linear_forward": ([vp, ctypes.POINTER(MoeFp8Matrix), i32, vp, ctypes.c_int64, i32, vp], st),
+            "moe_gated_linear_forward": ([vp, ctypes.POINTER(MoeFp8Matrix), i32, ctypes.POINTER(MoeFp8Matrix), vp], st),
+            "moe_linear_device_status": ([vp, vp, ctypes.POINTER(u32)], st),
             "moe_status_string": ([st], ctypes.c_char_p),
             "moe_last_error": ([], ctypes.c_char_p),
             "moe_abi_version": ([], i32),
@@ -293,6 +326,36 @@ def moe_profile_read(layer: int):
     return dict(zip(PROFILE_STAGES, [float(v) for v in buf]))
 
 
+def moe_add_rmsnorm(args: MoeRmsnormArgs, stream: int = 0) -> None:
+    _check(load().moe_add_rmsnorm(ctypes.byref(args), stream))
+
+
+def moe_linear_create(desc: MoeLinearDesc, weights: MoeLinearWeights, stream: int = 0) -> int:
+    h = ctypes.c_void_p()
+    _check(load().moe_linear_create(ctypes.byref(desc), ctypes.byref(weights), stream, ctypes.byref(h)))
+    return h.value
+
+
+def moe_linear_destroy(linear: int) -> None:
+    _check(load().moe_linear_destroy(linear))
+
+
+def moe_linear_forward(linear: int, a: MoeFp8Matrix, rows: int, y: int, ldy: int, y_type: int,
+                       stream: int = 0) -> None:
+    _check(load().moe_linear_forward(linear, ctypes.byref(a), rows, y, ldy, y_type, stream))
+
+
+def moe_gated_linear_forward(linear: int, a: MoeFp8Matrix, rows: int, h: MoeFp8Matrix, stream: int = 0) -> None:
+    _check(load().moe_gated_linear_forward(linear, ctypes.byref(a), rows, ctypes.byref(h), stream))
+
+
+def moe_linear_device_status(linear: int, stream: int = 0):
+    """Returns (status, flags) without raising, so callers can inspect both."""
+    f = ctypes.c_uint32()
+    st = load().moe_linear_device_status(linear, stream, ctypes.byref(f))
+    return int(st), int(f.value)
+
+
 # ---------------------------------------------------------------- torch convenience
 
 class Layer:
@@ -413,3 +476,234 @@ class StreamedStack:
             moe_forward_tiles(self.layers[l].handle, self.mode, self.slots[s].data_ptr(), src.data_ptr(), T,
                               dst.data_ptr(), self.ws.data_ptr(), self.ws.numel(), comp.cuda_stream)
             self.done[s].record(comp)
+
+
+# ---------------------------------------------------------------- dense operators (torch convenience)
+
+MOE_ERR_INVALID_ARG = 1
+_SCALES = {"f32": SCALE_F32, "e8m0": SCALE_E8M0}
+
+
+def _bad(message: str):
+    raise MoeError(MOE_ERR_INVALID_ARG, message)
+
+
+def _stream(device) -> int:
+    """The current torch stream's handle; the tensors' device has to be current."""
+    import torch
+    if device.index != torch.cuda.current_device():
+        _bad(f"the tensors are on {device}, which is not the current device")
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _dtype_code(t, what: str) -> int:
+    import torch
+    if t.dtype is torch.bfloat16:
+        return BF16
+    if t.dtype is torch.float32:
+        return F32
+    _bad(f"{what} must be bfloat16 or float32, not {t.dtype}")
+
+
+def _rows_of(t, rows: int, cols: int, what: str) -> int:
+    """Row stride of a [rows][cols] tensor with contiguous rows."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        _bad(f"{what} must be [{rows}][{cols}], not {list(t.shape)}")
+    if not t.is_cuda:
+        _bad(f"{what} must be a CUDA tensor")
+    if cols > 1 and t.stride(1) != 1:
+        _bad(f"{what} must have contiguous rows")
+    return max(t.stride(0), cols) if rows <= 1 else t.stride(0)
+
+
+class Fp8Tensor:
+    """E4M3 activations with 1x128 scales: value = q * s[column // 128].
+
+    q: float8_e4m3fn [rows][cols] (row stride a multiple of 16); s:
+    [ceil(cols / 128)][rows], float32 (scale="f32") or float8_e8m0fnu
+    (scale="e8m0").  matrix is the C ABI's view of both."""
+
+    def __init__(self, rows: int, cols: int, scale: str = "f32", device=None):
+        import torch
+        if scale not in _SCALES:
+            _bad(f"scale must be one of {sorted(_SCALES)}, not {scale!r}")
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+        ldq = (cols + 15) // 16 * 16
+        q = torch.empty(rows, ldq, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)[:, :cols]
+        s = (torch.empty((cols + 127) // 128, rows, dtype=torch.float32, device=device) if scale == "f32" else
+             torch.empty((cols + 127) // 128, rows, dtype=torch.uint8, device=device).view(torch.float8_e8m0fnu))
+        self._bind(q, s, scale, ldq, rows)
+
+    def _bind(self, q, s, scale, ldq, lds):
+        self.rows, self.cols, self.scale, self.q, self.s = q.shape[0], q.shape[1], scale, q, s
+        self.device = q.device
+        self.matrix = MoeFp8Matrix(q.data_ptr(), s.data_ptr(), ldq, lds, _SCALES[scale], 0)
+
+    @classmethod
+    def from_parts(cls, q, s):
+        """Wrap codes and scales that exist already; codes whose rows do not
+        lie on 16-byte strides are copied."""
+        import torch
+        if q.dim() != 2 or q.dtype is not torch.float8_e4m3fn or not q.is_cuda:
+            _bad("q must be a two-dimensional float8_e4m3fn CUDA tensor")
+        scale = {torch.float32: "f32", torch.float8_e8m0fnu: "e8m0"}.get(s.dtype)
+        rows, cols = q.shape
+        if scale is None or s.device != q.device or list(s.shape) != [(cols + 127) // 128, rows]:
+            _bad(f"s must be float32 or float8_e8m0fnu [{(cols + 127) // 128}][{rows}] beside q")
+        if (cols > 1 and q.stride(1) != 1) or (rows > 1 and (q.stride(0) % 16 or q.stride(0) < cols)) or q.data_ptr() % 16:
+            wide = torch.zeros(rows, (cols + 15) // 16 * 16, dtype=torch.uint8, device=q.device)
+            wide[:, :cols] = q.view(torch.uint8)
+            q = wide.view(torch.float8_e4m3fn)[:, :cols]
+        if (rows > 1 and s.stride(1) != 1) or (s.shape[0] > 1 and s.stride(0) < rows):
+            s = s.contiguous()
+        t = cls.__new__(cls)
+        t._bind(q, s, scale, q.stride(0) if rows > 1 else (cols + 15) // 16 * 16,
+                s.stride(0) if s.shape[0] > 1 else rows)
+        return t
+
+    def dequantise(self):
+        """The values the codes stand for, fp32."""
+        return self.q.float() * self.s.float().t().repeat_interleave(128, 1)[:, :self.cols]
+
+
+class RmsNorm:
+    """v = x + residual; n = v * rsqrt(mean(v^2) + eps) * weight.
+
+    Calling it writes whichever outputs are given: res_out (v, in the
+    residual's type; may be the residual itself), y (n, in x's type) and out
+    (n quantised, an Fp8Tensor)."""
+
+    def __init__(self, weight, eps: float = 1e-6):
+        import torch
+        if weight.dim() != 1 or not weight.is_cuda:
+            _bad("weight must be a one-dimensional CUDA tensor")
+        self.weight = weight.to(torch.float32).contiguous()
+        self.eps, self.cols = float(eps), weight.shape[0]
+        self._w = self.weight.data_ptr()
+
+    def __call__(self, x, residual=None, out=None, res_out=None, y=None):
+        cols, dev = self.cols, x.device
+        if x.dim() != 2 or x.shape[1] != cols or dev != self.weight.device:
+            _bad(f"x must be [rows][{cols}] on the weight's device")
+        rows = x.shape[0]
+        xt = _dtype_code(x, "x")
+        a = MoeRmsnormArgs(rows, cols, xt, xt, x.data_ptr(), _rows_of(x, rows, cols, "x"))
+        if residual is not None:
+            a.res_type = _dtype_code(residual, "residual")
+            a.res, a.ld_res = residual.data_ptr(), _rows_of(residual, rows, cols, "residual")
+            if residual.device != dev:
+                _bad("residual is on another device")
+        a.weight, a.eps = self._w, self.eps
+        if res_out is not None:
+            if residual is None or res_out.dtype is not residual.dtype or res_out.device != dev:
+                _bad("res_out needs a residual of its type and device")
+            a.res_out, a.ld_res_out = res_out.data_ptr(), _rows_of(res_out, rows, cols, "res_out")
+        if y is not None:
+            if y.dtype is not x.dtype or y.device != dev:
+                _bad("y must have x's type and device")
+            a.y, a.ldy = y.data_ptr(), _rows_of(y, rows, cols, "y")
+        if out is not None:
+            if out.rows != rows or out.cols != cols or out.device != dev:
+                _bad(f"out must be [{rows}][{cols}] on x's device")
+            a.out = out.matrix
+        moe_add_rmsnorm(a, _stream(dev))
+
+
+class _Weights:
+    """Handle of one projection's weights in the library's layout."""
+    gated = False
+
+    def _create(self, mats):
+        import torch
+        w = mats[0][0]
+        for q, s in mats:
+            if q.dim() != 2 or q.dtype is not torch.float8_e4m3fn or q.shape != w.shape or not q.is_cuda:
+                _bad("weights must be float8_e4m3fn [out][in] CUDA tensors of one shape")
+            if s.dtype not in (torch.float32, torch.float8_e8m0fnu) or s.dtype is not mats[0][1].dtype or \
+                    list(s.shape) != [(w.shape[0] + 127) // 128, (w.shape[1] + 127) // 128] or s.device != w.device:
+                _bad("scales must be float32 or float8_e8m0fnu, one per 128 x 128 block")
+        keep = [t.contiguous() for m in mats for t in m]
+        self.out_features, self.in_features = w.shape
+        self.scale = "f32" if mats[0][1].dtype is torch.float32 else "e8m0"
+        self.device = w.device
+        self.handle = None
+        self.handle = moe_linear_create(MoeLinearDesc(self.in_features, self.out_features, int(self.gated), _SCALES[self.scale]),
+                                        MoeLinearWeights(*[t.data_ptr() for t in keep]), _stream(w.device))
+
+    def _check_a(self, a):
+        if a.cols != self.in_features or a.scale != self.scale or a.device != self.device:
+            _bad(f"a must be [rows][{self.in_features}] with {self.scale} scales on the weights' device")
+
+    def device_status(self):
+        return moe_linear_device_status(self.handle, _stream(self.device))
+
+    def close(self):
+        if getattr(self, "handle", None):
+            moe_linear_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Fp8Linear(_Weights):
+    """y = a W^T with block-scaled E4M3 on both sides.  w: float8_e4m3fn
+    [out][in]; s: one scale per 128 x 128 block, float32 or float8_e8m0fnu.
+    The library keeps its own copy."""
+
+    def __init__(self, w, s):
+        self._create([(w, s)])
+
+    def __call__(self, a: Fp8Tensor, y):
+        self._check_a(a)
+        ldy = _rows_of(y, a.rows, self.out_features, "y")
+        if y.device != self.device:
+            _bad("y is on another device")
+        moe_linear_forward(self.handle, a.matrix, a.rows, y.data_ptr(), ldy, _dtype_code(y, "y"), _stream(self.device))
+        return y
+
+
+class Fp8GatedLinear(_Weights):
+    """h = SiLU(a Wg^T) * (a Wu^T), written as an Fp8Tensor."""
+    gated = True
+
+    def __init__(self, w_gate, s_gate, w_up, s_up):
+        self._create([(w_gate, s_gate), (w_up, s_up)])
+
+    def __call__(self, a: Fp8Tensor, h: Fp8Tensor):
+        self._check_a(a)
+        if h.rows != a.rows or h.cols != self.out_features or h.scale != self.scale or h.device != self.device:
+            _bad(f"h must be [{a.rows}][{self.out_features}] with {self.scale} scales on the weights' device")
+        moe_gated_linear_forward(self.handle, a.matrix, a.rows, h.matrix, _stream(self.device))
+        return h
+
+
+class DenseFfn:
+    """The dense FFN half of a pre-norm block, for up to max_rows tokens:
+
+        residual += x;  y = down(SiLU(gate(n)) * up(n)),  n = norm(residual)
+
+    The residual is updated in place; the caller adds y to it with the next
+    norm.  The intermediate E4M3 buffers are kept between calls, so calls of
+    one object belong on one stream at a time."""
+
+    def __init__(self, norm: RmsNorm, gate_up: Fp8GatedLinear, down: Fp8Linear):
+        if gate_up.in_features != norm.cols or down.in_features != gate_up.out_features or gate_up.scale != down.scale:
+            _bad("norm, gate_up and down do not fit together")
+        self.norm, self.gate_up, self.down = norm, gate_up, down
+        self._buf = {}
+
+    def buffers(self, rows: int):
+        if rows not in self._buf:
+            self._buf = {rows: (Fp8Tensor(rows, self.norm.cols, self.gate_up.scale, self.gate_up.device),
+                                Fp8Tensor(rows, self.gate_up.out_features, self.gate_up.scale, self.gate_up.device))}
+        return self._buf[rows]
+
+    def __call__(self, x, residual, y):
+        a, h = self.buffers(x.shape[0])
+        self.norm(x, residual, out=a, res_out=residual)
+        self.gate_up(a, h)
+        return self.down(h, y)

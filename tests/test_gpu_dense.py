@@ -1,0 +1,448 @@
+"""The dense operators on the GPU (residual RMS norm with E4M3 output, FP8
+linear and gated projections) against plain 64-bit forms of their definitions.
+
+Tolerances, derived from the arithmetic (u = 2^-24, half an fp32 ulp):
+
+- norm: x + r rounds once (u).  The sum of squares is a sum of at most 64 terms
+  per thread and a tree of 10 levels: its relative error is below 80 u, its
+  square root halves that, and the reciprocal, the two products and the square
+  root add 5 u: 45 u < 3e-6 relative on n.  Outputs add half a step of their type.
+- GEMM: a 128-channel partial is four MMAs whose aligned sums lose at most a few
+  fp32 units of the largest term; the scaling and the fp32 sum over kt blocks add
+  (kt + 2) u: (kt + 16) 2^-23 of the sum of magnitudes.
+- codes: half an E4M3 step of the quotient, 2^-4 relative for normal codes and
+  2^-10 absolute below them, plus the quotient's own error.
+"""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16_HALF = 2.0 ** -8          # half a step of a type with 8 significant bits, relative to the smallest value of a binade
+N_REL = 3e-6
+
+
+@pytest.fixture(scope="module")
+def moe():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import moe_expert_ffn_02_gb300 as m
+    m.load()
+    return m
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(shape, seed, scale=1.0, dtype=torch.float32):
+    return (torch.randn(shape, generator=gen(seed), device="cuda") * scale).to(dtype)
+
+
+def pad128(v, dim):
+    short = -v.shape[dim] % 128
+    if not short:
+        return v
+    shape = list(v.shape)
+    shape[dim] = short
+    return torch.cat([v, torch.zeros(shape, dtype=v.dtype, device=v.device)], dim)
+
+
+def scale64(amax, scale):
+    s = amax / 448
+    if scale == "e8m0":
+        s = torch.exp2(torch.ceil(torch.log2(s)))
+    return torch.where(amax / 448 < 2.0 ** -126, torch.ones_like(s), s)
+
+
+def e8m0(s):
+    return (torch.log2(s.double()).round() + 127).to(torch.uint8).view(torch.float8_e8m0fnu)
+
+
+def rows_fp8(v, scale):
+    """[rows][cols] -> codes and scales [groups][rows], made in 64 bits."""
+    g = pad128(v.double(), 1).view(v.shape[0], -1, 128)
+    s = scale64(g.abs().amax(-1), scale)
+    if scale == "f32":
+        s = s.float().double()
+    q = (g / s[..., None]).reshape(v.shape[0], -1)[:, :v.shape[1]].float().clamp(-448, 448).to(torch.float8_e4m3fn)
+    return q.contiguous(), (s.float().t().contiguous() if scale == "f32" else e8m0(s.t().contiguous()))
+
+
+def blocks_fp8(w, scale):
+    b = pad128(pad128(w.double(), 0), 1)
+    b = b.view(b.shape[0] // 128, 128, -1, 128)
+    s = scale64(b.abs().amax((1, 3)), scale)
+    if scale == "f32":
+        s = s.float().double()
+    q = (b / s[:, None, :, None]).reshape(b.shape[0] * 128, -1)[:w.shape[0], :w.shape[1]]
+    return q.float().clamp(-448, 448).to(torch.float8_e4m3fn).contiguous(), (s.float() if scale == "f32" else e8m0(s))
+
+
+def wide_rows(q, s):
+    return q.double() * s.double().t().repeat_interleave(128, 1)[:, :q.shape[1]]
+
+
+def wide_blocks(q, s):
+    return q.double() * s.double().repeat_interleave(128, 0)[:q.shape[0]].repeat_interleave(128, 1)[:, :q.shape[1]]
+
+
+def check_codes(q, s, want, slack, scale):
+    """q * s against the 64-bit values `want`, each known to within `slack`."""
+    rows, cols = want.shape
+    sd = s.double()
+    amax = pad128(want.abs(), 1).view(rows, -1, 128).amax(-1).t()
+    loose = pad128(slack.expand(rows, cols), 1).view(rows, -1, 128).amax(-1).t()
+    if scale == "f32":
+        ref = scale64(amax, scale)
+        assert ((sd - ref).abs() <= loose / 448 + ref * 2.0 ** -22).all()
+    else:
+        lo, hi = scale64((amax - loose).clamp_min(0) * (1 - 2.0 ** -22), scale), scale64((amax + loose) * (1 + 2.0 ** -22), scale)
+        assert ((sd == lo) | (sd == hi)).all()
+    wide = sd.t().repeat_interleave(128, 1)[:, :cols]
+    quot = want / wide
+    err = (q.double() - quot).abs()
+    tol = torch.maximum(quot.abs() * 2.0 ** -4, torch.full_like(quot, 2.0 ** -10)) + slack / wide + quot.abs() * 2.0 ** -22
+    assert (err <= tol).all(), float((err - tol).max())
+
+
+# ------------------------------------------------------------------ norm
+
+def norm64(x, r, w, eps):
+    v = x.double() + (r.double() if r is not None else 0)
+    return v, v / torch.sqrt(v.square().mean(-1, keepdim=True) + eps) * w.double()
+
+
+def check_norm(moe, x, r, w, scale, eps=1e-6, in_place=False):
+    rows, cols = x.shape
+    norm = moe.RmsNorm(w, eps)
+    out = moe.Fp8Tensor(rows, cols, scale)
+    y = torch.empty_like(x)
+    v, n = norm64(x, r, w, eps)
+    ro = None if r is None else (r if in_place else torch.empty_like(r))
+    norm(x, r, out=out, res_out=ro, y=y)
+    if r is not None:
+        half = 0 if r.dtype is torch.float32 else BF16_HALF
+        assert ((ro.double() - v).abs() <= v.abs() * (half + 2.0 ** -23)).all()
+    half = 0 if x.dtype is torch.float32 else BF16_HALF
+    assert ((y.double() - n).abs() <= n.abs() * (half + N_REL) + 1e-38).all()
+    check_codes(out.q, out.s, n, n.abs() * N_REL, scale)
+    return out, y, ro
+
+
+@pytest.mark.parametrize("types", ["bf16/bf16", "bf16/f32", "f32/f32", "bf16/-", "f32/-"])
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 7168), (3, 127), (2, 128), (5, 129), (17, 1000), (4, 7176), (300, 256),
+                                       (2, 16384), (1, 32768), (2, 20001)])
+def test_norm_against_64_bits(moe, types, scale, rows, cols):
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}
+    tx, tr = types.split("/")
+    x = randn((rows, cols), 1, dtype=dt[tx])
+    r = None if tr == "-" else randn((rows, cols), 2, 4.0, dt[tr])
+    check_norm(moe, x, r, 1 + randn((cols,), 3, 0.2), scale)
+
+
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+def test_norm_strides_and_alignment(moe, scale):
+    """Rows inside wider, unaligned storage; only the rows' own elements are written."""
+    store = randn((9, 517), 4, dtype=torch.bfloat16)
+    x, rs = store[:, 3:503], randn((9, 640), 5, dtype=torch.float32)
+    w = 1 + randn((501,), 6, 0.2)[1:]
+    before = rs.clone()
+    check_norm(moe, x, rs[:, 8:508], w, scale, in_place=True)
+    keep = torch.ones(640, dtype=torch.bool, device="cuda")
+    keep[8:508] = False
+    assert torch.equal(rs[:, keep], before[:, keep])
+    out = moe.Fp8Tensor(9, 500, scale)
+    guard = out.q.as_strided((9, 512), (512, 1)).view(torch.uint8)
+    guard.fill_(0xA5)
+    moe.RmsNorm(w)(x, out=out)
+    assert (guard[:, 500:] == 0xA5).all()
+
+
+def test_norm_in_place_equals_out_of_place(moe):
+    x, r, w = randn((33, 2048), 7, dtype=torch.bfloat16), randn((33, 2048), 8, 3.0, torch.bfloat16), torch.ones(2048, device="cuda")
+    norm = moe.RmsNorm(w)
+    ro, y = torch.empty_like(r), torch.empty_like(x)
+    norm(x, r, res_out=ro, y=y)
+    x2, r2 = x.clone(), r.clone()
+    norm(x2, r2, res_out=r2, y=x2)
+    assert torch.equal(ro, r2) and torch.equal(y, x2)
+
+
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+def test_norm_zeros_tiny_values_and_non_numbers(moe, scale):
+    cols = 384
+    x = randn((6, cols), 9)
+    x[0] = 0
+    x[1, 128:256] = 0
+    x[2] *= 1e-30
+    w = torch.ones(cols, device="cuda")
+    x[3, 5] = float("nan")
+    x[4, 200] = float("inf")
+    out, y = moe.Fp8Tensor(6, cols, scale), torch.empty_like(x)
+    moe.RmsNorm(w, 0.0)(x[1:2].expand(6, cols).contiguous(), out=out, y=y)          # a zero group: scale 1, zero codes
+    assert (out.s.float()[1] == 1).all() and (out.q.float()[:, 128:256] == 0).all()
+    moe.RmsNorm(w, 1e-6)(x, out=out, y=y)
+    q, s = out.q.float(), out.s.float()
+    assert (q[0] == 0).all() and (s[:, 0] == 1).all()
+    assert torch.isnan(y[3]).all() and torch.isnan(s[:, 3]).all() and torch.isnan(q[3]).all()
+    assert torch.isnan(s[1, 4]) and torch.isnan(y[4, 200]) and (y[4, :128] == 0).all() and (q[4, :128] == 0).all()
+    _, n = norm64(x[5:], None, w, 1e-6)
+    assert ((y[5:].double() - n).abs() <= n.abs() * N_REL).all()
+    tiny = torch.full((1, cols), 2.0 ** -140, device="cuda")                        # amax / 448 has no normal number
+    out1 = moe.Fp8Tensor(1, cols, scale)
+    moe.RmsNorm(w, 1.0)(tiny, out=out1)
+    assert (out1.s.float() == 1).all() and (out1.q.float() == 0).all()
+
+
+def test_norm_offsets_past_32_bits(moe):
+    cols, ld = 256, 2 ** 31 + 64
+    big = torch.empty(ld + cols, dtype=torch.bfloat16, device="cuda")
+    x = big.as_strided((2, cols), (ld, 1))
+    x.copy_(randn((2, cols), 10, dtype=torch.bfloat16))
+    check_norm(moe, x.contiguous(), None, torch.ones(cols, device="cuda"), "f32")
+    y = torch.empty(2, cols, dtype=torch.bfloat16, device="cuda")
+    z = torch.empty_like(y)
+    moe.RmsNorm(torch.ones(cols, device="cuda"))(x, y=y)
+    moe.RmsNorm(torch.ones(cols, device="cuda"))(x.contiguous(), y=z)
+    assert torch.equal(y, z)
+
+
+# ------------------------------------------------------------------ projections
+
+def product64(aq, a_s, wq, w_s):
+    a, w = wide_rows(aq, a_s), wide_blocks(wq, w_s)
+    kt = (aq.shape[1] + 127) // 128
+    return a @ w.t(), (a.abs() @ w.abs().t()) * (kt + 16) * 2.0 ** -23
+
+
+def check_linear(moe, m, k, n, scale, dtype, seed=20):
+    aq, a_s = rows_fp8(randn((m, k), seed), scale)
+    wq, w_s = blocks_fp8(randn((n, k), seed + 1, 0.02), scale)
+    lin = moe.Fp8Linear(wq, w_s)
+    y = lin(moe.Fp8Tensor.from_parts(aq, a_s), torch.full((m, n), float("nan"), dtype=dtype, device="cuda"))
+    want, tol = product64(aq, a_s, wq, w_s)
+    half = 0 if dtype is torch.float32 else BF16_HALF
+    err = (y.double() - want).abs()
+    assert (err <= tol + want.abs() * half + tol * half).all(), float((err - tol).max())
+    assert lin.device_status() == (0, 0)
+    return lin, y
+
+
+ODD = [(1, 1, 1), (1, 128, 16), (2, 100, 17), (7, 127, 127), (8, 129, 128), (9, 256, 129), (31, 1040, 1001), (33, 385, 64),
+       (64, 640, 250), (65, 1000, 96), (127, 513, 333), (128, 128, 256), (129, 1153, 257), (300, 1992, 1001), (1, 7168, 2048),
+       (16, 2048, 7168), (1000, 256, 2500)]
+
+
+@pytest.mark.parametrize("m,k,n", ODD)
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_linear_against_64_bits(moe, m, k, n, scale, dtype):
+    check_linear(moe, m, k, n, scale, dtype)
+
+
+def check_gated(moe, m, k, n, scale, seed=30):
+    aq, a_s = rows_fp8(randn((m, k), seed), scale)
+    g, u = blocks_fp8(randn((n, k), seed + 1, 0.05), scale), blocks_fp8(randn((n, k), seed + 2, 0.05), scale)
+    lin = moe.Fp8GatedLinear(*g, *u)
+    h = moe.Fp8Tensor(m, n, scale)
+    h.q.view(torch.uint8).fill_(0x7F)
+    lin(moe.Fp8Tensor.from_parts(aq, a_s), h)
+    gv, eg = product64(aq, a_s, *g)
+    uv, eu = product64(aq, a_s, *u)
+    silu = gv / (1 + torch.exp(-gv))
+    want = silu * uv
+    # SiLU's slope is at most 1.1; its fast exponential and quotient lose a few ulp, growing with |g|
+    slack = 1.1 * eg * (uv.abs() + eu) + silu.abs() * eu + want.abs() * (4 + gv.abs()) * 2.0 ** -22
+    check_codes(h.q, h.s, want, slack, scale)
+    assert lin.device_status() == (0, 0)
+    return lin, h
+
+
+@pytest.mark.parametrize("m,k,n", [(1, 128, 1), (1, 7168, 2048), (2, 100, 8), (7, 129, 17), (9, 640, 129), (33, 1040, 1000),
+                                   (64, 384, 250), (65, 257, 136), (127, 513, 333), (128, 256, 256), (129, 1153, 200),
+                                   (300, 1992, 1001), (1000, 256, 2500)])
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+def test_gated_against_64_bits(moe, m, k, n, scale):
+    check_gated(moe, m, k, n, scale)
+
+
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+def test_rows_do_not_depend_on_the_batch(moe, scale):
+    """Tile widths follow the batch size; a token's result does not."""
+    m, k, n = 700, 1160, 1400
+    aq, a_s = rows_fp8(randn((m, k), 40), scale)
+    w, u = blocks_fp8(randn((n, k), 41, 0.05), scale), blocks_fp8(randn((n, k), 42, 0.05), scale)
+    lin, gated = moe.Fp8Linear(*w), moe.Fp8GatedLinear(*w, *u)
+    a = moe.Fp8Tensor.from_parts(aq, a_s)
+    y = lin(a, torch.empty(m, n, dtype=torch.float32, device="cuda"))
+    h = gated(a, moe.Fp8Tensor(m, n, scale))
+    for lo, hi in ((0, 1), (5, 25), (100, 150), (200, 328), (300, 560)):
+        part = moe.Fp8Tensor.from_parts(aq[lo:hi].clone(), a_s.view(torch.uint8 if scale == "e8m0" else torch.float32)[:, lo:hi]
+                                        .contiguous().view(a_s.dtype))
+        assert torch.equal(lin(part, torch.empty(hi - lo, n, dtype=torch.float32, device="cuda")), y[lo:hi])
+        hp = gated(part, moe.Fp8Tensor(hi - lo, n, scale))
+        assert torch.equal(hp.q.view(torch.uint8), h.q[lo:hi].view(torch.uint8))
+        assert torch.equal(hp.s.float(), h.s.float()[:, lo:hi])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_linear_output_strides(moe, dtype):
+    """y inside wider storage, at aligned and odd offsets and strides; nothing beside it is written."""
+    m, k, n = 70, 300, 200
+    aq, a_s = rows_fp8(randn((m, k), 50), "f32")
+    lin = moe.Fp8Linear(*blocks_fp8(randn((n, k), 51, 0.05), "f32"))
+    a = moe.Fp8Tensor.from_parts(aq, a_s)
+    ref = lin(a, torch.empty(m, n, dtype=dtype, device="cuda"))
+    for width, off in ((256, 0), (256, 8), (259, 0), (261, 3), (208, 4)):
+        store = torch.full((m, width), 7.0, dtype=dtype, device="cuda")
+        y = lin(a, store[:, off:off + n])
+        assert torch.equal(y, ref)
+        keep = torch.ones(width, dtype=torch.bool, device="cuda")
+        keep[off:off + n] = False
+        assert (store[:, keep] == 7).all()
+
+
+def test_linear_offsets_past_32_bits(moe):
+    m, k, n = 3, 256, 130
+    aq, a_s = rows_fp8(randn((m, k), 60), "f32")
+    lin = moe.Fp8Linear(*blocks_fp8(randn((n, k), 61, 0.05), "f32"))
+    ref = lin(moe.Fp8Tensor.from_parts(aq, a_s), torch.empty(m, n, dtype=torch.bfloat16, device="cuda"))
+    ld = 2 ** 31 + 128
+    big = torch.empty(2 * ld + k, dtype=torch.uint8, device="cuda")
+    wide = big.as_strided((m, k), (ld, 1))
+    wide.copy_(aq.view(torch.uint8))
+    y = lin(moe.Fp8Tensor.from_parts(wide.view(torch.float8_e4m3fn), a_s), torch.empty(m, n, dtype=torch.bfloat16, device="cuda"))
+    assert torch.equal(y, ref)
+    del big, wide
+    out = torch.empty(2 * (2 ** 31 + 3) + n, dtype=torch.bfloat16, device="cuda").as_strided((m, n), (2 ** 31 + 3, 1))
+    assert torch.equal(lin(moe.Fp8Tensor.from_parts(aq, a_s), out), ref)
+
+
+@pytest.mark.parametrize("m", [1, 40, 200])
+def test_non_numbers_stay_in_their_row_and_column(moe, m):
+    k, n = 300, 260
+    aq, a_s = rows_fp8(randn((m, k), 70), "f32")
+    wq, w_s = blocks_fp8(randn((n, k), 71, 0.05), "f32")
+    aq.view(torch.uint8)[m // 2, 299] = 0x7F
+    wq.view(torch.uint8)[77, 3] = 0xFF
+    y = moe.Fp8Linear(wq, w_s)(moe.Fp8Tensor.from_parts(aq, a_s), torch.empty(m, n, dtype=torch.float32, device="cuda"))
+    bad = torch.zeros(m, n, dtype=torch.bool, device="cuda")
+    bad[m // 2] = True
+    bad[:, 77] = True
+    assert torch.equal(torch.isnan(y), bad)
+    h = moe.Fp8GatedLinear(wq, w_s, wq, w_s)(moe.Fp8Tensor.from_parts(aq, a_s), moe.Fp8Tensor(m, n))
+    s = torch.isnan(h.s)
+    assert s[0].all() and s[:, m // 2].all() and int(s.sum()) == m + h.s.shape[0] - 1      # feature 77's group, row m // 2
+
+
+def test_no_rows_is_a_no_op(moe):
+    a, w = moe.Fp8Tensor(0, 256), blocks_fp8(randn((128, 256), 80), "f32")
+    assert moe.Fp8Linear(*w)(a, torch.empty(0, 128, device="cuda")).shape == (0, 128)
+    moe.Fp8GatedLinear(*w, *w)(a, moe.Fp8Tensor(0, 128))
+    moe.RmsNorm(torch.ones(256, device="cuda"))(torch.empty(0, 256, device="cuda"), out=a)
+
+
+def block(moe, scale="f32", h=512, inner=1024):
+    norm = moe.RmsNorm(1 + randn((h,), 90, 0.2))
+    g, u = blocks_fp8(randn((inner, h), 91, 0.04), scale), blocks_fp8(randn((inner, h), 92, 0.04), scale)
+    d = blocks_fp8(randn((h, inner), 93, 0.04), scale)
+    return moe.DenseFfn(norm, moe.Fp8GatedLinear(*g, *u), moe.Fp8Linear(*d)), (g, u, d)
+
+
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("rows", [1, 50, 300])
+def test_the_operators_together(moe, scale, rows):
+    """Norm, gated and plain projection as one pre-norm FFN, each on what the one before it wrote."""
+    ffn, (g, u, d) = block(moe, scale)
+    x, r = randn((rows, 512), 94, dtype=torch.bfloat16), randn((rows, 512), 95, 2.0, torch.bfloat16)
+    v, n = norm64(x, r, ffn.norm.weight, 1e-6)
+    y = ffn(x, r, torch.empty(rows, 512, dtype=torch.float32, device="cuda"))
+    a, h = ffn.buffers(rows)
+    check_codes(a.q, a.s, n, n.abs() * N_REL, scale)
+    want, tol = product64(h.q, h.s, *d)
+    assert ((y.double() - want).abs() <= tol).all()
+    gv, uv = n @ wide_blocks(*g).t(), n @ wide_blocks(*u).t()
+    exact = (gv / (1 + torch.exp(-gv)) * uv) @ wide_blocks(*d).t()
+    # two quantisations of relative step 2^-4: errors of about 3 % each, independent over hundreds of terms
+    assert torch.linalg.norm(y.double() - exact) <= 0.1 * torch.linalg.norm(exact)
+
+
+def test_another_stream_and_a_graph(moe):
+    """Work goes to the current stream, in order with it, and can be captured."""
+    ffn, _ = block(moe)
+    x, r = randn((24, 512), 96, dtype=torch.bfloat16), randn((24, 512), 97, 2.0, torch.bfloat16)
+    ref_r = r.clone()
+    ref = ffn(x, ref_r, torch.empty(24, 512, dtype=torch.bfloat16, device="cuda"))
+    side = torch.cuda.Stream()
+    xs, rs = torch.zeros_like(x), torch.zeros_like(r)
+    y = torch.zeros_like(ref)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        xs.copy_(x)
+        rs.copy_(r)
+        ffn(xs, rs, y)
+    side.synchronize()
+    assert torch.equal(y, ref) and torch.equal(rs, ref_r)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        ffn(xs, rs, y)
+    for _ in range(2):
+        xs.copy_(x)
+        rs.copy_(r)
+        y.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, ref) and torch.equal(rs, ref_r)
+
+
+def test_repeated_calls_give_the_same_bits(moe):
+    lin, y = check_linear(moe, 150, 1000, 900, "f32", torch.float32)
+    aq, a_s = rows_fp8(randn((150, 1000), 20), "f32")
+    a = moe.Fp8Tensor.from_parts(aq, a_s)
+    for _ in range(5):
+        assert torch.equal(lin(a, torch.empty_like(y)), y)
+
+
+# ------------------------------------------------------------------ refusals
+
+def test_refusals(moe):
+    w = blocks_fp8(randn((128, 256), 100), "f32")
+    lin, gated = moe.Fp8Linear(*w), moe.Fp8GatedLinear(*w, *w)
+    a, y = moe.Fp8Tensor(4, 256), torch.empty(4, 128, device="cuda")
+    norm = moe.RmsNorm(torch.ones(256, device="cuda"))
+    x = torch.zeros(4, 256, device="cuda")
+
+    def refused(fn, code=1):
+        with pytest.raises(moe.MoeError) as e:
+            fn()
+        assert e.value.status == code
+    refused(lambda: lin(moe.Fp8Tensor(4, 256, "e8m0"), y))
+    refused(lambda: lin(moe.Fp8Tensor(4, 128), y))
+    refused(lambda: lin(a, torch.empty(4, 127, device="cuda")))
+    refused(lambda: lin(a, torch.empty(4, 128, dtype=torch.float16, device="cuda")))
+    refused(lambda: lin(a, torch.empty(128, 4, device="cuda").t()))
+    refused(lambda: lin(a, torch.empty(4, 128)))
+    refused(lambda: gated(a, moe.Fp8Tensor(3, 128)))
+    refused(lambda: gated(a, moe.Fp8Tensor(4, 128, "e8m0")))
+    refused(lambda: norm(x, out=moe.Fp8Tensor(4, 128)))
+    refused(lambda: norm(x))
+    refused(lambda: norm(x, res_out=x))
+    refused(lambda: norm(x, x.bfloat16(), y=x), 2)
+    refused(lambda: norm(x.half(), y=x.half()))
+    refused(lambda: norm(x, y=torch.empty(4, 256, dtype=torch.bfloat16, device="cuda")))
+    refused(lambda: moe.Fp8Linear(w[0], w[1][:, :1]))
+    refused(lambda: moe.Fp8Tensor(4, 256, "bf16"))
+    refused(lambda: moe.moe_linear_forward(gated.handle, a.matrix, 4, y.data_ptr(), 128, moe.F32))
+    refused(lambda: moe.moe_gated_linear_forward(lin.handle, a.matrix, 4, a.matrix))
+    refused(lambda: moe.moe_linear_forward(lin.handle, a.matrix, -1, y.data_ptr(), 128, moe.F32))
+    refused(lambda: moe.moe_linear_forward(lin.handle, a.matrix, 4, y.data_ptr(), 127, moe.F32))
+    refused(lambda: moe.moe_linear_forward(lin.handle, a.matrix, 4, y.data_ptr() + 2, 128, moe.F32))
+    odd = moe.MoeFp8Matrix(a.q.data_ptr(), a.s.data_ptr(), 264, 4, 0, 0)
+    refused(lambda: moe.moe_linear_forward(lin.handle, odd, 4, y.data_ptr(), 128, moe.F32))
+    short = moe.MoeFp8Matrix(a.q.data_ptr(), a.s.data_ptr(), 256, 3, 0, 0)
+    refused(lambda: moe.moe_linear_forward(lin.handle, short, 4, y.data_ptr(), 128, moe.F32))
+    assert lin.device_status() == (0, 0) and gated.device_status() == (0, 0)
+    lin(a, y)          # a refused call leaves the handle usable
