@@ -338,7 +338,8 @@ moe_status moe_profile_read(moe_layer* layer, float* stage_ms, int32_t n_stages)
  *
  * E4M3 activations: codes q[row][col] with a row stride of ldq bytes (a
  * multiple of 16; q 16-byte aligned), and one scale per row and 128 columns,
- * K-block-major: s[col / 128][row] with a stride of lds scales between blocks.
+ * K-block-major: s[col / 128][row] with a stride of lds scales between blocks
+ * (s 16-byte aligned, and lds scales a multiple of 16 bytes).
  * Value = E4M3(q) * s.  Scales are fp32, or powers of two in eight bits
  * (E8M0: 2^(b - 127), 255 is NaN).  A producer writes s = amax/448 of the 128
  * columns (E8M0: the smallest power of two not below that), or 1 where

@@ -519,51 +519,59 @@ def _rows_of(t, rows: int, cols: int, what: str) -> int:
 class Fp8Tensor:
     """E4M3 activations with 1x128 scales: value = q * s[column // 128].
 
-    q: float8_e4m3fn [rows][cols] (row stride a multiple of 16); s:
-    [ceil(cols / 128)][rows], float32 (scale="f32") or float8_e8m0fnu
-    (scale="e8m0").  matrix is the C ABI's view of both."""
+    q: float8_e4m3fn [rows][cols]; s: [ceil(cols / 128)][rows], float32
+    (scale="f32") or float8_e8m0fnu (scale="e8m0").  Rows of both lie on
+    16-byte strides.  matrix is the C ABI's view of them."""
 
     def __init__(self, rows: int, cols: int, scale: str = "f32", device=None):
         import torch
         if scale not in _SCALES:
             _bad(f"scale must be one of {sorted(_SCALES)}, not {scale!r}")
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-        ldq = (cols + 15) // 16 * 16
-        q = torch.empty(rows, ldq, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)[:, :cols]
-        s = (torch.empty((cols + 127) // 128, rows, dtype=torch.float32, device=device) if scale == "f32" else
-             torch.empty((cols + 127) // 128, rows, dtype=torch.uint8, device=device).view(torch.float8_e8m0fnu))
-        self._bind(q, s, scale, ldq, rows)
+        st = torch.float32 if scale == "f32" else torch.float8_e8m0fnu
+        q = torch.empty(rows, _up(cols, 16), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)[:, :cols]
+        s = torch.empty(_up(cols, 128) // 128, _up(rows, 16), dtype=torch.uint8 if scale == "e8m0" else st, device=device)
+        self._bind(q, s.view(st)[:, :rows], scale)
 
-    def _bind(self, q, s, scale, ldq, lds):
+    def _bind(self, q, s, scale):
         self.rows, self.cols, self.scale, self.q, self.s = q.shape[0], q.shape[1], scale, q, s
         self.device = q.device
-        self.matrix = MoeFp8Matrix(q.data_ptr(), s.data_ptr(), ldq, lds, _SCALES[scale], 0)
+        self.matrix = MoeFp8Matrix(q.data_ptr(), s.data_ptr(), q.stride(0), s.stride(0), _SCALES[scale], 0)
 
     @classmethod
     def from_parts(cls, q, s):
-        """Wrap codes and scales that exist already; codes whose rows do not
-        lie on 16-byte strides are copied."""
+        """Wrap codes and scales that exist already; an array whose rows do
+        not lie on 16-byte strides is copied."""
         import torch
         if q.dim() != 2 or q.dtype is not torch.float8_e4m3fn or not q.is_cuda:
             _bad("q must be a two-dimensional float8_e4m3fn CUDA tensor")
         scale = {torch.float32: "f32", torch.float8_e8m0fnu: "e8m0"}.get(s.dtype)
         rows, cols = q.shape
-        if scale is None or s.device != q.device or list(s.shape) != [(cols + 127) // 128, rows]:
-            _bad(f"s must be float32 or float8_e8m0fnu [{(cols + 127) // 128}][{rows}] beside q")
-        if (cols > 1 and q.stride(1) != 1) or (rows > 1 and (q.stride(0) % 16 or q.stride(0) < cols)) or q.data_ptr() % 16:
-            wide = torch.zeros(rows, (cols + 15) // 16 * 16, dtype=torch.uint8, device=q.device)
-            wide[:, :cols] = q.view(torch.uint8)
-            q = wide.view(torch.float8_e4m3fn)[:, :cols]
-        if (rows > 1 and s.stride(1) != 1) or (s.shape[0] > 1 and s.stride(0) < rows):
-            s = s.contiguous()
+        if scale is None or s.device != q.device or list(s.shape) != [_up(cols, 128) // 128, rows]:
+            _bad(f"s must be float32 or float8_e8m0fnu [{_up(cols, 128) // 128}][{rows}] beside q")
         t = cls.__new__(cls)
-        t._bind(q, s, scale, q.stride(0) if rows > 1 else (cols + 15) // 16 * 16,
-                s.stride(0) if s.shape[0] > 1 else rows)
+        t._bind(_on_strides(q), _on_strides(s), scale)
         return t
 
     def dequantise(self):
         """The values the codes stand for, fp32."""
         return self.q.float() * self.s.float().t().repeat_interleave(128, 1)[:, :self.cols]
+
+
+def _up(n: int, to: int) -> int:
+    return (n + to - 1) // to * to
+
+
+def _on_strides(t):
+    """t itself if it has contiguous rows on 16-byte strides, else a copy that has."""
+    import torch
+    n, es = t.shape[1], t.element_size()
+    if t.data_ptr() % 16 == 0 and t.stride(1) == 1 and t.stride(0) >= n and t.stride(0) * es % 16 == 0:
+        return t
+    bits = torch.uint8 if es == 1 else t.dtype
+    wide = torch.zeros(t.shape[0], _up(n, 16), dtype=bits, device=t.device)
+    wide[:, :n] = t.view(bits)
+    return wide.view(t.dtype)[:, :n]
 
 
 class RmsNorm:

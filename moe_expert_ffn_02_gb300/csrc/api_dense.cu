@@ -39,8 +39,8 @@ moe_status check_fp8(const moe_fp8_matrix& m, int rows, int cols, const char* wh
     if (m.lds < rows) return fail(MOE_ERR_INVALID_ARG, "%s: lds (%lld) is less than the %d rows", what, (long long)m.lds, rows);
     if (m.scale_type != MOE_SCALE_F32 && m.scale_type != MOE_SCALE_E8M0)
         return fail(MOE_ERR_INVALID_ARG, "%s: unknown scale type %d", what, m.scale_type);
-    if (m.scale_type == MOE_SCALE_F32 && !aligned(m.s, 4))
-        return fail(MOE_ERR_INVALID_ARG, "%s: scales are not 4-byte aligned", what);
+    if (!aligned(m.s, 16) || m.lds % (m.scale_type == MOE_SCALE_F32 ? 4 : 16))
+        return fail(MOE_ERR_INVALID_ARG, "%s: scale rows are not on 16-byte strides", what);
     return MOE_OK;
 }
 

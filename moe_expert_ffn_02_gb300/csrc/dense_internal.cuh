@@ -45,8 +45,10 @@ __device__ __forceinline__ float group_scale(float amax, bool e8m0, uint32_t& he
 // 1 / s for the scales above: finite scales lie in [2^-126, 2^120].
 __device__ __forceinline__ float inv_scale(float s) { return __frcp_rn(s); }
 
+// 2^(b - 127): the exponent field as it is, except 0 (a subnormal) and 255 (NaN), which both need
+// the mantissa's top bit.
 __device__ __forceinline__ float e8m0_to_f32(uint8_t b) {
-    return __uint_as_float(b == 255 ? 0x7FC00000u : b == 0 ? 0x00400000u : (uint32_t)b << 23);
+    return __uint_as_float(((uint32_t)b << 23) | ((uint8_t)(b + 1) <= 1 ? 0x400000u : 0u));
 }
 
 // max that keeps a NaN of either side.
@@ -78,6 +80,8 @@ cudaError_t launch_linear_repack(const moe_linear* L, const uint8_t* w, const vo
                                  const void* su, cudaStream_t st);
 cudaError_t launch_fp8_linear(const GemmCall& c, cudaStream_t s);
 cudaError_t launch_fp8_gated(const GemmCall& c, cudaStream_t s);
+bool few_tokens(const GemmCall& c, bool gated);         // whether the few-token form takes the call
+cudaError_t launch_fp8_few(const GemmCall& c, bool gated, cudaStream_t s);
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,

@@ -1,0 +1,528 @@
+// FP8 projections of few tokens (1 to 64), plain and gated: the weights are
+// streamed once, by all SMs.
+//
+// Bound by HBM: a call reads the weights' bytes and almost nothing else.  So
+// the weights are the MMA's 128-row operand and the tokens its 16, 32 or 64
+// columns: an MMA takes about 36 cycles here however few columns it has (it
+// reads its 128-row operand from shared memory), so 128 weight rows per MMA keep
+// the tensor core far ahead of the copies, and each of the four lane quarters
+// has its own warps to drain it.
+//
+// The weights are cut into tiles of R <= 128 rows and S ranges of K; the S CTAs
+// of a tile form a cluster and add their partial sums through distributed
+// shared memory, in rank order.  R and S follow from the weights' shape alone,
+// and blocks are added in K order, so a token's result does not depend on how
+// many others are in the batch.  One SM takes at most about 70 GB/s and 100 of
+// them saturate HBM (measured with bulk copies alone: 64 CTAs 4.4 TB/s, 96 6.3,
+// 112 6.7, 152 6.8), hence the rule: as many CTAs as there are SMs.
+//
+// A stage is a group of G K blocks (R rows of weights, the tokens, their
+// scales), closed by one commit and drained at once: waiting on or arriving at
+// an mbarrier takes a warp about 150 cycles and issuing a tensor copy about 90, so
+// narrow tiles need several blocks per hand-off.  Of a tile's blocks, pairs go to
+// the two warps of a lane quarter in turn, and the two sums are added once at the
+// end.  Half the SM's shared memory and tensor memory at most: two CTAs fit, so the
+// next call's weights are requested while this one ends, and a cluster of eight
+// finds room beside others.
+//
+// Gated: a cluster holds the 256 interleaved gate/up rows of 128 features (two
+// tiles of 128 rows, S ranges of K each), which is one quantisation group.
+#include "fp8_gemm.cuh"
+
+namespace moe {
+namespace few {
+
+using namespace dg;
+
+constexpr int MAX_M = 64;
+constexpr int ST_MAX = 8;                    // ring stages
+constexpr int KR_MAX = 512;                  // K blocks per range, at most (weight scales kept in shared memory)
+// 4 control warps and 8 drain warps, launched at 80 registers so that two CTAs fit: 128 x 48 + 256 x 96 = 384 x 80
+constexpr int FEW_CTRL_REGS = 48, FEW_DRAIN_REGS = 96;
+
+struct FewArgs {
+    const float* sw;
+    int M, N, kt, nblk;
+    int R, S, G;                             // rows per tile, K ranges, K blocks per stage (1, 2 or 4)
+    int a_rows, stages, kr;
+    bool a_whole;
+    void* y;
+    int64_t ldy;
+    bool y_f32;
+    uint8_t* hq;
+    int64_t ld_hq;
+    void* hs;
+    int64_t ld_hs;
+    uint32_t* status;
+    uint32_t wait_limit;
+};
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// (a0, a1) += (x0, x1) * s * (c0, c1), rounded as s * c and one fma each.
+__device__ __forceinline__ void fma2s(float& a0, float& a1, uint32_t x0, uint32_t x1, float s, float c0, float c1) {
+    asm("{\n .reg .b64 a, x, c, s;\n mov.b64 a, {%0, %1};\n mov.b64 x, {%2, %3};\n mov.b64 c, {%5, %6};\n mov.b64 s, {%4, %4};\n"
+        " mul.rn.f32x2 c, c, s;\n fma.rn.f32x2 a, x, c, a;\n mov.b64 {%0, %1}, a;\n}"
+        : "+f"(a0), "+f"(a1)
+        : "r"(x0), "r"(x1), "f"(s), "f"(c0), "f"(c1));
+}
+
+constexpr int group_cap(int tn) { return tn == 64 ? 2 : 4; }
+constexpr int tail_bytes(int tn) { return tn * BM * 4 > BM * 128 ? tn * BM * 4 : BM * 128; }   // partial sums; operand read
+
+// First K block of range p: ranges start at even blocks, whatever G is.
+__host__ __device__ inline int range_start(int kt, int S, int p) { return p == S ? kt : (kt + 1) / 2 * p / S * 2; }
+
+// Tensor-memory buffer and barrier phase of a warp's n-th group.  Groups that only one turn's
+// warps drain use that turn's half of the buffers, so that nobody waits on a barrier whose phases
+// it has not followed.
+struct BufAt {
+    int buf;
+    uint32_t phase;
+};
+template <int NBUF>
+__device__ __forceinline__ BufAt buf_at(int G, int turn, int n) {
+    if (G == 4) return BufAt{n % NBUF, (uint32_t)(n / NBUF) & 1u};
+    return BufAt{turn * (NBUF / 2) + n % (NBUF / 2), (uint32_t)(n / (NBUF / 2)) & 1u};
+}
+
+// Scales of 4 tokens of a K block's run.
+template <bool E8>
+__device__ __forceinline__ float4 load_sa4(const uint8_t* sl, int t, int a_rows) {
+    const int to = min(t, a_rows - 4);         // a multiple of 4; tokens past a_rows are nobody's
+    if constexpr (!E8) return *reinterpret_cast<const float4*>(sl + 4 * to);
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(sl + to);
+    return make_float4(e8m0_to_f32((uint8_t)v), e8m0_to_f32((uint8_t)(v >> 8)), e8m0_to_f32((uint8_t)(v >> 16)),
+                       e8m0_to_f32((uint8_t)(v >> 24)));
+}
+
+// acc[t] += D[t] * (s_w * s_x[t]) for KBS K blocks side by side in tensor memory, PC columns at a time.
+template <int TN, int KBS, int PC, bool E8>
+__device__ __forceinline__ void take(uint32_t tb, const uint8_t* sl, int pitch, const float* sw, int a_rows,
+                                     float (&acc)[TN]) {
+#pragma unroll
+    for (int p = 0; p < TN; p += PC) {
+        uint32_t raw[KBS][PC];
+#pragma unroll
+        for (int j = 0; j < KBS; ++j)
+#pragma unroll
+            for (int w = 0; w < PC; w += 16)
+                tc::tmem_ld16u(tb + j * TN + p + w, reinterpret_cast<uint32_t(&)[16]>(raw[j][w]));
+        float4 c[KBS][PC / 4];
+        float s[KBS];
+#pragma unroll
+        for (int j = 0; j < KBS; ++j) {
+            s[j] = sw[2 * j];
+#pragma unroll
+            for (int q = 0; q < PC / 4; ++q) c[j][q] = load_sa4<E8>(sl + j * pitch, p + 4 * q, a_rows);
+        }
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < KBS; ++j)
+#pragma unroll
+            for (int q = 0; q < PC / 4; ++q) {
+                const int t = p + 4 * q;
+                fma2s(acc[t], acc[t + 1], raw[j][4 * q], raw[j][4 * q + 1], s[j], c[j][q].x, c[j][q].y);
+                fma2s(acc[t + 2], acc[t + 3], raw[j][4 * q + 2], raw[j][4 * q + 3], s[j], c[j][q].z, c[j][q].w);
+            }
+    }
+}
+
+__device__ __forceinline__ void store_y(const FewArgs& a, int t, int n, float v) {
+    const int64_t at = (int64_t)t * a.ldy + n;
+    if (a.y_f32) static_cast<float*>(a.y)[at] = v;
+    else static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+}
+
+template <int TN, bool GATED, bool E8>
+__global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant__ Maps maps, FewArgs a) {
+    constexpr int BUFC = group_cap(TN) * TN, COLS = 256, NBUF = COLS / BUFC;        // TMEM columns
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int w_bytes = a.R * 128, a_bytes = a.a_rows * 128, stage_bytes = a.G * (w_bytes + a_bytes);
+    const int pitch = sa_pitch(a.a_rows, E8), slot_bytes = (a.G * pitch + 127) / 128 * 128;
+    float* part = reinterpret_cast<float*>(ring + a.stages * stage_bytes);          // [token][128 rows]
+    uint8_t* scales = reinterpret_cast<uint8_t*>(part) + tail_bytes(TN);            // [stage][slot]
+    float* sws = reinterpret_cast<float*>(scales + a.stages * slot_bytes);          // [kr][2]
+    __shared__ uint64_t full[ST_MAX], empty[ST_MAX], tfull[NBUF], tempty[NBUF];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int csize = GATED ? 2 * a.S : a.S;
+    const int rank = (int)blockIdx.x % csize, unit = (int)blockIdx.x / csize;
+    const int n0 = (GATED ? 2 * unit + rank / a.S : unit) * a.R;
+    const int kb0 = range_start(a.kt, a.S, rank % a.S), nkb = range_start(a.kt, a.S, rank % a.S + 1) - kb0;
+    const int n_grp = (nkb + a.G - 1) / a.G;
+
+    pdl_trigger();
+    if (threadIdx.x == 0) {
+        // a group of four blocks is drained by both warps of each quarter, a smaller one by one of them
+        const uint32_t drains = a.G == 4 ? EPI_WARPS : EPI_WARPS / 2;
+        for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], drains); }
+        for (int b = 0; b < NBUF; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], drains); }
+        fence_mbar_init();
+        abort_flag = 0;
+    }
+    __syncthreads();
+    volatile int* abort = &abort_flag;
+
+    if (warp < CTRL_WARPS) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FEW_CTRL_REGS));
+        if (warp == 0) {
+            // ------------------------------------------------ producer
+            const uint32_t el = elect_one();
+            const uint32_t ring0 = smem_addr(ring), scl0 = smem_addr(scales), full0 = smem_addr(full);
+            if (el) {
+                prefetch_map(&maps.w);
+                prefetch_map(&maps.a);
+                prefetch_map(&maps.s);
+            }
+            auto copy_w = [&](int st, int g) {
+                const int na = a.a_whole ? a.G : min(a.G, a.kt - kb0 - g * a.G);
+                if (el) {
+                    expect_tx(full0 + 8 * st, (uint32_t)(a.G * (w_bytes + pitch) + na * a_bytes));
+                    tma_load_3d(ring0 + st * stage_bytes, &maps.w, 0, n0, kb0 + g * a.G, full0 + 8 * st);
+                }
+            };
+            const int pre = min(a.stages, n_grp);    // the weights do not depend on the preceding kernel
+            for (int g = 0; g < pre; ++g) copy_w(g, g);
+            pdl_wait();
+            int st = 0, g = 0;
+            uint32_t phase = 0;
+            for (; g < n_grp; ++g) {
+                if (g >= pre) {
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[st], phase ^ 1u, a.wait_limit, a.status, abort))) break;
+                    copy_w(st, g);
+                }
+                if (el) {
+                    const uint32_t dst = ring0 + st * stage_bytes + a.G * w_bytes, bar = full0 + 8 * st;
+                    const int kb = kb0 + g * a.G;
+                    if (a.a_whole) {
+                        tma_load_3d(dst, &maps.a, 0, 0, kb, bar);
+                    } else {
+                        const int na = min(a.G, a.kt - kb);
+                        for (int i = 0; i < na; ++i) tma_load_3d(dst + i * a_bytes, &maps.a, (kb + i) * QB, 0, 0, bar);
+                    }
+                    tma_load_2d(scl0 + st * slot_bytes, &maps.s, 0, kb, bar);
+                }
+                if (++st == a.stages) { st = 0; phase ^= 1u; }
+            }
+            for (int n = min(g, a.stages); n > 0; --n) {   // every issued copy lands before the CTA exits
+                if (--st < 0) { st = a.stages - 1; phase ^= 1u; }
+                mbar_wait_bounded(&full[st], phase, a.wait_limit, a.status, nullptr);
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------ MMA issuer
+            tc::tmem_alloc(&tmem_slot, COLS);
+            tc::tc_fence_before();
+            named_bar_sync(2, (1 + EPI_WARPS) * 32);
+            tc::tc_fence_after();
+            const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_slot, 0);
+            const uint32_t el = elect_one();
+            const uint32_t idesc = (1u << 4) | ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+            const uint32_t d0 = (uint32_t)tc::sw128_desc(smem_addr(ring));
+            int st = 0, c0 = 0, c1 = 0;
+            uint32_t phase = 0;
+            for (int g = 0; g < n_grp; ++g) {
+                const bool second = a.G < 4 && ((g * a.G >> 1) & 1);
+                const BufAt at = buf_at<NBUF>(a.G, second, second ? c1 : c0);
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[st], phase, a.wait_limit, a.status, abort) &&
+                                                 mbar_wait_bounded(&tempty[at.buf], at.phase ^ 1u, a.wait_limit, a.status, abort)))
+                    break;
+                tc::tc_fence_after();
+                const int nk = min(a.G, nkb - g * a.G);
+                uint32_t wd = d0 + (uint32_t)((st * stage_bytes) >> 4), td = wd + (uint32_t)((a.G * w_bytes) >> 4);
+                uint32_t dt = tmem + (uint32_t)(at.buf * BUFC);
+                for (int i = 0; i < nk; ++i) {
+                    mma_block(dt, wd, td, idesc, el);
+                    wd += (uint32_t)(w_bytes >> 4);
+                    td += (uint32_t)(a_bytes >> 4);
+                    dt += TN;
+                }
+                if (el) tc::mma_commit(&tfull[at.buf]);
+                __syncwarp();
+                if (++st == a.stages) { st = 0; phase ^= 1u; }
+                if (second) ++c1; else ++c0;
+            }
+        }
+        __syncwarp();
+        named_bar_sync(3, NTHREADS);
+        if (warp == 1) {
+            tc::tc_fence_after();
+            tc::tmem_dealloc(tmem_slot, COLS);
+        }
+        if (csize > 1) {                                       // the drain warps' two cluster barriers below
+            cluster_arrive_release();
+            cluster_wait();
+            cluster_arrive_release();
+            cluster_wait();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FEW_DRAIN_REGS));
+        // ---------------------------------------------------- drain warps
+        const int ew = warp - CTRL_WARPS, quarter = warp & 3, turn = ew >> 2;
+        const int row = quarter * 32 + lane;                   // weight row of the tile = TMEM lane
+        const bool live = quarter * 32 < a.R;
+        // the range's weight scales, two per block: plain, those of the tile's first scale block and
+        // the next one; gated, gate and up
+        {
+            const int b0 = GATED ? unit : n0 / QB;
+            const float* s0 = a.sw + (size_t)min(b0, a.nblk - 1) * a.kt + kb0;
+            const float* s1 = a.sw + (size_t)(GATED ? b0 + a.nblk : min(b0 + 1, a.nblk - 1)) * a.kt + kb0;
+            for (int i = threadIdx.x - CTRL_WARPS * 32; i < 2 * nkb; i += EPI_WARPS * 32)
+                sws[i] = (i & 1) ? s1[i >> 1] : s0[i >> 1];
+        }
+        const int sel = GATED ? (row >> 3) & 1 : ((n0 + row) / QB != n0 / QB);
+        named_bar_sync(2, (1 + EPI_WARPS) * 32);
+        tc::tc_fence_after();
+        const uint32_t tmem = tmem_slot + ((uint32_t)(quarter * 32) << 16);
+        float acc[TN];
+#pragma unroll
+        for (int t = 0; t < TN; ++t) acc[t] = 0.f;
+        int st = 0, mine = 0;
+        uint32_t phase = 0;
+        bool dead = false;
+        for (int g = 0; g < n_grp; ++g) {
+            const int kb = g * a.G;
+            if (a.G == 4 || ((kb >> 1) & 1) == turn) {
+                // my blocks of this group: a pair (or, with G = 1 or at the end, one block)
+                const int k0 = kb + (a.G == 4 ? 2 * turn : 0), nk = min(min(a.G, 2), nkb - k0);
+                const BufAt at = buf_at<NBUF>(a.G, turn, mine++);
+                // the second wait returns at once: it makes the stage's scales visible to this thread
+                if (!dead && !(mbar_wait_bounded(&tfull[at.buf], at.phase, a.wait_limit, a.status, abort) &&
+                               mbar_wait_bounded(&full[st], phase, a.wait_limit, a.status, abort)))
+                    dead = true;
+                dead = __any_sync(0xFFFFFFFFu, dead);          // warp-uniform: tcgen05.ld is warp-collective
+                const bool work = !dead && live && nk > 0;
+                if (work) {
+                    tc::tc_fence_after();
+                    const uint32_t tb = tmem + (uint32_t)(at.buf * BUFC + (k0 - kb) * TN);
+                    const uint8_t* sl = scales + st * slot_bytes + (k0 - kb) * pitch;
+                    const float* sw = sws + 2 * k0 + sel;
+                    // Straight-line code from the loads to the products: the shared-memory reads of the
+                    // scales overlap the tensor-memory loads, which a branch between would prevent.
+                    if (TN == 16 && nk == 2) {
+                        take<TN, 2, 16, E8>(tb, sl, pitch, sw, a.a_rows, acc);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if (j < nk) take<TN, 1, 16, E8>(tb + j * TN, sl + j * pitch, pitch, sw + 2 * j, a.a_rows, acc);
+                    }
+                    tc::tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&empty[st]);
+                    mbar_arrive(&tempty[at.buf]);
+                }
+            }
+            if (++st == a.stages) { st = 0; phase ^= 1u; }
+        }
+        // the two warps of a quarter add their sums
+        if (turn == 1 && live) {
+#pragma unroll
+            for (int t = 0; t < TN; ++t)
+                if (t < a.M) part[t * BM + row] = acc[t];
+        }
+        pdl_wait();                                            // before the first write the preceding kernel may conflict with
+        named_bar_sync(1, EPI_WARPS * 32);
+        if (turn == 0 && live) {
+#pragma unroll
+            for (int t = 0; t < TN; ++t)
+                if (t < a.M) {
+                    const float v = acc[t] + part[t * BM + row];
+                    if (!GATED && csize == 1) {
+                        if (row < a.R && n0 + row < a.N) store_y(a, t, n0 + row, v);
+                    } else {
+                        part[t * BM + row] = v;
+                    }
+                }
+        }
+        // ------------------------------------------------------ join the K ranges
+        tc::tc_fence_before();
+        named_bar_sync(3, NTHREADS);
+        if (csize > 1) {
+            cluster_arrive_release();
+            cluster_wait();
+        }
+        const uint32_t part0 = smem_addr(part);
+        if (csize > 1 && !*abort) {
+            const int tid = threadIdx.x - CTRL_WARPS * 32;
+            if constexpr (GATED) {
+                // a warp takes a token: four features a lane, 128 in all
+                const int f = 4 * lane, ff = f & 63, r = (ff >> 3) * 16 + (ff & 7);
+                const int base = (f >> 6) * a.S;                   // first rank of the tile with these features
+                const int f0 = unit * QB + f;
+                for (int t = rank * EPI_WARPS + (tid >> 5); t < a.M; t += csize * EPI_WARPS) {
+                    float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+                    for (int p = 0; p < a.S; ++p) {
+                        const uint32_t at = map_to_rank(part0 + (uint32_t)(t * BM + r) * 4u, base + p);
+                        const float4 x = ld_cluster4(at), z = ld_cluster4(at + 32);
+                        g.x += x.x; g.y += x.y; g.z += x.z; g.w += x.w;
+                        u.x += z.x; u.y += z.y; u.z += z.z; u.w += z.w;
+                    }
+                    float h[4] = {silu_mul(g.x, u.x), silu_mul(g.y, u.y), silu_mul(g.z, u.z), silu_mul(g.w, u.w)};
+                    float am = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (f0 + e >= a.N) h[e] = 0.f;
+                        am = max_nan(am, fabsf(h[e]));
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+                    uint32_t held;
+                    const float is = inv_scale(group_scale(am, E8, held));
+                    const uint32_t v = pack4_e4m3(h[0] * is, h[1] * is, h[2] * is, h[3] * is);
+                    uint8_t* dst = a.hq + (int64_t)t * a.ld_hq + f0;
+                    if (f0 + 4 <= a.N) {
+                        *reinterpret_cast<uint32_t*>(dst) = v;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (f0 + e < a.N) dst[e] = (uint8_t)(v >> (8 * e));
+                    }
+                    if (lane == 0) {
+                        const int64_t at = (int64_t)unit * a.ld_hs + t;
+                        if (E8) static_cast<uint8_t*>(a.hs)[at] = (uint8_t)held;
+                        else static_cast<uint32_t*>(a.hs)[at] = held;
+                    }
+                }
+            } else {
+                // each CTA of the cluster finishes a slice of the tile's rows
+                const int rs = a.R / a.S, lo = rank * rs;
+                for (int i = tid; i < rs * a.M; i += EPI_WARPS * 32) {
+                    const int t = i / rs, r = lo + i % rs;
+                    float v = 0.f;
+                    for (int p = 0; p < a.S; ++p) v += ld_cluster(map_to_rank(part0 + (uint32_t)(t * BM + r) * 4u, p));
+                    if (n0 + r < a.N) store_y(a, t, n0 + r, v);
+                }
+            }
+        }
+        if (csize > 1) {                                           // nobody leaves while a peer may still read its sums
+            cluster_arrive_release();
+            cluster_wait();
+        }
+    }
+}
+
+struct FewPlan {
+    int R, S, G;
+};
+
+// Rows per tile and K ranges, from the weights' shape alone.  A CTA's time is its share of the
+// weights at the rate that so many SMs reach (at most 70 GB/s each and 6.8 TB/s together), or
+// a commit's 0.27 us per group where its rows are few; joining K ranges costs about a microsecond.
+static FewPlan plan_few(const moe_linear* L, bool gated) {
+    FewPlan best = {};
+    double best_us = 0;
+    for (int S = 1; S <= (gated ? 4 : 8); S *= 2) {
+        if (S > L->kt) break;
+        const int kr = range_start(L->kt, S, 1);               // the longest range
+        if (kr > KR_MAX || range_start(L->kt, S, S - 1) >= L->kt) continue;
+        for (int R = gated ? BM : 16; R <= BM; R += 16) {
+            if (R % S) continue;
+            const long long tiles = gated ? 2LL * ((L->d.out_features + QB - 1) / QB) : (L->rows + R - 1) / R;
+            const long long ctas = tiles * S;
+            const int G = R <= 64 && S == 1 ? 4 : 2;
+            const double sms = (double)std::min<long long>(ctas, L->num_sms);
+            const double rounds = (double)((ctas + L->num_sms - 1) / L->num_sms);
+            const double rate = std::min(70e3, 6.8e6 / sms);             // bytes per us and SM
+            const double us = rounds * std::max(kr * R * 128.0 / rate, kr * 0.27 / G) + (S > 1 ? 1.0 : 0.0);
+            if (!best.R || us < best_us) {
+                best_us = us;
+                best = FewPlan{R, S, G};
+            }
+        }
+    }
+    return best;
+}
+
+template <int TN, bool GATED, bool E8>
+cudaError_t launch_few(const GemmCall& c, const FewPlan& p, cudaStream_t s) {
+    const moe_linear* L = c.lin;
+    Args g = base_args(c);                    // what the tensor maps are made from
+    g.bn = p.R;
+    g.a_whole = L->d.in_features % QB == 0;
+    FewArgs a = {};
+    a.sw = L->sw;
+    a.M = c.M; a.N = L->d.out_features; a.kt = L->kt; a.nblk = g.nblk;
+    a.R = p.R; a.S = p.S;
+    a.a_rows = g.a_rows;
+    a.kr = range_start(L->kt, p.S, 1);
+    for (int i = 1; i < p.S; ++i) a.kr = std::max(a.kr, range_start(L->kt, p.S, i + 1) - range_start(L->kt, p.S, i));
+    a.a_whole = g.a_whole;
+    a.y = c.y; a.ldy = c.ldy; a.y_f32 = c.y_f32;
+    a.hq = c.hq; a.ld_hq = c.ld_hq; a.hs = c.hs; a.ld_hs = c.ld_hs;
+    a.status = L->dev_status; a.wait_limit = L->wait_limit;
+    // blocks per stage: the plan's, unless fewer than three stages would fit (two of one block always do)
+    const int fixed = 1024 + tail_bytes(TN) + a.kr * 8;
+    int stage = 0;
+    for (a.G = std::min(p.G, group_cap(TN)); a.G >= 1; a.G /= 2) {
+        stage = a.G * (p.R + a.a_rows) * 128 + (a.G * sa_pitch(a.a_rows, E8) + 127) / 128 * 128;
+        a.stages = std::min(ST_MAX, (SMEM_HALF - fixed) / stage);
+        if (a.stages >= 3 || a.G == 1) break;
+    }
+    if (a.stages < 1) return cudaErrorInvalidValue;
+    a.stages = std::min(a.stages, (a.kr + a.G - 1) / a.G);
+    Maps maps;
+    if (!encode_maps(c, g, a.G, &maps)) return cudaErrorInvalidValue;
+    const int smem = fixed + a.stages * stage;
+    cudaError_t e = ensure_smem_limit<few_kernel<TN, GATED, E8>>(SMEM_HALF);
+    if (e != cudaSuccess) return e;
+    const int cluster = GATED ? 2 * p.S : p.S;
+    const int tiles = GATED ? (L->d.out_features + QB - 1) / QB : (L->rows + p.R - 1) / p.R;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3((unsigned)(tiles * cluster));
+    cfg.blockDim = dim3(NTHREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    if (cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    return cudaLaunchKernelEx(&cfg, few_kernel<TN, GATED, E8>, maps, a);
+}
+
+}  // namespace few
+
+bool few_tokens(const GemmCall& c, bool gated) {
+    return c.M <= few::MAX_M && few::plan_few(c.lin, gated).R != 0;
+}
+
+namespace few {
+template <bool GATED, bool E8>
+static cudaError_t launch_tokens(const GemmCall& c, cudaStream_t s) {
+    const FewPlan p = plan_few(c.lin, GATED);
+    if (c.M <= 16) return launch_few<16, GATED, E8>(c, p, s);
+    if (c.M <= 32) return launch_few<32, GATED, E8>(c, p, s);
+    return launch_few<64, GATED, E8>(c, p, s);
+}
+}  // namespace few
+
+cudaError_t launch_fp8_few(const GemmCall& c, bool gated, cudaStream_t s) {
+    const bool e8 = c.lin->d.scale_type == MOE_SCALE_E8M0;
+    if (gated) return e8 ? few::launch_tokens<true, true>(c, s) : few::launch_tokens<true, false>(c, s);
+    return e8 ? few::launch_tokens<false, true>(c, s) : few::launch_tokens<false, false>(c, s);
+}
+
+}  // namespace moe

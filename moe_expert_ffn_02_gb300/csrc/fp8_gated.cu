@@ -16,7 +16,7 @@ static Plan plan_gated(const GemmCall& c, const Args& a) {
     double best_cost = 0;
     for (int cl = 1; cl <= MAX_CLUSTER; cl *= 2) {
         const int grp = cl, bn = BUF_COLS / cl;
-        if (2 * grp * (bn + a.a_rows) * 128 > RING_MAX) continue;
+        if (2 * stage_cost(grp, bn, a.a_rows, a.e8m0) > ring_max(true)) continue;
         const long long units = (long long)mt * nt;
         if (units > 0x3FFFFFFF) continue;
         const int slots = sms / cl;
@@ -39,6 +39,7 @@ static Plan plan_gated(const GemmCall& c, const Args& a) {
 
 cudaError_t launch_fp8_gated(const GemmCall& c, cudaStream_t s) {
     using namespace dg;
+    if (few_tokens(c, true)) return launch_fp8_few(c, true, s);
     Args a = base_args(c);
     a.hq = c.hq;
     a.ld_hq = c.ld_hq;
@@ -46,17 +47,11 @@ cudaError_t launch_fp8_gated(const GemmCall& c, cudaStream_t s) {
     a.ld_hs = c.ld_hs;
     const Plan p = plan_gated(c, a);
     if (!p.bn) return cudaErrorInvalidValue;
-    a.bn = p.bn;
-    a.n_nt = p.n_nt;
-    a.n_units = p.units;
-    CUtensorMap map;
-    cudaError_t e = encode_a(c, a.a_rows, &map);
-    if (e != cudaSuccess) return e;
     switch (p.grp) {
-        case 1: return launch<1, true>(c, p, a, map, s);
-        case 2: return launch<2, true>(c, p, a, map, s);
-        case 4: return launch<4, true>(c, p, a, map, s);
-        default: return launch<8, true>(c, p, a, map, s);
+        case 1: return launch<1, true>(c, p, a, s);
+        case 2: return launch<2, true>(c, p, a, s);
+        case 4: return launch<4, true>(c, p, a, s);
+        default: return launch<8, true>(c, p, a, s);
     }
 }
 

@@ -16,17 +16,23 @@
 // sum to join; with many, BN = 256.
 //
 // A TMEM buffer holds 256 columns: GRP = 1, 2, 4 or 8 K blocks of up to
-// 256 / GRP columns.  One commit covers the group, because a commit costs
-// about 512 cycles of MMA time however little work it closes: narrow tiles need
-// several blocks per commit.  Epilogue warp (quarter, half) owns 32 lanes and the
-// half's columns of every block of the group, so blocks are added in K order
-// into the same accumulators in every configuration and a row's result does
-// not depend on BN or on the batch size.
+// 256 / GRP columns, which are also one stage of the copy ring.  One commit
+// covers the group, because a commit costs about 512 cycles of MMA time however
+// little work it closes: narrow tiles need several blocks per commit.  Drain
+// warp (quarter, half) owns 32 lanes and the half's columns of every block of
+// the group, so blocks are added in K order into the same accumulators in every
+// configuration and a row's result does not depend on BN or on the batch size.
 //
-// Warps: 0 copies (TMA for A, bulk copies for the pre-swizzled weight image), 1
-// issues the MMAs, 2-3 idle, 4-11 drain.  Token tiles with fewer than 128 rows
-// copy only those rows (rounded up to 8); the MMA reads whatever lies behind
-// them in shared memory into TMEM lanes nobody reads.
+// Warps: 0 copies (TMA for A, bulk copies for the pre-swizzled weight image and
+// the token scales), 1 issues the MMAs, 2 fetches the weight scales with 4-byte
+// asynchronous copies, 3 idles, 4-11 drain.  Everything a block needs arrives on
+// its stage's barrier, so no warp waits for a load of its own.  Token tiles with
+// fewer than 128 rows copy only those rows (rounded up to 8); the MMA reads
+// whatever lies behind them in shared memory into TMEM lanes nobody reads.
+//
+// Copies of weights start before the wait for the preceding kernel, and before
+// the tensor memory is allocated: a small call's ring leaves room for two CTAs
+// on an SM, so the next call's weights are on their way while this one ends.
 #pragma once
 #include "dense_internal.cuh"
 #include "tcgen05.cuh"
@@ -50,7 +56,22 @@ constexpr int STG_BYTES = EPI_WARPS * 32 * STG_STRIDE * 4;
 constexpr int MAX_CLUSTER = 8;
 constexpr int AMAX_BYTES = 2 * MAX_CLUSTER * BM * 4;   // [unit parity][CTA rank][row]
 constexpr int SMEM_MAX = 232448 - 2048;       // dynamic limit, minus static barriers
-constexpr int RING_MAX = SMEM_MAX - 1024 - STG_BYTES - AMAX_BYTES - 2 * BM * 4;
+// What lies behind the ring: the plain epilogue's staging tiles, or the gated one's amax
+// exchange; at least the 16 KB that the last block's 128-row operand read may run into.
+constexpr int TAIL_PLAIN = STG_BYTES;
+constexpr int TAIL_GATED = 16384;
+static_assert(TAIL_PLAIN >= BM * 128 && TAIL_GATED >= BM * 128 && AMAX_BYTES + 2 * BM * 4 <= TAIL_GATED, "tail");
+// Stage bytes: GRP blocks of operands; its scales: GRP token runs and GRP pairs of weight scales.
+__host__ __device__ inline int sa_pitch(int a_rows, bool e8m0) { return e8m0 ? (a_rows + 15) / 16 * 16 : a_rows * 4; }
+__host__ __device__ inline int scale_slot(int grp, int a_rows, bool e8m0) {
+    return (grp * (sa_pitch(a_rows, e8m0) + 8) + 127) / 128 * 128;       // a TMA destination
+}
+inline int stage_cost(int grp, int bn, int a_rows, bool e8m0) {
+    return grp * (bn + a_rows) * 128 + scale_slot(grp, a_rows, e8m0);
+}
+inline int ring_max(bool gated) { return SMEM_MAX - 1024 - (gated ? TAIL_GATED : TAIL_PLAIN); }
+// Shared memory of a CTA that leaves room for a second one on the SM.
+constexpr int SMEM_HALF = 113 * 1024 - 2048;
 
 struct Args {
     const uint8_t* w;         // weight image [kt][rows_pad][128]
@@ -65,6 +86,7 @@ struct Args {
     int n_nt;                 // weight tiles per token tile
     int n_units;
     bool e8m0;
+    bool a_whole;             // K is a multiple of 128: one copy brings all of a group's token tiles
     // plain
     void* y;
     int64_t ldy;
@@ -78,15 +100,60 @@ struct Args {
     uint32_t wait_limit;
 };
 
+// The three operands that TMA brings: token codes, weight image, token scales.
+struct Maps {
+    CUtensorMap a, w, s;
+};
+
 __device__ __forceinline__ uint32_t idesc_for(int n) {   // D f32, A = B = E4M3, K-major, M = 128
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
 }
 
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
+// True in one lane of a converged warp.  The loops around it stay warp-uniform, so that
+// descriptors and addresses live in uniform registers and an issue costs a few cycles.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p;
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_addr(bar))
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// The four K32 steps of a block's MMA, by the elected lane.  lo: low words of the operands'
+// descriptors; a K step of 32 bytes inside the swizzle atom adds 2.
+__device__ __forceinline__ void mma_block(uint32_t d, uint32_t a_lo, uint32_t w_lo, uint32_t idesc, uint32_t elected) {
+    constexpr uint32_t HI = (uint32_t)(tc::DESC_HI >> 32);
+    asm volatile(
+        "{\n .reg .pred q, t;\n .reg .b64 a, w;\n .reg .b32 x, y;\n"
+        " setp.ne.b32 q, %5, 0;\n setp.ne.b32 t, 0, 0;\n"
+        " mov.b64 a, {%1, %4};\n mov.b64 w, {%2, %4};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, w, %3, t;\n"
+        " setp.eq.b32 t, 0, 0;\n"
+        " add.u32 x, %1, 2;\n add.u32 y, %2, 2;\n mov.b64 a, {x, %4};\n mov.b64 w, {y, %4};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, w, %3, t;\n"
+        " add.u32 x, %1, 4;\n add.u32 y, %2, 4;\n mov.b64 a, {x, %4};\n mov.b64 w, {y, %4};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, w, %3, t;\n"
+        " add.u32 x, %1, 6;\n add.u32 y, %2, 6;\n mov.b64 a, {x, %4};\n mov.b64 w, {y, %4};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, w, %3, t;\n}" ::"r"(d),
+        "r"(a_lo), "r"(w_lo), "r"(idesc), "n"(HI), "r"(elected)
         : "memory");
 }
 
@@ -100,9 +167,11 @@ __device__ __forceinline__ uint32_t cluster_size() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+// Relaxed: after mbarrier.init and its own fence.  Releasing: orders this thread's accesses to its
+// peers' shared memory before the arrival.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_release() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
@@ -140,27 +209,46 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     }
 }
 
-__device__ __forceinline__ float load_sa(const Args& a, int kb, int row) {
-    const int64_t at = (int64_t)kb * a.ld_sa + row;
-    return a.e8m0 ? e8m0_to_f32(static_cast<const uint8_t*>(a.sa)[at]) : static_cast<const float*>(a.sa)[at];
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+// An arrival on `bar` once this thread's earlier cp.async copies have landed (counted in the
+// barrier's expected arrivals).
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// GRP: K blocks per TMEM buffer (and per commit).  A thread's pieces are 16
-// columns each, 8 per buffer: PPK = 8 / GRP pieces per block.
+// Batch b of a thread's accumulator columns: PIECE consecutive ones of the sequence
+// (K block of the group, column of the half).
+template <int HALF, int COLS, int PIECE>
+__device__ __forceinline__ void ld_batch(uint32_t tb, int b, uint32_t (&raw)[PIECE]) {
+    constexpr int W = HALF < 32 ? 16 : 32;
+#pragma unroll
+    for (int t = 0; t < PIECE; t += W) {
+        const int seq = b * PIECE + t;
+        const uint32_t at = tb + (uint32_t)((seq / HALF) * COLS + seq % HALF);
+        if constexpr (W == 32) tc::tmem_ld32u(at, reinterpret_cast<uint32_t(&)[32]>(raw[t]));
+        else tc::tmem_ld16u(at, reinterpret_cast<uint32_t(&)[16]>(raw[t]));
+    }
+}
+
+// GRP: K blocks per stage, per TMEM buffer and per commit.
 template <int GRP, bool GATED>
-__global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_constant__ CUtensorMap ta, Args a) {
+__global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
     constexpr int COLS = BUF_COLS / GRP;      // columns reserved per K block
     constexpr int HALF = COLS / 2;            // accumulators per thread
-    constexpr int PPK = HALF / 16;
+    constexpr int PIECE = GRP == 1 ? 32 : 64; // columns per batch of tensor-memory loads (two in registers)
+    constexpr int NB = GRP * HALF / PIECE;    // batches per buffer
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int w_bytes = a.bn * 128, a_bytes = a.a_rows * 128;
     const int stage_bytes = GRP * (w_bytes + a_bytes);
-    // behind the ring, in this order, so that the last block's 128-row operand read stays inside
-    uint8_t* after = ring + a.stages * stage_bytes;
-    float* stg_all = reinterpret_cast<float*>(after);
-    float* amax_cta = reinterpret_cast<float*>(after + STG_BYTES);              // [half][128]
-    float* amax_all = amax_cta + 2 * BM;                                        // [parity][rank][128]
+    const int pitch = sa_pitch(a.a_rows, a.e8m0), slot_bytes = scale_slot(GRP, a.a_rows, a.e8m0);
+    uint8_t* tail = ring + a.stages * stage_bytes;
+    float* stg_all = reinterpret_cast<float*>(tail);                            // plain
+    float* amax_cta = reinterpret_cast<float*>(tail);                           // gated: [half][128]
+    float* amax_all = amax_cta + 2 * BM;                                        // gated: [parity][rank][128]
+    uint8_t* scales = tail + (GATED ? TAIL_GATED : TAIL_PLAIN);                 // [stage][slot_bytes]
     __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES], tfull[2], tempty[2], xbar[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
@@ -170,18 +258,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
     const int first = blockIdx.x / csize, step = gridDim.x / csize;   // units go to clusters
     const int n_grp = (a.kt + GRP - 1) / GRP;
 
+    pdl_trigger();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+        for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], 1 + 32); mbar_init(&empty[s], EPI_WARPS); }
         for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], EPI_WARPS); mbar_init(&xbar[b], 1); }
         fence_mbar_init();
         abort_flag = 0;
     }
-    if (warp == 1) tc::tmem_alloc(&tmem_slot, 512);
-    tc::tc_fence_before();
     __syncthreads();
-    if (GATED && csize > 1) cluster_sync();     // peers' barriers exist before anything is sent to them
-    tc::tc_fence_after();
-    const uint32_t tmem = tmem_slot;
+    if (GATED && csize > 1) cluster_arrive();   // waited for before anything is sent to a peer
     volatile int* abort = &abort_flag;
 
     // unit -> token tile and first weight row
@@ -193,31 +278,44 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
 
     if (warp < CTRL_WARPS) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CTRL_REGS));
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
             // ------------------------------------------------ producer
+            const uint32_t el = elect_one();
+            if (el) {
+                prefetch_map(&maps.w);
+                prefetch_map(&maps.a);
+                prefetch_map(&maps.s);
+            }
+            const uint32_t ring0 = smem_addr(ring), scl0 = smem_addr(scales), full0 = smem_addr(full);
             auto copy_w = [&](int stage, int n0, int g) {
-                const int nk = min(GRP, a.kt - g * GRP);
-                const int rows = max(0, min(a.bn, a.rows_pad - n0));
-                mbar_arrive_expect_tx(&full[stage], (uint32_t)(nk * (rows * 128 + a_bytes)));
-                if (rows > 0)
-                    for (int i = 0; i < nk; ++i)
-                        bulk_g2s(ring + stage * stage_bytes + i * w_bytes,
-                                 a.w + ((size_t)(g * GRP + i) * a.rows_pad + n0) * 128, (uint32_t)(rows * 128),
-                                 &full[stage]);
+                const int nk = a.a_whole ? GRP : min(GRP, a.kt - g * GRP);
+                const uint32_t bytes = (uint32_t)(GRP * (w_bytes + pitch) + nk * a_bytes);
+                if (el) {
+                    expect_tx(full0 + 8 * stage, bytes);
+                    tma_load_3d(ring0 + stage * stage_bytes, &maps.w, 0, n0, g * GRP, full0 + 8 * stage);
+                }
             };
             auto copy_a = [&](int stage, int m0, int g) {
-                const int nk = min(GRP, a.kt - g * GRP);
-                for (int i = 0; i < nk; ++i)
-                    tma_load_2d(ring + stage * stage_bytes + GRP * w_bytes + i * a_bytes, &ta, (g * GRP + i) * QB, m0,
-                                &full[stage]);
+                const uint32_t dst = ring0 + stage * stage_bytes + GRP * w_bytes, bar = full0 + 8 * stage;
+                if (el) {
+                    tma_load_2d(scl0 + stage * slot_bytes, &maps.s, m0, g * GRP, bar);
+                    if (a.a_whole) {
+                        tma_load_3d(dst, &maps.a, 0, m0, g * GRP, bar);
+                    } else {
+                        const int nk = min(GRP, a.kt - g * GRP);
+                        for (int i = 0; i < nk; ++i)
+                            tma_load_3d(dst + i * a_bytes, &maps.a, (g * GRP + i) * QB, m0, 0, bar);
+                    }
+                }
             };
             int stage = 0;
-            uint32_t phase = 0, armed = 0, armed_par = 0;
+            uint32_t phase = 0;
+            int issued = 0;
             bool ok = true;
             // the weights do not depend on the preceding kernel: the first unit's stages are
             // requested before the wait for it
             int pre = 0;
-            if (first < a.n_units) {
+            {
                 int m0, n0;
                 unit_rows(first, m0, n0);
                 for (; pre < min(a.stages, n_grp); ++pre) copy_w(pre, n0, pre);
@@ -230,51 +328,78 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
                     if (pre > 0) {
                         --pre;
                     } else {
-                        if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, a.wait_limit, a.status, abort)) {
-                            ok = false;
-                            break;
-                        }
+                        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[stage], phase ^ 1u, a.wait_limit, a.status, abort));
+                        if (!ok) break;
                         copy_w(stage, n0, g);
                     }
                     copy_a(stage, m0, g);
-                    armed |= 1u << stage;
-                    armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
+                    issued = min(issued + 1, a.stages);
                     if (++stage == a.stages) { stage = 0; phase ^= 1u; }
                 }
             }
-            // every issued copy lands before the CTA exits
-            for (int s = 0; s < a.stages; ++s)
-                if ((armed >> s) & 1u) mbar_wait_bounded(&full[s], (armed_par >> s) & 1u, a.wait_limit, a.status, nullptr);
-        } else if (warp == 1 && lane == 0) {
+            // every issued copy lands before the CTA exits: the last `issued` stages, newest first
+            for (; issued > 0; --issued) {
+                if (--stage < 0) { stage = a.stages - 1; phase ^= 1u; }
+                mbar_wait_bounded(&full[stage], phase, a.wait_limit, a.status, nullptr);
+            }
+        } else if (warp == 1) {
+            tc::tmem_alloc(&tmem_slot, 512);
+            tc::tc_fence_before();
+            named_bar_sync(2, (1 + EPI_WARPS) * 32);            // the drain warps read the address
+            tc::tc_fence_after();
             // ------------------------------------------------ MMA issuer
+            const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_slot, 0);
+            const uint32_t el = elect_one();
+            const uint32_t idesc = idesc_for(a.bn);
+            const uint32_t d0 = (uint32_t)tc::sw128_desc(smem_addr(ring));
             int stage = 0, buf = 0;
             uint32_t phase = 0, tphase = 0;
             bool ok = true;
-            const uint32_t idesc = idesc_for(a.bn);
-            const uint64_t d0 = tc::sw128_desc(smem_addr(ring));
             for (int u = first; u < a.n_units && ok; u += step) {
                 for (int g = 0; g < n_grp; ++g) {
-                    if (!mbar_wait_bounded(&full[stage], phase, a.wait_limit, a.status, abort) ||
-                        !mbar_wait_bounded(&tempty[buf], tphase ^ 1u, a.wait_limit, a.status, abort)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[stage], phase, a.wait_limit, a.status, abort) &&
+                                                     mbar_wait_bounded(&tempty[buf], tphase ^ 1u, a.wait_limit, a.status, abort));
+                    if (!ok) break;
                     tc::tc_fence_after();
                     const int nk = min(GRP, a.kt - g * GRP);
+                    uint32_t wd = d0 + (uint32_t)((stage * stage_bytes) >> 4);
+                    uint32_t ad = wd + (uint32_t)((GRP * w_bytes) >> 4);
+                    uint32_t dt = tmem + (uint32_t)(buf * BUF_COLS);
                     for (int i = 0; i < nk; ++i) {
-                        const uint64_t wd = d0 + (uint64_t)((stage * stage_bytes + i * w_bytes) >> 4);
-                        const uint64_t ad = d0 + (uint64_t)((stage * stage_bytes + GRP * w_bytes + i * a_bytes) >> 4);
-                        const uint32_t dt = tmem + (uint32_t)(buf * BUF_COLS + i * COLS);
-                        tc::mma_f8(dt, ad, wd, idesc, 0u);
-                        tc::mma_f8(dt, ad + 2, wd + 2, idesc, 1u);
-                        tc::mma_f8(dt, ad + 4, wd + 4, idesc, 1u);
-                        tc::mma_f8(dt, ad + 6, wd + 6, idesc, 1u);
+                        mma_block(dt, ad, wd, idesc, el);
+                        wd += (uint32_t)(w_bytes >> 4);
+                        ad += (uint32_t)(a_bytes >> 4);
+                        dt += (uint32_t)COLS;
                     }
-                    tc::mma_commit(&tfull[buf]);        // a drain warp hands the stage back after this
+                    if (el) tc::mma_commit(&tfull[buf]);        // the drain warps hand the stage back after this
+                    __syncwarp();
                     if (++stage == a.stages) { stage = 0; phase ^= 1u; }
                     if (++buf == 2) { buf = 0; tphase ^= 1u; }
                 }
             }
+        } else if (warp == 2) {
+            // ------------------------------------------------ weight scales: [block of the group][first, second]
+            // plain: the scale blocks of the tile's first column and the next; gated: gate and up
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            const int i = lane >> 1;
+            for (int u = first; u < a.n_units && ok; u += step) {
+                int m0, n0;
+                unit_rows(u, m0, n0);
+                const int blk = GATED ? min(n0 / (2 * QB), a.nblk - 1) + (lane & 1) * a.nblk
+                                      : min(n0 / QB + (lane & 1), a.nblk - 1);
+                const float* src = a.sw + (size_t)blk * a.kt;
+                for (int g = 0; g < n_grp; ++g) {
+                    if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, a.wait_limit, a.status, abort)) ok = false;
+                    if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+                    if (i < GRP && g * GRP + i < a.kt)
+                        cp_async4(scales + stage * slot_bytes + GRP * pitch + lane * 4, src + g * GRP + i);
+                    cp_async_arrive(&full[stage]);
+                    if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
         __syncwarp();
     } else {
@@ -283,9 +408,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
         const int ew = warp - CTRL_WARPS;
         const int quarter = warp & 3, half = ew >> 2;
         const int r = quarter * 32 + lane;                     // token row of the tile = TMEM lane
+        const int rs = min(r, a.a_rows - 1);                   // row whose scale this thread reads
+        named_bar_sync(2, (1 + EPI_WARPS) * 32);
+        tc::tc_fence_after();
+        const uint32_t tmem = tmem_slot + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * HALF);
         pdl_wait();
+        if (GATED && csize > 1) cluster_wait();
         int buf = 0, stage = 0, parity = 0;
-        uint32_t tphase = 0, xphase = 0;
+        uint32_t tphase = 0, phase = 0, xphase = 0;
         bool dead = false;
         for (int u = first; u < a.n_units; u += step) {
             int m0, n0;
@@ -294,72 +424,85 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
             const bool rv = r < valid;
             const bool live = quarter * 32 < valid;            // warp-uniform: some lane has a token
             const int col0 = n0 + half * HALF;                 // first weight-image row of this thread's columns
-            // weight scales: plain, the blocks of the half's first column and the next one (16-column
-            // piece p lies in the second where bit p of hi_mask is set); gated, gate and up of the unit's block
-            const float *sw0, *sw1;
+            // plain: bit p is set where the 16-column piece p lies in the second scale block
             uint32_t hi_mask = 0;
-            if (GATED) {
-                const int fb = min(n0 / (2 * QB), a.nblk - 1);
-                sw0 = a.sw + (size_t)fb * a.kt;
-                sw1 = sw0 + (size_t)a.nblk * a.kt;
-            } else {
-                const int b0 = col0 / QB;
-                sw0 = a.sw + (size_t)min(b0, a.nblk - 1) * a.kt;
-                sw1 = a.sw + (size_t)min(b0 + 1, a.nblk - 1) * a.kt;
+            if (!GATED) {
 #pragma unroll
-                for (int p = 0; p < PPK; ++p) hi_mask |= ((col0 + 16 * p) / QB != b0) ? 1u << p : 0u;
+                for (int p = 0; p < HALF / 16; ++p) hi_mask |= ((col0 + 16 * p) / QB != n0 / QB) ? 1u << p : 0u;
             }
             float acc[HALF];
 #pragma unroll
             for (int c = 0; c < HALF; ++c) acc[c] = 0.f;
-            float nx[GRP] = {}, n0s[GRP] = {}, n1s[GRP] = {};  // scales of the next group, fetched one group ahead
-            auto fetch = [&](int g) {
-#pragma unroll
-                for (int i = 0; i < GRP; ++i) {
-                    const int kb = g * GRP + i;
-                    const bool in = kb < a.kt;
-                    nx[i] = in && rv ? load_sa(a, kb, m0 + r) : 0.f;
-                    n0s[i] = in ? sw0[kb] : 0.f;
-                    n1s[i] = in ? sw1[kb] : 0.f;
-                }
-            };
-            if (live) fetch(0);
-            for (int g = 0; g < n_grp; ++g) {
-                float c0[GRP], c1[GRP];
-#pragma unroll
-                for (int i = 0; i < GRP; ++i) { c0[i] = nx[i] * n0s[i]; c1[i] = nx[i] * n1s[i]; }
-                if (live && g + 1 < n_grp) fetch(g + 1);
-                if (!dead && !mbar_wait_bounded(&tfull[buf], tphase, a.wait_limit, a.status, abort)) dead = true;
+            float c0[GRP], c1[GRP];                            // combined scales of the group being drained
+            uint32_t pa[PIECE], pb[PIECE];
+            // Waits for the group in (buf, stage), starts its first batch, takes its scales and
+            // hands the stage back.
+            auto open = [&](float (&d0)[GRP], float (&d1)[GRP]) {
+                if (!dead && !(mbar_wait_bounded(&tfull[buf], tphase, a.wait_limit, a.status, abort) &&
+                               mbar_wait_bounded(&full[stage], phase, a.wait_limit, a.status, abort)))
+                    dead = true;
                 dead = __any_sync(0xFFFFFFFFu, dead);          // warp-uniform: tcgen05.ld is warp-collective
-                if (ew == 0 && lane == 0) mbar_arrive(&empty[stage]);
                 if (!dead && live) {
                     tc::tc_fence_after();
-                    const uint32_t tb = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * BUF_COLS + half * HALF);
-                    auto col_of = [&](int j) -> uint32_t { return (uint32_t)((j / PPK) * COLS + (j % PPK) * 16); };
-                    uint32_t pa[16], pb[16];
-                    tc::tmem_ld16u(tb + col_of(0), pa);
-                    tc::tmem_wait_ld();
+                    ld_batch<HALF, COLS, PIECE>(tmem + buf * BUF_COLS, 0, pa);
+                    const uint8_t* sl = scales + stage * slot_bytes;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        uint32_t(&cur)[16] = (j & 1) ? pb : pa;
-                        uint32_t(&nxt)[16] = (j & 1) ? pa : pb;
-                        if (j < 7) tc::tmem_ld16u(tb + col_of(j + 1), nxt);
-                        const int i = j / PPK, p = j % PPK;
-                        if (g * GRP + i < a.kt) {
-                            const float cl = GATED ? c0[i] : (((hi_mask >> p) & 1u) ? c1[i] : c0[i]);
-                            const float ch = GATED ? c1[i] : cl;
-#pragma unroll
-                            for (int q = 0; q < 16; q += 2)
-                                tc::fma2(acc[16 * p + q], acc[16 * p + q + 1], cur[q], cur[q + 1], q < 8 ? cl : ch);
-                        }
-                        if (j < 7) tc::tmem_wait_ld();
+                    for (int i = 0; i < GRP; ++i) {
+                        const float sx = a.e8m0 ? e8m0_to_f32(sl[i * pitch + rs])
+                                                : reinterpret_cast<const float*>(sl + i * pitch)[rs];
+                        const float2 sw = *reinterpret_cast<const float2*>(sl + GRP * pitch + i * 8);
+                        d0[i] = sx * sw.x;
+                        d1[i] = sx * sw.y;
                     }
-                    tc::tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&tempty[buf]);
-                if (++buf == 2) { buf = 0; tphase ^= 1u; }
-                if (++stage == a.stages) stage = 0;
+                if (lane == 0) mbar_arrive(&empty[stage]);
+                if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+            };
+            open(c0, c1);
+            for (int g = 0; g < n_grp; ++g) {
+                const int nk = min(GRP, a.kt - g * GRP);
+                // Without a branch between the products of a block: a partial group (the last) is
+                // told apart per block, outside the column loop.
+                auto add = [&](int b, uint32_t (&raw)[PIECE]) {
+                    constexpr int RUN = HALF < PIECE ? HALF : PIECE;
+#pragma unroll
+                    for (int t0 = 0; t0 < PIECE; t0 += RUN) {
+                        const int i = (b * PIECE + t0) / HALF;
+                        if (GRP > 1 && i >= nk) break;
+#pragma unroll
+                        for (int t = t0; t < t0 + RUN; t += 2) {
+                            const int c = (b * PIECE + t) % HALF;
+                            const float k = GATED ? ((c & 8) ? c1[i] : c0[i]) : (((hi_mask >> (c / 16)) & 1u) ? c1[i] : c0[i]);
+                            tc::fma2(acc[c], acc[c + 1], raw[t], raw[t + 1], k);
+                        }
+                    }
+                };
+                float e0[GRP], e1[GRP];
+                const bool work = !dead && live;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    uint32_t(&cur)[PIECE] = (b & 1) ? pb : pa;
+                    uint32_t(&nxt)[PIECE] = (b & 1) ? pa : pb;
+                    if (work) tc::tmem_wait_ld();
+                    if (b < NB - 1) {
+                        if (work) ld_batch<HALF, COLS, PIECE>(tmem + buf * BUF_COLS, b + 1, nxt);
+                    } else {
+                        // the buffer is in registers: hand it back, and start on the next group
+                        // before this one's last products are added
+                        static_assert(NB % 2 == 0, "the next group's first batch goes into pa");
+                        tc::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&tempty[buf]);
+                        if (++buf == 2) { buf = 0; tphase ^= 1u; }
+                        if (g + 1 < n_grp) open(e0, e1);
+                    }
+                    if (work) add(b, cur);
+                }
+                if (g + 1 < n_grp) {
+#pragma unroll
+                    for (int i = 0; i < GRP; ++i) { c0[i] = e0[i]; c1[i] = e1[i]; }
+                }
             }
 
             if constexpr (GATED) {
@@ -419,7 +562,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
                 // instruction covers whole 32-byte sectors of 8 rows
                 float* stg = stg_all + (size_t)ew * 32 * STG_STRIDE;
 #pragma unroll
-                for (int p = 0; p < PPK; ++p) {
+                for (int p = 0; p < HALF / 16; ++p) {
                     const int cb = col0 + 16 * p;
                     if (cb >= a.N || half * HALF + 16 * p >= a.bn) continue;     // warp-uniform
 #pragma unroll
@@ -461,11 +604,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
             }
         }
     }
+    if (GATED && csize > 1 && warp < CTRL_WARPS) cluster_wait();
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    if (warp == 1) tc::tmem_dealloc(tmem, 512);
-    if (GATED && csize > 1) cluster_sync();     // nobody leaves while a peer may still send to it
+    if (warp == 1) tc::tmem_dealloc(tmem_slot, 512);
+    if (GATED && csize > 1) {                   // nobody leaves while a peer may still send to it
+        cluster_arrive_release();
+        cluster_wait();
+    }
 }
 
 // ------------------------------------------------------------------ launch
@@ -473,13 +620,49 @@ struct Plan {
     int grp, bn, cluster, units, n_nt;
 };
 
+// Tensor maps of one call.  Token codes: [K block][row][128 B] (the K blocks of a row lie side by
+// side), 128-byte swizzle; with a ragged last block, [1][row][K], so that the copy fills zeros past
+// K.  Weight image: [K block][row][128 B], swizzled already.  Scales: [K block][row].  Rows and
+// blocks past the end are filled with zeros.
+inline bool encode_maps(const GemmCall& c, const Args& a, int grp, Maps* m) {
+    EncodeTiledFn enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t K = c.lin->d.in_features, kt = a.kt, M = c.M;
+    const cuuint32_t one[3] = {1, 1, 1};
+    const cuuint64_t ad[3] = {a.a_whole ? (cuuint64_t)QB : K, M, a.a_whole ? kt : 1};
+    const cuuint64_t as[2] = {(cuuint64_t)c.ld_aq, (cuuint64_t)QB};
+    const cuuint32_t ab[3] = {(cuuint32_t)QB, (cuuint32_t)a.a_rows, a.a_whole ? (cuuint32_t)grp : 1u};
+    const cuuint64_t wd[3] = {(cuuint64_t)QB, (cuuint64_t)a.rows_pad, kt}, ws[2] = {(cuuint64_t)QB, (cuuint64_t)a.rows_pad * QB};
+    const cuuint32_t wb[3] = {(cuuint32_t)QB, (cuuint32_t)a.bn, (cuuint32_t)grp};
+    const int es = a.e8m0 ? 1 : 4;
+    const cuuint64_t sd[2] = {M, kt}, ss[1] = {(cuuint64_t)(a.ld_sa * es)};
+    const cuuint32_t sb[2] = {(cuuint32_t)(sa_pitch(a.a_rows, a.e8m0) / es), (cuuint32_t)grp};
+    const auto none = CU_TENSOR_MAP_INTERLEAVE_NONE;
+    const auto fill = CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE;
+    return enc(&m->a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(c.aq), ad, as, ab, one, none,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, fill) == CUDA_SUCCESS &&
+           enc(&m->w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.lin->w, wd, ws, wb, one, none, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, fill) == CUDA_SUCCESS &&
+           enc(&m->s, a.e8m0 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(c.as), sd,
+               ss, sb, one, none, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, fill) == CUDA_SUCCESS;
+}
+
 template <int GRP, bool GATED>
-cudaError_t launch(const GemmCall& c, const Plan& p, Args& a, const CUtensorMap& map, cudaStream_t s) {
-    a.stages = std::min(MAX_STAGES, RING_MAX / (GRP * (a.bn + a.a_rows) * 128));
-    // 16 KB behind the ring: the last block's operand read of a short token tile ends inside it
-    // (STG_BYTES + AMAX_BYTES + 1 KB lie there)
-    static_assert(STG_BYTES + AMAX_BYTES >= BM * 128, "operand read past the ring");
-    const int smem = 1024 + a.stages * GRP * (a.bn + a.a_rows) * 128 + STG_BYTES + AMAX_BYTES + 2 * BM * 4;
+cudaError_t launch(const GemmCall& c, const Plan& p, Args& a, cudaStream_t s) {
+    a.bn = p.bn;
+    a.n_nt = p.n_nt;
+    a.n_units = p.units;
+    a.a_whole = c.lin->d.in_features % QB == 0;
+    Maps maps;
+    if (!encode_maps(c, a, GRP, &maps)) return cudaErrorInvalidValue;
+    // A call of one wave at most takes half of the SM's shared memory where that holds two stages
+    // (or all the blocks there are): the next kernel's CTA can then start beside it.
+    const int cost = stage_cost(GRP, a.bn, a.a_rows, a.e8m0), fixed = 1024 + (GATED ? TAIL_GATED : TAIL_PLAIN);
+    const int n_grp = (a.kt + GRP - 1) / GRP;
+    const int half = (SMEM_HALF - fixed) / cost;
+    const bool small = (long long)p.units * p.cluster <= c.lin->num_sms && half >= std::min(2, n_grp);
+    a.stages = std::max(1, std::min(std::min(MAX_STAGES, small ? half : (SMEM_MAX - fixed) / cost), std::max(2, n_grp)));
+    const int smem = fixed + a.stages * cost;
     cudaError_t e = ensure_smem_limit<fp8_gemm_kernel<GRP, GATED>>(SMEM_MAX);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -512,19 +695,7 @@ cudaError_t launch(const GemmCall& c, const Plan& p, Args& a, const CUtensorMap&
         }
     }
     cfg.gridDim = dim3(std::min(p.units, slots) * p.cluster);
-    return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<GRP, GATED>, map, a);
-}
-
-inline cudaError_t encode_a(const GemmCall& c, int a_rows, CUtensorMap* map) {
-    EncodeTiledFn enc = tensor_map_encoder();
-    if (!enc) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {(cuuint64_t)c.lin->d.in_features, (cuuint64_t)c.M};
-    const cuuint64_t strides[1] = {(cuuint64_t)c.ld_aq};
-    const cuuint32_t box[2] = {128, (cuuint32_t)a_rows}, one[2] = {1, 1};
-    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(c.aq), dims, strides, box, one,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+    return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<GRP, GATED>, maps, a);
 }
 
 inline Args base_args(const GemmCall& c) {

@@ -18,7 +18,7 @@ static Plan plan_plain(const GemmCall& c, const Args& a) {
     for (int bn = 16; bn <= BUF_COLS; bn += 16) {
         const int grp = bn <= 32 ? 8 : bn <= 64 ? 4 : bn <= 128 ? 2 : 1;
         if (grp == 1 && bn != 256) continue;                   // 256: both halves in whole scale blocks
-        if (2 * grp * (bn + a.a_rows) * 128 > RING_MAX) continue;
+        if (2 * stage_cost(grp, bn, a.a_rows, a.e8m0) > ring_max(false)) continue;
         const int nt = (rows + bn - 1) / bn;
         const long long units = (long long)mt * nt;
         if (units > 0x3FFFFFFF) continue;
@@ -41,6 +41,7 @@ static Plan plan_plain(const GemmCall& c, const Args& a) {
 
 cudaError_t launch_fp8_linear(const GemmCall& c, cudaStream_t s) {
     using namespace dg;
+    if (few_tokens(c, false)) return launch_fp8_few(c, false, s);
     Args a = base_args(c);
     a.y = c.y;
     a.ldy = c.ldy;
@@ -49,17 +50,11 @@ cudaError_t launch_fp8_linear(const GemmCall& c, cudaStream_t s) {
     a.y_vec = c.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(c.y) % (c.y_f32 ? 16 : 8) == 0;
     const Plan p = plan_plain(c, a);
     if (!p.bn) return cudaErrorInvalidValue;
-    a.bn = p.bn;
-    a.n_nt = p.n_nt;
-    a.n_units = p.units;
-    CUtensorMap map;
-    cudaError_t e = encode_a(c, a.a_rows, &map);
-    if (e != cudaSuccess) return e;
     switch (p.grp) {
-        case 1: return launch<1, false>(c, p, a, map, s);
-        case 2: return launch<2, false>(c, p, a, map, s);
-        case 4: return launch<4, false>(c, p, a, map, s);
-        default: return launch<8, false>(c, p, a, map, s);
+        case 1: return launch<1, false>(c, p, a, s);
+        case 2: return launch<2, false>(c, p, a, s);
+        case 4: return launch<4, false>(c, p, a, s);
+        default: return launch<8, false>(c, p, a, s);
     }
 }
 

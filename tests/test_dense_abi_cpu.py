@@ -15,7 +15,7 @@ def lib():
 def norm_args(**over):
     a = moe.MoeRmsnormArgs(rows=2, cols=256, x_type=moe.BF16, res_type=moe.BF16, x=0x1000, ldx=256, res=0x2000,
                            ld_res=256, weight=0x3000, res_out=0x4000, ld_res_out=256, y=0x5000, ldy=256, eps=1e-6)
-    a.out = moe.MoeFp8Matrix(0x6000, 0x7000, 256, 2, moe.SCALE_F32, 0)
+    a.out = moe.MoeFp8Matrix(0x6000, 0x7000, 256, 4, moe.SCALE_F32, 0)
     for k, v in over.items():
         if k.startswith("out_"):
             setattr(a.out, k[4:], v)
@@ -29,7 +29,7 @@ def norm_args(**over):
     (dict(x_type=moe.F32), 2), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(x=None), 1), (dict(weight=None), 1),
     (dict(res=None), 1), (dict(x=0x1001), 1), (dict(ldx=255), 1), (dict(ld_res=255), 1), (dict(ld_res_out=0), 1),
     (dict(ldy=100), 1), (dict(out_q=None), 1), (dict(out_s=None), 1), (dict(out_ldq=250), 1), (dict(out_ldq=240), 1),
-    (dict(out_q=0x6008), 1), (dict(out_lds=1), 1), (dict(out_scale_type=2), 1), (dict(out_s=0x7002), 1),
+    (dict(out_q=0x6008), 1), (dict(out_lds=0), 1), (dict(out_lds=6), 1), (dict(out_scale_type=1), 1), (dict(out_scale_type=2), 1), (dict(out_s=0x7002), 1),
     (dict(y=None, res_out=None, out_q=None, out_s=None), 1),
 ])
 def test_norm_refuses_bad_arguments(lib, over, code):

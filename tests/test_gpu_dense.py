@@ -269,21 +269,25 @@ def test_gated_against_64_bits(moe, m, k, n, scale):
 
 @pytest.mark.parametrize("scale", ["f32", "e8m0"])
 def test_rows_do_not_depend_on_the_batch(moe, scale):
-    """Tile widths follow the batch size; a token's result does not."""
+    """Up to 64 tokens run one form of the product, more run another; inside
+    each, tile widths follow the batch size but a token's bits do not."""
     m, k, n = 700, 1160, 1400
     aq, a_s = rows_fp8(randn((m, k), 40), scale)
     w, u = blocks_fp8(randn((n, k), 41, 0.05), scale), blocks_fp8(randn((n, k), 42, 0.05), scale)
     lin, gated = moe.Fp8Linear(*w), moe.Fp8GatedLinear(*w, *u)
-    a = moe.Fp8Tensor.from_parts(aq, a_s)
-    y = lin(a, torch.empty(m, n, dtype=torch.float32, device="cuda"))
-    h = gated(a, moe.Fp8Tensor(m, n, scale))
-    for lo, hi in ((0, 1), (5, 25), (100, 150), (200, 328), (300, 560)):
-        part = moe.Fp8Tensor.from_parts(aq[lo:hi].clone(), a_s.view(torch.uint8 if scale == "e8m0" else torch.float32)[:, lo:hi]
-                                        .contiguous().view(a_s.dtype))
-        assert torch.equal(lin(part, torch.empty(hi - lo, n, dtype=torch.float32, device="cuda")), y[lo:hi])
-        hp = gated(part, moe.Fp8Tensor(hi - lo, n, scale))
-        assert torch.equal(hp.q.view(torch.uint8), h.q[lo:hi].view(torch.uint8))
-        assert torch.equal(hp.s.float(), h.s.float()[:, lo:hi])
+
+    def run(lo, hi):
+        s = a_s.view(torch.uint8 if scale == "e8m0" else torch.float32)[:, lo:hi].contiguous().view(a_s.dtype)
+        part = moe.Fp8Tensor.from_parts(aq[lo:hi].clone(), s)
+        h = gated(part, moe.Fp8Tensor(hi - lo, n, scale))
+        return (lin(part, torch.empty(hi - lo, n, dtype=torch.float32, device="cuda")), h.q.view(torch.uint8),
+                h.s.float().t())
+
+    for whole, parts in (((0, 64), ((0, 1), (5, 14), (20, 45), (10, 64))), ((0, m), ((0, 65), (100, 200), (200, 328), (300, 560)))):
+        ref = run(*whole)
+        for lo, hi in parts:
+            for got, want in zip(run(lo, hi), ref):
+                assert torch.equal(got, want[lo:hi])
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -442,7 +446,9 @@ def test_refusals(moe):
     refused(lambda: moe.moe_linear_forward(lin.handle, a.matrix, 4, y.data_ptr() + 2, 128, moe.F32))
     odd = moe.MoeFp8Matrix(a.q.data_ptr(), a.s.data_ptr(), 264, 4, 0, 0)
     refused(lambda: moe.moe_linear_forward(lin.handle, odd, 4, y.data_ptr(), 128, moe.F32))
-    short = moe.MoeFp8Matrix(a.q.data_ptr(), a.s.data_ptr(), 256, 3, 0, 0)
+    short = moe.MoeFp8Matrix(a.q.data_ptr(), a.s.data_ptr(), 256, 0, 0, 0)
+    ragged = moe.MoeFp8Matrix(a.q.data_ptr(), a.s.data_ptr(), 256, 5, 0, 0)
+    refused(lambda: moe.moe_linear_forward(lin.handle, ragged, 4, y.data_ptr(), 128, moe.F32))
     refused(lambda: moe.moe_linear_forward(lin.handle, short, 4, y.data_ptr(), 128, moe.F32))
     assert lin.device_status() == (0, 0) and gated.device_status() == (0, 0)
     lin(a, y)          # a refused call leaves the handle usable
