@@ -126,6 +126,8 @@ MOE_EXPORT moe_status moe_linear_create(const moe_linear_desc* d, const moe_line
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&L->num_sms, cudaDevAttrMultiProcessorCount, L->device);
     if (e == cudaSuccess) what = "allocating weights", e = cudaMalloc(&L->w, (size_t)L->kt * L->rows_pad * 128);
     if (e == cudaSuccess) what = "allocating scales", e = cudaMalloc(&L->sw, nsw * 4);
+    if (e == cudaSuccess && d->scale_type == MOE_SCALE_E8M0)
+        what = "allocating scale factors", e = cudaMalloc(&L->wsf, (size_t)((L->kt + 3) / 4) * ((L->rows_pad + moe::QB - 1) / moe::QB) * 512);
     if (e == cudaSuccess) what = "allocating status", e = cudaMalloc(&L->dev_status, 4);
     if (e == cudaSuccess) what = "memset", e = cudaMemsetAsync(L->dev_status, 0, 4, s);
     if (e == cudaSuccess)
@@ -134,7 +136,7 @@ MOE_EXPORT moe_status moe_linear_create(const moe_linear_desc* d, const moe_line
     if (e == cudaSuccess) what = "moe_linear_create synchronise", e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) {
         moe_status st = cuda_fail(e, what);
-        cudaFree(L->w); cudaFree(L->sw); cudaFree(L->dev_status);
+        cudaFree(L->w); cudaFree(L->sw); cudaFree(L->wsf); cudaFree(L->dev_status);
         delete L;
         return st;
     }
@@ -149,7 +151,7 @@ MOE_EXPORT moe_status moe_linear_destroy(moe_linear* L) {
     if (e == cudaSuccess && cur != L->device) e = cudaSetDevice(L->device);
     if (e != cudaSuccess) return cuda_fail(e, "moe_linear_destroy: selecting the weights' device");
     e = cudaDeviceSynchronize();
-    cudaFree(L->w); cudaFree(L->sw); cudaFree(L->dev_status);
+    cudaFree(L->w); cudaFree(L->sw); cudaFree(L->wsf); cudaFree(L->dev_status);
     const int dev = L->device;
     delete L;
     if (cur >= 0 && cur != dev) cudaSetDevice(cur);

@@ -14,6 +14,7 @@ struct moe_linear {
     int kt;                // K blocks: ceil(K / 128)
     uint8_t* w;            // [kt][rows_pad][128 B] E4M3, 128-byte swizzle, zeros past N and K
     float* sw;             // [1 or 2][ceil(N / 128)][kt] weight scales (gated: gate, then up)
+    uint8_t* wsf;          // e8m0: [ceil(kt / 4)][ceil(rows_pad / 128)][512 B] scale-factor blocks of the image's rows
     uint32_t* dev_status;  // device status word
     uint32_t wait_limit;
 };
@@ -80,6 +81,8 @@ cudaError_t launch_linear_repack(const moe_linear* L, const uint8_t* w, const vo
                                  const void* su, cudaStream_t st);
 cudaError_t launch_fp8_linear(const GemmCall& c, cudaStream_t s);
 cudaError_t launch_fp8_gated(const GemmCall& c, cudaStream_t s);
+bool mx_fits(const moe_linear* L);                      // whether the hardware-scaled form takes these weights
+cudaError_t launch_fp8_mx(const GemmCall& c, bool gated, cudaStream_t s);
 bool few_tokens(const GemmCall& c, bool gated);         // whether the few-token form takes the call
 cudaError_t launch_fp8_few(const GemmCall& c, bool gated, cudaStream_t s);
 

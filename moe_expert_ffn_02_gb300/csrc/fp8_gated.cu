@@ -40,6 +40,7 @@ static Plan plan_gated(const GemmCall& c, const Args& a) {
 cudaError_t launch_fp8_gated(const GemmCall& c, cudaStream_t s) {
     using namespace dg;
     if (few_tokens(c, true)) return launch_fp8_few(c, true, s);
+    if (mx_fits(c.lin)) return launch_fp8_mx(c, true, s);
     Args a = base_args(c);
     a.hq = c.hq;
     a.ld_hq = c.ld_hq;

@@ -232,6 +232,121 @@ __device__ __forceinline__ void ld_batch(uint32_t tb, int b, uint32_t (&raw)[PIE
     }
 }
 
+// ------------------------------------------------------------------ epilogues
+// One drain warp's place in the tile, and what the warps of the CTA (and cluster) share.
+struct EpiCtx {
+    int ew, quarter, half, lane;
+    uint32_t rank, csize;
+    float* stg;                    // plain: the warp's staging tile, 32 rows of STG_STRIDE floats
+    float* amax_cta;               // gated: [half][128]
+    float* amax_all;               // gated: [parity][rank][128]
+    uint64_t* xbar;                // gated: [parity]
+    int parity;
+    uint32_t xphase;
+    volatile int* abort;
+};
+
+// h = SiLU(g) * u of this thread's row and features, and its 1x128 E4M3 codes.  acc: pieces of 8
+// gate columns and the same 8 features' up columns.
+template <int HALF>
+__device__ __forceinline__ void epi_gated(const Args& a, EpiCtx& x, const float (&acc)[HALF], int m0, int n0, int valid,
+                                          bool& dead) {
+    const int r = x.quarter * 32 + x.lane;
+    const int f0 = (n0 + x.half * HALF) / 2;                   // first feature of this thread
+    float h[HALF / 2];
+    float am = 0.f;
+#pragma unroll
+    for (int e = 0; e < HALF / 2; ++e) {
+        const float gt = acc[(e / 8) * 16 + (e % 8)], up = acc[(e / 8) * 16 + 8 + (e % 8)];
+        h[e] = f0 + e < a.N ? silu_mul(gt, up) : 0.f;
+        am = max_nan(am, fabsf(h[e]));
+    }
+    x.amax_cta[x.half * BM + r] = am;
+    named_bar_sync(1, EPI_WARPS * 32);
+    am = max_nan(x.amax_cta[r], x.amax_cta[BM + r]);
+    if (x.csize > 1) {
+        // every CTA sends its rows' amax to every CTA of the cluster (itself included); a peer is
+        // at most one unit ahead, so two slots are enough
+        float* slot = x.amax_all + x.parity * MAX_CLUSTER * BM;
+        if (x.half == 0) {
+            const uint32_t mine = smem_addr(slot + x.rank * BM + r), bar = smem_addr(&x.xbar[x.parity]);
+            if (r == 0) mbar_arrive_expect_tx(&x.xbar[x.parity], x.csize * BM * 4u);
+            for (uint32_t p = 0; p < x.csize; ++p) st_async_f32(map_to_rank(mine, p), am, map_to_rank(bar, p));
+        }
+        if (!dead && !mbar_wait_cluster(&x.xbar[x.parity], x.xphase, a.wait_limit, a.status, x.abort)) dead = true;
+        for (uint32_t p = 0; p < x.csize; ++p) am = max_nan(am, slot[p * BM + r]);
+        if (++x.parity == 2) { x.parity = 0; x.xphase ^= 1u; }
+    }
+    uint32_t held;
+    // h / s as h * (1 / s): within one ulp of the quotient, far inside the code spacing
+    const float is = inv_scale(group_scale(am, a.e8m0, held));
+    if (r < valid && !dead) {
+        uint8_t* dst = a.hq + (int64_t)(m0 + r) * a.ld_hq + f0;
+#pragma unroll
+        for (int e = 0; e < HALF / 2; e += 8) {
+            const uint32_t lo = pack4_e4m3(h[e] * is, h[e + 1] * is, h[e + 2] * is, h[e + 3] * is);
+            const uint32_t hi = pack4_e4m3(h[e + 4] * is, h[e + 5] * is, h[e + 6] * is, h[e + 7] * is);
+            if (f0 + e + 8 <= a.N) {
+                *reinterpret_cast<uint2*>(dst + e) = make_uint2(lo, hi);
+            } else {
+                for (int b = 0; f0 + e + b < a.N; ++b) dst[e + b] = (uint8_t)((b < 4 ? lo : hi) >> (8 * (b & 3)));
+            }
+        }
+        if (x.half == 0 && x.rank == 0) {
+            const int64_t at = (int64_t)(n0 / (2 * QB)) * a.ld_hs + m0 + r;
+            if (a.e8m0) static_cast<uint8_t*>(a.hs)[at] = (uint8_t)held;
+            else static_cast<uint32_t*>(a.hs)[at] = held;
+        }
+    }
+    named_bar_sync(1, EPI_WARPS * 32);                         // amax_cta is reused by the next unit
+}
+
+// fp32 or bf16 rows: 16 columns at a time through the warp's staging tile, so that a store
+// instruction covers whole 32-byte sectors of 8 rows.
+template <int HALF>
+__device__ __forceinline__ void epi_plain(const Args& a, const EpiCtx& x, const float (&acc)[HALF], int m0, int n0, int valid) {
+    const int row0 = x.quarter * 32, lane = x.lane;
+#pragma unroll
+    for (int p = 0; p < HALF / 16; ++p) {
+        const int cb = n0 + x.half * HALF + 16 * p;
+        if (cb >= a.N || x.half * HALF + 16 * p >= a.bn) continue;           // warp-uniform
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(x.stg + lane * STG_STRIDE + 4 * i) =
+                make_float4(acc[16 * p + 4 * i], acc[16 * p + 4 * i + 1], acc[16 * p + 4 * i + 2], acc[16 * p + 4 * i + 3]);
+        __syncwarp();
+        if (a.y_vec && cb + 16 <= a.N) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int rr = 8 * t + (lane >> 2), c = 4 * (lane & 3);
+                const float4 v = *reinterpret_cast<const float4*>(x.stg + rr * STG_STRIDE + c);
+                if (row0 + rr < valid) {
+                    const int64_t at = (int64_t)(m0 + row0 + rr) * a.ldy + cb + c;
+                    if (a.y_f32) {
+                        *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = v;
+                    } else {
+                        __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
+                            make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+                    }
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int t = 0; t < 16; ++t) {
+                const int rr = 2 * t + (lane >> 4), c = lane & 15;
+                const float v = x.stg[rr * STG_STRIDE + c];
+                if (row0 + rr < valid && cb + c < a.N) {
+                    const int64_t at = (int64_t)(m0 + row0 + rr) * a.ldy + cb + c;
+                    if (a.y_f32) static_cast<float*>(a.y)[at] = v;
+                    else static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+                }
+            }
+        }
+        __syncwarp();
+    }
+}
+
 // GRP: K blocks per stage, per TMEM buffer and per commit.
 template <int GRP, bool GATED>
 __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
@@ -414,14 +529,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
         const uint32_t tmem = tmem_slot + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * HALF);
         pdl_wait();
         if (GATED && csize > 1) cluster_wait();
-        int buf = 0, stage = 0, parity = 0;
-        uint32_t tphase = 0, phase = 0, xphase = 0;
+        EpiCtx ctx = {ew, quarter, half, lane, rank, csize, stg_all + (size_t)ew * 32 * STG_STRIDE, amax_cta, amax_all, xbar, 0, 0u, abort};
+        int buf = 0, stage = 0;
+        uint32_t tphase = 0, phase = 0;
         bool dead = false;
         for (int u = first; u < a.n_units; u += step) {
             int m0, n0;
             unit_rows(u, m0, n0);
             const int valid = min(BM, a.M - m0);
-            const bool rv = r < valid;
             const bool live = quarter * 32 < valid;            // warp-uniform: some lane has a token
             const int col0 = n0 + half * HALF;                 // first weight-image row of this thread's columns
             // plain: bit p is set where the 16-column piece p lies in the second scale block
@@ -505,103 +620,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
                 }
             }
 
-            if constexpr (GATED) {
-                // piece p: 8 gate columns, then the same 8 features' up columns
-                const int f0 = col0 / 2;                       // first feature of this thread
-                float h[HALF / 2];
-                float am = 0.f;
-#pragma unroll
-                for (int e = 0; e < HALF / 2; ++e) {
-                    const float gt = acc[(e / 8) * 16 + (e % 8)], up = acc[(e / 8) * 16 + 8 + (e % 8)];
-                    h[e] = f0 + e < a.N ? silu_mul(gt, up) : 0.f;
-                    am = max_nan(am, fabsf(h[e]));
-                }
-                amax_cta[half * BM + r] = am;
-                named_bar_sync(1, EPI_WARPS * 32);
-                am = max_nan(amax_cta[r], amax_cta[BM + r]);
-                if (csize > 1) {
-                    // every CTA sends its rows' amax to every CTA of the cluster (itself included); a
-                    // peer is at most one unit ahead, so two slots are enough
-                    float* slot = amax_all + parity * MAX_CLUSTER * BM;
-                    if (half == 0) {
-                        const uint32_t mine = smem_addr(slot + rank * BM + r), bar = smem_addr(&xbar[parity]);
-                        if (r == 0) mbar_arrive_expect_tx(&xbar[parity], csize * BM * 4u);
-                        for (uint32_t p = 0; p < csize; ++p) st_async_f32(map_to_rank(mine, p), am, map_to_rank(bar, p));
-                    }
-                    if (!dead && !mbar_wait_cluster(&xbar[parity], xphase, a.wait_limit, a.status, abort)) dead = true;
-                    for (uint32_t p = 0; p < csize; ++p) am = max_nan(am, slot[p * BM + r]);
-                    if (++parity == 2) { parity = 0; xphase ^= 1u; }
-                }
-                uint32_t held;
-                const float sc = group_scale(am, a.e8m0, held);
-                const float is = inv_scale(sc);
-                if (rv && !dead) {
-                    uint8_t* dst = a.hq + (int64_t)(m0 + r) * a.ld_hq + f0;
-#pragma unroll
-                    for (int e = 0; e < HALF / 2; e += 8) {
-                        const uint32_t lo = pack4_e4m3(h[e] * is, h[e + 1] * is, h[e + 2] * is, h[e + 3] * is);
-                        const uint32_t hi = pack4_e4m3(h[e + 4] * is, h[e + 5] * is, h[e + 6] * is, h[e + 7] * is);
-                        if (f0 + e + 8 <= a.N) {
-                            *reinterpret_cast<uint2*>(dst + e) = make_uint2(lo, hi);
-                        } else {
-#pragma unroll
-                            for (int b = 0; b < 8; ++b)
-                                if (f0 + e + b < a.N) dst[e + b] = (uint8_t)((b < 4 ? lo >> (8 * b) : hi >> (8 * (b - 4))) & 0xFFu);
-                        }
-                    }
-                    const int fb = n0 / (2 * QB);
-                    if (half == 0 && rank == 0) {
-                        const int64_t at = (int64_t)fb * a.ld_hs + m0 + r;
-                        if (a.e8m0) static_cast<uint8_t*>(a.hs)[at] = (uint8_t)held;
-                        else static_cast<uint32_t*>(a.hs)[at] = held;
-                    }
-                }
-                named_bar_sync(1, EPI_WARPS * 32);             // amax_cta is reused by the next unit
-            } else if (live && !dead) {
-                // 16 columns at a time through the warp's staging tile, so that a store
-                // instruction covers whole 32-byte sectors of 8 rows
-                float* stg = stg_all + (size_t)ew * 32 * STG_STRIDE;
-#pragma unroll
-                for (int p = 0; p < HALF / 16; ++p) {
-                    const int cb = col0 + 16 * p;
-                    if (cb >= a.N || half * HALF + 16 * p >= a.bn) continue;     // warp-uniform
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<float4*>(stg + lane * STG_STRIDE + 4 * i) = make_float4(
-                            acc[16 * p + 4 * i], acc[16 * p + 4 * i + 1], acc[16 * p + 4 * i + 2], acc[16 * p + 4 * i + 3]);
-                    __syncwarp();
-                    if (a.y_vec && cb + 16 <= a.N) {
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const int rr = 8 * t + (lane >> 2), c = 4 * (lane & 3);
-                            const float4 v = *reinterpret_cast<const float4*>(stg + rr * STG_STRIDE + c);
-                            const int row = quarter * 32 + rr;
-                            if (row < valid) {
-                                const int64_t at = (int64_t)(m0 + row) * a.ldy + cb + c;
-                                if (a.y_f32) {
-                                    *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = v;
-                                } else {
-                                    __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-                                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
-                                        make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
-                                }
-                            }
-                        }
-                    } else {
-#pragma unroll 4
-                        for (int t = 0; t < 16; ++t) {
-                            const int rr = 2 * t + (lane >> 4), c = lane & 15, row = quarter * 32 + rr;
-                            const float v = stg[rr * STG_STRIDE + c];
-                            if (row < valid && cb + c < a.N) {
-                                const int64_t at = (int64_t)(m0 + row) * a.ldy + cb + c;
-                                if (a.y_f32) static_cast<float*>(a.y)[at] = v;
-                                else static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
-                            }
-                        }
-                    }
-                    __syncwarp();
-                }
-            }
+            if constexpr (GATED) epi_gated<HALF>(a, ctx, acc, m0, n0, valid, dead);
+            else if (live && !dead) epi_plain<HALF>(a, ctx, acc, m0, n0, valid);
         }
     }
     if (GATED && csize > 1 && warp < CTRL_WARPS) cluster_wait();

@@ -42,6 +42,7 @@ static Plan plan_plain(const GemmCall& c, const Args& a) {
 cudaError_t launch_fp8_linear(const GemmCall& c, cudaStream_t s) {
     using namespace dg;
     if (few_tokens(c, false)) return launch_fp8_few(c, false, s);
+    if (mx_fits(c.lin)) return launch_fp8_mx(c, false, s);
     Args a = base_args(c);
     a.y = c.y;
     a.ldy = c.ldy;
@@ -97,6 +98,20 @@ __global__ void linear_scales_kernel(const void* s, const void* su, int n, bool 
     }
 }
 
+// Scale-factor blocks for the tensor core's own scaling: 128 image rows x 4 K blocks in 512 bytes,
+// row r at (r mod 32) * 16 + (r / 32) * 4, one byte per K block.
+__global__ void linear_sf_kernel(const uint8_t* __restrict__ s, const uint8_t* __restrict__ su, int N, int kt, int rows_pad,
+                                 uint8_t* __restrict__ out) {
+    const int nrb = (rows_pad + QB - 1) / QB, nq = (kt + 3) / 4;
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < nq * nrb * 512; i += gridDim.x * blockDim.x) {
+        const int b = i & 511, rb = (i >> 9) % nrb, q = (i >> 9) / nrb;
+        const int r = rb * QB + ((b >> 2) & 3) * 32 + (b >> 4), kb = 4 * q + (b & 3);
+        const int f = su ? (r >> 4) * 8 + (r & 7) : r;
+        const uint8_t* src = su && (r & 8) ? su : s;
+        out[i] = f < N && kb < kt ? src[(size_t)(f / QB) * kt + kb] : 127;
+    }
+}
+
 cudaError_t launch_linear_repack(const moe_linear* L, const uint8_t* w, const void* s, const uint8_t* wu,
                                  const void* su, cudaStream_t st) {
     linear_image_kernel<<<8 * L->num_sms, 256, 0, st>>>(w, wu, L->d.out_features, L->d.in_features, L->kt, L->rows_pad,
@@ -105,6 +120,10 @@ cudaError_t launch_linear_repack(const moe_linear* L, const uint8_t* w, const vo
     if (e != cudaSuccess) return e;
     const int n = (L->d.out_features + QB - 1) / QB * L->kt;
     linear_scales_kernel<<<L->num_sms, 256, 0, st>>>(s, su, n, L->d.scale_type == MOE_SCALE_E8M0, L->sw);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !L->wsf) return e;
+    linear_sf_kernel<<<4 * L->num_sms, 256, 0, st>>>(static_cast<const uint8_t*>(s), static_cast<const uint8_t*>(su),
+                                                     L->d.out_features, L->kt, L->rows_pad, L->wsf);
     return cudaGetLastError();
 }
 
