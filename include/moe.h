@@ -380,6 +380,9 @@ typedef struct {
 } moe_rmsnorm_args;
 moe_status moe_add_rmsnorm(const moe_rmsnorm_args* args, void* stream);
 
+/* As moe_get_device_status, for the norms run on the current device. */
+moe_status moe_rmsnorm_device_status(void* stream, uint32_t* flags);
+
 /* Weights of a dense FP8 projection, copied into the library's tile layout
  * once; the caller may free its buffers afterwards.  Row-major E4M3FN
  * [out_features][in_features] with one scale per 128 x 128 block,

@@ -199,16 +199,28 @@ MOE_EXPORT moe_status moe_gated_linear_forward(moe_linear* L, const moe_fp8_matr
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "FP8 gated linear");
 }
 
-MOE_EXPORT moe_status moe_linear_device_status(moe_linear* L, void* stream, uint32_t* flags) {
-    moe_status st = check_linear(L);
-    if (st != MOE_OK) return st;
+namespace {
+// Synchronise, read and clear a device status word.
+moe_status read_status(uint32_t* word, void* stream, uint32_t* flags) {
     uint32_t v = 0;
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-    if (e == cudaSuccess) e = cudaMemcpy(&v, L->dev_status, 4, cudaMemcpyDeviceToHost);
-    if (e == cudaSuccess) e = cudaMemset(L->dev_status, 0, 4);
+    if (e == cudaSuccess) e = cudaMemcpy(&v, word, 4, cudaMemcpyDeviceToHost);
+    if (e == cudaSuccess && v) e = cudaMemset(word, 0, 4);
     if (e != cudaSuccess) return cuda_fail(e, "reading the status word");
     if (flags) *flags = v;
     if (v & MOE_DEV_WAIT_TIMEOUT) return fail(MOE_ERR_TIMEOUT, "a kernel wait gave up (status 0x%x)", v);
     if (v) return fail(MOE_ERR_DEVICE_CHECK, "a kernel flagged bad data (status 0x%x)", v);
     return MOE_OK;
+}
+}  // namespace
+
+MOE_EXPORT moe_status moe_linear_device_status(moe_linear* L, void* stream, uint32_t* flags) {
+    moe_status st = check_linear(L);
+    return st != MOE_OK ? st : read_status(L->dev_status, stream, flags);
+}
+
+MOE_EXPORT moe_status moe_rmsnorm_device_status(void* stream, uint32_t* flags) {
+    uint32_t* word = nullptr;
+    cudaError_t e = moe::norm_status_word(&word);
+    return e != cudaSuccess ? cuda_fail(e, "the norm's status word") : read_status(word, stream, flags);
 }

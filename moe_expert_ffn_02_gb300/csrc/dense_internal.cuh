@@ -77,6 +77,7 @@ struct GemmCall {
 };
 
 cudaError_t launch_rmsnorm(const moe_rmsnorm_args* a, cudaStream_t s);
+cudaError_t norm_status_word(uint32_t** p);             // the current device's
 cudaError_t launch_linear_repack(const moe_linear* L, const uint8_t* w, const void* s, const uint8_t* wu,
                                  const void* su, cudaStream_t st);
 cudaError_t launch_fp8_linear(const GemmCall& c, cudaStream_t s);

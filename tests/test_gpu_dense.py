@@ -141,6 +141,23 @@ def test_norm_against_64_bits(moe, types, scale, rows, cols):
     check_norm(moe, x, r, 1 + randn((cols,), 3, 0.2), scale)
 
 
+@pytest.mark.parametrize("types", ["bf16/bf16", "bf16/f32", "f32/f32", "bf16/-"])
+@pytest.mark.parametrize("rows,cols", [(1300, 264), (2500, 7168), (1217, 8), (1900, 4104), (1500, 16384), (3000, 1001), (1400, 8192)])
+def test_norm_of_many_rows(moe, types, rows, cols):
+    """Enough rows for the ring form, and sizes around its limits."""
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}
+    tx, tr = types.split("/")
+    x = randn((rows, cols), 1, dtype=dt[tx])
+    r = None if tr == "-" else randn((rows, cols), 2, 4.0, dt[tr])
+    ref_r = None if r is None else r.clone()
+    out, y, ro = check_norm(moe, x, r, 1 + randn((cols,), 3, 0.2), "f32")
+    if r is not None:        # the same in place
+        norm = moe.RmsNorm(1 + randn((cols,), 3, 0.2))
+        norm(x, ref_r, res_out=ref_r)
+        assert torch.equal(ref_r, ro)
+    assert moe.moe_rmsnorm_device_status(torch.cuda.current_stream().cuda_stream) == (0, 0)
+
+
 @pytest.mark.parametrize("scale", ["f32", "e8m0"])
 def test_norm_strides_and_alignment(moe, scale):
     """Rows inside wider, unaligned storage; only the rows' own elements are written."""
