@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -496,32 +497,32 @@ def _bad(message: str):
     raise MoeError(MOE_ERR_INVALID_ARG, message)
 
 
-def _stream(device) -> int:
-    """The current torch stream's handle; the tensors' device has to be current."""
+def _stream(dev: int) -> int:
+    """The current torch stream's handle on device `dev`, which has to be the
+    current device.  torch.cuda.current_stream() builds a Python object, which
+    takes longer than a small operator's launch; the raw handle does not."""
     import torch
-    if device.index != torch.cuda.current_device():
-        _bad(f"the tensors are on {device}, which is not the current device")
-    return torch.cuda.current_stream().cuda_stream
+    if dev != torch.cuda.current_device():
+        _bad(f"the tensors are on device {dev}, which is not the current one")
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw is not None else torch.cuda.current_stream().cuda_stream
 
 
-def _dtype_code(t, what: str) -> int:
+def _dtypes():
     import torch
-    if t.dtype is torch.bfloat16:
-        return BF16
-    if t.dtype is torch.float32:
-        return F32
-    _bad(f"{what} must be bfloat16 or float32, not {t.dtype}")
+    return {torch.bfloat16: BF16, torch.float32: F32}
 
 
-def _rows_of(t, rows: int, cols: int, what: str) -> int:
-    """Row stride of a [rows][cols] tensor with contiguous rows."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+def _rows_of(t, rows: int, cols: int, dev: int, what: str) -> int:
+    """Row stride of a [rows][cols] tensor with contiguous rows on device `dev`."""
+    if t.shape != (rows, cols):
         _bad(f"{what} must be [{rows}][{cols}], not {list(t.shape)}")
-    if not t.is_cuda:
-        _bad(f"{what} must be a CUDA tensor")
-    if cols > 1 and t.stride(1) != 1:
+    if t.get_device() != dev:
+        _bad(f"{what} must be on CUDA device {dev}")
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
         _bad(f"{what} must have contiguous rows")
-    return max(t.stride(0), cols) if rows <= 1 else t.stride(0)
+    return ld if rows > 1 or ld >= cols else cols
 
 
 class Fp8Tensor:
@@ -543,8 +544,10 @@ class Fp8Tensor:
 
     def _bind(self, q, s, scale):
         self.rows, self.cols, self.scale, self.q, self.s = q.shape[0], q.shape[1], scale, q, s
-        self.device = q.device
+        self.device, self._dev = q.device, q.get_device()
         self.matrix = MoeFp8Matrix(q.data_ptr(), s.data_ptr(), q.stride(0), s.stride(0), _SCALES[scale], 0)
+        self._ref = ctypes.byref(self.matrix)
+        self._packed = (q.data_ptr(), s.data_ptr(), q.stride(0), s.stride(0), _SCALES[scale])
 
     @classmethod
     def from_parts(cls, q, s):
@@ -582,6 +585,12 @@ def _on_strides(t):
     return wide.view(t.dtype)[:, :n]
 
 
+# MoeRmsnormArgs as one packed block: filling the ctypes structure field by field takes longer than the launch
+_RMSNORM_ARGS = struct.Struct("@iiiiPqPqPPqPqPPqqiifi")
+assert _RMSNORM_ARGS.size == ctypes.sizeof(MoeRmsnormArgs)
+_NO_OUT = (0, 0, 0, 0, 0)
+
+
 class RmsNorm:
     """v = x + residual; n = v * rsqrt(mean(v^2) + eps) * weight.
 
@@ -595,34 +604,36 @@ class RmsNorm:
             _bad("weight must be a one-dimensional CUDA tensor")
         self.weight = weight.to(torch.float32).contiguous()
         self.eps, self.cols = float(eps), weight.shape[0]
-        self._w = self.weight.data_ptr()
+        self._w, self._dev, self._types = self.weight.data_ptr(), weight.get_device(), _dtypes()
+        self._call = load()["moe_add_rmsnorm"]          # a prototype of its own, which takes the packed block
+        self._call.argtypes, self._call.restype = [ctypes.c_char_p, ctypes.c_void_p], ctypes.c_int
 
     def __call__(self, x, residual=None, out=None, res_out=None, y=None):
-        cols, dev = self.cols, x.device
-        if x.dim() != 2 or x.shape[1] != cols or dev != self.weight.device:
-            _bad(f"x must be [rows][{cols}] on the weight's device")
-        rows = x.shape[0]
-        xt = _dtype_code(x, "x")
-        a = MoeRmsnormArgs(rows, cols, xt, xt, x.data_ptr(), _rows_of(x, rows, cols, "x"))
+        cols, dev, rows = self.cols, self._dev, x.shape[0]
+        xt = rt = self._types.get(x.dtype)
+        if xt is None:
+            _bad(f"x must be bfloat16 or float32, not {x.dtype}")
+        ldx = _rows_of(x, rows, cols, dev, "x")
+        r = ldr = ro = ldro = yp = ldy = 0
         if residual is not None:
-            a.res_type = _dtype_code(residual, "residual")
-            a.res, a.ld_res = residual.data_ptr(), _rows_of(residual, rows, cols, "residual")
-            if residual.device != dev:
-                _bad("residual is on another device")
-        a.weight, a.eps = self._w, self.eps
+            rt = self._types.get(residual.dtype)
+            if rt is None:
+                _bad(f"residual must be bfloat16 or float32, not {residual.dtype}")
+            r, ldr = residual.data_ptr(), _rows_of(residual, rows, cols, dev, "residual")
         if res_out is not None:
-            if residual is None or res_out.dtype is not residual.dtype or res_out.device != dev:
-                _bad("res_out needs a residual of its type and device")
-            a.res_out, a.ld_res_out = res_out.data_ptr(), _rows_of(res_out, rows, cols, "res_out")
+            if residual is None or res_out.dtype is not residual.dtype:
+                _bad("res_out needs a residual of its type")
+            ro, ldro = res_out.data_ptr(), _rows_of(res_out, rows, cols, dev, "res_out")
         if y is not None:
-            if y.dtype is not x.dtype or y.device != dev:
-                _bad("y must have x's type and device")
-            a.y, a.ldy = y.data_ptr(), _rows_of(y, rows, cols, "y")
-        if out is not None:
-            if out.rows != rows or out.cols != cols or out.device != dev:
-                _bad(f"out must be [{rows}][{cols}] on x's device")
-            a.out = out.matrix
-        moe_add_rmsnorm(a, _stream(dev))
+            if y.dtype is not x.dtype:
+                _bad("y must have x's type")
+            yp, ldy = y.data_ptr(), _rows_of(y, rows, cols, dev, "y")
+        if out is not None and (out.rows != rows or out.cols != cols or out._dev != dev):
+            _bad(f"out must be [{rows}][{cols}] on x's device")
+        st = self._call(_RMSNORM_ARGS.pack(rows, cols, xt, rt, x.data_ptr(), ldx, r, ldr, self._w, ro, ldro, yp, ldy,
+                                           *(_NO_OUT if out is None else out._packed), 0, self.eps, 0), _stream(dev))
+        if st != MOE_OK:
+            _check(st)
 
 
 class _Weights:
@@ -641,17 +652,19 @@ class _Weights:
         keep = [t.contiguous() for m in mats for t in m]
         self.out_features, self.in_features = w.shape
         self.scale = "f32" if mats[0][1].dtype is torch.float32 else "e8m0"
-        self.device = w.device
+        self.device, self._dev, self._types = w.device, w.get_device(), _dtypes()
         self.handle = None
         self.handle = moe_linear_create(MoeLinearDesc(self.in_features, self.out_features, int(self.gated), _SCALES[self.scale]),
-                                        MoeLinearWeights(*[t.data_ptr() for t in keep]), _stream(w.device))
+                                        MoeLinearWeights(*[t.data_ptr() for t in keep]), _stream(self._dev))
+        lib = load()
+        self._call = lib.moe_gated_linear_forward if self.gated else lib.moe_linear_forward
 
     def _check_a(self, a):
-        if a.cols != self.in_features or a.scale != self.scale or a.device != self.device:
+        if a.cols != self.in_features or a.scale != self.scale or a._dev != self._dev:
             _bad(f"a must be [rows][{self.in_features}] with {self.scale} scales on the weights' device")
 
     def device_status(self):
-        return moe_linear_device_status(self.handle, _stream(self.device))
+        return moe_linear_device_status(self.handle, _stream(self._dev))
 
     def close(self):
         if getattr(self, "handle", None):
@@ -675,10 +688,13 @@ class Fp8Linear(_Weights):
 
     def __call__(self, a: Fp8Tensor, y):
         self._check_a(a)
-        ldy = _rows_of(y, a.rows, self.out_features, "y")
-        if y.device != self.device:
-            _bad("y is on another device")
-        moe_linear_forward(self.handle, a.matrix, a.rows, y.data_ptr(), ldy, _dtype_code(y, "y"), _stream(self.device))
+        ldy = _rows_of(y, a.rows, self.out_features, self._dev, "y")
+        yt = self._types.get(y.dtype)
+        if yt is None:
+            _bad(f"y must be bfloat16 or float32, not {y.dtype}")
+        st = self._call(self.handle, a._ref, a.rows, y.data_ptr(), ldy, yt, _stream(self._dev))
+        if st != MOE_OK:
+            _check(st)
         return y
 
 
@@ -691,9 +707,11 @@ class Fp8GatedLinear(_Weights):
 
     def __call__(self, a: Fp8Tensor, h: Fp8Tensor):
         self._check_a(a)
-        if h.rows != a.rows or h.cols != self.out_features or h.scale != self.scale or h.device != self.device:
+        if h.rows != a.rows or h.cols != self.out_features or h.scale != self.scale or h._dev != self._dev:
             _bad(f"h must be [{a.rows}][{self.out_features}] with {self.scale} scales on the weights' device")
-        moe_gated_linear_forward(self.handle, a.matrix, a.rows, h.matrix, _stream(self.device))
+        st = self._call(self.handle, a._ref, a.rows, h._ref, _stream(self._dev))
+        if st != MOE_OK:
+            _check(st)
         return h
 
 
