@@ -17,13 +17,19 @@
 // 112 6.7, 152 6.8), hence the rule: as many CTAs as there are SMs.
 //
 // A stage is a group of G K blocks (R rows of weights, the tokens, their
-// scales), closed by one commit and drained at once: waiting on or arriving at
-// an mbarrier takes a warp about 150 cycles and issuing a tensor copy about 90, so
-// narrow tiles need several blocks per hand-off.  Of a tile's blocks, pairs go to
-// the two warps of a lane quarter in turn, and the two sums are added once at the
-// end.  Half the SM's shared memory and tensor memory at most: two CTAs fit, so the
-// next call's weights are requested while this one ends, and a cluster of eight
-// finds room beside others.
+// scales): waiting on or arriving at an mbarrier takes a warp about 150 cycles
+// and issuing a tensor copy about 90, so narrow tiles need several blocks per
+// hand-off.  Half the SM's shared memory and tensor memory at most: two CTAs fit,
+// so the next call's weights are requested while this one ends, and a cluster of
+// eight finds room beside others.
+//
+// fp32 scales: each stage has its own tensor-memory buffer, drained and scaled in
+// registers as its MMAs end.  Pairs of blocks go to the two warps of a lane quarter
+// in turn, and the two sums are added once at the end.
+// e8m0 scales: the tensor core applies them (mxf8f6f4, block_scale; see the
+// many-token form), the range accumulates in tensor memory and is read once; warps
+// 2 and 3 lay out the scale factors.  Ranges of more than 64 blocks take the first
+// form, whose sums are not a single chain of truncating MMAs.
 //
 // Gated: a cluster holds the 256 interleaved gate/up rows of 128 features (two
 // tiles of 128 rows, S ranges of K each), which is one quantisation group.
@@ -44,7 +50,7 @@ struct FewArgs {
     const float* sw;
     int M, N, kt, nblk;
     int R, S, G;                             // rows per tile, K ranges, K blocks per stage (1, 2 or 4)
-    int a_rows, stages, kr;
+    int a_rows, stages, kr, kr4;             // kr: blocks of the longest range; kr4: up to a multiple of 4
     bool a_whole;
     void* y;
     int64_t ldy;
@@ -79,24 +85,18 @@ __device__ __forceinline__ void fma2s(float& a0, float& a1, uint32_t x0, uint32_
         : "r"(x0), "r"(x1), "f"(s), "f"(c0), "f"(c1));
 }
 
+constexpr int COLS = 256;                    // tensor-memory columns of a CTA
+// K blocks per stage, at most, and stages: each stage's accumulators have columns of their own.
 constexpr int group_cap(int tn) { return tn == 64 ? 2 : 4; }
 constexpr int tail_bytes(int tn) { return tn * BM * 4 > BM * 128 ? tn * BM * 4 : BM * 128; }   // partial sums; operand read
 
+enum Mode { F32, E8, MX };                   // fp32 scales; e8m0 scales applied in registers; by the tensor core
+constexpr int MX_MAX_KB = 64;                // K blocks of one accumulation chain
+constexpr int MX_QUADS = MX_MAX_KB / 4;
+constexpr int MX_SF_COL = 64;                // scale factors: columns 64 + 8 q, weights' then tokens'
+
 // First K block of range p: ranges start at even blocks, whatever G is.
 __host__ __device__ inline int range_start(int kt, int S, int p) { return p == S ? kt : (kt + 1) / 2 * p / S * 2; }
-
-// Tensor-memory buffer and barrier phase of a warp's n-th group.  Groups that only one turn's
-// warps drain use that turn's half of the buffers, so that nobody waits on a barrier whose phases
-// it has not followed.
-struct BufAt {
-    int buf;
-    uint32_t phase;
-};
-template <int NBUF>
-__device__ __forceinline__ BufAt buf_at(int G, int turn, int n) {
-    if (G == 4) return BufAt{n % NBUF, (uint32_t)(n / NBUF) & 1u};
-    return BufAt{turn * (NBUF / 2) + n % (NBUF / 2), (uint32_t)(n / (NBUF / 2)) & 1u};
-}
 
 // Scales of 4 tokens of a K block's run.
 template <bool E8>
@@ -140,23 +140,31 @@ __device__ __forceinline__ void take(uint32_t tb, const uint8_t* sl, int pitch, 
     }
 }
 
+__device__ __forceinline__ void ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
 __device__ __forceinline__ void store_y(const FewArgs& a, int t, int n, float v) {
     const int64_t at = (int64_t)t * a.ldy + n;
     if (a.y_f32) static_cast<float*>(a.y)[at] = v;
     else static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
 }
 
-template <int TN, bool GATED, bool E8>
+template <int TN, bool GATED, Mode MODE>
 __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant__ Maps maps, FewArgs a) {
-    constexpr int BUFC = group_cap(TN) * TN, COLS = 256, NBUF = COLS / BUFC;        // TMEM columns
+    constexpr bool E8S = MODE != F32;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int w_bytes = a.R * 128, a_bytes = a.a_rows * 128, stage_bytes = a.G * (w_bytes + a_bytes);
-    const int pitch = sa_pitch(a.a_rows, E8), slot_bytes = (a.G * pitch + 127) / 128 * 128;
+    const int pitch = sa_pitch(a.a_rows, E8S), slot_bytes = (a.G * pitch + 127) / 128 * 128;
     float* part = reinterpret_cast<float*>(ring + a.stages * stage_bytes);          // [token][128 rows]
-    uint8_t* scales = reinterpret_cast<uint8_t*>(part) + tail_bytes(TN);            // [stage][slot]
+    uint8_t* scales = reinterpret_cast<uint8_t*>(part) + tail_bytes(TN);            // [stage][slot]; MX: [kr4][pitch]
     float* sws = reinterpret_cast<float*>(scales + a.stages * slot_bytes);          // [kr][2]
-    __shared__ uint64_t full[ST_MAX], empty[ST_MAX], tfull[NBUF], tempty[NBUF];
+    uint8_t* packed = scales + (a.kr4 * pitch + 127) / 128 * 128;                   // MX: [quad][weights 512 B | tokens 512 B]
+    __shared__ uint64_t full[ST_MAX], empty[ST_MAX], tfull[ST_MAX], sfull, sready[MODE == MX ? MX_QUADS : 1];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
 
@@ -166,15 +174,30 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
     const int n0 = (GATED ? 2 * unit + rank / a.S : unit) * a.R;
     const int kb0 = range_start(a.kt, a.S, rank % a.S), nkb = range_start(a.kt, a.S, rank % a.S + 1) - kb0;
     const int n_grp = (nkb + a.G - 1) / a.G;
+    const int pre = min(a.stages, n_grp);
+    const uint32_t ring0 = smem_addr(ring), scl0 = smem_addr(scales), full0 = smem_addr(full);
+
+    // a stage's bytes and the copy of its weights, by one thread
+    auto copy_w = [&](int st, int g) {
+        const int na = a.a_whole ? a.G : min(a.G, a.kt - kb0 - g * a.G);
+        expect_tx(full0 + 8 * st, (uint32_t)(a.G * (w_bytes + (MODE == MX ? 0 : pitch)) + na * a_bytes));
+        tma_load_3d(ring0 + st * stage_bytes, &maps.w, 0, n0, kb0 + g * a.G, full0 + 8 * st);
+    };
 
     pdl_trigger();
     if (threadIdx.x == 0) {
-        // a group of four blocks is drained by both warps of each quarter, a smaller one by one of them
-        const uint32_t drains = a.G == 4 ? EPI_WARPS : EPI_WARPS / 2;
-        for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], drains); }
-        for (int b = 0; b < NBUF; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], drains); }
+        // fp32 form: a group of four blocks is drained by both warps of each quarter, a smaller one by one
+        const uint32_t drains = MODE == MX ? 1 : a.G == 4 ? EPI_WARPS : EPI_WARPS / 2;
+        for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], drains); mbar_init(&tfull[s], 1); }
+        if (MODE == MX) {
+            mbar_init(&sfull, 1);
+            for (int q = 0; q < (MODE == MX ? MX_QUADS : 1); ++q) mbar_init(&sready[q], 1);
+        }
         fence_mbar_init();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         abort_flag = 0;
+        // the weights do not depend on the preceding kernel, nor on the rest of this one's set-up
+        for (int g = 0; g < pre; ++g) copy_w(g, g);
     }
     __syncthreads();
     volatile int* abort = &abort_flag;
@@ -184,28 +207,17 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
         if (warp == 0) {
             // ------------------------------------------------ producer
             const uint32_t el = elect_one();
-            const uint32_t ring0 = smem_addr(ring), scl0 = smem_addr(scales), full0 = smem_addr(full);
-            if (el) {
-                prefetch_map(&maps.w);
-                prefetch_map(&maps.a);
-                prefetch_map(&maps.s);
-            }
-            auto copy_w = [&](int st, int g) {
-                const int na = a.a_whole ? a.G : min(a.G, a.kt - kb0 - g * a.G);
-                if (el) {
-                    expect_tx(full0 + 8 * st, (uint32_t)(a.G * (w_bytes + pitch) + na * a_bytes));
-                    tma_load_3d(ring0 + st * stage_bytes, &maps.w, 0, n0, kb0 + g * a.G, full0 + 8 * st);
-                }
-            };
-            const int pre = min(a.stages, n_grp);    // the weights do not depend on the preceding kernel
-            for (int g = 0; g < pre; ++g) copy_w(g, g);
             pdl_wait();
+            if (MODE == MX && el) {                  // the range's token scales, all at once
+                expect_tx(smem_addr(&sfull), (uint32_t)(a.kr4 * pitch));
+                tma_load_2d(scl0, &maps.s, 0, kb0, smem_addr(&sfull));
+            }
             int st = 0, g = 0;
             uint32_t phase = 0;
             for (; g < n_grp; ++g) {
                 if (g >= pre) {
                     if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[st], phase ^ 1u, a.wait_limit, a.status, abort))) break;
-                    copy_w(st, g);
+                    if (el) copy_w(st, g);
                 }
                 if (el) {
                     const uint32_t dst = ring0 + st * stage_bytes + a.G * w_bytes, bar = full0 + 8 * st;
@@ -216,14 +228,16 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
                         const int na = min(a.G, a.kt - kb);
                         for (int i = 0; i < na; ++i) tma_load_3d(dst + i * a_bytes, &maps.a, (kb + i) * QB, 0, 0, bar);
                     }
-                    tma_load_2d(scl0 + st * slot_bytes, &maps.s, 0, kb, bar);
+                    if (MODE != MX) tma_load_2d(scl0 + st * slot_bytes, &maps.s, 0, kb, bar);
                 }
+                __syncwarp();
                 if (++st == a.stages) { st = 0; phase ^= 1u; }
             }
             for (int n = min(g, a.stages); n > 0; --n) {   // every issued copy lands before the CTA exits
                 if (--st < 0) { st = a.stages - 1; phase ^= 1u; }
                 mbar_wait_bounded(&full[st], phase, a.wait_limit, a.status, nullptr);
             }
+            if (MODE == MX) mbar_wait_bounded(&sfull, 0, a.wait_limit, a.status, nullptr);
         } else if (warp == 1) {
             // ------------------------------------------------ MMA issuer
             tc::tmem_alloc(&tmem_slot, COLS);
@@ -233,29 +247,89 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
             const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_slot, 0);
             const uint32_t el = elect_one();
             const uint32_t idesc = (1u << 4) | ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
-            const uint32_t d0 = (uint32_t)tc::sw128_desc(smem_addr(ring));
-            int st = 0, c0 = 0, c1 = 0;
+            const uint32_t d0 = (uint32_t)tc::sw128_desc(ring0), sf0 = smem_addr(packed);
+            int st = 0;
             uint32_t phase = 0;
-            for (int g = 0; g < n_grp; ++g) {
-                const bool second = a.G < 4 && ((g * a.G >> 1) & 1);
-                const BufAt at = buf_at<NBUF>(a.G, second, second ? c1 : c0);
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[st], phase, a.wait_limit, a.status, abort) &&
-                                                 mbar_wait_bounded(&tempty[at.buf], at.phase ^ 1u, a.wait_limit, a.status, abort)))
-                    break;
+            bool ok = true;
+            for (int g = 0; g < n_grp && ok; ++g) {
+                // A stage's accumulators are free when the stage is: the warps that drained them handed
+                // it back, and its next copies were issued after that.
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[st], phase, a.wait_limit, a.status, abort));
+                if (!ok) break;
                 tc::tc_fence_after();
                 const int nk = min(a.G, nkb - g * a.G);
                 uint32_t wd = d0 + (uint32_t)((st * stage_bytes) >> 4), td = wd + (uint32_t)((a.G * w_bytes) >> 4);
-                uint32_t dt = tmem + (uint32_t)(at.buf * BUFC);
+                uint32_t dt = tmem + (uint32_t)(st * a.G * TN);
                 for (int i = 0; i < nk; ++i) {
-                    mma_block(dt, wd, td, idesc, el);
+                    if constexpr (MODE == MX) {
+                        const int k = g * a.G + i, q = k >> 2;
+                        const uint32_t sft = tmem + MX_SF_COL + 8 * q;
+                        if ((k & 3) == 0) {
+                            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&sready[q], 0, a.wait_limit, a.status, abort));
+                            if (!ok) break;
+                            sf_copy(sft, sf_desc(sf0 + q * 1024), el);
+                            sf_copy(sft + 4, sf_desc(sf0 + q * 1024 + 512), el);
+                        }
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            mma_mx(tmem, wd + 2 * s, td + 2 * s, idesc_mx(TN, k & 3), sft, sft + 4, (k | s) != 0, el);
+                    } else {
+                        mma_block(dt, wd, td, idesc, el);
+                    }
                     wd += (uint32_t)(w_bytes >> 4);
                     td += (uint32_t)(a_bytes >> 4);
                     dt += TN;
                 }
-                if (el) tc::mma_commit(&tfull[at.buf]);
+                if (el) {
+                    if (MODE == MX) {
+                        tc::mma_commit(&empty[st]);
+                        if (g == n_grp - 1) tc::mma_commit(&tfull[0]);
+                    } else {
+                        tc::mma_commit(&tfull[st]);
+                    }
+                }
                 __syncwarp();
                 if (++st == a.stages) { st = 0; phase ^= 1u; }
-                if (second) ++c1; else ++c0;
+            }
+        } else if (MODE == MX) {
+            // ------------------------------------------------ scale factors of every second quad of K blocks
+            // 128 rows x 4 bytes in 512: row r at (r mod 32) * 16 + (r / 32) * 4, one byte per K block.
+            // Weights: a tile lies in two scale blocks (plain) or has gate and up rows (gated), so a row's
+            // word is one of two.
+            const int b0 = GATED ? unit : n0 / QB;
+            const float* s0 = a.sw + (size_t)min(b0, a.nblk - 1) * a.kt + kb0;
+            const float* s1 = a.sw + (size_t)(GATED ? min(b0, a.nblk - 1) + a.nblk : min(b0 + 1, a.nblk - 1)) * a.kt + kb0;
+            const int nq = (nkb + 3) / 4;
+            for (int q = warp - 2; q < nq; q += 2) {
+                const int kb = 4 * q + (lane & 3);
+                // an fp32 power of two's exponent field is its e8m0 byte (NaN 255, 2^-127 0)
+                const uint32_t e = kb < nkb ? __float_as_uint(((lane & 4) ? s1 : s0)[kb]) >> 23 : 127u;
+                uint32_t w0 = 0, w1 = 0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    w0 |= __shfl_sync(0xFFFFFFFFu, e, b) << (8 * b);
+                    w1 |= __shfl_sync(0xFFFFFFFFu, e, 4 + b) << (8 * b);
+                }
+                uint32_t v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = 32 * j + lane;
+                    v[j] = (GATED ? ((r >> 3) & 1) != 0 : (n0 + r) / QB != n0 / QB) ? w1 : w0;
+                }
+                *reinterpret_cast<uint4*>(packed + q * 1024 + lane * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+            bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&sfull, 0, a.wait_limit, a.status, abort));
+            for (int q = warp - 2; q < nq && ok; q += 2) {
+                uint32_t v[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint8_t* p = scales + 4 * q * pitch + min(32 * j + lane, pitch - 1);
+                    v[j] = (uint32_t)p[0] | (uint32_t)p[pitch] << 8 | (uint32_t)p[2 * pitch] << 16 | (uint32_t)p[3 * pitch] << 24;
+                }
+                *reinterpret_cast<uint2*>(packed + q * 1024 + 512 + lane * 16) = make_uint2(v[0], v[1]);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sready[q]);
             }
         }
         __syncwarp();
@@ -270,29 +344,54 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
             cluster_arrive_release();
             cluster_wait();
         }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FEW_DRAIN_REGS));
-        // ---------------------------------------------------- drain warps
-        const int ew = warp - CTRL_WARPS, quarter = warp & 3, turn = ew >> 2;
-        const int row = quarter * 32 + lane;                   // weight row of the tile = TMEM lane
-        const bool live = quarter * 32 < a.R;
+        return;
+    }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FEW_DRAIN_REGS));
+    // -------------------------------------------------------- drain warps
+    const int ew = warp - CTRL_WARPS, quarter = warp & 3, turn = ew >> 2;
+    const int row = quarter * 32 + lane;                       // weight row of the tile = TMEM lane
+    const bool live = quarter * 32 < a.R;
+    if (MODE != MX) {
         // the range's weight scales, two per block: plain, those of the tile's first scale block and
         // the next one; gated, gate and up
-        {
-            const int b0 = GATED ? unit : n0 / QB;
-            const float* s0 = a.sw + (size_t)min(b0, a.nblk - 1) * a.kt + kb0;
-            const float* s1 = a.sw + (size_t)(GATED ? b0 + a.nblk : min(b0 + 1, a.nblk - 1)) * a.kt + kb0;
-            for (int i = threadIdx.x - CTRL_WARPS * 32; i < 2 * nkb; i += EPI_WARPS * 32)
-                sws[i] = (i & 1) ? s1[i >> 1] : s0[i >> 1];
+        const int b0 = GATED ? unit : n0 / QB;
+        const float* s0 = a.sw + (size_t)min(b0, a.nblk - 1) * a.kt + kb0;
+        const float* s1 = a.sw + (size_t)(GATED ? min(b0, a.nblk - 1) + a.nblk : min(b0 + 1, a.nblk - 1)) * a.kt + kb0;
+        for (int i = threadIdx.x - CTRL_WARPS * 32; i < 2 * nkb; i += EPI_WARPS * 32)
+            sws[i] = (i & 1) ? s1[i >> 1] : s0[i >> 1];
+    }
+    const int sel = GATED ? (row >> 3) & 1 : ((n0 + row) / QB != n0 / QB);
+    named_bar_sync(2, (1 + EPI_WARPS) * 32);
+    tc::tc_fence_after();
+    const uint32_t tmem = tmem_slot + ((uint32_t)(quarter * 32) << 16);
+    if constexpr (MODE == MX) {
+        pdl_wait();                                            // before the first write the preceding kernel may conflict with
+        const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[0], 0, a.wait_limit, a.status, abort));
+        if (live && ok) {
+            tc::tc_fence_after();
+            // the two warps of a quarter take eight tokens in turn
+#pragma unroll 1
+            for (int c = 8 * turn; c < min(TN, a.M); c += 16) {
+                uint32_t raw[8];
+                ld8(tmem + c, raw);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (c + e >= a.M) break;
+                    const float v = __uint_as_float(raw[e]);
+                    if (!GATED && csize == 1) {
+                        if (row < a.R && n0 + row < a.N) store_y(a, c + e, n0 + row, v);
+                    } else {
+                        part[(c + e) * BM + row] = v;
+                    }
+                }
+            }
         }
-        const int sel = GATED ? (row >> 3) & 1 : ((n0 + row) / QB != n0 / QB);
-        named_bar_sync(2, (1 + EPI_WARPS) * 32);
-        tc::tc_fence_after();
-        const uint32_t tmem = tmem_slot + ((uint32_t)(quarter * 32) << 16);
+    } else {
         float acc[TN];
 #pragma unroll
         for (int t = 0; t < TN; ++t) acc[t] = 0.f;
-        int st = 0, mine = 0;
+        int st = 0;
         uint32_t phase = 0;
         bool dead = false;
         for (int g = 0; g < n_grp; ++g) {
@@ -300,122 +399,119 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
             if (a.G == 4 || ((kb >> 1) & 1) == turn) {
                 // my blocks of this group: a pair (or, with G = 1 or at the end, one block)
                 const int k0 = kb + (a.G == 4 ? 2 * turn : 0), nk = min(min(a.G, 2), nkb - k0);
-                const BufAt at = buf_at<NBUF>(a.G, turn, mine++);
-                // the second wait returns at once: it makes the stage's scales visible to this thread
-                if (!dead && !(mbar_wait_bounded(&tfull[at.buf], at.phase, a.wait_limit, a.status, abort) &&
-                               mbar_wait_bounded(&full[st], phase, a.wait_limit, a.status, abort)))
-                    dead = true;
-                dead = __any_sync(0xFFFFFFFFu, dead);          // warp-uniform: tcgen05.ld is warp-collective
-                const bool work = !dead && live && nk > 0;
+                // Skipping groups is safe: MMAs end in order and the ring is long enough that the stage's
+                // previous use came before my last group.  The second wait returns at once: it makes the
+                // stage's scales visible here.
+                if (!dead) {
+                    dead = !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[st], phase, a.wait_limit, a.status, abort) &&
+                                                        mbar_wait_bounded(&full[st], phase, a.wait_limit, a.status, abort));
+                }
+                const bool work = !dead && live && nk > 0;     // warp-uniform: tcgen05.ld is warp-collective
                 if (work) {
                     tc::tc_fence_after();
-                    const uint32_t tb = tmem + (uint32_t)(at.buf * BUFC + (k0 - kb) * TN);
+                    const uint32_t tb = tmem + (uint32_t)((st * a.G + k0 - kb) * TN);
                     const uint8_t* sl = scales + st * slot_bytes + (k0 - kb) * pitch;
                     const float* sw = sws + 2 * k0 + sel;
                     // Straight-line code from the loads to the products: the shared-memory reads of the
                     // scales overlap the tensor-memory loads, which a branch between would prevent.
                     if (TN == 16 && nk == 2) {
-                        take<TN, 2, 16, E8>(tb, sl, pitch, sw, a.a_rows, acc);
+                        take<TN, 2, 16, E8S>(tb, sl, pitch, sw, a.a_rows, acc);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
-                            if (j < nk) take<TN, 1, 16, E8>(tb + j * TN, sl + j * pitch, pitch, sw + 2 * j, a.a_rows, acc);
+                            if (j < nk) take<TN, 1, 16, E8S>(tb + j * TN, sl + j * pitch, pitch, sw + 2 * j, a.a_rows, acc);
                     }
                     tc::tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&empty[st]);
-                    mbar_arrive(&tempty[at.buf]);
-                }
+                if (lane == 0) mbar_arrive(&empty[st]);
             }
             if (++st == a.stages) { st = 0; phase ^= 1u; }
         }
+        pdl_wait();                                            // before the first write the preceding kernel may conflict with
         // the two warps of a quarter add their sums
         if (turn == 1 && live) {
 #pragma unroll
-            for (int t = 0; t < TN; ++t)
-                if (t < a.M) part[t * BM + row] = acc[t];
+            for (int t = 0; t < TN; ++t) {
+                if (t >= a.M) break;
+                part[t * BM + row] = acc[t];
+            }
         }
-        pdl_wait();                                            // before the first write the preceding kernel may conflict with
         named_bar_sync(1, EPI_WARPS * 32);
         if (turn == 0 && live) {
 #pragma unroll
-            for (int t = 0; t < TN; ++t)
-                if (t < a.M) {
-                    const float v = acc[t] + part[t * BM + row];
-                    if (!GATED && csize == 1) {
-                        if (row < a.R && n0 + row < a.N) store_y(a, t, n0 + row, v);
-                    } else {
-                        part[t * BM + row] = v;
-                    }
-                }
-        }
-        // ------------------------------------------------------ join the K ranges
-        tc::tc_fence_before();
-        named_bar_sync(3, NTHREADS);
-        if (csize > 1) {
-            cluster_arrive_release();
-            cluster_wait();
-        }
-        const uint32_t part0 = smem_addr(part);
-        if (csize > 1 && !*abort) {
-            const int tid = threadIdx.x - CTRL_WARPS * 32;
-            if constexpr (GATED) {
-                // a warp takes a token: four features a lane, 128 in all
-                const int f = 4 * lane, ff = f & 63, r = (ff >> 3) * 16 + (ff & 7);
-                const int base = (f >> 6) * a.S;                   // first rank of the tile with these features
-                const int f0 = unit * QB + f;
-                for (int t = rank * EPI_WARPS + (tid >> 5); t < a.M; t += csize * EPI_WARPS) {
-                    float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
-                    for (int p = 0; p < a.S; ++p) {
-                        const uint32_t at = map_to_rank(part0 + (uint32_t)(t * BM + r) * 4u, base + p);
-                        const float4 x = ld_cluster4(at), z = ld_cluster4(at + 32);
-                        g.x += x.x; g.y += x.y; g.z += x.z; g.w += x.w;
-                        u.x += z.x; u.y += z.y; u.z += z.z; u.w += z.w;
-                    }
-                    float h[4] = {silu_mul(g.x, u.x), silu_mul(g.y, u.y), silu_mul(g.z, u.z), silu_mul(g.w, u.w)};
-                    float am = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (f0 + e >= a.N) h[e] = 0.f;
-                        am = max_nan(am, fabsf(h[e]));
-                    }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
-                    uint32_t held;
-                    const float is = inv_scale(group_scale(am, E8, held));
-                    const uint32_t v = pack4_e4m3(h[0] * is, h[1] * is, h[2] * is, h[3] * is);
-                    uint8_t* dst = a.hq + (int64_t)t * a.ld_hq + f0;
-                    if (f0 + 4 <= a.N) {
-                        *reinterpret_cast<uint32_t*>(dst) = v;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (f0 + e < a.N) dst[e] = (uint8_t)(v >> (8 * e));
-                    }
-                    if (lane == 0) {
-                        const int64_t at = (int64_t)unit * a.ld_hs + t;
-                        if (E8) static_cast<uint8_t*>(a.hs)[at] = (uint8_t)held;
-                        else static_cast<uint32_t*>(a.hs)[at] = held;
-                    }
-                }
-            } else {
-                // each CTA of the cluster finishes a slice of the tile's rows
-                const int rs = a.R / a.S, lo = rank * rs;
-                for (int i = tid; i < rs * a.M; i += EPI_WARPS * 32) {
-                    const int t = i / rs, r = lo + i % rs;
-                    float v = 0.f;
-                    for (int p = 0; p < a.S; ++p) v += ld_cluster(map_to_rank(part0 + (uint32_t)(t * BM + r) * 4u, p));
-                    if (n0 + r < a.N) store_y(a, t, n0 + r, v);
+            for (int t = 0; t < TN; ++t) {
+                if (t >= a.M) break;
+                const float v = acc[t] + part[t * BM + row];
+                if (!GATED && csize == 1) {
+                    if (row < a.R && n0 + row < a.N) store_y(a, t, n0 + row, v);
+                } else {
+                    part[t * BM + row] = v;
                 }
             }
         }
-        if (csize > 1) {                                           // nobody leaves while a peer may still read its sums
-            cluster_arrive_release();
-            cluster_wait();
+    }
+    // -------------------------------------------------------- join the K ranges
+    tc::tc_fence_before();
+    named_bar_sync(3, NTHREADS);
+    if (csize == 1) return;
+    cluster_arrive_release();
+    cluster_wait();
+    const uint32_t part0 = smem_addr(part);
+    if (!*abort) {
+        const int tid = threadIdx.x - CTRL_WARPS * 32;
+        if constexpr (GATED) {
+            // a warp takes a token: four features a lane, 128 in all
+            const int f = 4 * lane, ff = f & 63, r = (ff >> 3) * 16 + (ff & 7);
+            const int base = (f >> 6) * a.S;                   // first rank of the tile with these features
+            const int f0 = unit * QB + f;
+            for (int t = rank * EPI_WARPS + (tid >> 5); t < a.M; t += csize * EPI_WARPS) {
+                float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+                for (int p = 0; p < a.S; ++p) {
+                    const uint32_t at = map_to_rank(part0 + (uint32_t)(t * BM + r) * 4u, base + p);
+                    const float4 x = ld_cluster4(at), z = ld_cluster4(at + 32);
+                    g.x += x.x; g.y += x.y; g.z += x.z; g.w += x.w;
+                    u.x += z.x; u.y += z.y; u.z += z.z; u.w += z.w;
+                }
+                float h[4] = {silu_mul(g.x, u.x), silu_mul(g.y, u.y), silu_mul(g.z, u.z), silu_mul(g.w, u.w)};
+                float am = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (f0 + e >= a.N) h[e] = 0.f;
+                    am = max_nan(am, fabsf(h[e]));
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+                uint32_t held;
+                const float is = inv_scale(group_scale(am, E8S, held));
+                const uint32_t v = pack4_e4m3(h[0] * is, h[1] * is, h[2] * is, h[3] * is);
+                uint8_t* dst = a.hq + (int64_t)t * a.ld_hq + f0;
+                if (f0 + 4 <= a.N) {
+                    *reinterpret_cast<uint32_t*>(dst) = v;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (f0 + e < a.N) dst[e] = (uint8_t)(v >> (8 * e));
+                }
+                if (lane == 0) {
+                    const int64_t at = (int64_t)unit * a.ld_hs + t;
+                    if (E8S) static_cast<uint8_t*>(a.hs)[at] = (uint8_t)held;
+                    else static_cast<uint32_t*>(a.hs)[at] = held;
+                }
+            }
+        } else {
+            // each CTA of the cluster finishes a slice of the tile's rows
+            const int rs = a.R / a.S, lo = rank * rs;
+            for (int i = tid; i < rs * a.M; i += EPI_WARPS * 32) {
+                const int t = i / rs, r = lo + i % rs;
+                float v = 0.f;
+                for (int p = 0; p < a.S; ++p) v += ld_cluster(map_to_rank(part0 + (uint32_t)(t * BM + r) * 4u, p));
+                if (n0 + r < a.N) store_y(a, t, n0 + r, v);
+            }
         }
     }
+    cluster_arrive_release();                                  // nobody leaves while a peer may still read its sums
+    cluster_wait();
 }
 
 struct FewPlan {
@@ -429,9 +525,9 @@ static FewPlan plan_few(const moe_linear* L, bool gated) {
     FewPlan best = {};
     double best_us = 0;
     for (int S = 1; S <= (gated ? 4 : 8); S *= 2) {
-        if (S > L->kt) break;
-        const int kr = range_start(L->kt, S, 1);               // the longest range
-        if (kr > KR_MAX || range_start(L->kt, S, S - 1) >= L->kt) continue;
+        if (S > (L->kt + 1) / 2) break;                        // every range holds a pair of blocks
+        const int kr = range_start(L->kt, S, 1);               // the longest range, or two blocks less
+        if (kr + 2 > KR_MAX) continue;
         for (int R = gated ? BM : 16; R <= BM; R += 16) {
             if (R % S) continue;
             const long long tiles = gated ? 2LL * ((L->d.out_features + QB - 1) / QB) : (L->rows + R - 1) / R;
@@ -450,8 +546,8 @@ static FewPlan plan_few(const moe_linear* L, bool gated) {
     return best;
 }
 
-template <int TN, bool GATED, bool E8>
-cudaError_t launch_few(const GemmCall& c, const FewPlan& p, cudaStream_t s) {
+template <int TN, bool GATED, Mode MODE>
+cudaError_t launch_few(const GemmCall& c, const FewPlan& p, int kr, cudaStream_t s) {
     const moe_linear* L = c.lin;
     Args g = base_args(c);                    // what the tensor maps are made from
     g.bn = p.R;
@@ -461,26 +557,38 @@ cudaError_t launch_few(const GemmCall& c, const FewPlan& p, cudaStream_t s) {
     a.M = c.M; a.N = L->d.out_features; a.kt = L->kt; a.nblk = g.nblk;
     a.R = p.R; a.S = p.S;
     a.a_rows = g.a_rows;
-    a.kr = range_start(L->kt, p.S, 1);
-    for (int i = 1; i < p.S; ++i) a.kr = std::max(a.kr, range_start(L->kt, p.S, i + 1) - range_start(L->kt, p.S, i));
+    a.kr = kr;
+    a.kr4 = (kr + 3) / 4 * 4;
     a.a_whole = g.a_whole;
     a.y = c.y; a.ldy = c.ldy; a.y_f32 = c.y_f32;
     a.hq = c.hq; a.ld_hq = c.ld_hq; a.hs = c.hs; a.ld_hs = c.ld_hs;
     a.status = L->dev_status; a.wait_limit = L->wait_limit;
-    // blocks per stage: the plan's, unless fewer than three stages would fit (two of one block always do)
-    const int fixed = 1024 + tail_bytes(TN) + a.kr * 8;
-    int stage = 0;
+    // Blocks per stage: the plan's, unless fewer than three stages would fit.  The fp32 form needs three
+    // where its drain warps skip groups (one block a stage always gives them: 24 KB at most); the other
+    // works with two.
+    const int pitch = sa_pitch(a.a_rows, MODE != F32);
+    int smem = 0;
     for (a.G = std::min(p.G, group_cap(TN)); a.G >= 1; a.G /= 2) {
-        stage = a.G * (p.R + a.a_rows) * 128 + (a.G * sa_pitch(a.a_rows, E8) + 127) / 128 * 128;
+        const int fixed = 1024 + tail_bytes(TN) + (MODE == MX ? (a.kr4 * pitch + 127) / 128 * 128 + a.kr4 / 4 * 1024 : kr * 8);
+        const int stage = a.G * (p.R + a.a_rows) * 128 + (MODE == MX ? 0 : (a.G * pitch + 127) / 128 * 128);
         a.stages = std::min(ST_MAX, (SMEM_HALF - fixed) / stage);
-        if (a.stages >= 3 || a.G == 1) break;
+        if (MODE != MX) a.stages = std::min(a.stages, COLS / (a.G * TN));
+        a.stages = std::min(a.stages, (kr + a.G - 1) / a.G);
+        smem = fixed + a.stages * stage;
+        if (a.stages >= std::min(MODE == MX && a.G == 1 ? 2 : 3, (kr + a.G - 1) / a.G)) break;
     }
-    if (a.stages < 1) return cudaErrorInvalidValue;
-    a.stages = std::min(a.stages, (a.kr + a.G - 1) / a.G);
+    if (a.G < 1) return cudaErrorInvalidValue;
     Maps maps;
     if (!encode_maps(c, g, a.G, &maps)) return cudaErrorInvalidValue;
-    const int smem = fixed + a.stages * stage;
-    cudaError_t e = ensure_smem_limit<few_kernel<TN, GATED, E8>>(SMEM_HALF);
+    if (MODE == MX) {                         // the tokens' scales of a whole range in one copy
+        const cuuint64_t sd[2] = {(cuuint64_t)c.M, (cuuint64_t)a.kt}, ss[1] = {(cuuint64_t)c.ld_as};
+        const cuuint32_t sb[2] = {(cuuint32_t)pitch, (cuuint32_t)a.kr4}, one[2] = {1, 1};
+        if (tensor_map_encoder()(&maps.s, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(c.as), sd, ss, sb, one,
+                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    cudaError_t e = ensure_smem_limit<few_kernel<TN, GATED, MODE>>(SMEM_HALF);
     if (e != cudaSuccess) return e;
     const int cluster = GATED ? 2 * p.S : p.S;
     const int tiles = GATED ? (L->d.out_features + QB - 1) / QB : (L->rows + p.R - 1) / p.R;
@@ -500,7 +608,23 @@ cudaError_t launch_few(const GemmCall& c, const FewPlan& p, cudaStream_t s) {
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.numAttrs = 2;
     }
-    return cudaLaunchKernelEx(&cfg, few_kernel<TN, GATED, E8>, maps, a);
+    return cudaLaunchKernelEx(&cfg, few_kernel<TN, GATED, MODE>, maps, a);
+}
+
+template <bool GATED, Mode MODE>
+static cudaError_t launch_tokens(const GemmCall& c, const FewPlan& p, int kr, cudaStream_t s) {
+    if (c.M <= 16) return launch_few<16, GATED, MODE>(c, p, kr, s);
+    if (c.M <= 32) return launch_few<32, GATED, MODE>(c, p, kr, s);
+    return launch_few<64, GATED, MODE>(c, p, kr, s);
+}
+
+template <bool GATED>
+static cudaError_t launch_mode(const GemmCall& c, cudaStream_t s) {
+    const FewPlan p = plan_few(c.lin, GATED);
+    int kr = 0;
+    for (int i = 0; i < p.S; ++i) kr = std::max(kr, range_start(c.lin->kt, p.S, i + 1) - range_start(c.lin->kt, p.S, i));
+    if (c.lin->d.scale_type == MOE_SCALE_F32) return launch_tokens<GATED, F32>(c, p, kr, s);
+    return kr <= MX_MAX_KB ? launch_tokens<GATED, MX>(c, p, kr, s) : launch_tokens<GATED, E8>(c, p, kr, s);
 }
 
 }  // namespace few
@@ -509,20 +633,8 @@ bool few_tokens(const GemmCall& c, bool gated) {
     return c.M <= few::MAX_M && few::plan_few(c.lin, gated).R != 0;
 }
 
-namespace few {
-template <bool GATED, bool E8>
-static cudaError_t launch_tokens(const GemmCall& c, cudaStream_t s) {
-    const FewPlan p = plan_few(c.lin, GATED);
-    if (c.M <= 16) return launch_few<16, GATED, E8>(c, p, s);
-    if (c.M <= 32) return launch_few<32, GATED, E8>(c, p, s);
-    return launch_few<64, GATED, E8>(c, p, s);
-}
-}  // namespace few
-
 cudaError_t launch_fp8_few(const GemmCall& c, bool gated, cudaStream_t s) {
-    const bool e8 = c.lin->d.scale_type == MOE_SCALE_E8M0;
-    if (gated) return e8 ? few::launch_tokens<true, true>(c, s) : few::launch_tokens<true, false>(c, s);
-    return e8 ? few::launch_tokens<false, true>(c, s) : few::launch_tokens<false, false>(c, s);
+    return gated ? few::launch_mode<true>(c, s) : few::launch_mode<false>(c, s);
 }
 
 }  // namespace moe

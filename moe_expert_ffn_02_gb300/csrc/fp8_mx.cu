@@ -39,34 +39,6 @@ constexpr int slot_bytes() { return RAW_BYTES + SF_BYTES + BN / QB * SF_BYTES; }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
 
-// Descriptor of a scale-factor block: no swizzle, 8-row groups of 128 bytes one after the other.
-__device__ __forceinline__ uint64_t sf_desc(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-}
-__device__ __forceinline__ void sf_copy(uint32_t taddr, uint64_t desc, uint32_t elected) {
-    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n @q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(taddr),
-                 "l"(desc), "r"(elected)
-                 : "memory");
-}
-
-// One K32 step with scale factors.
-__device__ __forceinline__ void mma_mx(uint32_t d, uint32_t a_lo, uint32_t w_lo, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                       uint32_t accumulate, uint32_t elected) {
-    constexpr uint32_t HI = (uint32_t)(tc::DESC_HI >> 32);
-    asm volatile(
-        "{\n .reg .pred q, t;\n .reg .b64 a, w;\n"
-        " setp.ne.b32 q, %8, 0;\n setp.ne.b32 t, %7, 0;\n"
-        " mov.b64 a, {%1, %4};\n mov.b64 w, {%2, %4};\n"
-        " @q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, w, %3, [%5], [%6], t;\n}" ::"r"(d),
-        "r"(a_lo), "r"(w_lo), "r"(idesc), "n"(HI), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(elected)
-        : "memory");
-}
-
-// Instruction descriptor, kind::mxf8f6f4: A = B = E4M3, K-major, UE8M0 scales, M = 128, N = n.
-__device__ __forceinline__ uint32_t idesc_mx(int n, int sf_id) {
-    return ((uint32_t)sf_id << 4) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(BM >> 4) << 24) | ((uint32_t)sf_id << 29);
-}
-
 template <int BN, bool GATED>
 __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__ Maps maps, const uint8_t* __restrict__ wsf, int nrb,
                                                         Args a) {

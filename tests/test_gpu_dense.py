@@ -258,6 +258,13 @@ def test_linear_against_64_bits(moe, m, k, n, scale, dtype):
     check_linear(moe, m, k, n, scale, dtype)
 
 
+@pytest.mark.parametrize("m,k,n", [(3, 70000, 20), (70, 8300, 40), (2, 530000, 16), (40, 33000, 130)])
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+def test_linear_of_long_rows(moe, m, k, n, scale):
+    """K past what one chain of scaled MMAs, or one CTA's share of the few-token form, may hold."""
+    check_linear(moe, m, k, n, scale, torch.float32)
+
+
 def check_gated(moe, m, k, n, scale, seed=30):
     aq, a_s = rows_fp8(randn((m, k), seed), scale)
     g, u = blocks_fp8(randn((n, k), seed + 1, 0.05), scale), blocks_fp8(randn((n, k), seed + 2, 0.05), scale)
@@ -278,7 +285,7 @@ def check_gated(moe, m, k, n, scale, seed=30):
 
 @pytest.mark.parametrize("m,k,n", [(1, 128, 1), (1, 7168, 2048), (2, 100, 8), (7, 129, 17), (9, 640, 129), (33, 1040, 1000),
                                    (64, 384, 250), (65, 257, 136), (127, 513, 333), (128, 256, 256), (129, 1153, 200),
-                                   (300, 1992, 1001), (1000, 256, 2500)])
+                                   (300, 1992, 1001), (1000, 256, 2500), (20, 33100, 50), (66, 8300, 136)])
 @pytest.mark.parametrize("scale", ["f32", "e8m0"])
 def test_gated_against_64_bits(moe, m, k, n, scale):
     check_gated(moe, m, k, n, scale)
