@@ -24,8 +24,11 @@
 // eight finds room beside others.
 //
 // fp32 scales: each stage has its own tensor-memory buffer, drained and scaled in
-// registers as its MMAs end.  Pairs of blocks go to the two warps of a lane quarter
-// in turn, and the two sums are added once at the end.
+// registers as its MMAs end, block by block in K order.  The two warps of a lane
+// quarter take half of the tokens each: 8, 16 or 32 sums a thread, which leaves
+// the 96 registers that two CTAs per SM allow without spilling (64 sums a thread
+// spilled, and with shared memory taking the L1, 64 tokens cost 90 us where 16
+// took 17).
 // e8m0 scales: the tensor core applies them (mxf8f6f4, block_scale; see the
 // many-token form), the range accumulates in tensor memory and is read once; warps
 // 2 and 3 lay out the scale factors.  Ranges of more than 64 blocks take the first
@@ -34,6 +37,8 @@
 // Gated: a cluster holds the 256 interleaved gate/up rows of 128 features (two
 // tiles of 128 rows, S ranges of K each), which is one quantisation group.
 #include "fp8_gemm.cuh"
+
+#include <cmath>
 
 namespace moe {
 namespace few {
@@ -108,25 +113,35 @@ __device__ __forceinline__ float4 load_sa4(const uint8_t* sl, int t, int a_rows)
                        e8m0_to_f32((uint8_t)(v >> 24)));
 }
 
-// acc[t] += D[t] * (s_w * s_x[t]) for KBS K blocks side by side in tensor memory, PC columns at a time.
-template <int TN, int KBS, int PC, bool E8>
-__device__ __forceinline__ void take(uint32_t tb, const uint8_t* sl, int pitch, const float* sw, int a_rows,
-                                     float (&acc)[TN]) {
+__device__ __forceinline__ void ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// acc[t] += D[t] * (s_w * s_x[t]) for HT tokens from t0 of KBS K blocks, TN columns apart in tensor
+// memory.  Straight-line code from the loads to the products: the shared-memory reads of the scales
+// overlap the tensor-memory loads, which a branch between would prevent.
+template <int TN, int KBS, bool E8>
+__device__ __forceinline__ void take(uint32_t tb, const uint8_t* sl, int pitch, const float* sw, int t0, int a_rows,
+                                     float (&acc)[TN / 2]) {
+    constexpr int HT = TN / 2, PC = HT < 16 ? HT : 16;
 #pragma unroll
-    for (int p = 0; p < TN; p += PC) {
+    for (int p = 0; p < HT; p += PC) {
         uint32_t raw[KBS][PC];
 #pragma unroll
-        for (int j = 0; j < KBS; ++j)
-#pragma unroll
-            for (int w = 0; w < PC; w += 16)
-                tc::tmem_ld16u(tb + j * TN + p + w, reinterpret_cast<uint32_t(&)[16]>(raw[j][w]));
+        for (int j = 0; j < KBS; ++j) {
+            if constexpr (PC == 8) ld8(tb + j * TN, raw[j]);
+            else tc::tmem_ld16u(tb + j * TN + p, raw[j]);
+        }
         float4 c[KBS][PC / 4];
         float s[KBS];
 #pragma unroll
         for (int j = 0; j < KBS; ++j) {
             s[j] = sw[2 * j];
 #pragma unroll
-            for (int q = 0; q < PC / 4; ++q) c[j][q] = load_sa4<E8>(sl + j * pitch, p + 4 * q, a_rows);
+            for (int q = 0; q < PC / 4; ++q) c[j][q] = load_sa4<E8>(sl + j * pitch, t0 + p + 4 * q, a_rows);
         }
         tc::tmem_wait_ld();
 #pragma unroll
@@ -138,13 +153,6 @@ __device__ __forceinline__ void take(uint32_t tb, const uint8_t* sl, int pitch, 
                 fma2s(acc[t + 2], acc[t + 3], raw[j][4 * q + 2], raw[j][4 * q + 3], s[j], c[j][q].z, c[j][q].w);
             }
     }
-}
-
-__device__ __forceinline__ void ld8(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr)
-                 : "memory");
 }
 
 __device__ __forceinline__ void store_y(const FewArgs& a, int t, int n, float v) {
@@ -186,8 +194,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
 
     pdl_trigger();
     if (threadIdx.x == 0) {
-        // fp32 form: a group of four blocks is drained by both warps of each quarter, a smaller one by one
-        const uint32_t drains = MODE == MX ? 1 : a.G == 4 ? EPI_WARPS : EPI_WARPS / 2;
+        const uint32_t drains = MODE == MX ? 1 : EPI_WARPS;
         for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], drains); mbar_init(&tfull[s], 1); }
         if (MODE == MX) {
             mbar_init(&sfull, 1);
@@ -348,7 +355,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
     }
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FEW_DRAIN_REGS));
     // -------------------------------------------------------- drain warps
-    const int ew = warp - CTRL_WARPS, quarter = warp & 3, turn = ew >> 2;
+    const int ew = warp - CTRL_WARPS, quarter = warp & 3, half = ew >> 2;
     const int row = quarter * 32 + lane;                       // weight row of the tile = TMEM lane
     const bool live = quarter * 32 < a.R;
     if (MODE != MX) {
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
             tc::tc_fence_after();
             // the two warps of a quarter take eight tokens in turn
 #pragma unroll 1
-            for (int c = 8 * turn; c < min(TN, a.M); c += 16) {
+            for (int c = 8 * half; c < min(TN, a.M); c += 16) {
                 uint32_t raw[8];
                 ld8(tmem + c, raw);
                 tc::tmem_wait_ld();
@@ -388,65 +395,49 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
             }
         }
     } else {
-        float acc[TN];
+        constexpr int HT = TN / 2;
+        const int t0 = half * HT;                              // my first token
+        const bool mine = live && t0 < a.M;                    // warp-uniform: tcgen05.ld is warp-collective
+        float acc[HT];
 #pragma unroll
-        for (int t = 0; t < TN; ++t) acc[t] = 0.f;
+        for (int t = 0; t < HT; ++t) acc[t] = 0.f;
         int st = 0;
         uint32_t phase = 0;
         bool dead = false;
         for (int g = 0; g < n_grp; ++g) {
-            const int kb = g * a.G;
-            if (a.G == 4 || ((kb >> 1) & 1) == turn) {
-                // my blocks of this group: a pair (or, with G = 1 or at the end, one block)
-                const int k0 = kb + (a.G == 4 ? 2 * turn : 0), nk = min(min(a.G, 2), nkb - k0);
-                // Skipping groups is safe: MMAs end in order and the ring is long enough that the stage's
-                // previous use came before my last group.  The second wait returns at once: it makes the
-                // stage's scales visible here.
-                if (!dead) {
-                    dead = !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[st], phase, a.wait_limit, a.status, abort) &&
-                                                        mbar_wait_bounded(&full[st], phase, a.wait_limit, a.status, abort));
-                }
-                const bool work = !dead && live && nk > 0;     // warp-uniform: tcgen05.ld is warp-collective
-                if (work) {
-                    tc::tc_fence_after();
-                    const uint32_t tb = tmem + (uint32_t)((st * a.G + k0 - kb) * TN);
-                    const uint8_t* sl = scales + st * slot_bytes + (k0 - kb) * pitch;
-                    const float* sw = sws + 2 * k0 + sel;
-                    // Straight-line code from the loads to the products: the shared-memory reads of the
-                    // scales overlap the tensor-memory loads, which a branch between would prevent.
-                    if (TN == 16 && nk == 2) {
-                        take<TN, 2, 16, E8S>(tb, sl, pitch, sw, a.a_rows, acc);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            if (j < nk) take<TN, 1, 16, E8S>(tb + j * TN, sl + j * pitch, pitch, sw + 2 * j, a.a_rows, acc);
-                    }
-                    tc::tc_fence_before();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[st]);
+            const int k0 = g * a.G, nk = min(a.G, nkb - k0);
+            // the second wait returns at once: it makes the stage's scales visible here
+            if (!dead) {
+                dead = !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[st], phase, a.wait_limit, a.status, abort) &&
+                                                    mbar_wait_bounded(&full[st], phase, a.wait_limit, a.status, abort));
             }
+            if (mine && !dead) {
+                tc::tc_fence_after();
+                const uint32_t tb = tmem + (uint32_t)(st * a.G * TN + t0);
+                const uint8_t* sl = scales + st * slot_bytes;
+                const float* sw = sws + 2 * k0 + sel;
+                int i = 0;
+                if constexpr (TN <= 32) {                      // two blocks' loads in flight where registers allow
+#pragma unroll 1
+                    for (; i + 2 <= nk; i += 2) take<TN, 2, E8S>(tb + i * TN, sl + i * pitch, pitch, sw + 2 * i, t0, a.a_rows, acc);
+                }
+#pragma unroll 1
+                for (; i < nk; ++i) take<TN, 1, E8S>(tb + i * TN, sl + i * pitch, pitch, sw + 2 * i, t0, a.a_rows, acc);
+                tc::tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[st]);
             if (++st == a.stages) { st = 0; phase ^= 1u; }
         }
         pdl_wait();                                            // before the first write the preceding kernel may conflict with
-        // the two warps of a quarter add their sums
-        if (turn == 1 && live) {
+        if (live) {
 #pragma unroll
-            for (int t = 0; t < TN; ++t) {
-                if (t >= a.M) break;
-                part[t * BM + row] = acc[t];
-            }
-        }
-        named_bar_sync(1, EPI_WARPS * 32);
-        if (turn == 0 && live) {
-#pragma unroll
-            for (int t = 0; t < TN; ++t) {
-                if (t >= a.M) break;
-                const float v = acc[t] + part[t * BM + row];
+            for (int t = 0; t < HT; ++t) {
+                if (t0 + t >= a.M) break;
                 if (!GATED && csize == 1) {
-                    if (row < a.R && n0 + row < a.N) store_y(a, t, n0 + row, v);
+                    if (row < a.R && n0 + row < a.N) store_y(a, t0 + t, n0 + row, acc[t]);
                 } else {
-                    part[t * BM + row] = v;
+                    part[(t0 + t) * BM + row] = acc[t];
                 }
             }
         }
@@ -518,28 +509,38 @@ struct FewPlan {
     int R, S, G;
 };
 
-// Rows per tile and K ranges, from the weights' shape alone.  A CTA's time is its share of the
-// weights at the rate that so many SMs reach (at most 70 GB/s each and 6.8 TB/s together), or
-// a commit's 0.27 us per group where its rows are few; joining K ranges costs about a microsecond.
+// The longest of S ranges of kt blocks.
+static int longest_range(int kt, int S) {
+    int kr = 0;
+    for (int i = 0; i < S; ++i) kr = std::max(kr, range_start(kt, S, i + 1) - range_start(kt, S, i));
+    return kr;
+}
+
+// Rows per tile and K ranges, from the weights' shape alone.  Fitted to sweeps of R, S and G on this
+// GPU: a CTA takes 0.14 us + 1.3 ns per row for a K block (its MMAs and hand-offs), an SM at most 70 GB/s,
+// all of them 6.8 TB/s; these add up like sides of a right angle, as each covers part of the other.
+// Joining K ranges costs about 1 us, and each CTA 3 ns.  Two CTAs per SM with shorter ranges beat one:
+// 7168 x 7168 takes 11.1 us with R = 112, S = 4 (256 CTAs) and 16.7 with R = 48, S = 1 (150).  Clusters do not
+// pack every SM: past 92 % of the slots a second wave starts (300 CTAs in clusters of four: 12.1 us).
 static FewPlan plan_few(const moe_linear* L, bool gated) {
     FewPlan best = {};
     double best_us = 0;
+    const double slots = 2.0 * L->num_sms;
     for (int S = 1; S <= (gated ? 4 : 8); S *= 2) {
         if (S > (L->kt + 1) / 2) break;                        // every range holds a pair of blocks
-        const int kr = range_start(L->kt, S, 1);               // the longest range, or two blocks less
-        if (kr + 2 > KR_MAX) continue;
+        const int kr = longest_range(L->kt, S);
+        if (kr > KR_MAX) continue;
         for (int R = gated ? BM : 16; R <= BM; R += 16) {
             if (R % S) continue;
-            const long long tiles = gated ? 2LL * ((L->d.out_features + QB - 1) / QB) : (L->rows + R - 1) / R;
-            const long long ctas = tiles * S;
-            const int G = R <= 64 && S == 1 ? 4 : 2;
-            const double sms = (double)std::min<long long>(ctas, L->num_sms);
-            const double rounds = (double)((ctas + L->num_sms - 1) / L->num_sms);
-            const double rate = std::min(70e3, 6.8e6 / sms);             // bytes per us and SM
-            const double us = rounds * std::max(kr * R * 128.0 / rate, kr * 0.27 / G) + (S > 1 ? 1.0 : 0.0);
+            const double tiles = gated ? 2.0 * ((L->d.out_features + QB - 1) / QB) : (double)((L->rows + R - 1) / R);
+            const double ctas = tiles * S, per_sm = ctas <= L->num_sms ? 1.0 : 2.0;
+            const double rounds = std::ceil(ctas / (gated || S > 1 ? 0.92 * slots : slots));
+            const double cta = rounds * std::max(kr * (0.14 + 0.0013 * R), per_sm * kr * R * 128.0 / 70e3);
+            const double hbm = L->kt * tiles * R * 128.0 / 6.8e6;
+            const double us = std::sqrt(cta * cta + hbm * hbm) + (S > 1 ? 1.0 : 0.0) + 0.003 * ctas;
             if (!best.R || us < best_us) {
                 best_us = us;
-                best = FewPlan{R, S, G};
+                best = FewPlan{R, S, R <= 64 && kr >= 8 ? 4 : 2};
             }
         }
     }
@@ -563,9 +564,7 @@ cudaError_t launch_few(const GemmCall& c, const FewPlan& p, int kr, cudaStream_t
     a.y = c.y; a.ldy = c.ldy; a.y_f32 = c.y_f32;
     a.hq = c.hq; a.ld_hq = c.ld_hq; a.hs = c.hs; a.ld_hs = c.ld_hs;
     a.status = L->dev_status; a.wait_limit = L->wait_limit;
-    // Blocks per stage: the plan's, unless fewer than three stages would fit.  The fp32 form needs three
-    // where its drain warps skip groups (one block a stage always gives them: 24 KB at most); the other
-    // works with two.
+    // blocks per stage: the plan's, unless fewer than three stages would fit (one block: two)
     const int pitch = sa_pitch(a.a_rows, MODE != F32);
     int smem = 0;
     for (a.G = std::min(p.G, group_cap(TN)); a.G >= 1; a.G /= 2) {
@@ -575,7 +574,7 @@ cudaError_t launch_few(const GemmCall& c, const FewPlan& p, int kr, cudaStream_t
         if (MODE != MX) a.stages = std::min(a.stages, COLS / (a.G * TN));
         a.stages = std::min(a.stages, (kr + a.G - 1) / a.G);
         smem = fixed + a.stages * stage;
-        if (a.stages >= std::min(MODE == MX && a.G == 1 ? 2 : 3, (kr + a.G - 1) / a.G)) break;
+        if (a.stages >= std::min(a.G == 1 ? 2 : 3, (kr + a.G - 1) / a.G)) break;
     }
     if (a.G < 1) return cudaErrorInvalidValue;
     Maps maps;
@@ -621,8 +620,7 @@ static cudaError_t launch_tokens(const GemmCall& c, const FewPlan& p, int kr, cu
 template <bool GATED>
 static cudaError_t launch_mode(const GemmCall& c, cudaStream_t s) {
     const FewPlan p = plan_few(c.lin, GATED);
-    int kr = 0;
-    for (int i = 0; i < p.S; ++i) kr = std::max(kr, range_start(c.lin->kt, p.S, i + 1) - range_start(c.lin->kt, p.S, i));
+    const int kr = longest_range(c.lin->kt, p.S);
     if (c.lin->d.scale_type == MOE_SCALE_F32) return launch_tokens<GATED, F32>(c, p, kr, s);
     return kr <= MX_MAX_KB ? launch_tokens<GATED, MX>(c, p, kr, s) : launch_tokens<GATED, E8>(c, p, kr, s);
 }
