@@ -238,6 +238,17 @@ __device__ __forceinline__ uint32_t idesc_mx(int n, int sf_id) {
     return ((uint32_t)sf_id << 4) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(BM >> 4) << 24) | ((uint32_t)sf_id << 29);
 }
 
+// One look at a barrier; unlike try_wait it never suspends the thread.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
@@ -376,6 +387,12 @@ __device__ __forceinline__ void epi_plain(const Args& a, const EpiCtx& x, const 
     }
 }
 
+// A block's scales as they were loaded: the token's (bits, or the e8m0 byte) and the weights'.
+struct Fetched {
+    uint32_t x;
+    float w0, w1;
+};
+
 // GRP: K blocks per stage, per TMEM buffer and per commit.
 template <int GRP, bool GATED>
 __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
@@ -404,7 +421,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
 
     pdl_trigger();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], 1 + 32); mbar_init(&empty[s], EPI_WARPS); }
+        for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], GRP == 1 ? 1 : 1 + 32); mbar_init(&empty[s], GRP == 1 ? 1 : EPI_WARPS); }
         for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], EPI_WARPS); mbar_init(&xbar[b], 1); }
         fence_mbar_init();
         abort_flag = 0;
@@ -433,7 +450,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
             const uint32_t ring0 = smem_addr(ring), scl0 = smem_addr(scales), full0 = smem_addr(full);
             auto copy_w = [&](int stage, int n0, int g) {
                 const int nk = a.a_whole ? GRP : min(GRP, a.kt - g * GRP);
-                const uint32_t bytes = (uint32_t)(GRP * (w_bytes + pitch) + nk * a_bytes);
+                const uint32_t bytes = (uint32_t)(GRP * (w_bytes + (GRP == 1 ? 0 : pitch)) + nk * a_bytes);
                 if (el) {
                     expect_tx(full0 + 8 * stage, bytes);
                     tma_load_3d(ring0 + stage * stage_bytes, &maps.w, 0, n0, g * GRP, full0 + 8 * stage);
@@ -442,7 +459,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
             auto copy_a = [&](int stage, int m0, int g) {
                 const uint32_t dst = ring0 + stage * stage_bytes + GRP * w_bytes, bar = full0 + 8 * stage;
                 if (el) {
-                    tma_load_2d(scl0 + stage * slot_bytes, &maps.s, m0, g * GRP, bar);
+                    if (GRP > 1) tma_load_2d(scl0 + stage * slot_bytes, &maps.s, m0, g * GRP, bar);
                     if (a.a_whole) {
                         tma_load_3d(dst, &maps.a, 0, m0, g * GRP, bar);
                     } else {
@@ -515,13 +532,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
                         ad += (uint32_t)(a_bytes >> 4);
                         dt += (uint32_t)COLS;
                     }
-                    if (el) tc::mma_commit(&tfull[buf]);        // the drain warps hand the stage back after this
+                    if (el) {
+                        tc::mma_commit(&tfull[buf]);            // GRP > 1: the drain warps hand the stage back after this
+                        if (GRP == 1) tc::mma_commit(&empty[stage]);
+                    }
                     __syncwarp();
                     if (++stage == a.stages) { stage = 0; phase ^= 1u; }
                     if (++buf == 2) { buf = 0; tphase ^= 1u; }
                 }
             }
-        } else if (warp == 2) {
+        } else if (GRP > 1 && warp == 2) {
             // ------------------------------------------------ weight scales: [block of the group][first, second]
             // plain: the scale blocks of the tile's first column and the next; gated: gate and up
             int stage = 0;
@@ -560,7 +580,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
         if (GATED && csize > 1) cluster_wait();
         EpiCtx ctx = {ew, quarter, half, lane, rank, csize, stg_all + (size_t)ew * 32 * STG_STRIDE, amax_cta, amax_all, xbar, 0, 0u, abort};
         int buf = 0, stage = 0;
-        uint32_t tphase = 0, phase = 0;
+        uint32_t tphase = 0;
         bool dead = false;
         for (int u = first; u < a.n_units; u += step) {
             int m0, n0;
@@ -577,75 +597,168 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
             float acc[HALF];
 #pragma unroll
             for (int c = 0; c < HALF; ++c) acc[c] = 0.f;
-            float c0[GRP], c1[GRP];                            // combined scales of the group being drained
             uint32_t pa[PIECE], pb[PIECE];
-            // Waits for the group in (buf, stage), starts its first batch, takes its scales and
-            // hands the stage back.
-            auto open = [&](float (&d0)[GRP], float (&d1)[GRP]) {
-                if (!dead && !(mbar_wait_bounded(&tfull[buf], tphase, a.wait_limit, a.status, abort) &&
-                               mbar_wait_bounded(&full[stage], phase, a.wait_limit, a.status, abort)))
-                    dead = true;
-                dead = __any_sync(0xFFFFFFFFu, dead);          // warp-uniform: tcgen05.ld is warp-collective
-                if (!dead && live) {
-                    tc::tc_fence_after();
-                    ld_batch<HALF, COLS, PIECE>(tmem + buf * BUF_COLS, 0, pa);
-                    const uint8_t* sl = scales + stage * slot_bytes;
-#pragma unroll
-                    for (int i = 0; i < GRP; ++i) {
-                        const float sx = a.e8m0 ? e8m0_to_f32(sl[i * pitch + rs])
-                                                : reinterpret_cast<const float*>(sl + i * pitch)[rs];
-                        const float2 sw = *reinterpret_cast<const float2*>(sl + GRP * pitch + i * 8);
-                        d0[i] = sx * sw.x;
-                        d1[i] = sx * sw.y;
+            if constexpr (GRP == 1) {
+                // One K block per hand-off: what bounds the kernel is this warp's way round a block, so
+                // nothing but tensor memory is waited for.  The scales come straight from global memory
+                // into registers, two blocks ahead, and the MMA warp hands the stage back itself.
+                const int rl = m0 + min(r, valid - 1);
+                const int blk = GATED ? min(n0 / (2 * QB), a.nblk - 1) : min(col0 / QB, a.nblk - 1);
+                const float* sw0 = a.sw + (size_t)blk * a.kt;
+                const float* sw1 = GATED ? sw0 + (size_t)a.nblk * a.kt : sw0;
+                auto fetch = [&](Fetched& f, int kb) {
+                    kb = min(kb, a.kt - 1);
+                    const int64_t at = (int64_t)kb * a.ld_sa + rl;
+                    f.x = a.e8m0 ? (uint32_t)static_cast<const uint8_t*>(a.sa)[at] : static_cast<const uint32_t*>(a.sa)[at];
+                    f.w0 = sw0[kb];
+                    if (GATED) f.w1 = sw1[kb];
+                };
+                auto scales_of = [&](const Fetched& f, float& d0, float& d1) {
+                    const float x = a.e8m0 ? e8m0_to_f32((uint8_t)f.x) : __uint_as_float(f.x);
+                    d0 = x * f.w0;
+                    d1 = GATED ? x * f.w1 : d0;
+                };
+                auto arrived = [&](bool ready) {
+                    if (!__all_sync(0xFFFFFFFFu, ready))
+                        dead = !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[buf], tphase, a.wait_limit, a.status, abort));
+                };
+                auto release = [&]() {
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tempty[buf]);
+                    if (++buf == 2) { buf = 0; tphase ^= 1u; }
+                };
+                if (!live) {
+                    for (int g = 0; g < n_grp && !dead; ++g) {
+                        arrived(false);
+                        release();
                     }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[stage]);
-                if (++stage == a.stages) { stage = 0; phase ^= 1u; }
-            };
-            open(c0, c1);
-            for (int g = 0; g < n_grp; ++g) {
-                const int nk = min(GRP, a.kt - g * GRP);
-                // Without a branch between the products of a block: a partial group (the last) is
-                // told apart per block, outside the column loop.
-                auto add = [&](int b, uint32_t (&raw)[PIECE]) {
-                    constexpr int RUN = HALF < PIECE ? HALF : PIECE;
+                } else if (!dead) {
+                    float c0, c1;
+                    auto add = [&](int b, const uint32_t (&raw)[PIECE]) {
 #pragma unroll
-                    for (int t0 = 0; t0 < PIECE; t0 += RUN) {
-                        const int i = (b * PIECE + t0) / HALF;
-                        if (GRP > 1 && i >= nk) break;
-#pragma unroll
-                        for (int t = t0; t < t0 + RUN; t += 2) {
-                            const int c = (b * PIECE + t) % HALF;
-                            const float k = GATED ? ((c & 8) ? c1[i] : c0[i]) : (((hi_mask >> (c / 16)) & 1u) ? c1[i] : c0[i]);
-                            tc::fma2(acc[c], acc[c + 1], raw[t], raw[t + 1], k);
+                        for (int t = 0; t < PIECE; t += 2)
+                            tc::fma2(acc[b * PIECE + t], acc[b * PIECE + t + 1], raw[t], raw[t + 1], GATED && (t & 8) ? c1 : c0);
+                    };
+                    // block g, whose first batch is on its way into pa; f: the scales of g + 1
+                    auto block = [&](int g, Fetched& f) {
+                        const uint32_t tb = tmem + buf * BUF_COLS;
+                        tc::tmem_wait_ld();
+                        ld_batch<HALF, COLS, PIECE>(tb, 1, pb);
+                        add(0, pa);
+                        tc::tmem_wait_ld();
+                        ld_batch<HALF, COLS, PIECE>(tb, 2, pa);
+                        add(1, pb);
+                        tc::tmem_wait_ld();
+                        ld_batch<HALF, COLS, PIECE>(tb, 3, pb);
+                        // a look at the next block's barrier takes about 100 cycles: the products hide it
+                        const bool ready = mbar_test(&tfull[buf ^ 1], tphase ^ (uint32_t)buf);
+                        add(2, pa);
+                        tc::tmem_wait_ld();
+                        release();
+                        float d0, d1;
+                        if (g + 1 < n_grp) {
+                            arrived(ready);
+                            if (dead) return;
+                            tc::tc_fence_after();
+                            ld_batch<HALF, COLS, PIECE>(tmem + buf * BUF_COLS, 0, pa);
+                            scales_of(f, d0, d1);
+                            fetch(f, g + 3);
+                        }
+                        add(3, pb);
+                        c0 = d0;
+                        c1 = d1;
+                    };
+                    Fetched f0, f1, f2;
+                    fetch(f2, 0);
+                    fetch(f1, 1);
+                    fetch(f0, 2);
+                    arrived(false);
+                    if (!dead) {
+                        tc::tc_fence_after();
+                        ld_batch<HALF, COLS, PIECE>(tmem + buf * BUF_COLS, 0, pa);
+                        scales_of(f2, c0, c1);
+                        for (int g = 0; g < n_grp; g += 2) {
+                            block(g, f1);
+                            if (dead || g + 1 >= n_grp) break;
+                            block(g + 1, f0);
+                            if (dead) break;
                         }
                     }
-                };
-                float e0[GRP], e1[GRP];
-                const bool work = !dead && live;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    uint32_t(&cur)[PIECE] = (b & 1) ? pb : pa;
-                    uint32_t(&nxt)[PIECE] = (b & 1) ? pa : pb;
-                    if (work) tc::tmem_wait_ld();
-                    if (b < NB - 1) {
-                        if (work) ld_batch<HALF, COLS, PIECE>(tmem + buf * BUF_COLS, b + 1, nxt);
-                    } else {
-                        // the buffer is in registers: hand it back, and start on the next group
-                        // before this one's last products are added
-                        static_assert(NB % 2 == 0, "the next group's first batch goes into pa");
-                        tc::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&tempty[buf]);
-                        if (++buf == 2) { buf = 0; tphase ^= 1u; }
-                        if (g + 1 < n_grp) open(e0, e1);
-                    }
-                    if (work) add(b, cur);
                 }
-                if (g + 1 < n_grp) {
+            } else {
+                float c0[GRP], c1[GRP];                            // combined scales of the group being drained
+                // Waits for the group in (buf, stage) unless it is known to be there, starts its first batch,
+                // takes its scales and hands the stage back.  The scales arrived on the stage's barrier, which
+                // the MMA warp waited for before it issued the MMAs whose commit is waited for here.
+                auto open = [&](float (&d0)[GRP], float (&d1)[GRP], bool ready) {
+                    if (!dead && !__all_sync(0xFFFFFFFFu, ready))
+                        dead = !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[buf], tphase, a.wait_limit, a.status, abort));
+                    if (!dead && live) {                           // warp-uniform: tcgen05.ld is warp-collective
+                        tc::tc_fence_after();
+                        ld_batch<HALF, COLS, PIECE>(tmem + buf * BUF_COLS, 0, pa);
+                        const uint8_t* sl = scales + stage * slot_bytes;
 #pragma unroll
-                    for (int i = 0; i < GRP; ++i) { c0[i] = e0[i]; c1[i] = e1[i]; }
+                        for (int i = 0; i < GRP; ++i) {
+                            const float sx = a.e8m0 ? e8m0_to_f32(sl[i * pitch + rs])
+                                                    : reinterpret_cast<const float*>(sl + i * pitch)[rs];
+                            const float2 sw = *reinterpret_cast<const float2*>(sl + GRP * pitch + i * 8);
+                            d0[i] = sx * sw.x;
+                            d1[i] = sx * sw.y;
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&empty[stage]);
+                    if (++stage == a.stages) stage = 0;
+                };
+                open(c0, c1, false);
+                for (int g = 0; g < n_grp; ++g) {
+                    const int nk = min(GRP, a.kt - g * GRP);
+                    // Without a branch between the products of a block: a partial group (the last) is
+                    // told apart per block, outside the column loop.
+                    auto add = [&](int b, uint32_t (&raw)[PIECE]) {
+                        constexpr int RUN = HALF < PIECE ? HALF : PIECE;
+#pragma unroll
+                        for (int t0 = 0; t0 < PIECE; t0 += RUN) {
+                            const int i = (b * PIECE + t0) / HALF;
+                            if (i >= nk) break;
+#pragma unroll
+                            for (int t = t0; t < t0 + RUN; t += 2) {
+                                const int c = (b * PIECE + t) % HALF;
+                                const float k = GATED ? ((c & 8) ? c1[i] : c0[i]) : (((hi_mask >> (c / 16)) & 1u) ? c1[i] : c0[i]);
+                                tc::fma2(acc[c], acc[c + 1], raw[t], raw[t + 1], k);
+                            }
+                        }
+                    };
+                    float e0[GRP], e1[GRP];
+                    bool ready = false;
+                    const bool work = !dead && live;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        uint32_t(&cur)[PIECE] = (b & 1) ? pb : pa;
+                        uint32_t(&nxt)[PIECE] = (b & 1) ? pa : pb;
+                        if (work) tc::tmem_wait_ld();
+                        if (b < NB - 1) {
+                            if (work) ld_batch<HALF, COLS, PIECE>(tmem + buf * BUF_COLS, b + 1, nxt);
+                        } else {
+                            // the buffer is in registers: hand it back, and start on the next group
+                            // before this one's last products are added
+                            static_assert(NB % 2 == 0, "the next group's first batch goes into pa");
+                            tc::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&tempty[buf]);
+                            if (++buf == 2) { buf = 0; tphase ^= 1u; }
+                            if (g + 1 < n_grp) open(e0, e1, ready);
+                        }
+                        // the poll of the next group's barrier takes about 150 cycles: this batch's products hide it
+                        if (b == NB - 2 && !dead)
+                            ready = mbar_test(&tfull[buf ^ 1], tphase ^ (uint32_t)buf);
+                        if (work) add(b, cur);
+                    }
+                    if (g + 1 < n_grp) {
+#pragma unroll
+                        for (int i = 0; i < GRP; ++i) { c0[i] = e0[i]; c1[i] = e1[i]; }
+                    }
                 }
             }
 
