@@ -73,15 +73,6 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
 // (a0, a1) += (x0, x1) * s * (c0, c1), rounded as s * c and one fma each.
 __device__ __forceinline__ void fma2s(float& a0, float& a1, uint32_t x0, uint32_t x1, float s, float c0, float c1) {
     asm("{\n .reg .b64 a, x, c, s;\n mov.b64 a, {%0, %1};\n mov.b64 x, {%2, %3};\n mov.b64 c, {%5, %6};\n mov.b64 s, {%4, %4};\n"
@@ -455,40 +446,15 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
             // a warp takes a token: four features a lane, 128 in all
             const int f = 4 * lane, ff = f & 63, r = (ff >> 3) * 16 + (ff & 7);
             const int base = (f >> 6) * a.S;                   // first rank of the tile with these features
-            const int f0 = unit * QB + f;
             for (int t = rank * EPI_WARPS + (tid >> 5); t < a.M; t += csize * EPI_WARPS) {
                 float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
                 for (int p = 0; p < a.S; ++p) {
                     const uint32_t at = map_to_rank(part0 + (uint32_t)(t * BM + r) * 4u, base + p);
                     const float4 x = ld_cluster4(at), z = ld_cluster4(at + 32);
-                    g.x += x.x; g.y += x.y; g.z += x.z; g.w += x.w;
-                    u.x += z.x; u.y += z.y; u.z += z.z; u.w += z.w;
+                    g = add4(g, x);
+                    u = add4(u, z);
                 }
-                float h[4] = {silu_mul(g.x, u.x), silu_mul(g.y, u.y), silu_mul(g.z, u.z), silu_mul(g.w, u.w)};
-                float am = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (f0 + e >= a.N) h[e] = 0.f;
-                    am = max_nan(am, fabsf(h[e]));
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
-                uint32_t held;
-                const float is = inv_scale(group_scale(am, E8S, held));
-                const uint32_t v = pack4_e4m3(h[0] * is, h[1] * is, h[2] * is, h[3] * is);
-                uint8_t* dst = a.hq + (int64_t)t * a.ld_hq + f0;
-                if (f0 + 4 <= a.N) {
-                    *reinterpret_cast<uint32_t*>(dst) = v;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (f0 + e < a.N) dst[e] = (uint8_t)(v >> (8 * e));
-                }
-                if (lane == 0) {
-                    const int64_t at = (int64_t)unit * a.ld_hs + t;
-                    if (E8S) static_cast<uint8_t*>(a.hs)[at] = (uint8_t)held;
-                    else static_cast<uint32_t*>(a.hs)[at] = held;
-                }
+                quantise_row(a, E8S, t, unit, lane, g, u);
             }
         } else {
             // each CTA of the cluster finishes a slice of the tile's rows

@@ -9,27 +9,35 @@
 namespace moe {
 namespace dg {
 
+// CTAs per unit of 128 features: a cluster that shares its rows, or its K.
 static Plan plan_gated(const GemmCall& c, const Args& a) {
     const int sms = c.lin->num_sms;
     const int mt = (c.M + BM - 1) / BM, nt = (c.lin->d.out_features + QB - 1) / QB;
+    const long long units = (long long)mt * nt;
     Plan best = {};
-    double best_cost = 0;
+    double best_us = 0;
+    if (units > 0x3FFFFFFF) return best;
+    // microseconds of a K block: draining its columns, or the copies into one SM
+    auto block_us = [&](int grp, int bn) {
+        const double drain = grp == 1 ? 0.55 : grp == 2 ? 0.42 : grp == 4 ? 0.23 : 0.15;
+        return std::max(drain, (bn + a.a_rows) * 128.0 / 110e3);
+    };
     for (int cl = 1; cl <= MAX_CLUSTER; cl *= 2) {
         const int grp = cl, bn = BUF_COLS / cl;
-        if (2 * stage_cost(grp, bn, a.a_rows, a.e8m0) > ring_max(true)) continue;
-        const long long units = (long long)mt * nt;
-        if (units > 0x3FFFFFFF) continue;
-        const int slots = sms / cl;
-        const double waves = (double)((units + slots - 1) / slots);
-        const double drain = grp == 1 ? 1000 : grp == 2 ? 560 : grp == 4 ? 300 : 180;
-        const double share = (double)(units < slots ? units : slots) * cl;
-        const double hbm = mt == 1 ? bn * 128.0 * share / 3600.0 : 0.0;
-        const double l2 = (bn + a.a_rows) * 128.0 / 60.0;
-        const double per = std::max(drain, std::max(hbm, l2));
-        const double cost = waves * (a.kt * per + 3000.0 + (cl > 1 ? 1500.0 : 0.0));
-        if (best.bn == 0 || cost < best_cost) {
-            best_cost = cost;
-            best = Plan{grp, bn, cl, (int)units, nt};
+        if (2 * stage_cost(grp, bn, a.a_rows, a.e8m0) <= ring_max(true)) {
+            const int slots = (int)(cl > 2 ? 0.92 * sms / cl : sms / cl);
+            const double us = (double)((units + slots - 1) / slots) * (a.kt * block_us(grp, bn) + 1.0) + (cl > 1 ? 0.8 : 0.0);
+            if (best.bn == 0 || us < best_us) {
+                best_us = us;
+                best = Plan{grp, bn, cl, (int)units, nt, 1};
+            }
+        }
+        if (cl > 1 && cl <= a.kt && units * cl <= 0.92 * sms) {
+            const double us = ((a.kt + cl - 1) / cl) * block_us(1, BUF_COLS) + 4.5;
+            if (us < best_us) {
+                best_us = us;
+                best = Plan{1, BUF_COLS, cl, (int)units, nt, cl};
+            }
         }
     }
     return best;

@@ -31,8 +31,10 @@
 // whatever lies behind them in shared memory into TMEM lanes nobody reads.
 //
 // Copies of weights start before the wait for the preceding kernel, and before
-// the tensor memory is allocated: a small call's ring leaves room for two CTAs
-// on an SM, so the next call's weights are on their way while this one ends.
+// the tensor memory is allocated.
+//
+// Where tiles alone leave SMs idle, a cluster of S CTAs shares each tile's K and
+// adds the partial sums through distributed shared memory (BN = 128 and 256).
 #pragma once
 #include "dense_internal.cuh"
 #include "tcgen05.cuh"
@@ -85,6 +87,7 @@ struct Args {
     int stages;
     int n_nt;                 // weight tiles per token tile
     int n_units;
+    int S;                    // K ranges of a unit, one per CTA of its cluster; 1: none
     bool e8m0;
     bool a_whole;             // K is a multiple of 128: one copy brings all of a group's token tiles
     // plain
@@ -387,6 +390,98 @@ __device__ __forceinline__ void epi_plain(const Args& a, const EpiCtx& x, const 
     }
 }
 
+// ------------------------------------------------------------------ K ranges
+// With S > 1 the CTAs of a cluster have a K range of the same unit each.  Every one leaves its
+// partial sums in its shared memory, [128 rows][BN + 4] fp32 over the ring (one unit per cluster, so
+// no copy is in flight any more); then the rows are dealt out, and a warp adds a row's S partials in
+// rank order and finishes it.
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+
+constexpr int part_pitch(int bn) { return bn + 4; }          // floats; 16-byte rows, free of bank conflicts
+
+template <int HALF>
+__device__ __forceinline__ void leave_partial(float* part, int half, int r, const float (&acc)[HALF]) {
+    float* p = part + r * part_pitch(2 * HALF) + half * HALF;
+#pragma unroll
+    for (int c = 0; c < HALF; c += 4) *reinterpret_cast<float4*>(p + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+}
+
+// 4 features' codes and, by lane 0, the group's scale: one warp holds a row's 128 features.
+template <class A>
+__device__ __forceinline__ void quantise_row(const A& a, bool e8, int64_t row, int unit, int lane, const float4& g, const float4& u) {
+    const int f0 = unit * QB + 4 * lane;
+    float h[4] = {silu_mul(g.x, u.x), silu_mul(g.y, u.y), silu_mul(g.z, u.z), silu_mul(g.w, u.w)};
+    float am = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (f0 + e >= a.N) h[e] = 0.f;
+        am = max_nan(am, fabsf(h[e]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+    uint32_t held;
+    const float is = inv_scale(group_scale(am, e8, held));
+    const uint32_t v = pack4_e4m3(h[0] * is, h[1] * is, h[2] * is, h[3] * is);
+    uint8_t* dst = a.hq + row * a.ld_hq + f0;
+    if (f0 + 4 <= a.N) {
+        *reinterpret_cast<uint32_t*>(dst) = v;
+    } else {
+        for (int e = 0; f0 + e < a.N; ++e) dst[e] = (uint8_t)(v >> (8 * e));
+    }
+    if (lane == 0) {
+        const int64_t at = (int64_t)unit * a.ld_hs + row;
+        if (e8) static_cast<uint8_t*>(a.hs)[at] = (uint8_t)held;
+        else static_cast<uint32_t*>(a.hs)[at] = held;
+    }
+}
+
+// Drain warp ew of CTA `rank` adds and finishes rows ew S + rank, + 8 S, ...
+template <int BN, bool GATED>
+__device__ __forceinline__ void join_partials(const Args& a, uint32_t part0, int rank, int ew, int lane, int m0, int n0, int valid) {
+    for (int r = ew * a.S + rank; r < valid; r += EPI_WARPS * a.S) {
+        const uint32_t row = part0 + (uint32_t)(r * part_pitch(BN)) * 4u;
+        if constexpr (GATED) {
+            const uint32_t at = row + (uint32_t)((lane >> 1) * 16 + (lane & 1) * 4) * 4u;      // 8 gate columns, then 8 up
+            float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+            for (int p = 0; p < a.S; ++p) {
+                const uint32_t from = map_to_rank(at, p);
+                g = add4(g, ld_cluster4(from));
+                u = add4(u, ld_cluster4(from + 32));
+            }
+            quantise_row(a, a.e8m0, m0 + r, n0 / (2 * QB), lane, g, u);
+        } else {
+            for (int c = 4 * lane; c < BN && n0 + c < a.N; c += 128) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int p = 0; p < a.S; ++p) v = add4(v, ld_cluster4(map_to_rank(row + 4u * c, p)));
+                const int64_t at = (int64_t)(m0 + r) * a.ldy + n0 + c;
+                if (a.y_vec && n0 + c + 4 <= a.N) {
+                    if (a.y_f32) {
+                        *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = v;
+                    } else {
+                        __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
+                            make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+                    }
+                } else {
+                    const float e[4] = {v.x, v.y, v.z, v.w};
+                    for (int i = 0; i < 4 && n0 + c + i < a.N; ++i) {
+                        if (a.y_f32) static_cast<float*>(a.y)[at + i] = e[i];
+                        else static_cast<__nv_bfloat16*>(a.y)[at + i] = __float2bfloat16_rn(e[i]);
+                    }
+                }
+            }
+        }
+    }
+}
+
 // A block's scales as they were loaded: the token's (bits, or the e8m0 byte) and the weights'.
 struct Fetched {
     uint32_t x;
@@ -415,9 +510,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
     __shared__ int abort_flag;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = GATED ? cluster_rank() : 0u, csize = GATED ? cluster_size() : 1u;
-    const int first = blockIdx.x / csize, step = gridDim.x / csize;   // units go to clusters
-    const int n_grp = (a.kt + GRP - 1) / GRP;
+    // a cluster shares a unit's K (S > 1), or the 128 features of a gated unit
+    constexpr bool CAN_SPLIT = GRP == 1 || (GRP == 2 && !GATED);
+    const bool shared_k = CAN_SPLIT && a.S > 1;
+    const uint32_t crank = GATED || CAN_SPLIT ? cluster_rank() : 0u, cctas = GATED || CAN_SPLIT ? cluster_size() : 1u;
+    const uint32_t rank = shared_k ? 0u : crank, csize = shared_k ? 1u : cctas;
+    const int first = blockIdx.x / cctas, step = gridDim.x / cctas;   // units go to clusters
+    const int groups = (a.kt + GRP - 1) / GRP, split = shared_k ? (int)crank : 0;
+    const int g0 = groups * split / a.S, n_grp = groups * (split + 1) / a.S - g0;      // this CTA's groups of K blocks
+    const int kb_end = min(a.kt, (g0 + n_grp) * GRP);
 
     pdl_trigger();
     if (threadIdx.x == 0) {
@@ -449,23 +550,23 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
             }
             const uint32_t ring0 = smem_addr(ring), scl0 = smem_addr(scales), full0 = smem_addr(full);
             auto copy_w = [&](int stage, int n0, int g) {
-                const int nk = a.a_whole ? GRP : min(GRP, a.kt - g * GRP);
+                const int nk = a.a_whole ? GRP : min(GRP, a.kt - (g0 + g) * GRP);
                 const uint32_t bytes = (uint32_t)(GRP * (w_bytes + (GRP == 1 ? 0 : pitch)) + nk * a_bytes);
                 if (el) {
                     expect_tx(full0 + 8 * stage, bytes);
-                    tma_load_3d(ring0 + stage * stage_bytes, &maps.w, 0, n0, g * GRP, full0 + 8 * stage);
+                    tma_load_3d(ring0 + stage * stage_bytes, &maps.w, 0, n0, (g0 + g) * GRP, full0 + 8 * stage);
                 }
             };
             auto copy_a = [&](int stage, int m0, int g) {
                 const uint32_t dst = ring0 + stage * stage_bytes + GRP * w_bytes, bar = full0 + 8 * stage;
                 if (el) {
-                    if (GRP > 1) tma_load_2d(scl0 + stage * slot_bytes, &maps.s, m0, g * GRP, bar);
+                    if (GRP > 1) tma_load_2d(scl0 + stage * slot_bytes, &maps.s, m0, (g0 + g) * GRP, bar);
                     if (a.a_whole) {
-                        tma_load_3d(dst, &maps.a, 0, m0, g * GRP, bar);
+                        tma_load_3d(dst, &maps.a, 0, m0, (g0 + g) * GRP, bar);
                     } else {
-                        const int nk = min(GRP, a.kt - g * GRP);
+                        const int nk = min(GRP, a.kt - (g0 + g) * GRP);
                         for (int i = 0; i < nk; ++i)
-                            tma_load_3d(dst + i * a_bytes, &maps.a, (g * GRP + i) * QB, m0, 0, bar);
+                            tma_load_3d(dst + i * a_bytes, &maps.a, ((g0 + g) * GRP + i) * QB, m0, 0, bar);
                     }
                 }
             };
@@ -522,7 +623,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
                                                      mbar_wait_bounded(&tempty[buf], tphase ^ 1u, a.wait_limit, a.status, abort));
                     if (!ok) break;
                     tc::tc_fence_after();
-                    const int nk = min(GRP, a.kt - g * GRP);
+                    const int nk = min(GRP, kb_end - (g0 + g) * GRP);
                     uint32_t wd = d0 + (uint32_t)((stage * stage_bytes) >> 4);
                     uint32_t ad = wd + (uint32_t)((GRP * w_bytes) >> 4);
                     uint32_t dt = tmem + (uint32_t)(buf * BUF_COLS);
@@ -557,8 +658,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
                 for (int g = 0; g < n_grp; ++g) {
                     if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, a.wait_limit, a.status, abort)) ok = false;
                     if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-                    if (i < GRP && g * GRP + i < a.kt)
-                        cp_async4(scales + stage * slot_bytes + GRP * pitch + lane * 4, src + g * GRP + i);
+                    if (i < GRP && (g0 + g) * GRP + i < a.kt)
+                        cp_async4(scales + stage * slot_bytes + GRP * pitch + lane * 4, src + (g0 + g) * GRP + i);
                     cp_async_arrive(&full[stage]);
                     if (++stage == a.stages) { stage = 0; phase ^= 1u; }
                 }
@@ -607,7 +708,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
                 const float* sw0 = a.sw + (size_t)blk * a.kt;
                 const float* sw1 = GATED ? sw0 + (size_t)a.nblk * a.kt : sw0;
                 auto fetch = [&](Fetched& f, int kb) {
-                    kb = min(kb, a.kt - 1);
+                    kb = min(g0 + kb, a.kt - 1);
                     const int64_t at = (int64_t)kb * a.ld_sa + rl;
                     f.x = a.e8m0 ? (uint32_t)static_cast<const uint8_t*>(a.sa)[at] : static_cast<const uint32_t*>(a.sa)[at];
                     f.w0 = sw0[kb];
@@ -713,7 +814,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
                 };
                 open(c0, c1, false);
                 for (int g = 0; g < n_grp; ++g) {
-                    const int nk = min(GRP, a.kt - g * GRP);
+                    const int nk = min(GRP, kb_end - (g0 + g) * GRP);
                     // Without a branch between the products of a block: a partial group (the last) is
                     // told apart per block, outside the column loop.
                     auto add = [&](int b, uint32_t (&raw)[PIECE]) {
@@ -762,16 +863,28 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
                 }
             }
 
+            if constexpr (CAN_SPLIT) {
+                if (shared_k) {
+                    if (live) leave_partial<HALF>(reinterpret_cast<float*>(ring), half, r, acc);
+                    cluster_arrive_release();
+                    cluster_wait();
+                    if (!*abort) join_partials<COLS, GATED>(a, smem_addr(ring), split, ew, lane, m0, n0, valid);
+                    continue;
+                }
+            }
             if constexpr (GATED) epi_gated<HALF>(a, ctx, acc, m0, n0, valid, dead);
             else if (live && !dead) epi_plain<HALF>(a, ctx, acc, m0, n0, valid);
         }
     }
-    if (GATED && csize > 1 && warp < CTRL_WARPS) cluster_wait();
+    if (warp < CTRL_WARPS) {
+        if (shared_k) cluster_arrive_release();                // the drain warps' barrier before they join
+        if (shared_k || (GATED && csize > 1)) cluster_wait();
+    }
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     if (warp == 1) tc::tmem_dealloc(tmem_slot, 512);
-    if (GATED && csize > 1) {                   // nobody leaves while a peer may still send to it
+    if (shared_k || (GATED && csize > 1)) {     // nobody leaves while a peer may still reach into it
         cluster_arrive_release();
         cluster_wait();
     }
@@ -779,7 +892,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
 
 // ------------------------------------------------------------------ launch
 struct Plan {
-    int grp, bn, cluster, units, n_nt;
+    int grp, bn, cluster, units, n_nt, S;
 };
 
 // Tensor maps of one call.  Token codes: [K block][row][128 B] (the K blocks of a row lie side by
@@ -814,17 +927,16 @@ cudaError_t launch(const GemmCall& c, const Plan& p, Args& a, cudaStream_t s) {
     a.bn = p.bn;
     a.n_nt = p.n_nt;
     a.n_units = p.units;
+    a.S = p.S;
     a.a_whole = c.lin->d.in_features % QB == 0;
     Maps maps;
     if (!encode_maps(c, a, GRP, &maps)) return cudaErrorInvalidValue;
-    // A call of one wave at most takes half of the SM's shared memory where that holds two stages
-    // (or all the blocks there are): the next kernel's CTA can then start beside it.
     const int cost = stage_cost(GRP, a.bn, a.a_rows, a.e8m0), fixed = 1024 + (GATED ? TAIL_GATED : TAIL_PLAIN);
-    const int n_grp = (a.kt + GRP - 1) / GRP;
-    const int half = (SMEM_HALF - fixed) / cost;
-    const bool small = (long long)p.units * p.cluster <= c.lin->num_sms && half >= std::min(2, n_grp);
-    a.stages = std::max(1, std::min(std::min(MAX_STAGES, small ? half : (SMEM_MAX - fixed) / cost), std::max(2, n_grp)));
+    const int groups = (a.kt + GRP - 1) / GRP;
+    a.stages = std::max(1, std::min(MAX_STAGES, (SMEM_MAX - fixed) / cost));
+    if (p.S == 1) a.stages = std::min(a.stages, std::max(2, groups));      // S > 1 also keeps its sums there
     const int smem = fixed + a.stages * cost;
+    if (p.S > 1 && a.stages * GRP * (a.bn + a.a_rows) * 128 < BM * part_pitch(a.bn) * 4) return cudaErrorInvalidValue;
     cudaError_t e = ensure_smem_limit<fp8_gemm_kernel<GRP, GATED>>(SMEM_MAX);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -836,16 +948,18 @@ cudaError_t launch(const GemmCall& c, const Plan& p, Args& a, cudaStream_t s) {
     cfg.numAttrs = 1;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    if (GATED && p.cluster > 1) {
+    if (p.cluster > 1) {
         attr[1].id = cudaLaunchAttributeClusterDimension;
         attr[1].val.clusterDim.x = p.cluster;
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.numAttrs = 2;
     }
     int slots = c.lin->num_sms;
-    if (GATED && p.cluster > 1) {
+    if (p.S > 1) {
+        slots = p.units;                      // one unit per cluster
+    } else if (p.cluster > 1) {
         // clusters that fit at once (a cluster stays inside one GPC), asked once: every plan of
-        // this kernel has the same cluster size and one CTA per SM
+        // this kernel without K ranges has the same cluster size and one CTA per SM
         static std::atomic<int> fit{0};
         slots = fit.load(std::memory_order_relaxed);
         if (slots == 0) {

@@ -6,32 +6,36 @@
 namespace moe {
 namespace dg {
 
-// Weight rows per tile.  Few token tiles: narrow tiles, so that every SM
-// streams a share of the weights; many: wide ones, which reuse the tokens.
-// The estimate per K block is the slower of draining the accumulators and of
-// bringing the operands in, and the narrowest cost over whole waves wins.
+// Microseconds of a tile's K block, fitted to sweeps: draining BN columns, or the copies into one SM.
+static double block_us(int grp, int bn, int a_rows) {
+    const double drain = grp == 1 ? 0.55 : grp == 2 ? 0.42 : 0.06 + 0.0027 * bn;
+    return std::max(drain, (bn + a_rows) * 128.0 / 110e3);
+}
+
+// Weight rows per tile, and K ranges: few token tiles take narrow tiles, so that every SM streams a
+// share of the weights, or split K where rows are few and long; many take wide ones, which reuse the
+// tokens.  The shortest estimate over whole waves of tiles wins.
 static Plan plan_plain(const GemmCall& c, const Args& a) {
     const int sms = c.lin->num_sms, rows = c.lin->rows;
     const int mt = (c.M + BM - 1) / BM;
     Plan best = {};
-    double best_cost = 0;
+    double best_us = 0;
     for (int bn = 16; bn <= BUF_COLS; bn += 16) {
         const int grp = bn <= 32 ? 8 : bn <= 64 ? 4 : bn <= 128 ? 2 : 1;
         if (grp == 1 && bn != 256) continue;                   // 256: both halves in whole scale blocks
         if (2 * stage_cost(grp, bn, a.a_rows, a.e8m0) > ring_max(false)) continue;
-        const int nt = (rows + bn - 1) / bn;
+        const int nt = (rows + bn - 1) / bn, groups = (a.kt + grp - 1) / grp;
         const long long units = (long long)mt * nt;
         if (units > 0x3FFFFFFF) continue;
-        const double waves = (double)((units + sms - 1) / sms);
-        const double drain = grp == 1 ? 1000 : grp == 2 ? 560 : grp == 4 ? 300 : 180;
-        const double share = (double)(units < sms ? units : sms);
-        const double hbm = mt == 1 ? bn * 128.0 * share / 3600.0 : 0.0;     // 3600 B per clock from HBM
-        const double l2 = (bn + a.a_rows) * 128.0 / 60.0;                   // B per clock into one SM
-        const double per = std::max(drain, std::max(hbm, l2));
-        const double cost = waves * (a.kt * per + 3000.0);
-        if (best.bn == 0 || cost < best_cost) {
-            best_cost = cost;
-            best = Plan{grp, bn, 1, (int)units, nt};
+        for (int S = 1; S <= 8 && S <= groups; S *= 2) {
+            if (S > 1 && ((bn != 128 && bn != 256) || units * S > 0.92 * sms)) break;
+            const double kr = S > 1 ? std::min<double>(a.kt, (double)grp * ((groups + S - 1) / S)) : a.kt;
+            const double us = (double)((units + sms - 1) / sms) * (kr * block_us(grp, bn, a.a_rows) + 1.0) +
+                              (S > 1 ? 1.5 + bn / 128.0 : 0.0);
+            if (best.bn == 0 || us < best_us) {
+                best_us = us;
+                best = Plan{grp, bn, S, (int)units, nt, S};
+            }
         }
     }
     return best;

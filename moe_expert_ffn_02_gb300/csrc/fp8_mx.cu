@@ -24,6 +24,8 @@
 // and stores, which the next tile's MMAs cover; BN = 128: two accumulators.
 #include "fp8_gemm.cuh"
 
+#include <cmath>
+
 namespace moe {
 namespace mx {
 
@@ -58,9 +60,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
     __shared__ int abort_flag;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = GATED ? cluster_rank() : 0u, csize = GATED ? cluster_size() : 1u;
-    const int first = blockIdx.x / csize, step = gridDim.x / csize;
-    const int kt = a.kt;
+    // a cluster shares a unit's K (S > 1), or the 128 features of a gated unit
+    constexpr bool CAN_SPLIT = !GATED || BN == 256;
+    const bool shared_k = CAN_SPLIT && a.S > 1;
+    const uint32_t crank = cluster_rank(), cctas = cluster_size();
+    const uint32_t rank = shared_k ? 0u : crank, csize = shared_k ? 1u : cctas;
+    const int first = blockIdx.x / cctas, step = gridDim.x / cctas;
+    // this CTA's K blocks [kb0, kb0 + kt): whole quads
+    const int quads = (a.kt + 3) / 4, split = shared_k ? (int)crank : 0;
+    const int kb0 = quads * split / a.S * 4, kt = min(a.kt, quads * (split + 1) / a.S * 4) - kb0;
 
     pdl_trigger();
     if (threadIdx.x == 0) {
@@ -108,10 +116,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
                         if (!ok) break;
                         if (el) {
                             expect_tx(sfull0 + 8 * slot, (uint32_t)(RAW_BYTES + blocks * SF_BYTES));
-                            tma_load_2d(sf0 + slot * SLOT, &maps.s, m0, kb, sfull0 + 8 * slot);
+                            tma_load_2d(sf0 + slot * SLOT, &maps.s, m0, kb0 + kb, sfull0 + 8 * slot);
                             if (blocks > 0)
                                 bulk_g2s(sf + slot * SLOT + RAW_BYTES + SF_BYTES,
-                                         wsf + ((size_t)(kb >> 2) * nrb + n0 / QB) * SF_BYTES, (uint32_t)(blocks * SF_BYTES),
+                                         wsf + ((size_t)((kb0 + kb) >> 2) * nrb + n0 / QB) * SF_BYTES, (uint32_t)(blocks * SF_BYTES),
                                          &sfull[slot]);
                         }
                         sissued = min(sissued + 1, SF_SLOTS);
@@ -122,9 +130,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
                     if (el) {
                         const uint32_t dst = ring0 + stage * stage_bytes, bar = full0 + 8 * stage;
                         expect_tx(bar, (uint32_t)stage_bytes);
-                        tma_load_3d(dst, &maps.w, 0, n0, kb, bar);
-                        if (a.a_whole) tma_load_3d(dst + w_bytes, &maps.a, 0, m0, kb, bar);
-                        else tma_load_3d(dst + w_bytes, &maps.a, kb * QB, m0, 0, bar);
+                        tma_load_3d(dst, &maps.w, 0, n0, kb0 + kb, bar);
+                        if (a.a_whole) tma_load_3d(dst + w_bytes, &maps.a, 0, m0, kb0 + kb, bar);
+                        else tma_load_3d(dst + w_bytes, &maps.a, (kb0 + kb) * QB, m0, 0, bar);
                     }
                     issued = min(issued + 1, a.stages);
                     if (++stage == a.stages) { stage = 0; phase ^= 1u; }
@@ -249,25 +257,38 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
             __syncwarp();
             if (lane == 0) mbar_arrive(&tempty[buf]);
             if (++buf == NBUF) { buf = 0; tphase ^= 1u; }
+            if constexpr (CAN_SPLIT) {
+                if (shared_k) {
+                    if (live) leave_partial<HALF>(reinterpret_cast<float*>(ring), half, quarter * 32 + lane, acc);
+                    cluster_arrive_release();
+                    cluster_wait();
+                    if (!*abort) join_partials<BN, GATED>(a, smem_addr(ring), split, ew, lane, m0, n0, valid);
+                    continue;
+                }
+            }
             if constexpr (GATED) epi_gated<HALF>(a, ctx, acc, m0, n0, valid, dead);
             else if (live && !dead) epi_plain<HALF>(a, ctx, acc, m0, n0, valid);
         }
     }
-    if (GATED && csize > 1 && warp < CTRL_WARPS) cluster_wait();
+    if (warp < CTRL_WARPS) {
+        if (shared_k) cluster_arrive_release();                // the drain warps' barrier before they join
+        if (shared_k || (GATED && csize > 1)) cluster_wait();
+    }
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     if (warp == 1) tc::tmem_dealloc(tmem_slot, 512);
-    if (GATED && csize > 1) {                   // nobody leaves while a peer may still send to it
+    if (shared_k || (GATED && csize > 1)) {     // nobody leaves while a peer may still reach into it
         cluster_arrive_release();
         cluster_wait();
     }
 }
 
 template <int BN, bool GATED>
-cudaError_t launch_mx(const GemmCall& c, Args& a, cudaStream_t s) {
+cudaError_t launch_mx(const GemmCall& c, Args& a, int S, cudaStream_t s) {
     const moe_linear* L = c.lin;
-    const int cluster = GATED ? BUF_COLS / BN : 1;
+    const int cluster = S > 1 ? S : GATED ? BUF_COLS / BN : 1;
+    a.S = S;
     const int mt = (c.M + BM - 1) / BM;
     a.bn = BN;
     a.n_nt = GATED ? (L->d.out_features + QB - 1) / QB : (L->rows + BN - 1) / BN;
@@ -286,6 +307,7 @@ cudaError_t launch_mx(const GemmCall& c, Args& a, cudaStream_t s) {
         return cudaErrorInvalidValue;
     const int stage = (BN + a.a_rows) * 128, fixed = 1024 + (GATED ? TAIL_GATED : TAIL_PLAIN) + SF_SLOTS * slot_bytes<BN>();
     a.stages = std::min(MAX_STAGES, (SMEM_MAX - fixed) / stage);
+    if (S > 1 && a.stages * stage < BM * part_pitch(BN) * 4) return cudaErrorInvalidValue;
     cudaError_t e = ensure_smem_limit<mx_kernel<BN, GATED>>(SMEM_MAX);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -303,7 +325,7 @@ cudaError_t launch_mx(const GemmCall& c, Args& a, cudaStream_t s) {
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.numAttrs = 2;
     }
-    cfg.gridDim = dim3((unsigned)(std::min<long long>(units, L->num_sms / cluster) * cluster));
+    cfg.gridDim = dim3((unsigned)((S > 1 ? units : std::min<long long>(units, L->num_sms / cluster)) * cluster));
     return cudaLaunchKernelEx(&cfg, mx_kernel<BN, GATED>, maps, (const uint8_t*)L->wsf, (L->rows_pad + QB - 1) / QB, a);
 }
 
@@ -317,13 +339,29 @@ cudaError_t launch_fp8_mx(const GemmCall& c, bool gated, cudaStream_t s) {
     a.y = c.y; a.ldy = c.ldy; a.y_f32 = c.y_f32;
     a.y_vec = c.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(c.y) % (c.y_f32 ? 16 : 8) == 0;
     a.hq = c.hq; a.ld_hq = c.ld_hq; a.hs = c.hs; a.ld_hs = c.ld_hs;
-    // Tiles of 256 weight rows reuse the tokens best; 128 where they leave SMs idle: waves of
-    // tiles times a tile's MMA time, 512 or 256 cycles a K block.
-    const long long sms = c.lin->num_sms, mt = (c.M + BM - 1) / BM;
-    const long long rows = gated ? 2LL * ((c.lin->d.out_features + QB - 1) / QB * QB) : c.lin->rows;
-    const long long t256 = (mt * ((rows + 255) / 256) + sms - 1) / sms * 2, t128 = (mt * ((rows + 127) / 128) + sms - 1) / sms;
-    if (t128 < t256) return gated ? mx::launch_mx<128, true>(c, a, s) : mx::launch_mx<128, false>(c, a, s);
-    return gated ? mx::launch_mx<256, true>(c, a, s) : mx::launch_mx<256, false>(c, a, s);
+    // A tile's K block takes its MMAs (512 cycles for 256 rows, half for 128) or, with few tiles, the
+    // copies into its SM at about 110 GB/s.  256 rows reuse the tokens best; 128 rows, or K split over
+    // S CTAs, use SMs that tiles alone would leave idle.  Joining costs about 1.5 us and 1 us per 128 rows.
+    const double mt = (c.M + BM - 1) / BM, sms = c.lin->num_sms;
+    const double rows = gated ? 2.0 * ((c.lin->d.out_features + QB - 1) / QB * QB) : (double)c.lin->rows;
+    const int quads = (a.kt + 3) / 4;
+    int bn = 256, S = 1;
+    double best = 0;
+    for (int b = 128; b <= 256; b += 128) {
+        const double units = mt * std::ceil(rows / b), kb = std::max(b / 256.0 * 0.3, (b + a.a_rows) * 128.0 / 110e3);
+        for (int k = 1; k <= 8 && k <= quads; k *= 2) {
+            if (k > 1 && (units * k > 0.92 * sms || (gated && b == 128))) break;
+            const double kr = k > 1 ? std::min<double>(a.kt, 4.0 * ((quads + k - 1) / k)) : a.kt;
+            const double us = std::ceil(units / sms) * (kr * kb + 1.0) + (k > 1 ? 1.5 + b / 128.0 : 0.0);
+            if (best == 0 || us < best) {
+                best = us;
+                bn = b;
+                S = k;
+            }
+        }
+    }
+    if (bn == 128) return gated ? mx::launch_mx<128, true>(c, a, S, s) : mx::launch_mx<128, false>(c, a, S, s);
+    return gated ? mx::launch_mx<256, true>(c, a, S, s) : mx::launch_mx<256, false>(c, a, S, s);
 }
 
 }  // namespace moe
