@@ -518,7 +518,6 @@ cudaError_t launch_few(const GemmCall& c, const FewPlan& p, int kr, cudaStream_t
     const moe_linear* L = c.lin;
     Args g = base_args(c);                    // what the tensor maps are made from
     g.bn = p.R;
-    g.a_whole = L->d.in_features % QB == 0;
     FewArgs a = {};
     a.sw = L->sw;
     a.M = c.M; a.N = L->d.out_features; a.kt = L->kt; a.nblk = g.nblk;

@@ -17,24 +17,23 @@ static Plan plan_gated(const GemmCall& c, const Args& a) {
     Plan best = {};
     double best_us = 0;
     if (units > 0x3FFFFFFF) return best;
-    // microseconds of a K block: draining its columns, or the copies into one SM
+    // a unit's K block takes the draining of its columns, or its copies
     auto block_us = [&](int grp, int bn) {
-        const double drain = grp == 1 ? 0.55 : grp == 2 ? 0.42 : grp == 4 ? 0.23 : 0.15;
-        return std::max(drain, (bn + a.a_rows) * 128.0 / 110e3);
+        return std::max(grp == 1 ? 0.48 : grp == 2 ? 0.43 : grp == 4 ? 0.23 : 0.15, copy_us(bn, a.a_rows));
     };
+    const double weights = (double)c.lin->rows * a.kt * 128.0;
     for (int cl = 1; cl <= MAX_CLUSTER; cl *= 2) {
-        const int grp = cl, bn = BUF_COLS / cl;
+        const int grp = cl, bn = BUF_COLS / cl, slots = cluster_slots(sms, cl);
         if (2 * stage_cost(grp, bn, a.a_rows, a.e8m0) <= ring_max(true)) {
-            const int slots = (int)(cl > 2 ? 0.92 * sms / cl : sms / cl);
-            const double us = (double)((units + slots - 1) / slots) * (a.kt * block_us(grp, bn) + 1.0) + (cl > 1 ? 0.8 : 0.0);
+            const double us = plan_us((double)((units + slots - 1) / slots), a.kt, block_us(grp, bn), weights, bn, 1, 0) + (cl > 1 ? 0.8 : 0.0);
             if (best.bn == 0 || us < best_us) {
                 best_us = us;
                 best = Plan{grp, bn, cl, (int)units, nt, 1};
             }
         }
-        if (cl > 1 && cl <= a.kt && units * cl <= 0.92 * sms) {
-            const double us = ((a.kt + cl - 1) / cl) * block_us(1, BUF_COLS) + 4.5;
-            if (us < best_us) {
+        if (cl > 1 && cl <= a.kt && units <= slots) {
+            const double us = plan_us(1.0, (a.kt + cl - 1) / cl, block_us(1, BUF_COLS), weights, BUF_COLS, cl, (double)units * cl);
+            if (best.bn == 0 || us < best_us) {
                 best_us = us;
                 best = Plan{1, BUF_COLS, cl, (int)units, nt, cl};
             }

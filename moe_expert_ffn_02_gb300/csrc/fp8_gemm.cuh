@@ -40,6 +40,7 @@
 #include "tcgen05.cuh"
 
 #include <algorithm>
+#include <cmath>
 
 namespace moe {
 namespace dg {
@@ -443,24 +444,33 @@ __device__ __forceinline__ void quantise_row(const A& a, bool e8, int64_t row, i
     }
 }
 
+// Sum of 4 fp32 at `at` over the S CTAs, in rank order; all S loads are in flight at once.
+template <int S>
+__device__ __forceinline__ float4 sum_ranks(uint32_t at) {
+    float4 v[S];
+#pragma unroll
+    for (int p = 0; p < S; ++p) v[p] = ld_cluster4(map_to_rank(at, p));
+#pragma unroll
+    for (int p = 1; p < S; ++p) v[0] = add4(v[0], v[p]);
+    return v[0];
+}
+
 // Drain warp ew of CTA `rank` adds and finishes rows ew S + rank, + 8 S, ...
-template <int BN, bool GATED>
-__device__ __forceinline__ void join_partials(const Args& a, uint32_t part0, int rank, int ew, int lane, int m0, int n0, int valid) {
-    for (int r = ew * a.S + rank; r < valid; r += EPI_WARPS * a.S) {
+template <int BN, bool GATED, int S>
+__device__ __forceinline__ void join_rows(const Args& a, uint32_t part0, int rank, int ew, int lane, int m0, int n0, int valid) {
+#pragma unroll 1
+    for (int r = ew * S + rank; r < valid; r += EPI_WARPS * S) {
         const uint32_t row = part0 + (uint32_t)(r * part_pitch(BN)) * 4u;
         if constexpr (GATED) {
             const uint32_t at = row + (uint32_t)((lane >> 1) * 16 + (lane & 1) * 4) * 4u;      // 8 gate columns, then 8 up
-            float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
-            for (int p = 0; p < a.S; ++p) {
-                const uint32_t from = map_to_rank(at, p);
-                g = add4(g, ld_cluster4(from));
-                u = add4(u, ld_cluster4(from + 32));
-            }
+            const float4 g = sum_ranks<S>(at), u = sum_ranks<S>(at + 32);
             quantise_row(a, a.e8m0, m0 + r, n0 / (2 * QB), lane, g, u);
         } else {
-            for (int c = 4 * lane; c < BN && n0 + c < a.N; c += 128) {
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int p = 0; p < a.S; ++p) v = add4(v, ld_cluster4(map_to_rank(row + 4u * c, p)));
+#pragma unroll
+            for (int c0 = 0; c0 < BN; c0 += 128) {
+                const int c = c0 + 4 * lane;
+                if (n0 + c >= a.N) break;
+                const float4 v = sum_ranks<S>(row + 4u * c);
                 const int64_t at = (int64_t)(m0 + r) * a.ldy + n0 + c;
                 if (a.y_vec && n0 + c + 4 <= a.N) {
                     if (a.y_f32) {
@@ -472,7 +482,9 @@ __device__ __forceinline__ void join_partials(const Args& a, uint32_t part0, int
                     }
                 } else {
                     const float e[4] = {v.x, v.y, v.z, v.w};
-                    for (int i = 0; i < 4 && n0 + c + i < a.N; ++i) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (n0 + c + i >= a.N) break;
                         if (a.y_f32) static_cast<float*>(a.y)[at + i] = e[i];
                         else static_cast<__nv_bfloat16*>(a.y)[at + i] = __float2bfloat16_rn(e[i]);
                     }
@@ -480,6 +492,12 @@ __device__ __forceinline__ void join_partials(const Args& a, uint32_t part0, int
             }
         }
     }
+}
+template <int BN, bool GATED>
+__device__ __forceinline__ void join_partials(const Args& a, uint32_t part0, int rank, int ew, int lane, int m0, int n0, int valid) {
+    if (a.S == 2) join_rows<BN, GATED, 2>(a, part0, rank, ew, lane, m0, n0, valid);
+    else if (a.S == 4) join_rows<BN, GATED, 4>(a, part0, rank, ew, lane, m0, n0, valid);
+    else join_rows<BN, GATED, 8>(a, part0, rank, ew, lane, m0, n0, valid);
 }
 
 // A block's scales as they were loaded: the token's (bits, or the e8m0 byte) and the weights'.
@@ -891,6 +909,20 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------------ launch
+// Clusters of c CTAs (one per SM) that run at once: a cluster stays inside a GPC, and the GPCs' SMs
+// are no multiple of it (152 SMs: 76 clusters of 2, 36 of 4, 15 of 8).
+inline int cluster_slots(int sms, int c) { return c <= 2 ? sms / c : c == 4 ? sms * 95 / 400 : sms * 80 / 800; }
+
+// Microseconds of a call, fitted to sweeps of tile heights and K ranges on this GPU: `waves` tiles of kr K
+// blocks one after the other in a CTA, against the weights' way from HBM (each covers part of the
+// other), and the joining of S ranges.
+inline double plan_us(double waves, double kr, double block_us, double weight_bytes, int bn, int S, double ctas) {
+    const double cta = waves * (kr * block_us + 1.0), hbm = weight_bytes / 6.8e6;
+    return std::sqrt(cta * cta + hbm * hbm) + (S > 1 ? bn / 128.0 * (0.7 + 0.2 * S) + 0.01 * ctas : 0.0);
+}
+// The copies of a K block's operands into one SM run at about 110 GB/s.
+inline double copy_us(int bn, int a_rows) { return (bn + a_rows) * 128.0 / 110e3; }
+
 struct Plan {
     int grp, bn, cluster, units, n_nt, S;
 };
@@ -928,7 +960,6 @@ cudaError_t launch(const GemmCall& c, const Plan& p, Args& a, cudaStream_t s) {
     a.n_nt = p.n_nt;
     a.n_units = p.units;
     a.S = p.S;
-    a.a_whole = c.lin->d.in_features % QB == 0;
     Maps maps;
     if (!encode_maps(c, a, GRP, &maps)) return cudaErrorInvalidValue;
     const int cost = stage_cost(GRP, a.bn, a.a_rows, a.e8m0), fixed = 1024 + (GATED ? TAIL_GATED : TAIL_PLAIN);
@@ -988,6 +1019,7 @@ inline Args base_args(const GemmCall& c) {
     a.nblk = (L->d.out_features + QB - 1) / QB;
     a.a_rows = c.M >= BM ? BM : (c.M + 7) / 8 * 8;
     a.e8m0 = L->d.scale_type == MOE_SCALE_E8M0;
+    a.a_whole = L->d.in_features % QB == 0;
     a.status = L->dev_status;
     a.wait_limit = L->wait_limit;
     return a;

@@ -6,15 +6,9 @@
 namespace moe {
 namespace dg {
 
-// Microseconds of a tile's K block, fitted to sweeps: draining BN columns, or the copies into one SM.
-static double block_us(int grp, int bn, int a_rows) {
-    const double drain = grp == 1 ? 0.55 : grp == 2 ? 0.42 : 0.06 + 0.0027 * bn;
-    return std::max(drain, (bn + a_rows) * 128.0 / 110e3);
-}
-
 // Weight rows per tile, and K ranges: few token tiles take narrow tiles, so that every SM streams a
 // share of the weights, or split K where rows are few and long; many take wide ones, which reuse the
-// tokens.  The shortest estimate over whole waves of tiles wins.
+// tokens.  A tile's K block takes the draining of its columns, or its copies.
 static Plan plan_plain(const GemmCall& c, const Args& a) {
     const int sms = c.lin->num_sms, rows = c.lin->rows;
     const int mt = (c.M + BM - 1) / BM;
@@ -27,11 +21,13 @@ static Plan plan_plain(const GemmCall& c, const Args& a) {
         const int nt = (rows + bn - 1) / bn, groups = (a.kt + grp - 1) / grp;
         const long long units = (long long)mt * nt;
         if (units > 0x3FFFFFFF) continue;
+        // narrow groups of a ragged K bring their token tiles block by block
+        const double drain = grp == 1 ? 0.48 : grp == 2 ? 0.43 : 0.06 + 0.0027 * bn + (a.a_whole ? 0.0 : 0.1);
         for (int S = 1; S <= 8 && S <= groups; S *= 2) {
-            if (S > 1 && ((bn != 128 && bn != 256) || units * S > 0.92 * sms)) break;
-            const double kr = S > 1 ? std::min<double>(a.kt, (double)grp * ((groups + S - 1) / S)) : a.kt;
-            const double us = (double)((units + sms - 1) / sms) * (kr * block_us(grp, bn, a.a_rows) + 1.0) +
-                              (S > 1 ? 1.5 + bn / 128.0 : 0.0);
+            if (S > 1 && ((bn != 128 && bn != 256) || units > cluster_slots(sms, S))) break;
+            const double kr = std::min<double>(a.kt, (double)grp * ((groups + S - 1) / S));
+            const double us = plan_us(S > 1 ? 1.0 : (double)((units + sms - 1) / sms), kr, std::max(drain, copy_us(bn, a.a_rows)),
+                                      (double)rows * a.kt * 128.0, bn, S, (double)units * S);
             if (best.bn == 0 || us < best_us) {
                 best_us = us;
                 best = Plan{grp, bn, S, (int)units, nt, S};

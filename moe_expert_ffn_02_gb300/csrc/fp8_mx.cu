@@ -24,8 +24,6 @@
 // and stores, which the next tile's MMAs cover; BN = 128: two accumulators.
 #include "fp8_gemm.cuh"
 
-#include <cmath>
-
 namespace moe {
 namespace mx {
 
@@ -295,7 +293,6 @@ cudaError_t launch_mx(const GemmCall& c, Args& a, int S, cudaStream_t s) {
     const long long units = (long long)mt * a.n_nt;
     if (units > 0x3FFFFFFF) return cudaErrorInvalidValue;
     a.n_units = (int)units;
-    a.a_whole = L->d.in_features % QB == 0;
     Maps maps;
     if (!encode_maps(c, a, 1, &maps)) return cudaErrorInvalidValue;
     // the tokens' scales: four K blocks of 128 rows
@@ -339,20 +336,19 @@ cudaError_t launch_fp8_mx(const GemmCall& c, bool gated, cudaStream_t s) {
     a.y = c.y; a.ldy = c.ldy; a.y_f32 = c.y_f32;
     a.y_vec = c.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(c.y) % (c.y_f32 ? 16 : 8) == 0;
     a.hq = c.hq; a.ld_hq = c.ld_hq; a.hs = c.hs; a.ld_hs = c.ld_hs;
-    // A tile's K block takes its MMAs (512 cycles for 256 rows, half for 128) or, with few tiles, the
-    // copies into its SM at about 110 GB/s.  256 rows reuse the tokens best; 128 rows, or K split over
-    // S CTAs, use SMs that tiles alone would leave idle.  Joining costs about 1.5 us and 1 us per 128 rows.
-    const double mt = (c.M + BM - 1) / BM, sms = c.lin->num_sms;
+    // A tile's K block takes its MMAs (512 cycles for 256 rows, half for 128) or its copies.  256 rows
+    // reuse the tokens best; 128 rows, or K split over S CTAs, use SMs that tiles alone leave idle.
+    const int sms = c.lin->num_sms, quads = (a.kt + 3) / 4;
+    const double mt = (c.M + BM - 1) / BM;
     const double rows = gated ? 2.0 * ((c.lin->d.out_features + QB - 1) / QB * QB) : (double)c.lin->rows;
-    const int quads = (a.kt + 3) / 4;
     int bn = 256, S = 1;
     double best = 0;
     for (int b = 128; b <= 256; b += 128) {
-        const double units = mt * std::ceil(rows / b), kb = std::max(b / 256.0 * 0.3, (b + a.a_rows) * 128.0 / 110e3);
+        const double units = mt * std::ceil(rows / b), kb = std::max(b / 256.0 * 0.3, copy_us(b, a.a_rows));
         for (int k = 1; k <= 8 && k <= quads; k *= 2) {
-            if (k > 1 && (units * k > 0.92 * sms || (gated && b == 128))) break;
-            const double kr = k > 1 ? std::min<double>(a.kt, 4.0 * ((quads + k - 1) / k)) : a.kt;
-            const double us = std::ceil(units / sms) * (kr * kb + 1.0) + (k > 1 ? 1.5 + b / 128.0 : 0.0);
+            if (k > 1 && (units > cluster_slots(sms, k) || (gated && b == 128))) break;
+            const double kr = std::min<double>(a.kt, 4.0 * ((quads + k - 1) / k));
+            const double us = plan_us(k > 1 ? 1.0 : std::ceil(units / sms), kr, kb, rows * a.kt * 128.0, b, k, units * k);
             if (best == 0 || us < best) {
                 best = us;
                 bn = b;
