@@ -142,7 +142,7 @@ def test_norm_against_64_bits(moe, types, scale, rows, cols):
 
 
 @pytest.mark.parametrize("types", ["bf16/bf16", "bf16/f32", "f32/f32", "bf16/-"])
-@pytest.mark.parametrize("rows,cols", [(1300, 264), (2500, 7168), (1217, 8), (1900, 4104), (1500, 16384), (3000, 1001), (1400, 8192)])
+@pytest.mark.parametrize("rows,cols", [(1300, 264), (2500, 7168), (1217, 8), (1900, 4104), (2500, 7001), (5000, 131), (700, 1000), (1500, 999), (1300, 9001), (1500, 16384), (3000, 1001), (1400, 8192)])
 def test_norm_of_many_rows(moe, types, rows, cols):
     """Enough rows for the ring form, and sizes around its limits."""
     dt = {"bf16": torch.bfloat16, "f32": torch.float32}
