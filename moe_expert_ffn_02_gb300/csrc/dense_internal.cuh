@@ -82,8 +82,12 @@ cudaError_t launch_linear_repack(const moe_linear* L, const uint8_t* w, const vo
                                  const void* su, cudaStream_t st);
 cudaError_t launch_fp8_linear(const GemmCall& c, cudaStream_t s);
 cudaError_t launch_fp8_gated(const GemmCall& c, cudaStream_t s);
-bool mx_fits(const moe_linear* L);                      // whether the hardware-scaled form takes these weights
-cudaError_t launch_fp8_mx(const GemmCall& c, bool gated, cudaStream_t s);
+struct MxPlan {
+    int bn, S;             // rows per tile, K ranges; bn 0: the form does not take these weights
+    double us;             // estimate
+};
+MxPlan plan_fp8_mx(const GemmCall& c, bool gated);      // the form in which the tensor core applies e8m0 scales
+cudaError_t launch_fp8_mx(const GemmCall& c, bool gated, const MxPlan& p, cudaStream_t s);
 bool few_tokens(const GemmCall& c, bool gated);         // whether the few-token form takes the call
 cudaError_t launch_fp8_few(const GemmCall& c, bool gated, cudaStream_t s);
 

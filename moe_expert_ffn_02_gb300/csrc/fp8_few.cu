@@ -56,7 +56,7 @@ struct FewArgs {
     int M, N, kt, nblk;
     int R, S, G;                             // rows per tile, K ranges, K blocks per stage (1, 2 or 4)
     int a_rows, stages, kr, kr4;             // kr: blocks of the longest range; kr4: up to a multiple of 4
-    bool a_whole;
+    int k_full;
     void* y;
     int64_t ldy;
     bool y_f32;
@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
 
     // a stage's bytes and the copy of its weights, by one thread
     auto copy_w = [&](int st, int g) {
-        const int na = a.a_whole ? a.G : min(a.G, a.kt - kb0 - g * a.G);
-        expect_tx(full0 + 8 * st, (uint32_t)(a.G * (w_bytes + (MODE == MX ? 0 : pitch)) + na * a_bytes));
+        expect_tx(full0 + 8 * st, (uint32_t)(a.G * (w_bytes + (MODE == MX ? 0 : pitch)) +
+                                             tokens_bytes(a.k_full, a.kt, kb0 + g * a.G, a.G, a_bytes)));
         tma_load_3d(ring0 + st * stage_bytes, &maps.w, 0, n0, kb0 + g * a.G, full0 + 8 * st);
     };
 
@@ -220,12 +220,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
                 if (el) {
                     const uint32_t dst = ring0 + st * stage_bytes + a.G * w_bytes, bar = full0 + 8 * st;
                     const int kb = kb0 + g * a.G;
-                    if (a.a_whole) {
-                        tma_load_3d(dst, &maps.a, 0, 0, kb, bar);
-                    } else {
-                        const int na = min(a.G, a.kt - kb);
-                        for (int i = 0; i < na; ++i) tma_load_3d(dst + i * a_bytes, &maps.a, (kb + i) * QB, 0, 0, bar);
-                    }
+                    copy_tokens(maps, a.k_full, a.kt, dst, kb, a.G, 0, a_bytes, bar);
                     if (MODE != MX) tma_load_2d(scl0 + st * slot_bytes, &maps.s, 0, kb, bar);
                 }
                 __syncwarp();
@@ -525,7 +520,7 @@ cudaError_t launch_few(const GemmCall& c, const FewPlan& p, int kr, cudaStream_t
     a.a_rows = g.a_rows;
     a.kr = kr;
     a.kr4 = (kr + 3) / 4 * 4;
-    a.a_whole = g.a_whole;
+    a.k_full = g.k_full;
     a.y = c.y; a.ldy = c.ldy; a.y_f32 = c.y_f32;
     a.hq = c.hq; a.ld_hq = c.ld_hq; a.hs = c.hs; a.ld_hs = c.ld_hs;
     a.status = L->dev_status; a.wait_limit = L->wait_limit;
@@ -542,16 +537,8 @@ cudaError_t launch_few(const GemmCall& c, const FewPlan& p, int kr, cudaStream_t
         if (a.stages >= std::min(a.G == 1 ? 2 : 3, (kr + a.G - 1) / a.G)) break;
     }
     if (a.G < 1) return cudaErrorInvalidValue;
-    Maps maps;
-    if (!encode_maps(c, g, a.G, &maps)) return cudaErrorInvalidValue;
-    if (MODE == MX) {                         // the tokens' scales of a whole range in one copy
-        const cuuint64_t sd[2] = {(cuuint64_t)c.M, (cuuint64_t)a.kt}, ss[1] = {(cuuint64_t)c.ld_as};
-        const cuuint32_t sb[2] = {(cuuint32_t)pitch, (cuuint32_t)a.kr4}, one[2] = {1, 1};
-        if (tensor_map_encoder()(&maps.s, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(c.as), sd, ss, sb, one,
-                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return cudaErrorInvalidValue;
-    }
+    Maps maps;                                // MX: the tokens' scales of a whole range in one copy
+    if (!encode_maps(c, g, a.G, MODE == F32 ? a.a_rows : pitch, MODE == MX ? a.kr4 : a.G, &maps)) return cudaErrorInvalidValue;
     cudaError_t e = ensure_smem_limit<few_kernel<TN, GATED, MODE>>(SMEM_HALF);
     if (e != cudaSuccess) return e;
     const int cluster = GATED ? 2 * p.S : p.S;

@@ -24,18 +24,18 @@ static Plan plan_gated(const GemmCall& c, const Args& a) {
     const double weights = (double)c.lin->rows * a.kt * 128.0;
     for (int cl = 1; cl <= MAX_CLUSTER; cl *= 2) {
         const int grp = cl, bn = BUF_COLS / cl, slots = cluster_slots(sms, cl);
-        if (2 * stage_cost(grp, bn, a.a_rows, a.e8m0) <= ring_max(true)) {
+        if (2 * stage_cost(grp, bn, a.a_rows) <= ring_max(true)) {
             const double us = plan_us((double)((units + slots - 1) / slots), a.kt, block_us(grp, bn), weights, bn, 1, 0) + (cl > 1 ? 0.8 : 0.0);
             if (best.bn == 0 || us < best_us) {
                 best_us = us;
-                best = Plan{grp, bn, cl, (int)units, nt, 1};
+                best = Plan{grp, bn, cl, (int)units, nt, 1, us};
             }
         }
         if (cl > 1 && cl <= a.kt && units <= slots) {
             const double us = plan_us(1.0, (a.kt + cl - 1) / cl, block_us(1, BUF_COLS), weights, BUF_COLS, cl, (double)units * cl);
             if (best.bn == 0 || us < best_us) {
                 best_us = us;
-                best = Plan{1, BUF_COLS, cl, (int)units, nt, cl};
+                best = Plan{1, BUF_COLS, cl, (int)units, nt, cl, us};
             }
         }
     }
@@ -47,7 +47,6 @@ static Plan plan_gated(const GemmCall& c, const Args& a) {
 cudaError_t launch_fp8_gated(const GemmCall& c, cudaStream_t s) {
     using namespace dg;
     if (few_tokens(c, true)) return launch_fp8_few(c, true, s);
-    if (mx_fits(c.lin)) return launch_fp8_mx(c, true, s);
     Args a = base_args(c);
     a.hq = c.hq;
     a.ld_hq = c.ld_hq;
@@ -55,6 +54,8 @@ cudaError_t launch_fp8_gated(const GemmCall& c, cudaStream_t s) {
     a.ld_hs = c.ld_hs;
     const Plan p = plan_gated(c, a);
     if (!p.bn) return cudaErrorInvalidValue;
+    const MxPlan mx = plan_fp8_mx(c, true);
+    if (mx.bn && mx.us <= p.us) return launch_fp8_mx(c, true, mx, s);
     switch (p.grp) {
         case 1: return launch<1, true>(c, p, a, s);
         case 2: return launch<2, true>(c, p, a, s);

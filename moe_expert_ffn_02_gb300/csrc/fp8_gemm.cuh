@@ -23,12 +23,10 @@
 // the group, so blocks are added in K order into the same accumulators in every
 // configuration and a row's result does not depend on BN or on the batch size.
 //
-// Warps: 0 copies (TMA for A, bulk copies for the pre-swizzled weight image and
-// the token scales), 1 issues the MMAs, 2 fetches the weight scales with 4-byte
-// asynchronous copies, 3 idles, 4-11 drain.  Everything a block needs arrives on
-// its stage's barrier, so no warp waits for a load of its own.  Token tiles with
-// fewer than 128 rows copy only those rows (rounded up to 8); the MMA reads
-// whatever lies behind them in shared memory into TMEM lanes nobody reads.
+// Warps: 0 copies (TMA), 1 issues the MMAs, 2 and 3 idle, 4-11 drain; the drain
+// warps fetch the scales themselves, two groups ahead.  Token tiles with fewer
+// than 128 rows copy only those rows (rounded up to 8); the MMA reads whatever lies
+// behind them in shared memory into TMEM lanes nobody reads.
 //
 // Copies of weights start before the wait for the preceding kernel, and before
 // the tensor memory is allocated.
@@ -64,14 +62,10 @@ constexpr int SMEM_MAX = 232448 - 2048;       // dynamic limit, minus static bar
 constexpr int TAIL_PLAIN = STG_BYTES;
 constexpr int TAIL_GATED = 16384;
 static_assert(TAIL_PLAIN >= BM * 128 && TAIL_GATED >= BM * 128 && AMAX_BYTES + 2 * BM * 4 <= TAIL_GATED, "tail");
-// Stage bytes: GRP blocks of operands; its scales: GRP token runs and GRP pairs of weight scales.
+// Bytes of one K block's token scales in shared memory (few-token form).
 __host__ __device__ inline int sa_pitch(int a_rows, bool e8m0) { return e8m0 ? (a_rows + 15) / 16 * 16 : a_rows * 4; }
-__host__ __device__ inline int scale_slot(int grp, int a_rows, bool e8m0) {
-    return (grp * (sa_pitch(a_rows, e8m0) + 8) + 127) / 128 * 128;       // a TMA destination
-}
-inline int stage_cost(int grp, int bn, int a_rows, bool e8m0) {
-    return grp * (bn + a_rows) * 128 + scale_slot(grp, a_rows, e8m0);
-}
+// Bytes of a stage: GRP blocks of operands.
+inline int stage_cost(int grp, int bn, int a_rows) { return grp * (bn + a_rows) * 128; }
 inline int ring_max(bool gated) { return SMEM_MAX - 1024 - (gated ? TAIL_GATED : TAIL_PLAIN); }
 // Shared memory of a CTA that leaves room for a second one on the SM.
 constexpr int SMEM_HALF = 113 * 1024 - 2048;
@@ -90,7 +84,7 @@ struct Args {
     int n_units;
     int S;                    // K ranges of a unit, one per CTA of its cluster; 1: none
     bool e8m0;
-    bool a_whole;             // K is a multiple of 128: one copy brings all of a group's token tiles
+    int k_full;               // whole K blocks: K / 128; a ragged last one is copied on its own
     // plain
     void* y;
     int64_t ldy;
@@ -104,9 +98,9 @@ struct Args {
     uint32_t wait_limit;
 };
 
-// The three operands that TMA brings: token codes, weight image, token scales.
+// What TMA brings: token codes (whole K blocks, and a ragged last one), weight image, token scales.
 struct Maps {
-    CUtensorMap a, w, s;
+    CUtensorMap a, a_last, w, s;
 };
 
 __device__ __forceinline__ uint32_t idesc_for(int n) {   // D f32, A = B = E4M3, K-major, M = 128
@@ -134,6 +128,19 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
 }
+// Token tiles of n K blocks from kb, rows m0.., one after the other at dst: one copy, or block by
+// block where the ragged last one is among them.  Bytes that arrive: tokens_bytes.
+__device__ __forceinline__ void copy_tokens(const Maps& m, int k_full, int kt, uint32_t dst, int kb, int n, int m0, int a_bytes, uint32_t bar) {
+    if (k_full == kt || kb + n <= k_full) {
+        tma_load_3d(dst, &m.a, 0, m0, kb, bar);
+        return;
+    }
+    for (int i = 0; i < n && kb + i < kt; ++i) tma_load_3d(dst + i * a_bytes, &m.a_last, (kb + i) * QB, m0, 0, bar);
+}
+__device__ __forceinline__ int tokens_bytes(int k_full, int kt, int kb, int n, int a_bytes) {
+    return (k_full == kt || kb + n <= k_full ? n : min(n, kt - kb)) * a_bytes;
+}
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -253,15 +260,6 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
-__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-// An arrival on `bar` once this thread's earlier cp.async copies have landed (counted in the
-// barrier's expected arrivals).
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
 // Batch b of a thread's accumulator columns: PIECE consecutive ones of the sequence
 // (K block of the group, column of the half).
 template <int HALF, int COLS, int PIECE>
@@ -376,14 +374,20 @@ __device__ __forceinline__ void epi_plain(const Args& a, const EpiCtx& x, const 
                 }
             }
         } else {
+            // rows or columns off the vector grid: two rows of 16 columns a store, eight loads ahead
 #pragma unroll 1
-            for (int t = 0; t < 16; ++t) {
-                const int rr = 2 * t + (lane >> 4), c = lane & 15;
-                const float v = x.stg[rr * STG_STRIDE + c];
-                if (row0 + rr < valid && cb + c < a.N) {
-                    const int64_t at = (int64_t)(m0 + row0 + rr) * a.ldy + cb + c;
-                    if (a.y_f32) static_cast<float*>(a.y)[at] = v;
-                    else static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+            for (int t0 = 0; t0 < 16; t0 += 8) {
+                float v[8];
+#pragma unroll
+                for (int t = 0; t < 8; ++t) v[t] = x.stg[(2 * (t0 + t) + (lane >> 4)) * STG_STRIDE + (lane & 15)];
+                const int c = lane & 15;
+                int64_t at = (int64_t)(m0 + row0 + 2 * t0 + (lane >> 4)) * a.ldy + cb + c;
+#pragma unroll
+                for (int t = 0; t < 8; ++t, at += 2 * a.ldy) {
+                    if (row0 + 2 * (t0 + t) + (lane >> 4) < valid && cb + c < a.N) {
+                        if (a.y_f32) static_cast<float*>(a.y)[at] = v[t];
+                        else static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v[t]);
+                    }
                 }
             }
         }
@@ -511,18 +515,15 @@ template <int GRP, bool GATED>
 __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_constant__ Maps maps, Args a) {
     constexpr int COLS = BUF_COLS / GRP;      // columns reserved per K block
     constexpr int HALF = COLS / 2;            // accumulators per thread
-    constexpr int PIECE = GRP == 1 ? 32 : 64; // columns per batch of tensor-memory loads (two in registers)
-    constexpr int NB = GRP * HALF / PIECE;    // batches per buffer
+    constexpr int PIECE = 32;                 // columns per batch of tensor-memory loads (two batches in registers)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int w_bytes = a.bn * 128, a_bytes = a.a_rows * 128;
     const int stage_bytes = GRP * (w_bytes + a_bytes);
-    const int pitch = sa_pitch(a.a_rows, a.e8m0), slot_bytes = scale_slot(GRP, a.a_rows, a.e8m0);
     uint8_t* tail = ring + a.stages * stage_bytes;
     float* stg_all = reinterpret_cast<float*>(tail);                            // plain
     float* amax_cta = reinterpret_cast<float*>(tail);                           // gated: [half][128]
     float* amax_all = amax_cta + 2 * BM;                                        // gated: [parity][rank][128]
-    uint8_t* scales = tail + (GATED ? TAIL_GATED : TAIL_PLAIN);                 // [stage][slot_bytes]
     __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES], tfull[2], tempty[2], xbar[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
 
     pdl_trigger();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], GRP == 1 ? 1 : 1 + 32); mbar_init(&empty[s], GRP == 1 ? 1 : EPI_WARPS); }
+        for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
         for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], EPI_WARPS); mbar_init(&xbar[b], 1); }
         fence_mbar_init();
         abort_flag = 0;
@@ -564,29 +565,19 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
             if (el) {
                 prefetch_map(&maps.w);
                 prefetch_map(&maps.a);
-                prefetch_map(&maps.s);
             }
-            const uint32_t ring0 = smem_addr(ring), scl0 = smem_addr(scales), full0 = smem_addr(full);
+            const uint32_t ring0 = smem_addr(ring), full0 = smem_addr(full);
             auto copy_w = [&](int stage, int n0, int g) {
-                const int nk = a.a_whole ? GRP : min(GRP, a.kt - (g0 + g) * GRP);
-                const uint32_t bytes = (uint32_t)(GRP * (w_bytes + (GRP == 1 ? 0 : pitch)) + nk * a_bytes);
+                const int kb = (g0 + g) * GRP;
                 if (el) {
-                    expect_tx(full0 + 8 * stage, bytes);
-                    tma_load_3d(ring0 + stage * stage_bytes, &maps.w, 0, n0, (g0 + g) * GRP, full0 + 8 * stage);
+                    expect_tx(full0 + 8 * stage, (uint32_t)(GRP * w_bytes + tokens_bytes(a.k_full, a.kt, kb, GRP, a_bytes)));
+                    tma_load_3d(ring0 + stage * stage_bytes, &maps.w, 0, n0, kb, full0 + 8 * stage);
                 }
             };
             auto copy_a = [&](int stage, int m0, int g) {
-                const uint32_t dst = ring0 + stage * stage_bytes + GRP * w_bytes, bar = full0 + 8 * stage;
-                if (el) {
-                    if (GRP > 1) tma_load_2d(scl0 + stage * slot_bytes, &maps.s, m0, (g0 + g) * GRP, bar);
-                    if (a.a_whole) {
-                        tma_load_3d(dst, &maps.a, 0, m0, (g0 + g) * GRP, bar);
-                    } else {
-                        const int nk = min(GRP, a.kt - (g0 + g) * GRP);
-                        for (int i = 0; i < nk; ++i)
-                            tma_load_3d(dst + i * a_bytes, &maps.a, ((g0 + g) * GRP + i) * QB, m0, 0, bar);
-                    }
-                }
+                if (el)
+                    copy_tokens(maps, a.k_full, a.kt, ring0 + stage * stage_bytes + GRP * w_bytes, (g0 + g) * GRP, GRP, m0, a_bytes,
+                                full0 + 8 * stage);
             };
             int stage = 0;
             uint32_t phase = 0;
@@ -652,37 +643,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
                         dt += (uint32_t)COLS;
                     }
                     if (el) {
-                        tc::mma_commit(&tfull[buf]);            // GRP > 1: the drain warps hand the stage back after this
-                        if (GRP == 1) tc::mma_commit(&empty[stage]);
+                        tc::mma_commit(&tfull[buf]);
+                        tc::mma_commit(&empty[stage]);
                     }
                     __syncwarp();
                     if (++stage == a.stages) { stage = 0; phase ^= 1u; }
                     if (++buf == 2) { buf = 0; tphase ^= 1u; }
                 }
             }
-        } else if (GRP > 1 && warp == 2) {
-            // ------------------------------------------------ weight scales: [block of the group][first, second]
-            // plain: the scale blocks of the tile's first column and the next; gated: gate and up
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            const int i = lane >> 1;
-            for (int u = first; u < a.n_units && ok; u += step) {
-                int m0, n0;
-                unit_rows(u, m0, n0);
-                const int blk = GATED ? min(n0 / (2 * QB), a.nblk - 1) + (lane & 1) * a.nblk
-                                      : min(n0 / QB + (lane & 1), a.nblk - 1);
-                const float* src = a.sw + (size_t)blk * a.kt;
-                for (int g = 0; g < n_grp; ++g) {
-                    if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, a.wait_limit, a.status, abort)) ok = false;
-                    if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-                    if (i < GRP && (g0 + g) * GRP + i < a.kt)
-                        cp_async4(scales + stage * slot_bytes + GRP * pitch + lane * 4, src + (g0 + g) * GRP + i);
-                    cp_async_arrive(&full[stage]);
-                    if (++stage == a.stages) { stage = 0; phase ^= 1u; }
-                }
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
         }
         __syncwarp();
     } else {
@@ -691,14 +659,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
         const int ew = warp - CTRL_WARPS;
         const int quarter = warp & 3, half = ew >> 2;
         const int r = quarter * 32 + lane;                     // token row of the tile = TMEM lane
-        const int rs = min(r, a.a_rows - 1);                   // row whose scale this thread reads
         named_bar_sync(2, (1 + EPI_WARPS) * 32);
         tc::tc_fence_after();
         const uint32_t tmem = tmem_slot + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * HALF);
         pdl_wait();
         if (GATED && csize > 1) cluster_wait();
         EpiCtx ctx = {ew, quarter, half, lane, rank, csize, stg_all + (size_t)ew * 32 * STG_STRIDE, amax_cta, amax_all, xbar, 0, 0u, abort};
-        int buf = 0, stage = 0;
+        int buf = 0;
         uint32_t tphase = 0;
         bool dead = false;
         for (int u = first; u < a.n_units; u += step) {
@@ -716,167 +683,108 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
             float acc[HALF];
 #pragma unroll
             for (int c = 0; c < HALF; ++c) acc[c] = 0.f;
+            // What bounds the kernel is this warp's way round a group, so nothing but tensor memory is
+            // waited for.  The scales come straight from global memory into registers, two groups ahead,
+            // and the MMA warp hands the stage back itself.
             uint32_t pa[PIECE], pb[PIECE];
-            if constexpr (GRP == 1) {
-                // One K block per hand-off: what bounds the kernel is this warp's way round a block, so
-                // nothing but tensor memory is waited for.  The scales come straight from global memory
-                // into registers, two blocks ahead, and the MMA warp hands the stage back itself.
-                const int rl = m0 + min(r, valid - 1);
-                const int blk = GATED ? min(n0 / (2 * QB), a.nblk - 1) : min(col0 / QB, a.nblk - 1);
-                const float* sw0 = a.sw + (size_t)blk * a.kt;
-                const float* sw1 = GATED ? sw0 + (size_t)a.nblk * a.kt : sw0;
-                auto fetch = [&](Fetched& f, int kb) {
-                    kb = min(g0 + kb, a.kt - 1);
+            const int rl = m0 + min(r, valid - 1);
+            // gated: gate and up of the unit's features; plain: the tile's two scale blocks, or with
+            // 256 rows the one that this half lies in
+            const int blk = min(GATED ? n0 / (2 * QB) : (GRP == 1 ? col0 : n0) / QB, a.nblk - 1);
+            const float* sw0 = a.sw + (size_t)blk * a.kt;
+            const float* sw1 = a.sw + (size_t)(GATED ? blk + a.nblk : min(blk + 1, a.nblk - 1)) * a.kt;
+            auto fetch = [&](Fetched (&f)[GRP], int g) {
+#pragma unroll
+                for (int i = 0; i < GRP; ++i) {
+                    const int kb = min((g0 + g) * GRP + i, a.kt - 1);
                     const int64_t at = (int64_t)kb * a.ld_sa + rl;
-                    f.x = a.e8m0 ? (uint32_t)static_cast<const uint8_t*>(a.sa)[at] : static_cast<const uint32_t*>(a.sa)[at];
-                    f.w0 = sw0[kb];
-                    if (GATED) f.w1 = sw1[kb];
-                };
-                auto scales_of = [&](const Fetched& f, float& d0, float& d1) {
-                    const float x = a.e8m0 ? e8m0_to_f32((uint8_t)f.x) : __uint_as_float(f.x);
-                    d0 = x * f.w0;
-                    d1 = GATED ? x * f.w1 : d0;
-                };
-                auto arrived = [&](bool ready) {
-                    if (!__all_sync(0xFFFFFFFFu, ready))
-                        dead = !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[buf], tphase, a.wait_limit, a.status, abort));
-                };
-                auto release = [&]() {
-                    tc::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&tempty[buf]);
-                    if (++buf == 2) { buf = 0; tphase ^= 1u; }
-                };
-                if (!live) {
-                    for (int g = 0; g < n_grp && !dead; ++g) {
-                        arrived(false);
-                        release();
-                    }
-                } else if (!dead) {
-                    float c0, c1;
-                    auto add = [&](int b, const uint32_t (&raw)[PIECE]) {
-#pragma unroll
-                        for (int t = 0; t < PIECE; t += 2)
-                            tc::fma2(acc[b * PIECE + t], acc[b * PIECE + t + 1], raw[t], raw[t + 1], GATED && (t & 8) ? c1 : c0);
-                    };
-                    // block g, whose first batch is on its way into pa; f: the scales of g + 1
-                    auto block = [&](int g, Fetched& f) {
-                        const uint32_t tb = tmem + buf * BUF_COLS;
-                        tc::tmem_wait_ld();
-                        ld_batch<HALF, COLS, PIECE>(tb, 1, pb);
-                        add(0, pa);
-                        tc::tmem_wait_ld();
-                        ld_batch<HALF, COLS, PIECE>(tb, 2, pa);
-                        add(1, pb);
-                        tc::tmem_wait_ld();
-                        ld_batch<HALF, COLS, PIECE>(tb, 3, pb);
-                        // a look at the next block's barrier takes about 100 cycles: the products hide it
-                        const bool ready = mbar_test(&tfull[buf ^ 1], tphase ^ (uint32_t)buf);
-                        add(2, pa);
-                        tc::tmem_wait_ld();
-                        release();
-                        float d0, d1;
-                        if (g + 1 < n_grp) {
-                            arrived(ready);
-                            if (dead) return;
-                            tc::tc_fence_after();
-                            ld_batch<HALF, COLS, PIECE>(tmem + buf * BUF_COLS, 0, pa);
-                            scales_of(f, d0, d1);
-                            fetch(f, g + 3);
-                        }
-                        add(3, pb);
-                        c0 = d0;
-                        c1 = d1;
-                    };
-                    Fetched f0, f1, f2;
-                    fetch(f2, 0);
-                    fetch(f1, 1);
-                    fetch(f0, 2);
-                    arrived(false);
-                    if (!dead) {
-                        tc::tc_fence_after();
-                        ld_batch<HALF, COLS, PIECE>(tmem + buf * BUF_COLS, 0, pa);
-                        scales_of(f2, c0, c1);
-                        for (int g = 0; g < n_grp; g += 2) {
-                            block(g, f1);
-                            if (dead || g + 1 >= n_grp) break;
-                            block(g + 1, f0);
-                            if (dead) break;
-                        }
-                    }
+                    f[i].x = a.e8m0 ? (uint32_t)static_cast<const uint8_t*>(a.sa)[at] : static_cast<const uint32_t*>(a.sa)[at];
+                    f[i].w0 = sw0[kb];
+                    if (GATED || GRP > 1) f[i].w1 = sw1[kb];
                 }
-            } else {
-                float c0[GRP], c1[GRP];                            // combined scales of the group being drained
-                // Waits for the group in (buf, stage) unless it is known to be there, starts its first batch,
-                // takes its scales and hands the stage back.  The scales arrived on the stage's barrier, which
-                // the MMA warp waited for before it issued the MMAs whose commit is waited for here.
-                auto open = [&](float (&d0)[GRP], float (&d1)[GRP], bool ready) {
-                    if (!dead && !__all_sync(0xFFFFFFFFu, ready))
-                        dead = !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[buf], tphase, a.wait_limit, a.status, abort));
-                    if (!dead && live) {                           // warp-uniform: tcgen05.ld is warp-collective
+            };
+            auto scales_of = [&](const Fetched (&f)[GRP], float (&d0)[GRP], float (&d1)[GRP]) {
+#pragma unroll
+                for (int i = 0; i < GRP; ++i) {
+                    const float x = a.e8m0 ? e8m0_to_f32((uint8_t)f[i].x) : __uint_as_float(f[i].x);
+                    d0[i] = x * f[i].w0;
+                    d1[i] = GATED || GRP > 1 ? x * f[i].w1 : 0.f;
+                }
+            };
+            auto arrived = [&](bool ready) {
+                if (!__all_sync(0xFFFFFFFFu, ready))
+                    dead = !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[buf], tphase, a.wait_limit, a.status, abort));
+            };
+            auto release = [&]() {
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tempty[buf]);
+                if (++buf == 2) { buf = 0; tphase ^= 1u; }
+            };
+            if (!live) {
+                for (int g = 0; g < n_grp && !dead; ++g) {
+                    arrived(false);
+                    release();
+                }
+            } else if (!dead) {
+                float c0[GRP], c1[GRP];                        // combined scales of the group being drained
+                auto add = [&](int g, int b, const uint32_t (&raw)[PIECE]) {
+                    constexpr int RUN = HALF < PIECE ? HALF : PIECE;
+#pragma unroll
+                    for (int t0 = 0; t0 < PIECE; t0 += RUN) {
+                        const int i = (b * PIECE + t0) / HALF;                     // block of the group
+                        if (GRP > 1 && (g0 + g) * GRP + i >= kb_end) break;        // the last group may be partial
+#pragma unroll
+                        for (int t = t0; t < t0 + RUN; t += 2) {
+                            const int c = (b * PIECE + t) % HALF;
+                            const float k = (GATED ? (c & 8) != 0 : GRP > 1 && ((hi_mask >> (c / 16)) & 1u) != 0) ? c1[i] : c0[i];
+                            tc::fma2(acc[c], acc[c + 1], raw[t], raw[t + 1], k);
+                        }
+                    }
+                };
+                // group g, whose first batch is on its way into pa; f: the scales of g + 1
+                auto drain = [&](int g, Fetched (&f)[GRP]) {
+                    const uint32_t tb = tmem + buf * BUF_COLS;
+                    tc::tmem_wait_ld();
+                    ld_batch<HALF, COLS, PIECE>(tb, 1, pb);
+                    add(g, 0, pa);
+                    tc::tmem_wait_ld();
+                    ld_batch<HALF, COLS, PIECE>(tb, 2, pa);
+                    add(g, 1, pb);
+                    tc::tmem_wait_ld();
+                    ld_batch<HALF, COLS, PIECE>(tb, 3, pb);
+                    // a look at the next group's barrier takes about 100 cycles: the products hide it
+                    const bool ready = mbar_test(&tfull[buf ^ 1], tphase ^ (uint32_t)buf);
+                    add(g, 2, pa);
+                    tc::tmem_wait_ld();
+                    release();
+                    float d0[GRP], d1[GRP];                    // the next group's; unused after the last
+                    if (g + 1 < n_grp) {
+                        arrived(ready);
+                        if (dead) return;
                         tc::tc_fence_after();
                         ld_batch<HALF, COLS, PIECE>(tmem + buf * BUF_COLS, 0, pa);
-                        const uint8_t* sl = scales + stage * slot_bytes;
-#pragma unroll
-                        for (int i = 0; i < GRP; ++i) {
-                            const float sx = a.e8m0 ? e8m0_to_f32(sl[i * pitch + rs])
-                                                    : reinterpret_cast<const float*>(sl + i * pitch)[rs];
-                            const float2 sw = *reinterpret_cast<const float2*>(sl + GRP * pitch + i * 8);
-                            d0[i] = sx * sw.x;
-                            d1[i] = sx * sw.y;
-                        }
+                        scales_of(f, d0, d1);
+                        fetch(f, g + 3);
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&empty[stage]);
-                    if (++stage == a.stages) stage = 0;
+                    add(g, 3, pb);
+#pragma unroll
+                    for (int i = 0; i < GRP; ++i) { c0[i] = d0[i]; c1[i] = d1[i]; }
                 };
-                open(c0, c1, false);
-                for (int g = 0; g < n_grp; ++g) {
-                    const int nk = min(GRP, kb_end - (g0 + g) * GRP);
-                    // Without a branch between the products of a block: a partial group (the last) is
-                    // told apart per block, outside the column loop.
-                    auto add = [&](int b, uint32_t (&raw)[PIECE]) {
-                        constexpr int RUN = HALF < PIECE ? HALF : PIECE;
-#pragma unroll
-                        for (int t0 = 0; t0 < PIECE; t0 += RUN) {
-                            const int i = (b * PIECE + t0) / HALF;
-                            if (i >= nk) break;
-#pragma unroll
-                            for (int t = t0; t < t0 + RUN; t += 2) {
-                                const int c = (b * PIECE + t) % HALF;
-                                const float k = GATED ? ((c & 8) ? c1[i] : c0[i]) : (((hi_mask >> (c / 16)) & 1u) ? c1[i] : c0[i]);
-                                tc::fma2(acc[c], acc[c + 1], raw[t], raw[t + 1], k);
-                            }
-                        }
-                    };
-                    float e0[GRP], e1[GRP];
-                    bool ready = false;
-                    const bool work = !dead && live;
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        uint32_t(&cur)[PIECE] = (b & 1) ? pb : pa;
-                        uint32_t(&nxt)[PIECE] = (b & 1) ? pa : pb;
-                        if (work) tc::tmem_wait_ld();
-                        if (b < NB - 1) {
-                            if (work) ld_batch<HALF, COLS, PIECE>(tmem + buf * BUF_COLS, b + 1, nxt);
-                        } else {
-                            // the buffer is in registers: hand it back, and start on the next group
-                            // before this one's last products are added
-                            static_assert(NB % 2 == 0, "the next group's first batch goes into pa");
-                            tc::tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&tempty[buf]);
-                            if (++buf == 2) { buf = 0; tphase ^= 1u; }
-                            if (g + 1 < n_grp) open(e0, e1, ready);
-                        }
-                        // the poll of the next group's barrier takes about 150 cycles: this batch's products hide it
-                        if (b == NB - 2 && !dead)
-                            ready = mbar_test(&tfull[buf ^ 1], tphase ^ (uint32_t)buf);
-                        if (work) add(b, cur);
-                    }
-                    if (g + 1 < n_grp) {
-#pragma unroll
-                        for (int i = 0; i < GRP; ++i) { c0[i] = e0[i]; c1[i] = e1[i]; }
+                Fetched f0[GRP], f1[GRP], f2[GRP];
+                fetch(f2, 0);
+                fetch(f1, 1);
+                fetch(f0, 2);
+                arrived(false);
+                if (!dead) {
+                    tc::tc_fence_after();
+                    ld_batch<HALF, COLS, PIECE>(tmem + buf * BUF_COLS, 0, pa);
+                    scales_of(f2, c0, c1);
+                    for (int g = 0; g < n_grp; g += 2) {
+                        drain(g, f1);
+                        if (dead || g + 1 >= n_grp) break;
+                        drain(g + 1, f0);
+                        if (dead) break;
                     }
                 }
             }
@@ -918,40 +826,53 @@ inline int cluster_slots(int sms, int c) { return c <= 2 ? sms / c : c == 4 ? sm
 // other), and the joining of S ranges.
 inline double plan_us(double waves, double kr, double block_us, double weight_bytes, int bn, int S, double ctas) {
     const double cta = waves * (kr * block_us + 1.0), hbm = weight_bytes / 6.8e6;
-    return std::sqrt(cta * cta + hbm * hbm) + (S > 1 ? bn / 128.0 * (0.7 + 0.2 * S) + 0.01 * ctas : 0.0);
+    return std::sqrt(cta * cta + hbm * hbm) + (S > 1 ? bn / 128.0 * (0.4 + 0.2 * S) + 0.01 * ctas : 0.0);
 }
 // The copies of a K block's operands into one SM run at about 110 GB/s.
 inline double copy_us(int bn, int a_rows) { return (bn + a_rows) * 128.0 / 110e3; }
 
 struct Plan {
     int grp, bn, cluster, units, n_nt, S;
+    double us;                // the estimate it was chosen by
 };
 
 // Tensor maps of one call.  Token codes: [K block][row][128 B] (the K blocks of a row lie side by
-// side), 128-byte swizzle; with a ragged last block, [1][row][K], so that the copy fills zeros past
-// K.  Weight image: [K block][row][128 B], swizzled already.  Scales: [K block][row].  Rows and
-// blocks past the end are filled with zeros.
-inline bool encode_maps(const GemmCall& c, const Args& a, int grp, Maps* m) {
+// side), 128-byte swizzle; a ragged last block through [1][row][K], so that the copy fills zeros past
+// K.  Weight image: [K block][row][128 B], swizzled already.  Rows and blocks past the end are filled
+// with zeros.  scale_rows, scale_blocks: the box of the token scales' map ([K block][row]), 0 for none.
+inline bool encode_maps(const GemmCall& c, const Args& a, int grp, int scale_rows, int scale_blocks, Maps* m) {
     EncodeTiledFn enc = tensor_map_encoder();
     if (!enc) return false;
-    const cuuint64_t K = c.lin->d.in_features, kt = a.kt, M = c.M;
-    const cuuint32_t one[3] = {1, 1, 1};
-    const cuuint64_t ad[3] = {a.a_whole ? (cuuint64_t)QB : K, M, a.a_whole ? kt : 1};
-    const cuuint64_t as[2] = {(cuuint64_t)c.ld_aq, (cuuint64_t)QB};
-    const cuuint32_t ab[3] = {(cuuint32_t)QB, (cuuint32_t)a.a_rows, a.a_whole ? (cuuint32_t)grp : 1u};
-    const cuuint64_t wd[3] = {(cuuint64_t)QB, (cuuint64_t)a.rows_pad, kt}, ws[2] = {(cuuint64_t)QB, (cuuint64_t)a.rows_pad * QB};
-    const cuuint32_t wb[3] = {(cuuint32_t)QB, (cuuint32_t)a.bn, (cuuint32_t)grp};
-    const int es = a.e8m0 ? 1 : 4;
-    const cuuint64_t sd[2] = {M, kt}, ss[1] = {(cuuint64_t)(a.ld_sa * es)};
-    const cuuint32_t sb[2] = {(cuuint32_t)(sa_pitch(a.a_rows, a.e8m0) / es), (cuuint32_t)grp};
+    const cuuint64_t K = c.lin->d.in_features, kt = a.kt, M = c.M, Q = QB;
+    const cuuint32_t one[3] = {1, 1, 1}, q = QB;
+    const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const auto none = CU_TENSOR_MAP_INTERLEAVE_NONE;
+    const auto wide = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
     const auto fill = CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE;
-    return enc(&m->a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(c.aq), ad, as, ab, one, none,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, fill) == CUDA_SUCCESS &&
-           enc(&m->w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.lin->w, wd, ws, wb, one, none, CU_TENSOR_MAP_SWIZZLE_NONE,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, fill) == CUDA_SUCCESS &&
-           enc(&m->s, a.e8m0 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(c.as), sd,
-               ss, sb, one, none, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, fill) == CUDA_SUCCESS;
+    uint8_t* codes = const_cast<uint8_t*>(c.aq);
+    const cuuint64_t as[2] = {(cuuint64_t)c.ld_aq, Q};
+    bool ok = true;
+    if (a.k_full > 0) {
+        const cuuint64_t ad[3] = {Q, M, (cuuint64_t)a.k_full};
+        const cuuint32_t ab[3] = {q, (cuuint32_t)a.a_rows, (cuuint32_t)grp};
+        ok = enc(&m->a, u8, 3, codes, ad, as, ab, one, none, CU_TENSOR_MAP_SWIZZLE_128B, wide, fill) == CUDA_SUCCESS;
+    }
+    if (ok && a.k_full < a.kt) {
+        const cuuint64_t ad[3] = {K, M, 1};
+        const cuuint32_t ab[3] = {q, (cuuint32_t)a.a_rows, 1};
+        ok = enc(&m->a_last, u8, 3, codes, ad, as, ab, one, none, CU_TENSOR_MAP_SWIZZLE_128B, wide, fill) == CUDA_SUCCESS;
+        if (a.k_full == 0) m->a = m->a_last;      // a valid descriptor to prefetch
+    }
+    const cuuint64_t wd[3] = {Q, (cuuint64_t)a.rows_pad, kt}, ws[2] = {Q, (cuuint64_t)a.rows_pad * Q};
+    const cuuint32_t wb[3] = {q, (cuuint32_t)a.bn, (cuuint32_t)grp};
+    ok = ok && enc(&m->w, u8, 3, c.lin->w, wd, ws, wb, one, none, CU_TENSOR_MAP_SWIZZLE_NONE, wide, fill) == CUDA_SUCCESS;
+    if (scale_rows > 0) {
+        const cuuint64_t sd[2] = {M, kt}, ss[1] = {(cuuint64_t)(a.ld_sa * (a.e8m0 ? 1 : 4))};
+        const cuuint32_t sb[2] = {(cuuint32_t)scale_rows, (cuuint32_t)scale_blocks};
+        ok = ok && enc(&m->s, a.e8m0 ? u8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(c.as), sd, ss, sb, one, none,
+                       CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, fill) == CUDA_SUCCESS;
+    }
+    return ok;
 }
 
 template <int GRP, bool GATED>
@@ -961,8 +882,8 @@ cudaError_t launch(const GemmCall& c, const Plan& p, Args& a, cudaStream_t s) {
     a.n_units = p.units;
     a.S = p.S;
     Maps maps;
-    if (!encode_maps(c, a, GRP, &maps)) return cudaErrorInvalidValue;
-    const int cost = stage_cost(GRP, a.bn, a.a_rows, a.e8m0), fixed = 1024 + (GATED ? TAIL_GATED : TAIL_PLAIN);
+    if (!encode_maps(c, a, GRP, 0, 0, &maps)) return cudaErrorInvalidValue;
+    const int cost = stage_cost(GRP, a.bn, a.a_rows), fixed = 1024 + (GATED ? TAIL_GATED : TAIL_PLAIN);
     const int groups = (a.kt + GRP - 1) / GRP;
     a.stages = std::max(1, std::min(MAX_STAGES, (SMEM_MAX - fixed) / cost));
     if (p.S == 1) a.stages = std::min(a.stages, std::max(2, groups));      // S > 1 also keeps its sums there
@@ -1019,7 +940,7 @@ inline Args base_args(const GemmCall& c) {
     a.nblk = (L->d.out_features + QB - 1) / QB;
     a.a_rows = c.M >= BM ? BM : (c.M + 7) / 8 * 8;
     a.e8m0 = L->d.scale_type == MOE_SCALE_E8M0;
-    a.a_whole = L->d.in_features % QB == 0;
+    a.k_full = L->d.in_features / QB;
     a.status = L->dev_status;
     a.wait_limit = L->wait_limit;
     return a;

@@ -17,12 +17,11 @@ static Plan plan_plain(const GemmCall& c, const Args& a) {
     for (int bn = 16; bn <= BUF_COLS; bn += 16) {
         const int grp = bn <= 32 ? 8 : bn <= 64 ? 4 : bn <= 128 ? 2 : 1;
         if (grp == 1 && bn != 256) continue;                   // 256: both halves in whole scale blocks
-        if (2 * stage_cost(grp, bn, a.a_rows, a.e8m0) > ring_max(false)) continue;
+        if (2 * stage_cost(grp, bn, a.a_rows) > ring_max(false)) continue;
         const int nt = (rows + bn - 1) / bn, groups = (a.kt + grp - 1) / grp;
         const long long units = (long long)mt * nt;
         if (units > 0x3FFFFFFF) continue;
-        // narrow groups of a ragged K bring their token tiles block by block
-        const double drain = grp == 1 ? 0.48 : grp == 2 ? 0.43 : 0.06 + 0.0027 * bn + (a.a_whole ? 0.0 : 0.1);
+        const double drain = grp == 1 ? 0.48 : grp == 2 ? 0.43 : 0.08 + 0.0025 * bn;
         for (int S = 1; S <= 8 && S <= groups; S *= 2) {
             if (S > 1 && ((bn != 128 && bn != 256) || units > cluster_slots(sms, S))) break;
             const double kr = std::min<double>(a.kt, (double)grp * ((groups + S - 1) / S));
@@ -30,7 +29,7 @@ static Plan plan_plain(const GemmCall& c, const Args& a) {
                                       (double)rows * a.kt * 128.0, bn, S, (double)units * S);
             if (best.bn == 0 || us < best_us) {
                 best_us = us;
-                best = Plan{grp, bn, S, (int)units, nt, S};
+                best = Plan{grp, bn, S, (int)units, nt, S, us};
             }
         }
     }
@@ -42,7 +41,6 @@ static Plan plan_plain(const GemmCall& c, const Args& a) {
 cudaError_t launch_fp8_linear(const GemmCall& c, cudaStream_t s) {
     using namespace dg;
     if (few_tokens(c, false)) return launch_fp8_few(c, false, s);
-    if (mx_fits(c.lin)) return launch_fp8_mx(c, false, s);
     Args a = base_args(c);
     a.y = c.y;
     a.ldy = c.ldy;
@@ -51,6 +49,8 @@ cudaError_t launch_fp8_linear(const GemmCall& c, cudaStream_t s) {
     a.y_vec = c.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(c.y) % (c.y_f32 ? 16 : 8) == 0;
     const Plan p = plan_plain(c, a);
     if (!p.bn) return cudaErrorInvalidValue;
+    const MxPlan mx = plan_fp8_mx(c, false);
+    if (mx.bn && mx.us <= p.us) return launch_fp8_mx(c, false, mx, s);
     switch (p.grp) {
         case 1: return launch<1, false>(c, p, a, s);
         case 2: return launch<2, false>(c, p, a, s);

@@ -129,8 +129,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
                         const uint32_t dst = ring0 + stage * stage_bytes, bar = full0 + 8 * stage;
                         expect_tx(bar, (uint32_t)stage_bytes);
                         tma_load_3d(dst, &maps.w, 0, n0, kb0 + kb, bar);
-                        if (a.a_whole) tma_load_3d(dst + w_bytes, &maps.a, 0, m0, kb0 + kb, bar);
-                        else tma_load_3d(dst + w_bytes, &maps.a, (kb0 + kb) * QB, m0, 0, bar);
+                        copy_tokens(maps, a.k_full, a.kt, dst + w_bytes, kb0 + kb, 1, m0, a_bytes, bar);
                     }
                     issued = min(issued + 1, a.stages);
                     if (++stage == a.stages) { stage = 0; phase ^= 1u; }
@@ -294,14 +293,7 @@ cudaError_t launch_mx(const GemmCall& c, Args& a, int S, cudaStream_t s) {
     if (units > 0x3FFFFFFF) return cudaErrorInvalidValue;
     a.n_units = (int)units;
     Maps maps;
-    if (!encode_maps(c, a, 1, &maps)) return cudaErrorInvalidValue;
-    // the tokens' scales: four K blocks of 128 rows
-    const cuuint64_t sd[2] = {(cuuint64_t)c.M, (cuuint64_t)a.kt}, ss[1] = {(cuuint64_t)a.ld_sa};
-    const cuuint32_t sb[2] = {BM, 4}, one[2] = {1, 1};
-    if (tensor_map_encoder()(&maps.s, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(c.as), sd, ss, sb, one,
-                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
+    if (!encode_maps(c, a, 1, BM, 4, &maps)) return cudaErrorInvalidValue;       // scales: a quad of 128 rows
     const int stage = (BN + a.a_rows) * 128, fixed = 1024 + (GATED ? TAIL_GATED : TAIL_PLAIN) + SF_SLOTS * slot_bytes<BN>();
     a.stages = std::min(MAX_STAGES, (SMEM_MAX - fixed) / stage);
     if (S > 1 && a.stages * stage < BM * part_pitch(BN) * 4) return cudaErrorInvalidValue;
@@ -328,36 +320,37 @@ cudaError_t launch_mx(const GemmCall& c, Args& a, int S, cudaStream_t s) {
 
 }  // namespace mx
 
-bool mx_fits(const moe_linear* L) { return L->wsf && L->kt <= mx::MAX_KT; }
-
-cudaError_t launch_fp8_mx(const GemmCall& c, bool gated, cudaStream_t s) {
+MxPlan plan_fp8_mx(const GemmCall& c, bool gated) {
     using namespace dg;
-    Args a = base_args(c);
-    a.y = c.y; a.ldy = c.ldy; a.y_f32 = c.y_f32;
-    a.y_vec = c.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(c.y) % (c.y_f32 ? 16 : 8) == 0;
-    a.hq = c.hq; a.ld_hq = c.ld_hq; a.hs = c.hs; a.ld_hs = c.ld_hs;
+    MxPlan best = {};
+    const Args a = base_args(c);
+    if (!c.lin->wsf || a.kt > mx::MAX_KT) return best;
     // A tile's K block takes its MMAs (512 cycles for 256 rows, half for 128) or its copies.  256 rows
     // reuse the tokens best; 128 rows, or K split over S CTAs, use SMs that tiles alone leave idle.
     const int sms = c.lin->num_sms, quads = (a.kt + 3) / 4;
     const double mt = (c.M + BM - 1) / BM;
     const double rows = gated ? 2.0 * ((c.lin->d.out_features + QB - 1) / QB * QB) : (double)c.lin->rows;
-    int bn = 256, S = 1;
-    double best = 0;
     for (int b = 128; b <= 256; b += 128) {
         const double units = mt * std::ceil(rows / b), kb = std::max(b / 256.0 * 0.3, copy_us(b, a.a_rows));
         for (int k = 1; k <= 8 && k <= quads; k *= 2) {
             if (k > 1 && (units > cluster_slots(sms, k) || (gated && b == 128))) break;
             const double kr = std::min<double>(a.kt, 4.0 * ((quads + k - 1) / k));
-            const double us = plan_us(k > 1 ? 1.0 : std::ceil(units / sms), kr, kb, rows * a.kt * 128.0, b, k, units * k);
-            if (best == 0 || us < best) {
-                best = us;
-                bn = b;
-                S = k;
-            }
+            const double us = plan_us(k > 1 ? 1.0 : std::ceil(units / sms), kr, kb, rows * a.kt * 128.0, b, k, units * k) +
+                              (gated && b == 128 ? 0.8 : 0.0);
+            if (best.bn == 0 || us < best.us) best = MxPlan{b, k, us};
         }
     }
-    if (bn == 128) return gated ? mx::launch_mx<128, true>(c, a, S, s) : mx::launch_mx<128, false>(c, a, S, s);
-    return gated ? mx::launch_mx<256, true>(c, a, S, s) : mx::launch_mx<256, false>(c, a, S, s);
+    return best;
+}
+
+cudaError_t launch_fp8_mx(const GemmCall& c, bool gated, const MxPlan& p, cudaStream_t s) {
+    using namespace dg;
+    Args a = base_args(c);
+    a.y = c.y; a.ldy = c.ldy; a.y_f32 = c.y_f32;
+    a.y_vec = c.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(c.y) % (c.y_f32 ? 16 : 8) == 0;
+    a.hq = c.hq; a.ld_hq = c.ld_hq; a.hs = c.hs; a.ld_hs = c.ld_hs;
+    if (p.bn == 128) return gated ? mx::launch_mx<128, true>(c, a, p.S, s) : mx::launch_mx<128, false>(c, a, p.S, s);
+    return gated ? mx::launch_mx<256, true>(c, a, p.S, s) : mx::launch_mx<256, false>(c, a, p.S, s);
 }
 
 }  // namespace moe
