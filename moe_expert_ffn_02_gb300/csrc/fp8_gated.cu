@@ -48,10 +48,6 @@ cudaError_t launch_fp8_gated(const GemmCall& c, cudaStream_t s) {
     using namespace dg;
     if (few_tokens(c, true)) return launch_fp8_few(c, true, s);
     Args a = base_args(c);
-    a.hq = c.hq;
-    a.ld_hq = c.ld_hq;
-    a.hs = c.hs;
-    a.ld_hs = c.ld_hs;
     const Plan p = plan_gated(c, a);
     if (!p.bn) return cudaErrorInvalidValue;
     const MxPlan mx = plan_fp8_mx(c, true);

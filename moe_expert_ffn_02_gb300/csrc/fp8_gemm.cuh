@@ -88,7 +88,7 @@ struct Args {
     // plain
     void* y;
     int64_t ldy;
-    bool y_f32, y_vec;
+    bool y_f32, y_vec, y_wide; // y_vec: four columns a store; y_wide: eight, bf16
     // gated
     uint8_t* hq;
     int64_t ld_hq;
@@ -348,6 +348,36 @@ __device__ __forceinline__ void epi_gated(const Args& a, EpiCtx& x, const float 
 template <int HALF>
 __device__ __forceinline__ void epi_plain(const Args& a, const EpiCtx& x, const float (&acc)[HALF], int m0, int n0, int valid) {
     const int row0 = x.quarter * 32, lane = x.lane;
+    const int first = n0 + x.half * HALF;
+    if (a.y_wide && HALF >= 32 && first + HALF <= a.N && x.half * HALF + HALF <= a.bn) {
+        // bf16, 32 columns at a time: a store covers 64 bytes of 8 rows, with half the instructions of the
+        // 16-column form below (8192 x 2048 x 7168: 134 -> 118 us; e8m0 4096 x 7168 x 7168: 133.5 -> 132)
+        uint8_t* st = reinterpret_cast<uint8_t*>(x.stg);
+        constexpr int PITCH = STG_STRIDE * 4;
+#pragma unroll
+        for (int c0 = 0; c0 < HALF; c0 += 32) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    __nv_bfloat162 v = __floats2bfloat162_rn(acc[(c0 + i + 2 * k) % HALF], acc[(c0 + i + 2 * k + 1) % HALF]);
+                    w[k] = *reinterpret_cast<uint32_t*>(&v);
+                }
+                *reinterpret_cast<uint4*>(st + lane * PITCH + 2 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int rr = 8 * t + (lane >> 2);
+                const uint4 v = *reinterpret_cast<const uint4*>(st + rr * PITCH + 16 * (lane & 3));
+                if (row0 + rr < valid)
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + (int64_t)(m0 + row0 + rr) * a.ldy + first + c0 + 8 * (lane & 3)) = v;
+            }
+            __syncwarp();
+        }
+        return;
+    }
 #pragma unroll
     for (int p = 0; p < HALF / 16; ++p) {
         const int cb = n0 + x.half * HALF + 16 * p;
@@ -928,6 +958,11 @@ cudaError_t launch(const GemmCall& c, const Plan& p, Args& a, cudaStream_t s) {
 
 inline Args base_args(const GemmCall& c) {
     Args a = {};
+    a.y = c.y; a.ldy = c.ldy; a.y_f32 = c.y_f32;
+    // four columns per store are 16 bytes of fp32 or 8 of bf16; eight of bf16 are 16
+    a.y_vec = c.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(c.y) % (c.y_f32 ? 16 : 8) == 0;
+    a.y_wide = !c.y_f32 && c.ldy % 8 == 0 && reinterpret_cast<uintptr_t>(c.y) % 16 == 0;
+    a.hq = c.hq; a.ld_hq = c.ld_hq; a.hs = c.hs; a.ld_hs = c.ld_hs;
     const moe_linear* L = c.lin;
     a.w = L->w;
     a.sw = L->sw;

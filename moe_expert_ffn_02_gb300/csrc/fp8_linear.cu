@@ -42,11 +42,6 @@ cudaError_t launch_fp8_linear(const GemmCall& c, cudaStream_t s) {
     using namespace dg;
     if (few_tokens(c, false)) return launch_fp8_few(c, false, s);
     Args a = base_args(c);
-    a.y = c.y;
-    a.ldy = c.ldy;
-    a.y_f32 = c.y_f32;
-    // four columns per store: 16 bytes of fp32, 8 of bf16
-    a.y_vec = c.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(c.y) % (c.y_f32 ? 16 : 8) == 0;
     const Plan p = plan_plain(c, a);
     if (!p.bn) return cudaErrorInvalidValue;
     const MxPlan mx = plan_fp8_mx(c, false);

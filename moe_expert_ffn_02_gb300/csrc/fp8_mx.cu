@@ -346,9 +346,6 @@ MxPlan plan_fp8_mx(const GemmCall& c, bool gated) {
 cudaError_t launch_fp8_mx(const GemmCall& c, bool gated, const MxPlan& p, cudaStream_t s) {
     using namespace dg;
     Args a = base_args(c);
-    a.y = c.y; a.ldy = c.ldy; a.y_f32 = c.y_f32;
-    a.y_vec = c.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(c.y) % (c.y_f32 ? 16 : 8) == 0;
-    a.hq = c.hq; a.ld_hq = c.ld_hq; a.hs = c.hs; a.ld_hs = c.ld_hs;
     if (p.bn == 128) return gated ? mx::launch_mx<128, true>(c, a, p.S, s) : mx::launch_mx<128, false>(c, a, p.S, s);
     return gated ? mx::launch_mx<256, true>(c, a, p.S, s) : mx::launch_mx<256, false>(c, a, p.S, s);
 }
