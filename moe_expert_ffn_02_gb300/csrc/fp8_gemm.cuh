@@ -297,12 +297,16 @@ __device__ __forceinline__ void epi_gated(const Args& a, EpiCtx& x, const float 
     const int f0 = (n0 + x.half * HALF) / 2;                   // first feature of this thread
     float h[HALF / 2];
     float am = 0.f;
+    // no test per feature: a branch round each SiLU serialises their chains (106 cycles a feature instead of 32)
 #pragma unroll
-    for (int e = 0; e < HALF / 2; ++e) {
-        const float gt = acc[(e / 8) * 16 + (e % 8)], up = acc[(e / 8) * 16 + 8 + (e % 8)];
-        h[e] = f0 + e < a.N ? silu_mul(gt, up) : 0.f;
-        am = max_nan(am, fabsf(h[e]));
+    for (int e = 0; e < HALF / 2; ++e) h[e] = silu_mul(acc[(e / 8) * 16 + (e % 8)], acc[(e / 8) * 16 + 8 + (e % 8)]);
+    if (f0 + HALF / 2 > a.N) {                                 // warp-uniform
+#pragma unroll
+        for (int e = 0; e < HALF / 2; ++e)
+            if (f0 + e >= a.N) h[e] = 0.f;
     }
+#pragma unroll
+    for (int e = 0; e < HALF / 2; ++e) am = max_nan(am, fabsf(h[e]));
     x.amax_cta[x.half * BM + r] = am;
     named_bar_sync(1, EPI_WARPS * 32);
     am = max_nan(x.amax_cta[r], x.amax_cta[BM + r]);
@@ -324,14 +328,19 @@ __device__ __forceinline__ void epi_gated(const Args& a, EpiCtx& x, const float 
     const float is = inv_scale(group_scale(am, a.e8m0, held));
     if (r < valid && !dead) {
         uint8_t* dst = a.hq + (int64_t)(m0 + r) * a.ld_hq + f0;
+        uint32_t w[HALF / 8];
 #pragma unroll
-        for (int e = 0; e < HALF / 2; e += 8) {
-            const uint32_t lo = pack4_e4m3(h[e] * is, h[e + 1] * is, h[e + 2] * is, h[e + 3] * is);
-            const uint32_t hi = pack4_e4m3(h[e + 4] * is, h[e + 5] * is, h[e + 6] * is, h[e + 7] * is);
-            if (f0 + e + 8 <= a.N) {
-                *reinterpret_cast<uint2*>(dst + e) = make_uint2(lo, hi);
+        for (int e = 0; e < HALF / 2; e += 4) w[e / 4] = pack4_e4m3(h[e] * is, h[e + 1] * is, h[e + 2] * is, h[e + 3] * is);
+        constexpr int V = HALF >= 32 ? 4 : 2;                  // words a store: rows start on 16 bytes
+#pragma unroll
+        for (int i = 0; i < HALF / 8; i += V) {
+            if (f0 + 4 * (i + V) <= a.N) {
+                if constexpr (V == 4) *reinterpret_cast<uint4*>(dst + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+                else *reinterpret_cast<uint2*>(dst + 4 * i) = make_uint2(w[i], w[i + 1]);
             } else {
-                for (int b = 0; f0 + e + b < a.N; ++b) dst[e + b] = (uint8_t)((b < 4 ? lo : hi) >> (8 * (b & 3)));
+#pragma unroll
+                for (int b = 0; b < 4 * V; ++b)
+                    if (f0 + 4 * i + b < a.N) dst[4 * i + b] = (uint8_t)(w[i + b / 4] >> (8 * (b & 3)));
             }
         }
         if (x.half == 0 && x.rank == 0) {
@@ -698,6 +707,37 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
         int buf = 0;
         uint32_t tphase = 0;
         bool dead = false;
+        // What bounds the kernel is this warp's way round a group, so nothing but tensor memory is
+        // waited for.  The scales come straight from global memory into registers, two groups ahead (a
+        // unit's first ones before the last unit's results are written), and the MMA warp hands the
+        // stage back itself.
+        const float *sw0, *sw1;
+        int rl;
+        auto fetch = [&](Fetched (&f)[GRP], int g) {
+#pragma unroll
+            for (int i = 0; i < GRP; ++i) {
+                const int kb = min((g0 + g) * GRP + i, a.kt - 1);
+                const int64_t at = (int64_t)kb * a.ld_sa + rl;
+                f[i].x = a.e8m0 ? (uint32_t)static_cast<const uint8_t*>(a.sa)[at] : static_cast<const uint32_t*>(a.sa)[at];
+                f[i].w0 = sw0[kb];
+                if (GATED || GRP > 1) f[i].w1 = sw1[kb];
+            }
+        };
+        Fetched f0[GRP], f1[GRP], f2[GRP];                     // of groups 2, 1 and 0 at a unit's start
+        auto fetch_unit = [&](int u) {
+            int m0, n0;
+            unit_rows(u, m0, n0);
+            rl = min(m0 + r, a.M - 1);
+            // gated: gate and up of the unit's features; plain: the tile's two scale blocks, or with
+            // 256 rows the one that this half lies in
+            const int blk = min(GATED ? n0 / (2 * QB) : (GRP == 1 ? n0 + half * HALF : n0) / QB, a.nblk - 1);
+            sw0 = a.sw + (size_t)blk * a.kt;
+            sw1 = a.sw + (size_t)(GATED ? blk + a.nblk : min(blk + 1, a.nblk - 1)) * a.kt;
+            fetch(f2, 0);
+            fetch(f1, 1);
+            fetch(f0, 2);
+        };
+        if (first < a.n_units) fetch_unit(first);
         for (int u = first; u < a.n_units; u += step) {
             int m0, n0;
             unit_rows(u, m0, n0);
@@ -713,26 +753,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
             float acc[HALF];
 #pragma unroll
             for (int c = 0; c < HALF; ++c) acc[c] = 0.f;
-            // What bounds the kernel is this warp's way round a group, so nothing but tensor memory is
-            // waited for.  The scales come straight from global memory into registers, two groups ahead,
-            // and the MMA warp hands the stage back itself.
             uint32_t pa[PIECE], pb[PIECE];
-            const int rl = m0 + min(r, valid - 1);
-            // gated: gate and up of the unit's features; plain: the tile's two scale blocks, or with
-            // 256 rows the one that this half lies in
-            const int blk = min(GATED ? n0 / (2 * QB) : (GRP == 1 ? col0 : n0) / QB, a.nblk - 1);
-            const float* sw0 = a.sw + (size_t)blk * a.kt;
-            const float* sw1 = a.sw + (size_t)(GATED ? blk + a.nblk : min(blk + 1, a.nblk - 1)) * a.kt;
-            auto fetch = [&](Fetched (&f)[GRP], int g) {
-#pragma unroll
-                for (int i = 0; i < GRP; ++i) {
-                    const int kb = min((g0 + g) * GRP + i, a.kt - 1);
-                    const int64_t at = (int64_t)kb * a.ld_sa + rl;
-                    f[i].x = a.e8m0 ? (uint32_t)static_cast<const uint8_t*>(a.sa)[at] : static_cast<const uint32_t*>(a.sa)[at];
-                    f[i].w0 = sw0[kb];
-                    if (GATED || GRP > 1) f[i].w1 = sw1[kb];
-                }
-            };
             auto scales_of = [&](const Fetched (&f)[GRP], float (&d0)[GRP], float (&d1)[GRP]) {
 #pragma unroll
                 for (int i = 0; i < GRP; ++i) {
@@ -801,10 +822,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
 #pragma unroll
                     for (int i = 0; i < GRP; ++i) { c0[i] = d0[i]; c1[i] = d1[i]; }
                 };
-                Fetched f0[GRP], f1[GRP], f2[GRP];
-                fetch(f2, 0);
-                fetch(f1, 1);
-                fetch(f0, 2);
                 arrived(false);
                 if (!dead) {
                     tc::tc_fence_after();
@@ -828,6 +845,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
                     continue;
                 }
             }
+            if (u + step < a.n_units) fetch_unit(u + step);
             if constexpr (GATED) epi_gated<HALF>(a, ctx, acc, m0, n0, valid, dead);
             else if (live && !dead) epi_plain<HALF>(a, ctx, acc, m0, n0, valid);
         }
