@@ -57,11 +57,15 @@ constexpr int STG_BYTES = EPI_WARPS * 32 * STG_STRIDE * 4;
 constexpr int MAX_CLUSTER = 8;
 constexpr int AMAX_BYTES = 2 * MAX_CLUSTER * BM * 4;   // [unit parity][CTA rank][row]
 constexpr int SMEM_MAX = 232448 - 2048;       // dynamic limit, minus static barriers
-// What lies behind the ring: the plain epilogue's staging tiles, or the gated one's amax
-// exchange; at least the 16 KB that the last block's 128-row operand read may run into.
-constexpr int TAIL_PLAIN = STG_BYTES;
-constexpr int TAIL_GATED = 16384;
-static_assert(TAIL_PLAIN >= BM * 128 && TAIL_GATED >= BM * 128 && AMAX_BYTES + 2 * BM * 4 <= TAIL_GATED, "tail");
+// What lies behind the ring: the plain epilogue's staging tiles (4 KB a warp where the copy engine
+// writes the rows), or the gated one's amax of each half and, behind it, its amax exchange or its
+// staging tiles (2 KB a warp); at least the 16 KB that the last block's 128-row operand read may run
+// into.
+constexpr int TMA_STG = 4096, CODE_STG = 2048;
+constexpr int TAIL_PLAIN = STG_BYTES, TAIL_PLAIN_TMA = EPI_WARPS * TMA_STG;
+constexpr int AMAX_CTA = 2 * BM * 4, TAIL_GATED = AMAX_CTA + EPI_WARPS * CODE_STG;
+static_assert(TAIL_PLAIN >= BM * 128 && TAIL_GATED >= BM * 128 && AMAX_BYTES + AMAX_CTA <= TAIL_GATED, "tail");
+constexpr int tail_bytes(int grp, bool gated) { return gated ? TAIL_GATED : grp == 1 ? TAIL_PLAIN_TMA : TAIL_PLAIN; }
 // Bytes of one K block's token scales in shared memory (few-token form).
 __host__ __device__ inline int sa_pitch(int a_rows, bool e8m0) { return e8m0 ? (a_rows + 15) / 16 * 16 : a_rows * 4; }
 // Bytes of a stage: GRP blocks of operands.
@@ -89,6 +93,7 @@ struct Args {
     void* y;
     int64_t ldy;
     bool y_f32, y_vec, y_wide; // y_vec: four columns a store; y_wide: eight, bf16
+    bool y_tma;                // rows on 16-byte strides, written by the copy engine
     // gated
     uint8_t* hq;
     int64_t ld_hq;
@@ -99,8 +104,9 @@ struct Args {
 };
 
 // What TMA brings: token codes (whole K blocks, and a ragged last one), weight image, token scales.
+// What it takes: y, 32 rows of 128 bytes at a time.
 struct Maps {
-    CUtensorMap a, a_last, w, s;
+    CUtensorMap a, a_last, w, s, y;
 };
 
 __device__ __forceinline__ uint32_t idesc_for(int n) {   // D f32, A = B = E4M3, K-major, M = 128
@@ -128,6 +134,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
 }
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n cp.async.bulk.commit_group;" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(src)
+                 : "memory");
+}
+// This thread's stores have read shared memory; have written memory.
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // Token tiles of n K blocks from kb, rows m0.., one after the other at dst: one copy, or block by
 // block where the ragged last one is among them.  Bytes that arrive: tokens_bytes.
 __device__ __forceinline__ void copy_tokens(const Maps& m, int k_full, int kt, uint32_t dst, int kb, int n, int m0, int a_bytes, uint32_t bar) {
@@ -279,7 +294,7 @@ __device__ __forceinline__ void ld_batch(uint32_t tb, int b, uint32_t (&raw)[PIE
 struct EpiCtx {
     int ew, quarter, half, lane;
     uint32_t rank, csize;
-    float* stg;                    // plain: the warp's staging tile, 32 rows of STG_STRIDE floats
+    uint8_t* stg;                  // the warp's staging tile: 32 rows of STG_STRIDE floats, 128 bytes (TMA) or 64 codes
     float* amax_cta;               // gated: [half][128]
     float* amax_all;               // gated: [parity][rank][128]
     uint64_t* xbar;                // gated: [parity]
@@ -287,6 +302,11 @@ struct EpiCtx {
     uint32_t xphase;
     volatile int* abort;
 };
+
+template <bool TMA>
+__device__ __forceinline__ uint8_t* staging(uint8_t* tail, bool gated, int ew) {
+    return gated ? tail + AMAX_CTA + ew * CODE_STG : tail + ew * (TMA ? TMA_STG : 32 * STG_STRIDE * 4);
+}
 
 // h = SiLU(g) * u of this thread's row and features, and its 1x128 E4M3 codes.  acc: pieces of 8
 // gate columns and the same 8 features' up columns.
@@ -326,14 +346,30 @@ __device__ __forceinline__ void epi_gated(const Args& a, EpiCtx& x, const float 
     uint32_t held;
     // h / s as h * (1 / s): within one ulp of the quotient, far inside the code spacing
     const float is = inv_scale(group_scale(am, a.e8m0, held));
+    uint32_t w[HALF / 8];
+#pragma unroll
+    for (int e = 0; e < HALF / 2; e += 4) w[e / 4] = pack4_e4m3(h[e] * is, h[e + 1] * is, h[e + 2] * is, h[e + 3] * is);
+    // 64 codes a row go through the staging tile, so that a store covers them in 8 rows; its 16-byte
+    // chunks are swizzled over the banks
+    const bool staged = HALF == 128 && f0 + HALF / 2 <= a.N;   // warp-uniform
+    if (staged && !dead) {
+#pragma unroll
+        for (int i = 0; i < HALF / 32; ++i)
+            *reinterpret_cast<uint4*>(x.stg + x.lane * 64 + ((i ^ ((x.lane >> 1) & 3)) * 16)) =
+                make_uint4(w[4 * i % (HALF / 8)], w[(4 * i + 1) % (HALF / 8)], w[(4 * i + 2) % (HALF / 8)], w[(4 * i + 3) % (HALF / 8)]);
+        __syncwarp();
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int rr = 8 * t + (x.lane >> 2), row = x.quarter * 32 + rr;
+            const uint4 v = *reinterpret_cast<const uint4*>(x.stg + rr * 64 + (((x.lane & 3) ^ ((rr >> 1) & 3)) * 16));
+            if (row < valid) *reinterpret_cast<uint4*>(a.hq + (int64_t)(m0 + row) * a.ld_hq + f0 + 16 * (x.lane & 3)) = v;
+        }
+    }
     if (r < valid && !dead) {
         uint8_t* dst = a.hq + (int64_t)(m0 + r) * a.ld_hq + f0;
-        uint32_t w[HALF / 8];
-#pragma unroll
-        for (int e = 0; e < HALF / 2; e += 4) w[e / 4] = pack4_e4m3(h[e] * is, h[e + 1] * is, h[e + 2] * is, h[e + 3] * is);
         constexpr int V = HALF >= 32 ? 4 : 2;                  // words a store: rows start on 16 bytes
 #pragma unroll
-        for (int i = 0; i < HALF / 8; i += V) {
+        for (int i = 0; i < HALF / 8 && !staged; i += V) {
             if (f0 + 4 * (i + V) <= a.N) {
                 if constexpr (V == 4) *reinterpret_cast<uint4*>(dst + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
                 else *reinterpret_cast<uint2*>(dst + 4 * i) = make_uint2(w[i], w[i + 1]);
@@ -355,13 +391,53 @@ __device__ __forceinline__ void epi_gated(const Args& a, EpiCtx& x, const float 
 // fp32 or bf16 rows: 16 columns at a time through the warp's staging tile, so that a store
 // instruction covers whole 32-byte sectors of 8 rows.
 template <int HALF>
-__device__ __forceinline__ void epi_plain(const Args& a, const EpiCtx& x, const float (&acc)[HALF], int m0, int n0, int valid) {
+__device__ __forceinline__ void epi_plain(const CUtensorMap& map_y, const Args& a, const EpiCtx& x, const float (&acc)[HALF], int m0, int n0, int valid) {
     const int row0 = x.quarter * 32, lane = x.lane;
     const int first = n0 + x.half * HALF;
+    if (HALF == 128 && a.y_tma) {
+        // 128 bytes of 32 rows at a time, handed to the copy engine: all CTAs finish their tiles at about
+        // the same time, and the last piece's way to memory overlaps the next tile.  Columns and rows
+        // past the end are clipped by the tensor map.  Swizzle: 16-byte chunk c of row r at c ^ (r mod 8).
+        uint8_t* row = x.stg + lane * 128;
+        const int per = a.y_f32 ? 32 : 64;
+#pragma unroll
+        for (int c0 = 0; c0 < HALF; c0 += 32) {
+            const bool fresh = a.y_f32 || c0 % 64 == 0;
+            if (fresh) {
+                if (lane == 0) tma_store_read();
+                __syncwarp();
+            }
+            if (a.y_f32) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<float4*>(row + ((j ^ (lane & 7)) * 16)) =
+                        make_float4(acc[(c0 + 4 * j) % HALF], acc[(c0 + 4 * j + 1) % HALF], acc[(c0 + 4 * j + 2) % HALF],
+                                    acc[(c0 + 4 * j + 3) % HALF]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        __nv_bfloat162 v = __floats2bfloat162_rn(acc[(c0 + 8 * j + 2 * k) % HALF], acc[(c0 + 8 * j + 2 * k + 1) % HALF]);
+                        w[k] = *reinterpret_cast<uint32_t*>(&v);
+                    }
+                    *reinterpret_cast<uint4*>(row + (((j + (c0 / 32 % 2) * 4) ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            if (a.y_f32 || c0 % 64 == 32) {
+                const int c = first + (c0 + 32 - per);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0 && c < a.N) tma_store_2d(&map_y, smem_addr(x.stg), c, m0 + row0);
+            }
+        }
+        return;
+    }
     if (a.y_wide && HALF >= 32 && first + HALF <= a.N && x.half * HALF + HALF <= a.bn) {
         // bf16, 32 columns at a time: a store covers 64 bytes of 8 rows, with half the instructions of the
         // 16-column form below (8192 x 2048 x 7168: 134 -> 118 us; e8m0 4096 x 7168 x 7168: 133.5 -> 132)
-        uint8_t* st = reinterpret_cast<uint8_t*>(x.stg);
+        uint8_t* st = x.stg;
         constexpr int PITCH = STG_STRIDE * 4;
 #pragma unroll
         for (int c0 = 0; c0 < HALF; c0 += 32) {
@@ -387,20 +463,21 @@ __device__ __forceinline__ void epi_plain(const Args& a, const EpiCtx& x, const 
         }
         return;
     }
+    float* stg = reinterpret_cast<float*>(x.stg);
 #pragma unroll
     for (int p = 0; p < HALF / 16; ++p) {
         const int cb = n0 + x.half * HALF + 16 * p;
         if (cb >= a.N || x.half * HALF + 16 * p >= a.bn) continue;           // warp-uniform
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4*>(x.stg + lane * STG_STRIDE + 4 * i) =
+            *reinterpret_cast<float4*>(stg + lane * STG_STRIDE + 4 * i) =
                 make_float4(acc[16 * p + 4 * i], acc[16 * p + 4 * i + 1], acc[16 * p + 4 * i + 2], acc[16 * p + 4 * i + 3]);
         __syncwarp();
         if (a.y_vec && cb + 16 <= a.N) {
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int rr = 8 * t + (lane >> 2), c = 4 * (lane & 3);
-                const float4 v = *reinterpret_cast<const float4*>(x.stg + rr * STG_STRIDE + c);
+                const float4 v = *reinterpret_cast<const float4*>(stg + rr * STG_STRIDE + c);
                 if (row0 + rr < valid) {
                     const int64_t at = (int64_t)(m0 + row0 + rr) * a.ldy + cb + c;
                     if (a.y_f32) {
@@ -418,7 +495,7 @@ __device__ __forceinline__ void epi_plain(const Args& a, const EpiCtx& x, const 
             for (int t0 = 0; t0 < 16; t0 += 8) {
                 float v[8];
 #pragma unroll
-                for (int t = 0; t < 8; ++t) v[t] = x.stg[(2 * (t0 + t) + (lane >> 4)) * STG_STRIDE + (lane & 15)];
+                for (int t = 0; t < 8; ++t) v[t] = stg[(2 * (t0 + t) + (lane >> 4)) * STG_STRIDE + (lane & 15)];
                 const int c = lane & 15;
                 int64_t at = (int64_t)(m0 + row0 + 2 * t0 + (lane >> 4)) * a.ldy + cb + c;
 #pragma unroll
@@ -560,9 +637,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
     const int w_bytes = a.bn * 128, a_bytes = a.a_rows * 128;
     const int stage_bytes = GRP * (w_bytes + a_bytes);
     uint8_t* tail = ring + a.stages * stage_bytes;
-    float* stg_all = reinterpret_cast<float*>(tail);                            // plain
     float* amax_cta = reinterpret_cast<float*>(tail);                           // gated: [half][128]
-    float* amax_all = amax_cta + 2 * BM;                                        // gated: [parity][rank][128]
+    float* amax_all = amax_cta + 2 * BM;                                        // gated: [parity][rank][128], or staging
     __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES], tfull[2], tempty[2], xbar[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
@@ -703,7 +779,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
         const uint32_t tmem = tmem_slot + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * HALF);
         pdl_wait();
         if (GATED && csize > 1) cluster_wait();
-        EpiCtx ctx = {ew, quarter, half, lane, rank, csize, stg_all + (size_t)ew * 32 * STG_STRIDE, amax_cta, amax_all, xbar, 0, 0u, abort};
+        EpiCtx ctx = {ew, quarter, half, lane, rank, csize, staging<GRP == 1>(tail, GATED, ew), amax_cta, amax_all, xbar, 0, 0u, abort};
         int buf = 0;
         uint32_t tphase = 0;
         bool dead = false;
@@ -847,8 +923,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
             }
             if (u + step < a.n_units) fetch_unit(u + step);
             if constexpr (GATED) epi_gated<HALF>(a, ctx, acc, m0, n0, valid, dead);
-            else if (live && !dead) epi_plain<HALF>(a, ctx, acc, m0, n0, valid);
+            else if (live && !dead) epi_plain<HALF>(maps.y, a, ctx, acc, m0, n0, valid);
         }
+        if (!GATED && GRP == 1 && lane == 0) tma_store_done();
     }
     if (warp < CTRL_WARPS) {
         if (shared_k) cluster_arrive_release();                // the drain warps' barrier before they join
@@ -920,6 +997,12 @@ inline bool encode_maps(const GemmCall& c, const Args& a, int grp, int scale_row
         ok = ok && enc(&m->s, a.e8m0 ? u8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(c.as), sd, ss, sb, one, none,
                        CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, fill) == CUDA_SUCCESS;
     }
+    if (a.y_tma) {
+        const cuuint64_t yd[2] = {(cuuint64_t)a.N, M}, ys[1] = {(cuuint64_t)c.ldy * (c.y_f32 ? 4 : 2)};
+        const cuuint32_t yb[2] = {c.y_f32 ? 32u : 64u, 32};
+        ok = ok && enc(&m->y, c.y_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.y, yd, ys, yb, one, none,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, fill) == CUDA_SUCCESS;
+    }
     return ok;
 }
 
@@ -929,9 +1012,10 @@ cudaError_t launch(const GemmCall& c, const Plan& p, Args& a, cudaStream_t s) {
     a.n_nt = p.n_nt;
     a.n_units = p.units;
     a.S = p.S;
+    a.y_tma = !GATED && GRP == 1 && p.S == 1 && c.ldy * (c.y_f32 ? 4 : 2) % 16 == 0 && reinterpret_cast<uintptr_t>(c.y) % 16 == 0;
     Maps maps;
     if (!encode_maps(c, a, GRP, 0, 0, &maps)) return cudaErrorInvalidValue;
-    const int cost = stage_cost(GRP, a.bn, a.a_rows), fixed = 1024 + (GATED ? TAIL_GATED : TAIL_PLAIN);
+    const int cost = stage_cost(GRP, a.bn, a.a_rows), fixed = 1024 + tail_bytes(GRP, GATED);
     const int groups = (a.kt + GRP - 1) / GRP;
     a.stages = std::max(1, std::min(MAX_STAGES, (SMEM_MAX - fixed) / cost));
     if (p.S == 1) a.stages = std::min(a.stages, std::max(2, groups));      // S > 1 also keeps its sums there

@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
         const uint32_t tmem = tmem_slot + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * HALF);
         pdl_wait();
         if (GATED && csize > 1) cluster_wait();
-        EpiCtx ctx = {ew, quarter, half, lane, rank, csize, reinterpret_cast<float*>(tail) + (size_t)ew * 32 * STG_STRIDE, amax_cta,
+        EpiCtx ctx = {ew, quarter, half, lane, rank, csize, staging<false>(tail, GATED, ew), amax_cta,
                       amax_cta + 2 * BM, xbar, 0, 0u, abort};
         int buf = 0;
         uint32_t tphase = 0;
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
                 }
             }
             if constexpr (GATED) epi_gated<HALF>(a, ctx, acc, m0, n0, valid, dead);
-            else if (live && !dead) epi_plain<HALF>(a, ctx, acc, m0, n0, valid);
+            else if (live && !dead) epi_plain<HALF>(maps.y, a, ctx, acc, m0, n0, valid);
         }
     }
     if (warp < CTRL_WARPS) {

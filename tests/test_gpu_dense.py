@@ -330,6 +330,23 @@ def test_linear_output_strides(moe, dtype):
         assert (store[:, keep] == 7).all()
 
 
+@pytest.mark.parametrize("m,k,n", [(2333, 640, 4040), (1921, 1100, 5000)])
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_linear_of_many_rows(moe, m, k, n, scale, dtype):
+    """Several tiles per SM, the last ones ending inside the output: against 64 bits, and the same bits in wider storage
+    with nothing beside them written."""
+    lin, ref = check_linear(moe, m, k, n, scale, dtype, seed=56)
+    aq, a_s = rows_fp8(randn((m, k), 56), scale)
+    a = moe.Fp8Tensor.from_parts(aq, a_s)
+    for width, off in ((n + 24, 8), (n + 3, 1)):
+        store = torch.full((m + 2, width), 7.0, dtype=dtype, device="cuda")
+        assert torch.equal(lin(a, store[1:m + 1, off:off + n]), ref)
+        keep = torch.ones(m + 2, width, dtype=torch.bool, device="cuda")
+        keep[1:m + 1, off:off + n] = False
+        assert (store[keep] == 7).all()
+
+
 def test_linear_offsets_past_32_bits(moe):
     m, k, n = 3, 256, 130
     aq, a_s = rows_fp8(randn((m, k), 60), "f32")
