@@ -68,10 +68,12 @@ struct FewArgs {
     uint32_t wait_limit;
 };
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+// Four fp32 into a CTA of the cluster, counted on that CTA's mbarrier.
+__device__ __forceinline__ void st_async_4(uint32_t remote, const float* v, uint32_t remote_bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(remote),
+                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+                 "r"(remote_bar)
+                 : "memory");
 }
 // (a0, a1) += (x0, x1) * s * (c0, c1), rounded as s * c and one fma each.
 __device__ __forceinline__ void fma2s(float& a0, float& a1, uint32_t x0, uint32_t x1, float s, float c0, float c1) {
@@ -159,11 +161,12 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int w_bytes = a.R * 128, a_bytes = a.a_rows * 128, stage_bytes = a.G * (w_bytes + a_bytes);
     const int pitch = sa_pitch(a.a_rows, E8S), slot_bytes = (a.G * pitch + 127) / 128 * 128;
-    float* part = reinterpret_cast<float*>(ring + a.stages * stage_bytes);          // [token][128 rows]
-    uint8_t* scales = reinterpret_cast<uint8_t*>(part) + tail_bytes(TN);            // [stage][slot]; MX: [kr4][pitch]
+    uint8_t* recv = ring + a.stages * stage_bytes;                                  // [own token group][rank][row][4 tokens] fp32
+    uint8_t* scales = recv + tail_bytes(TN);                                        // [stage][slot]; MX: [kr4][pitch]
     float* sws = reinterpret_cast<float*>(scales + a.stages * slot_bytes);          // [kr][2]
     uint8_t* packed = scales + (a.kr4 * pitch + 127) / 128 * 128;                   // MX: [quad][weights 512 B | tokens 512 B]
-    __shared__ uint64_t full[ST_MAX], empty[ST_MAX], tfull[ST_MAX], sfull, sready[MODE == MX ? MX_QUADS : 1];
+    __shared__ uint64_t full[ST_MAX], empty[ST_MAX], tfull[ST_MAX], sfull, sready[MODE == MX ? MX_QUADS : 1], joined;
+    __shared__ __align__(16) float amax[GATED ? 2 : 1][2][4][4];                                  // [parity][half of the threads][warp][token]
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
 
@@ -174,6 +177,8 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
     const int kb0 = range_start(a.kt, a.S, rank % a.S), nkb = range_start(a.kt, a.S, rank % a.S + 1) - kb0;
     const int n_grp = (nkb + a.G - 1) / a.G;
     const int pre = min(a.stages, n_grp);
+    // groups of 4 tokens go to the cluster's CTAs in turn; this one finishes `own` of them
+    const int own = csize > 1 ? ((a.M + 3) / 4 + csize - 1 - rank) / csize : 0;
     const uint32_t ring0 = smem_addr(ring), scl0 = smem_addr(scales), full0 = smem_addr(full);
 
     // a stage's bytes and the copy of its weights, by one thread
@@ -187,6 +192,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
     if (threadIdx.x == 0) {
         const uint32_t drains = MODE == MX ? 1 : EPI_WARPS;
         for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], drains); mbar_init(&tfull[s], 1); }
+        mbar_init(&joined, 1);
         if (MODE == MX) {
             mbar_init(&sfull, 1);
             for (int q = 0; q < (MODE == MX ? MX_QUADS : 1); ++q) mbar_init(&sready[q], 1);
@@ -194,10 +200,12 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
         fence_mbar_init();
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         abort_flag = 0;
+        if (own > 0) expect_tx(smem_addr(&joined), (uint32_t)(own * csize * a.R * 16));
         // the weights do not depend on the preceding kernel, nor on the rest of this one's set-up
         for (int g = 0; g < pre; ++g) copy_w(g, g);
     }
     __syncthreads();
+    if (csize > 1) cluster_arrive();                           // waited for before anything is sent to a peer
     volatile int* abort = &abort_flag;
 
     if (warp < CTRL_WARPS) {
@@ -332,9 +340,8 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
             tc::tmem_dealloc(tmem_slot, COLS);
         }
         if (csize > 1) {                                       // the drain warps' two cluster barriers below
-            cluster_arrive_release();
             cluster_wait();
-            cluster_arrive_release();
+            cluster_arrive();
             cluster_wait();
         }
         return;
@@ -357,6 +364,14 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
     named_bar_sync(2, (1 + EPI_WARPS) * 32);
     tc::tc_fence_after();
     const uint32_t tmem = tmem_slot + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t recv0 = smem_addr(recv), joined0 = smem_addr(&joined);
+    // this row's sums of 4 tokens from t, to the CTA that finishes them
+    auto send = [&](int t, const float* v) {
+        const int g = t / 4, to = g % csize, slot = g / csize;
+        if (row < a.R)
+            st_async_4(map_to_rank(recv0 + (uint32_t)(((slot * csize + rank) * a.R + row) * 16), to), v, map_to_rank(joined0, to));
+    };
+    if (csize > 1) cluster_wait();                             // the peers have set up their barriers
     if constexpr (MODE == MX) {
         pdl_wait();                                            // before the first write the preceding kernel may conflict with
         const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[0], 0, a.wait_limit, a.status, abort));
@@ -368,15 +383,18 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
                 uint32_t raw[8];
                 ld8(tmem + c, raw);
                 tc::tmem_wait_ld();
+                float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (c + e >= a.M) break;
-                    const float v = __uint_as_float(raw[e]);
-                    if (!GATED && csize == 1) {
-                        if (row < a.R && n0 + row < a.N) store_y(a, c + e, n0 + row, v);
-                    } else {
-                        part[(c + e) * BM + row] = v;
+                for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(raw[e]);
+                if (!GATED && csize == 1) {
+                    if (row < a.R && n0 + row < a.N) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (c + e < a.M) store_y(a, c + e, n0 + row, v[e]);
                     }
+                } else {
+                    send(c, v);
+                    if (c + 4 < a.M) send(c + 4, v + 4);
                 }
             }
         }
@@ -418,52 +436,90 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
         pdl_wait();                                            // before the first write the preceding kernel may conflict with
         if (live) {
 #pragma unroll
-            for (int t = 0; t < HT; ++t) {
+            for (int t = 0; t < HT; t += 4) {
                 if (t0 + t >= a.M) break;
                 if (!GATED && csize == 1) {
-                    if (row < a.R && n0 + row < a.N) store_y(a, t0 + t, n0 + row, acc[t]);
+                    if (row < a.R && n0 + row < a.N) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (t0 + t + e < a.M) store_y(a, t0 + t + e, n0 + row, acc[t + e]);
+                    }
                 } else {
-                    part[(t0 + t) * BM + row] = acc[t];
+                    send(t0 + t, acc + t);
                 }
             }
         }
     }
     // -------------------------------------------------------- join the K ranges
+    // The sums were sent as they were drained, 512 bytes a warp and instruction; each CTA waits for its
+    // token groups' bytes and finishes them from its own shared memory.  (Leaving them at home, a cluster
+    // barrier and loads from the peers took 5,400 cycles, with another barrier before anyone may leave:
+    // 64 x 7168 x 2048 gated 17.5 us, 50 x 1040 x 1000 5.7.)
     tc::tc_fence_before();
     named_bar_sync(3, NTHREADS);
     if (csize == 1) return;
-    cluster_arrive_release();
-    cluster_wait();
-    const uint32_t part0 = smem_addr(part);
-    if (!*abort) {
-        const int tid = threadIdx.x - CTRL_WARPS * 32;
+    cluster_arrive();                                          // everything sent
+    if (own > 0 && __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&joined, 0, a.wait_limit, a.status, abort))) {
+        const int tid = threadIdx.x - CTRL_WARPS * 32, side = tid >> 7, i = tid & 127;   // 128 threads a group
+        const float4* in = reinterpret_cast<const float4*>(recv);
         if constexpr (GATED) {
-            // a warp takes a token: four features a lane, 128 in all
-            const int f = 4 * lane, ff = f & 63, r = (ff >> 3) * 16 + (ff & 7);
-            const int base = (f >> 6) * a.S;                   // first rank of the tile with these features
-            for (int t = rank * EPI_WARPS + (tid >> 5); t < a.M; t += csize * EPI_WARPS) {
+            // a thread takes a feature of four tokens
+            const int ff = i & 63, r = (ff >> 3) * 16 + (ff & 7);
+            const int base = (i >> 6) * a.S;                   // first rank of the tile with this feature
+            const int f = unit * QB + i;
+            int parity = 0;
+            for (int slot = side; slot < own; slot += 2, parity ^= 1) {
                 float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
                 for (int p = 0; p < a.S; ++p) {
-                    const uint32_t at = map_to_rank(part0 + (uint32_t)(t * BM + r) * 4u, base + p);
-                    const float4 x = ld_cluster4(at), z = ld_cluster4(at + 32);
-                    g = add4(g, x);
-                    u = add4(u, z);
+                    const float4* at = in + (slot * csize + base + p) * BM + r;
+                    g = add4(g, at[0]);
+                    u = add4(u, at[8]);
                 }
-                quantise_row(a, E8S, t, unit, lane, g, u);
+                float h[4] = {silu_mul(g.x, u.x), silu_mul(g.y, u.y), silu_mul(g.z, u.z), silu_mul(g.w, u.w)}, am[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (f >= a.N) h[e] = 0.f;
+                    am[e] = fabsf(h[e]);
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) am[e] = max_nan(am[e], __shfl_xor_sync(0xFFFFFFFFu, am[e], o));
+                }
+                float (&all)[4][4] = amax[parity][side];
+                if (lane == 0) *reinterpret_cast<float4*>(all[ew & 3]) = make_float4(am[0], am[1], am[2], am[3]);
+                if (side == 0) named_bar_sync(4, 128);
+                else named_bar_sync(5, 128);
+                const int t0 = 4 * (slot * csize + rank);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float m = max_nan(max_nan(all[0][e], all[1][e]), max_nan(all[2][e], all[3][e]));
+                    uint32_t held;
+                    const float is = inv_scale(group_scale(m, E8S, held));
+                    if (t0 + e >= a.M) continue;
+                    if (f < a.N) a.hq[(int64_t)(t0 + e) * a.ld_hq + f] = (uint8_t)f32x2_to_e4m3x2(h[e] * is, 0.f);
+                    if (i == 0) {
+                        const int64_t at = (int64_t)unit * a.ld_hs + t0 + e;
+                        if (E8S) static_cast<uint8_t*>(a.hs)[at] = (uint8_t)held;
+                        else static_cast<uint32_t*>(a.hs)[at] = held;
+                    }
+                }
             }
         } else {
-            // each CTA of the cluster finishes a slice of the tile's rows
-            const int rs = a.R / a.S, lo = rank * rs;
-            for (int i = tid; i < rs * a.M; i += EPI_WARPS * 32) {
-                const int t = i / rs, r = lo + i % rs;
-                float v = 0.f;
-                for (int p = 0; p < a.S; ++p) v += ld_cluster(map_to_rank(part0 + (uint32_t)(t * BM + r) * 4u, p));
-                if (n0 + r < a.N) store_y(a, t, n0 + r, v);
+            // a thread takes a row of four tokens
+            for (int slot = side; slot < own; slot += 2) {
+                if (i >= a.R || n0 + i >= a.N) break;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int p = 0; p < a.S; ++p) v = add4(v, in[(slot * csize + p) * a.R + i]);
+                const int t0 = 4 * (slot * csize + rank);
+                const float y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (t0 + e < a.M) store_y(a, t0 + e, n0 + i, y[e]);
             }
         }
     }
-    cluster_arrive_release();                                  // nobody leaves while a peer may still read its sums
-    cluster_wait();
+    cluster_wait();                                            // nobody leaves while a peer may still send to it
 }
 
 struct FewPlan {
