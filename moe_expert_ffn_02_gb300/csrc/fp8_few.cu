@@ -213,6 +213,11 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
         if (warp == 0) {
             // ------------------------------------------------ producer
             const uint32_t el = elect_one();
+            if (el) {
+                prefetch_map(&maps.a);
+                if (a.k_full < a.kt) prefetch_map(&maps.a_last);
+                prefetch_map(&maps.s);
+            }
             pdl_wait();
             if (MODE == MX && el) {                  // the range's token scales, all at once
                 expect_tx(smem_addr(&sfull), (uint32_t)(a.kr4 * pitch));
@@ -364,10 +369,11 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
     named_bar_sync(2, (1 + EPI_WARPS) * 32);
     tc::tc_fence_after();
     const uint32_t tmem = tmem_slot + ((uint32_t)(quarter * 32) << 16);
+    const int csize_log = 31 - __clz(csize);                   // csize is a power of two
     const uint32_t recv0 = smem_addr(recv), joined0 = smem_addr(&joined);
     // this row's sums of 4 tokens from t, to the CTA that finishes them
     auto send = [&](int t, const float* v) {
-        const int g = t / 4, to = g % csize, slot = g / csize;
+        const int g = t / 4, to = g & (csize - 1), slot = g >> csize_log;
         if (row < a.R)
             st_async_4(map_to_rank(recv0 + (uint32_t)(((slot * csize + rank) * a.R + row) * 16), to), v, map_to_rank(joined0, to));
     };
@@ -378,14 +384,17 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
         if (live && ok) {
             tc::tc_fence_after();
             // the two warps of a quarter take eight tokens in turn
-#pragma unroll 1
-            for (int c = 8 * half; c < min(TN, a.M); c += 16) {
-                uint32_t raw[8];
-                ld8(tmem + c, raw);
-                tc::tmem_wait_ld();
+            uint32_t raw[TN / 16][8];
+#pragma unroll
+            for (int j = 0; j < TN / 16; ++j) ld8(tmem + 8 * half + 16 * j, raw[j]);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < TN / 16; ++j) {
+                const int c = 8 * half + 16 * j;
+                if (c >= a.M) break;
                 float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(raw[e]);
+                for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(raw[j][e]);
                 if (!GATED && csize == 1) {
                     if (row < a.R && n0 + row < a.N) {
 #pragma unroll
@@ -470,6 +479,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
             int parity = 0;
             for (int slot = side; slot < own; slot += 2, parity ^= 1) {
                 float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+#pragma unroll 4
                 for (int p = 0; p < a.S; ++p) {
                     const float4* at = in + (slot * csize + base + p) * BM + r;
                     g = add4(g, at[0]);
@@ -491,18 +501,21 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
                 if (side == 0) named_bar_sync(4, 128);
                 else named_bar_sync(5, 128);
                 const int t0 = 4 * (slot * csize + rank);
+                // lane e mod 4 works out token e's scale
+                const int q = lane & 3;
+                uint32_t held;
+                const float is = inv_scale(group_scale(max_nan(max_nan(all[0][q], all[1][q]), max_nan(all[2][q], all[3][q])), E8S, held));
+                uint8_t code[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float m = max_nan(max_nan(all[0][e], all[1][e]), max_nan(all[2][e], all[3][e]));
-                    uint32_t held;
-                    const float is = inv_scale(group_scale(m, E8S, held));
-                    if (t0 + e >= a.M) continue;
-                    if (f < a.N) a.hq[(int64_t)(t0 + e) * a.ld_hq + f] = (uint8_t)f32x2_to_e4m3x2(h[e] * is, 0.f);
-                    if (i == 0) {
-                        const int64_t at = (int64_t)unit * a.ld_hs + t0 + e;
-                        if (E8S) static_cast<uint8_t*>(a.hs)[at] = (uint8_t)held;
-                        else static_cast<uint32_t*>(a.hs)[at] = held;
-                    }
+                for (int e = 0; e < 4; ++e) code[e] = (uint8_t)f32x2_to_e4m3x2(h[e] * __shfl_sync(0xFFFFFFFFu, is, e), 0.f);
+                uint8_t* dst = a.hq + (int64_t)t0 * a.ld_hq + f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e, dst += a.ld_hq)
+                    if (t0 + e < a.M && f < a.N) *dst = code[e];
+                if (i < 4 && t0 + i < a.M) {
+                    const int64_t at = (int64_t)unit * a.ld_hs + t0 + i;
+                    if (E8S) static_cast<uint8_t*>(a.hs)[at] = (uint8_t)held;
+                    else static_cast<uint32_t*>(a.hs)[at] = held;
                 }
             }
         } else {
@@ -510,6 +523,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
             for (int slot = side; slot < own; slot += 2) {
                 if (i >= a.R || n0 + i >= a.N) break;
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
                 for (int p = 0; p < a.S; ++p) v = add4(v, in[(slot * csize + p) * a.R + i]);
                 const int t0 = 4 * (slot * csize + rank);
                 const float y[4] = {v.x, v.y, v.z, v.w};
