@@ -547,12 +547,13 @@ static int longest_range(int kt, int S) {
     return kr;
 }
 
-// Rows per tile and K ranges, from the weights' shape alone.  Fitted to sweeps of R, S and G on this
-// GPU: a CTA takes 0.14 us + 1.3 ns per row for a K block (its MMAs and hand-offs), an SM at most 70 GB/s,
-// all of them 6.8 TB/s; these add up like sides of a right angle, as each covers part of the other.
-// Joining K ranges costs about 1 us, and each CTA 3 ns.  Two CTAs per SM with shorter ranges beat one:
-// 7168 x 7168 takes 11.1 us with R = 112, S = 4 (256 CTAs) and 16.7 with R = 48, S = 1 (150).  Clusters do not
-// pack every SM: past 92 % of the slots a second wave starts (300 CTAs in clusters of four: 12.1 us).
+// Rows per tile and K ranges, from the weights' shape alone.  The weights of the estimate are fitted to
+// which of the measured R and S is fastest (12 shapes, both scale types, 1, 20 and 64 tokens: within 1 % of
+// the best on average), not to the times: a K block's MMAs and hand-offs, an SM's 70 GB/s, all SMs'
+// 6.8 TB/s, a fixed cost per tile, per joined range and per CTA.  Short ranges win: 2048 x 7168, one token, takes
+// 4.3 us with R = 128, S = 4 (224 CTAs) and 5.4 with R = 96, S = 2; 7168 x 4096, 64 tokens, 11.6 with R = 128,
+// S = 8 and 15.2 with R = 64, S = 4.  Clusters do not pack every SM: past 92 % of the slots a second wave
+// starts (7168 x 7168: 300 CTAs in clusters of four 12.1 us, 256 10.3).
 static FewPlan plan_few(const moe_linear* L, bool gated) {
     FewPlan best = {};
     double best_us = 0;
@@ -562,13 +563,12 @@ static FewPlan plan_few(const moe_linear* L, bool gated) {
         const int kr = longest_range(L->kt, S);
         if (kr > KR_MAX) continue;
         for (int R = gated ? BM : 16; R <= BM; R += 16) {
-            if (R % S) continue;
             const double tiles = gated ? 2.0 * ((L->d.out_features + QB - 1) / QB) : (double)((L->rows + R - 1) / R);
             const double ctas = tiles * S, per_sm = ctas <= L->num_sms ? 1.0 : 2.0;
             const double rounds = std::ceil(ctas / (gated || S > 1 ? 0.92 * slots : slots));
-            const double cta = rounds * std::max(kr * (0.14 + 0.0013 * R), per_sm * kr * R * 128.0 / 70e3);
+            const double cta = rounds * std::max(kr * (0.5 + 0.0013 * R), per_sm * kr * R * 128.0 / 70e3) + 1.2;
             const double hbm = L->kt * tiles * R * 128.0 / 6.8e6;
-            const double us = std::sqrt(cta * cta + hbm * hbm) + (S > 1 ? 1.0 : 0.0) + 0.003 * ctas;
+            const double us = std::sqrt(cta * cta + hbm * hbm) + (S > 1 ? 1.0 : 0.0) + 0.007 * ctas;
             if (!best.R || us < best_us) {
                 best_us = us;
                 best = FewPlan{R, S, R <= 64 && kr >= 8 ? 4 : 2};
