@@ -535,32 +535,52 @@ __device__ __forceinline__ void leave_partial(float* part, int half, int r, cons
     for (int c = 0; c < HALF; c += 4) *reinterpret_cast<float4*>(p + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
 }
 
-// 4 features' codes and, by lane 0, the group's scale: one warp holds a row's 128 features.
-template <class A>
-__device__ __forceinline__ void quantise_row(const A& a, bool e8, int64_t row, int unit, int lane, const float4& g, const float4& u) {
-    const int f0 = unit * QB + 4 * lane;
-    float h[4] = {silu_mul(g.x, u.x), silu_mul(g.y, u.y), silu_mul(g.z, u.z), silu_mul(g.w, u.w)};
-    float am = 0.f;
+// The codes of 4 features from f (of the unit's 128) and, by lane 0, the group's scale, of R rows: one
+// warp holds the rows' 128 features.  A row's way through SiLU, the largest of 32 lanes and the scale is a
+// chain of several hundred cycles, so R of them run side by side.  row: -1 for none (warp-uniform).
+template <int R>
+__device__ __forceinline__ void quantise_rows(const Args& a, const int (&row)[R], int unit, int lane, int f, const float4 (&g)[R],
+                                              const float4 (&u)[R]) {
+    const int f0 = unit * QB + f;
+    float h[R][4], am[R];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        if (f0 + e >= a.N) h[e] = 0.f;
-        am = max_nan(am, fabsf(h[e]));
+    for (int i = 0; i < R; ++i) {
+        h[i][0] = silu_mul(g[i].x, u[i].x);
+        h[i][1] = silu_mul(g[i].y, u[i].y);
+        h[i][2] = silu_mul(g[i].z, u[i].z);
+        h[i][3] = silu_mul(g[i].w, u[i].w);
+        am[i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            h[i][e] = f0 + e < a.N ? h[i][e] : 0.f;
+            am[i] = max_nan(am[i], fabsf(h[i][e]));
+        }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
-    uint32_t held;
-    const float is = inv_scale(group_scale(am, e8, held));
-    const uint32_t v = pack4_e4m3(h[0] * is, h[1] * is, h[2] * is, h[3] * is);
-    uint8_t* dst = a.hq + row * a.ld_hq + f0;
-    if (f0 + 4 <= a.N) {
-        *reinterpret_cast<uint32_t*>(dst) = v;
-    } else {
-        for (int e = 0; f0 + e < a.N; ++e) dst[e] = (uint8_t)(v >> (8 * e));
+    for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) am[i] = max_nan(am[i], __shfl_xor_sync(0xFFFFFFFFu, am[i], o));
     }
-    if (lane == 0) {
-        const int64_t at = (int64_t)unit * a.ld_hs + row;
-        if (e8) static_cast<uint8_t*>(a.hs)[at] = (uint8_t)held;
-        else static_cast<uint32_t*>(a.hs)[at] = held;
+    uint32_t v[R], held[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const float is = inv_scale(group_scale(am[i], a.e8m0, held[i]));
+        v[i] = pack4_e4m3(h[i][0] * is, h[i][1] * is, h[i][2] * is, h[i][3] * is);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (row[i] < 0) continue;
+        uint8_t* dst = a.hq + (int64_t)row[i] * a.ld_hq + f0;
+        if (f0 + 4 <= a.N) {
+            *reinterpret_cast<uint32_t*>(dst) = v[i];
+        } else {
+            for (int e = 0; f0 + e < a.N; ++e) dst[e] = (uint8_t)(v[i] >> (8 * e));
+        }
+        if (lane == 0) {
+            const int64_t at = (int64_t)unit * a.ld_hs + row[i];
+            if (a.e8m0) static_cast<uint8_t*>(a.hs)[at] = (uint8_t)held[i];
+            else static_cast<uint32_t*>(a.hs)[at] = held[i];
+        }
     }
 }
 
@@ -575,38 +595,68 @@ __device__ __forceinline__ float4 sum_ranks(uint32_t at) {
     return v[0];
 }
 
-// Drain warp ew of CTA `rank` adds and finishes rows ew S + rank, + 8 S, ...
+// Drain warp ew of CTA `rank` adds and finishes rows ew S + rank, + 8 S, ..., gated R at a time.  Loads from
+// the peers run at about 15 bytes a cycle into an SM, which bounds this (128 x 256 sums: 4 to 5 us).
 template <int BN, bool GATED, int S>
 __device__ __forceinline__ void join_rows(const Args& a, uint32_t part0, int rank, int ew, int lane, int m0, int n0, int valid) {
+    constexpr int R = GATED ? 8 / S : 1, STEP = EPI_WARPS * S;
 #pragma unroll 1
-    for (int r = ew * S + rank; r < valid; r += EPI_WARPS * S) {
-        const uint32_t row = part0 + (uint32_t)(r * part_pitch(BN)) * 4u;
+    for (int r = ew * S + rank; r < valid; r += R * STEP) {
+        uint32_t part[R];
+        int row[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const bool in = r + i * STEP < valid;
+            row[i] = in ? m0 + r + i * STEP : -1;
+            part[i] = part0 + (uint32_t)((in ? r + i * STEP : r) * part_pitch(BN)) * 4u + 16u * lane;
+        }
         if constexpr (GATED) {
-            const uint32_t at = row + (uint32_t)((lane >> 1) * 16 + (lane & 1) * 4) * 4u;      // 8 gate columns, then 8 up
-            const float4 g = sum_ranks<S>(at), u = sum_ranks<S>(at + 32);
-            quantise_row(a, a.e8m0, m0 + r, n0 / (2 * QB), lane, g, u);
+            // Whole 512-byte runs of the row (a lane's own gate and up columns, 32 bytes of every 64, took
+            // 1.4 times as long); each 16 columns are 8 gate, then 8 up, so lanes l and l ^ 2 swap halves.
+            const bool up = (lane & 2) != 0;
+            float4 g[R], u[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                g[i] = sum_ranks<S>(part[i]);
+                u[i] = sum_ranks<S>(part[i] + 512);
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float4 give = up ? g[i] : u[i];
+                const float4 got = make_float4(__shfl_xor_sync(0xFFFFFFFFu, give.x, 2), __shfl_xor_sync(0xFFFFFFFFu, give.y, 2),
+                                               __shfl_xor_sync(0xFFFFFFFFu, give.z, 2), __shfl_xor_sync(0xFFFFFFFFu, give.w, 2));
+                if (up) g[i] = got;
+                else u[i] = got;
+            }
+            quantise_rows<R>(a, row, n0 / (2 * QB), lane, (lane >> 2) * 8 + (lane & 1) * 4 + (up ? 64 : 0), g, u);
         } else {
 #pragma unroll
             for (int c0 = 0; c0 < BN; c0 += 128) {
                 const int c = c0 + 4 * lane;
                 if (n0 + c >= a.N) break;
-                const float4 v = sum_ranks<S>(row + 4u * c);
-                const int64_t at = (int64_t)(m0 + r) * a.ldy + n0 + c;
-                if (a.y_vec && n0 + c + 4 <= a.N) {
-                    if (a.y_f32) {
-                        *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = v;
-                    } else {
-                        __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
-                            make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
-                    }
-                } else {
-                    const float e[4] = {v.x, v.y, v.z, v.w};
+                float4 v[R];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (n0 + c + i >= a.N) break;
-                        if (a.y_f32) static_cast<float*>(a.y)[at + i] = e[i];
-                        else static_cast<__nv_bfloat16*>(a.y)[at + i] = __float2bfloat16_rn(e[i]);
+                for (int i = 0; i < R; ++i) v[i] = sum_ranks<S>(part[i] + 4u * c0);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    if (row[i] < 0) continue;
+                    const int64_t at = (int64_t)row[i] * a.ldy + n0 + c;
+                    if (a.y_vec && n0 + c + 4 <= a.N) {
+                        if (a.y_f32) {
+                            *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = v[i];
+                        } else {
+                            __nv_bfloat162 lo = __floats2bfloat162_rn(v[i].x, v[i].y), hi = __floats2bfloat162_rn(v[i].z, v[i].w);
+                            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
+                                make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+                        }
+                    } else {
+                        const float e[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (n0 + c + j >= a.N) break;
+                            if (a.y_f32) static_cast<float*>(a.y)[at + j] = e[j];
+                            else static_cast<__nv_bfloat16*>(a.y)[at + j] = __float2bfloat16_rn(e[j]);
+                        }
                     }
                 }
             }
