@@ -19,20 +19,23 @@ static Plan plan_gated(const GemmCall& c, const Args& a) {
     if (units > 0x3FFFFFFF) return best;
     // a unit's K block takes the draining of its columns, or its copies
     auto block_us = [&](int grp, int bn) {
-        return std::max(grp == 1 ? 0.48 : grp == 2 ? 0.43 : grp == 4 ? 0.23 : 0.15, copy_us(bn, a.a_rows));
+        return std::max(grp == 1 ? 0.46 : grp == 2 ? 0.305 : 0.098, copy_us(bn, a.a_rows));
     };
-    const double weights = (double)c.lin->rows * a.kt * 128.0;
+    auto fixed_us = [](int bn) { return 1.635 + 0.447 * bn / 256; };
+    const double bytes = memory_bytes(c, true);
     for (int cl = 1; cl <= MAX_CLUSTER; cl *= 2) {
         const int grp = cl, bn = BUF_COLS / cl, slots = cluster_slots(sms, cl);
         if (2 * stage_cost(grp, bn, a.a_rows) <= ring_max(true)) {
-            const double us = plan_us((double)((units + slots - 1) / slots), a.kt, block_us(grp, bn), weights, bn, 1, 0) + (cl > 1 ? 0.8 : 0.0);
+            const double us = plan_us((double)((units + slots - 1) / slots), a.kt, block_us(grp, bn), fixed_us(bn), bytes) +
+                              (cl > 1 ? 0.126 : 0.0);
             if (best.bn == 0 || us < best_us) {
                 best_us = us;
                 best = Plan{grp, bn, cl, (int)units, nt, 1, us};
             }
         }
         if (cl > 1 && cl <= a.kt && units <= slots) {
-            const double us = plan_us(1.0, (a.kt + cl - 1) / cl, block_us(1, BUF_COLS), weights, BUF_COLS, cl, (double)units * cl);
+            const double us = plan_us(1.0, (a.kt + cl - 1) / cl, block_us(1, BUF_COLS), fixed_us(BUF_COLS), bytes) +
+                              join_us(true, BUF_COLS, cl, c.M, (double)units * cl);
             if (best.bn == 0 || us < best_us) {
                 best_us = us;
                 best = Plan{1, BUF_COLS, cl, (int)units, nt, cl, us};

@@ -996,15 +996,26 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
 // are no multiple of it (152 SMs: 76 clusters of 2, 36 of 4, 15 of 8).
 inline int cluster_slots(int sms, int c) { return c <= 2 ? sms / c : c == 4 ? sms * 95 / 400 : sms * 80 / 800; }
 
-// Microseconds of a call, fitted to sweeps of tile heights and K ranges on this GPU: `waves` tiles of kr K
-// blocks one after the other in a CTA, against the weights' way from HBM (each covers part of the
-// other), and the joining of S ranges.
-inline double plan_us(double waves, double kr, double block_us, double weight_bytes, int bn, int S, double ctas) {
-    const double cta = waves * (kr * block_us + 1.0), hbm = weight_bytes / 6.8e6;
-    return std::sqrt(cta * cta + hbm * hbm) + (S > 1 ? bn / 128.0 * (0.4 + 0.2 * S) + 0.01 * ctas : 0.0);
+// Microseconds of a call, up to a constant, fitted to sweeps on this GPU (29 shapes, 70 to 3000 tokens, both
+// scale types, every tile height and K range: the choice is within 0.7 % of the fastest on average).
+// `waves` tiles of kr K blocks one after the other in a CTA, each with `fixed` for its start and its
+// results, against the bytes of memory_bytes; each covers part of the other.
+inline double plan_us(double waves, double kr, double block_us, double fixed, double memory_bytes) {
+    const double cta = waves * (kr * block_us + fixed), hbm = memory_bytes / 6.8e6;
+    return std::sqrt(cta * cta + hbm * hbm);
 }
-// The copies of a K block's operands into one SM run at about 110 GB/s.
-inline double copy_us(int bn, int a_rows) { return (bn + a_rows) * 128.0 / 110e3; }
+// Weights, and results at a third of the reading rate: all CTAs write theirs at about the same time.
+inline double memory_bytes(const GemmCall& c, bool gated) {
+    const double n = c.lin->d.out_features, rows = gated ? 2.0 * ((c.lin->d.out_features + QB - 1) / QB * QB) : n;
+    return rows * c.lin->kt * 128.0 + 2.9 * c.M * n * (gated ? 1 : c.y_f32 ? 4 : 2);
+}
+// Joining S K ranges: sums of the tile's rows through distributed shared memory.
+inline double join_us(bool gated, int bn, int S, int M, double ctas) {
+    if (S == 1) return 0.0;
+    return bn / 128.0 * (gated ? 1.55 * std::min(M, BM) / BM : 0.157 + 0.178 * S) + (gated ? 0.0054 : 0.0084) * ctas;
+}
+// The copies of a K block's operands into one SM run at about 118 GB/s.
+inline double copy_us(int bn, int a_rows) { return (bn + a_rows) * 128.0 / 118e3; }
 
 struct Plan {
     int grp, bn, cluster, units, n_nt, S;

@@ -21,12 +21,13 @@ static Plan plan_plain(const GemmCall& c, const Args& a) {
         const int nt = (rows + bn - 1) / bn, groups = (a.kt + grp - 1) / grp;
         const long long units = (long long)mt * nt;
         if (units > 0x3FFFFFFF) continue;
-        const double drain = grp == 1 ? 0.48 : grp == 2 ? 0.43 : 0.08 + 0.0025 * bn;
+        const double drain = grp == 1 ? 0.42 : grp == 2 ? 0.246 : 0.15;
         for (int S = 1; S <= 8 && S <= groups; S *= 2) {
             if (S > 1 && ((bn != 128 && bn != 256) || units > cluster_slots(sms, S))) break;
             const double kr = std::min<double>(a.kt, (double)grp * ((groups + S - 1) / S));
             const double us = plan_us(S > 1 ? 1.0 : (double)((units + sms - 1) / sms), kr, std::max(drain, copy_us(bn, a.a_rows)),
-                                      (double)rows * a.kt * 128.0, bn, S, (double)units * S);
+                                      0.965, memory_bytes(c, false)) +
+                              join_us(false, bn, S, c.M, (double)units * S);
             if (best.bn == 0 || us < best_us) {
                 best_us = us;
                 best = Plan{grp, bn, S, (int)units, nt, S, us};

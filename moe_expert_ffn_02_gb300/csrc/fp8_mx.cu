@@ -331,12 +331,12 @@ MxPlan plan_fp8_mx(const GemmCall& c, bool gated) {
     const double mt = (c.M + BM - 1) / BM;
     const double rows = gated ? 2.0 * ((c.lin->d.out_features + QB - 1) / QB * QB) : (double)c.lin->rows;
     for (int b = 128; b <= 256; b += 128) {
-        const double units = mt * std::ceil(rows / b), kb = std::max(b / 256.0 * 0.3, copy_us(b, a.a_rows));
+        const double units = mt * std::ceil(rows / b), kb = std::max(b / 256.0 * 0.257, copy_us(b, a.a_rows));
         for (int k = 1; k <= 8 && k <= quads; k *= 2) {
             if (k > 1 && (units > cluster_slots(sms, k) || (gated && b == 128))) break;
             const double kr = std::min<double>(a.kt, 4.0 * ((quads + k - 1) / k));
-            const double us = plan_us(k > 1 ? 1.0 : std::ceil(units / sms), kr, kb, rows * a.kt * 128.0, b, k, units * k) +
-                              (gated && b == 128 ? 0.8 : 0.0);
+            const double us = plan_us(k > 1 ? 1.0 : std::ceil(units / sms), kr, kb, 0.734 + 0.19 * b / 256 + (gated ? 0.69 : 0.0), memory_bytes(c, gated)) +
+                              join_us(gated, b, k, c.M, units * k) + (gated && b == 128 ? 0.126 : 0.0);
             if (best.bn == 0 || us < best.us) best = MxPlan{b, k, us};
         }
     }
