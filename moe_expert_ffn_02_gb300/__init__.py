@@ -497,15 +497,22 @@ def _bad(message: str):
     raise MoeError(MOE_ERR_INVALID_ARG, message)
 
 
+_current = None          # torch's functions for the current device and a device's current stream, looked up once
+
+
 def _stream(dev: int) -> int:
     """The current torch stream's handle on device `dev`, which has to be the
     current device.  torch.cuda.current_stream() builds a Python object, which
     takes longer than a small operator's launch; the raw handle does not."""
-    import torch
-    if dev != torch.cuda.current_device():
+    global _current
+    if _current is None:
+        import torch
+        torch.cuda.init()
+        _current = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                    getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream))
+    if dev != _current[0]():
         _bad(f"the tensors are on device {dev}, which is not the current one")
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(dev) if raw is not None else torch.cuda.current_stream().cuda_stream
+    return _current[1](dev)
 
 
 def _dtypes():

@@ -124,6 +124,7 @@ MOE_EXPORT moe_status moe_linear_create(const moe_linear_desc* d, const moe_line
     const char* what = "device query";
     cudaError_t e = cudaGetDevice(&L->device);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&L->num_sms, cudaDevAttrMultiProcessorCount, L->device);
+    if (e == cudaSuccess) moe::plan_fp8_few(L);
     if (e == cudaSuccess) what = "allocating weights", e = cudaMalloc(&L->w, (size_t)L->kt * L->rows_pad * 128);
     if (e == cudaSuccess) what = "allocating scales", e = cudaMalloc(&L->sw, nsw * 4);
     if (e == cudaSuccess && d->scale_type == MOE_SCALE_E8M0)

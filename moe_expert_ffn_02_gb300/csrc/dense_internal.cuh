@@ -17,6 +17,7 @@ struct moe_linear {
     uint8_t* wsf;          // e8m0: [ceil(kt / 4)][ceil(rows_pad / 128)][512 B] scale-factor blocks of the image's rows
     uint32_t* dev_status;  // device status word
     uint32_t wait_limit;
+    int few_R, few_S, few_G;  // the few-token form's rows per tile, K ranges and K blocks per stage; few_R 0: it does not fit
 };
 
 namespace moe {
@@ -88,7 +89,8 @@ struct MxPlan {
 };
 MxPlan plan_fp8_mx(const GemmCall& c, bool gated);      // the form in which the tensor core applies e8m0 scales
 cudaError_t launch_fp8_mx(const GemmCall& c, bool gated, const MxPlan& p, cudaStream_t s);
-bool few_tokens(const GemmCall& c, bool gated);         // whether the few-token form takes the call
+void plan_fp8_few(moe_linear* L);                       // sets few_*, from the weights' shape
+bool few_tokens(const GemmCall& c);                     // whether the few-token form takes the call
 cudaError_t launch_fp8_few(const GemmCall& c, bool gated, cudaStream_t s);
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

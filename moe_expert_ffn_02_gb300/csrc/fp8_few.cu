@@ -554,7 +554,8 @@ static int longest_range(int kt, int S) {
 // 4.3 us with R = 128, S = 4 (224 CTAs) and 5.4 with R = 96, S = 2; 7168 x 4096, 64 tokens, 11.6 with R = 128,
 // S = 8 and 15.2 with R = 64, S = 4.  Clusters do not pack every SM: past 92 % of the slots a second wave
 // starts (7168 x 7168: 300 CTAs in clusters of four 12.1 us, 256 10.3).
-static FewPlan plan_few(const moe_linear* L, bool gated) {
+static FewPlan plan_few(const moe_linear* L) {
+    const bool gated = L->d.gated != 0;
     FewPlan best = {};
     double best_us = 0;
     const double slots = 2.0 * L->num_sms;
@@ -641,7 +642,7 @@ static cudaError_t launch_tokens(const GemmCall& c, const FewPlan& p, int kr, cu
 
 template <bool GATED>
 static cudaError_t launch_mode(const GemmCall& c, cudaStream_t s) {
-    const FewPlan p = plan_few(c.lin, GATED);
+    const FewPlan p = {c.lin->few_R, c.lin->few_S, c.lin->few_G};
     const int kr = longest_range(c.lin->kt, p.S);
     if (c.lin->d.scale_type == MOE_SCALE_F32) return launch_tokens<GATED, F32>(c, p, kr, s);
     return kr <= MX_MAX_KB ? launch_tokens<GATED, MX>(c, p, kr, s) : launch_tokens<GATED, E8>(c, p, kr, s);
@@ -649,9 +650,14 @@ static cudaError_t launch_mode(const GemmCall& c, cudaStream_t s) {
 
 }  // namespace few
 
-bool few_tokens(const GemmCall& c, bool gated) {
-    return c.M <= few::MAX_M && few::plan_few(c.lin, gated).R != 0;
+void plan_fp8_few(moe_linear* L) {
+    const few::FewPlan p = few::plan_few(L);
+    L->few_R = p.R;
+    L->few_S = p.S;
+    L->few_G = p.G;
 }
+
+bool few_tokens(const GemmCall& c) { return c.M <= few::MAX_M && c.lin->few_R != 0; }
 
 cudaError_t launch_fp8_few(const GemmCall& c, bool gated, cudaStream_t s) {
     return gated ? few::launch_mode<true>(c, s) : few::launch_mode<false>(c, s);

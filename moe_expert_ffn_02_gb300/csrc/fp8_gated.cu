@@ -49,7 +49,7 @@ static Plan plan_gated(const GemmCall& c, const Args& a) {
 
 cudaError_t launch_fp8_gated(const GemmCall& c, cudaStream_t s) {
     using namespace dg;
-    if (few_tokens(c, true)) return launch_fp8_few(c, true, s);
+    if (few_tokens(c)) return launch_fp8_few(c, true, s);
     Args a = base_args(c);
     const Plan p = plan_gated(c, a);
     if (!p.bn) return cudaErrorInvalidValue;

@@ -41,7 +41,7 @@ static Plan plan_plain(const GemmCall& c, const Args& a) {
 
 cudaError_t launch_fp8_linear(const GemmCall& c, cudaStream_t s) {
     using namespace dg;
-    if (few_tokens(c, false)) return launch_fp8_few(c, false, s);
+    if (few_tokens(c)) return launch_fp8_few(c, false, s);
     Args a = base_args(c);
     const Plan p = plan_plain(c, a);
     if (!p.bn) return cudaErrorInvalidValue;
