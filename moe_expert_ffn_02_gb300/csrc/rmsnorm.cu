@@ -11,14 +11,15 @@
 // for bf16 streams with codes only.  A lane holds 8 consecutive channels per
 // vector, so 16 lanes hold one scale group and its amax takes four shuffles.
 //
-// Three forms.  Few rows: one CTA per row, as many threads as vectors (latency
-// counts; a row of 7168 takes 2.7 us).  Many rows: persistent CTAs with a ring of
+// Four forms.  Few rows: one CTA per row, as many threads as vectors (latency
+// counts; a row of 7168 takes 2.5 us).  Many rows: persistent CTAs with a ring of
 // rows in shared memory, filled by bulk copies that run ahead of the
 // arithmetic; loading straight into registers leaves HBM idle while a CTA waits
 // for its row's sum (8192 x 7168 bf16: 102 us, now 65 to 67, 0.92 of the copy
 // bandwidth).  Rows off the 16-byte grid: contiguous two- and four-byte accesses,
 // a warp per scale group, and the ring with each row's 16-byte window (8192 x 7001
 // bf16: 143 us; the two-byte accesses bound it; 8000 x 3001 fp32: 79 us, 0.76).
+// Short rows (256 channels at most): a warp per row.
 #include "dense_internal.cuh"
 
 #include <algorithm>
