@@ -571,6 +571,12 @@ class Fp8Tensor:
         t._bind(_on_strides(q), _on_strides(s), scale)
         return t
 
+    def first(self, rows: int):
+        """The first rows as an Fp8Tensor over the same storage."""
+        t = type(self).__new__(type(self))
+        t._bind(self.q[:rows], self.s[:, :rows], self.scale)
+        return t
+
     def dequantise(self):
         """The values the codes stand for, fp32."""
         return self.q.float() * self.s.float().t().repeat_interleave(128, 1)[:, :self.cols]
@@ -723,25 +729,31 @@ class Fp8GatedLinear(_Weights):
 
 
 class DenseFfn:
-    """The dense FFN half of a pre-norm block, for up to max_rows tokens:
+    """The dense FFN half of a pre-norm block:
 
         residual += x;  y = down(SiLU(gate(n)) * up(n)),  n = norm(residual)
 
     The residual is updated in place; the caller adds y to it with the next
     norm.  The intermediate E4M3 buffers are kept between calls, so calls of
-    one object belong on one stream at a time."""
+    one object belong on one stream at a time.  They are made per power of two
+    of rows and never freed while the object lives: a captured graph may go on
+    using them whatever sizes are called in between."""
 
     def __init__(self, norm: RmsNorm, gate_up: Fp8GatedLinear, down: Fp8Linear):
         if gate_up.in_features != norm.cols or down.in_features != gate_up.out_features or gate_up.scale != down.scale:
             _bad("norm, gate_up and down do not fit together")
         self.norm, self.gate_up, self.down = norm, gate_up, down
-        self._buf = {}
+        self._store, self._views = {}, {}
 
     def buffers(self, rows: int):
-        if rows not in self._buf:
-            self._buf = {rows: (Fp8Tensor(rows, self.norm.cols, self.gate_up.scale, self.gate_up.device),
-                                Fp8Tensor(rows, self.gate_up.out_features, self.gate_up.scale, self.gate_up.device))}
-        return self._buf[rows]
+        got = self._views.get(rows)
+        if got is None:
+            cap = 1 << max(rows - 1, 0).bit_length()
+            if cap not in self._store:
+                self._store[cap] = [Fp8Tensor(cap, n, self.gate_up.scale, self.gate_up.device)
+                                    for n in (self.norm.cols, self.gate_up.out_features)]
+            got = self._views[rows] = [t.first(rows) for t in self._store[cap]]
+        return got
 
     def __call__(self, x, residual, y):
         a, h = self.buffers(x.shape[0])

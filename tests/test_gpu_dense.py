@@ -13,6 +13,10 @@ Tolerances, derived from the arithmetic (u = 2^-24, half an fp32 ulp):
 - codes: half an E4M3 step of the quotient, 2^-4 relative for normal codes and
   2^-10 absolute below them, plus the quotient's own error.
 """
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -412,6 +416,26 @@ def test_the_operators_together(moe, scale, rows):
     assert torch.linalg.norm(y.double() - exact) <= 0.1 * torch.linalg.norm(exact)
 
 
+def test_a_graph_outlives_calls_of_other_sizes(moe):
+    """A captured call of the dense FFN keeps its buffers when the same object is called with more rows."""
+    ffn, _ = block(moe)
+    x, res = randn((5, 512), 94, dtype=torch.bfloat16), randn((5, 512), 95, dtype=torch.bfloat16)
+    start, y = res.clone(), torch.empty(5, 512, dtype=torch.bfloat16, device="cuda")
+    want = ffn(x, res, y).clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ffn(x, res, y)
+    for rows in (300, 6, 40):
+        big = randn((rows, 512), 96, dtype=torch.bfloat16)
+        ffn(big, big.clone(), torch.empty_like(big))
+        junk = [torch.full((rows, 1024), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        res.copy_(start)
+        y.zero_()
+        g.replay()
+        assert torch.equal(y, want)
+        del junk
+
+
 def test_another_stream_and_a_graph(moe):
     """Work goes to the current stream, in order with it, and can be captured."""
     ffn, _ = block(moe)
@@ -492,3 +516,13 @@ def test_refusals(moe):
     refused(lambda: moe.moe_linear_forward(lin.handle, short, 4, y.data_ptr(), 128, moe.F32))
     assert lin.device_status() == (0, 0) and gated.device_status() == (0, 0)
     lin(a, y)          # a refused call leaves the handle usable
+
+
+@pytest.mark.parametrize("tokens", [8, 100])
+def test_the_example_runs(moe, tokens):
+    """The dense FFN and the expert layer in one captured step; the script checks its residual stream itself."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, os.path.join(root, "examples", "transformer_ffn.py"), "--tokens", str(tokens), "--steps", "3"],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert "us a step" in r.stdout
