@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
                 }
             }
             if constexpr (GATED) epi_gated<HALF>(a, ctx, acc, m0, n0, valid, dead);
-            else if (live && !dead) epi_plain<HALF>(maps.y, a, ctx, acc, m0, n0, valid);
+            else if (live && !dead) epi_plain<HALF, false>(maps.y, a, ctx, acc, m0, n0, valid);
         }
     }
     if (warp < CTRL_WARPS) {

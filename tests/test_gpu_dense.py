@@ -343,7 +343,7 @@ def test_linear_of_many_rows(moe, m, k, n, scale, dtype):
     lin, ref = check_linear(moe, m, k, n, scale, dtype, seed=56)
     aq, a_s = rows_fp8(randn((m, k), 56), scale)
     a = moe.Fp8Tensor.from_parts(aq, a_s)
-    for width, off in ((n + 24, 8), (n + 3, 1)):
+    for width, off in ((n + 24, 8), (n + 3, 1), (n + 6, 1), (n + 6, 2)):
         store = torch.full((m + 2, width), 7.0, dtype=dtype, device="cuda")
         assert torch.equal(lin(a, store[1:m + 1, off:off + n]), ref)
         keep = torch.ones(m + 2, width, dtype=torch.bool, device="cuda")
