@@ -18,7 +18,7 @@
 // for its row's sum (8192 x 7168 bf16: 102 us, now 65 to 67, 0.92 of the copy
 // bandwidth).  Rows off the 16-byte grid: contiguous two- and four-byte accesses,
 // a warp per scale group, and the ring with each row's 16-byte window (8192 x 7001
-// bf16: 143 us; the two-byte accesses bound it; 8000 x 3001 fp32: 79 us, 0.76).
+// bf16 141 us, without residual 93, fp32 133; bound by its instructions and two-byte accesses).
 // Short rows (256 channels at most): a warp per row.
 #include "dense_internal.cuh"
 
@@ -277,9 +277,19 @@ __global__ void __launch_bounds__(512, VPT > 2 ? 1 : 2) rmsnorm_stream_kernel(No
 // of 4 x 32 channels per warp.
 template <int GPW>
 struct Narrow {
-    float v[GPW][4];
+    static constexpr bool KEEP_W = GPW <= 4;               // this thread's weights in registers
+    float v[GPW][4], w[KEEP_W ? GPW : 1][4];
     int warp, warps;
     __device__ __forceinline__ int channel(int i, int k) const { return (warp + i * warps) * QB + 32 * k + (threadIdx.x & 31); }
+
+    __device__ __forceinline__ void load_weights(const NormArgs& a) {
+        if constexpr (KEEP_W) {
+#pragma unroll
+            for (int i = 0; i < GPW; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[i][k] = channel(i, k) < a.cols ? a.w[channel(i, k)] : 0.f;
+        }
+    }
 
     // v = x + r, in place of r's row where ro is given; the sum of squares of this thread's part.
     template <typename TX, typename TR>
@@ -310,43 +320,55 @@ struct Narrow {
         return ss;
     }
 
+    // The groups' chains (largest of 32 lanes, scale, codes) run side by side.
     template <typename TX>
     __device__ __forceinline__ void finish(const NormArgs& a, int64_t row, float rstd) {
+        float am[GPW];
 #pragma unroll
         for (int i = 0; i < GPW; ++i) {
-            float am = 0.f;
+            am[i] = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int c = channel(i, k);
                 if (c < a.cols) {
-                    v[i][k] = v[i][k] * rstd * a.w[c];
+                    v[i][k] = v[i][k] * rstd * (KEEP_W ? w[KEEP_W ? i : 0][k] : a.w[c]);
                     if (a.y) static_cast<TX*>(a.y)[row * a.ldy + c] = from_f32<TX>(v[i][k]);
                 }
-                am = max_nan(am, fabsf(v[i][k]));
+                am[i] = max_nan(am[i], fabsf(v[i][k]));
             }
-            if (a.q) {                                 // uniform: every lane takes part in the shuffles
+        }
+        if (!a.q) return;                                  // uniform: every lane takes part in the shuffles
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
-                uint32_t held;
-                const float is = inv_scale(group_scale(am, a.e8m0, held));
-                // lane l holds channels l, 32 + l, ..; it stores channels 4 l .. 4 l + 3, four bytes at a time
-                const uint32_t mine = pack4_e4m3(v[i][0] * is, v[i][1] * is, v[i][2] * is, v[i][3] * is);
-                const int lane = threadIdx.x & 31, g = warp + i * warps, c = g * QB + 4 * lane;
-                uint32_t out = 0;
+        for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    out |= ((__shfl_sync(0xFFFFFFFFu, mine, (4 * lane + j) & 31) >> (8 * (lane >> 3))) & 0xFFu) << (8 * j);
-                uint8_t* q = a.q + row * a.ldq + c;
-                if (c + 4 <= a.cols) {
-                    *reinterpret_cast<uint32_t*>(q) = out;
-                } else {
-                    for (int j = 0; c + j < a.cols; ++j) q[j] = (uint8_t)(out >> (8 * j));
-                }
-                if ((threadIdx.x & 31) == 0 && g * QB < a.cols) {
-                    const int64_t at = (int64_t)g * a.lds + row;
-                    if (a.e8m0) static_cast<uint8_t*>(a.s)[at] = (uint8_t)held;
-                    else static_cast<uint32_t*>(a.s)[at] = held;
-                }
+            for (int i = 0; i < GPW; ++i) am[i] = max_nan(am[i], __shfl_xor_sync(0xFFFFFFFFu, am[i], o));
+        uint32_t held[GPW], mine[GPW], out[GPW];
+#pragma unroll
+        for (int i = 0; i < GPW; ++i) {
+            const float is = inv_scale(group_scale(am[i], a.e8m0, held[i]));
+            mine[i] = pack4_e4m3(v[i][0] * is, v[i][1] * is, v[i][2] * is, v[i][3] * is);
+            out[i] = 0;
+        }
+        // lane l holds channels l, 32 + l, ..; it stores channels 4 l .. 4 l + 3, four bytes at a time
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < GPW; ++i)
+                out[i] |= ((__shfl_sync(0xFFFFFFFFu, mine[i], (4 * lane + j) & 31) >> (8 * (lane >> 3))) & 0xFFu) << (8 * j);
+#pragma unroll
+        for (int i = 0; i < GPW; ++i) {
+            const int g = warp + i * warps, c = g * QB + 4 * lane;
+            uint8_t* q = a.q + row * a.ldq + c;
+            if (c + 4 <= a.cols) {
+                *reinterpret_cast<uint32_t*>(q) = out[i];
+            } else {
+                for (int j = 0; c + j < a.cols; ++j) q[j] = (uint8_t)(out[i] >> (8 * j));
+            }
+            if (lane == 0 && g * QB < a.cols) {
+                const int64_t at = (int64_t)g * a.lds + row;
+                if (a.e8m0) static_cast<uint8_t*>(a.s)[at] = (uint8_t)held[i];
+                else static_cast<uint32_t*>(a.s)[at] = held[i];
             }
         }
     }
@@ -357,11 +379,12 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_narrow_kernel(NormA
     __shared__ float part[32];
     const RowOf at = row_of<WARP>();
     pdl_trigger();
-    pdl_wait();
-    if (WARP && at.row >= a.rows) return;
     Narrow<GPW> n;
     n.warp = at.warp;
     n.warps = at.warps;
+    n.load_weights(a);
+    pdl_wait();
+    if (WARP && at.row >= a.rows) return;
     const float ss = n.template take<TX, TR>(a, static_cast<const TX*>(a.x) + at.row * a.ldx,
                                              a.r ? static_cast<const TR*>(a.r) + at.row * a.ldr : nullptr,
                                              a.ro ? static_cast<TR*>(a.ro) + at.row * a.ldro : nullptr);
@@ -394,6 +417,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_narrow_stream_kernel(NormArgs a,
         fence_mbar_init();
     }
     pdl_trigger();
+    Narrow<GPW> n;
+    n.warp = threadIdx.x >> 5;
+    n.warps = blockDim.x >> 5;
+    n.load_weights(a);
     __syncthreads();
     pdl_wait();
     auto x_window = [&](int64_t row) { return window_of(a.x, a.ldx, row, a.rows, a.cols, (int)sizeof(TX)); };
@@ -409,9 +436,6 @@ __global__ void __launch_bounds__(1024) rmsnorm_narrow_stream_kernel(NormArgs a,
     if (threadIdx.x == 0)
         for (int s = 0; s < stages && (int64_t)blockIdx.x + (int64_t)s * gridDim.x < a.rows; ++s)
             fetch((int64_t)blockIdx.x + (int64_t)s * gridDim.x, s);
-    Narrow<GPW> n;
-    n.warp = threadIdx.x >> 5;
-    n.warps = blockDim.x >> 5;
     int st = 0, par = 0;
     uint32_t phase = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -507,10 +531,10 @@ cudaError_t pick(const NormArgs& a, bool vec, cudaStream_t s) {
         return go<TX, TR, 1>(a, s);
     }
     const int groups = (a.cols + QB - 1) / QB;
-    const int gpw = warp ? groups : groups <= 8 ? 1 : groups <= 64 ? 2 : groups <= 128 ? 4 : 8;
+    const int gpw = warp ? groups : groups <= 8 ? 1 : groups <= 16 ? 2 : groups <= 128 ? 4 : 8;
     int stages = 0, ctas = 0;
     if (!warp && gpw > 1) {
-        const int threads = (groups + gpw - 1) / gpw * 32, per_sm = std::max(1, std::min(4, 2048 / threads));
+        const int threads = (groups + gpw - 1) / gpw * 32, per_sm = std::max(1, std::min(8, 1024 / threads));
         stages = std::min(MAX_ROWS, (int)(std::min(RING_BYTES, 2 * RING_BYTES / per_sm) / (xb + rb)));
         ctas = per_sm * sms;
         if (stages < 2 || a.rows < 2 * ctas) stages = 0;
