@@ -14,7 +14,7 @@
 // and blocks are added in K order, so a token's result does not depend on how
 // many others are in the batch.  One SM takes at most about 70 GB/s and 100 of
 // them saturate HBM (measured with bulk copies alone: 64 CTAs 4.4 TB/s, 96 6.3,
-// 112 6.7, 152 6.8), hence the rule: as many CTAs as there are SMs.
+// 112 6.7, 152 6.8); two CTAs per SM with short ranges also shorten the chain of a call.
 //
 // A stage is a group of G K blocks (R rows of weights, the tokens, their
 // scales): waiting on or arriving at an mbarrier takes a warp about 150 cycles
