@@ -2,11 +2,11 @@
 // core applies the scales itself (tcgen05.mma kind::mxf8f6f4, block_scale), so
 // a whole K range accumulates in tensor memory and is drained once.
 //
-// Bound by the tensor core.  The fp32-scale form has to drain and scale 128 x 256
+// Bound by the SM: a K block's 48 KB are written to shared memory and read by the MMAs in about 680 cycles,
+// 512 of them MMA work (0.355 us a block with 19 CTAs as with 152).  The fp32-scale form has to drain and scale 128 x 256
 // partial sums for every 512 cycles of MMA work (about 780 in all); here a tile
 // costs its MMAs plus one drain: 4096 x 7168 x 7168 131 us (3.2 PFLOP/s, 0.85 of twice the bf16 rate),
-// gated 8192 x 7168 x 2048 144 us (0.89); the tensor pipe is busy 70 and 73 % of the time at the
-// clock that the power limit leaves.  The hardware takes one power-of-two factor per
+// gated 8192 x 7168 x 2048 144 us (0.89); the tensor pipe is busy 70 and 73 % of the time.  The hardware takes one power-of-two factor per
 // row and 32 channels: the four K32 steps of a 128-channel block use the same
 // byte, and the four bytes of a 32-bit word hold four consecutive K blocks (a
 // quad), selected by the instruction's scale-factor id.
