@@ -209,12 +209,6 @@ __global__ void __launch_bounds__(512, VPT > 2 ? 1 : 2) rmsnorm_stream_kernel(No
         fence_mbar_init();
     }
     pdl_trigger();
-    float w[VPT][8];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * 8;
-        if (c < a.cols) load8<float>(a.w + c, w[i]);
-    }
     __syncthreads();
     pdl_wait();
     auto fetch = [&](int64_t row, int st) {
@@ -225,6 +219,12 @@ __global__ void __launch_bounds__(512, VPT > 2 ? 1 : 2) rmsnorm_stream_kernel(No
     if (threadIdx.x == 0)
         for (int s = 0; s < stages && (int64_t)blockIdx.x + (int64_t)s * gridDim.x < rows; ++s)
             fetch((int64_t)blockIdx.x + (int64_t)s * gridDim.x, s);
+    float w[VPT][8];                           // the caller's memory, like the rows: read after the wait, under the first copies
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * 8;
+        if (c < a.cols) load8<float>(a.w + c, w[i]);
+    }
     int st = 0, par = 0;
     uint32_t phase = 0;
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
@@ -382,9 +382,9 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_narrow_kernel(NormA
     Narrow<GPW> n;
     n.warp = at.warp;
     n.warps = at.warps;
-    n.load_weights(a);
     pdl_wait();
     if (WARP && at.row >= a.rows) return;
+    n.load_weights(a);
     const float ss = n.template take<TX, TR>(a, static_cast<const TX*>(a.x) + at.row * a.ldx,
                                              a.r ? static_cast<const TR*>(a.r) + at.row * a.ldr : nullptr,
                                              a.ro ? static_cast<TR*>(a.ro) + at.row * a.ldro : nullptr);
@@ -420,7 +420,6 @@ __global__ void __launch_bounds__(1024) rmsnorm_narrow_stream_kernel(NormArgs a,
     Narrow<GPW> n;
     n.warp = threadIdx.x >> 5;
     n.warps = blockDim.x >> 5;
-    n.load_weights(a);
     __syncthreads();
     pdl_wait();
     auto x_window = [&](int64_t row) { return window_of(a.x, a.ldx, row, a.rows, a.cols, (int)sizeof(TX)); };
@@ -436,6 +435,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_narrow_stream_kernel(NormArgs a,
     if (threadIdx.x == 0)
         for (int s = 0; s < stages && (int64_t)blockIdx.x + (int64_t)s * gridDim.x < a.rows; ++s)
             fetch((int64_t)blockIdx.x + (int64_t)s * gridDim.x, s);
+    n.load_weights(a);
     int st = 0, par = 0;
     uint32_t phase = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {

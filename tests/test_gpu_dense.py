@@ -216,6 +216,23 @@ def test_norm_zeros_tiny_values_and_non_numbers(moe, scale):
     assert (out1.s.float() == 1).all() and (out1.q.float() == 0).all()
 
 
+@pytest.mark.parametrize("rows,cols", [(1, 1032), (2500, 1032), (700, 128), (3, 1033), (2500, 1033), (700, 131)])
+def test_norm_weight_written_by_the_kernel_before(moe, rows, cols):
+    """The kernel ahead on the stream, which lets the norm start early, writes the norm's weight: every form waits for it."""
+    k = 33000
+    lin = moe.Fp8Linear(*blocks_fp8(randn((cols, k), 11, 0.02), "f32"))
+    a = moe.Fp8Tensor.from_parts(*rows_fp8(randn((1, k), 12), "f32"))
+    x, weight = randn((rows, cols), 13), torch.empty(1, cols, device="cuda")
+    norm, got, want = moe.RmsNorm(weight[0]), torch.empty_like(x), torch.empty_like(x)
+    moe.RmsNorm(lin(a, torch.empty_like(weight))[0])(x, y=want)
+    for _ in range(3):
+        weight.fill_(float("nan"))
+        torch.cuda.synchronize()
+        lin(a, weight)
+        norm(x, y=got)
+        assert torch.equal(got, want)
+
+
 def test_norm_offsets_past_32_bits(moe):
     cols, ld = 256, 2 ** 31 + 64
     big = torch.empty(ld + cols, dtype=torch.bfloat16, device="cuda")
