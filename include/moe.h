@@ -383,6 +383,16 @@ moe_status moe_add_rmsnorm(const moe_rmsnorm_args* args, void* stream);
 /* As moe_get_device_status, for the norms run on the current device. */
 moe_status moe_rmsnorm_device_status(void* stream, uint32_t* flags);
 
+/* As moe_set_wait_limit, for the norms that this process calls from now on.
+ * What a call whose wait expired has written is right; the row and the rows
+ * after it in its thread block are left out (of that row's res_out, perhaps
+ * only a part). */
+moe_status moe_rmsnorm_set_wait_limit(uint32_t microseconds);
+
+/* Test hook: in the next norm of many rows that copies them to shared memory
+ * first, the wait for one row expires. */
+moe_status moe_rmsnorm_debug_timeout(void);
+
 /* Weights of a dense FP8 projection, copied into the library's tile layout
  * once; the caller may free its buffers afterwards.  Row-major E4M3FN
  * [out_features][in_features] with one scale per 128 x 128 block,

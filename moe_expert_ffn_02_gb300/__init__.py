@@ -27,7 +27,7 @@ __all__ = [
     "moe_forward_layers", "smallep_groups", "moe_create_ex", "moe_tiles_bytes", "moe_tiles_load", "moe_forward_tiles",
     "CREATE_HOST_TILES", "library_path", "load", "Layer", "LayerStackGraph", "StreamedStack",
     "MoeFp8Matrix", "MoeRmsnormArgs", "MoeLinearDesc", "MoeLinearWeights", "BF16", "F32", "SCALE_F32", "SCALE_E8M0",
-    "moe_add_rmsnorm", "moe_rmsnorm_device_status", "moe_linear_create", "moe_linear_destroy", "moe_linear_forward", "moe_gated_linear_forward",
+    "moe_add_rmsnorm", "moe_rmsnorm_device_status", "moe_rmsnorm_set_wait_limit", "moe_rmsnorm_debug_timeout", "moe_linear_create", "moe_linear_destroy", "moe_linear_forward", "moe_gated_linear_forward",
     "moe_linear_device_status", "Fp8Tensor", "RmsNorm", "Fp8Linear", "Fp8GatedLinear", "DenseFfn",
 ]
 
@@ -134,6 +134,8 @@ def load(build_if_missing: bool = False):
             "moe_profile_read": ([vp, ctypes.POINTER(ctypes.c_float), i32], st),
             "moe_add_rmsnorm": ([ctypes.POINTER(MoeRmsnormArgs), vp], st),
             "moe_rmsnorm_device_status": ([vp, ctypes.POINTER(u32)], st),
+            "moe_rmsnorm_set_wait_limit": ([u32], st),
+            "moe_rmsnorm_debug_timeout": ([], st),
             "moe_linear_create": ([ctypes.POINTER(MoeLinearDesc), ctypes.POINTER(MoeLinearWeights), vp,
                                    ctypes.POINTER(vp)], st),
             "moe_linear_destroy": ([vp], st),
@@ -337,6 +339,15 @@ def moe_rmsnorm_device_status(stream: int = 0):
     f = ctypes.c_uint32()
     st = load().moe_rmsnorm_device_status(stream, ctypes.byref(f))
     return int(st), int(f.value)
+
+
+def moe_rmsnorm_set_wait_limit(microseconds: int) -> None:
+    _check(load().moe_rmsnorm_set_wait_limit(microseconds))
+
+
+def moe_rmsnorm_debug_timeout() -> None:
+    """In the next norm of many rows that copies them to shared memory first, the wait for one row expires."""
+    _check(load().moe_rmsnorm_debug_timeout())
 
 
 def moe_linear_create(desc: MoeLinearDesc, weights: MoeLinearWeights, stream: int = 0) -> int:

@@ -225,3 +225,14 @@ MOE_EXPORT moe_status moe_rmsnorm_device_status(void* stream, uint32_t* flags) {
     cudaError_t e = moe::norm_status_word(&word);
     return e != cudaSuccess ? cuda_fail(e, "the norm's status word") : read_status(word, stream, flags);
 }
+
+MOE_EXPORT moe_status moe_rmsnorm_set_wait_limit(uint32_t microseconds) {
+    if (microseconds == 0) return fail(MOE_ERR_INVALID_ARG, "limit must be positive");
+    moe::norm_set_wait_limit(microseconds);
+    return MOE_OK;
+}
+
+MOE_EXPORT moe_status moe_rmsnorm_debug_timeout(void) {
+    moe::norm_plant_timeout();
+    return MOE_OK;
+}

@@ -22,6 +22,10 @@ struct moe_linear {
 
 namespace moe {
 
+// Limit of the waits that let a CTA's own copies and MMAs finish before it leaves, whatever the limit of the
+// others: leaving earlier would let them land in memory that is no longer its own.
+constexpr uint32_t LANDING_LIMIT_US = 2000000u;
+
 // Scale of a quantisation group from its largest magnitude, shared by the
 // norm and the gated projection.  f32: amax / 448.  e8m0: the smallest power
 // of two that is at least amax / 448, held as its biased exponent; found from
@@ -79,6 +83,8 @@ struct GemmCall {
 
 cudaError_t launch_rmsnorm(const moe_rmsnorm_args* a, cudaStream_t s);
 cudaError_t norm_status_word(uint32_t** p);             // the current device's
+void norm_set_wait_limit(uint32_t us);
+void norm_plant_timeout();
 cudaError_t launch_linear_repack(const moe_linear* L, const uint8_t* w, const void* s, const uint8_t* wu,
                                  const void* su, cudaStream_t st);
 cudaError_t launch_fp8_linear(const GemmCall& c, cudaStream_t s);

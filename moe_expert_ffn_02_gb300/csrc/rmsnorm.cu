@@ -23,12 +23,14 @@
 #include "dense_internal.cuh"
 
 #include <algorithm>
+#include <atomic>
 
 namespace moe {
 namespace {
 
 __device__ uint32_t g_status;                // MOE_DEV_WAIT_TIMEOUT once a wait gave up, per device
-constexpr uint32_t WAIT_LIMIT_US = 2000000;
+std::atomic<uint32_t> g_wait_limit{LANDING_LIMIT_US};
+std::atomic<bool> g_plant{false};            // moe_rmsnorm_debug_timeout, for the next ring-form call
 
 constexpr int MAX_ROWS = 16;                 // ring stages, at most
 constexpr int RING_BYTES = 96 * 1024;        // per CTA; two CTAs share an SM
@@ -45,6 +47,13 @@ struct NormArgs {
     void* s;
     int64_t ldx, ldr, ldro, ldy, ldq, lds;
     bool e8m0;
+};
+
+struct RingArgs {
+    int stages;
+    uint32_t xb, rb;           // bytes of a stage's x and r
+    uint32_t wait_limit;
+    bool plant;                // moe_rmsnorm_debug_timeout: the first CTA's second row never counts as copied
 };
 
 template <typename T>
@@ -196,17 +205,38 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(NormArgs a) 
 }
 
 // Many rows.  Row i of this CTA lies in stage i % stages: x, then r.  Every thread has read its
-// part of a stage before the barrier in row_rstd, so the stage is refilled right after it.
+// part of a stage before the barrier in row_rstd, so the stage is refilled right after it.  A thread
+// that gave up waiting for a row stores nothing of it, and raises the row's flag before that barrier;
+// after it all threads see the flag and leave.  Sums and flags have two buffers, because the next
+// row's may come early (a flag raised at any time let threads of one row decide differently).
+
+// The ring's barriers; the planted one expects an arrival more than it gets.
+__device__ __forceinline__ void init_ring(uint64_t* full, const RingArgs& ra) {
+    for (int s = 0; s < ra.stages; ++s) mbar_init(&full[s], ra.plant && blockIdx.x == 0 && s == 1 ? 2 : 1);
+    fence_mbar_init();
+}
+
+// Thread 0, before a CTA that gave up at `row` in stage st leaves: the copies of that row and of those requested
+// after it land.
+__device__ __forceinline__ void land(uint64_t* full, const RingArgs& ra, int64_t row, int rows, int st, uint32_t phase) {
+    if (ra.plant && blockIdx.x == 0) mbar_arrive(&full[1]);
+    for (int s = 0; s < ra.stages && row < rows; ++s, row += gridDim.x) {
+        mbar_wait_bounded(&full[st], phase, LANDING_LIMIT_US, &g_status, nullptr);
+        if (++st == ra.stages) { st = 0; phase ^= 1u; }
+    }
+}
+
 template <typename TX, typename TR, int VPT>
-__global__ void __launch_bounds__(512, VPT > 2 ? 1 : 2) rmsnorm_stream_kernel(NormArgs a, int rows, int stages, uint32_t xb, uint32_t rb) {
+__global__ void __launch_bounds__(512, VPT > 2 ? 1 : 2) rmsnorm_stream_kernel(NormArgs a, RingArgs ra) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ float part[2][32];
     __shared__ uint64_t full[MAX_ROWS];
-    __shared__ volatile int abort_flag;
+    __shared__ volatile int abort_flag, gave_up[2];
+    const int rows = a.rows, stages = ra.stages;
+    const uint32_t xb = ra.xb, rb = ra.rb;
     if (threadIdx.x == 0) {
-        abort_flag = 0;
-        for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
-        fence_mbar_init();
+        abort_flag = gave_up[0] = gave_up[1] = 0;
+        init_ring(full, ra);
     }
     pdl_trigger();
     __syncthreads();
@@ -228,33 +258,38 @@ __global__ void __launch_bounds__(512, VPT > 2 ? 1 : 2) rmsnorm_stream_kernel(No
     int st = 0, par = 0;
     uint32_t phase = 0;
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-        // a wait that runs out raises the flag; the row's garbage is dropped after the barrier below
-        mbar_wait_bounded(&full[st], phase, WAIT_LIMIT_US, &g_status, &abort_flag);
-        const TX* x = reinterpret_cast<const TX*>(ring + (size_t)st * (xb + rb));
-        const TR* r = reinterpret_cast<const TR*>(ring + (size_t)st * (xb + rb) + xb);
         float v[VPT][8];
         float ss = 0.f;
+        if (mbar_wait_bounded(&full[st], phase, ra.wait_limit, &g_status, &abort_flag)) {
+            const TX* x = reinterpret_cast<const TX*>(ring + (size_t)st * (xb + rb));
+            const TR* r = reinterpret_cast<const TR*>(ring + (size_t)st * (xb + rb) + xb);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * 8;
-            if (c < a.cols) {
-                load8<TX>(x + c, v[i]);
-                if (rb) {
-                    float u[8];
-                    load8<TR>(r + c, u);
+            for (int i = 0; i < VPT; ++i) {
+                const int c = (i * blockDim.x + threadIdx.x) * 8;
+                if (c < a.cols) {
+                    load8<TX>(x + c, v[i]);
+                    if (rb) {
+                        float u[8];
+                        load8<TR>(r + c, u);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[i][e] += u[e];
-                    if (a.ro) store8<TR>(static_cast<TR*>(a.ro) + row * a.ldro + c, v[i]);
+                        for (int e = 0; e < 8; ++e) v[i][e] += u[e];
+                        if (a.ro) store8<TR>(static_cast<TR*>(a.ro) + row * a.ldro + c, v[i]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
                 }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
             }
+        } else {
+            gave_up[par] = 1;
         }
-        const float rstd = row_rstd<false>(a, ss, part[par]);     // two buffers: the next row's sums may come early
-        if (abort_flag) break;
+        const float rstd = row_rstd<false>(a, ss, part[par]);
+        if (gave_up[par]) {                    // seen by every thread, or by none
+            if (threadIdx.x == 0) land(full, ra, row, rows, st, phase);
+            break;
+        }
         par ^= 1;
         const int64_t next = row + (int64_t)stages * gridDim.x;
         if (threadIdx.x == 0 && next < rows) fetch(next, st);
@@ -265,11 +300,6 @@ __global__ void __launch_bounds__(512, VPT > 2 ? 1 : 2) rmsnorm_stream_kernel(No
             finish8<TX>(a, row, c, c < a.cols, v[i], w[i], rstd);
         }
     }
-    if (abort_flag && threadIdx.x == 0)                    // copies in flight land before the CTA leaves
-        for (int s = 0; s < stages; ++s) {
-            mbar_wait_bounded(&full[st], phase, WAIT_LIMIT_US, &g_status, nullptr);
-            if (++st == stages) { st = 0; phase ^= 1u; }
-        }
 }
 
 // Rows that do not lie on 16-byte boundaries (odd widths, views).  A warp takes whole scale groups, its
@@ -406,15 +436,16 @@ __device__ __forceinline__ Window window_of(const void* base, int64_t ld, int64_
 }
 
 template <typename TX, typename TR, int GPW>
-__global__ void __launch_bounds__(1024) rmsnorm_narrow_stream_kernel(NormArgs a, int stages, uint32_t xb, uint32_t rb) {
+__global__ void __launch_bounds__(1024) rmsnorm_narrow_stream_kernel(NormArgs a, RingArgs ra) {
     extern __shared__ __align__(128) uint8_t ring[];       // [stage][xb | rb]: room for the largest windows
     __shared__ float part[2][32];
     __shared__ uint64_t full[MAX_ROWS];
-    __shared__ volatile int abort_flag;
+    __shared__ volatile int abort_flag, gave_up[2];
+    const int stages = ra.stages;
+    const uint32_t xb = ra.xb, rb = ra.rb;
     if (threadIdx.x == 0) {
-        abort_flag = 0;
-        for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
-        fence_mbar_init();
+        abort_flag = gave_up[0] = gave_up[1] = 0;
+        init_ring(full, ra);
     }
     pdl_trigger();
     Narrow<GPW> n;
@@ -439,26 +470,28 @@ __global__ void __launch_bounds__(1024) rmsnorm_narrow_stream_kernel(NormArgs a,
     int st = 0, par = 0;
     uint32_t phase = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        mbar_wait_bounded(&full[st], phase, WAIT_LIMIT_US, &g_status, &abort_flag);
-        uint8_t* at = ring + (size_t)st * (xb + rb);
-        const Window xw = x_window(row), rw = rb ? r_window(row) : Window{nullptr, 0, 0, true};
-        const TX* x = xw.inside ? reinterpret_cast<const TX*>(at + xw.skip) : static_cast<const TX*>(a.x) + row * a.ldx;
-        const TR* r = !rb ? nullptr : rw.inside ? reinterpret_cast<const TR*>(at + xb + rw.skip)
-                                                : static_cast<const TR*>(a.r) + row * a.ldr;
-        const float ss = n.template take<TX, TR>(a, x, r, a.ro ? static_cast<TR*>(a.ro) + row * a.ldro : nullptr);
+        float ss = 0.f;
+        if (mbar_wait_bounded(&full[st], phase, ra.wait_limit, &g_status, &abort_flag)) {
+            uint8_t* at = ring + (size_t)st * (xb + rb);
+            const Window xw = x_window(row), rw = rb ? r_window(row) : Window{nullptr, 0, 0, true};
+            const TX* x = xw.inside ? reinterpret_cast<const TX*>(at + xw.skip) : static_cast<const TX*>(a.x) + row * a.ldx;
+            const TR* r = !rb ? nullptr : rw.inside ? reinterpret_cast<const TR*>(at + xb + rw.skip)
+                                                    : static_cast<const TR*>(a.r) + row * a.ldr;
+            ss = n.template take<TX, TR>(a, x, r, a.ro ? static_cast<TR*>(a.ro) + row * a.ldro : nullptr);
+        } else {
+            gave_up[par] = 1;
+        }
         const float rstd = row_rstd<false>(a, ss, part[par]);
-        if (abort_flag) break;
+        if (gave_up[par]) {
+            if (threadIdx.x == 0) land(full, ra, row, a.rows, st, phase);
+            break;
+        }
         par ^= 1;
         const int64_t next = row + (int64_t)stages * gridDim.x;
         if (threadIdx.x == 0 && next < a.rows) fetch(next, st);
         if (++st == stages) { st = 0; phase ^= 1u; }
         n.template finish<TX>(a, row, rstd);
     }
-    if (abort_flag && threadIdx.x == 0)                    // copies in flight land before the CTA leaves
-        for (int s = 0; s < stages; ++s) {
-            mbar_wait_bounded(&full[st], phase, WAIT_LIMIT_US, &g_status, nullptr);
-            if (++st == stages) { st = 0; phase ^= 1u; }
-        }
 }
 
 int sm_count(cudaError_t& e) {
@@ -474,6 +507,11 @@ cudaError_t go(const NormArgs& a, cudaStream_t s) {
     return launch_pdl(rmsnorm_kernel<TX, TR, VPT, false>, dim3(a.rows), dim3(threads), 0, s, a);
 }
 
+RingArgs ring_args(int stages, uint32_t xb, uint32_t rb) {
+    const bool plant = g_plant.load(std::memory_order_relaxed) && g_plant.exchange(false);
+    return RingArgs{stages, xb, rb, g_wait_limit.load(std::memory_order_relaxed), plant};
+}
+
 template <typename TX, typename TR, int GPW>
 cudaError_t go_narrow(const NormArgs& a, bool warp, int stages, uint32_t xb, uint32_t rb, int ctas, cudaStream_t s) {
     if constexpr (GPW <= 2)
@@ -484,7 +522,8 @@ cudaError_t go_narrow(const NormArgs& a, bool warp, int stages, uint32_t xb, uin
         if (stages) {
             cudaError_t e = ensure_smem_limit<rmsnorm_narrow_stream_kernel<TX, TR, GPW>>(RING_BYTES);
             if (e != cudaSuccess) return e;
-            return launch_pdl(rmsnorm_narrow_stream_kernel<TX, TR, GPW>, dim3(ctas), threads, (size_t)stages * (xb + rb), s, a, stages, xb, rb);
+            return launch_pdl(rmsnorm_narrow_stream_kernel<TX, TR, GPW>, dim3(ctas), threads, (size_t)stages * (xb + rb), s, a,
+                              ring_args(stages, xb, rb));
         }
     return launch_pdl(rmsnorm_narrow_kernel<TX, TR, GPW, false>, dim3(a.rows), threads, 0, s, a);
 }
@@ -493,7 +532,8 @@ template <typename TX, typename TR, int VPT>
 cudaError_t go_stream(const NormArgs& a, int threads, int stages, uint32_t xb, uint32_t rb, int ctas, cudaStream_t s) {
     cudaError_t e = ensure_smem_limit<rmsnorm_stream_kernel<TX, TR, VPT>>(RING_BYTES);
     if (e != cudaSuccess) return e;
-    return launch_pdl(rmsnorm_stream_kernel<TX, TR, VPT>, dim3(ctas), dim3(threads), (size_t)stages * (xb + rb), s, a, a.rows, stages, xb, rb);
+    return launch_pdl(rmsnorm_stream_kernel<TX, TR, VPT>, dim3(ctas), dim3(threads), (size_t)stages * (xb + rb), s, a,
+                      ring_args(stages, xb, rb));
 }
 
 // vec: every row on 16-byte boundaries and a whole number of 16-byte vectors.
@@ -568,6 +608,8 @@ cudaError_t launch_rmsnorm(const moe_rmsnorm_args* p, cudaStream_t s) {
     return pick<uint16_t, uint16_t>(a, vec, s);
 }
 
+void norm_set_wait_limit(uint32_t us) { g_wait_limit.store(us, std::memory_order_relaxed); }
+void norm_plant_timeout() { g_plant.store(true); }
 cudaError_t norm_status_word(uint32_t** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_status); }
 
 }  // namespace moe

@@ -61,3 +61,8 @@ def test_null_handles(lib):
     assert lib.moe_linear_destroy(None) == 1
     assert lib.moe_linear_device_status(None, None, None) == 1
     assert lib.moe_linear_create(None, None, None, None) == 1
+
+
+def test_wait_limit_of_zero_is_refused(lib):
+    assert lib.moe_rmsnorm_set_wait_limit(0) == 1
+    assert lib.moe_rmsnorm_set_wait_limit(2_000_000) == 0

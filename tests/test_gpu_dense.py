@@ -233,6 +233,46 @@ def test_norm_weight_written_by_the_kernel_before(moe, rows, cols):
         assert torch.equal(got, want)
 
 
+TIMEOUT = (6, 4)               # MOE_ERR_TIMEOUT, MOE_DEV_WAIT_TIMEOUT
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(2500, 7168, torch.bfloat16), (2500, 1032, torch.float32), (2500, 7001, torch.bfloat16),
+                                             (3000, 9001, torch.bfloat16)])
+def test_norm_wait_that_expires(moe, rows, cols, dtype):
+    """The wait for one row expires: the call ends with MOE_ERR_TIMEOUT, each row has all of its outputs or, as the residual was in
+    place, is as it was, and the next call is right."""
+    stream = torch.cuda.current_stream().cuda_stream
+    x, r, norm = randn((rows, cols), 14, dtype=dtype), randn((rows, cols), 15, 3.0, dtype), moe.RmsNorm(1 + randn((cols,), 16, 0.2))
+
+    def call():
+        res, y, out = r.clone(), torch.full_like(x, 7.0), moe.Fp8Tensor(rows, cols)
+        out.q.view(torch.uint8).fill_(0x7F)
+        out.s.fill_(-1)
+        norm(x, res, out=out, res_out=res, y=y)
+        status = moe.moe_rmsnorm_device_status(stream)
+        return status, res, y, out.q.view(torch.uint8), out.s.t()
+
+    def rows_equal(a, b):
+        return (a == b).all(1)
+
+    status, *want = call()
+    assert status == (0, 0)
+    moe.moe_rmsnorm_set_wait_limit(5000)
+    try:
+        moe.moe_rmsnorm_debug_timeout()
+        status, *got = call()
+    finally:
+        moe.moe_rmsnorm_set_wait_limit(2_000_000)
+    assert status == TIMEOUT
+    done = rows_equal(got[0], want[0])
+    assert 0 < int((~done).sum()) < rows // 50               # the row, and those after it in its thread block
+    for g, w, untouched in zip(got, want, (r, torch.full_like(x, 7.0), torch.full_like(want[2], 0x7F), torch.full_like(want[3], -1))):
+        assert rows_equal(g, w)[done].all() and rows_equal(g, untouched)[~done].all()
+    status, *again = call()                                  # read and cleared; fires once
+    assert status == (0, 0)
+    assert all(torch.equal(g, w) for g, w in zip(again, want))
+
+
 def test_norm_offsets_past_32_bits(moe):
     cols, ld = 256, 2 ** 31 + 64
     big = torch.empty(ld + cols, dtype=torch.bfloat16, device="cuda")
