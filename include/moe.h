@@ -428,6 +428,14 @@ moe_status moe_gated_linear_forward(moe_linear* linear, const moe_fp8_matrix* a,
 /* As moe_get_device_status, for a projection's kernels. */
 moe_status moe_linear_device_status(moe_linear* linear, void* stream, uint32_t* flags);
 
+/* As moe_set_wait_limit, for a projection's kernels. */
+moe_status moe_linear_set_wait_limit(moe_linear* linear, uint32_t microseconds);
+
+/* Test hook: in the next forward call of this projection the first thread
+ * block leaves out the last products of its first tile, so that the wait for
+ * them expires. */
+moe_status moe_linear_debug_timeout(moe_linear* linear);
+
 const char* moe_status_string(moe_status s);
 const char* moe_last_error(void);   /* thread-local; "" when none */
 int32_t moe_abi_version(void);

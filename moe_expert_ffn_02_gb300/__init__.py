@@ -28,7 +28,7 @@ __all__ = [
     "CREATE_HOST_TILES", "library_path", "load", "Layer", "LayerStackGraph", "StreamedStack",
     "MoeFp8Matrix", "MoeRmsnormArgs", "MoeLinearDesc", "MoeLinearWeights", "BF16", "F32", "SCALE_F32", "SCALE_E8M0",
     "moe_add_rmsnorm", "moe_rmsnorm_device_status", "moe_rmsnorm_set_wait_limit", "moe_rmsnorm_debug_timeout", "moe_linear_create", "moe_linear_destroy", "moe_linear_forward", "moe_gated_linear_forward",
-    "moe_linear_device_status", "Fp8Tensor", "RmsNorm", "Fp8Linear", "Fp8GatedLinear", "DenseFfn",
+    "moe_linear_device_status", "moe_linear_set_wait_limit", "moe_linear_debug_timeout", "Fp8Tensor", "RmsNorm", "Fp8Linear", "Fp8GatedLinear", "DenseFfn",
 ]
 
 MODE_ROUTE, MODE_PREFILL, MODE_DECODE = 0, 1, 2
@@ -142,6 +142,8 @@ def load(build_if_missing: bool = False):
             "moe_linear_forward": ([vp, ctypes.POINTER(MoeFp8Matrix), i32, vp, ctypes.c_int64, i32, vp], st),
             "moe_gated_linear_forward": ([vp, ctypes.POINTER(MoeFp8Matrix), i32, ctypes.POINTER(MoeFp8Matrix), vp], st),
             "moe_linear_device_status": ([vp, vp, ctypes.POINTER(u32)], st),
+            "moe_linear_set_wait_limit": ([vp, u32], st),
+            "moe_linear_debug_timeout": ([vp], st),
             "moe_status_string": ([st], ctypes.c_char_p),
             "moe_last_error": ([], ctypes.c_char_p),
             "moe_abi_version": ([], i32),
@@ -374,6 +376,15 @@ def moe_linear_device_status(linear: int, stream: int = 0):
     f = ctypes.c_uint32()
     st = load().moe_linear_device_status(linear, stream, ctypes.byref(f))
     return int(st), int(f.value)
+
+
+def moe_linear_set_wait_limit(linear: int, microseconds: int) -> None:
+    _check(load().moe_linear_set_wait_limit(linear, microseconds))
+
+
+def moe_linear_debug_timeout(linear: int) -> None:
+    """In the next forward call of this projection the wait for the last products of one tile expires."""
+    _check(load().moe_linear_debug_timeout(linear))
 
 
 # ---------------------------------------------------------------- torch convenience

@@ -172,6 +172,8 @@ MOE_EXPORT moe_status moe_linear_forward(moe_linear* L, const moe_fp8_matrix* a,
         return fail(MOE_ERR_INVALID_ARG, "ldy (%lld) is less than out_features (%d)", (long long)ldy, L->d.out_features);
     moe::GemmCall c = {};
     c.lin = L;
+    c.plant = L->plant;
+    L->plant = false;
     c.aq = a->q; c.ld_aq = a->ldq; c.as = a->s; c.ld_as = a->lds;
     c.M = rows;
     c.y = y; c.ldy = ldy; c.y_f32 = y_type == MOE_F32;
@@ -193,6 +195,8 @@ MOE_EXPORT moe_status moe_gated_linear_forward(moe_linear* L, const moe_fp8_matr
         return fail(MOE_ERR_INVALID_ARG, "h's scale type (%d) is not the weights' (%d)", h->scale_type, L->d.scale_type);
     moe::GemmCall c = {};
     c.lin = L;
+    c.plant = L->plant;
+    L->plant = false;
     c.aq = a->q; c.ld_aq = a->ldq; c.as = a->s; c.ld_as = a->lds;
     c.M = rows;
     c.hq = h->q; c.ld_hq = h->ldq; c.hs = h->s; c.ld_hs = h->lds;
@@ -218,6 +222,19 @@ moe_status read_status(uint32_t* word, void* stream, uint32_t* flags) {
 MOE_EXPORT moe_status moe_linear_device_status(moe_linear* L, void* stream, uint32_t* flags) {
     moe_status st = check_linear(L);
     return st != MOE_OK ? st : read_status(L->dev_status, stream, flags);
+}
+
+MOE_EXPORT moe_status moe_linear_set_wait_limit(moe_linear* L, uint32_t microseconds) {
+    if (!L) return fail(MOE_ERR_INVALID_ARG, "linear is NULL");
+    if (microseconds == 0) return fail(MOE_ERR_INVALID_ARG, "limit must be positive");
+    L->wait_limit = microseconds;
+    return MOE_OK;
+}
+
+MOE_EXPORT moe_status moe_linear_debug_timeout(moe_linear* L) {
+    if (!L) return fail(MOE_ERR_INVALID_ARG, "linear is NULL");
+    L->plant = true;
+    return MOE_OK;
 }
 
 MOE_EXPORT moe_status moe_rmsnorm_device_status(void* stream, uint32_t* flags) {

@@ -17,6 +17,7 @@ struct moe_linear {
     uint8_t* wsf;          // e8m0: [ceil(kt / 4)][ceil(rows_pad / 128)][512 B] scale-factor blocks of the image's rows
     uint32_t* dev_status;  // device status word
     uint32_t wait_limit;
+    bool plant;            // moe_linear_debug_timeout, for the next forward call
     int few_R, few_S, few_G;  // the few-token form's rows per tile, K ranges and K blocks per stage; few_R 0: it does not fit
 };
 
@@ -79,6 +80,7 @@ struct GemmCall {
     int64_t ld_hq;
     void* hs;
     int64_t ld_hs;
+    bool plant;
 };
 
 cudaError_t launch_rmsnorm(const moe_rmsnorm_args* a, cudaStream_t s);

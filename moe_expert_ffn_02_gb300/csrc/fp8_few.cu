@@ -71,6 +71,7 @@ struct FewArgs {
     int64_t ld_hs;
     uint32_t* status;
     uint32_t wait_limit;
+    bool plant;                              // the first CTA issues all of its MMAs but the last ones
 };
 
 // Four fp32 into a CTA of the cluster, counted on that CTA's mbarrier.
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
     uint8_t* scales = recv + tail_bytes(TN);                                        // [stage][slot]; MX: [kr4][pitch]
     float* sws = reinterpret_cast<float*>(scales + a.stages * slot_bytes);          // [kr][2]
     uint8_t* packed = scales + (a.kr4 * pitch + 127) / 128 * 128;                   // MX: [quad][weights 512 B | tokens 512 B]
-    __shared__ uint64_t full[ST_MAX], empty[ST_MAX], tfull[ST_MAX], sfull, sready[MODE == MX ? MX_QUADS : 1], joined;
+    __shared__ uint64_t full[ST_MAX], empty[ST_MAX], tfull[ST_MAX], sfull, sready[MODE == MX ? MX_QUADS : 1], joined, mma_done;
     __shared__ __align__(16) float amax[GATED ? 2 : 1][2][4][4];                                  // [parity][half of the threads][warp][token]
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
         const uint32_t drains = MODE == MX ? 1 : EPI_WARPS;
         for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], drains); mbar_init(&tfull[s], 1); }
         mbar_init(&joined, 1);
+        mbar_init(&mma_done, 1);
         if (MODE == MX) {
             mbar_init(&sfull, 1);
             for (int q = 0; q < (MODE == MX ? MX_QUADS : 1); ++q) mbar_init(&sready[q], 1);
@@ -246,9 +248,9 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
             }
             for (int n = min(g, a.stages); n > 0; --n) {   // every issued copy lands before the CTA exits
                 if (--st < 0) { st = a.stages - 1; phase ^= 1u; }
-                mbar_wait_bounded(&full[st], phase, a.wait_limit, a.status, nullptr);
+                mbar_wait_bounded(&full[st], phase, LANDING_LIMIT_US, a.status, nullptr);
             }
-            if (MODE == MX) mbar_wait_bounded(&sfull, 0, a.wait_limit, a.status, nullptr);
+            if (MODE == MX) mbar_wait_bounded(&sfull, 0, LANDING_LIMIT_US, a.status, nullptr);
         } else if (warp == 1) {
             // ------------------------------------------------ MMA issuer
             tc::tmem_alloc(&tmem_slot, COLS);
@@ -261,13 +263,15 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
             const uint32_t d0 = (uint32_t)tc::sw128_desc(ring0), sf0 = smem_addr(packed);
             int st = 0;
             uint32_t phase = 0;
-            bool ok = true;
+            bool ok = true, issued = false;
+            const int stop = a.plant && blockIdx.x == 0 ? n_grp - 1 : -1;
             for (int g = 0; g < n_grp && ok; ++g) {
                 // A stage's accumulators are free when the stage is: the warps that drained them handed
                 // it back, and its next copies were issued after that.
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[st], phase, a.wait_limit, a.status, abort));
+                ok = g != stop && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[st], phase, a.wait_limit, a.status, abort));
                 if (!ok) break;
                 tc::tc_fence_after();
+                issued = true;
                 const int nk = min(a.G, nkb - g * a.G);
                 uint32_t wd = d0 + (uint32_t)((st * stage_bytes) >> 4), td = wd + (uint32_t)((a.G * w_bytes) >> 4);
                 uint32_t dt = tmem + (uint32_t)(st * a.G * TN);
@@ -302,6 +306,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
                 __syncwarp();
                 if (++st == a.stages) { st = 0; phase ^= 1u; }
             }
+            if (!ok && issued) finish_mmas(&mma_done, el, a.status);
         } else if (MODE == MX) {
             // ------------------------------------------------ scale factors of every second quad of K blocks
             // 128 rows x 4 bytes in 512: row r at (r mod 32) * 16 + (r / 32) * 4, one byte per K block.
@@ -599,7 +604,7 @@ cudaError_t launch_few(const GemmCall& c, const FewPlan& p, int kr, cudaStream_t
     a.k_full = g.k_full;
     a.y = c.y; a.ldy = c.ldy; a.y_f32 = c.y_f32;
     a.hq = c.hq; a.ld_hq = c.ld_hq; a.hs = c.hs; a.ld_hs = c.ld_hs;
-    a.status = L->dev_status; a.wait_limit = L->wait_limit;
+    a.status = L->dev_status; a.wait_limit = L->wait_limit; a.plant = c.plant;
     // blocks per stage: the plan's, unless fewer than three stages would fit (one block: two)
     const int pitch = sa_pitch(a.a_rows, MODE != F32);
     int smem = 0;

@@ -103,6 +103,7 @@ struct Args {
     int64_t ld_hs;
     uint32_t* status;
     uint32_t wait_limit;
+    bool plant;                // the first CTA issues all MMAs of its first tile but the last ones
 };
 
 // What TMA brings: token codes (whole K blocks, and a ragged last one), weight image, token scales.
@@ -235,6 +236,14 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
             return false;
         }
     }
+}
+
+// For an issuer that stopped early: the MMAs and scale copies that it has issued finish, before tensor memory is
+// freed and the CTA leaves.
+__device__ __forceinline__ void finish_mmas(uint64_t* done, uint32_t elected, uint32_t* status) {
+    if (elected) tc::mma_commit(done);
+    __syncwarp();
+    mbar_wait_bounded(done, 0, LANDING_LIMIT_US, status, nullptr);
 }
 
 // ------------------------------------------------------------------ scaling by the tensor core
@@ -746,7 +755,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
     uint8_t* tail = ring + a.stages * stage_bytes;
     float* amax_cta = reinterpret_cast<float*>(tail);                           // gated: [half][128]
     float* amax_all = amax_cta + 2 * BM;                                        // gated: [parity][rank][128], or staging
-    __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES], tfull[2], tempty[2], xbar[2];
+    __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES], tfull[2], tempty[2], xbar[2], mma_done;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
 
@@ -765,6 +774,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
         for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], EPI_WARPS); mbar_init(&xbar[b], 1); }
+        mbar_init(&mma_done, 1);
         fence_mbar_init();
         abort_flag = 0;
     }
@@ -833,7 +843,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
             // every issued copy lands before the CTA exits: the last `issued` stages, newest first
             for (; issued > 0; --issued) {
                 if (--stage < 0) { stage = a.stages - 1; phase ^= 1u; }
-                mbar_wait_bounded(&full[stage], phase, a.wait_limit, a.status, nullptr);
+                mbar_wait_bounded(&full[stage], phase, LANDING_LIMIT_US, a.status, nullptr);
             }
         } else if (warp == 1) {
             tc::tmem_alloc(&tmem_slot, 512);
@@ -847,10 +857,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
             const uint32_t d0 = (uint32_t)tc::sw128_desc(smem_addr(ring));
             int stage = 0, buf = 0;
             uint32_t phase = 0, tphase = 0;
-            bool ok = true;
+            bool ok = true, issued = false;
+            const int stop = a.plant && blockIdx.x == 0 ? n_grp - 1 : -1;
             for (int u = first; u < a.n_units && ok; u += step) {
                 for (int g = 0; g < n_grp; ++g) {
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[stage], phase, a.wait_limit, a.status, abort) &&
+                    ok = g != stop && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[stage], phase, a.wait_limit, a.status, abort) &&
                                                      mbar_wait_bounded(&tempty[buf], tphase ^ 1u, a.wait_limit, a.status, abort));
                     if (!ok) break;
                     tc::tc_fence_after();
@@ -869,10 +880,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
                         tc::mma_commit(&empty[stage]);
                     }
                     __syncwarp();
+                    issued = true;
                     if (++stage == a.stages) { stage = 0; phase ^= 1u; }
                     if (++buf == 2) { buf = 0; tphase ^= 1u; }
                 }
             }
+            if (!ok && issued) finish_mmas(&mma_done, el, a.status);
         }
         __syncwarp();
     } else {
@@ -1198,6 +1211,7 @@ inline Args base_args(const GemmCall& c) {
     a.k_full = L->d.in_features / QB;
     a.status = L->dev_status;
     a.wait_limit = L->wait_limit;
+    a.plant = c.plant;
     return a;
 }
 

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
     float* amax_cta = reinterpret_cast<float*>(tail);
     uint8_t* sf = tail + (GATED ? TAIL_GATED : TAIL_PLAIN);                     // [SF_SLOTS][raw | tokens | weights]
     __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES], tfull[NBUF], tempty[NBUF], xbar[2];
-    __shared__ uint64_t sfull[SF_SLOTS], sready[SF_SLOTS], sempty[SF_SLOTS];
+    __shared__ uint64_t sfull[SF_SLOTS], sready[SF_SLOTS], sempty[SF_SLOTS], mma_done;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
 
@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
         for (int b = 0; b < NBUF; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], EPI_WARPS); }
         for (int b = 0; b < SF_SLOTS; ++b) { mbar_init(&sfull[b], 1); mbar_init(&sready[b], 1); mbar_init(&sempty[b], 1); }
         for (int b = 0; b < 2; ++b) mbar_init(&xbar[b], 1);
+        mbar_init(&mma_done, 1);
         fence_mbar_init();
         abort_flag = 0;
     }
@@ -139,11 +140,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
             }
             for (; issued > 0; --issued) {                 // every issued copy lands before the CTA exits
                 if (--stage < 0) { stage = a.stages - 1; phase ^= 1u; }
-                mbar_wait_bounded(&full[stage], phase, a.wait_limit, a.status, nullptr);
+                mbar_wait_bounded(&full[stage], phase, LANDING_LIMIT_US, a.status, nullptr);
             }
             for (; sissued > 0; --sissued) {
                 if (--slot < 0) { slot = SF_SLOTS - 1; sphase ^= 1u; }
-                mbar_wait_bounded(&sfull[slot], sphase, a.wait_limit, a.status, nullptr);
+                mbar_wait_bounded(&sfull[slot], sphase, LANDING_LIMIT_US, a.status, nullptr);
             }
         } else if (warp == 1) {
             // ------------------------------------------------ MMA issuer
@@ -156,7 +157,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
             const uint32_t d0 = (uint32_t)tc::sw128_desc(smem_addr(ring)), sf0 = smem_addr(sf);
             int stage = 0, slot = 0, tslot = 0, buf = 0;
             uint32_t phase = 0, sphase = 0, tphase = 0;
-            bool ok = true;
+            bool ok = true, issued = false;
+            const int stop = a.plant && blockIdx.x == 0 ? kt - 1 : -1;
             for (int u = first; u < a.n_units && ok; u += step) {
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tempty[buf], tphase ^ 1u, a.wait_limit, a.status, abort));
                 const uint32_t dt = tmem + (uint32_t)(buf * BN);
@@ -166,12 +168,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
                         ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&sready[slot], sphase, a.wait_limit, a.status, abort) &&
                                                          mbar_wait_bounded(&sfull[slot], sphase, a.wait_limit, a.status, abort));
                         if (!ok) break;
+                        issued = true;
                         const uint32_t at = sf0 + slot * SLOT + RAW_BYTES;
                         sf_copy(sft, sf_desc(at), el);
 #pragma unroll
                         for (int b = 0; b < BN / QB; ++b) sf_copy(sft + 4 + 4 * b, sf_desc(at + SF_BYTES * (1 + b)), el);
                     }
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[stage], phase, a.wait_limit, a.status, abort));
+                    ok = kb != stop && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[stage], phase, a.wait_limit, a.status, abort));
                     if (!ok) break;
                     tc::tc_fence_after();
                     const uint32_t wd = d0 + (uint32_t)((stage * stage_bytes) >> 4), ad = wd + (uint32_t)(w_bytes >> 4);
@@ -193,6 +196,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
                 }
                 if (++buf == NBUF) { buf = 0; tphase ^= 1u; }
             }
+            if (!ok && issued) finish_mmas(&mma_done, el, a.status);
         } else if (warp == 2) {
             // ------------------------------------------------ tokens' scale factors: [4 K blocks][row] -> [row][4 K blocks]
             int slot = 0;

@@ -66,3 +66,8 @@ def test_null_handles(lib):
 def test_wait_limit_of_zero_is_refused(lib):
     assert lib.moe_rmsnorm_set_wait_limit(0) == 1
     assert lib.moe_rmsnorm_set_wait_limit(2_000_000) == 0
+
+
+def test_null_handles_of_the_test_hooks(lib):
+    assert lib.moe_linear_set_wait_limit(None, 1000) == 1
+    assert lib.moe_linear_debug_timeout(None) == 1

@@ -531,6 +531,44 @@ def test_repeated_calls_give_the_same_bits(moe):
         assert torch.equal(lin(a, torch.empty_like(y)), y)
 
 
+# ------------------------------------------------------------------ waits that expire
+
+def check_expired(moe, lin, call):
+    """call() runs a forward into buffers filled beforehand and returns its outputs, rows first.  With the last products of one
+    tile left out it ends with MOE_ERR_TIMEOUT, every element is right or as it was, and the next call is right."""
+    want = call()
+    assert lin.device_status() == (0, 0)
+    moe.moe_linear_set_wait_limit(lin.handle, 20_000)
+    try:
+        moe.moe_linear_debug_timeout(lin.handle)
+        got = call()
+        assert lin.device_status() == TIMEOUT
+    finally:
+        moe.moe_linear_set_wait_limit(lin.handle, 2_000_000)
+    again = call()                                           # read and cleared; fires once
+    assert lin.device_status() == (0, 0)
+    assert all(torch.equal(g, w) for g, w in zip(again, want))
+    return got, want
+
+
+def expired_linear(moe, m, k, n, scale, dtype=torch.float32):
+    lin = moe.Fp8Linear(*blocks_fp8(randn((n, k), 111, 0.02), scale))
+    a = moe.Fp8Tensor.from_parts(*rows_fp8(randn((m, k), 110), scale))
+    (got,), (want,) = check_expired(moe, lin, lambda: [lin(a, torch.full((m, n), 7.0, dtype=dtype, device="cuda"))])
+    left = got == 7
+    assert torch.equal(torch.where(left, want, got), want)
+    return left
+
+
+# tiles of 256, 80, 48 and 16 weight rows in the fp32-scale form, 256 and 128 in the other
+@pytest.mark.parametrize("m,k,n,scale", [(1921, 1100, 5000, "f32"), (700, 1000, 2000, "f32"), (777, 1992, 1001, "f32"),
+                                         (65, 1000, 96, "f32"), (1921, 1100, 5000, "e8m0"), (1500, 4000, 1500, "e8m0")])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_linear_wait_that_expires(moe, m, k, n, scale, dtype):
+    left = expired_linear(moe, m, k, n, scale, dtype)
+    assert left.any() and not left.all()
+
+
 # ------------------------------------------------------------------ refusals
 
 def test_refusals(moe):
