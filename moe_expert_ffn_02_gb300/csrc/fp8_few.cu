@@ -295,6 +295,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
                     td += (uint32_t)(a_bytes >> 4);
                     dt += TN;
                 }
+                if (!ok) break;
                 if (el) {
                     if (MODE == MX) {
                         tc::mma_commit(&empty[st]);
@@ -453,7 +454,8 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
             if (++st == a.stages) { st = 0; phase ^= 1u; }
         }
         pdl_wait();                                            // before the first write the preceding kernel may conflict with
-        if (live) {
+        // sums that are not whole go nowhere: the CTA that waits for them gives up too, and writes nothing
+        if (live && !dead) {
 #pragma unroll
             for (int t = 0; t < HT; t += 4) {
                 if (t0 + t >= a.M) break;

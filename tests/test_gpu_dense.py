@@ -569,6 +569,14 @@ def test_linear_wait_that_expires(moe, m, k, n, scale, dtype):
     assert left.any() and not left.all()
 
 
+# one CTA a tile, four, and eight; few and many K blocks
+@pytest.mark.parametrize("m,k,n", [(16, 500, 4000), (40, 7168, 2048), (1, 7168, 300), (64, 33000, 130), (5, 70000, 40)])
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+def test_few_token_linear_wait_that_expires(moe, m, k, n, scale):
+    left = expired_linear(moe, m, k, n, scale)
+    assert left.any() and not left.all()
+
+
 # ------------------------------------------------------------------ refusals
 
 def test_refusals(moe):
