@@ -81,6 +81,15 @@ __device__ __forceinline__ void st_async_4(uint32_t remote, const float* v, uint
                  "r"(remote_bar)
                  : "memory");
 }
+// A named barrier that also tells every thread whether `mine` held in all of them.
+__device__ __forceinline__ bool named_bar_and(int id, int threads, bool mine) {
+    uint32_t all;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %3, 0;\n barrier.cta.red.and.pred p, %1, %2, q;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(all)
+                 : "r"(id), "r"(threads), "r"((uint32_t)mine)
+                 : "memory");
+    return all != 0;
+}
 // (a0, a1) += (x0, x1) * s * (c0, c1), rounded as s * c and one fma each.
 __device__ __forceinline__ void fma2s(float& a0, float& a1, uint32_t x0, uint32_t x1, float s, float c0, float c1) {
     asm("{\n .reg .b64 a, x, c, s;\n mov.b64 a, {%0, %1};\n mov.b64 x, {%2, %3};\n mov.b64 c, {%5, %6};\n mov.b64 s, {%4, %4};\n"
@@ -480,7 +489,10 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
     named_bar_sync(3, NTHREADS);
     if (csize == 1) return;
     cluster_arrive();                                          // everything sent
-    if (own > 0 && __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&joined, 0, a.wait_limit, a.status, abort))) {
+    const bool whole = own > 0 && __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&joined, 0, a.wait_limit, a.status, abort));
+    // gated: all warps go through, because they meet at a barrier there, which also tells them whether any of
+    // them gave up (each on its own look at the clock); then none stores
+    if (GATED ? own > 0 : whole) {
         const int tid = threadIdx.x - CTRL_WARPS * 32, side = tid >> 7, i = tid & 127;   // 128 threads a group
         const float4* in = reinterpret_cast<const float4*>(recv);
         if constexpr (GATED) {
@@ -510,8 +522,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
                 }
                 float (&all)[4][4] = amax[parity][side];
                 if (lane == 0) *reinterpret_cast<float4*>(all[ew & 3]) = make_float4(am[0], am[1], am[2], am[3]);
-                if (side == 0) named_bar_sync(4, 128);
-                else named_bar_sync(5, 128);
+                const bool store = named_bar_and(4 + side, 128, whole);
                 const int t0 = 4 * (slot * csize + rank);
                 // lane e mod 4 works out token e's scale
                 const int q = lane & 3;
@@ -523,8 +534,8 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
                 uint8_t* dst = a.hq + (int64_t)t0 * a.ld_hq + f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e, dst += a.ld_hq)
-                    if (t0 + e < a.M && f < a.N) *dst = code[e];
-                if (i < 4 && t0 + i < a.M) {
+                    if (store && t0 + e < a.M && f < a.N) *dst = code[e];
+                if (store && i < 4 && t0 + i < a.M) {
                     const int64_t at = (int64_t)unit * a.ld_hs + t0 + i;
                     if (E8S) static_cast<uint8_t*>(a.hs)[at] = (uint8_t)held;
                     else static_cast<uint32_t*>(a.hs)[at] = held;

@@ -569,12 +569,39 @@ def test_linear_wait_that_expires(moe, m, k, n, scale, dtype):
     assert left.any() and not left.all()
 
 
+def expired_gated(moe, m, k, n, scale):
+    """The rows' groups that were left out, [m][groups]; a group is right or left out as a whole, codes and scale."""
+    lin = moe.Fp8GatedLinear(*blocks_fp8(randn((n, k), 121, 0.05), scale), *blocks_fp8(randn((n, k), 122, 0.05), scale))
+    a = moe.Fp8Tensor.from_parts(*rows_fp8(randn((m, k), 120), scale))
+
+    def call():
+        h = moe.Fp8Tensor(m, n, scale)
+        h.q.view(torch.uint8).fill_(0x7F)
+        s = h.s.view(torch.uint8 if scale == "e8m0" else torch.float32)
+        s.fill_(3)
+        lin(a, h)
+        return pad128(h.q.view(torch.uint8), 1).view(m, -1, 128), s.t()
+
+    (gq, gs), (wq, ws) = check_expired(moe, lin, call)
+    untouched = pad128(torch.full((m, n), 0x7F, dtype=torch.uint8, device="cuda"), 1).view(gq.shape)
+    left = (gq == untouched).all(-1) & (gs == 3)
+    assert ((gq == wq).all(-1) & (gs == ws))[~left].all()
+    return left
+
+
 # one CTA a tile, four, and eight; few and many K blocks
 @pytest.mark.parametrize("m,k,n", [(16, 500, 4000), (40, 7168, 2048), (1, 7168, 300), (64, 33000, 130), (5, 70000, 40)])
 @pytest.mark.parametrize("scale", ["f32", "e8m0"])
 def test_few_token_linear_wait_that_expires(moe, m, k, n, scale):
     left = expired_linear(moe, m, k, n, scale)
     assert left.any() and not left.all()
+
+
+@pytest.mark.parametrize("m,k,n", [(5, 1000, 20000), (3, 500, 300), (64, 7168, 2048), (20, 33100, 50)])
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+def test_few_token_gated_wait_that_expires(moe, m, k, n, scale):
+    left = expired_gated(moe, m, k, n, scale)
+    assert left.any() and not left[:, 1:].any()              # the first unit's features only
 
 
 # ------------------------------------------------------------------ refusals
