@@ -341,11 +341,14 @@ __device__ __forceinline__ void epi_gated(const Args& a, EpiCtx& x, const float 
     x.amax_cta[x.half * BM + r] = am;
     named_bar_sync(1, EPI_WARPS * 32);
     am = max_nan(x.amax_cta[r], x.amax_cta[BM + r]);
+    // a warp that gave up has no whole sums, and its amax belongs to all of the row's codes: after it the CTA neither
+    // stores nor sends, so that the waits of its peers expire too and nobody's scales follow a part of a row
+    dead = dead || *x.abort != 0;
     if (x.csize > 1) {
         // every CTA sends its rows' amax to every CTA of the cluster (itself included); a peer is
         // at most one unit ahead, so two slots are enough
         float* slot = x.amax_all + x.parity * MAX_CLUSTER * BM;
-        if (x.half == 0) {
+        if (x.half == 0 && !dead) {
             const uint32_t mine = smem_addr(slot + x.rank * BM + r), bar = smem_addr(&x.xbar[x.parity]);
             if (r == 0) mbar_arrive_expect_tx(&x.xbar[x.parity], x.csize * BM * 4u);
             for (uint32_t p = 0; p < x.csize; ++p) st_async_f32(map_to_rank(mine, p), am, map_to_rank(bar, p));

@@ -604,6 +604,14 @@ def test_few_token_gated_wait_that_expires(moe, m, k, n, scale):
     assert left.any() and not left[:, 1:].any()              # the first unit's features only
 
 
+# one CTA a unit, two and four, with fp32 scales; one and two with the tensor core's own scaling
+@pytest.mark.parametrize("m,k,n,scale", [(3000, 1000, 2048, "f32"), (1000, 1000, 1000, "f32"), (300, 1992, 1001, "f32"),
+                                         (3000, 1000, 2048, "e8m0"), (1000, 1000, 1000, "e8m0")])
+def test_gated_wait_that_expires(moe, m, k, n, scale):
+    left = expired_gated(moe, m, k, n, scale)
+    assert left[:128, 0].all() and not left.all()            # the whole first unit
+
+
 # ------------------------------------------------------------------ refusals
 
 def test_refusals(moe):
