@@ -595,6 +595,14 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
 }
 __device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 
+// Before the barrier after which the sums are joined: a warp that gave up raises the flags of all the cluster's
+// CTAs, and none of them joins the unit.
+__device__ __forceinline__ void tell_peers(bool dead, volatile int* abort, int ctas, int lane) {
+    if (dead && lane < ctas)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(smem_addr(const_cast<int*>(abort)), (uint32_t)lane)), "r"(1u)
+                     : "memory");
+}
+
 constexpr int part_pitch(int bn) { return bn + 4; }          // floats; 16-byte rows, free of bank conflicts
 
 template <int HALF>
@@ -1038,6 +1046,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
             if constexpr (CAN_SPLIT) {
                 if (shared_k) {
                     if (live) leave_partial<HALF>(reinterpret_cast<float*>(ring), half, r, acc);
+                    tell_peers(dead, abort, a.S, lane);
                     cluster_arrive_release();
                     cluster_wait();
                     if (!*abort) join_partials<COLS, GATED>(a, smem_addr(ring), split, ew, lane, m0, n0, valid);

@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
             if constexpr (CAN_SPLIT) {
                 if (shared_k) {
                     if (live) leave_partial<HALF>(reinterpret_cast<float*>(ring), half, quarter * 32 + lane, acc);
+                    tell_peers(dead, abort, a.S, lane);
                     cluster_arrive_release();
                     cluster_wait();
                     if (!*abort) join_partials<BN, GATED>(a, smem_addr(ring), split, ew, lane, m0, n0, valid);

@@ -612,6 +612,15 @@ def test_gated_wait_that_expires(moe, m, k, n, scale):
     assert left[:128, 0].all() and not left.all()            # the whole first unit
 
 
+@pytest.mark.parametrize("gated,m,k,n,scale", [(False, 300, 1992, 1001, "f32"), (False, 70, 7168, 300, "f32"), (False, 128, 7168, 7168, "f32"),
+                                               (False, 70, 7168, 300, "e8m0"), (False, 1024, 4000, 1024, "e8m0"),
+                                               (True, 70, 7168, 300, "f32"), (True, 300, 7168, 1400, "f32"), (True, 70, 7168, 300, "e8m0")])
+def test_joined_ranges_wait_that_expires(moe, gated, m, k, n, scale):
+    """K split over two, four or eight CTAs: a range that was not finished keeps the whole tile from being joined."""
+    left = expired_gated(moe, m, k, n, scale)[:, 0] if gated else expired_linear(moe, m, k, n, scale)[:, 0]
+    assert left[:128].all() and not left[128:].any()
+
+
 # ------------------------------------------------------------------ refusals
 
 def test_refusals(moe):
