@@ -557,6 +557,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
         }
     }
     cluster_wait();                                            // nobody leaves while a peer may still send to it
+    let_land(abort);
 }
 
 struct FewPlan {

@@ -246,6 +246,14 @@ __device__ __forceinline__ void finish_mmas(uint64_t* done, uint32_t elected, ui
     mbar_wait_bounded(done, 0, LANDING_LIMIT_US, status, nullptr);
 }
 
+// After a cluster's last barrier, in a CTA that gave up: what its peers sent before they arrived there (a store into
+// a peer's shared memory takes about a microsecond) lands before that memory is given back.  A CTA that did not give
+// up has waited for every byte.
+__device__ __forceinline__ void let_land(volatile int* abort) {
+    if (*abort != 0)
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+}
+
 // ------------------------------------------------------------------ scaling by the tensor core
 // Descriptor of a scale-factor block: no swizzle, 8-row groups of 128 bytes one after the other.
 __device__ __forceinline__ uint64_t sf_desc(uint32_t saddr) {
@@ -1070,6 +1078,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
     if (shared_k || (GATED && csize > 1)) {     // nobody leaves while a peer may still reach into it
         cluster_arrive_release();
         cluster_wait();
+        if (GATED) let_land(abort);
     }
 }
 

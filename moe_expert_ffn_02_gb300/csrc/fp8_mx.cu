@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
     if (shared_k || (GATED && csize > 1)) {     // nobody leaves while a peer may still reach into it
         cluster_arrive_release();
         cluster_wait();
+        if (GATED) let_land(abort);
     }
 }
 
