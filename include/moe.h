@@ -428,7 +428,9 @@ moe_status moe_gated_linear_forward(moe_linear* linear, const moe_fp8_matrix* a,
 /* As moe_get_device_status, for a projection's kernels. */
 moe_status moe_linear_device_status(moe_linear* linear, void* stream, uint32_t* flags);
 
-/* As moe_set_wait_limit, for a projection's kernels. */
+/* As moe_set_wait_limit, for a projection's kernels.  Time in which a kernel
+ * waits for the one before it on the stream does not count.  Of a call whose
+ * wait expired, an element of the output is right or as it was. */
 moe_status moe_linear_set_wait_limit(moe_linear* linear, uint32_t microseconds);
 
 /* Test hook: in the next forward call of this projection the first thread

@@ -266,6 +266,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
             tc::tc_fence_before();
             named_bar_sync(2, (1 + EPI_WARPS) * 32);
             tc::tc_fence_after();
+            pdl_wait();                                        // no bounded wait before it: limits count this kernel's time alone
             const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_slot, 0);
             const uint32_t el = elect_one();
             const uint32_t idesc = (1u << 4) | ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
@@ -344,6 +345,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
                 }
                 *reinterpret_cast<uint4*>(packed + q * 1024 + lane * 16) = make_uint4(v[0], v[1], v[2], v[3]);
             }
+            pdl_wait();
             bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&sfull, 0, a.wait_limit, a.status, abort));
             for (int q = warp - 2; q < nq && ok; q += 2) {
                 uint32_t v[2];
@@ -398,8 +400,8 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
             st_async_4(map_to_rank(recv0 + (uint32_t)(((slot * csize + rank) * a.R + row) * 16), to), v, map_to_rank(joined0, to));
     };
     if (csize > 1) cluster_wait();                             // the peers have set up their barriers
+    pdl_wait();                                                // before the first bounded wait, and the first write
     if constexpr (MODE == MX) {
-        pdl_wait();                                            // before the first write the preceding kernel may conflict with
         const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[0], 0, a.wait_limit, a.status, abort));
         if (live && ok) {
             tc::tc_fence_after();
@@ -462,7 +464,6 @@ __global__ void __launch_bounds__(NTHREADS, 2) few_kernel(const __grid_constant_
             if (lane == 0) mbar_arrive(&empty[st]);
             if (++st == a.stages) { st = 0; phase ^= 1u; }
         }
-        pdl_wait();                                            // before the first write the preceding kernel may conflict with
         // sums that are not whole go nowhere: the CTA that waits for them gives up too, and writes nothing
         if (live && !dead) {
 #pragma unroll

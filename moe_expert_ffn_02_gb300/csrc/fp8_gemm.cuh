@@ -869,6 +869,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
             tc::tc_fence_before();
             named_bar_sync(2, (1 + EPI_WARPS) * 32);            // the drain warps read the address
             tc::tc_fence_after();
+            pdl_wait();                      // no bounded wait before it: limits count this kernel's time alone
             // ------------------------------------------------ MMA issuer
             const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_slot, 0);
             const uint32_t el = elect_one();

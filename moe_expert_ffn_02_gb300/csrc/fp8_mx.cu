@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
             tc::tc_fence_before();
             named_bar_sync(2, (1 + EPI_WARPS) * 32);
             tc::tc_fence_after();
+            pdl_wait();                                    // no bounded wait before it
             const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_slot, 0);
             const uint32_t el = elect_one();
             const uint32_t d0 = (uint32_t)tc::sw128_desc(smem_addr(ring)), sf0 = smem_addr(sf);
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx_kernel(const __grid_constant__
             int slot = 0;
             uint32_t sphase = 0;
             bool ok = true;
+            pdl_wait();
             for (int u = first; u < a.n_units && ok; u += step) {
                 for (int q = 0; q < (kt + 3) / 4; ++q) {
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&sfull[slot], sphase, a.wait_limit, a.status, abort));
