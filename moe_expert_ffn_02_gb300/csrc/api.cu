@@ -24,7 +24,9 @@ moe_status fail(moe_status s, const char* fmt, ...) {
     return s;
 }
 
+// The runtime keeps a failed call's error until somebody asks; left there, the next checked launch would report it.
 moe_status cuda_fail(cudaError_t e, const char* what) {
+    cudaGetLastError();
     return fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 

@@ -13,6 +13,7 @@ Tolerances, derived from the arithmetic (u = 2^-24, half an fp32 ulp):
 - codes: half an E4M3 step of the quotient, 2^-4 relative for normal codes and
   2^-10 absolute below them, plus the quotient's own error.
 """
+import ctypes
 import os
 import subprocess
 import sys
@@ -692,3 +693,14 @@ def test_the_example_runs(moe, tokens):
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
     assert "us a step" in r.stdout
+
+
+def test_a_failed_call_leaves_no_error_behind(moe):
+    """Weights that do not fit the device are refused with a CUDA error; the next launches do not inherit it."""
+    d, h = moe.MoeLinearDesc(1 << 20, 1 << 20, 1, 0), ctypes.c_void_p()        # 2 TB; refused before the pointers are read
+    w = moe.MoeLinearWeights(*[0x10000 * (i + 1) for i in range(4)])
+    assert moe.load().moe_linear_create(ctypes.byref(d), ctypes.byref(w), None, ctypes.byref(h)) == 4 and h.value is None
+    assert "out of memory" in moe.moe_last_error()
+    x = torch.ones(300, device="cuda") + 1                                     # torch checks the last error after its launches
+    assert float(x.sum()) == 600
+    check_linear(moe, 5, 300, 40, "f32", torch.float32)
