@@ -399,6 +399,7 @@ moe_status moe_rmsnorm_debug_timeout(void);
  * [ceil(out / 128)][ceil(in / 128)].  gated: w, s are the gate matrix and
  * w_up, s_up the up matrix of the same shape. */
 #define MOE_LINEAR_MAX_FEATURES (1 << 20)
+#define MOE_LINEAR_MAX_ROWS (2147483647 - 255)    /* the end of the last 128-row tile is a 32-bit count */
 typedef struct moe_linear moe_linear;    /* opaque; owned by the library */
 typedef struct {
     int32_t in_features, out_features;

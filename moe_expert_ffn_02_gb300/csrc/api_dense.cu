@@ -58,6 +58,7 @@ moe_status check_linear(const moe_linear* L) {
 
 moe_status check_input(const moe_linear* L, const moe_fp8_matrix* a, int rows) {
     if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows = %d is negative", rows);
+    if (rows > MOE_LINEAR_MAX_ROWS) return fail(MOE_ERR_UNSUPPORTED, "rows (%d) is over %d", rows, MOE_LINEAR_MAX_ROWS);
     if (!a) return fail(MOE_ERR_INVALID_ARG, "a is NULL");
     if (rows == 0) return MOE_OK;
     moe_status st = check_fp8(*a, rows, L->d.in_features, "a");

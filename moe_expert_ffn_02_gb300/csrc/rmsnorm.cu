@@ -515,7 +515,7 @@ RingArgs ring_args(int stages, uint32_t xb, uint32_t rb) {
 template <typename TX, typename TR, int GPW>
 cudaError_t go_narrow(const NormArgs& a, bool warp, int stages, uint32_t xb, uint32_t rb, int ctas, cudaStream_t s) {
     if constexpr (GPW <= 2)
-        if (warp) return launch_pdl(rmsnorm_narrow_kernel<TX, TR, GPW, true>, dim3((a.rows + 7) / 8), dim3(256), 0, s, a);
+        if (warp) return launch_pdl(rmsnorm_narrow_kernel<TX, TR, GPW, true>, dim3((a.rows - 1) / 8 + 1), dim3(256), 0, s, a);
     const int groups = (a.cols + QB - 1) / QB;
     const dim3 threads((groups + GPW - 1) / GPW * 32);
     if constexpr (GPW > 1)
@@ -567,7 +567,7 @@ cudaError_t pick(const NormArgs& a, bool vec, cudaStream_t s) {
         }
         if (vecs > 2048) return go<TX, TR, 4>(a, s);
         if (vecs > 1024) return go<TX, TR, 2>(a, s);
-        if (warp) return launch_pdl(rmsnorm_kernel<TX, TR, 1, true>, dim3((a.rows + 7) / 8), dim3(256), 0, s, a);
+        if (warp) return launch_pdl(rmsnorm_kernel<TX, TR, 1, true>, dim3((a.rows - 1) / 8 + 1), dim3(256), 0, s, a);
         return go<TX, TR, 1>(a, s);
     }
     const int groups = (a.cols + QB - 1) / QB;

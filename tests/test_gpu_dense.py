@@ -287,6 +287,17 @@ def test_norm_offsets_past_32_bits(moe):
     assert torch.equal(y, z)
 
 
+def test_norm_of_as_many_rows_as_a_count_holds(moe):
+    rows = 2 ** 31 - 1
+    x = torch.full((rows, 1), 2.0, dtype=torch.bfloat16, device="cuda")
+    x[-300:] = randn((300, 1), 17, dtype=torch.bfloat16)
+    y = torch.zeros_like(x)
+    moe.RmsNorm(torch.full((1,), 3.0, device="cuda"))(x, y=y)
+    assert (y[:-300] == 3).all()
+    _, n = norm64(x[-300:], None, torch.full((1,), 3.0, device="cuda"), 1e-6)
+    assert ((y[-300:].double() - n).abs() <= n.abs() * (BF16_HALF + N_REL)).all()
+
+
 # ------------------------------------------------------------------ projections
 
 def product64(aq, a_s, wq, w_s):
@@ -423,6 +434,16 @@ def test_linear_offsets_past_32_bits(moe):
     del big, wide
     out = torch.empty(2 * (2 ** 31 + 3) + n, dtype=torch.bfloat16, device="cuda").as_strided((m, n), (2 ** 31 + 3, 1))
     assert torch.equal(lin(moe.Fp8Tensor.from_parts(aq, a_s), out), ref)
+
+
+def test_more_rows_than_tiles_can_count_are_refused(moe):
+    w = blocks_fp8(randn((16, 16), 62), "f32")
+    m = moe.MoeFp8Matrix(0x10000, 0x20000, 16, 2 ** 31, moe.SCALE_F32, 0)
+    for call, lin in ((lambda h: moe.moe_linear_forward(h, m, 2 ** 31 - 255, 0x30000, 16, moe.BF16), moe.Fp8Linear(*w)),
+                      (lambda h: moe.moe_gated_linear_forward(h, m, 2 ** 31 - 255, m), moe.Fp8GatedLinear(*w, *w))):
+        with pytest.raises(moe.MoeError) as e:
+            call(lin.handle)
+        assert e.value.status == 2
 
 
 @pytest.mark.parametrize("m", [1, 40, 200])
