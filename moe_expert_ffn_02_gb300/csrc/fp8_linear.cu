@@ -98,9 +98,10 @@ __global__ void linear_scales_kernel(const void* s, const void* su, int n, bool 
 // row r at (r mod 32) * 16 + (r / 32) * 4, one byte per K block.
 __global__ void linear_sf_kernel(const uint8_t* __restrict__ s, const uint8_t* __restrict__ su, int N, int kt, int rows_pad,
                                  uint8_t* __restrict__ out) {
-    const int nrb = (rows_pad + QB - 1) / QB, nq = (kt + 3) / 4;
-    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < nq * nrb * 512; i += gridDim.x * blockDim.x) {
-        const int b = i & 511, rb = (i >> 9) % nrb, q = (i >> 9) / nrb;
+    const int nrb = (rows_pad + QB - 1) / QB;
+    const size_t n = (size_t)((kt + 3) / 4) * nrb * 512;
+    for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) {
+        const int b = (int)(i & 511), rb = (int)((i >> 9) % nrb), q = (int)((i >> 9) / nrb);
         const int r = rb * QB + ((b >> 2) & 3) * 32 + (b >> 4), kb = 4 * q + (b & 3);
         const int f = su ? (r >> 4) * 8 + (r & 7) : r;
         const uint8_t* src = su && (r & 8) ? su : s;
