@@ -12,9 +12,12 @@
 // quad), selected by the instruction's scale-factor id.
 //
 // The accumulator is fp32 and truncates: each MMA loses up to one unit in the
-// last place of the running sum, so a chain is limited to MAX_KT blocks (256
-// MMAs: below 256 x 2^-23 of the sum, in practice a few 1e-6); longer ones take
-// the form that adds blocks in registers.
+// last place of the running sum at that point, always towards zero, so a chain is
+// limited to MAX_KT blocks: 256 MMAs lose below 256 x 2^-23 of the largest partial
+// sum, which sums that cancel later may leave far behind (in terms of the result
+// there is no bound), and operands of one sign lose all in the same direction
+// (2100 x 8192 x 2100, chains of 64 blocks: 5e-6 of the sum; fp32 scales 6e-7).
+// Longer ones take the form that adds blocks in registers, each sum rounded.
 //
 // Scale factors reach tensor memory through shared memory (tcgen05.cp
 // 32x128b.warpx4): 128 rows x 4 K blocks in 512 bytes, row r at (r mod 32) * 16 +

@@ -338,6 +338,32 @@ def test_linear_of_long_rows(moe, m, k, n, scale):
     check_linear(moe, m, k, n, scale, torch.float32)
 
 
+# few tokens, chains of 64 K blocks in each of eight ranges; many tokens, one chain; ranges of the many-token form
+@pytest.mark.parametrize("m,k,n", [(3, 65536, 40), (40, 65300, 130), (2100, 8192, 2100), (1500, 8192, 1500), (100, 8192, 150)])
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("signs", ["one", "cancel"])
+def test_linear_sums_of_one_sign_and_sums_that_cancel(moe, m, k, n, scale, signs):
+    """Truncation shows where every term has one sign, or a large partial sum is taken back later.
+
+    fp32 scales: rounded sums, (kt + 16) 2^-23 of the magnitudes as above.  e8m0: each of a chain's 4 kt MMAs, at most 256,
+    may lose one unit of the last place of its running sum, which the magnitudes bound, and the ranges' sums are rounded."""
+    kt = (k + 127) // 128
+    half = kt // 2 * 128
+    a, w = randn((m, k), 25).abs(), randn((n, k), 26, 0.02).abs()
+    if signs == "cancel":
+        a[:, half:2 * half] = a[:, :half]
+        w[:, half:2 * half] = -w[:, :half] * (1 + randn((n, half), 27, 0.1))
+    aq, a_s = rows_fp8(a, scale)
+    wq, w_s = blocks_fp8(w, scale)
+    y = moe.Fp8Linear(wq, w_s)(moe.Fp8Tensor.from_parts(aq, a_s), torch.empty(m, n, device="cuda"))
+    A, W = wide_rows(aq, a_s), wide_blocks(wq, w_s)
+    magnitude = A.abs() @ W.abs().t()
+    tol = magnitude * 2.0 ** -23 * (kt + 16 + (4 * min(kt, 64) if scale == "e8m0" else 0))
+    if signs == "cancel":
+        assert ((A @ W.t()).abs() < 0.1 * magnitude).all()
+    assert ((y.double() - A @ W.t()).abs() <= tol).all()
+
+
 def check_gated(moe, m, k, n, scale, seed=30):
     aq, a_s = rows_fp8(randn((m, k), seed), scale)
     g, u = blocks_fp8(randn((n, k), seed + 1, 0.05), scale), blocks_fp8(randn((n, k), seed + 2, 0.05), scale)
