@@ -2,7 +2,7 @@
 // in the GEMM's epilogue, so the two fp32 products never leave the SM.
 //
 // A unit is 128 tokens x 128 features: 256 interleaved gate/up rows, in one
-// CTA or split over a cluster of 2, 4 or 8 CTAs.  The CTAs of a cluster exchange
+// CTA or split over a cluster of 2 or 4 CTAs, or its K over 2, 4 or 8.  The CTAs of a cluster exchange
 // their rows' amax through distributed shared memory before they quantise.
 // Bound like the plain one; the epilogue of a unit (SiLU's exponential and quotient,
 // two special-function operations a feature: 2000 cycles) is not covered by the next
@@ -28,7 +28,8 @@ static Plan plan_gated(const GemmCall& c, const Args& a) {
     const double bytes = memory_bytes(c, true);
     for (int cl = 1; cl <= MAX_CLUSTER; cl *= 2) {
         const int grp = cl, bn = BUF_COLS / cl, slots = cluster_slots(sms, cl);
-        if (2 * stage_cost(grp, bn, a.a_rows) <= ring_max(true)) {
+        // rows over eight CTAs: two stages of eight K blocks do not fit beside 72 token rows and more
+        if (cl <= 4) {
             const double us = plan_us((double)((units + slots - 1) / slots), a.kt, block_us(grp, bn), fixed_us(bn), bytes) +
                               (cl > 1 ? 0.126 : 0.0);
             if (best.bn == 0 || us < best_us) {
@@ -61,8 +62,7 @@ cudaError_t launch_fp8_gated(const GemmCall& c, cudaStream_t s) {
     switch (p.grp) {
         case 1: return launch<1, true>(c, p, a, s);
         case 2: return launch<2, true>(c, p, a, s);
-        case 4: return launch<4, true>(c, p, a, s);
-        default: return launch<8, true>(c, p, a, s);
+        default: return launch<4, true>(c, p, a, s);
     }
 }
 

@@ -72,7 +72,7 @@ constexpr int tail_bytes(int grp, bool gated) { return gated ? TAIL_GATED : grp 
 __host__ __device__ inline int sa_pitch(int a_rows, bool e8m0) { return e8m0 ? (a_rows + 15) / 16 * 16 : a_rows * 4; }
 // Bytes of a stage: GRP blocks of operands.
 inline int stage_cost(int grp, int bn, int a_rows) { return grp * (bn + a_rows) * 128; }
-inline int ring_max(bool gated) { return SMEM_MAX - 1024 - (gated ? TAIL_GATED : TAIL_PLAIN); }
+inline int ring_max() { return SMEM_MAX - 1024 - TAIL_PLAIN; }         // plain
 // Shared memory of a CTA that leaves room for a second one on the SM.
 constexpr int SMEM_HALF = 113 * 1024 - 2048;
 
@@ -389,15 +389,14 @@ __device__ __forceinline__ void epi_gated(const Args& a, EpiCtx& x, const float 
     }
     if (r < valid && !dead) {
         uint8_t* dst = a.hq + (int64_t)(m0 + r) * a.ld_hq + f0;
-        constexpr int V = HALF >= 32 ? 4 : 2;                  // words a store: rows start on 16 bytes
+        static_assert(HALF >= 32, "16 codes a store");         // rows start on 16 bytes
 #pragma unroll
-        for (int i = 0; i < HALF / 8 && !staged; i += V) {
-            if (f0 + 4 * (i + V) <= a.N) {
-                if constexpr (V == 4) *reinterpret_cast<uint4*>(dst + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-                else *reinterpret_cast<uint2*>(dst + 4 * i) = make_uint2(w[i], w[i + 1]);
+        for (int i = 0; i < HALF / 8 && !staged; i += 4) {
+            if (f0 + 4 * (i + 4) <= a.N) {
+                *reinterpret_cast<uint4*>(dst + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
             } else {
 #pragma unroll
-                for (int b = 0; b < 4 * V; ++b)
+                for (int b = 0; b < 16; ++b)
                     if (f0 + 4 * i + b < a.N) dst[4 * i + b] = (uint8_t)(w[i + b / 4] >> (8 * (b & 3)));
             }
         }

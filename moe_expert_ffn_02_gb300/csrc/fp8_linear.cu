@@ -17,7 +17,7 @@ static Plan plan_plain(const GemmCall& c, const Args& a) {
     for (int bn = 16; bn <= BUF_COLS; bn += 16) {
         const int grp = bn <= 32 ? 8 : bn <= 64 ? 4 : bn <= 128 ? 2 : 1;
         if (grp == 1 && bn != 256) continue;                   // 256: both halves in whole scale blocks
-        if (2 * stage_cost(grp, bn, a.a_rows) > ring_max(false)) continue;
+        if (2 * stage_cost(grp, bn, a.a_rows) > ring_max()) continue;
         const int nt = (rows + bn - 1) / bn, groups = (a.kt + grp - 1) / grp;
         const long long units = (long long)mt * nt;
         if (units > 0x3FFFFFFF) continue;

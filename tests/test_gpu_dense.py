@@ -390,6 +390,13 @@ def test_gated_against_64_bits(moe, m, k, n, scale):
     check_gated(moe, m, k, n, scale)
 
 
+@pytest.mark.parametrize("m", [2, 40])
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+def test_gated_of_few_tokens_and_rows_too_long_for_their_form(moe, m, scale):
+    """More than 4 x 512 K blocks: the form of many tokens takes the call."""
+    check_gated(moe, m, 263000, 24, scale)
+
+
 @pytest.mark.parametrize("scale", ["f32", "e8m0"])
 def test_rows_do_not_depend_on_the_batch(moe, scale):
     """Up to 64 tokens, tile widths follow the batch size but a token's bits do
