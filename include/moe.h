@@ -343,8 +343,10 @@ moe_status moe_profile_read(moe_layer* layer, float* stage_ms, int32_t n_stages)
  * Value = E4M3(q) * s.  Scales are fp32, or powers of two in eight bits
  * (E8M0: 2^(b - 127), 255 is NaN).  A producer writes s = amax/448 of the 128
  * columns (E8M0: the smallest power of two not below that), or 1 where
- * amax/448 is below 2^-126; NaN and infinity are not hidden: they make the
- * group's scale NaN or infinite and its codes NaN. */
+ * amax/448 is below 2^-126; NaN and infinity are not hidden: a NaN makes the
+ * group's scale and all its codes NaN, an infinity makes the scale infinite
+ * (E8M0: NaN) and its own code NaN (E8M0: all codes).  The codes of an infinite
+ * scale's finite values are zeros, and their value, 0 * infinity, is NaN. */
 typedef enum { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
 typedef enum { MOE_SCALE_F32 = 0, MOE_SCALE_E8M0 = 1 } moe_scale_type;
 

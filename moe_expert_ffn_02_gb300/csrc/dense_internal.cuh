@@ -33,7 +33,8 @@ constexpr uint32_t LANDING_LIMIT_US = 2000000u;
 // the rounded quotient's bits (a non-zero mantissa rounds the exponent up).  A
 // group whose quotient lies below the normal range (2^-126) gets scale 1, so
 // 1 / s is finite and its codes are zeros.  NaN and infinity give a NaN (e8m0:
-// code 255) or infinite scale: they are not hidden.
+// code 255) or infinite scale: they are not hidden.  (With an infinite scale, 1 / s
+// is 0: finite values get code 0, infinite ones NaN.)
 // `held` is what the scale array stores (the float's bits, or the byte).
 __device__ __forceinline__ float group_scale(float amax, bool e8m0, uint32_t& held) {
     float s = __fdiv_rn(amax, 448.0f);

@@ -496,6 +496,53 @@ def test_non_numbers_stay_in_their_row_and_column(moe, m):
     assert s[0].all() and s[:, m // 2].all() and int(s.sum()) == m + h.s.shape[0] - 1      # feature 77's group, row m // 2
 
 
+@pytest.mark.parametrize("m,k,n", [(1, 300, 260), (40, 300, 260), (200, 300, 260), (600, 1000, 1500), (3, 70000, 40), (70, 9000, 300)])
+@pytest.mark.parametrize("what", ["code", "weight", "scale", "weight scale"])
+def test_non_numbers_with_e8m0_scales(moe, m, k, n, what):
+    """A NaN code or scale (255) reaches its row, its column or its scale block's 128 columns, and nothing else."""
+    aq, a_s = rows_fp8(randn((m, k), 72), "e8m0")
+    wq, w_s = blocks_fp8(randn((n, k), 73, 0.05), "e8m0")
+    bad = torch.zeros(m, n, dtype=torch.bool, device="cuda")
+    if what == "code":
+        aq.view(torch.uint8)[m // 2, k - 1] = 0x7F
+        bad[m // 2] = True
+    elif what == "weight":
+        wq.view(torch.uint8)[n - 3, k // 2] = 0xFF
+        bad[:, n - 3] = True
+    elif what == "scale":
+        a_s.view(torch.uint8)[k // 256, m // 2] = 255
+        bad[m // 2] = True
+    else:
+        w_s.view(torch.uint8)[-1, k // 256] = 255
+        bad[:, (n - 1) // 128 * 128:] = True
+    a = moe.Fp8Tensor.from_parts(aq, a_s)
+    y = moe.Fp8Linear(wq, w_s)(a, torch.empty(m, n, dtype=torch.float32, device="cuda"))
+    assert torch.equal(torch.isnan(y), bad)
+    h = moe.Fp8GatedLinear(wq, w_s, wq, w_s)(a, moe.Fp8Tensor(m, n, "e8m0"))
+    groups = pad128(bad, 1).view(m, -1, 128).any(-1)
+    assert torch.equal(torch.isnan(h.s.float()).t(), groups)
+    assert torch.equal(torch.isnan(h.q.float()), groups.repeat_interleave(128, 1)[:, :n])
+
+
+@pytest.mark.parametrize("m", [2, 200])
+def test_infinite_results_of_the_gated_projection(moe, m):
+    """An infinite h: its group's scale is infinite (e8m0: NaN), its own code NaN; finite values beside it become 0 * infinity."""
+    k, n = 128, 200
+    for scale in ("f32", "e8m0"):
+        aq, a_s = rows_fp8(torch.ones(m, k, device="cuda"), scale)
+        w, big = torch.full((n, k), 2.0 ** -10, device="cuda"), torch.full((n, k), 2.0 ** 118, device="cuda")
+        big[1:] = 2.0 ** 100
+        aq = (aq.float() * 0 + 448).to(torch.float8_e4m3fn)
+        a = moe.Fp8Tensor.from_parts(aq, (a_s.float() * 0 + 1).to(a_s.dtype) if scale == "f32" else e8m0(torch.ones_like(a_s.float())))
+        h = moe.Fp8GatedLinear(*blocks_fp8(w, scale), *blocks_fp8(big, scale))(a, moe.Fp8Tensor(m, n, scale))
+        s, q = h.s.float(), h.q.float()
+        assert torch.isnan(q[:, 0]).all() and torch.isfinite(s[1]).all() and torch.isfinite(q[:, 128:]).all()
+        if scale == "f32":
+            assert torch.isinf(s[0]).all() and (q[:, 1:128] == 0).all()
+        else:
+            assert torch.isnan(s[0]).all() and torch.isnan(q[:, :128]).all()
+
+
 def test_no_rows_is_a_no_op(moe):
     a, w = moe.Fp8Tensor(0, 256), blocks_fp8(randn((128, 256), 80), "f32")
     assert moe.Fp8Linear(*w)(a, torch.empty(0, 128, device="cuda")).shape == (0, 128)
