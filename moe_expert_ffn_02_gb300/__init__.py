@@ -778,7 +778,15 @@ class DenseFfn:
         return got
 
     def __call__(self, x, residual, y):
-        a, h = self.buffers(x.shape[0])
+        rows, dev = x.shape[0], self.down._dev
+        # the norm refuses x and residual before it starts; y has to be refused before the residual is changed, too
+        if residual is None:
+            _bad("residual is None")
+        if y.dtype not in self.down._types:
+            _bad(f"y must be bfloat16 or float32, not {y.dtype}")
+        if _rows_of(y, rows, self.down.out_features, dev, "y") < self.down.out_features:
+            _bad("y's rows overlap")
+        a, h = self.buffers(rows)
         self.norm(x, residual, out=a, res_out=residual)
         self.gate_up(a, h)
         return self.down(h, y)

@@ -786,6 +786,20 @@ def test_refusals(moe):
     lin(a, y)          # a refused call leaves the handle usable
 
 
+def test_a_refused_dense_ffn_leaves_the_residual(moe):
+    ffn, _ = block(moe)
+    x, r = randn((4, 512), 94, dtype=torch.bfloat16), randn((4, 512), 95, dtype=torch.bfloat16)
+    before, y = r.clone(), torch.empty(4, 512, device="cuda")
+    for args in ((x, r, y[:3]), (x, r, y[:, :500]), (x, r, y.half()), (x, r, y.cpu()), (x, r, y[:1].expand(4, 512)), (x, None, y),
+                 (x, r[:3], y), (x.half(), r, y), (x[:, :500], r, y), (x.float(), r, y), (x, r, y.t().contiguous().t())):
+        with pytest.raises(moe.MoeError):
+            ffn(*args)
+        torch.cuda.synchronize()
+        assert torch.equal(r, before)
+    ffn(x, r, y)
+    assert not torch.equal(r, before)
+
+
 @pytest.mark.parametrize("tokens", [8, 100])
 def test_the_example_runs(moe, tokens):
     """The dense FFN and the expert layer in one captured step; the script checks its residual stream itself."""
