@@ -759,13 +759,15 @@ class DenseFfn:
     norm.  The intermediate E4M3 buffers are kept between calls, so calls of
     one object belong on one stream at a time.  They are made per power of two
     of rows and never freed while the object lives: a captured graph may go on
-    using them whatever sizes are called in between."""
+    using them whatever sizes are called in between.  Every stream that a call
+    ran on is recorded with torch's allocator, so that dropping the object while
+    its kernels are queued is safe (a graph needs the object as long as it is replayed)."""
 
     def __init__(self, norm: RmsNorm, gate_up: Fp8GatedLinear, down: Fp8Linear):
         if gate_up.in_features != norm.cols or down.in_features != gate_up.out_features or gate_up.scale != down.scale:
             _bad("norm, gate_up and down do not fit together")
         self.norm, self.gate_up, self.down = norm, gate_up, down
-        self._store, self._views = {}, {}
+        self._store, self._views, self._streams = {}, {}, {}
 
     def buffers(self, rows: int):
         got = self._views.get(rows)
@@ -774,8 +776,19 @@ class DenseFfn:
             if cap not in self._store:
                 self._store[cap] = [Fp8Tensor(cap, n, self.gate_up.scale, self.gate_up.device)
                                     for n in (self.norm.cols, self.gate_up.out_features)]
+                self._streams.clear()
             got = self._views[rows] = [t.first(rows) for t in self._store[cap]]
         return got
+
+    def _record_stream(self, handle: int):
+        """The current stream, seen for the first time (or since the last buffers were made), uses all of them."""
+        import torch
+        stream = torch.cuda.current_stream(self.down._dev)
+        for pair in self._store.values():
+            for t in pair:
+                t.q.record_stream(stream)
+                t.s.record_stream(stream)
+        self._streams[handle] = True
 
     def __call__(self, x, residual, y):
         rows, dev = x.shape[0], self.down._dev
@@ -787,6 +800,9 @@ class DenseFfn:
         if _rows_of(y, rows, self.down.out_features, dev, "y") < self.down.out_features:
             _bad("y's rows overlap")
         a, h = self.buffers(rows)
+        stream = _stream(dev)
+        if stream not in self._streams:
+            self._record_stream(stream)
         self.norm(x, residual, out=a, res_out=residual)
         self.gate_up(a, h)
         return self.down(h, y)

@@ -625,6 +625,29 @@ def test_another_stream_and_a_graph(moe):
         assert torch.equal(y, ref) and torch.equal(rs, ref_r)
 
 
+def test_a_dropped_dense_ffn_keeps_its_buffers_for_another_stream(moe):
+    """Made on one stream, called on another and dropped while that one still has its kernels queued."""
+    first, _ = block(moe)
+    ffn = moe.DenseFfn(first.norm, first.gate_up, first.down)       # the weights live on
+    x, r = randn((300, 512), 96, dtype=torch.bfloat16), randn((300, 512), 97, 2.0, torch.bfloat16)
+    y = torch.zeros(300, 512, dtype=torch.bfloat16, device="cuda")
+    want = ffn(x, r.clone(), torch.empty_like(y))
+    side, pieces = torch.cuda.Stream(), [t for b in ffn._store[512] for t in (b.q, b.s)]
+    held = {t.untyped_storage().data_ptr(): t.untyped_storage().nbytes() for t in pieces}
+    del pieces
+    torch.cuda.synchronize()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+        ffn(x, r, y)
+    del ffn
+    new = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in held.values() for _ in range(8)]
+    assert not held.keys() & {t.data_ptr() for t in new}
+    assert not side.query()                                         # or the buffers were free by right
+    side.synchronize()
+    assert torch.equal(y, want)
+
+
 def test_repeated_calls_give_the_same_bits(moe):
     lin, y = check_linear(moe, 150, 1000, 900, "f32", torch.float32)
     aq, a_s = rows_fp8(randn((150, 1000), 20), "f32")
