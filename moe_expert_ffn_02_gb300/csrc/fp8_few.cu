@@ -34,8 +34,8 @@
 // 2 and 3 lay out the scale factors.  Ranges of more than 64 blocks take the first
 // form, whose sums are not a single chain of truncating MMAs.
 //
-// Measured: 1 x 2048 x 7168 4.3 us, 16 x 7168 x 4096 with e8m0 scales 6.8 (4.4 TB/s), 1 x 7168 x 7168 10.2 (5.0),
-// gated 1 x 7168 x 2048 8.1 (3.6): what is left is the chain from the preceding kernel's end
+// Measured: 1 x 2048 x 7168 4.35 us, 16 x 7168 x 4096 with e8m0 scales 6.8 (4.4 TB/s), 1 x 18432 x 7168 20.8 (6.4),
+// gated 1 x 7168 x 2048 8.25 (3.6), 1 x 7168 x 18432 47 (5.6): what is left is the chain from the preceding kernel's end
 // (tokens' way in, last block, join, about 2.5 us), in which only the next call's first stages are
 // copied.
 //

@@ -6,7 +6,7 @@
 // their rows' amax through distributed shared memory before they quantise.
 // Bound like the plain one; the epilogue of a unit (SiLU's exponential and quotient,
 // two special-function operations a feature: 2000 cycles) is not covered by the next
-// unit's MMAs beyond two K blocks: 7 x 4300 cycles of 200 us at 8192 x 7168 x 2048.
+// unit's MMAs beyond two K blocks: 7 x 4300 cycles of 196 us at 8192 x 7168 x 2048.
 #include "fp8_gemm.cuh"
 
 namespace moe {

@@ -32,8 +32,8 @@
 // adds the partial sums through distributed shared memory (BN = 128 and 256).
 //
 // Bound, many tokens: a 256-row block's MMAs take 512 cycles, its draining and
-// scaling with the hand-offs round it about 780 (two buffers, eight warps).  8192 tokens: 2048 x 7168 104 us
-// (2.3 PFLOP/s; the tensor pipe busy 47 % of the time), gated 7168 x 2048 200 us (2.4; 51 %).  Some hundreds
+// scaling with the hand-offs round it about 780 (two buffers, eight warps).  8192 tokens: 2048 x 7168 105 us
+// (2.3 PFLOP/s; the tensor pipe busy 47 % of the time), gated 7168 x 2048 196 us (2.45; 51 %).  Some hundreds
 // of tokens: the copies into an SM, about 118 GB/s (777 x 1992 x 1001: 8.1 us).
 #pragma once
 #include "dense_internal.cuh"
@@ -1088,7 +1088,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fp8_gemm_kernel(const __grid_cons
 inline int cluster_slots(int sms, int c) { return c <= 2 ? sms / c : c == 4 ? sms * 95 / 400 : sms * 80 / 800; }
 
 // Microseconds of a call, up to a constant, fitted to sweeps on this GPU (29 shapes, 70 to 3000 tokens, both
-// scale types, every tile height and K range: the choice is within 0.7 % of the fastest on average).
+// scale types, every tile height and K range: the choice is within 0.7 % of the fastest of them on average).
 // `waves` tiles of kr K blocks one after the other in a CTA, each with `fixed` for its start and its
 // results, against the bytes of memory_bytes; each covers part of the other.
 inline double plan_us(double waves, double kr, double block_us, double fixed, double memory_bytes) {

@@ -15,10 +15,10 @@
 // counts; a row of 7168 takes 2.5 us).  Many rows: persistent CTAs with a ring of
 // rows in shared memory, filled by bulk copies that run ahead of the
 // arithmetic; loading straight into registers leaves HBM idle while a CTA waits
-// for its row's sum (8192 x 7168 bf16: 102 us, now 65 to 67, 0.92 of the copy
+// for its row's sum (8192 x 7168 bf16: 102 us, now 67 to 69, 0.91 of the copy
 // bandwidth).  Rows off the 16-byte grid: contiguous two- and four-byte accesses,
 // a warp per scale group, and the ring with each row's 16-byte window (8192 x 7001
-// bf16 141 us, without residual 93, fp32 133; bound by its instructions and two-byte accesses).
+// bf16 141 us, without residual 100, fp32 134; bound by its instructions and two-byte accesses).
 // Short rows (256 channels at most): a warp per row.
 #include "dense_internal.cuh"
 
