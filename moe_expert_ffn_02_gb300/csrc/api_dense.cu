@@ -175,8 +175,7 @@ MOE_EXPORT moe_status moe_linear_forward(moe_linear* L, const moe_fp8_matrix* a,
         return fail(MOE_ERR_INVALID_ARG, "ldy (%lld) is less than out_features (%d)", (long long)ldy, L->d.out_features);
     moe::GemmCall c = {};
     c.lin = L;
-    c.plant = L->plant;
-    L->plant = false;
+    c.plant = L->plant.load(std::memory_order_relaxed) && L->plant.exchange(false);     // threads may share the weights
     c.aq = a->q; c.ld_aq = a->ldq; c.as = a->s; c.ld_as = a->lds;
     c.M = rows;
     c.y = y; c.ldy = ldy; c.y_f32 = y_type == MOE_F32;
@@ -198,8 +197,7 @@ MOE_EXPORT moe_status moe_gated_linear_forward(moe_linear* L, const moe_fp8_matr
         return fail(MOE_ERR_INVALID_ARG, "h's scale type (%d) is not the weights' (%d)", h->scale_type, L->d.scale_type);
     moe::GemmCall c = {};
     c.lin = L;
-    c.plant = L->plant;
-    L->plant = false;
+    c.plant = L->plant.load(std::memory_order_relaxed) && L->plant.exchange(false);     // threads may share the weights
     c.aq = a->q; c.ld_aq = a->ldq; c.as = a->s; c.ld_as = a->lds;
     c.M = rows;
     c.hq = h->q; c.ld_hq = h->ldq; c.hs = h->s; c.ld_hs = h->lds;

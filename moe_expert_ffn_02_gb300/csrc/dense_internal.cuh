@@ -3,6 +3,8 @@
 #pragma once
 #include <cuda.h>
 
+#include <atomic>
+
 #include "moe_internal.cuh"
 
 struct moe_linear {
@@ -17,7 +19,7 @@ struct moe_linear {
     uint8_t* wsf;          // e8m0: [ceil(kt / 4)][ceil(rows_pad / 128)][512 B] scale-factor blocks of the image's rows
     uint32_t* dev_status;  // device status word
     uint32_t wait_limit;
-    bool plant;            // moe_linear_debug_timeout, for the next forward call
+    std::atomic<bool> plant;  // moe_linear_debug_timeout, for the next forward call
     int few_R, few_S, few_G;  // the few-token form's rows per tile, K ranges and K blocks per stage; few_R 0: it does not fit
 };
 
