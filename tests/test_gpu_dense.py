@@ -750,7 +750,7 @@ def test_joined_ranges_wait_that_expires(moe, gated, m, k, n, scale):
 @pytest.mark.parametrize("m", [3, 200])
 @pytest.mark.parametrize("scale", ["f32", "e8m0"])
 def test_limit_counts_from_the_end_of_the_kernel_before(moe, gated, m, scale):
-    """A call that starts on SMs which a long projection ahead of it (some 250 us) leaves idle, with a limit of 60 us."""
+    """A call that starts on SMs which a long projection ahead of it (some 250 us) leaves idle, with a limit of 120 us."""
     k = 1 << 20
     ahead = moe.Fp8Linear(*blocks_fp8(randn((16, k), 131, 0.02), "f32"))
     a0, y0 = moe.Fp8Tensor.from_parts(*rows_fp8(randn((1, k), 130), "f32")), torch.empty(1, 16, device="cuda")
@@ -758,7 +758,7 @@ def test_limit_counts_from_the_end_of_the_kernel_before(moe, gated, m, scale):
     lin = moe.Fp8GatedLinear(*w, *w) if gated else moe.Fp8Linear(*w)
     a = moe.Fp8Tensor.from_parts(*rows_fp8(randn((m, 1000), 133), scale))
     y = moe.Fp8Tensor(m, 600, scale) if gated else torch.empty(m, 600, device="cuda")
-    moe.moe_linear_set_wait_limit(lin.handle, 60)
+    moe.moe_linear_set_wait_limit(lin.handle, 120)
     for _ in range(3):
         ahead(a0, y0)
         lin(a, y)
