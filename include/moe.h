@@ -445,6 +445,86 @@ moe_status moe_linear_set_wait_limit(moe_linear* linear, uint32_t microseconds);
  * them expires. */
 moe_status moe_linear_debug_timeout(moe_linear* linear);
 
+/* ---------------------------------------------------------------- experts outside the fused layer
+ * The steps around experts whose products the caller runs: the sort of the
+ * tokens by expert with the copy of their rows (dispatch), the weighted way
+ * back (combine), and the gradients of both.  Expert e of the n_experts held
+ * here is id first_expert + e; a (token, slot) pair whose id is any other has
+ * no row: it was dropped, or its expert is held elsewhere (SmallEP ranks).
+ * Rows are numbered as in moe_route_out: expert e owns rows [offsets[e],
+ * offsets[e + 1]), in ascending order of (token, slot); the outputs of
+ * moe_route fit as they are.
+ *
+ * Types bf16 and fp32 (moe_dtype).  Strides ld* count elements.  Rows whose
+ * operands all lie on 16-byte boundaries are moved 16 bytes at a time, others
+ * in smaller steps.  Every result is the same in each run: sums have a fixed
+ * order and nothing is added by atomics.  All calls may be captured into a
+ * CUDA graph. */
+#define MOE_DISPATCH_MAX_TOPK 32
+#define MOE_DISPATCH_MAX_EXPERTS 1024
+#define MOE_DISPATCH_MAX_COLS (1 << 20)
+
+/* ids given: sorts the pairs and writes expert_offsets, sorted_token (-1 past
+ * the last row) and inv_row (-1: no row).  ids NULL: inv_row is an input and
+ * the other two are not used.  x given: rows[inv_row[t][j]] = x[t] for every
+ * pair that has a row; rows behind the last stay as they were.  A row from
+ * n_rows on (and, with ids NULL, one below -1) sets MOE_DEV_BAD_ROW and is not
+ * written.  Workspace (256-byte aligned): moe_dispatch_workspace_bytes, which
+ * does not fall as tokens grows; small batches need none. */
+typedef struct {
+    int32_t tokens, top_k;
+    int32_t n_experts, first_expert;
+    const int32_t* ids;          /* [tokens][top_k]                             */
+    int32_t* expert_offsets;     /* [n_experts + 1]                             */
+    int32_t* sorted_token;       /* [tokens * top_k] token of each row          */
+    int32_t* inv_row;            /* [tokens][top_k]                             */
+    const void* x;    int64_t ldx;       /* [tokens][cols], or NULL: sort only  */
+    void* rows;       int64_t ld_rows;   /* [n_rows][cols]                      */
+    int32_t cols, n_rows;
+    int32_t x_type, reserved;
+} moe_dispatch_args;
+moe_status moe_dispatch_workspace_bytes(int32_t tokens, int32_t top_k, int32_t n_experts, size_t* bytes);
+moe_status moe_dispatch(const moe_dispatch_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/* y[t] = add[t] + sum over j of w[t][j] * o[inv_row[t][j]], one fused
+ * multiply-add per term in slot order in fp32, rounded once.  w NULL: weights
+ * of 1 (with o the gradient of the rows, y is the gradient of dispatch's x).
+ * add NULL: no addition; y may be add (same strides).  Pairs without a row
+ * are left out, whatever their weight; a row outside [-1, n_rows) sets
+ * MOE_DEV_BAD_ROW and is left out too.  The y of tokens without any row is
+ * add, or 0. */
+typedef struct {
+    int32_t tokens, top_k, cols, n_rows;
+    int32_t o_type, y_type;
+    const int32_t* inv_row;      /* [tokens][top_k]                             */
+    const float* w;              /* [tokens][top_k] or NULL                     */
+    const void* o;    int64_t ldo;       /* [n_rows][cols]                      */
+    const void* add;  int64_t ld_add;    /* [tokens][cols] of y_type, or NULL   */
+    void* y;          int64_t ldy;       /* [tokens][cols]                      */
+} moe_combine_args;
+moe_status moe_combine(const moe_combine_args* args, void* stream);
+
+/* Gradients of moe_combine (that of add is dy itself), from dy of y_type:
+ *   d_o[inv_row[t][j]] = w[t][j] * dy[t]          rounded once to o_type
+ *   d_w[t][j] = <o[inv_row[t][j]], dy[t]>         fp32, 0 without a row
+ * Either output may be NULL; o is read for d_w only.  d_o may be o (same
+ * strides).  Rows of d_o that no pair has stay as they were.  Rows are checked
+ * as in moe_combine; no two pairs may have the same row. */
+typedef struct {
+    int32_t tokens, top_k, cols, n_rows;
+    int32_t o_type, y_type;
+    const int32_t* inv_row;      /* [tokens][top_k]                             */
+    const float* w;              /* [tokens][top_k] or NULL                     */
+    const void* dy;   int64_t ld_dy;     /* [tokens][cols]                      */
+    const void* o;    int64_t ldo;       /* [n_rows][cols]                      */
+    void* d_o;        int64_t ld_d_o;    /* [n_rows][cols] or NULL              */
+    float* d_w;                  /* [tokens][top_k] or NULL                     */
+} moe_combine_grad_args;
+moe_status moe_combine_grad(const moe_combine_grad_args* args, void* stream);
+
+/* As moe_get_device_status, for these calls on the current device. */
+moe_status moe_dispatch_device_status(void* stream, uint32_t* flags);
+
 const char* moe_status_string(moe_status s);
 const char* moe_last_error(void);   /* thread-local; "" when none */
 int32_t moe_abi_version(void);

@@ -29,6 +29,8 @@ __all__ = [
     "MoeFp8Matrix", "MoeRmsnormArgs", "MoeLinearDesc", "MoeLinearWeights", "BF16", "F32", "SCALE_F32", "SCALE_E8M0",
     "moe_add_rmsnorm", "moe_rmsnorm_device_status", "moe_rmsnorm_set_wait_limit", "moe_rmsnorm_debug_timeout", "moe_linear_create", "moe_linear_destroy", "moe_linear_forward", "moe_gated_linear_forward",
     "moe_linear_device_status", "moe_linear_set_wait_limit", "moe_linear_debug_timeout", "Fp8Tensor", "RmsNorm", "Fp8Linear", "Fp8GatedLinear", "DenseFfn",
+    "MoeDispatchArgs", "MoeCombineArgs", "MoeCombineGradArgs", "moe_dispatch_workspace_bytes", "moe_dispatch", "moe_combine",
+    "moe_combine_grad", "moe_dispatch_device_status", "ExpertPlan",
 ]
 
 MODE_ROUTE, MODE_PREFILL, MODE_DECODE = 0, 1, 2
@@ -80,6 +82,27 @@ class MoeLinearDesc(ctypes.Structure):
 
 class MoeLinearWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("w", "s", "w_up", "s_up")]
+
+
+class MoeDispatchArgs(ctypes.Structure):
+    _fields_ = [*[(n, ctypes.c_int32) for n in ("tokens", "top_k", "n_experts", "first_expert")],
+                *[(n, ctypes.c_void_p) for n in ("ids", "expert_offsets", "sorted_token", "inv_row")],
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("rows", ctypes.c_void_p), ("ld_rows", ctypes.c_int64),
+                *[(n, ctypes.c_int32) for n in ("cols", "n_rows", "x_type", "reserved")]]
+
+
+_COMBINE_HEAD = [*[(n, ctypes.c_int32) for n in ("tokens", "top_k", "cols", "n_rows", "o_type", "y_type")],
+                 ("inv_row", ctypes.c_void_p), ("w", ctypes.c_void_p)]
+
+
+class MoeCombineArgs(ctypes.Structure):
+    _fields_ = [*_COMBINE_HEAD, ("o", ctypes.c_void_p), ("ldo", ctypes.c_int64), ("add", ctypes.c_void_p),
+                ("ld_add", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64)]
+
+
+class MoeCombineGradArgs(ctypes.Structure):
+    _fields_ = [*_COMBINE_HEAD, ("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64), ("o", ctypes.c_void_p),
+                ("ldo", ctypes.c_int64), ("d_o", ctypes.c_void_p), ("ld_d_o", ctypes.c_int64), ("d_w", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -144,6 +167,11 @@ def load(build_if_missing: bool = False):
             "moe_linear_device_status": ([vp, vp, ctypes.POINTER(u32)], st),
             "moe_linear_set_wait_limit": ([vp, u32], st),
             "moe_linear_debug_timeout": ([vp], st),
+            "moe_dispatch_workspace_bytes": ([i32, i32, i32, ctypes.POINTER(sz)], st),
+            "moe_dispatch": ([ctypes.POINTER(MoeDispatchArgs), vp, sz, vp], st),
+            "moe_combine": ([ctypes.POINTER(MoeCombineArgs), vp], st),
+            "moe_combine_grad": ([ctypes.POINTER(MoeCombineGradArgs), vp], st),
+            "moe_dispatch_device_status": ([vp, ctypes.POINTER(u32)], st),
             "moe_status_string": ([st], ctypes.c_char_p),
             "moe_last_error": ([], ctypes.c_char_p),
             "moe_abi_version": ([], i32),
@@ -387,6 +415,31 @@ def moe_linear_debug_timeout(linear: int) -> None:
     _check(load().moe_linear_debug_timeout(linear))
 
 
+def moe_dispatch_workspace_bytes(tokens: int, top_k: int, n_experts: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().moe_dispatch_workspace_bytes(tokens, top_k, n_experts, ctypes.byref(n)))
+    return n.value
+
+
+def moe_dispatch(args: MoeDispatchArgs, ws: int = 0, ws_bytes: int = 0, stream: int = 0) -> None:
+    _check(load().moe_dispatch(ctypes.byref(args), ws, ws_bytes, stream))
+
+
+def moe_combine(args: MoeCombineArgs, stream: int = 0) -> None:
+    _check(load().moe_combine(ctypes.byref(args), stream))
+
+
+def moe_combine_grad(args: MoeCombineGradArgs, stream: int = 0) -> None:
+    _check(load().moe_combine_grad(ctypes.byref(args), stream))
+
+
+def moe_dispatch_device_status(stream: int = 0):
+    """Returns (status, flags) without raising, so callers can inspect both."""
+    f = ctypes.c_uint32()
+    st = load().moe_dispatch_device_status(stream, ctypes.byref(f))
+    return int(st), int(f.value)
+
+
 # ---------------------------------------------------------------- torch convenience
 
 class Layer:
@@ -626,6 +679,13 @@ assert _RMSNORM_ARGS.size == ctypes.sizeof(MoeRmsnormArgs)
 _NO_OUT = (0, 0, 0, 0, 0)
 
 
+def _packed_call(name: str, trailing):
+    """The library's entry `name` with a prototype of its own: a packed argument block, then `trailing`."""
+    fn = load()[name]
+    fn.argtypes, fn.restype = [ctypes.c_char_p, *trailing], ctypes.c_int
+    return fn
+
+
 class RmsNorm:
     """v = x + residual; n = v * rsqrt(mean(v^2) + eps) * weight.
 
@@ -640,8 +700,7 @@ class RmsNorm:
         self.weight = weight.to(torch.float32).contiguous()
         self.eps, self.cols = float(eps), weight.shape[0]
         self._w, self._dev, self._types = self.weight.data_ptr(), weight.get_device(), _dtypes()
-        self._call = load()["moe_add_rmsnorm"]          # a prototype of its own, which takes the packed block
-        self._call.argtypes, self._call.restype = [ctypes.c_char_p, ctypes.c_void_p], ctypes.c_int
+        self._call = _packed_call("moe_add_rmsnorm", [ctypes.c_void_p])
 
     def __call__(self, x, residual=None, out=None, res_out=None, y=None):
         cols, dev, rows = self.cols, self._dev, x.shape[0]
@@ -806,3 +865,153 @@ class DenseFfn:
         self.norm(x, residual, out=a, res_out=residual)
         self.gate_up(a, h)
         return self.down(h, y)
+
+
+# ---------------------------------------------------------------- experts outside the fused layer (torch convenience)
+
+_DISPATCH_ARGS = struct.Struct("@iiiiPPPPPqPqiiii")
+_COMBINE_ARGS = struct.Struct("@iiiiiiPPPqPqPq")
+_COMBINE_GRAD_ARGS = struct.Struct("@iiiiiiPPPqPqPqP")
+assert _DISPATCH_ARGS.size == ctypes.sizeof(MoeDispatchArgs)
+assert _COMBINE_ARGS.size == ctypes.sizeof(MoeCombineArgs) and _COMBINE_GRAD_ARGS.size == ctypes.sizeof(MoeCombineGradArgs)
+
+
+class ExpertPlan:
+    """The order of a batch's (token, slot) pairs by expert, and the moves that follow it.
+
+    dispatch(ids, x, rows) sorts the pairs of ids (int32 [tokens][top_k]) and
+    copies x's rows into that order; sort(ids) only sorts.  The other calls use
+    the order made last:
+
+        combine(rows, w, y, add)     y[t] = add[t] + sum of w[t][j] * rows[row of (t, j)]
+        combine_grad(dy, rows, w, d_rows, d_w)
+        dispatch_grad(d_rows, dx)    dx[t] = sum of d_rows[row of (t, j)]
+
+    Only ids in [first_expert, first_expert + n_experts) have rows.  The order
+    is in expert_offsets [n_experts + 1], sorted_token [tokens * top_k] (the
+    token of each row, -1 past the last) and inv_row [tokens][top_k] (-1: no
+    row), int32, valid for the tokens sorted last.  rows may have fewer rows
+    than there are pairs; a pair whose row does not fit is left out and flagged
+    (device_status).
+
+    The buffers serve batches of up to `tokens` tokens, are never remade and
+    belong to one stream at a time: a captured graph goes on using them, and
+    two graphs that may run side by side need a plan each."""
+
+    def __init__(self, tokens: int, top_k: int, n_experts: int, first_expert: int = 0, device=None):
+        import torch
+        need = moe_dispatch_workspace_bytes(tokens, top_k, n_experts)
+        if not 0 <= first_expert <= 2 ** 31 - 1 - n_experts:
+            _bad(f"first_expert = {first_expert}")
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if device.type != "cuda":
+            _bad("device must be a CUDA device")
+        self.max_tokens, self.top_k, self.n_experts, self.first_expert = tokens, top_k, n_experts, first_expert
+        self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        self.expert_offsets = torch.zeros(n_experts + 1, dtype=torch.int32, device=device)
+        self._token, self._inv = (torch.full((max(tokens * top_k, 1),), -1, dtype=torch.int32, device=device) for _ in range(2))
+        self._dev, self._types, self._int = self._ws.get_device(), _dtypes(), torch.int32
+        self._f32 = torch.float32
+        self._ptrs = (self.expert_offsets.data_ptr(), self._token.data_ptr(), self._inv.data_ptr())
+        self._ws_at = (self._ws.data_ptr(), self._ws.numel())
+        vp = ctypes.c_void_p
+        self._dispatch = _packed_call("moe_dispatch", [vp, ctypes.c_size_t, vp])
+        self._combine = _packed_call("moe_combine", [vp])
+        self._grad = _packed_call("moe_combine_grad", [vp])
+        self._bind(0)
+
+    def _bind(self, tokens):
+        self.tokens = tokens
+        self.sorted_token = self._token[:tokens * self.top_k]
+        self.inv_row = self._inv[:tokens * self.top_k].view(tokens, self.top_k)
+
+    def _check_ids(self, ids):
+        if ids.dtype is not self._int or ids.dim() != 2 or ids.shape[1] != self.top_k or not ids.is_contiguous():
+            _bad(f"ids must be contiguous int32 [tokens][{self.top_k}]")
+        if ids.get_device() != self._dev:
+            _bad(f"ids must be on CUDA device {self._dev}")
+        if ids.shape[0] > self.max_tokens:
+            _bad(f"the plan holds {self.max_tokens} tokens, not {ids.shape[0]}")
+
+    def _matrix(self, t, what, cols=None, rows=None):
+        """Type, pointer, row stride and shape of a matrix operand."""
+        kind = self._types.get(t.dtype)
+        if kind is None or t.dim() != 2:
+            _bad(f"{what} must be bfloat16 or float32 with two dimensions")
+        n, c = t.shape
+        return kind, t.data_ptr(), _rows_of(t, n if rows is None else rows, c if cols is None else cols, self._dev, what), n, c
+
+    def _weight(self, w, what):
+        if w.dtype is not self._f32 or w.shape != (self.tokens, self.top_k) or not w.is_contiguous() or w.get_device() != self._dev:
+            _bad(f"{what} must be contiguous float32 [{self.tokens}][{self.top_k}] on CUDA device {self._dev}")
+        return w.data_ptr()
+
+    def sort(self, ids):
+        self.dispatch(ids)
+
+    def dispatch(self, ids, x=None, rows=None):
+        """Sorts by ids (None: keeps the order made before) and, with x and rows, copies."""
+        t = self.tokens
+        if ids is not None:
+            self._check_ids(ids)
+            t = ids.shape[0]
+        kind = xp = ldx = rp = ldr = cols = n_rows = 0
+        if x is not None:
+            kind, xp, ldx, _, cols = self._matrix(x, "x", rows=t)
+            if rows is None or rows.dtype is not x.dtype:
+                _bad("rows must be given, in x's type")
+            _, rp, ldr, n_rows, _ = self._matrix(rows, "rows", cols)
+        elif rows is not None or ids is None:
+            _bad("x is missing")
+        o, tok, inv = self._ptrs
+        stream = _stream(self._dev)
+        # a tensor without elements has no address: with no tokens nothing is read there
+        ip = 0 if ids is None else ids.data_ptr() or o
+        st = self._dispatch(_DISPATCH_ARGS.pack(t, self.top_k, self.n_experts, self.first_expert, ip, o, tok, inv,
+                                                xp, ldx, rp, ldr, cols, n_rows, kind, 0), *self._ws_at, stream)
+        if st != MOE_OK:
+            _check(st)
+        if t != self.tokens:
+            self._bind(t)
+        return rows
+
+    def combine(self, rows, w, y, add=None):
+        """y[t] = add[t] + sum over t's rows of w[t][j] * rows[row]; w None: weights of 1; y may be add."""
+        okind, op, ldo, n_rows, cols = self._matrix(rows, "rows")
+        ykind, yp, ldy, _, _ = self._matrix(y, "y", cols, self.tokens)
+        ap = lda = 0
+        if add is not None:
+            akind, ap, lda, _, _ = self._matrix(add, "add", cols, self.tokens)
+            if akind != ykind:
+                _bad("add must have y's type")
+        wp = 0 if w is None else self._weight(w, "w")
+        st = self._combine(_COMBINE_ARGS.pack(self.tokens, self.top_k, cols, n_rows, okind, ykind, self._ptrs[2], wp, op, ldo,
+                                              ap, lda, yp, ldy), _stream(self._dev))
+        if st != MOE_OK:
+            _check(st)
+        return y
+
+    def dispatch_grad(self, d_rows, dx):
+        """dx[t] = sum over t's rows of d_rows[row]."""
+        return self.combine(d_rows, None, dx)
+
+    def combine_grad(self, dy, rows, w, d_rows=None, d_w=None):
+        """d_rows[row] = w[t][j] * dy[t] (d_rows may be rows) and d_w[t][j] = <rows[row], dy[t]>, 0 without a row."""
+        ykind, gp, ldg, _, cols = self._matrix(dy, "dy", rows=self.tokens)
+        okind, op, ldo, n_rows, _ = self._matrix(rows, "rows", cols)
+        dp = ldd = 0
+        if d_rows is None and d_w is None:
+            _bad("no output")
+        if d_rows is not None:
+            dkind, dp, ldd, _, _ = self._matrix(d_rows, "d_rows", cols, n_rows)
+            if dkind != okind:
+                _bad("d_rows must have rows' type")
+        wp = 0 if w is None else self._weight(w, "w")
+        dwp = 0 if d_w is None else self._weight(d_w, "d_w")
+        st = self._grad(_COMBINE_GRAD_ARGS.pack(self.tokens, self.top_k, cols, n_rows, okind, ykind, self._ptrs[2], wp, gp, ldg,
+                                                op, ldo, dp, ldd, dwp), _stream(self._dev))
+        if st != MOE_OK:
+            _check(st)
+
+    def device_status(self):
+        return moe_dispatch_device_status(_stream(self._dev))

@@ -1,38 +1,18 @@
 // C ABI of the dense operators (declared in include/moe.h): argument checks,
 // weight ownership and launches.
+#include "api_common.cuh"
 #include "dense_internal.cuh"
 
 #include <climits>
-#include <cstdarg>
-#include <cstdio>
 #include <new>
 
-#define MOE_EXPORT extern "C" __attribute__((visibility("default")))
+using moe::aligned;
+using moe::cuda_fail;
+using moe::fail;
+using moe::kDefaultWaitLimitUs;
+using moe::read_status;
 
 namespace {
-
-moe_status fail(moe_status s, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    try {
-        moe::set_last_error(buf);
-    } catch (...) {          // no memory for the message: the status still says what happened
-    }
-    return s;
-}
-
-// The runtime keeps a failed call's error until somebody asks; left there, the next checked launch would report it.
-moe_status cuda_fail(cudaError_t e, const char* what) {
-    cudaGetLastError();
-    return fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-constexpr uint32_t kDefaultWaitLimitUs = 2000000u;
 
 moe_status check_fp8(const moe_fp8_matrix& m, int rows, int cols, const char* what) {
     if (!m.q || !m.s) return fail(MOE_ERR_INVALID_ARG, "%s: codes or scales are NULL", what);
@@ -204,21 +184,6 @@ MOE_EXPORT moe_status moe_gated_linear_forward(moe_linear* L, const moe_fp8_matr
     cudaError_t e = moe::launch_fp8_gated(c, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "FP8 gated linear");
 }
-
-namespace {
-// Synchronise, read and clear a device status word.
-moe_status read_status(uint32_t* word, void* stream, uint32_t* flags) {
-    uint32_t v = 0;
-    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-    if (e == cudaSuccess) e = cudaMemcpy(&v, word, 4, cudaMemcpyDeviceToHost);
-    if (e == cudaSuccess && v) e = cudaMemset(word, 0, 4);
-    if (e != cudaSuccess) return cuda_fail(e, "reading the status word");
-    if (flags) *flags = v;
-    if (v & MOE_DEV_WAIT_TIMEOUT) return fail(MOE_ERR_TIMEOUT, "a kernel wait gave up (status 0x%x)", v);
-    if (v) return fail(MOE_ERR_DEVICE_CHECK, "a kernel flagged bad data (status 0x%x)", v);
-    return MOE_OK;
-}
-}  // namespace
 
 MOE_EXPORT moe_status moe_linear_device_status(moe_linear* L, void* stream, uint32_t* flags) {
     moe_status st = check_linear(L);
