@@ -525,6 +525,61 @@ moe_status moe_combine_grad(const moe_combine_grad_args* args, void* stream);
 /* As moe_get_device_status, for these calls on the current device. */
 moe_status moe_dispatch_device_status(void* stream, uint32_t* flags);
 
+/* ---------------------------------------------------------------- 4-bit weights
+ * Products of bf16 rows with weights of 4 bits, one matrix or one per expert:
+ *   W[n][k] = (code[n][k] - zero[n][k / group]) * s[n][k / group]
+ *   y[r] = x[r] W^T,  or gated  y[r] = SiLU(x[r] Wg^T) * (x[r] Wu^T)
+ * Codes are 0 to 15, two a byte, the even channel in the low four bits, rows
+ * of ceil(in / 2) bytes; scales bf16 or fp32; zero points one byte each, 0 to
+ * 127 (its low seven bits), or 8 everywhere.  All sizes may be ragged; group is a multiple of
+ * 32 (in_features or more: one scale per row).  With more than one expert, expert e
+ * takes the rows [offsets[e], offsets[e + 1]) of y, as moe_dispatch and
+ * moe_route number them; rows outside all of them stay as they were.  token
+ * given: row r reads row token[r] of x (the sorted_token of those calls), so
+ * that x need not be copied into the experts' order.
+ * Accuracy: codes less zero points and their products with x are exact; they
+ * are summed over 32 or 64 channels by the tensor cores, scaled in fp32 and
+ * added in fp32: (in / 32 + 32) 2^-23 of the sum of the products' magnitudes,
+ * before SiLU and the one rounding to y_type.  A group's sum before its scale
+ * has to fit fp32.  Which form adds up a call follows from its sizes. */
+#define MOE_INT4_MAX_FEATURES (1 << 20)
+typedef struct moe_int4 moe_int4;    /* opaque; owned by the library */
+typedef struct {
+    int32_t in_features, out_features;
+    int32_t n_experts;           /* 1 to MOE_DISPATCH_MAX_EXPERTS               */
+    int32_t gated;               /* 0 or 1                                      */
+    int32_t group;               /* input channels that share a scale           */
+    int32_t scale_type;          /* moe_dtype                                   */
+} moe_int4_desc;
+typedef struct {                 /* read only during moe_int4_create            */
+    const uint8_t* q;            /* [n_experts][out][ceil(in / 2)]              */
+    const void* s;               /* [n_experts][out][ceil(in / group)]          */
+    const uint8_t* z;            /* the same shape, or NULL                     */
+    const uint8_t* q_up;         /* gated only (q, s, z are then the gate's)    */
+    const void* s_up;
+    const uint8_t* z_up;         /* given where z is                            */
+} moe_int4_weights;
+moe_status moe_int4_create(const moe_int4_desc* desc, const moe_int4_weights* w, void* stream, moe_int4** out);
+moe_status moe_int4_destroy(moe_int4* weights);      /* synchronises the device first */
+
+/* Offsets that fall or leave [0, rows] and tokens outside [0, x_rows) set
+ * MOE_DEV_BAD_ROW and are cut off (such a token reads as zeros).  y must not
+ * overlap x.  rows = 0 is a valid no-op. */
+typedef struct {
+    int32_t rows, x_rows;        /* of y and of x (the same without token)      */
+    const uint16_t* x; int64_t ldx;      /* [x_rows][in] bf16                   */
+    const int32_t* offsets;      /* [n_experts + 1]; NULL with one expert: all  */
+    const int32_t* token;        /* [rows] or NULL                              */
+    void* y;           int64_t ldy;      /* [rows][out]                         */
+    int32_t y_type, reserved;    /* moe_dtype                                   */
+} moe_int4_args;
+moe_status moe_int4_forward(moe_int4* weights, const moe_int4_args* args, void* stream);
+
+/* As moe_get_device_status and moe_set_wait_limit, for a handle's kernels.  Of
+ * a call whose wait expired, an element of y is right or as it was. */
+moe_status moe_int4_device_status(moe_int4* weights, void* stream, uint32_t* flags);
+moe_status moe_int4_set_wait_limit(moe_int4* weights, uint32_t microseconds);
+
 const char* moe_status_string(moe_status s);
 const char* moe_last_error(void);   /* thread-local; "" when none */
 int32_t moe_abi_version(void);

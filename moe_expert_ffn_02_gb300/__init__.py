@@ -31,6 +31,8 @@ __all__ = [
     "moe_linear_device_status", "moe_linear_set_wait_limit", "moe_linear_debug_timeout", "Fp8Tensor", "RmsNorm", "Fp8Linear", "Fp8GatedLinear", "DenseFfn",
     "MoeDispatchArgs", "MoeCombineArgs", "MoeCombineGradArgs", "moe_dispatch_workspace_bytes", "moe_dispatch", "moe_combine",
     "moe_combine_grad", "moe_dispatch_device_status", "ExpertPlan",
+    "MoeInt4Desc", "MoeInt4Weights", "MoeInt4Args", "moe_int4_create", "moe_int4_destroy", "moe_int4_forward",
+    "moe_int4_device_status", "moe_int4_set_wait_limit", "Int4Linear", "Int4GatedLinear", "Int4ExpertFfn",
 ]
 
 MODE_ROUTE, MODE_PREFILL, MODE_DECODE = 0, 1, 2
@@ -105,6 +107,20 @@ class MoeCombineGradArgs(ctypes.Structure):
                 ("ldo", ctypes.c_int64), ("d_o", ctypes.c_void_p), ("ld_d_o", ctypes.c_int64), ("d_w", ctypes.c_void_p)]
 
 
+class MoeInt4Desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("in_features", "out_features", "n_experts", "gated", "group", "scale_type")]
+
+
+class MoeInt4Weights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "s", "z", "q_up", "s_up", "z_up")]
+
+
+class MoeInt4Args(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("x_rows", ctypes.c_int32), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("offsets", ctypes.c_void_p), ("token", ctypes.c_void_p), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("y_type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -172,6 +188,11 @@ def load(build_if_missing: bool = False):
             "moe_combine": ([ctypes.POINTER(MoeCombineArgs), vp], st),
             "moe_combine_grad": ([ctypes.POINTER(MoeCombineGradArgs), vp], st),
             "moe_dispatch_device_status": ([vp, ctypes.POINTER(u32)], st),
+            "moe_int4_create": ([ctypes.POINTER(MoeInt4Desc), ctypes.POINTER(MoeInt4Weights), vp, ctypes.POINTER(vp)], st),
+            "moe_int4_destroy": ([vp], st),
+            "moe_int4_forward": ([vp, ctypes.POINTER(MoeInt4Args), vp], st),
+            "moe_int4_device_status": ([vp, vp, ctypes.POINTER(u32)], st),
+            "moe_int4_set_wait_limit": ([vp, u32], st),
             "moe_status_string": ([st], ctypes.c_char_p),
             "moe_last_error": ([], ctypes.c_char_p),
             "moe_abi_version": ([], i32),
@@ -440,6 +461,31 @@ def moe_dispatch_device_status(stream: int = 0):
     return int(st), int(f.value)
 
 
+def moe_int4_create(desc: MoeInt4Desc, weights: MoeInt4Weights, stream: int = 0) -> int:
+    h = ctypes.c_void_p()
+    _check(load().moe_int4_create(ctypes.byref(desc), ctypes.byref(weights), stream, ctypes.byref(h)))
+    return h.value
+
+
+def moe_int4_destroy(weights: int) -> None:
+    _check(load().moe_int4_destroy(weights))
+
+
+def moe_int4_forward(weights: int, args: MoeInt4Args, stream: int = 0) -> None:
+    _check(load().moe_int4_forward(weights, ctypes.byref(args), stream))
+
+
+def moe_int4_device_status(weights: int, stream: int = 0):
+    """Returns (status, flags) without raising, so callers can inspect both."""
+    f = ctypes.c_uint32()
+    st = load().moe_int4_device_status(weights, stream, ctypes.byref(f))
+    return int(st), int(f.value)
+
+
+def moe_int4_set_wait_limit(weights: int, microseconds: int) -> None:
+    _check(load().moe_int4_set_wait_limit(weights, microseconds))
+
+
 # ---------------------------------------------------------------- torch convenience
 
 class Layer:
@@ -679,10 +725,10 @@ assert _RMSNORM_ARGS.size == ctypes.sizeof(MoeRmsnormArgs)
 _NO_OUT = (0, 0, 0, 0, 0)
 
 
-def _packed_call(name: str, trailing):
-    """The library's entry `name` with a prototype of its own: a packed argument block, then `trailing`."""
+def _packed_call(name: str, trailing, first=None):
+    """The library's entry `name` with a prototype of its own: `first`, a packed argument block, then `trailing`."""
     fn = load()[name]
-    fn.argtypes, fn.restype = [ctypes.c_char_p, *trailing], ctypes.c_int
+    fn.argtypes, fn.restype = [*([] if first is None else [first]), ctypes.c_char_p, *trailing], ctypes.c_int
     return fn
 
 
@@ -1015,3 +1061,160 @@ class ExpertPlan:
 
     def device_status(self):
         return moe_dispatch_device_status(_stream(self._dev))
+
+
+_INT4_ARGS = struct.Struct("@iiPqPPPqii")
+assert _INT4_ARGS.size == ctypes.sizeof(MoeInt4Args)
+
+
+class _Int4Weights:
+    """Handle of 4-bit weights in the library's layout: one matrix, or one per expert."""
+    gated = False
+
+    def _create(self, mats, group, in_features):
+        import torch
+        q, s, z = mats[0]
+        self._types = _dtypes()
+        if not q.is_cuda or q.dtype is not torch.uint8 or q.dim() not in (2, 3):
+            _bad("codes must be uint8 [out][ceil(in / 2)] or [experts][out][ceil(in / 2)] CUDA tensors")
+        k = 2 * q.shape[-1] if in_features is None else in_features
+        if k < 1 or (k + 1) // 2 != q.shape[-1]:
+            _bad(f"rows of {q.shape[-1]} bytes do not hold {k} channels")
+        if not isinstance(group, int) or group < 32 or group % 32:
+            _bad(f"group must be a positive multiple of 32, not {group}")
+        groups = (*q.shape[:-1], (k + group - 1) // group)
+        for qi, si, zi in mats:
+            if qi.dtype is not torch.uint8 or qi.shape != q.shape or qi.device != q.device:
+                _bad("gate and up codes must have one shape, on one device")
+            if si.dtype not in self._types or si.dtype is not s.dtype or si.shape != groups or si.device != q.device:
+                _bad(f"scales must be bfloat16 or float32 {list(groups)} beside the codes")
+            if (zi is None) != (z is None) or (zi is not None and (zi.dtype is not torch.uint8 or zi.shape != groups or zi.device != q.device)):
+                _bad(f"zero points must be uint8 {list(groups)} beside the codes, or None for every matrix")
+        keep = [None if t is None else t.contiguous() for m in mats for t in m]
+        self.n_experts, self.out_features, self.in_features = (1 if q.dim() == 2 else q.shape[0]), q.shape[-2], k
+        self.group, self.device, self._dev = group, q.device, q.get_device()
+        self._bf16, self._int = torch.bfloat16, torch.int32
+        self.handle = None
+        # a group is no longer than the type of the call's argument can say
+        desc = MoeInt4Desc(k, self.out_features, self.n_experts, int(self.gated), min(group, 2 ** 31 - 32), self._types[s.dtype])
+        self.handle = moe_int4_create(desc, MoeInt4Weights(*[None if t is None else t.data_ptr() for t in keep]), _stream(self._dev))
+        self._call = _packed_call("moe_int4_forward", [ctypes.c_void_p], first=ctypes.c_void_p)
+
+    def _index(self, t, n, what):
+        if t.dtype is not self._int or t.shape != (n,) or not t.is_contiguous() or t.get_device() != self._dev:
+            _bad(f"{what} must be contiguous int32 [{n}] on CUDA device {self._dev}")
+        return t.data_ptr()
+
+    def __call__(self, x, y, offsets=None, token=None):
+        """y[r] = x[r] W^T (gated: SiLU of the gate's product times the up's).  With experts, expert e takes rows
+        [offsets[e], offsets[e + 1]); with token, row r of y reads row token[r] of x.  y: bfloat16 or float32."""
+        rows, x_rows = y.shape[0], x.shape[0]
+        if x.dtype is not self._bf16:
+            _bad(f"x must be bfloat16, not {x.dtype}")
+        yt = self._types.get(y.dtype)
+        if yt is None:
+            _bad(f"y must be bfloat16 or float32, not {y.dtype}")
+        ldx = _rows_of(x, x_rows if token is not None else rows, self.in_features, self._dev, "x")
+        ldy = _rows_of(y, rows, self.out_features, self._dev, "y")
+        op = 0 if offsets is None else self._index(offsets, self.n_experts + 1, "offsets")
+        tp = 0 if token is None else self._index(token, rows, "token")
+        st = self._call(self.handle, _INT4_ARGS.pack(rows, x_rows, x.data_ptr(), ldx, op, tp, y.data_ptr(), ldy, yt, 0), _stream(self._dev))
+        if st != MOE_OK:
+            _check(st)
+        return y
+
+    def device_status(self):
+        return moe_int4_device_status(self.handle, _stream(self._dev))
+
+    def close(self):
+        if getattr(self, "handle", None):
+            moe_int4_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Int4Linear(_Int4Weights):
+    """y = x W^T, W[n][k] = (code - zero) * scale of the row's group of `group` channels.
+
+    q: uint8 [out][ceil(in / 2)], or [experts][out][ceil(in / 2)], two codes a
+    byte, the even channel in the low four bits; s: bfloat16 or float32, one
+    per group; zero: uint8 0 to 127 likewise, or None (8 everywhere).  The
+    library keeps its own copy."""
+
+    def __init__(self, q, s, zero=None, group: int = 128, in_features=None):
+        self._create([(q, s, zero)], group, in_features)
+
+
+class Int4GatedLinear(_Int4Weights):
+    """h = SiLU(x Wg^T) * (x Wu^T) on two matrices as Int4Linear takes them."""
+    gated = True
+
+    def __init__(self, q_gate, s_gate, q_up, s_up, zero_gate=None, zero_up=None, group: int = 128, in_features=None):
+        self._create([(q_gate, s_gate, zero_gate), (q_up, s_up, zero_up)], group, in_features)
+
+
+class Int4ExpertFfn:
+    """The routed experts of a layer on 4-bit weights:
+
+        y[t] = add[t] + sum over j of w[t][j] * down(SiLU(gate(x[t])) * up(x[t])), the matrices of expert ids[t][j]
+
+    One sort, the gated product reading x's rows in place, the down product and
+    the combine.  ids: int32 [tokens][top_k], w: float32 likewise; pairs of ids
+    outside [first_expert, first_expert + n_experts) are held elsewhere and
+    left out.  x bfloat16, y bfloat16 or float32, add in y's type (it may be y).
+
+    Buffers are kept between calls, so calls of one object belong on one stream
+    at a time.  They are made per power of two of tokens and never freed while
+    the object lives: a captured graph may go on using them whatever sizes are
+    called in between.  Every stream that a call ran on is recorded with
+    torch's allocator, so that dropping the object while its kernels are queued
+    is safe (a graph needs the object as long as it is replayed)."""
+
+    def __init__(self, gate_up: Int4GatedLinear, down: Int4Linear, top_k: int, first_expert: int = 0):
+        if not gate_up.gated or down.gated or down.in_features != gate_up.out_features or down.n_experts != gate_up.n_experts or \
+                down._dev != gate_up._dev:
+            _bad("gate_up and down do not fit together")
+        self.gate_up, self.down, self.top_k, self.first_expert = gate_up, down, top_k, first_expert
+        ExpertPlan(0, top_k, down.n_experts, first_expert, down.device)      # refuses what no plan can have
+        self._store, self._streams = {}, {}
+
+    def buffers(self, tokens: int):
+        cap = 1 << max(tokens - 1, 0).bit_length()
+        got = self._store.get(cap)
+        if got is None:
+            import torch
+            rows = cap * self.top_k
+            got = self._store[cap] = (ExpertPlan(cap, self.top_k, self.down.n_experts, self.first_expert, self.down.device),
+                                      *(torch.empty(rows, p.out_features, dtype=torch.bfloat16, device=self.down.device)
+                                        for p in (self.gate_up, self.down)))
+            self._streams.clear()
+        return got
+
+    def _record_stream(self, handle: int):
+        """The current stream, seen for the first time (or since the last buffers were made), uses all of them."""
+        import torch
+        stream = torch.cuda.current_stream(self.down._dev)
+        for plan, *mats in self._store.values():
+            for t in (plan._ws, plan.expert_offsets, plan._token, plan._inv, *mats):
+                t.record_stream(stream)
+        self._streams[handle] = True
+
+    def __call__(self, x, ids, w, y, add=None):
+        if ids.dim() != 2 or x.dim() != 2 or x.shape[0] != ids.shape[0]:
+            _bad("x and ids must be [tokens][in] and [tokens][top_k]")
+        tokens = ids.shape[0]
+        stream = _stream(self.down._dev)
+        plan, h, o = self.buffers(tokens)
+        if stream not in self._streams:
+            self._record_stream(stream)
+        rows = tokens * self.top_k
+        h, o = h[:rows], o[:rows]
+        plan.sort(ids)
+        self.gate_up(x, h, plan.expert_offsets, plan.sorted_token)
+        self.down(h, o, plan.expert_offsets)
+        return plan.combine(o, w, y, add)

@@ -1,0 +1,153 @@
+// C ABI of the products with 4-bit weights (declared in include/moe.h):
+// argument checks, weight ownership and launches.
+#include <algorithm>
+#include <new>
+
+#include "api_common.cuh"
+#include "experts_internal.cuh"
+
+using moe::aligned;
+using moe::cuda_fail;
+using moe::fail;
+using moe::kDefaultWaitLimitUs;
+using moe::read_status;
+
+namespace {
+
+moe_status check_handle(const moe_int4* L) {
+    if (!L) return fail(MOE_ERR_INVALID_ARG, "weights is NULL");
+    int cur = -1;
+    cudaError_t e = cudaGetDevice(&cur);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (cur != L->device)
+        return fail(MOE_ERR_INVALID_ARG, "the current device (%d) is not the weights' device (%d)", cur, L->device);
+    return MOE_OK;
+}
+
+void free_all(moe_int4* L) {
+    cudaFree(L->w);
+    cudaFree(L->s);
+    cudaFree(L->z);
+    cudaFree(L->dev_status);
+    delete L;
+}
+
+}  // namespace
+
+MOE_EXPORT moe_status moe_int4_create(const moe_int4_desc* d, const moe_int4_weights* w, void* stream, moe_int4** out) {
+    if (!d || !w || !out) return fail(MOE_ERR_INVALID_ARG, "desc, weights and out must be non-NULL");
+    *out = nullptr;
+    if (d->in_features < 1 || d->out_features < 1 || d->in_features > MOE_INT4_MAX_FEATURES || d->out_features > MOE_INT4_MAX_FEATURES)
+        return fail(MOE_ERR_UNSUPPORTED, "in_features (%d) and out_features (%d) must lie in [1, %d]", d->in_features, d->out_features,
+                    MOE_INT4_MAX_FEATURES);
+    if (d->n_experts < 1 || d->n_experts > MOE_DISPATCH_MAX_EXPERTS)
+        return fail(MOE_ERR_UNSUPPORTED, "n_experts (%d) must lie in [1, %d]", d->n_experts, MOE_DISPATCH_MAX_EXPERTS);
+    if (d->gated != 0 && d->gated != 1) return fail(MOE_ERR_INVALID_ARG, "gated must be 0 or 1");
+    if (d->group < 32 || d->group % 32) return fail(MOE_ERR_UNSUPPORTED, "group (%d) must be a positive multiple of 32", d->group);
+    if (d->scale_type != MOE_BF16 && d->scale_type != MOE_F32) return fail(MOE_ERR_INVALID_ARG, "unknown scale type %d", d->scale_type);
+    if (!w->q || !w->s || (d->gated && (!w->q_up || !w->s_up))) return fail(MOE_ERR_INVALID_ARG, "a code or scale pointer is NULL");
+    if (d->gated && !w->z != !w->z_up) return fail(MOE_ERR_INVALID_ARG, "zero points for one of gate and up only");
+    const size_t ss = d->scale_type == MOE_F32 ? 4 : 2;
+    if (!aligned(w->s, ss) || (d->gated && !aligned(w->s_up, ss))) return fail(MOE_ERR_INVALID_ARG, "scales are not aligned to their elements");
+    moe_int4* L = new (std::nothrow) moe_int4{};
+    if (!L) return fail(MOE_ERR_CUDA, "out of host memory");
+    L->d = *d;
+    L->kt = (d->in_features + moe::I4_K - 1) / moe::I4_K;
+    L->d.group = std::min(d->group, L->kt * moe::I4_K);         // one scale per row
+    L->groups = (L->kt * moe::I4_K + L->d.group - 1) / L->d.group;
+    const int per = d->gated ? 8 : moe::I4_ROWS;
+    L->blocks = ((d->out_features + per - 1) / per + 3) / 4 * 4;
+    L->wait_limit = kDefaultWaitLimitUs;
+    const size_t eb = (size_t)d->n_experts * L->blocks, recs = eb * L->groups * 8;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const char* what = "device query";
+    cudaError_t e = cudaGetDevice(&L->device);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&L->num_sms, cudaDevAttrMultiProcessorCount, L->device);
+    if (e == cudaSuccess) what = "allocating weights", e = cudaMalloc(&L->w, eb * L->kt * 512);
+    if (e == cudaSuccess) what = "allocating scales", e = cudaMalloc(&L->s, recs * 2 * ss);
+    if (e == cudaSuccess && w->z) what = "allocating zero points", e = cudaMalloc(&L->z, recs * 4);
+    if (e == cudaSuccess) what = "allocating status", e = cudaMalloc(&L->dev_status, 4);
+    if (e == cudaSuccess) what = "memset", e = cudaMemsetAsync(L->dev_status, 0, 4, s);
+    if (e == cudaSuccess) what = "weight repack", e = moe::launch_int4_repack(L, w, s);
+    if (e == cudaSuccess) what = "moe_int4_create synchronise", e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) {
+        moe_status st = cuda_fail(e, what);
+        free_all(L);
+        return st;
+    }
+    *out = L;
+    return MOE_OK;
+}
+
+MOE_EXPORT moe_status moe_int4_destroy(moe_int4* L) {
+    if (!L) return fail(MOE_ERR_INVALID_ARG, "weights is NULL");
+    int cur = -1;
+    cudaError_t e = cudaGetDevice(&cur);
+    if (e == cudaSuccess && cur != L->device) e = cudaSetDevice(L->device);
+    if (e != cudaSuccess) return cuda_fail(e, "moe_int4_destroy: selecting the weights' device");
+    const int dev = L->device;
+    e = cudaDeviceSynchronize();
+    free_all(L);
+    if (cur != dev) cudaSetDevice(cur);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_int4_destroy synchronise");
+}
+
+MOE_EXPORT moe_status moe_int4_forward(moe_int4* L, const moe_int4_args* a, void* stream) {
+    moe_status st = check_handle(L);
+    if (st != MOE_OK) return st;
+    if (!a) return fail(MOE_ERR_INVALID_ARG, "args is NULL");
+    if (a->rows < 0 || a->x_rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows = %d, x_rows = %d", a->rows, a->x_rows);
+    if (a->y_type != MOE_BF16 && a->y_type != MOE_F32) return fail(MOE_ERR_INVALID_ARG, "unknown y type %d", a->y_type);
+    if (!a->offsets && L->d.n_experts > 1) return fail(MOE_ERR_INVALID_ARG, "%d experts need offsets", L->d.n_experts);
+    if (!a->token && a->x_rows != a->rows)
+        return fail(MOE_ERR_INVALID_ARG, "x has %d rows and y %d, without tokens", a->x_rows, a->rows);
+    if (a->rows == 0) return MOE_OK;
+    if (!aligned(a->offsets, 4) || !aligned(a->token, 4)) return fail(MOE_ERR_INVALID_ARG, "offsets or token is not 4-byte aligned");
+    if (!a->x || !aligned(a->x, 2)) return fail(MOE_ERR_INVALID_ARG, "x is NULL or misaligned");
+    if (!a->y || !aligned(a->y, a->y_type == MOE_F32 ? 4 : 2)) return fail(MOE_ERR_INVALID_ARG, "y is NULL or misaligned");
+    if (a->ldx < L->d.in_features) return fail(MOE_ERR_INVALID_ARG, "ldx (%lld) is less than in_features (%d)", (long long)a->ldx, L->d.in_features);
+    if (a->ldy < L->d.out_features) return fail(MOE_ERR_INVALID_ARG, "ldy (%lld) is less than out_features (%d)", (long long)a->ldy, L->d.out_features);
+    // units (8 rows by a block of 16 weight rows at the least) are numbered in 32 bits
+    if (((int64_t)a->rows / 8 + L->d.n_experts) * L->blocks > INT32_MAX)
+        return fail(MOE_ERR_UNSUPPORTED, "%d rows of %d features are too many for one call", a->rows, L->d.out_features);
+    moe::Int4Call c = {};
+    c.w = L->w;
+    c.s = static_cast<const char*>(L->s);
+    c.z = L->z;
+    c.x = a->x;
+    c.ldx = a->ldx;
+    c.offsets = a->offsets;
+    c.token = a->token;
+    c.y = a->y;
+    c.ldy = a->ldy;
+    c.status = L->dev_status;
+    const uint32_t g32 = L->d.group / 32;
+    c.group_inv = ((uint64_t(1) << 32) + g32 - 1) / g32;
+    c.rows = a->rows;
+    c.x_rows = a->x_rows;
+    c.N = L->d.out_features;
+    c.K = L->d.in_features;
+    c.E = L->d.n_experts;
+    c.blocks = L->blocks;
+    c.kt = L->kt;
+    c.groups = L->groups;
+    c.wait_limit = L->wait_limit;
+    c.s_f32 = L->d.scale_type == MOE_F32;
+    c.y_f32 = a->y_type == MOE_F32;
+    c.gated = L->d.gated;
+    c.x_vec = aligned(a->x, 16) && a->ldx % 8 == 0;
+    cudaError_t e = moe::launch_int4_few(L, c, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "4-bit product");
+}
+
+MOE_EXPORT moe_status moe_int4_device_status(moe_int4* L, void* stream, uint32_t* flags) {
+    moe_status st = check_handle(L);
+    return st != MOE_OK ? st : read_status(L->dev_status, stream, flags);
+}
+
+MOE_EXPORT moe_status moe_int4_set_wait_limit(moe_int4* L, uint32_t microseconds) {
+    if (!L) return fail(MOE_ERR_INVALID_ARG, "weights is NULL");
+    if (microseconds == 0) return fail(MOE_ERR_INVALID_ARG, "limit must be positive");
+    L->wait_limit = microseconds;
+    return MOE_OK;
+}

@@ -4,7 +4,60 @@
 #pragma once
 #include "moe_internal.cuh"
 
+// ---------------------------------------------------------------------------
+// Image of 4-bit weights.  A block is 16 rows of one expert's matrix (gated:
+// 8 gate rows, then the 8 up rows of the same features), a tile 64 input
+// channels of a block in 512 bytes, 16 for each lane of a warp.  Lane
+// 4 g + q has, one word of 8 codes each, the channels 8 q .. 8 q + 7 and
+// 32 + 8 q .. 32 + 8 q + 7 of row g, then the same of row g + 8: what it
+// feeds to a 16 x 16 tensor-core operand, so a warp takes its operand by one
+// 16-byte load per lane.  In a word, nibbles 0 to 3 are the even channels and
+// 4 to 7 the odd ones: (word >> 4 i) & 0x000F000F are channels 2 i and 2 i + 1
+// as two halves.  Tiles of a block follow one another; channels past the
+// matrix meet zeros of x.
+// Scales: [expert][block][group][8] pairs (row g, row g + 8); zero points
+// likewise as 128 + z in bf16.  Rows past the matrix have scales of zero.
+// ---------------------------------------------------------------------------
+struct moe_int4 {
+    moe_int4_desc d;
+    int device;
+    int num_sms;
+    int blocks;            // per expert, a multiple of 4
+    int kt;                // tiles per block: ceil(in / 64)
+    int groups;            // per row, over the tiles' 64 kt channels
+    uint4* w;              // [expert][block][kt][32]
+    void* s;               // [expert][block][groups][8] pairs of bf16 or fp32
+    uint32_t* z;           // [expert][block][groups][8] pairs of bf16, or NULL: 136
+    uint32_t* dev_status;  // device status word
+    uint32_t wait_limit;
+};
+
 namespace moe {
+
+constexpr int I4_K = 64;               // channels of a tile
+constexpr int I4_ROWS = 16;            // rows of a block
+constexpr uint32_t I4_ZERO = 0x43084308u;   // 136 = 128 + 8 in bf16, twice
+
+struct Int4Call {
+    const uint4* w;
+    const char* s;
+    const uint32_t* z;
+    const uint16_t* x;
+    int64_t ldx;
+    const int32_t* offsets;
+    const int32_t* token;
+    void* y;
+    int64_t ldy;
+    uint32_t* status;
+    uint64_t group_inv;    // ceil(2^32 / (group / 32)): 32-channel step n is in group n * group_inv >> 32
+    int rows, x_rows;
+    int N, K, E, blocks, kt, groups;
+    uint32_t wait_limit;
+    bool s_f32, y_f32, gated, x_vec;
+};
+
+cudaError_t launch_int4_repack(const moe_int4* L, const moe_int4_weights* w, cudaStream_t s);
+cudaError_t launch_int4_few(const moe_int4* L, const Int4Call& c, cudaStream_t s);
 
 // Tokens per chunk of the multi-CTA sort and the chunks of a call, and no fewer than any smaller batch has
 // (the workspace, int32 [most_chunks + 1][n_experts]).  chunks = 0: one kernel does it without workspace.

@@ -1,0 +1,39 @@
+"""Host-only checks of the C ABI of the products with 4-bit weights: argument
+errors are found before anything touches CUDA."""
+import ctypes
+
+import pytest
+
+import moe_expert_ffn_02_gb300 as moe
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return moe.load(build_if_missing=True)
+
+
+DESC = dict(in_features=128, out_features=64, n_experts=1, gated=0, group=64, scale_type=moe.BF16)
+WEIGHTS = dict(q=0x1000, s=0x2000, z=0x3000, q_up=0x4000, s_up=0x5000, z_up=0x6000)
+
+
+@pytest.mark.parametrize("desc,weights,code", [
+    (dict(in_features=0), {}, 2), (dict(out_features=0), {}, 2), (dict(in_features=(1 << 20) + 1), {}, 2), (dict(out_features=1 << 21), {}, 2),
+    (dict(n_experts=0), {}, 2), (dict(n_experts=1025), {}, 2), (dict(gated=2), {}, 1), (dict(group=0), {}, 2), (dict(group=-32), {}, 2),
+    (dict(group=48), {}, 2), (dict(scale_type=2), {}, 1), ({}, dict(q=None), 1), ({}, dict(s=None), 1), ({}, dict(s=0x2001), 1),
+    (dict(scale_type=moe.F32), dict(s=0x2002), 1), (dict(gated=1), dict(q_up=None), 1), (dict(gated=1), dict(s_up=None), 1),
+    (dict(gated=1), dict(s_up=0x5001), 1), (dict(gated=1), dict(z_up=None), 1), (dict(gated=1), dict(z=None), 1),
+])
+def test_create_refuses(lib, desc, weights, code):
+    h = ctypes.c_void_p()
+    d, w = moe.MoeInt4Desc(**{**DESC, **desc}), moe.MoeInt4Weights(**{**WEIGHTS, **weights})
+    assert lib.moe_int4_create(ctypes.byref(d), ctypes.byref(w), None, ctypes.byref(h)) == code
+    assert h.value is None and moe.moe_last_error()
+
+
+def test_null(lib):
+    a = moe.MoeInt4Args()
+    assert lib.moe_int4_create(None, None, None, None) == 1
+    assert lib.moe_int4_forward(None, ctypes.byref(a), None) == 1
+    assert lib.moe_int4_destroy(None) == 1
+    assert lib.moe_int4_device_status(None, None, None) == 1
+    assert lib.moe_int4_set_wait_limit(None, 1000) == 1
