@@ -8,13 +8,14 @@
 // Image of 4-bit weights.  A block is 16 rows of one expert's matrix (gated:
 // 8 gate rows, then the 8 up rows of the same features), a tile 64 input
 // channels of a block in 512 bytes, 16 for each lane of a warp.  Lane
-// 4 g + q has, one word of 8 codes each, the channels 8 q .. 8 q + 7 and
-// 32 + 8 q .. 32 + 8 q + 7 of row g, then the same of row g + 8: what it
-// feeds to a 16 x 16 tensor-core operand, so a warp takes its operand by one
-// 16-byte load per lane.  In a word, nibbles 0 to 3 are the even channels and
-// 4 to 7 the odd ones: (word >> 4 i) & 0x000F000F are channels 2 i and 2 i + 1
-// as two halves.  Tiles of a block follow one another; channels past the
-// matrix meet zeros of x.
+// 4 g + q has the channels 16 i + 4 q .. 16 i + 4 q + 3 (i = 0 to 3) of row g
+// in two words of 8 codes, then those of row g + 8: what a lane holds of a
+// 16 x 16 mma.sync operand (with x in the same order of channels) and of a
+// 16 x 256-bit store to tensor memory, so either kernel takes its operand by
+// one 16-byte load per lane.  In a word, nibbles 0 to 3 are the even channels
+// and 4 to 7 the odd ones: (word >> 4 j) & 0x000F000F are the j-th two
+// channels as two halves.  Tiles of a block follow one another; channels past
+// the matrix meet zeros of x.
 // Scales: [expert][block][group][8] pairs (row g, row g + 8); zero points
 // likewise as 128 + z in bf16.  Rows past the matrix have scales of zero.
 // ---------------------------------------------------------------------------
@@ -53,11 +54,14 @@ struct Int4Call {
     int rows, x_rows;
     int N, K, E, blocks, kt, groups;
     uint32_t wait_limit;
-    bool s_f32, y_f32, gated, x_vec;
+    bool s_f32, y_f32, gated;
+    int x_grid;            // 16, 8 or 2: the bytes whose multiples all rows of x start on
 };
 
 cudaError_t launch_int4_repack(const moe_int4* L, const moe_int4_weights* w, cudaStream_t s);
 cudaError_t launch_int4_few(const moe_int4* L, const Int4Call& c, cudaStream_t s);
+bool int4_takes_many(const Int4Call& c);        // whether the form for many rows takes the call
+cudaError_t launch_int4_many(const moe_int4* L, const Int4Call& c, cudaStream_t s);
 
 // Tokens per chunk of the multi-CTA sort and the chunks of a call, and no fewer than any smaller batch has
 // (the workspace, int32 [most_chunks + 1][n_experts]).  chunks = 0: one kernel does it without workspace.

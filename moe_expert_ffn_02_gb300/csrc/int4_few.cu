@@ -35,7 +35,7 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 template <int RB, int NB, int SUB>
 struct Slot {
     uint4 w[RB][32];
-    uint4 x[NB][2][32];                // [channels 8 q, 32 + 8 q][lane]
+    uint2 x[NB][4][32];                // [channels 16 i + 4 q][lane]
     uint2 s[SUB][RB][8];               // pairs (row g, row g + 8): two fp32, or two bf16 in .x
     uint32_t z[SUB][RB][8];
 };
@@ -99,16 +99,16 @@ __global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int k = t * I4_K + h * 32 + q * 8;
-                    const int have = p_x[n] < 0 ? 0 : min(max(c.K - k, 0), 8);
+                for (int i = 0; i < 4; ++i) {
+                    const int k = t * I4_K + i * 16 + q * 4;
+                    const int have = p_x[n] < 0 ? 0 : min(max(c.K - k, 0), 4);
                     const uint16_t* src = have ? c.x + p_x[n] + k : c.x;
-                    if (c.x_vec) {
-                        i4::copy16(smem_addr(&slot.x[n][h][lane]), src, have * 2);
+                    if (c.x_grid >= 8) {
+                        i4::copy8(smem_addr(&slot.x[n][i][lane]), src, have * 2);
                     } else {
-                        uint16_t* to = reinterpret_cast<uint16_t*>(&slot.x[n][h][lane]);
+                        uint16_t* to = reinterpret_cast<uint16_t*>(&slot.x[n][i][lane]);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) to[i] = i < have ? src[i] : (uint16_t)0;
+                        for (int j = 0; j < 4; ++j) to[j] = j < have ? src[j] : (uint16_t)0;
                     }
                 }
             }
@@ -143,12 +143,11 @@ __global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
             copy_next();
             const Slot<RB, NB, SUB>& slot = sm.ring[warp][slot_at];
             slot_at = slot_at + 1 == DEPTH ? 0 : slot_at + 1;
-            uint4 xv[NB][2];
+            uint2 xv[NB][4];
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                xv[n][0] = slot.x[n][0][lane];
-                xv[n][1] = slot.x[n][1][lane];
-            }
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) xv[n][i] = slot.x[n][i][lane];
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) {
                 const uint4 w = slot.w[rb][lane];
@@ -169,8 +168,8 @@ __global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
                     const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
                     for (int n = 0; n < NB; ++n) {
-                        mma(part[n], a0, xv[n][half].x, xv[n][half].y);
-                        mma(part[n], a1, xv[n][half].z, xv[n][half].w);
+                        mma(part[n], a0, xv[n][2 * half].x, xv[n][2 * half].y);
+                        mma(part[n], a1, xv[n][2 * half + 1].x, xv[n][2 * half + 1].y);
                     }
                     if (half == 1 || SUB == 2) {
                         const uint2 sv = slot.s[sub][rb][g];
@@ -275,11 +274,11 @@ __global__ void __launch_bounds__(256) int4_repack_kernel(const uint8_t* __restr
             const uint8_t* src = (q_up && r ? q_up : q) + (e * N + n) * row_bytes;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int k = t * I4_K + h * 32 + qd * 8;
                 uint32_t v = 0;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    const uint32_t byte = k / 2 + b < row_bytes ? src[k / 2 + b] : 0u;
+                    const int at = (t * I4_K + h * 32 + (b >> 1) * 16 + qd * 4 + (b & 1) * 2) / 2;
+                    const uint32_t byte = at < row_bytes ? src[at] : 0u;
                     v |= (byte & 15u) << (4 * b) | (byte >> 4) << (16 + 4 * b);
                 }
                 out[r * 2 + h] = v;
