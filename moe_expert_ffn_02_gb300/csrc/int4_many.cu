@@ -6,8 +6,11 @@
 // the codes, less their zero points, to bf16, exactly, and store them straight
 // into tensor memory as the MMA's first operand: through shared memory each
 // weight would be written and read there at two bytes, 256 clocks of that
-// memory for a stage of 64 columns whose MMAs take 256.  Three warps bring x
-// into swizzled shared memory, one issues the MMAs, eight drain.
+// memory for a stage of 64 columns whose MMAs take 256.  Eight warps drain;
+// of the rest one brings codes, scales and zero points (bulk copies), one the
+// rows of x (TMA, gathered by token where there are tokens) and one issues the
+// MMAs.  Rows of x off the 16-byte grid, which TMA does not take, are brought
+// by six warps.
 //
 // The tensor core's running sum truncates, and scales are per 32 channels at
 // the finest: each stage goes into fresh accumulators, CHUNKS of them (1, 2 or
@@ -17,6 +20,7 @@
 // of accumulators, so that BN = 128 / CHUNKS, and four stages of operands.
 #include <algorithm>
 
+#include "dense_internal.cuh"
 #include "int4.cuh"
 #include "tcgen05.cuh"
 
@@ -24,33 +28,39 @@ namespace moe {
 
 namespace {
 
-constexpr int DRAIN_WARPS = 8, WIDEN_WARPS = 8, LOAD_WARPS = 3;
-constexpr int NTHREADS = (DRAIN_WARPS + WIDEN_WARPS + LOAD_WARPS + 1) * 32;      // 640: five warpgroups
-// setmaxnreg: launched at 96 per thread (640 x 96 = 61,440); the drain warps rise to 112, the others drop
-// to 80: 8 * 32 * 112 + 12 * 32 * 80 = 59,392
-constexpr int DRAIN_REGS = 112, OTHER_REGS = 80;
-static_assert(DRAIN_WARPS * 32 * DRAIN_REGS + (NTHREADS - DRAIN_WARPS * 32) * OTHER_REGS <= NTHREADS * 96, "register split");
+constexpr int DRAIN_WARPS = 8, WIDEN_WARPS = 8, X_WARPS = 6;
+constexpr int CODE_WARP = DRAIN_WARPS + WIDEN_WARPS, MMA_WARP = CODE_WARP + 1, X_WARP = MMA_WARP + 1;
+constexpr int NTHREADS = (X_WARP + X_WARPS) * 32;        // 768: six warpgroups
+// setmaxnreg: launched at 80 per thread (768 x 80 = 61,440); the drain warps rise to 120, the others drop
+// to 56: 8 * 32 * 120 + 16 * 32 * 56 = 59,392
+constexpr int DRAIN_REGS = 120, OTHER_REGS = 56;
+static_assert(DRAIN_WARPS * 32 * DRAIN_REGS + (NTHREADS - DRAIN_WARPS * 32) * OTHER_REGS <= NTHREADS * 80, "register split");
 
 constexpr int BM_BLOCKS = 8;                     // 128 weight rows
 constexpr int STAGE_K = 128, STAGE_TILES = 2;    // channels; 64-channel tiles
-constexpr int STAGES = 4;
+constexpr int STAGES = 4;                        // operands of the MMA
+constexpr int RING = 6;                          // codes: 8 KB a stage, to keep some 40 KB in flight
 constexpr int COLS = 128;                        // accumulator columns of one set, two sets
 constexpr int A_COLS = STAGE_K / 2;              // operand columns of a stage: two bf16 channels each
 constexpr int A_BASE = 2 * COLS;
 static_assert(A_BASE + STAGES * A_COLS <= 512, "tensor memory");
-constexpr int CODE_DEPTH = 5;                    // stages of codes in flight per widening warp
-constexpr int SCALE_DEPTH = 4;                   // stages of scales in flight per drain thread
-constexpr uint32_t LANDING_LIMIT = 2000000u;      // us, of the wait for MMAs in flight, whatever the limit of the others
-constexpr int LOAD_LAG = 2;                      // stages of x in flight behind the one being issued
+constexpr int X_BOX = 32;                        // rows of x that one copy brings
+
+// A stage of weights as it is copied: per block its tiles and the records of the groups that it meets.
+template <int CHUNKS>
+struct Codes {
+    uint4 w[BM_BLOCKS][STAGE_TILES][32];
+    uint2 s[BM_BLOCKS][CHUNKS][8];               // fp32 pairs; bf16 pairs lie in the first half of each block's
+    uint32_t z[BM_BLOCKS][CHUNKS][8];
+};
 
 template <int CHUNKS>
 struct Smem {
     static constexpr int BN = COLS / CHUNKS;
     uint8_t x[STAGES][STAGE_TILES][BN * 128];    // 128-byte swizzle, 1024-byte aligned
-    uint4 codes[WIDEN_WARPS][CODE_DEPTH][STAGE_TILES][32];
-    uint32_t zeros[WIDEN_WARPS][CODE_DEPTH][STAGE_TILES * 2][8];
-    uint32_t scales[SCALE_DEPTH][CHUNKS][DRAIN_WARPS * 32];
+    Codes<CHUNKS> ring[RING];
     uint64_t full[STAGES], done[STAGES], drained[2], last;
+    uint64_t code_full[RING], code_free[RING];
     uint32_t tmem;
     int abort;
     int table[1];                                // start[E + 1], first[E + 1]
@@ -67,25 +77,78 @@ __device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&r
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// kind::f16 with the first operand in tensor memory.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// Two K16 steps (32 channels), the first operand in tensor memory, by the elected lane.  b_lo: low word of
+// the second operand's descriptor, 2 more per step.  accumulate: whether the first adds to what is there.
+__device__ __forceinline__ void mma_ts2(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t elected, uint32_t accumulate) {
+    constexpr uint32_t HI = (uint32_t)(tc::DESC_HI >> 32);
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n .reg .pred q, t;\n .reg .b64 b;\n .reg .b32 x, y;\n"
+        " setp.ne.b32 q, %5, 0;\n setp.ne.b32 t, %6, 0;\n"
+        " mov.b64 b, {%2, %4};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, t;\n"
+        " setp.eq.b32 t, 0, 0;\n"
+        " add.u32 x, %1, 8;\n add.u32 y, %2, 2;\n mov.b64 b, {y, %4};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(idesc), "n"(HI), "r"(elected), "r"(accumulate)
         : "memory");
 }
 
+// True in one lane of a converged warp; the loops around it stay warp-uniform.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p;
+}
+
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int k, int row, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(k), "r"(row), "r"(bar)
+        : "memory");
+}
+// Four rows anywhere, one after the other at dst.
+__device__ __forceinline__ void tma_gather(uint32_t dst, const CUtensorMap* map, int k, const int (&row)[4], uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(k), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar)
+        : "memory");
+}
 
 // D f32, A = B = bf16, both K-major, M = 128.
 __device__ __forceinline__ uint32_t idesc_for(int n) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-template <int CHUNKS>
-__global__ void __launch_bounds__(NTHREADS, 1) int4_many_kernel(const Int4Call c, int bn) {
+// Eight channels of a row that starts on a 2-byte boundary, those from `have` on as zeros.  Words that
+// straddle the piece's ends are read as halves: nothing outside it is touched.
+__device__ __forceinline__ uint4 load8(const uint16_t* p, int have) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (have >= 8) {
+        if ((reinterpret_cast<uintptr_t>(p) & 2) == 0) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+            v = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(p + 1);
+            const uint32_t a = p[0], b = w[0], c = w[1], d = w[2], e = p[7];
+            v = make_uint4(a | b << 16, __funnelshift_l(b, c, 16), __funnelshift_l(c, d, 16), d >> 16 | e << 16);
+        }
+    } else if (have > 0) {
+        uint32_t h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = i < have ? p[i] : 0u;
+        v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    }
+    return v;
+}
+
+enum XMode { X_TILE, X_GATHER, X_COPY };
+
+template <int CHUNKS, XMode MODE, bool ZEROS>
+__global__ void __launch_bounds__(NTHREADS, 1) int4_many_kernel(const __grid_constant__ CUtensorMap x_map, const Int4Call c) {
     using S = Smem<CHUNKS>;
+    constexpr int BN = S::BN;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     int* start = sm.table;
@@ -96,8 +159,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) int4_many_kernel(const Int4Call c
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&sm.full[s], WIDEN_WARPS + LOAD_WARPS);
+            mbar_init(&sm.full[s], WIDEN_WARPS + (MODE == X_COPY ? X_WARPS : 1));
             mbar_init(&sm.done[s], 1);
+        }
+        for (int s = 0; s < RING; ++s) {
+            mbar_init(&sm.code_full[s], 1);
+            mbar_init(&sm.code_free[s], WIDEN_WARPS + DRAIN_WARPS);
         }
         for (int b = 0; b < 2; ++b) mbar_init(&sm.drained[b], DRAIN_WARPS);
         mbar_init(&sm.last, 1);
@@ -105,81 +172,59 @@ __global__ void __launch_bounds__(NTHREADS, 1) int4_many_kernel(const Int4Call c
         sm.abort = 0;
     }
     if (warp == 0) tc::tmem_alloc(&sm.tmem, 512);
-    pdl_wait();
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    i4::row_tiles<NTHREADS>(c, bn, start, first);
+    if (c.offsets) pdl_wait();
+    i4::row_tiles<NTHREADS>(c, BN, start, first);
     const uint32_t tmem = sm.tmem;
     volatile int* abort = &sm.abort;
     const int units = start[c.E] * feature_tiles;
-    auto unit_at = [&](int u) { return i4::unit_at(c, u, feature_tiles, bn, start, first); };
+    auto unit_at = [&](int u) { return i4::unit_at(c, u, feature_tiles, BN, start, first); };
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, c.wait_limit, c.status, abort); };
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)); };
 
     if (warp >= DRAIN_WARPS) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
-        if (warp < DRAIN_WARPS + WIDEN_WARPS) {
+        if (warp < CODE_WARP) {
             // ------------------------------------------------------------ codes into tensor memory
+            pdl_wait();                          // no bounded wait before it: limits count this kernel's time alone
             const int w = warp - DRAIN_WARPS, quarter = w & 3, block = quarter * 2 + (w >> 2), g = lane >> 2;
             const uint32_t to = tmem + ((uint32_t)(quarter * 32 + (w >> 2) * 16) << 16) + A_BASE;
-            int p_unit = blockIdx.x, p_stage = 0, p_slot = 0;
-            const uint4* p_w = nullptr;
-            size_t p_rec = 0;
-            bool p_have = false;
-            auto enter = [&](int u) {
-                const i4::Unit un = unit_at(u);
-                const int b = un.tile * BM_BLOCKS + block;
-                const size_t at = (size_t)un.expert * c.blocks + b;
-                p_have = b < c.blocks;
-                p_w = c.w + at * c.kt * 32 + lane;
-                p_rec = at * c.groups * 8 + (lane & 7);
-            };
-            auto copy_next = [&]() {
-                if (p_unit < units) {
-                    if (p_have) {
-                        const int t = p_stage * STAGE_TILES;
-                        i4::copy16(smem_addr(&sm.codes[w][p_slot][0][lane]), p_w);
-                        if (t + 1 < c.kt) i4::copy16(smem_addr(&sm.codes[w][p_slot][1][lane]), p_w + 32);
-                        if (c.z && 2 * t + (lane >> 3) < 2 * c.kt)
-                            i4::copy_small<4>(smem_addr(&sm.zeros[w][p_slot][lane >> 3][lane & 7]),
-                                              c.z + p_rec + (size_t)i4::group_of(c, 2 * t + (lane >> 3)) * 8);
-                    }
-                    p_w += STAGE_TILES * 32;
-                    if (++p_stage == stages) {
-                        p_stage = 0;
-                        p_unit += gridDim.x;
-                        if (p_unit < units) enter(p_unit);
-                    }
-                }
-                p_slot = p_slot + 1 == CODE_DEPTH ? 0 : p_slot + 1;
-                i4::copy_commit();
-            };
-            if (p_unit < units) enter(p_unit);
-#pragma unroll 1
-            for (int i = 0; i < CODE_DEPTH - 1; ++i) copy_next();
-            uint32_t n = 0;
-            int at = 0;
+            int slot = 0, at = 0;
+            uint32_t phase = 0, code_phase = 0;
             bool ok = true;
             for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-                for (int st = 0; st < stages; ++st, ++n) {
-                    const int slot = n % STAGES;
-                    i4::copy_wait<CODE_DEPTH - 2>();
-                    ok = __all_sync(0xFFFFFFFFu, wait(&sm.done[slot], ((n / STAGES) & 1u) ^ 1u));
+                for (int st = 0; st < stages; ++st) {
+                    ok = warp_wait(&sm.code_full[at], code_phase);
+                    if (!ok) break;
+                    const Codes<CHUNKS>& in = sm.ring[at];
+                    uint4 code[STAGE_TILES];
+                    uint32_t zero[4];
+#pragma unroll
+                    for (int tile = 0; tile < STAGE_TILES; ++tile) code[tile] = in.w[block][tile][lane];
+                    if (ZEROS) {
+                        const int g0 = i4::group_of(c, st * 4);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            zero[i] = in.z[block][CHUNKS == 1 ? 0 : min(i4::group_of(c, st * 4 + i) - g0, CHUNKS - 1)][g];
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.code_free[at]);
+                    if (++at == RING) { at = 0; code_phase ^= 1u; }
+                    ok = warp_wait(&sm.done[slot], phase ^ 1u);
                     if (!ok) break;
                     tc::tc_fence_after();
-                    __syncwarp();                // the other lanes' copies (zero points)
-                    copy_next();
 #pragma unroll
                     for (int tile = 0; tile < STAGE_TILES; ++tile) {
                         uint32_t r[16], v[4];
-                        if (2 * st + tile < c.kt) {
-                            const uint4 code = sm.codes[w][at][tile][lane];
+                        if (STAGE_TILES * st + tile < c.kt) {
 #pragma unroll
                             for (int half = 0; half < 2; ++half) {
-                                const uint32_t z = c.z ? sm.zeros[w][at][tile * 2 + half][g] : I4_ZERO;
-                                i4::widen(half ? code.y : code.x, __byte_perm(z, 0, 0x1010), v);
+                                const uint32_t z = ZEROS ? zero[tile * 2 + half] : I4_ZERO;
+                                i4::widen(half ? code[tile].y : code[tile].x, ZEROS ? __byte_perm(z, 0, 0x1010) : z, v);
                                 r[8 * half] = v[0], r[8 * half + 1] = v[1], r[8 * half + 4] = v[2], r[8 * half + 5] = v[3];
-                                i4::widen(half ? code.w : code.z, __byte_perm(z, 0, 0x3232), v);
+                                i4::widen(half ? code[tile].w : code[tile].z, ZEROS ? __byte_perm(z, 0, 0x3232) : z, v);
                                 r[8 * half + 2] = v[0], r[8 * half + 3] = v[1], r[8 * half + 6] = v[2], r[8 * half + 7] = v[3];
                             }
                         } else {                 // channels past the image
@@ -188,192 +233,212 @@ __global__ void __launch_bounds__(NTHREADS, 1) int4_many_kernel(const Int4Call c
                         }
                         tmem_st_16x32(to + slot * A_COLS + tile * (A_COLS / STAGE_TILES), r);
                     }
-                    at = at + 1 == CODE_DEPTH ? 0 : at + 1;
                     tmem_wait_st();
                     tc::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.full[slot]);
+                    if (++slot == STAGES) { slot = 0; phase ^= 1u; }
                 }
             }
-            i4::copy_wait<0>();
-        } else if (warp < DRAIN_WARPS + WIDEN_WARPS + LOAD_WARPS) {
-            // ------------------------------------------------------------ rows of x into shared memory
-            const int tid = threadIdx.x - (DRAIN_WARPS + WIDEN_WARPS) * 32, lw = tid >> 5;
-            constexpr int STEP = LOAD_WARPS * 4;             // rows that the threads cover at once, 8 chunks each
-            constexpr int PER = (S::BN + STEP - 1) / STEP;
-            const int chunk = tid & 7, r0 = tid >> 3;
-            uint32_t n = 0, arrived = 0;
+        } else if (warp == CODE_WARP) {
+            // ------------------------------------------------------------ codes, scales, zero points
+            // lanes 0 to 7 copy a block's tiles, 8 to 15 its scales, 16 to 23 its zero points
+            constexpr int Z_REC = 32;
+            const int s_rec = c.s_f32 ? 64 : 32;
+            const int block = lane & 7, what = lane >> 3;
+            int slot = 0, issued = 0;
+            uint32_t phase = 0;
             bool ok = true;
             for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
                 const i4::Unit un = unit_at(u);
-                int src[PER];
-                if (c.x_grid == 16) {
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        const int r = r0 + i * STEP;
-                        src[i] = r < un.count ? i4::source_row(c, un.row0 + r) : -1;
-                    }
-                }
-                for (int st = 0; st < stages; ++st, ++n) {
-                    const int slot = n % STAGES;
-                    ok = __all_sync(0xFFFFFFFFu, wait(&sm.done[slot], ((n / STAGES) & 1u) ^ 1u));
+                const int blocks = min(BM_BLOCKS, c.blocks - un.tile * BM_BLOCKS);
+                const size_t b = (size_t)un.expert * c.blocks + un.tile * BM_BLOCKS + block;
+                const bool copies = block < blocks && what < (ZEROS ? 3 : 2);
+                const char* src = what == 0 ? reinterpret_cast<const char*>(c.w) + b * c.kt * 512
+                                : what == 1 ? c.s + b * c.groups * s_rec : reinterpret_cast<const char*>(c.z) + b * c.groups * Z_REC;
+                for (int st = 0; st < stages; ++st) {
+                    if (issued == RING) pdl_wait();
+                    ok = issued < RING || warp_wait(&sm.code_free[slot], phase ^ 1u);
                     if (!ok) break;
-                    if (c.x_grid == 16) {
-                        const int k = st * STAGE_K + chunk * 8;
-                        const uint32_t base = smem_addr(sm.x[slot][0]) + ((chunk ^ (r0 & 7)) << 4) + r0 * 128;
-                        const int have0 = min(max(c.K - k, 0), 8) * 2, have1 = min(max(c.K - k - I4_K, 0), 8) * 2;
-#pragma unroll
-                        for (int i = 0; i < PER; ++i) {
-                            if (r0 + i * STEP >= un.count) break;
-                            // the swizzle of rows r0 + 12 i: 12 i changes r & 7 by 4 for odd i
-                            const uint32_t to = (base + i * STEP * 128) ^ ((i & 1) << 6);
-                            const uint16_t* from = c.x + (src[i] < 0 ? 0 : src[i]) * c.ldx + k;
-                            const int b0 = src[i] < 0 ? 0 : have0, b1 = src[i] < 0 ? 0 : have1;
-                            i4::copy16(to, b0 ? from : c.x, b0);
-                            i4::copy16(to + S::BN * 128, b1 ? from + I4_K : c.x, b1);
-                        }
-                    } else {
-                        // rows off the 16-byte grid: a warp takes a row, two channels a lane, eight rows at a time
-                        constexpr int BATCH = 8;
-#pragma unroll 1
-                        for (int rb = lw; rb < un.count; rb += LOAD_WARPS * BATCH) {
-#pragma unroll 1
-                            for (int tile = 0; tile < STAGE_TILES; ++tile) {
-                                const int k = (st * STAGE_TILES + tile) * I4_K + lane * 2;
-                                uint32_t v[BATCH];
-#pragma unroll
-                                for (int i = 0; i < BATCH; ++i) {
-                                    const int r = rb + i * LOAD_WARPS;
-                                    const int from = r < un.count ? i4::source_row(c, un.row0 + r) : -1;
-                                    const uint16_t* p = c.x + (from < 0 ? 0 : from) * c.ldx + k;
-                                    const uint32_t lo = from >= 0 && k < c.K ? p[0] : 0u, hi = from >= 0 && k + 1 < c.K ? p[1] : 0u;
-                                    v[i] = lo | hi << 16;
-                                }
-#pragma unroll
-                                for (int i = 0; i < BATCH; ++i) {
-                                    const int r = rb + i * LOAD_WARPS;
-                                    if (r < un.count)
-                                        *reinterpret_cast<uint32_t*>(sm.x[slot][tile] + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) = v[i];
-                                }
-                            }
-                        }
+                    Codes<CHUNKS>& in = sm.ring[slot];
+                    const int tiles = min(STAGE_TILES, c.kt - st * STAGE_TILES);
+                    const int g0 = i4::group_of(c, st * 4), groups = i4::group_of(c, min(st * 4 + 3, 2 * c.kt - 1)) - g0 + 1;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&sm.code_full[slot], blocks * (tiles * 512 + groups * (s_rec + (ZEROS ? Z_REC : 0))));
+                    __syncwarp();
+                    if (copies) {
+                        if (what == 0) bulk_g2s(&in.w[block], src + st * (STAGE_TILES * 512), tiles * 512, &sm.code_full[slot]);
+                        else if (what == 1) bulk_g2s(&in.s[block], src + (size_t)g0 * s_rec, groups * s_rec, &sm.code_full[slot]);
+                        else bulk_g2s(&in.z[block], src + (size_t)g0 * Z_REC, groups * Z_REC, &sm.code_full[slot]);
                     }
-                    i4::copy_commit();
-                    if (n >= LOAD_LAG) {
-                        i4::copy_wait<LOAD_LAG>();
-                        fence_async_proxy();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm.full[arrived % STAGES]);
-                        ++arrived;
-                    }
+                    ++issued;
+                    if (issued > RING) issued = RING + 1;
+                    if (++slot == RING) { slot = 0; phase ^= 1u; }
                 }
             }
-            i4::copy_wait<0>();
-            fence_async_proxy();
-            __syncwarp();
-            for (; arrived < n; ++arrived)
-                if (lane == 0) mbar_arrive(&sm.full[arrived % STAGES]);
-        } else if (lane == 0) {
+            // every issued copy lands before the CTA exits: the last ones, newest first
+            for (issued = min(issued, RING); issued > 0; --issued) {
+                if (--slot < 0) { slot = RING - 1; phase ^= 1u; }
+                mbar_wait_bounded(&sm.code_full[slot], phase, LANDING_LIMIT_US, c.status, nullptr);
+            }
+        } else if (warp == MMA_WARP) {
             // ------------------------------------------------------------ MMA issuer
-            uint32_t n = 0;
+            pdl_wait();
+            const uint32_t el = elect_one();
+            const uint32_t b0 = (uint32_t)tc::sw128_desc(smem_addr(sm.x[0][0]));
+            int slot = 0;
+            uint32_t phase = 0, n = 0;
             bool ok = true;
             for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
                 const i4::Unit un = unit_at(u);
                 const uint32_t idesc = idesc_for((un.count + 15) / 16 * 16);
                 for (int st = 0; st < stages; ++st, ++n) {
-                    const int slot = n % STAGES;
-                    ok = wait(&sm.drained[n & 1], ((n >> 1) & 1u) ^ 1u) && wait(&sm.full[slot], (n / STAGES) & 1u);
+                    ok = __all_sync(0xFFFFFFFFu, wait(&sm.drained[n & 1], ((n >> 1) & 1u) ^ 1u) && wait(&sm.full[slot], phase));
                     if (!ok) break;
                     tc::tc_fence_after();
-                    const uint32_t a = tmem + A_BASE + slot * A_COLS;
+                    const uint32_t a = tmem + A_BASE + slot * A_COLS, d = tmem + (n & 1) * COLS;
+                    const uint32_t b = b0 + ((slot * (STAGE_TILES * BN * 128)) >> 4);
 #pragma unroll
-                    for (int k = 0; k < STAGE_K / 16; ++k) {
-                        const uint32_t d = tmem + (n & 1) * COLS + k / (8 / CHUNKS) * S::BN;
-                        const uint64_t b = tc::sw128_desc(smem_addr(sm.x[slot][k / 4])) + 2 * (k % 4);
-                        mma_ts(d, a + k * 8, b, idesc, k % (8 / CHUNKS) != 0);
-                    }
-                    tc::mma_commit(&sm.done[slot]);
+                    for (int i = 0; i < 4; ++i)
+                        mma_ts2(d + i / (4 / CHUNKS) * BN, a + i * 16, b + (i >> 1) * ((BN * 128) >> 4) + (i & 1) * 4, idesc, el,
+                                i % (4 / CHUNKS) != 0);
+                    if (el) tc::mma_commit(&sm.done[slot]);
+                    __syncwarp();
+                    if (++slot == STAGES) { slot = 0; phase ^= 1u; }
                 }
             }
             // every issued MMA must complete before the tensor memory is released
             if (n) {
-                tc::mma_commit(&sm.last);
-                mbar_wait_bounded(&sm.last, 0u, LANDING_LIMIT, c.status, nullptr);
+                if (el) tc::mma_commit(&sm.last);
+                __syncwarp();
+                mbar_wait_bounded(&sm.last, 0u, LANDING_LIMIT_US, c.status, nullptr);
+            }
+        } else if (MODE == X_COPY || warp == X_WARP) {
+            // ------------------------------------------------------------ rows of x into shared memory
+            pdl_wait();
+            const int xw = warp - X_WARP;
+            int slot = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+                const i4::Unit un = unit_at(u);
+                int row[4];
+                if (MODE == X_GATHER) {          // lane i has rows 4 i to 4 i + 3; -1 reads as zeros
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) row[i] = lane * 4 + i < un.count ? i4::source_row(c, un.row0 + lane * 4 + i) : -1;
+                }
+                for (int st = 0; st < stages; ++st) {
+                    ok = warp_wait(&sm.done[slot], phase ^ 1u);
+                    if (!ok) break;
+                    const uint32_t bar = smem_addr(&sm.full[slot]), to = smem_addr(sm.x[slot][0]);
+                    if (MODE == X_TILE) {
+                        const int boxes = (un.count + X_BOX - 1) / X_BOX;
+                        if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], boxes * (STAGE_TILES * X_BOX * 128));
+                        __syncwarp();
+                        const int box = lane >> 1, tile = lane & 1;
+                        if (box < boxes)
+                            tma_rows(to + tile * (BN * 128) + box * (X_BOX * 128), &x_map, st * STAGE_K + tile * I4_K, un.row0 + box * X_BOX, bar);
+                    } else if (MODE == X_GATHER) {
+                        const int fours = (un.count + 3) / 4;
+                        if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], fours * (STAGE_TILES * 512));
+                        __syncwarp();
+                        if (lane < fours) {
+#pragma unroll
+                            for (int tile = 0; tile < STAGE_TILES; ++tile)
+                                tma_gather(to + tile * (BN * 128) + lane * 512, &x_map, st * STAGE_K + tile * I4_K, row, bar);
+                        }
+                    } else {
+                        // a warp's lanes take 8 rows by 4 of the 16 pieces of 8 channels
+                        constexpr int BATCH = 4;
+                        const int r8 = lane >> 2;
+#pragma unroll 1
+                        for (int r0 = xw * 8; r0 < un.count; r0 += X_WARPS * 8) {
+                            const int r = r0 + r8;
+                            const int from = r < un.count ? i4::source_row(c, un.row0 + r) : -1;
+                            const uint16_t* p = c.x + (from < 0 ? 0 : from) * c.ldx + st * STAGE_K;
+                            uint4 v[BATCH];
+#pragma unroll
+                            for (int i = 0; i < BATCH; ++i) {
+                                const int k = ((lane & 3) + 4 * i) * 8;
+                                v[i] = load8(p + k, from < 0 ? 0 : min(c.K - st * STAGE_K - k, 8));
+                            }
+                            if (r < un.count) {
+#pragma unroll
+                                for (int i = 0; i < BATCH; ++i) {
+                                    const int piece = (lane & 3) + 4 * i;
+                                    *reinterpret_cast<uint4*>(sm.x[slot][piece >> 3] + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) = v[i];
+                                }
+                            }
+                        }
+                        fence_async_proxy();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.full[slot]);
+                    }
+                    issued = min(issued + 1, STAGES);
+                    if (++slot == STAGES) { slot = 0; phase ^= 1u; }
+                }
+            }
+            // Every issued copy lands before the CTA exits.  (A stage that lacks other arrivals, after an expired wait, only
+            // gives them their time.)
+            if (MODE != X_COPY) {
+                for (; issued > 0; --issued) {
+                    if (--slot < 0) { slot = STAGES - 1; phase ^= 1u; }
+                    mbar_wait_bounded(&sm.full[slot], phase, LANDING_LIMIT_US, c.status, nullptr);
+                }
             }
         }
+        __syncwarp();
     } else {
         // ---------------------------------------------------------------- drain, scale, add up
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(DRAIN_REGS));
-        constexpr int PIECES = S::BN / 32;                   // 16-column pieces per thread: every second one
+        constexpr int W = BN >= 64 ? 32 : 16, PIECES = BN / 2 / W;      // columns a load; loads per thread and chunk
         const int quarter = warp & 3, side = warp >> 2;
-        const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + side * 16;
+        const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + side * W;
         const int row = quarter * 32 + lane, block = row >> 4, g = row & 7, upper = (row >> 3) & 1;
-        int p_unit = blockIdx.x, p_stage = 0, p_slot = 0;
-        size_t p_rec = 0;
-        bool p_have = false;
-        auto enter = [&](int u) {
-            const i4::Unit un = unit_at(u);
-            const int b = un.tile * BM_BLOCKS + block;
-            p_have = b < c.blocks;
-            p_rec = ((size_t)un.expert * c.blocks + b) * c.groups * 8 + g;
-        };
-        auto copy_next = [&]() {
-            if (p_unit < units) {
-#pragma unroll
-                for (int j = 0; j < CHUNKS; ++j) {
-                    const int step = p_stage * 4 + j * (4 / CHUNKS);
-                    if (p_have && step < 2 * c.kt) {
-                        const size_t rec = p_rec + (size_t)i4::group_of(c, step) * 8;
-                        i4::copy_small<4>(smem_addr(&sm.scales[p_slot][j][threadIdx.x]),
-                                          c.s_f32 ? c.s + rec * 8 + upper * 4 : c.s + rec * 4);
-                    }
-                }
-                if (++p_stage == stages) {
-                    p_stage = 0;
-                    p_unit += gridDim.x;
-                    if (p_unit < units) enter(p_unit);
-                }
-            }
-            p_slot = (p_slot + 1) % SCALE_DEPTH;
-            i4::copy_commit();
-        };
-        if (p_unit < units) enter(p_unit);
-#pragma unroll 1
-        for (int i = 0; i < SCALE_DEPTH - 1; ++i) copy_next();
-        uint32_t n = 0;
+        pdl_wait();
+        int slot = 0, at = 0;
+        uint32_t phase = 0, code_phase = 0, n = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
             const i4::Unit un = unit_at(u);
-            float acc[PIECES][16];
+            float acc[PIECES][W];
 #pragma unroll
             for (int p = 0; p < PIECES; ++p)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[p][i] = 0.f;
+                for (int i = 0; i < W; ++i) acc[p][i] = 0.f;
             for (int st = 0; st < stages; ++st, ++n) {
-                const int slot = n % STAGES;
-                i4::copy_wait<SCALE_DEPTH - 2>();
-                copy_next();
+                ok = warp_wait(&sm.code_full[at], code_phase);
+                if (!ok) break;
                 float sc[CHUNKS];
+                const int g0 = i4::group_of(c, st * 4);
 #pragma unroll
                 for (int j = 0; j < CHUNKS; ++j) {
-                    const uint32_t v = sm.scales[n % SCALE_DEPTH][j][threadIdx.x];
+                    const int rec = CHUNKS == 1 ? 0 : min(i4::group_of(c, st * 4 + j * (4 / CHUNKS)) - g0, CHUNKS - 1);
+                    const uint32_t* s = reinterpret_cast<const uint32_t*>(sm.ring[at].s[block]);
+                    const uint32_t v = c.s_f32 ? s[(rec * 8 + g) * 2 + upper] : s[rec * 8 + g];
                     sc[j] = __uint_as_float(c.s_f32 ? v : upper ? v & 0xFFFF0000u : v << 16);
                     // the last stage's second tile may lie past the matrix
-                    if (st * 4 + j * (4 / CHUNKS) >= 2 * c.kt) sc[j] = 0.f;
+                    if (CHUNKS > 1 && st * 4 + j * (4 / CHUNKS) >= 2 * c.kt) sc[j] = 0.f;
                 }
-                ok = __all_sync(0xFFFFFFFFu, wait(&sm.done[slot], (n / STAGES) & 1u));   // tcgen05.ld below is warp-collective
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.code_free[at]);
+                if (++at == RING) { at = 0; code_phase ^= 1u; }
+                ok = warp_wait(&sm.done[slot], phase);           // tcgen05.ld below is warp-collective
                 if (!ok) break;
+                if (++slot == STAGES) { slot = 0; phase ^= 1u; }
                 tc::tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < CHUNKS; ++j)
 #pragma unroll
                     for (int p = 0; p < PIECES; ++p)
-                        if (p * 32 + side * 16 < un.count) {
-                            uint32_t part[16];
-                            tc::tmem_ld16u(from + (n & 1) * COLS + j * S::BN + p * 32, part);
+                        if ((2 * p + side) * W < un.count) {
+                            uint32_t part[W];
+                            const uint32_t t = from + (n & 1) * COLS + j * BN + 2 * p * W;
+                            if constexpr (W == 32) tc::tmem_ld32u(t, part);
+                            else tc::tmem_ld16u(t, part);
                             tc::tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) tc::fma2(acc[p][i], acc[p][i + 1], part[i], part[i + 1], sc[j]);
+                            for (int i = 0; i < W; i += 2) tc::fma2(acc[p][i], acc[p][i + 1], part[i], part[i + 1], sc[j]);
                         }
                 tc::tc_fence_before();
                 __syncwarp();
@@ -385,17 +450,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) int4_many_kernel(const Int4Call c
 #pragma unroll
             for (int p = 0; p < PIECES; ++p)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int m = p * 32 + side * 16 + i;
+                for (int i = 0; i < W; ++i) {
+                    const int m = (2 * p + side) * W + i;
                     float v = acc[p][i];
-                    if (c.gated) {
-                        const float up = __shfl_xor_sync(0xFFFFFFFFu, v, 8);
-                        v = i4::gate(v, up);
-                    }
+                    if (c.gated) v = i4::gate(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
                     if (mine && m < un.count) i4::store_y(c, un.row0 + m, n0, v);
                 }
         }
-        i4::copy_wait<0>();
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -403,18 +464,39 @@ __global__ void __launch_bounds__(NTHREADS, 1) int4_many_kernel(const Int4Call c
     if (warp == 0) tc::tmem_dealloc(tmem, 512);
 }
 
-template <int CHUNKS>
-cudaError_t launch(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
+template <int CHUNKS, XMode MODE, bool ZEROS>
+cudaError_t launch(const moe_int4* L, const Int4Call& c, const CUtensorMap& map, cudaStream_t s) {
     constexpr int fixed = sizeof(Smem<CHUNKS>) + 1024;
     constexpr int most = fixed + 2 * (MOE_DISPATCH_MAX_EXPERTS + 1) * (int)sizeof(int);
     static_assert(most <= 227 * 1024 - 1024, "shared memory");
-    cudaError_t e = ensure_smem_limit<int4_many_kernel<CHUNKS>>(most);
+    constexpr int bn = Smem<CHUNKS>::BN;
+    cudaError_t e = ensure_smem_limit<int4_many_kernel<CHUNKS, MODE, ZEROS>>(most);
     if (e != cudaSuccess) return e;
-    const int bn = Smem<CHUNKS>::BN;
     const int64_t tiles = (c.blocks + BM_BLOCKS - 1) / BM_BLOCKS;
     const int64_t row_tiles = c.offsets ? std::min<int64_t>(c.rows, c.rows / bn + c.E) : (c.rows + bn - 1) / bn;
     const int64_t grid = std::min<int64_t>(tiles * row_tiles, L->num_sms);
-    return launch_pdl(int4_many_kernel<CHUNKS>, dim3((unsigned)grid), dim3(NTHREADS), fixed + 2 * (c.E + 1) * (int)sizeof(int), s, c, bn);
+    return launch_pdl(int4_many_kernel<CHUNKS, MODE, ZEROS>, dim3((unsigned)grid), dim3(NTHREADS),
+                      fixed + 2 * (c.E + 1) * (int)sizeof(int), s, map, c);
+}
+
+template <int CHUNKS, XMode MODE>
+cudaError_t launch_types(const moe_int4* L, const Int4Call& c, const CUtensorMap& map, cudaStream_t s) {
+    return c.z ? launch<CHUNKS, MODE, true>(L, c, map, s) : launch<CHUNKS, MODE, false>(L, c, map, s);
+}
+
+template <int CHUNKS>
+cudaError_t launch_mode(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
+    CUtensorMap map = {};
+    if (c.x_grid < 16) return launch_types<CHUNKS, X_COPY>(L, c, map, s);
+    const EncodeTiledFn encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {(cuuint64_t)c.K, (cuuint64_t)c.x_rows}, strides[1] = {(cuuint64_t)c.ldx * 2};
+    const cuuint32_t box[2] = {I4_K, c.token ? 1u : (cuuint32_t)X_BOX}, step[2] = {1, 1};
+    if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(c.x), dims, strides, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    return c.token ? launch_types<CHUNKS, X_GATHER>(L, c, map, s) : launch_types<CHUNKS, X_TILE>(L, c, map, s);
 }
 
 }  // namespace
@@ -423,8 +505,8 @@ bool int4_takes_many(const Int4Call& c) { return (c.offsets ? c.rows / c.E : c.r
 
 cudaError_t launch_int4_many(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
     const int group = L->d.group;
-    if (group % 128 == 0 || L->groups == 1) return launch<1>(L, c, s);
-    return group % 64 == 0 ? launch<2>(L, c, s) : launch<4>(L, c, s);
+    if (group % 128 == 0 || L->groups == 1) return launch_mode<1>(L, c, s);
+    return group % 64 == 0 ? launch_mode<2>(L, c, s) : launch_mode<4>(L, c, s);
 }
 
 }  // namespace moe
