@@ -57,13 +57,14 @@ MOE_EXPORT moe_status moe_int4_create(const moe_int4_desc* d, const moe_int4_wei
     L->groups = (L->kt * moe::I4_K + L->d.group - 1) / L->d.group;
     const int per = d->gated ? 8 : moe::I4_ROWS;
     L->blocks = ((d->out_features + per - 1) / per + 3) / 4 * 4;
+    L->strips = (L->blocks + moe::I4_STRIP - 1) / moe::I4_STRIP;
     L->wait_limit = kDefaultWaitLimitUs;
-    const size_t eb = (size_t)d->n_experts * L->blocks, recs = eb * L->groups * 8;
+    const size_t strips = (size_t)d->n_experts * L->strips, recs = strips * L->groups * moe::I4_STRIP * 8;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const char* what = "device query";
     cudaError_t e = cudaGetDevice(&L->device);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&L->num_sms, cudaDevAttrMultiProcessorCount, L->device);
-    if (e == cudaSuccess) what = "allocating weights", e = cudaMalloc(&L->w, eb * L->kt * 512);
+    if (e == cudaSuccess) what = "allocating weights", e = cudaMalloc(&L->w, strips * L->kt * moe::I4_STRIP * 512);
     if (e == cudaSuccess) what = "allocating scales", e = cudaMalloc(&L->s, recs * 2 * ss);
     if (e == cudaSuccess && w->z) what = "allocating zero points", e = cudaMalloc(&L->z, recs * 4);
     if (e == cudaSuccess) what = "allocating status", e = cudaMalloc(&L->dev_status, 4);
@@ -129,6 +130,7 @@ MOE_EXPORT moe_status moe_int4_forward(moe_int4* L, const moe_int4_args* a, void
     c.K = L->d.in_features;
     c.E = L->d.n_experts;
     c.blocks = L->blocks;
+    c.strips = L->strips;
     c.kt = L->kt;
     c.groups = L->groups;
     c.wait_limit = L->wait_limit;

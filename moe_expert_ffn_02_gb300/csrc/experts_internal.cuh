@@ -6,29 +6,32 @@
 
 // ---------------------------------------------------------------------------
 // Image of 4-bit weights.  A block is 16 rows of one expert's matrix (gated:
-// 8 gate rows, then the 8 up rows of the same features), a tile 64 input
-// channels of a block in 512 bytes, 16 for each lane of a warp.  Lane
-// 4 g + q has the channels 16 i + 4 q .. 16 i + 4 q + 3 (i = 0 to 3) of row g
-// in two words of 8 codes, then those of row g + 8: what a lane holds of a
-// 16 x 16 mma.sync operand (with x in the same order of channels) and of a
-// 16 x 256-bit store to tensor memory, so either kernel takes its operand by
-// one 16-byte load per lane.  In a word, nibbles 0 to 3 are the even channels
-// and 4 to 7 the odd ones: (word >> 4 j) & 0x000F000F are the j-th two
-// channels as two halves.  Tiles of a block follow one another; channels past
-// the matrix meet zeros of x.
-// Scales: [expert][block][group][8] pairs (row g, row g + 8); zero points
-// likewise as 128 + z in bf16.  Rows past the matrix have scales of zero.
+// 8 gate rows, then the 8 up rows of the same features), a strip 8 blocks, a
+// tile 64 input channels of a block in 512 bytes, 16 for each lane of a warp.
+// Tiles lie [expert][strip][64 channels][block of the strip], so that what a
+// strip needs for a run of channels is one piece.  Lane 4 g + q has the
+// channels 16 i + 4 q .. 16 i + 4 q + 3 (i = 0 to 3) of row g in two words of
+// 8 codes, then those of row g + 8: what a lane holds of a 16 x 16 mma.sync
+// operand (with x in the same order of channels) and of a 16 x 256-bit store
+// to tensor memory, so either kernel takes its operand by one 16-byte load per
+// lane.  In a word, nibbles 0 to 3 are the even channels and 4 to 7 the odd
+// ones: (word >> 4 j) & 0x000F000F are the j-th two channels as two halves.
+// Channels past the matrix meet zeros of x.
+// Scales: [expert][strip][group][block of the strip][8] pairs (row g, row
+// g + 8); zero points likewise as 128 + z in bf16.  Rows past the matrix have
+// scales of zero.
 // ---------------------------------------------------------------------------
 struct moe_int4 {
     moe_int4_desc d;
     int device;
     int num_sms;
-    int blocks;            // per expert, a multiple of 4
+    int blocks;            // per expert that hold rows, up to a multiple of 4
+    int strips;            // per expert
     int kt;                // tiles per block: ceil(in / 64)
     int groups;            // per row, over the tiles' 64 kt channels
-    uint4* w;              // [expert][block][kt][32]
-    void* s;               // [expert][block][groups][8] pairs of bf16 or fp32
-    uint32_t* z;           // [expert][block][groups][8] pairs of bf16, or NULL: 136
+    uint4* w;              // [expert][strip][kt][8][32]
+    void* s;               // [expert][strip][groups][8][8] pairs of bf16 or fp32
+    uint32_t* z;           // [expert][strip][groups][8][8] pairs of bf16, or NULL: 136
     uint32_t* dev_status;  // device status word
     uint32_t wait_limit;
 };
@@ -37,6 +40,7 @@ namespace moe {
 
 constexpr int I4_K = 64;               // channels of a tile
 constexpr int I4_ROWS = 16;            // rows of a block
+constexpr int I4_STRIP = 8;            // blocks of a strip
 constexpr uint32_t I4_ZERO = 0x43084308u;   // 136 = 128 + 8 in bf16, twice
 
 struct Int4Call {
@@ -52,7 +56,7 @@ struct Int4Call {
     uint32_t* status;
     uint64_t group_inv;    // ceil(2^32 / (group / 32)): 32-channel step n is in group n * group_inv >> 32
     int rows, x_rows;
-    int N, K, E, blocks, kt, groups;
+    int N, K, E, blocks, strips, kt, groups;
     uint32_t wait_limit;
     bool s_f32, y_f32, gated;
     int x_grid;            // 16, 8 or 2: the bytes whose multiples all rows of x start on

@@ -24,34 +24,43 @@ namespace moe {
 namespace {
 
 constexpr int THREADS = 256, WARPS = 8;
+constexpr int X_PITCH = 160;           // bytes between rows of a tile of x: the lanes' 8-byte reads fall into different banks
 
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// d (+)= a b; the first of a chain starts from zeros.
+template <bool FIRST>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint2 b) {
+    if (FIRST)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y), "f"(0.f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
 }
 
 // One warp's slot of the ring: a tile of RB blocks and of NB * 8 rows of x.
-template <int RB, int NB, int SUB>
+template <int RB, int NB, int SUB, bool ZEROS>
 struct Slot {
     uint4 w[RB][32];
-    uint2 x[NB][4][32];                // [channels 16 i + 4 q][lane]
-    uint2 s[SUB][RB][8];               // pairs (row g, row g + 8): two fp32, or two bf16 in .x
-    uint32_t z[SUB][RB][8];
+    uint8_t x[NB][8 * X_PITCH];        // [row][64 channels]
+    uint2 s[SUB][RB * 8];              // fp32 pairs (row g, row g + 8); bf16 pairs fill the first half
+    uint32_t z[SUB][ZEROS ? RB * 8 : 4];
 };
 
-template <int RB, int NB, int SUB, int DEPTH>
+template <int RB, int NB, int SUB, bool ZEROS, int DEPTH>
 struct Smem {
-    Slot<RB, NB, SUB> ring[WARPS][DEPTH];
+    Slot<RB, NB, SUB, ZEROS> ring[WARPS][DEPTH];
     float sums[WARPS][NB * 8][RB * I4_ROWS + 4];      // + 4: the lanes' rows fall into different banks
     int table[1];                      // start[E + 1], first[E + 1]
 };
 
 // SUB: scales per tile and row (2 where a group may end inside a tile).
-template <int RB, int NB, int SUB, int DEPTH>
+template <int RB, int NB, int SUB, bool ZEROS, int DEPTH>
 __global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
+    using W = Slot<RB, NB, SUB, ZEROS>;
     extern __shared__ __align__(16) char smem_raw[];
-    auto& sm = *reinterpret_cast<Smem<RB, NB, SUB, DEPTH>*>(smem_raw);
+    auto& sm = *reinterpret_cast<Smem<RB, NB, SUB, ZEROS, DEPTH>*>(smem_raw);
     int* start = sm.table;
     int* first = sm.table + c.E + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -59,74 +68,90 @@ __global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
     // this warp's tiles of 64 channels
     const int per = (c.kt + WARPS - 1) / WARPS, t0 = min(c.kt, warp * per), steps = min(c.kt, t0 + per) - t0;
     pdl_trigger();
-    pdl_wait();
+    if (c.offsets) pdl_wait();
     i4::row_tiles<THREADS>(c, NB * 8, start, first);
     const int units = start[c.E] * feature_tiles;
 
-    // what is copied next
+    // What is copied next.  p_x: where this lane's row of x starts, -1: as zeros, -2: nobody reads it.
     int p_unit = blockIdx.x, p_step = 0, p_slot = 0;
     const uint4* p_w = nullptr;
     size_t p_rec = 0;
     int64_t p_x[NB];
-    auto enter = [&](int u) {
-        const i4::Unit un = i4::unit_at(c, u, feature_tiles, NB * 8, start, first);
-        const size_t block = (size_t)un.expert * c.blocks + un.tile * RB;
-        p_w = c.w + (block * c.kt + t0) * 32 + lane;
-        p_rec = (block + (lane >> 3)) * c.groups * 8 + (lane & 7);
+    auto enter_w = [&](const i4::Unit& un) {
+        const int block = un.tile * RB;
+        const size_t strip = (size_t)un.expert * c.strips + block / I4_STRIP;
+        p_w = c.w + ((strip * c.kt + t0) * I4_STRIP + block % I4_STRIP) * 32 + lane;
+        p_rec = (strip * c.groups * I4_STRIP + block % I4_STRIP) * 8 + lane;
+    };
+    auto enter_x = [&](const i4::Unit& un) {
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-            const int m = n * 8 + g;
-            const int r = m < un.count ? i4::source_row(c, un.row0 + m) : -1;
-            p_x[n] = r < 0 ? -1 : r * c.ldx;
+            const int m = n * 8 + g, r = m < un.count ? i4::source_row(c, un.row0 + m) : -2;
+            p_x[n] = r < 0 ? r : r * c.ldx;
         }
     };
-    auto copy_next = [&]() {
+    auto copy = [&](bool weights, bool rows) {
         if (p_unit < units) {
-            Slot<RB, NB, SUB>& slot = sm.ring[warp][p_slot];
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) i4::copy16(smem_addr(&slot.w[rb][lane]), p_w + (size_t)rb * c.kt * 32);
+            W& slot = sm.ring[warp][p_slot];
             const int t = t0 + p_step;
-            if (lane < RB * 8) {
-#pragma unroll
-                for (int sub = 0; sub < SUB; ++sub) {
-                    const size_t rec = p_rec + (size_t)i4::group_of(c, 2 * t + sub) * 8;
-                    const uint32_t to = smem_addr(&slot.s[sub][lane >> 3][lane & 7]);
-                    if (c.s_f32) i4::copy_small<8>(to, c.s + rec * 8);
-                    else i4::copy_small<4>(to, c.s + rec * 4);
-                    if (c.z) i4::copy_small<4>(smem_addr(&slot.z[sub][lane >> 3][lane & 7]), c.z + rec);
-                }
+            if (p_step == 0) {
+                const i4::Unit un = i4::unit_at(c, p_unit, feature_tiles, NB * 8, start, first);
+                if (weights) enter_w(un);
+                if (rows) enter_x(un);
             }
+            if (weights) {
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
+                for (int rb = 0; rb < RB; ++rb) i4::copy16(smem_addr(&slot.w[rb][lane]), p_w + rb * 32);
+                p_w += I4_STRIP * 32;
+                if (RB == 4 || lane < RB * 8) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = t * I4_K + i * 16 + q * 4;
-                    const int have = p_x[n] < 0 ? 0 : min(max(c.K - k, 0), 4);
-                    const uint16_t* src = have ? c.x + p_x[n] + k : c.x;
-                    if (c.x_grid >= 8) {
-                        i4::copy8(smem_addr(&slot.x[n][i][lane]), src, have * 2);
-                    } else {
-                        uint16_t* to = reinterpret_cast<uint16_t*>(&slot.x[n][i][lane]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) to[j] = j < have ? src[j] : (uint16_t)0;
+                    for (int sub = 0; sub < SUB; ++sub) {
+                        const size_t rec = p_rec + (size_t)i4::group_of(c, 2 * t + sub) * (I4_STRIP * 8);
+                        if (c.s_f32) i4::copy_small<8>(smem_addr(&slot.s[sub][lane]), c.s + rec * 8);
+                        else i4::copy_small<4>(smem_addr(reinterpret_cast<uint32_t*>(slot.s[sub]) + lane), c.s + rec * 4);
+                        if (ZEROS) i4::copy_small<4>(smem_addr(&slot.z[sub][lane]), c.z + rec);
                     }
                 }
             }
-            p_w += 32;
+            if (rows) {
+                const int k = t * I4_K + q * 8;
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    if (p_x[n] == -2) continue;
+                    uint8_t* to = slot.x[n] + g * X_PITCH + q * 16;
+                    const uint16_t* src = c.x + max(p_x[n], (int64_t)0) + k;
+                    const int have = p_x[n] < 0 ? 0 : c.K - k;          // channels from k on
+                    if (c.x_grid == 16) {
+                        const int b0 = min(max(have, 0), 8) * 2, b1 = min(max(have - 32, 0), 8) * 2;
+                        i4::copy16(smem_addr(to), b0 ? src : c.x, b0);
+                        i4::copy16(smem_addr(to + 64), b1 ? src + 32 : c.x, b1);
+                    } else {
+                        *reinterpret_cast<uint4*>(to) = i4::load8(src, have);
+                        *reinterpret_cast<uint4*>(to + 64) = i4::load8(src + 32, have - 32);
+                    }
+                }
+            }
             if (++p_step == steps) {
                 p_step = 0;
                 p_unit += gridDim.x;
-                if (p_unit < units) enter(p_unit);
             }
         }
         p_slot = p_slot + 1 == DEPTH ? 0 : p_slot + 1;
-        i4::copy_commit();
     };
 
+    // the weights do not depend on the preceding kernel: the first of them are requested before the wait for it
     if (steps > 0) {
-        if (p_unit < units) enter(p_unit);
-#pragma unroll
-        for (int i = 0; i < DEPTH - 1; ++i) copy_next();
+#pragma unroll 1
+        for (int i = 0; i < DEPTH - 1; ++i) copy(true, false);
+    }
+    if (!c.offsets) pdl_wait();
+    if (steps > 0) {
+        p_unit = blockIdx.x, p_step = p_slot = 0;
+#pragma unroll 1
+        for (int i = 0; i < DEPTH - 1; ++i) {
+            copy(false, true);
+            i4::copy_commit();
+        }
     }
     int slot_at = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
@@ -139,15 +164,16 @@ __global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
                 for (int i = 0; i < 4; ++i) acc[rb][n][i] = 0.f;
         for (int step = 0; step < steps; ++step) {
             i4::copy_wait<DEPTH - 2>();
-            __syncwarp();                      // the other lanes' copies (scales), and their reads of the slot filled next
-            copy_next();
-            const Slot<RB, NB, SUB>& slot = sm.ring[warp][slot_at];
+            __syncwarp();                      // the other lanes' copies, and their reads of the slot filled next
+            copy(true, true);
+            i4::copy_commit();
+            const W& slot = sm.ring[warp][slot_at];
             slot_at = slot_at + 1 == DEPTH ? 0 : slot_at + 1;
             uint2 xv[NB][4];
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) xv[n][i] = slot.x[n][i][lane];
+                for (int i = 0; i < 4; ++i) xv[n][i] = *reinterpret_cast<const uint2*>(slot.x[n] + g * X_PITCH + i * 32 + q * 8);
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) {
                 const uint4 w = slot.w[rb][lane];
@@ -155,26 +181,26 @@ __global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {         // 32 channels: two k16 steps
                     const int sub = SUB == 2 ? half : 0;
-                    const uint32_t zp = c.z ? slot.z[sub][rb][g] : I4_ZERO;
+                    const uint32_t z = ZEROS ? slot.z[sub][ZEROS ? rb * 8 + g : 0] : I4_ZERO;
                     uint32_t lo[4], hi[4];
-                    i4::widen(half ? w.y : w.x, __byte_perm(zp, 0, 0x1010), lo);
-                    i4::widen(half ? w.w : w.z, __byte_perm(zp, 0, 0x3232), hi);
-                    if (half == 0 || SUB == 2) {
-#pragma unroll
-                        for (int n = 0; n < NB; ++n)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) part[n][i] = 0.f;
-                    }
+                    i4::widen(half ? w.y : w.x, ZEROS ? __byte_perm(z, 0, 0x1010) : z, lo);
+                    i4::widen(half ? w.w : w.z, ZEROS ? __byte_perm(z, 0, 0x3232) : z, hi);
                     const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
                     for (int n = 0; n < NB; ++n) {
-                        mma(part[n], a0, xv[n][2 * half].x, xv[n][2 * half].y);
-                        mma(part[n], a1, xv[n][2 * half + 1].x, xv[n][2 * half + 1].y);
+                        if (half == 0 || SUB == 2) mma<true>(part[n], a0, xv[n][2 * half]);
+                        else mma<false>(part[n], a0, xv[n][2 * half]);
+                        mma<false>(part[n], a1, xv[n][2 * half + 1]);
                     }
                     if (half == 1 || SUB == 2) {
-                        const uint2 sv = slot.s[sub][rb][g];
-                        const float s0 = c.s_f32 ? __uint_as_float(sv.x) : __uint_as_float(sv.x << 16);
-                        const float s1 = c.s_f32 ? __uint_as_float(sv.y) : __uint_as_float(sv.x & 0xFFFF0000u);
+                        float s0, s1;
+                        if (c.s_f32) {
+                            const uint2 v = slot.s[sub][rb * 8 + g];
+                            s0 = __uint_as_float(v.x), s1 = __uint_as_float(v.y);
+                        } else {
+                            const uint32_t v = reinterpret_cast<const uint32_t*>(slot.s[sub])[rb * 8 + g];
+                            s0 = __uint_as_float(v << 16), s1 = __uint_as_float(v & 0xFFFF0000u);
+                        }
 #pragma unroll
                         for (int n = 0; n < NB; ++n) {
                             acc[rb][n][0] = __fmaf_rn(s0, part[n][0], acc[rb][n][0]);
@@ -200,7 +226,7 @@ __global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
         __syncthreads();
         const int wide = c.gated ? RB * 8 : RB * 16;           // output features of a tile
         for (int i = threadIdx.x; i < un.count * wide; i += THREADS) {
-            const int m = i / wide, f = i - m * wide;
+            const int m = c.gated ? i / (RB * 8) : i / (RB * 16), f = i - m * wide;
             const int n = un.tile * wide + f;
             if (n >= c.N) continue;
             if (c.gated) {
@@ -224,13 +250,14 @@ __global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
     i4::copy_wait<0>();
 }
 
-template <int RB, int NB, int SUB>
+template <int RB, int NB, int SUB, bool ZEROS>
 cudaError_t launch(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
-    constexpr int DEPTH = RB == 4 ? 3 : 4;
-    constexpr auto kernel = int4_few_kernel<RB, NB, SUB, DEPTH>;
-    const int bytes = sizeof(Smem<RB, NB, SUB, DEPTH>) + 2 * (c.E + 1) * (int)sizeof(int);
-    constexpr int most = sizeof(Smem<RB, NB, SUB, DEPTH>) + 2 * (MOE_DISPATCH_MAX_EXPERTS + 1) * (int)sizeof(int);
-    static_assert(most <= 227 * 1024, "shared memory");
+    constexpr int DEPTH = RB == 4 || NB == 4 ? 3 : 4;
+    using S = Smem<RB, NB, SUB, ZEROS, DEPTH>;
+    constexpr auto kernel = int4_few_kernel<RB, NB, SUB, ZEROS, DEPTH>;
+    const int bytes = sizeof(S) + 2 * (c.E + 1) * (int)sizeof(int);
+    constexpr int most = sizeof(S) + 2 * (MOE_DISPATCH_MAX_EXPERTS + 1) * (int)sizeof(int);
+    static_assert(most <= 227 * 1024 - 1024, "shared memory");
     cudaError_t e = ensure_smem_limit<kernel>(most);
     if (e != cudaSuccess) return e;
     const int per_sm = std::min(4, 227 * 1024 / (bytes + 1024));
@@ -243,7 +270,8 @@ cudaError_t launch(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
 
 template <int RB, int NB>
 cudaError_t launch_sub(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
-    return L->d.group % I4_K ? launch<RB, NB, 2>(L, c, s) : launch<RB, NB, 1>(L, c, s);
+    if (L->d.group % I4_K) return c.z ? launch<RB, NB, 2, true>(L, c, s) : launch<RB, NB, 2, false>(L, c, s);
+    return c.z ? launch<RB, NB, 1, true>(L, c, s) : launch<RB, NB, 1, false>(L, c, s);
 }
 
 template <int RB>
@@ -256,15 +284,12 @@ cudaError_t launch_rows(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
 
 // One thread per lane's 16 bytes.
 __global__ void __launch_bounds__(256) int4_repack_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ q_up,
-                                                          int N, int K, int blocks, int kt, int64_t total,
+                                                          int N, int K, int strips, int kt, int64_t total,
                                                           uint4* __restrict__ w) {
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int lane = i & 31, g = lane >> 2, qd = lane & 3;
-        const int64_t tile = i >> 5;
-        const int t = tile % kt;
-        const int64_t eb = tile / kt;
-        const int block = eb % blocks;
-        const int64_t e = eb / blocks;
+        const int lane = i & 31, g = lane >> 2, qd = lane & 3, in = i >> 5 & (I4_STRIP - 1);
+        const int64_t tile = i >> 8, es = tile / kt, e = es / strips;
+        const int t = tile - es * kt, block = (int)(es - e * strips) * I4_STRIP + in;
         const int64_t row_bytes = (K + 1) / 2;
         uint32_t out[4] = {};
 #pragma unroll
@@ -292,15 +317,12 @@ __global__ void __launch_bounds__(256) int4_repack_kernel(const uint8_t* __restr
 template <typename T>
 __global__ void __launch_bounds__(256) int4_scales_kernel(const T* __restrict__ s, const T* __restrict__ s_up,
                                                           const uint8_t* __restrict__ z, const uint8_t* __restrict__ z_up,
-                                                          int N, int src_groups, int blocks, int groups, int64_t total,
+                                                          int N, int src_groups, int strips, int groups, int64_t total,
                                                           T* __restrict__ s_out, uint32_t* __restrict__ z_out) {
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int g = i & 7;
-        const int64_t rec = i >> 3;
-        const int gi = rec % groups;
-        const int64_t eb = rec / groups;
-        const int block = eb % blocks;
-        const int64_t e = eb / blocks;
+        const int g = i & 7, in = i >> 3 & (I4_STRIP - 1);
+        const int64_t rec = i >> 6, es = rec / groups, e = es / strips;
+        const int gi = rec - es * groups, block = (int)(es - e * strips) * I4_STRIP + in;
         uint32_t zs[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -318,10 +340,10 @@ __global__ void __launch_bounds__(256) int4_scales_kernel(const T* __restrict__ 
 
 cudaError_t launch_int4_repack(const moe_int4* L, const moe_int4_weights* w, cudaStream_t s) {
     const moe_int4_desc& d = L->d;
-    const int64_t words = (int64_t)d.n_experts * L->blocks * L->kt * 32;
-    const int64_t recs = (int64_t)d.n_experts * L->blocks * L->groups * 8;
+    const int64_t words = (int64_t)d.n_experts * L->strips * L->kt * I4_STRIP * 32;
+    const int64_t recs = (int64_t)d.n_experts * L->strips * L->groups * I4_STRIP * 8;
     auto grid = [](int64_t n) { return dim3((unsigned)std::min<int64_t>((n + 255) / 256, 1 << 20)); };
-    int4_repack_kernel<<<grid(words), 256, 0, s>>>(w->q, d.gated ? w->q_up : nullptr, d.out_features, d.in_features, L->blocks, L->kt,
+    int4_repack_kernel<<<grid(words), 256, 0, s>>>(w->q, d.gated ? w->q_up : nullptr, d.out_features, d.in_features, L->strips, L->kt,
                                                    words, L->w);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -329,12 +351,12 @@ cudaError_t launch_int4_repack(const moe_int4* L, const moe_int4_weights* w, cud
     const uint8_t* z_up = d.gated ? w->z_up : nullptr;
     if (d.scale_type == MOE_F32)
         int4_scales_kernel<<<grid(recs), 256, 0, s>>>(static_cast<const float*>(w->s), static_cast<const float*>(d.gated ? w->s_up : nullptr),
-                                                      w->z, z_up, d.out_features, src_groups, L->blocks, L->groups, recs,
+                                                      w->z, z_up, d.out_features, src_groups, L->strips, L->groups, recs,
                                                       static_cast<float*>(L->s), L->z);
     else
         int4_scales_kernel<<<grid(recs), 256, 0, s>>>(static_cast<const __nv_bfloat16*>(w->s),
                                                       static_cast<const __nv_bfloat16*>(d.gated ? w->s_up : nullptr), w->z, z_up,
-                                                      d.out_features, src_groups, L->blocks, L->groups, recs,
+                                                      d.out_features, src_groups, L->strips, L->groups, recs,
                                                       static_cast<__nv_bfloat16*>(L->s), L->z);
     return cudaGetLastError();
 }

@@ -36,7 +36,6 @@ constexpr int NTHREADS = (X_WARP + X_WARPS) * 32;        // 768: six warpgroups
 constexpr int DRAIN_REGS = 120, OTHER_REGS = 56;
 static_assert(DRAIN_WARPS * 32 * DRAIN_REGS + (NTHREADS - DRAIN_WARPS * 32) * OTHER_REGS <= NTHREADS * 80, "register split");
 
-constexpr int BM_BLOCKS = 8;                     // 128 weight rows
 constexpr int STAGE_K = 128, STAGE_TILES = 2;    // channels; 64-channel tiles
 constexpr int STAGES = 4;                        // operands of the MMA
 constexpr int RING = 6;                          // codes: 8 KB a stage, to keep some 40 KB in flight
@@ -46,12 +45,12 @@ constexpr int A_BASE = 2 * COLS;
 static_assert(A_BASE + STAGES * A_COLS <= 512, "tensor memory");
 constexpr int X_BOX = 32;                        // rows of x that one copy brings
 
-// A stage of weights as it is copied: per block its tiles and the records of the groups that it meets.
+// A stage of a strip as it is copied: its tiles and the records of the groups that it meets.
 template <int CHUNKS>
 struct Codes {
-    uint4 w[BM_BLOCKS][STAGE_TILES][32];
-    uint2 s[BM_BLOCKS][CHUNKS][8];               // fp32 pairs; bf16 pairs lie in the first half of each block's
-    uint32_t z[BM_BLOCKS][CHUNKS][8];
+    uint4 w[STAGE_TILES][I4_STRIP][32];
+    uint2 s[CHUNKS][I4_STRIP][8];                // fp32 pairs; bf16 pairs fill the first half
+    uint32_t z[CHUNKS][I4_STRIP][8];
 };
 
 template <int CHUNKS>
@@ -121,28 +120,6 @@ __device__ __forceinline__ uint32_t idesc_for(int n) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-// Eight channels of a row that starts on a 2-byte boundary, those from `have` on as zeros.  Words that
-// straddle the piece's ends are read as halves: nothing outside it is touched.
-__device__ __forceinline__ uint4 load8(const uint16_t* p, int have) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (have >= 8) {
-        if ((reinterpret_cast<uintptr_t>(p) & 2) == 0) {
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
-            v = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(p + 1);
-            const uint32_t a = p[0], b = w[0], c = w[1], d = w[2], e = p[7];
-            v = make_uint4(a | b << 16, __funnelshift_l(b, c, 16), __funnelshift_l(c, d, 16), d >> 16 | e << 16);
-        }
-    } else if (have > 0) {
-        uint32_t h[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = i < have ? p[i] : 0u;
-        v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-    }
-    return v;
-}
-
 enum XMode { X_TILE, X_GATHER, X_COPY };
 
 template <int CHUNKS, XMode MODE, bool ZEROS>
@@ -154,7 +131,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) int4_many_kernel(const __grid_con
     int* start = sm.table;
     int* first = sm.table + c.E + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int feature_tiles = (c.blocks + BM_BLOCKS - 1) / BM_BLOCKS;
+    const int feature_tiles = c.strips;
     const int stages = (c.kt + STAGE_TILES - 1) / STAGE_TILES;      // per unit
 
     if (threadIdx.x == 0) {
@@ -202,12 +179,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) int4_many_kernel(const __grid_con
                     uint4 code[STAGE_TILES];
                     uint32_t zero[4];
 #pragma unroll
-                    for (int tile = 0; tile < STAGE_TILES; ++tile) code[tile] = in.w[block][tile][lane];
+                    for (int tile = 0; tile < STAGE_TILES; ++tile) code[tile] = in.w[tile][block][lane];
                     if (ZEROS) {
                         const int g0 = i4::group_of(c, st * 4);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            zero[i] = in.z[block][CHUNKS == 1 ? 0 : min(i4::group_of(c, st * 4 + i) - g0, CHUNKS - 1)][g];
+                            zero[i] = in.z[CHUNKS == 1 ? 0 : min(i4::group_of(c, st * 4 + i) - g0, CHUNKS - 1)][block][g];
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.code_free[at]);
@@ -242,37 +219,32 @@ __global__ void __launch_bounds__(NTHREADS, 1) int4_many_kernel(const __grid_con
             }
         } else if (warp == CODE_WARP) {
             // ------------------------------------------------------------ codes, scales, zero points
-            // lanes 0 to 7 copy a block's tiles, 8 to 15 its scales, 16 to 23 its zero points
-            constexpr int Z_REC = 32;
-            const int s_rec = c.s_f32 ? 64 : 32;
-            const int block = lane & 7, what = lane >> 3;
+            const uint32_t el = elect_one();
+            const int s_rec = (c.s_f32 ? 8 : 4) * I4_STRIP * 8, z_rec = 4 * I4_STRIP * 8;    // bytes of a strip's group
             int slot = 0, issued = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
                 const i4::Unit un = unit_at(u);
-                const int blocks = min(BM_BLOCKS, c.blocks - un.tile * BM_BLOCKS);
-                const size_t b = (size_t)un.expert * c.blocks + un.tile * BM_BLOCKS + block;
-                const bool copies = block < blocks && what < (ZEROS ? 3 : 2);
-                const char* src = what == 0 ? reinterpret_cast<const char*>(c.w) + b * c.kt * 512
-                                : what == 1 ? c.s + b * c.groups * s_rec : reinterpret_cast<const char*>(c.z) + b * c.groups * Z_REC;
+                const size_t strip = (size_t)un.expert * c.strips + un.tile;
+                const char* w = reinterpret_cast<const char*>(c.w) + strip * c.kt * (I4_STRIP * 512);
+                const char* s = c.s + strip * c.groups * s_rec;
+                const char* z = reinterpret_cast<const char*>(c.z) + strip * c.groups * z_rec;
                 for (int st = 0; st < stages; ++st) {
                     if (issued == RING) pdl_wait();
                     ok = issued < RING || warp_wait(&sm.code_free[slot], phase ^ 1u);
                     if (!ok) break;
                     Codes<CHUNKS>& in = sm.ring[slot];
-                    const int tiles = min(STAGE_TILES, c.kt - st * STAGE_TILES);
+                    const int bytes = min(STAGE_TILES, c.kt - st * STAGE_TILES) * (I4_STRIP * 512);
                     const int g0 = i4::group_of(c, st * 4), groups = i4::group_of(c, min(st * 4 + 3, 2 * c.kt - 1)) - g0 + 1;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(&sm.code_full[slot], blocks * (tiles * 512 + groups * (s_rec + (ZEROS ? Z_REC : 0))));
-                    __syncwarp();
-                    if (copies) {
-                        if (what == 0) bulk_g2s(&in.w[block], src + st * (STAGE_TILES * 512), tiles * 512, &sm.code_full[slot]);
-                        else if (what == 1) bulk_g2s(&in.s[block], src + (size_t)g0 * s_rec, groups * s_rec, &sm.code_full[slot]);
-                        else bulk_g2s(&in.z[block], src + (size_t)g0 * Z_REC, groups * Z_REC, &sm.code_full[slot]);
+                    if (el) {
+                        mbar_arrive_expect_tx(&sm.code_full[slot], bytes + groups * (s_rec + (ZEROS ? z_rec : 0)));
+                        bulk_g2s(in.w, w + (size_t)st * (STAGE_TILES * I4_STRIP * 512), bytes, &sm.code_full[slot]);
+                        bulk_g2s(in.s, s + (size_t)g0 * s_rec, groups * s_rec, &sm.code_full[slot]);
+                        if (ZEROS) bulk_g2s(in.z, z + (size_t)g0 * z_rec, groups * z_rec, &sm.code_full[slot]);
                     }
-                    ++issued;
-                    if (issued > RING) issued = RING + 1;
+                    __syncwarp();
+                    issued = min(issued, RING) + 1;
                     if (++slot == RING) { slot = 0; phase ^= 1u; }
                 }
             }
@@ -360,7 +332,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) int4_many_kernel(const __grid_con
 #pragma unroll
                             for (int i = 0; i < BATCH; ++i) {
                                 const int k = ((lane & 3) + 4 * i) * 8;
-                                v[i] = load8(p + k, from < 0 ? 0 : min(c.K - st * STAGE_K - k, 8));
+                                v[i] = i4::load8(p + k, from < 0 ? 0 : min(c.K - st * STAGE_K - k, 8));
                             }
                             if (r < un.count) {
 #pragma unroll
@@ -414,8 +386,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) int4_many_kernel(const __grid_con
 #pragma unroll
                 for (int j = 0; j < CHUNKS; ++j) {
                     const int rec = CHUNKS == 1 ? 0 : min(i4::group_of(c, st * 4 + j * (4 / CHUNKS)) - g0, CHUNKS - 1);
-                    const uint32_t* s = reinterpret_cast<const uint32_t*>(sm.ring[at].s[block]);
-                    const uint32_t v = c.s_f32 ? s[(rec * 8 + g) * 2 + upper] : s[rec * 8 + g];
+                    const uint32_t* s = reinterpret_cast<const uint32_t*>(sm.ring[at].s);
+                    const int pair = (rec * I4_STRIP + block) * 8 + g;
+                    const uint32_t v = c.s_f32 ? s[pair * 2 + upper] : s[pair];
                     sc[j] = __uint_as_float(c.s_f32 ? v : upper ? v & 0xFFFF0000u : v << 16);
                     // the last stage's second tile may lie past the matrix
                     if (CHUNKS > 1 && st * 4 + j * (4 / CHUNKS) >= 2 * c.kt) sc[j] = 0.f;
@@ -445,7 +418,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) int4_many_kernel(const __grid_con
                 if (lane == 0) mbar_arrive(&sm.drained[n & 1]);
             }
             if (!ok) break;
-            const int n0 = c.gated ? (un.tile * BM_BLOCKS + block) * 8 + g : un.tile * 128 + row;
+            const int n0 = c.gated ? (un.tile * I4_STRIP + block) * 8 + g : un.tile * 128 + row;
             const bool mine = n0 < c.N && !(c.gated && upper);
 #pragma unroll
             for (int p = 0; p < PIECES; ++p)
@@ -472,7 +445,7 @@ cudaError_t launch(const moe_int4* L, const Int4Call& c, const CUtensorMap& map,
     constexpr int bn = Smem<CHUNKS>::BN;
     cudaError_t e = ensure_smem_limit<int4_many_kernel<CHUNKS, MODE, ZEROS>>(most);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (c.blocks + BM_BLOCKS - 1) / BM_BLOCKS;
+    const int64_t tiles = c.strips;
     const int64_t row_tiles = c.offsets ? std::min<int64_t>(c.rows, c.rows / bn + c.E) : (c.rows + bn - 1) / bn;
     const int64_t grid = std::min<int64_t>(tiles * row_tiles, L->num_sms);
     return launch_pdl(int4_many_kernel<CHUNKS, MODE, ZEROS>, dim3((unsigned)grid), dim3(NTHREADS),
