@@ -59,6 +59,7 @@ struct Int4Call {
     int N, K, E, blocks, strips, kt, groups;
     uint32_t wait_limit;
     bool s_f32, y_f32, gated;
+    bool groups_are_chunks;    // many rows: a group is what one accumulator sums up
     int x_grid;            // 16, 8 or 2: the bytes whose multiples all rows of x start on
 };
 

@@ -143,6 +143,8 @@ __device__ __forceinline__ int source_row(const Int4Call& c, int r) {
 // infinite and the quotient -0.
 __device__ __forceinline__ float gate(float g, float u) { return __fdiv_rn(g, 1.0f + expf(-g)) * u; }
 
+__device__ __forceinline__ void put_y(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put_y(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store_y(const Int4Call& c, int row, int n, float v) {
     if (c.y_f32)
         static_cast<float*>(c.y)[row * c.ldy + n] = v;
