@@ -2,22 +2,23 @@
 // tensor cores (tcgen05, sm_103a).
 //
 // A tile is 128 weight rows (the MMA's M, tensor-memory lanes) by up to BN
-// rows of x (its N, columns), a stage 256 input channels in two halves.  Four
-// warps widen the codes, less their zero points, to bf16, exactly, and store
-// them straight into tensor memory as the MMA's first operand: through shared
+// rows of x (its N, columns), a stage 128 input channels.  Four warps widen the
+// codes of a stage, less their zero points, to bf16, exactly, and store them
+// straight into tensor memory as the MMA's first operand: through shared
 // memory each weight would be written and read there at two bytes, as long as
-// the MMAs of 64 columns take.  Four warps drain; of the rest one brings codes,
-// scales and zero points (bulk copies), one the rows of x (TMA, gathered by
-// token where there are tokens) and one issues the MMAs.  Rows of x off the
-// 16-byte grid, which TMA does not take, are brought by ten warps.
+// the MMAs of 64 columns take.  One of them issues the MMAs; all wait, scale
+// what came out and add it up in fp32 registers.
 //
 // The tensor core's running sum truncates, and scales are per 32 channels at
-// the finest: each half goes into fresh accumulators, CHUNKS of them (1, 2 or
-// 4, of 128, 64 or 32 channels, as fine as the groups), which the drain warps
-// scale and add up in fp32 registers.  A lane is one weight row, so a scale is
-// one scalar per thread and chunk.  Tensor memory holds 128 columns of
-// accumulators per half, so that BN = 128 / CHUNKS, and two stages of operands.
+// the finest: each stage goes into fresh accumulators, CHUNKS of them (1, 2 or
+// 4, of 128, 64 or 32 channels, as fine as the groups).  A lane is one weight
+// row, so a scale is one scalar per thread and chunk.
 //
+// What there is to overlap, CTAs overlap: four share an SM (two where CHUNKS is
+// more than one and the accumulators take more of the tensor memory).  Warps
+// with roles of their own, one CTA to the SM, were twice as slow: each hand-off
+// between roles costs its 100 to 300 clocks, each role's code its place in the
+// instruction cache, and the widening warps keep the others from issuing.
 #include <algorithm>
 
 #include "dense_internal.cuh"
@@ -28,51 +29,35 @@ namespace moe {
 
 namespace {
 
-constexpr int DRAIN_WARPS = 4, WIDEN_WARPS = 4;
-constexpr int CODE_WARP = DRAIN_WARPS + WIDEN_WARPS, MMA_WARP = CODE_WARP + 1, X_WARP = MMA_WARP + 1;
+constexpr int THREADS = 128;
+constexpr int TILES = 2, STAGE_K = TILES * I4_K, STEPS = STAGE_K / 32;     // of 64 and of 32 channels
+constexpr int A_COLS = STAGE_K / 2;              // operand columns: two bf16 channels each
+constexpr int X_SLOTS = 2;                       // stages of x
 
 enum XMode { X_TILE, X_GATHER, X_COPY };
 
-// Warps that bring x, and the register split of setmaxnreg: the drain warps rise to DRAIN_REGS, the others drop
-// to OTHER_REGS, of LAUNCH_REGS per thread.  (A warpgroup is four warps: without the copying warps one idles.)
-template <XMode MODE>
+// Tensor memory: accumulators, then the operand.
+template <int CHUNKS>
 struct Shape {
-    static constexpr int X_WARPS = MODE == X_COPY ? 10 : 1;
-    static constexpr int THREADS = MODE == X_COPY ? 640 : 384;
-    static constexpr int LAUNCH_REGS = MODE == X_COPY ? 96 : 168;
-    static constexpr int DRAIN_REGS = MODE == X_COPY ? 208 : 232, OTHER_REGS = MODE == X_COPY ? 64 : 136;
-    static_assert(X_WARP + X_WARPS <= THREADS / 32, "warps");
-    static_assert(DRAIN_WARPS * 32 * DRAIN_REGS + (THREADS - DRAIN_WARPS * 32) * OTHER_REGS <= THREADS * LAUNCH_REGS, "register split");
+    static constexpr int BN = CHUNKS == 4 ? 48 : 64;
+    static constexpr int TMEM_COLS = CHUNKS == 1 ? 128 : 256;
+    static constexpr int CTAS = 512 / TMEM_COLS;             // per SM
+    static constexpr int CODE_SLOTS = CHUNKS == 1 ? 2 : 4;   // stages of codes
+    static constexpr int SCALE_SLOTS = 2 * CODE_SLOTS;       // of scales, which are read after the codes' slot is filled anew
+    static constexpr int BOX = BN % 32 ? 16 : 32;            // rows of x that one copy brings
+    static constexpr int PIECE = BN % 32 ? 16 : 32;          // columns that one load of accumulators brings
+    static_assert(CHUNKS * BN + A_COLS <= TMEM_COLS, "tensor memory");
 };
-
-constexpr int HALF_K = 128, HALF_TILES = 2;      // channels, 64-channel tiles
-constexpr int STAGE_K = 256, STAGE_TILES = 4;
-constexpr int STAGES = 2;                        // widened operands in tensor memory
-constexpr int COLS = 128;                        // accumulator columns of a half
-constexpr int A_COLS = STAGE_K / 2;              // operand columns of a stage: two bf16 channels each
-constexpr int A_BASE = 2 * COLS;
-static_assert(A_BASE + STAGES * A_COLS <= 512, "tensor memory");
-constexpr int RING = 4;                          // codes: 16 KB a stage
-// Scales are needed until a stage is drained.  Their slots need no barrier to become free: who hands back
-// codes of stage n - RING has seen the MMAs of n - RING - STAGES complete, and those waited for the draining
-// of the stage before.
-constexpr int SCALE_RING = 8;
-static_assert(SCALE_RING >= RING + STAGES + 1, "scales");
-constexpr int X_RING = 8;                        // halves of x at most
-constexpr int X_BOX = 32;                        // rows of x that one copy brings
-constexpr int DONE = 8;                          // stages whose completion can be asked for
 
 template <int CHUNKS>
 struct Smem {
-    static constexpr int BN = COLS / CHUNKS;
-    uint8_t x[(CHUNKS == 4 ? 64 : 128) * 1024];  // halves of two tiles of bn rows, 128-byte swizzle, 1024-byte aligned
-    uint4 codes[RING][STAGE_TILES][I4_STRIP][32];
-    uint32_t zeros[RING][2 * CHUNKS][I4_STRIP][8];
-    uint2 scales[SCALE_RING][2 * CHUNKS][I4_STRIP][8];   // per chunk fp32 pairs; bf16 pairs fill the first half of a stage's
-    uint64_t code_full[RING], code_free[RING], scale_full[SCALE_RING];
-    uint64_t a_full[STAGES], x_full[X_RING], done[2][DONE], drained[2], last;
+    using Sh = Shape<CHUNKS>;
+    uint8_t x[X_SLOTS][TILES][Sh::BN * 128];     // 128-byte swizzle, 1024-byte aligned
+    uint4 codes[Sh::CODE_SLOTS][TILES][I4_STRIP][32];
+    uint32_t zeros[Sh::CODE_SLOTS][CHUNKS][I4_STRIP][8];
+    uint2 scales[Sh::SCALE_SLOTS][CHUNKS][I4_STRIP][8];      // fp32 pairs; bf16 pairs fill the first half of a stage's
+    uint64_t code_full[Sh::CODE_SLOTS], x_full[X_SLOTS], done;
     uint32_t tmem;
-    int abort;
     int table[1];                                // start[E + 1], first[E + 1]
 };
 
@@ -103,7 +88,7 @@ __device__ __forceinline__ void mma_ts2(uint32_t d, uint32_t a, uint32_t b_lo, u
         : "memory");
 }
 
-// True in one lane of a converged warp; the loops around it stay warp-uniform.
+// True in one lane of a converged warp.
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t p;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
@@ -126,37 +111,6 @@ __device__ __forceinline__ void tma_gather(uint32_t dst, const CUtensorMap* map,
         : "memory");
 }
 
-// Tries a wait up to 256 times, in the fewest instructions: what waiting warps issue the others lack.
-__device__ __forceinline__ bool try_wait_many(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
-        "AGAIN:\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
-        " @p bra OVER;\n add.u32 n, n, 1;\n setp.lt.u32 q, n, 256;\n @q bra AGAIN;\n"
-        "OVER:\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
-        : "memory");
-    return ok != 0;
-}
-
-// As mbar_wait_bounded.  PATIENT: by a warp that works ahead and can sleep between its looks.
-template <bool PATIENT>
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, uint32_t limit_us, uint32_t* status, volatile int* abort) {
-    if (PATIENT ? mbar_try_wait(bar, parity) : try_wait_many(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    while (true) {
-        if (PATIENT) __nanosleep(100);
-        if (PATIENT ? mbar_try_wait(bar, parity) : try_wait_many(bar, parity)) return true;
-        if (*abort) return false;
-        if (global_ns() - t0 > (uint64_t)limit_us * 1000ull) {
-            atomicOr(status, MOE_DEV_WAIT_TIMEOUT);
-            *abort = 1;
-            return false;
-        }
-    }
-}
-
 // (a0, a1) += (p0, p1) * (s, s): two fp32 fused multiply-adds in one instruction.
 __device__ __forceinline__ void fma_pair(uint64_t& a, uint32_t p0, uint32_t p1, uint64_t ss) {
     asm("{\n .reg .b64 t;\n mov.b64 t, {%1, %2};\n fma.rn.f32x2 %0, t, %3, %0;\n}" : "+l"(a) : "r"(p0), "r"(p1), "l"(ss));
@@ -168,361 +122,270 @@ __device__ __forceinline__ uint32_t idesc_for(int n) {
 }
 
 template <int CHUNKS, XMode MODE, bool ZEROS, bool GATED>
-__global__ void __launch_bounds__(Shape<MODE>::THREADS, 1) int4_many_kernel(const __grid_constant__ CUtensorMap x_map, const Int4Call c, int bn,
-                                                                               int x_slots) {
-    using S = Smem<CHUNKS>;
-    constexpr int NTHREADS = Shape<MODE>::THREADS, X_WARPS = Shape<MODE>::X_WARPS;
-    constexpr int BN = S::BN;                    // columns reserved per chunk; bn, at most that, rows per tile
-    constexpr int CHUNK_STEPS = 4 / CHUNKS;      // 32-channel steps of a chunk
+__global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel(const __grid_constant__ CUtensorMap x_map, const Int4Call c) {
+    using Sh = Shape<CHUNKS>;
+    constexpr int BN = Sh::BN, CODE_SLOTS = Sh::CODE_SLOTS, SCALE_SLOTS = Sh::SCALE_SLOTS, CHUNK_STEPS = STEPS / CHUNKS;
+    constexpr uint32_t TILE_BYTES = BN * 128, A_AT = CHUNKS * BN;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    auto& sm = *reinterpret_cast<Smem<CHUNKS>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     int* start = sm.table;
     int* first = sm.table + c.E + 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int feature_tiles = c.strips;
-    const int stages = (c.kt + STAGE_TILES - 1) / STAGE_TILES;      // per unit
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
+    const int stages = (c.kt + TILES - 1) / TILES;          // per unit
+    const int s_rec = (c.s_f32 ? 8 : 4) * I4_STRIP * 8, z_rec = 4 * I4_STRIP * 8;    // bytes of a strip's group
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) mbar_init(&sm.a_full[s], WIDEN_WARPS);
-        for (int s = 0; s < X_RING; ++s) mbar_init(&sm.x_full[s], X_WARPS);
-        for (int s = 0; s < DONE; ++s) {
-            mbar_init(&sm.done[0][s], 1);
-            mbar_init(&sm.done[1][s], 1);
-        }
-        for (int s = 0; s < RING; ++s) {
-            mbar_init(&sm.code_full[s], 1);
-            mbar_init(&sm.code_free[s], WIDEN_WARPS);
-        }
-        for (int s = 0; s < SCALE_RING; ++s) mbar_init(&sm.scale_full[s], 1);
-        for (int b = 0; b < 2; ++b) mbar_init(&sm.drained[b], DRAIN_WARPS);
-        mbar_init(&sm.last, 1);
+        for (int s = 0; s < CODE_SLOTS; ++s) mbar_init(&sm.code_full[s], 1);
+        for (int s = 0; s < X_SLOTS; ++s) mbar_init(&sm.x_full[s], 1);
+        mbar_init(&sm.done, 1);
         fence_mbar_init();
-        sm.abort = 0;
     }
-    if (warp == 0) tc::tmem_alloc(&sm.tmem, 512);
+    if (warp == 0) tc::tmem_alloc(&sm.tmem, Sh::TMEM_COLS);
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     if (c.offsets) pdl_wait();
-    i4::row_tiles<NTHREADS>(c, bn, start, first);
-    constexpr uint32_t tmem = 0;                 // where an allocation of all 512 columns starts
-    volatile int* abort = &sm.abort;
-    const int units = start[c.E] * feature_tiles;
-    auto unit_at = [&](int u) { return i4::unit_at(c, u, feature_tiles, bn, start, first); };
-    auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xFFFFFFFFu, wait_bounded<false>(bar, parity, c.wait_limit, c.status, abort));
+    i4::row_tiles<THREADS>(c, BN, start, first);
+    const uint32_t tmem = sm.tmem;
+    const int units = start[c.E] * c.strips;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, c.wait_limit, c.status, nullptr));
     };
-    auto patient_wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xFFFFFFFFu, wait_bounded<true>(bar, parity, c.wait_limit, c.status, abort));
-    };
-    // waits until the MMAs of half h of stage n are complete
-    auto done = [&](int h, uint32_t n) { return warp_wait(&sm.done[h][n % DONE], n / DONE & 1u); };
 
-    if (warp >= DRAIN_WARPS) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape<MODE>::OTHER_REGS));
-        if (warp < CODE_WARP) {
-            // ------------------------------------------------------------ codes into tensor memory
-            pdl_wait();                          // no bounded wait before it: limits count this kernel's time alone
-            const int w = warp - DRAIN_WARPS, g = lane >> 2;         // blocks 2 w and 2 w + 1
-            const uint32_t to = tmem + ((uint32_t)(w * 32) << 16) + A_BASE;
-            int at = 0;
-            uint32_t code_phase = 0, n = 0;
-            bool ok = true;
-            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-                for (int st = 0; st < stages; ++st, ++n) {
-                    ok = warp_wait(&sm.code_full[at], code_phase);
-                    if (!ok) break;
-                    ok = n < STAGES || done(1, n - STAGES);
-                    if (!ok) break;
-                    const int slot = n % STAGES;
-                    tc::tc_fence_after();
+    // ---- Copies.  Warp 0 requests codes, scales and zero points, warp 1 rows of x (MODE X_COPY: all warps bring them,
+    // stage by stage); both are ahead of the sums by as many stages as there are slots.
+    int p_unit = blockIdx.x, p_stage = 0;
+    uint32_t p_n = 0;
+    size_t p_strip = 0;
+    int p_row0 = 0, p_count = 0, p_row[4];
+    auto enter = [&]() {
+        const i4::Unit un = i4::unit_at(c, p_unit, c.strips, BN, start, first);
+        p_strip = (size_t)un.expert * c.strips + un.tile;
+        p_row0 = un.row0;
+        p_count = un.count;
+        if (MODE == X_GATHER && warp == 1) {     // lane i has rows 4 i to 4 i + 3; -1 reads as zeros
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int block = 2 * w + i;
-#pragma unroll
-                        for (int tile = 0; tile < STAGE_TILES; ++tile) {
-                            uint32_t r[16], v[4];
-                            if (STAGE_TILES * st + tile < c.kt) {
-                                const uint4 code = sm.codes[at][tile][block][lane];
-#pragma unroll
-                                for (int half = 0; half < 2; ++half) {
-                                    const uint32_t z = ZEROS ? sm.zeros[at][(tile * 2 + half) / CHUNK_STEPS][block][g] : I4_ZERO;
-                                    i4::widen(half ? code.y : code.x, ZEROS ? __byte_perm(z, 0, 0x1010) : z, v);
-                                    r[8 * half] = v[0], r[8 * half + 1] = v[1], r[8 * half + 4] = v[2], r[8 * half + 5] = v[3];
-                                    i4::widen(half ? code.w : code.z, ZEROS ? __byte_perm(z, 0, 0x3232) : z, v);
-                                    r[8 * half + 2] = v[0], r[8 * half + 3] = v[1], r[8 * half + 6] = v[2], r[8 * half + 7] = v[3];
-                                }
-                            } else {             // channels past the image
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) r[e] = 0u;
-                            }
-                            tmem_st_16x32(to + ((uint32_t)(i * 16) << 16) + slot * A_COLS + tile * (A_COLS / STAGE_TILES), r);
-                        }
-                    }
-                    tmem_wait_st();
-                    tc::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&sm.code_free[at]);
-                        mbar_arrive(&sm.a_full[slot]);
-                    }
-                    if (++at == RING) { at = 0; code_phase ^= 1u; }
-                }
-            }
-        } else if (warp == CODE_WARP) {
-            // ------------------------------------------------------------ codes, scales, zero points
-            const uint32_t el = elect_one();
-            const int s_rec = (c.s_f32 ? 8 : 4) * I4_STRIP * 8, z_rec = 4 * I4_STRIP * 8;    // bytes of a strip's group
-            uint32_t n = 0;
-            bool ok = true;
-            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-                const i4::Unit un = unit_at(u);
-                const size_t strip = (size_t)un.expert * c.strips + un.tile;
-                const char* w = reinterpret_cast<const char*>(c.w) + strip * c.kt * (I4_STRIP * 512);
-                const char* s = c.s + strip * c.groups * s_rec;
-                const char* z = reinterpret_cast<const char*>(c.z) + strip * c.groups * z_rec;
-                for (int st = 0; st < stages; ++st, ++n) {
-                    // the weights do not depend on the preceding kernel: the first of them are requested before the wait for it
-                    if (n == RING) pdl_wait();
-                    const uint32_t slot = n % RING, s_slot = n % SCALE_RING;
-                    ok = n < RING || patient_wait(&sm.code_free[slot], (n / RING & 1u) ^ 1u);
-                    if (!ok) break;
-                    const int tiles = min(STAGE_TILES, c.kt - st * STAGE_TILES), bytes = tiles * (I4_STRIP * 512);
-                    // a record for every chunk, whatever the groups: neighbours where groups are as long as chunks
-                    const int step = st * (2 * STAGE_TILES), chunks = (2 * tiles + CHUNK_STEPS - 1) / CHUNK_STEPS;
-                    const int pieces = c.groups_are_chunks ? 1 : chunks, records = c.groups_are_chunks ? chunks : 1;
-                    if (el) {
-                        mbar_arrive_expect_tx(&sm.code_full[slot], bytes + (ZEROS ? chunks * z_rec : 0));
-                        bulk_g2s(sm.codes[slot], w + (size_t)st * (STAGE_TILES * I4_STRIP * 512), bytes, &sm.code_full[slot]);
-                        mbar_arrive_expect_tx(&sm.scale_full[s_slot], chunks * s_rec);
+            for (int i = 0; i < 4; ++i) p_row[i] = lane * 4 + i < un.count ? i4::source_row(c, un.row0 + lane * 4 + i) : -1;
+        }
+    };
+    auto advance = [&]() {
+        ++p_n;
+        if (++p_stage == stages) {
+            p_stage = 0;
+            p_unit += gridDim.x;
+            if (p_unit < units) enter();
+        }
+    };
+    auto copy_codes = [&]() {
+        if (p_unit >= units) return;
+        if (elect_one()) {
+            const uint32_t slot = p_n % CODE_SLOTS;
+            const int tiles = min(TILES, c.kt - p_stage * TILES), step = p_stage * STEPS;
+            // a record for every chunk, whatever the groups: neighbours where groups are as long as chunks
+            const int chunks = (2 * tiles + CHUNK_STEPS - 1) / CHUNK_STEPS;
+            const int pieces = CHUNKS == 1 || c.groups_are_chunks ? 1 : chunks, records = pieces == 1 ? chunks : 1;
+            uint64_t* bar = &sm.code_full[slot];
+            mbar_arrive_expect_tx(bar, tiles * (I4_STRIP * 512) + chunks * (s_rec + (ZEROS ? z_rec : 0)));
+            bulk_g2s(sm.codes[slot], reinterpret_cast<const char*>(c.w) + (p_strip * c.kt + p_stage * TILES) * (I4_STRIP * 512),
+                     tiles * (I4_STRIP * 512), bar);
 #pragma unroll 1
-                        for (int j = 0; j < pieces; ++j) {
-                            const size_t from = i4::group_of(c, step + j * CHUNK_STEPS);
-                            if (ZEROS)
-                                bulk_g2s(reinterpret_cast<char*>(sm.zeros[slot]) + j * z_rec, z + from * z_rec, records * z_rec, &sm.code_full[slot]);
-                            bulk_g2s(reinterpret_cast<char*>(sm.scales[s_slot]) + j * s_rec, s + from * s_rec, records * s_rec, &sm.scale_full[s_slot]);
-                        }
-                    }
-                    __syncwarp();
-                }
+            for (int j = 0; j < pieces; ++j) {
+                const size_t from = p_strip * c.groups + i4::group_of(c, step + j * CHUNK_STEPS);
+                if (ZEROS)
+                    bulk_g2s(reinterpret_cast<char*>(sm.zeros[slot]) + j * z_rec, reinterpret_cast<const char*>(c.z) + from * z_rec, records * z_rec, bar);
+                bulk_g2s(reinterpret_cast<char*>(sm.scales[p_n % SCALE_SLOTS]) + j * s_rec, c.s + from * s_rec, records * s_rec, bar);
             }
-            // every issued copy lands before the CTA exits
-            for (uint32_t i = n - min(n, (uint32_t)SCALE_RING); i < n; ++i) {
-                if (i + RING >= n) mbar_wait_bounded(&sm.code_full[i % RING], i / RING & 1u, LANDING_LIMIT_US, c.status, nullptr);
-                mbar_wait_bounded(&sm.scale_full[i % SCALE_RING], i / SCALE_RING & 1u, LANDING_LIMIT_US, c.status, nullptr);
-            }
-        } else if (warp == MMA_WARP) {
-            // ------------------------------------------------------------ MMA issuer
-            pdl_wait();
-            const uint32_t el = elect_one();
-            const uint32_t b0 = (uint32_t)tc::sw128_desc(smem_addr(sm.x));
-            const uint32_t tile_step = (uint32_t)(bn * 128) >> 4;
-            uint32_t n = 0, xs = 0, x_phase = 0;
-            bool ok = true, any = false;
-            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-                const i4::Unit un = unit_at(u);
-                const uint32_t idesc = idesc_for((un.count + 15) / 16 * 16);
-                for (int st = 0; st < stages && ok; ++st, ++n) {
-                    const uint32_t slot = n % STAGES;
-                    ok = warp_wait(&sm.a_full[slot], n / STAGES & 1u);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        ok = ok && warp_wait(&sm.x_full[xs], x_phase) && warp_wait(&sm.drained[h], (n & 1u) ^ 1u);
-                        if (!ok) break;
-                        tc::tc_fence_after();
-                        const uint32_t a = tmem + A_BASE + slot * A_COLS + h * (A_COLS / 2), d = tmem + h * COLS;
-                        const uint32_t b = b0 + xs * (HALF_TILES * tile_step);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_ts2(d + i / CHUNK_STEPS * BN, a + i * 16, b + (i >> 1) * tile_step + (i & 1) * 4, idesc, el, i % CHUNK_STEPS != 0);
-                        if (el) tc::mma_commit(&sm.done[h][n % DONE]);
-                        __syncwarp();
-                        any = true;
-                        if (++xs == x_slots) { xs = 0; x_phase ^= 1u; }
-                    }
-                }
-            }
-            // every issued MMA must complete before the tensor memory is released
-            if (any) {
-                if (el) tc::mma_commit(&sm.last);
-                __syncwarp();
-                mbar_wait_bounded(&sm.last, 0u, LANDING_LIMIT_US, c.status, nullptr);
-            }
-        } else if (warp < X_WARP + X_WARPS) {
-            // ------------------------------------------------------------ rows of x into shared memory
-            pdl_wait();
-            const int xw = warp - X_WARP;
-            const uint32_t tile_bytes = bn * 128;
-            uint32_t n = 0, xs = 0;              // halves
-            bool ok = true;
-            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-                const i4::Unit un = unit_at(u);
-                int row[4];
-                if (MODE == X_GATHER) {          // lane i has rows 4 i to 4 i + 3; -1 reads as zeros
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) row[i] = lane * 4 + i < un.count ? i4::source_row(c, un.row0 + lane * 4 + i) : -1;
-                }
-                for (int st = 0; st < 2 * stages; ++st, ++n) {
-                    const uint32_t before = n - x_slots;
-                    ok = n < x_slots || patient_wait(&sm.done[before & 1][before / 2 % DONE], before / 2 / DONE & 1u);
-                    if (!ok) break;
-                    uint8_t* const slot = sm.x + xs * (HALF_TILES * tile_bytes);
-                    const uint32_t bar = smem_addr(&sm.x_full[xs]), to = smem_addr(slot);
-                    if (MODE == X_TILE) {
-                        const int boxes = (un.count + X_BOX - 1) / X_BOX;
-                        if (lane == 0) mbar_arrive_expect_tx(&sm.x_full[xs], boxes * (HALF_TILES * X_BOX * 128));
-                        __syncwarp();
-                        const int box = lane / HALF_TILES, tile = lane % HALF_TILES;
-                        if (box < boxes)
-                            tma_rows(to + tile * tile_bytes + box * (X_BOX * 128), &x_map, st * HALF_K + tile * I4_K, un.row0 + box * X_BOX, bar);
-                    } else if (MODE == X_GATHER) {
-                        const int fours = (un.count + 3) / 4;
-                        if (lane == 0) mbar_arrive_expect_tx(&sm.x_full[xs], fours * (HALF_TILES * 512));
-                        __syncwarp();
-                        if (lane < fours) {
-#pragma unroll
-                            for (int tile = 0; tile < HALF_TILES; ++tile)
-                                tma_gather(to + tile * tile_bytes + lane * 512, &x_map, st * HALF_K + tile * I4_K, row, bar);
-                        }
-                    } else {
-                        // a warp's lanes take 8 rows by 4 of the 16 pieces of 8 channels
-                        constexpr int BATCH = 4;
-                        const int r8 = lane >> 2;
-#pragma unroll 1
-                        for (int r0 = xw * 8; r0 < un.count; r0 += X_WARPS * 8) {
-                            const int r = r0 + r8;
-                            const int from = r < un.count ? i4::source_row(c, un.row0 + r) : -1;
-                            const uint16_t* p = c.x + (from < 0 ? 0 : from) * c.ldx + st * HALF_K;
-                            uint4 v[BATCH];
-#pragma unroll
-                            for (int i = 0; i < BATCH; ++i) {
-                                const int k = ((lane & 3) + 4 * i) * 8;
-                                v[i] = i4::load8(p + k, from < 0 ? 0 : min(c.K - st * HALF_K - k, 8));
-                            }
-                            if (r < un.count) {
-#pragma unroll
-                                for (int i = 0; i < BATCH; ++i) {
-                                    const int piece = (lane & 3) + 4 * i;
-                                    *reinterpret_cast<uint4*>(slot + (piece >> 3) * tile_bytes + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) = v[i];
-                                }
-                            }
-                        }
-                        fence_async_proxy();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm.x_full[xs]);
-                    }
-                    if (++xs == x_slots) xs = 0;
-                }
-            }
-            // every issued copy lands before the CTA exits
-            if (MODE != X_COPY)
-                for (uint32_t i = n - min(n, (uint32_t)x_slots); i < n; ++i)
-                    mbar_wait_bounded(&sm.x_full[i % x_slots], i / x_slots & 1u, LANDING_LIMIT_US, c.status, nullptr);
         }
         __syncwarp();
-    } else {
-        // ---------------------------------------------------------------- drain, scale, add up
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Shape<MODE>::DRAIN_REGS));
-        constexpr int PIECES = BN / 32;                      // of 32 columns, per chunk; four per half
-        const uint32_t from = tmem + ((uint32_t)(warp * 32) << 16);
-        const int row = warp * 32 + lane, block = row >> 4, g = row & 7, upper = (row >> 3) & 1;
-        // where the row's scale lies in a record, in words, and which of its bytes make it an fp32
-        const int s_at = (block * 8 + g) * (c.s_f32 ? 2 : 1) + (c.s_f32 ? upper : 0), s_step = I4_STRIP * 8 * (c.s_f32 ? 2 : 1);
-        const uint32_t s_bytes = c.s_f32 ? 0x3210u : upper ? 0x3244u : 0x1044u;
-        pdl_wait();
-        uint32_t n = 0;
-        bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            const i4::Unit un = unit_at(u);
-            uint64_t acc[PIECES][16];
+        advance();
+    };
+    auto copy_x = [&]() {
+        if (p_unit >= units) return;
+        const uint32_t slot = p_n % X_SLOTS, bar = smem_addr(&sm.x_full[slot]), to = smem_addr(sm.x[slot][0]);
+        const int copies = MODE == X_TILE ? (p_count + Sh::BOX - 1) / Sh::BOX : (p_count + 3) / 4;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.x_full[slot], copies * TILES * (MODE == X_TILE ? Sh::BOX : 4) * 128);
+        __syncwarp();
+        if (MODE == X_TILE) {
+            const int box = lane / TILES, tile = lane % TILES;
+            if (box < copies)
+                tma_rows(to + tile * TILE_BYTES + box * (Sh::BOX * 128), &x_map, p_stage * STAGE_K + tile * I4_K, p_row0 + box * Sh::BOX, bar);
+        } else if (lane < copies) {
 #pragma unroll
-            for (int p = 0; p < PIECES; ++p)
+            for (int tile = 0; tile < TILES; ++tile)
+                tma_gather(to + tile * TILE_BYTES + lane * 512, &x_map, p_stage * STAGE_K + tile * I4_K, p_row, bar);
+        }
+        advance();
+    };
+    // rows of x off the 16-byte grid: 8 rows by 4 of the 16 pieces of 8 channels a warp each time
+    auto copy_x_by_hand = [&](const i4::Unit& un, int st, uint8_t* slot) {
+#pragma unroll 1
+        for (int r = warp * 8 + g; r < un.count; r += THREADS / 4) {
+            const int from = i4::source_row(c, un.row0 + r);
+            const uint16_t* p = c.x + (from < 0 ? 0 : from) * c.ldx + st * STAGE_K;
+            uint4 v[4];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[p][i] = 0;
-            for (int st = 0; st < stages && ok; ++st, ++n) {
-                const uint32_t at = n % SCALE_RING;
-                ok = warp_wait(&sm.scale_full[at], n / SCALE_RING & 1u);
-                const uint32_t* s = reinterpret_cast<const uint32_t*>(sm.scales[at]) + s_at;
+            for (int i = 0; i < 4; ++i) {
+                const int k = ((lane & 3) + 4 * i) * 8;
+                v[i] = i4::load8(p + k, from < 0 ? 0 : min(c.K - st * STAGE_K - k, 8));
+            }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint64_t sc[CHUNKS];
+            for (int i = 0; i < 4; ++i) {
+                const int piece = (lane & 3) + 4 * i;
+                *reinterpret_cast<uint4*>(slot + (piece >> 3) * TILE_BYTES + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) = v[i];
+            }
+        }
+        fence_async_proxy();
+        __syncwarp();
+    };
+    const bool copies_codes = warp == 0, copies_x = MODE != X_COPY && warp == 1;
+    if (p_unit < units) enter();
+    // The weights do not depend on the preceding kernel: the first of them are requested before the wait for it.
+    if (copies_codes)
+#pragma unroll 1
+        for (int i = 0; i < CODE_SLOTS; ++i) copy_codes();
+    if (!c.offsets) pdl_wait();
+    if (copies_x)
+#pragma unroll 1
+        for (int i = 0; i < X_SLOTS; ++i) copy_x();
+
+    // ---- Sums.
+    const int row = warp * 32 + lane, row_block = row >> 4, row_g = row & 7, upper = (row >> 3) & 1;
+    // where the row's scale lies in a record, in words, and which of its bytes make it an fp32
+    const int s_at = (row_block * 8 + row_g) * (c.s_f32 ? 2 : 1) + (c.s_f32 ? upper : 0), s_step = I4_STRIP * 8 * (c.s_f32 ? 2 : 1);
+    const uint32_t s_bytes = c.s_f32 ? 0x3210u : upper ? 0x3244u : 0x1044u;
+    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    uint32_t n = 0;
+    bool ok = true, pending = false;             // pending: MMAs that nobody has seen complete
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        const i4::Unit un = i4::unit_at(c, u, c.strips, BN, start, first);
+        const uint32_t idesc = idesc_for((un.count + 15) / 16 * 16);
+        uint64_t acc[BN / 2];
 #pragma unroll
-                    for (int j = 0; j < CHUNKS; ++j) {
-                        uint32_t v = __byte_perm(s[(h * CHUNKS + j) * s_step], 0, s_bytes);
-                        // chunks of the last stage may lie past the matrix
-                        if (st * (2 * STAGE_TILES) + (h * CHUNKS + j) * CHUNK_STEPS >= 2 * c.kt) v = 0;
-                        sc[j] = (uint64_t)v << 32 | v;
+        for (int i = 0; i < BN / 2; ++i) acc[i] = 0;
+        for (int st = 0; st < stages; ++st, ++n) {
+            const uint32_t slot = n % CODE_SLOTS;
+            if (MODE == X_COPY) copy_x_by_hand(un, st, sm.x[n % X_SLOTS][0]);
+            ok = ok && wait(&sm.code_full[slot], n / CODE_SLOTS & 1u);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {        // the warp's blocks: 16 lanes of tensor memory each
+                const int block = 2 * warp + i;
+#pragma unroll
+                for (int tile = 0; tile < TILES; ++tile) {
+                    uint32_t r[16], v[4];
+                    const uint4 code = sm.codes[slot][tile][block][lane];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t z = ZEROS ? sm.zeros[slot][(tile * 2 + half) / CHUNK_STEPS][block][g] : I4_ZERO;
+                        i4::widen(half ? code.y : code.x, ZEROS ? __byte_perm(z, 0, 0x1010) : z, v);
+                        r[8 * half] = v[0], r[8 * half + 1] = v[1], r[8 * half + 4] = v[2], r[8 * half + 5] = v[3];
+                        i4::widen(half ? code.w : code.z, ZEROS ? __byte_perm(z, 0, 0x3232) : z, v);
+                        r[8 * half + 2] = v[0], r[8 * half + 3] = v[1], r[8 * half + 6] = v[2], r[8 * half + 7] = v[3];
                     }
-                    ok = ok && done(h, n);       // tcgen05.ld below is warp-collective
-                    if (!ok) break;
-                    tc::tc_fence_after();
+                    // channels past the image: the slot holds what was there before, which the zeros of x must not meet
+                    if (st * TILES + tile >= c.kt) {
 #pragma unroll
-                    for (int b = 0; b < 4; b += 2) {
-                        uint32_t part[2][32];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int j = (b + i) / PIECES, p = (b + i) % PIECES;
-                            if (p * 32 < un.count) tc::tmem_ld32u(from + h * COLS + j * BN + p * 32, part[i]);
-                        }
-                        tc::tmem_wait_ld();
-                        if (b == 2) {
-                            tc::tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&sm.drained[h]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int j = (b + i) / PIECES, p = (b + i) % PIECES;
-                            if (p * 32 < un.count) {
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) fma_pair(acc[p][e], part[i][2 * e], part[i][2 * e + 1], sc[j]);
-                            }
-                        }
+                        for (int e = 0; e < 16; ++e) r[e] = 0u;
                     }
+                    tmem_st_16x32(lanes + ((uint32_t)(i * 16) << 16) + A_AT + tile * (A_COLS / TILES), r);
                 }
             }
+            tmem_wait_st();
+            tc::tc_fence_before();
+            // all of the operand is there, and everybody has read the accumulators; a wait that gave up ends it for all
+            ok = !__syncthreads_or(!ok);
             if (!ok) break;
-            const int n0 = GATED ? (un.tile * I4_STRIP + block) * 8 + g : un.tile * 128 + row;
-            const bool mine = n0 < c.N && !(GATED && upper);
-            auto store = [&](auto* y) {
+            tc::tc_fence_after();
+            if (warp == 2) {
+                ok = MODE == X_COPY || wait(&sm.x_full[n % X_SLOTS], n / X_SLOTS & 1u);
+                if (ok) {
+                    const uint32_t el = elect_one(), b = (uint32_t)tc::sw128_desc(smem_addr(sm.x[n % X_SLOTS][0]));
 #pragma unroll
-                for (int p = 0; p < PIECES; ++p) {
-                    const int m0 = p * 32;
-                    if (m0 >= un.count) break;
-                    auto* at = y + (un.row0 + m0) * c.ldy + n0;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i, at += c.ldy) {
-                        float v = __uint_as_float((uint32_t)(acc[p][i / 2] >> (32 * (i & 1))));
-                        if (GATED) v = i4::gate(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
-                        if (mine && m0 + i < un.count) i4::put_y(at, v);
-                    }
+                    for (int i = 0; i < STEPS; ++i)
+                        mma_ts2(tmem + i / CHUNK_STEPS * BN, tmem + A_AT + i * 16, b + (i >> 1) * (TILE_BYTES >> 4) + (i & 1) * 4, idesc, el,
+                                i % CHUNK_STEPS != 0);
+                    if (el) tc::mma_commit(&sm.done);
+                    __syncwarp();
+                    pending = true;
                 }
-            };
-            if (c.y_f32) store(static_cast<float*>(c.y));
-            else store(static_cast<__nv_bfloat16*>(c.y));
+            }
+            if (copies_codes) copy_codes();
+            uint64_t sc[CHUNKS];
+#pragma unroll
+            for (int j = 0; j < CHUNKS; ++j) {
+                uint32_t v = __byte_perm(reinterpret_cast<const uint32_t*>(sm.scales[n % SCALE_SLOTS])[s_at + j * s_step], 0, s_bytes);
+                // chunks of the last stage may lie past the matrix
+                if (CHUNKS > 1 && st * STEPS + j * CHUNK_STEPS >= 2 * c.kt) v = 0;
+                sc[j] = (uint64_t)v << 32 | v;
+            }
+            ok = ok && wait(&sm.done, n & 1u);
+            if (ok) pending = false;
+            tc::tc_fence_after();
+            if (copies_x && ok) copy_x();
+#pragma unroll
+            for (int i = 0; i < CHUNKS * BN / Sh::PIECE; ++i) {
+                const int j = i * Sh::PIECE / BN, col = i * Sh::PIECE % BN;
+                if (ok && col < un.count) {
+                    uint32_t part[Sh::PIECE];
+                    if constexpr (Sh::PIECE == 32) tc::tmem_ld32u(lanes + j * BN + col, part);
+                    else tc::tmem_ld16u(lanes + j * BN + col, part);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < Sh::PIECE / 2; ++e) fma_pair(acc[col / 2 + e], part[2 * e], part[2 * e + 1], sc[j]);
+                }
+            }
         }
+        ok = !__syncthreads_or(!ok);
+        if (!ok) break;
+        const int n0 = GATED ? (un.tile * I4_STRIP + row_block) * 8 + row_g : un.tile * 128 + row;
+        auto store = [&](auto* y) {
+            auto* at = y + (un.row0 + (GATED ? upper : 0)) * c.ldy + n0;
+#pragma unroll
+            for (int m = 0; m < BN; m += 2) {
+                if (m % 16 == 0 && m >= un.count) break;
+                const float even = __uint_as_float((uint32_t)acc[m / 2]), odd = __uint_as_float((uint32_t)(acc[m / 2] >> 32));
+                if (GATED) {
+                    // lanes of a gate row take the even rows of x, those of its up row, 8 lanes on, the odd ones
+                    const float got = __shfl_xor_sync(0xFFFFFFFFu, upper ? even : odd, 8);
+                    const float h = i4::gate(upper ? got : even, upper ? odd : got);
+                    if (n0 < c.N && m + upper < un.count) i4::put_y(at, h);
+                } else {
+                    if (n0 < c.N && m < un.count) i4::put_y(at, even);
+                    if (n0 < c.N && m + 1 < un.count) i4::put_y(at + c.ldy, odd);
+                }
+                at += 2 * c.ldy;
+            }
+        };
+        if (c.y_f32) store(static_cast<float*>(c.y));
+        else store(static_cast<__nv_bfloat16*>(c.y));
+    }
+    // After an expired wait, MMAs and copies in flight get their time before the CTA leaves.
+    if (!ok) {
+        if (pending) mbar_wait_bounded(&sm.done, n & 1u, LANDING_LIMIT_US, c.status, nullptr);
+        if (copies_codes)
+            for (uint32_t i = p_n - min(p_n, (uint32_t)CODE_SLOTS); i < p_n; ++i)
+                mbar_wait_bounded(&sm.code_full[i % CODE_SLOTS], i / CODE_SLOTS & 1u, LANDING_LIMIT_US, c.status, nullptr);
+        if (copies_x)
+            for (uint32_t i = p_n - min(p_n, (uint32_t)X_SLOTS); i < p_n; ++i)
+                mbar_wait_bounded(&sm.x_full[i % X_SLOTS], i / X_SLOTS & 1u, LANDING_LIMIT_US, c.status, nullptr);
     }
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+    if (warp == 0) tc::tmem_dealloc(tmem, Sh::TMEM_COLS);
 }
 
 template <int CHUNKS, XMode MODE, bool ZEROS, bool GATED>
 cudaError_t launch(const moe_int4* L, const Int4Call& c, const CUtensorMap& map, cudaStream_t s) {
+    using Sh = Shape<CHUNKS>;
+    constexpr auto kernel = int4_many_kernel<CHUNKS, MODE, ZEROS, GATED>;
     constexpr int fixed = sizeof(Smem<CHUNKS>) + 1024;
     constexpr int most = fixed + 2 * (MOE_DISPATCH_MAX_EXPERTS + 1) * (int)sizeof(int);
-    static_assert(most <= 227 * 1024 - 1024, "shared memory");
-    cudaError_t e = ensure_smem_limit<int4_many_kernel<CHUNKS, MODE, ZEROS, GATED>>(most);
+    cudaError_t e = ensure_smem_limit<kernel>(most);
     if (e != cudaSuccess) return e;
     const int64_t tiles = c.strips;
-    // rows per tile, and as many halves of x as fit
-    const int bn = Smem<CHUNKS>::BN;
-    const int x_slots = std::min(X_RING, (int)sizeof(Smem<CHUNKS>::x) / (bn * 128 * HALF_TILES));
-    const int64_t row_tiles = c.offsets ? std::min<int64_t>(c.rows, c.rows / bn + c.E) : ((int64_t)c.rows + bn - 1) / bn;
-    const int64_t grid = std::min<int64_t>(tiles * row_tiles, L->num_sms);
-    return launch_pdl(int4_many_kernel<CHUNKS, MODE, ZEROS, GATED>, dim3((unsigned)grid), dim3(Shape<MODE>::THREADS),
-                      fixed + 2 * (c.E + 1) * (int)sizeof(int), s, map, c, bn, x_slots);
+    const int64_t row_tiles = c.offsets ? std::min<int64_t>(c.rows, c.rows / Sh::BN + c.E) : ((int64_t)c.rows + Sh::BN - 1) / Sh::BN;
+    const int64_t grid = std::min<int64_t>(tiles * row_tiles, (int64_t)L->num_sms * Sh::CTAS);
+    return launch_pdl(kernel, dim3((unsigned)grid), dim3(THREADS), fixed + 2 * (c.E + 1) * (int)sizeof(int), s, map, c);
 }
 
 template <int CHUNKS, XMode MODE>
@@ -538,7 +401,7 @@ cudaError_t launch_mode(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
     const EncodeTiledFn encode = tensor_map_encoder();
     if (!encode) return cudaErrorNotSupported;
     const cuuint64_t dims[2] = {(cuuint64_t)c.K, (cuuint64_t)c.x_rows}, strides[1] = {(cuuint64_t)c.ldx * 2};
-    const cuuint32_t box[2] = {I4_K, c.token ? 1u : (cuuint32_t)X_BOX}, step[2] = {1, 1};
+    const cuuint32_t box[2] = {I4_K, c.token ? 1u : (cuuint32_t)Shape<CHUNKS>::BOX}, step[2] = {1, 1};
     if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(c.x), dims, strides, box, step,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
