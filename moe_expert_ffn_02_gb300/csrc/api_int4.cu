@@ -52,7 +52,7 @@ MOE_EXPORT moe_status moe_int4_create(const moe_int4_desc* d, const moe_int4_wei
     moe_int4* L = new (std::nothrow) moe_int4{};
     if (!L) return fail(MOE_ERR_CUDA, "out of host memory");
     L->d = *d;
-    L->kt = (d->in_features + moe::I4_K - 1) / moe::I4_K;
+    L->kt = (d->in_features + 2 * moe::I4_K - 1) / (2 * moe::I4_K) * 2;
     L->d.group = std::min(d->group, L->kt * moe::I4_K);         // one scale per row
     L->groups = (L->kt * moe::I4_K + L->d.group - 1) / L->d.group;
     const int per = d->gated ? 8 : moe::I4_ROWS;

@@ -27,7 +27,7 @@ struct moe_int4 {
     int num_sms;
     int blocks;            // per expert that hold rows, up to a multiple of 4
     int strips;            // per expert
-    int kt;                // tiles per block: ceil(in / 64)
+    int kt;                // tiles per block: ceil(in / 128) * 2
     int groups;            // per row, over the tiles' 64 kt channels
     uint4* w;              // [expert][strip][kt][8][32]
     void* s;               // [expert][strip][groups][8][8] pairs of bf16 or fp32

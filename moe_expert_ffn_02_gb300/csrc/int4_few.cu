@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int feature_tiles = c.blocks / RB;
     // this warp's tiles of 64 channels
-    const int per = (c.kt + WARPS - 1) / WARPS, t0 = min(c.kt, warp * per), steps = min(c.kt, t0 + per) - t0;
+    const int kt = (c.K + I4_K - 1) / I4_K, per = (kt + WARPS - 1) / WARPS, t0 = min(kt, warp * per), steps = min(kt, t0 + per) - t0;
     pdl_trigger();
     if (c.offsets) pdl_wait();
     i4::row_tiles<THREADS>(c, NB * 8, start, first);

@@ -122,7 +122,7 @@ __device__ __forceinline__ uint32_t idesc_for(int n) {
 }
 
 template <int CHUNKS, XMode MODE, bool ZEROS, bool GATED>
-__global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel(const __grid_constant__ CUtensorMap x_map, const Int4Call c) {
+__global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel(const __grid_constant__ CUtensorMap x_map, const Int4Call c, int bn) {
     using Sh = Shape<CHUNKS>;
     constexpr int BN = Sh::BN, CODE_SLOTS = Sh::CODE_SLOTS, SCALE_SLOTS = Sh::SCALE_SLOTS, CHUNK_STEPS = STEPS / CHUNKS;
     constexpr uint32_t TILE_BYTES = BN * 128, A_AT = CHUNKS * BN;
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
     int* start = sm.table;
     int* first = sm.table + c.E + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
-    const int stages = (c.kt + TILES - 1) / TILES;          // per unit
+    const int stages = c.kt / TILES;             // per unit
     const int s_rec = (c.s_f32 ? 8 : 4) * I4_STRIP * 8, z_rec = 4 * I4_STRIP * 8;    // bytes of a strip's group
 
     if (threadIdx.x == 0) {
@@ -145,21 +145,21 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
     __syncthreads();
     tc::tc_fence_after();
     if (c.offsets) pdl_wait();
-    i4::row_tiles<THREADS>(c, BN, start, first);
+    i4::row_tiles<THREADS>(c, bn, start, first);
     const uint32_t tmem = sm.tmem;
     const int units = start[c.E] * c.strips;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, c.wait_limit, c.status, nullptr));
     };
 
-    // ---- Copies.  Warp 0 requests codes, scales and zero points, warp 1 rows of x (MODE X_COPY: all warps bring them,
+    // ---- Copies.  Warp 3 requests codes, scales and zero points, warp 1 rows of x (MODE X_COPY: all warps bring them,
     // stage by stage); both are ahead of the sums by as many stages as there are slots.
     int p_unit = blockIdx.x, p_stage = 0;
     uint32_t p_n = 0;
     size_t p_strip = 0;
     int p_row0 = 0, p_count = 0, p_row[4];
     auto enter = [&]() {
-        const i4::Unit un = i4::unit_at(c, p_unit, c.strips, BN, start, first);
+        const i4::Unit un = i4::unit_at(c, p_unit, c.strips, bn, start, first);
         p_strip = (size_t)un.expert * c.strips + un.tile;
         p_row0 = un.row0;
         p_count = un.count;
@@ -180,14 +180,12 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
         if (p_unit >= units) return;
         if (elect_one()) {
             const uint32_t slot = p_n % CODE_SLOTS;
-            const int tiles = min(TILES, c.kt - p_stage * TILES), step = p_stage * STEPS;
             // a record for every chunk, whatever the groups: neighbours where groups are as long as chunks
-            const int chunks = (2 * tiles + CHUNK_STEPS - 1) / CHUNK_STEPS;
-            const int pieces = CHUNKS == 1 || c.groups_are_chunks ? 1 : chunks, records = pieces == 1 ? chunks : 1;
+            const int pieces = CHUNKS == 1 || c.groups_are_chunks ? 1 : CHUNKS, records = CHUNKS / pieces, step = p_stage * STEPS;
             uint64_t* bar = &sm.code_full[slot];
-            mbar_arrive_expect_tx(bar, tiles * (I4_STRIP * 512) + chunks * (s_rec + (ZEROS ? z_rec : 0)));
+            mbar_arrive_expect_tx(bar, TILES * (I4_STRIP * 512) + CHUNKS * (s_rec + (ZEROS ? z_rec : 0)));
             bulk_g2s(sm.codes[slot], reinterpret_cast<const char*>(c.w) + (p_strip * c.kt + p_stage * TILES) * (I4_STRIP * 512),
-                     tiles * (I4_STRIP * 512), bar);
+                     TILES * (I4_STRIP * 512), bar);
 #pragma unroll 1
             for (int j = 0; j < pieces; ++j) {
                 const size_t from = p_strip * c.groups + i4::group_of(c, step + j * CHUNK_STEPS);
@@ -237,7 +235,7 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
         fence_async_proxy();
         __syncwarp();
     };
-    const bool copies_codes = warp == 0, copies_x = MODE != X_COPY && warp == 1;
+    const bool copies_codes = warp == 3, copies_x = MODE != X_COPY && warp == 1;
     if (p_unit < units) enter();
     // The weights do not depend on the preceding kernel: the first of them are requested before the wait for it.
     if (copies_codes)
@@ -256,15 +254,18 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
     const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
     uint32_t n = 0;
     bool ok = true, pending = false;             // pending: MMAs that nobody has seen complete
+    i4::Unit un = {};
+    if (blockIdx.x < units) un = i4::unit_at(c, blockIdx.x, c.strips, bn, start, first);
+    if (MODE == X_COPY && blockIdx.x < units) copy_x_by_hand(un, 0, sm.x[0][0]);
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
-        const i4::Unit un = i4::unit_at(c, u, c.strips, BN, start, first);
+        i4::Unit next = un;
+        if (u + (int)gridDim.x < units) next = i4::unit_at(c, u + gridDim.x, c.strips, bn, start, first);
         const uint32_t idesc = idesc_for((un.count + 15) / 16 * 16);
         uint64_t acc[BN / 2];
 #pragma unroll
         for (int i = 0; i < BN / 2; ++i) acc[i] = 0;
         for (int st = 0; st < stages; ++st, ++n) {
             const uint32_t slot = n % CODE_SLOTS;
-            if (MODE == X_COPY) copy_x_by_hand(un, st, sm.x[n % X_SLOTS][0]);
             ok = ok && wait(&sm.code_full[slot], n / CODE_SLOTS & 1u);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {        // the warp's blocks: 16 lanes of tensor memory each
@@ -280,11 +281,6 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
                         r[8 * half] = v[0], r[8 * half + 1] = v[1], r[8 * half + 4] = v[2], r[8 * half + 5] = v[3];
                         i4::widen(half ? code.w : code.z, ZEROS ? __byte_perm(z, 0, 0x3232) : z, v);
                         r[8 * half + 2] = v[0], r[8 * half + 3] = v[1], r[8 * half + 6] = v[2], r[8 * half + 7] = v[3];
-                    }
-                    // channels past the image: the slot holds what was there before, which the zeros of x must not meet
-                    if (st * TILES + tile >= c.kt) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) r[e] = 0u;
                     }
                     tmem_st_16x32(lanes + ((uint32_t)(i * 16) << 16) + A_AT + tile * (A_COLS / TILES), r);
                 }
@@ -309,12 +305,13 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
                 }
             }
             if (copies_codes) copy_codes();
+            // by hand the next stage's x, while the MMAs of this one run
+            if (MODE == X_COPY && (st + 1 < stages || u + (int)gridDim.x < units))
+                copy_x_by_hand(st + 1 < stages ? un : next, st + 1 < stages ? st + 1 : 0, sm.x[(n + 1) % X_SLOTS][0]);
             uint64_t sc[CHUNKS];
 #pragma unroll
             for (int j = 0; j < CHUNKS; ++j) {
                 uint32_t v = __byte_perm(reinterpret_cast<const uint32_t*>(sm.scales[n % SCALE_SLOTS])[s_at + j * s_step], 0, s_bytes);
-                // chunks of the last stage may lie past the matrix
-                if (CHUNKS > 1 && st * STEPS + j * CHUNK_STEPS >= 2 * c.kt) v = 0;
                 sc[j] = (uint64_t)v << 32 | v;
             }
             ok = ok && wait(&sm.done, n & 1u);
@@ -357,6 +354,7 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
         };
         if (c.y_f32) store(static_cast<float*>(c.y));
         else store(static_cast<__nv_bfloat16*>(c.y));
+        un = next;
     }
     // After an expired wait, MMAs and copies in flight get their time before the CTA leaves.
     if (!ok) {
@@ -382,10 +380,15 @@ cudaError_t launch(const moe_int4* L, const Int4Call& c, const CUtensorMap& map,
     constexpr int most = fixed + 2 * (MOE_DISPATCH_MAX_EXPERTS + 1) * (int)sizeof(int);
     cudaError_t e = ensure_smem_limit<kernel>(most);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = c.strips;
-    const int64_t row_tiles = c.offsets ? std::min<int64_t>(c.rows, c.rows / Sh::BN + c.E) : ((int64_t)c.rows + Sh::BN - 1) / Sh::BN;
-    const int64_t grid = std::min<int64_t>(tiles * row_tiles, (int64_t)L->num_sms * Sh::CTAS);
-    return launch_pdl(kernel, dim3((unsigned)grid), dim3(THREADS), fixed + 2 * (c.E + 1) * (int)sizeof(int), s, map, c);
+    // Rows per tile: as many as fit, or fewer while SMs would be left without work (a stage costs a CTA about as much
+    // whatever its rows: the weights are widened for it anyway).
+    auto units = [&](int bn) {
+        return (int64_t)c.strips * (c.offsets ? std::min<int64_t>(c.rows, c.rows / bn + c.E) : ((int64_t)c.rows + bn - 1) / bn);
+    };
+    int bn = Sh::BN;
+    while (bn > 16 && units(bn) * 2 <= (int64_t)L->num_sms * Sh::CTAS) bn = bn > 32 ? 32 : 16;
+    const int64_t grid = std::min<int64_t>(units(bn), (int64_t)L->num_sms * Sh::CTAS);
+    return launch_pdl(kernel, dim3((unsigned)grid), dim3(THREADS), fixed + 2 * (c.E + 1) * (int)sizeof(int), s, map, c, bn);
 }
 
 template <int CHUNKS, XMode MODE>
