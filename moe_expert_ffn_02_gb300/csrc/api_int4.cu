@@ -123,7 +123,7 @@ MOE_EXPORT moe_status moe_int4_forward(moe_int4* L, const moe_int4_args* a, void
     c.ldy = a->ldy;
     c.status = L->dev_status;
     const uint32_t g32 = L->d.group / 32;
-    c.group_inv = ((uint64_t(1) << 32) + g32 - 1) / g32;
+    c.group_inv = g32 == 1 ? 0 : (uint32_t)(((uint64_t(1) << 32) + g32 - 1) / g32);
     c.rows = a->rows;
     c.x_rows = a->x_rows;
     c.N = L->d.out_features;

@@ -54,7 +54,7 @@ struct Int4Call {
     void* y;
     int64_t ldy;
     uint32_t* status;
-    uint64_t group_inv;    // ceil(2^32 / (group / 32)): 32-channel step n is in group n * group_inv >> 32
+    uint32_t group_inv;    // ceil(2^32 / (group / 32)), 0 for groups of 32: 32-channel step n is in group n * group_inv >> 32, or n
     int rows, x_rows;
     int N, K, E, blocks, strips, kt, groups;
     uint32_t wait_limit;

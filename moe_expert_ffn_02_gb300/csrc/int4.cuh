@@ -36,7 +36,7 @@ __device__ __forceinline__ void copy_wait() {
 }
 
 __device__ __forceinline__ int group_of(const Int4Call& c, int step32) {
-    return (int)(((uint64_t)(uint32_t)step32 * c.group_inv) >> 32);
+    return c.group_inv ? (int)__umulhi((uint32_t)step32, c.group_inv) : step32;
 }
 
 // Row tiles per expert as prefix sums: start[e] row tiles of `tile_rows` rows lie before expert e's, whose
@@ -86,6 +86,10 @@ __device__ void row_tiles(const Int4Call& c, int tile_rows, int* start, int* fir
     }
     if (threadIdx.x == THREADS - 1) start[c.E] = at;
     __syncthreads();
+}
+
+__device__ __forceinline__ void put16(uint32_t dst, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // Eight channels of a row that starts on a 2-byte boundary, those from `have` on as zeros.  Words that

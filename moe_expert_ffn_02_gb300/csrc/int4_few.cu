@@ -16,6 +16,7 @@
 // the weights; their sums meet in shared memory in the order of the warps.
 // CTAs are persistent; the ring is filled for the next unit while one ends.
 #include <algorithm>
+#include <cstddef>
 
 #include "int4.cuh"
 
@@ -46,6 +47,7 @@ struct Slot {
     uint8_t x[NB][8 * X_PITCH];        // [row][64 channels]
     uint2 s[SUB][RB * 8];              // fp32 pairs (row g, row g + 8); bf16 pairs fill the first half
     uint32_t z[SUB][ZEROS ? RB * 8 : 4];
+    static_assert(!ZEROS || sizeof(z[0]) == RB * 32, "records");
 };
 
 template <int RB, int NB, int SUB, bool ZEROS, int DEPTH>
@@ -72,27 +74,36 @@ __global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
     i4::row_tiles<THREADS>(c, NB * 8, start, first);
     const int units = start[c.E] * feature_tiles;
 
-    // What is copied next.  p_x: where this lane's row of x starts, -1: as zeros, -2: nobody reads it.
-    int p_unit = blockIdx.x, p_step = 0, p_slot = 0;
+    // What is copied next, in addresses that advance with it.  p_x: where this lane's piece of its row of x lies, as
+    // zeros, or nobody reads it.
+    constexpr uint32_t SLOT = sizeof(W);
+    const uint32_t ring = smem_addr(sm.ring[warp]);
+    int p_unit = blockIdx.x, p_step = 0;
+    uint32_t p_at = ring;
     const uint4* p_w = nullptr;
-    size_t p_rec = 0;
-    int64_t p_x[NB];
+    const char *p_s = nullptr, *p_z = nullptr;
+    const uint16_t* p_x[NB];
+    enum { READ, ZERO, NOBODY };
+    int p_how[NB];
+    const int rec = c.s_f32 ? 8 : 4;
     auto enter_w = [&](const i4::Unit& un) {
         const int block = un.tile * RB;
         const size_t strip = (size_t)un.expert * c.strips + block / I4_STRIP;
         p_w = c.w + ((strip * c.kt + t0) * I4_STRIP + block % I4_STRIP) * 32 + lane;
-        p_rec = (strip * c.groups * I4_STRIP + block % I4_STRIP) * 8 + lane;
+        const size_t first_rec = (strip * c.groups * I4_STRIP + block % I4_STRIP) * 8 + lane;
+        p_s = c.s + first_rec * rec;
+        if (ZEROS) p_z = reinterpret_cast<const char*>(c.z + first_rec);
     };
     auto enter_x = [&](const i4::Unit& un) {
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-            const int m = n * 8 + g, r = m < un.count ? i4::source_row(c, un.row0 + m) : -2;
-            p_x[n] = r < 0 ? r : r * c.ldx;
+            const int m = n * 8 + g, r = m < un.count ? i4::source_row(c, un.row0 + m) : -1;
+            p_how[n] = m >= un.count ? NOBODY : r < 0 ? ZERO : READ;
+            p_x[n] = c.x + (r < 0 ? 0 : r * c.ldx + t0 * I4_K + q * 8);
         }
     };
     auto copy = [&](bool weights, bool rows) {
         if (p_unit < units) {
-            W& slot = sm.ring[warp][p_slot];
             const int t = t0 + p_step;
             if (p_step == 0) {
                 const i4::Unit un = i4::unit_at(c, p_unit, feature_tiles, NB * 8, start, first);
@@ -101,34 +112,41 @@ __global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
             }
             if (weights) {
 #pragma unroll
-                for (int rb = 0; rb < RB; ++rb) i4::copy16(smem_addr(&slot.w[rb][lane]), p_w + rb * 32);
+                for (int rb = 0; rb < RB; ++rb) i4::copy16(p_at + offsetof(W, w) + rb * 512 + lane * 16, p_w + rb * 32);
                 p_w += I4_STRIP * 32;
                 if (RB == 4 || lane < RB * 8) {
 #pragma unroll
                     for (int sub = 0; sub < SUB; ++sub) {
-                        const size_t rec = p_rec + (size_t)i4::group_of(c, 2 * t + sub) * (I4_STRIP * 8);
-                        if (c.s_f32) i4::copy_small<8>(smem_addr(&slot.s[sub][lane]), c.s + rec * 8);
-                        else i4::copy_small<4>(smem_addr(reinterpret_cast<uint32_t*>(slot.s[sub]) + lane), c.s + rec * 4);
-                        if (ZEROS) i4::copy_small<4>(smem_addr(&slot.z[sub][lane]), c.z + rec);
+                        const uint32_t group = i4::group_of(c, 2 * t + sub);
+                        const uint32_t to = p_at + offsetof(W, s) + sub * (RB * 64);
+                        if (c.s_f32) i4::copy_small<8>(to + lane * 8, p_s + (size_t)group * (I4_STRIP * 64));
+                        else i4::copy_small<4>(to + lane * 4, p_s + (size_t)group * (I4_STRIP * 32));
+                        if (ZEROS) i4::copy_small<4>(p_at + offsetof(W, z) + sub * (RB * 32) + lane * 4, p_z + (size_t)group * (I4_STRIP * 32));
                     }
                 }
             }
             if (rows) {
-                const int k = t * I4_K + q * 8;
+                const bool whole = (t + 1) * I4_K <= c.K && c.x_grid == 16;
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    if (p_x[n] == -2) continue;
-                    uint8_t* to = slot.x[n] + g * X_PITCH + q * 16;
-                    const uint16_t* src = c.x + max(p_x[n], (int64_t)0) + k;
-                    const int have = p_x[n] < 0 ? 0 : c.K - k;          // channels from k on
+                    if (p_how[n] == NOBODY) continue;
+                    const uint32_t to = p_at + offsetof(W, x) + n * (8 * X_PITCH) + g * X_PITCH + q * 16;
+                    if (whole && p_how[n] == READ) {
+                        i4::copy16(to, p_x[n]);
+                        i4::copy16(to + 64, p_x[n] + 32);
+                        p_x[n] += I4_K;
+                        continue;
+                    }
+                    const int have = p_how[n] == ZERO ? 0 : c.K - t * I4_K - q * 8;      // channels from here on
                     if (c.x_grid == 16) {
                         const int b0 = min(max(have, 0), 8) * 2, b1 = min(max(have - 32, 0), 8) * 2;
-                        i4::copy16(smem_addr(to), b0 ? src : c.x, b0);
-                        i4::copy16(smem_addr(to + 64), b1 ? src + 32 : c.x, b1);
+                        i4::copy16(to, b0 ? p_x[n] : c.x, b0);
+                        i4::copy16(to + 64, b1 ? p_x[n] + 32 : c.x, b1);
                     } else {
-                        *reinterpret_cast<uint4*>(to) = i4::load8(src, have);
-                        *reinterpret_cast<uint4*>(to + 64) = i4::load8(src + 32, have - 32);
+                        i4::put16(to, i4::load8(p_x[n], have));
+                        i4::put16(to + 64, i4::load8(p_x[n] + 32, have - 32));
                     }
+                    if (p_how[n] == READ) p_x[n] += I4_K;
                 }
             }
             if (++p_step == steps) {
@@ -136,7 +154,7 @@ __global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
                 p_unit += gridDim.x;
             }
         }
-        p_slot = p_slot + 1 == DEPTH ? 0 : p_slot + 1;
+        p_at = p_at + SLOT == ring + DEPTH * SLOT ? ring : p_at + SLOT;
     };
 
     // the weights do not depend on the preceding kernel: the first of them are requested before the wait for it
@@ -146,7 +164,7 @@ __global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
     }
     if (!c.offsets) pdl_wait();
     if (steps > 0) {
-        p_unit = blockIdx.x, p_step = p_slot = 0;
+        p_unit = blockIdx.x, p_step = 0, p_at = ring;
 #pragma unroll 1
         for (int i = 0; i < DEPTH - 1; ++i) {
             copy(false, true);
