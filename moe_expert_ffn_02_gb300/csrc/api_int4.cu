@@ -139,7 +139,9 @@ MOE_EXPORT moe_status moe_int4_forward(moe_int4* L, const moe_int4_args* a, void
     c.gated = L->d.gated;
     c.x_grid = aligned(a->x, 16) && a->ldx % 8 == 0 ? 16 : aligned(a->x, 8) && a->ldx % 4 == 0 ? 8 : 2;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = moe::int4_takes_many(c) ? moe::launch_int4_many(L, c, s) : moe::launch_int4_few(L, c, s);
+    int groups = 0;
+    const bool many = moe::int4_many_us(L, c) < moe::int4_few_us(L, c, &groups);
+    cudaError_t e = many ? moe::launch_int4_many(L, c, s) : moe::launch_int4_few(L, c, s);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "4-bit product");
 }
 

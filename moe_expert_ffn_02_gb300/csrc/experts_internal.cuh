@@ -65,7 +65,11 @@ struct Int4Call {
 
 cudaError_t launch_int4_repack(const moe_int4* L, const moe_int4_weights* w, cudaStream_t s);
 cudaError_t launch_int4_few(const moe_int4* L, const Int4Call& c, cudaStream_t s);
-bool int4_takes_many(const Int4Call& c);        // whether the form for many rows takes the call
+// Row tiles of `height` rows that a call is expected to have: exact without offsets, else as if the rows were
+// spread over the experts by chance (half a tile more than they fill, and one for each expert that has any).
+double int4_row_tiles(const Int4Call& c, int height);
+double int4_few_us(const moe_int4* L, const Int4Call& c, int* row_groups);     // estimates, with 8 * row_groups rows a tile
+double int4_many_us(const moe_int4* L, const Int4Call& c);
 cudaError_t launch_int4_many(const moe_int4* L, const Int4Call& c, cudaStream_t s);
 
 // Tokens per chunk of the multi-CTA sort and the chunks of a call, and no fewer than any smaller batch has

@@ -40,21 +40,13 @@ __device__ __forceinline__ int group_of(const Int4Call& c, int step32) {
 }
 
 // Row tiles per expert as prefix sums: start[e] row tiles of `tile_rows` rows lie before expert e's, whose
-// first row is first[e].  Offsets are cut to [0, rows] and to rising ones.  Called by the whole CTA.
+// first row is first[e].  Offsets are cut to [0, rows] and to rising ones.  Called by the whole CTA; without
+// offsets there is nothing to make.
 template <int THREADS>
 __device__ void row_tiles(const Int4Call& c, int tile_rows, int* start, int* first) {
     __shared__ int sums[THREADS / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (!c.offsets) {
-        if (threadIdx.x == 0) {
-            start[0] = 0;
-            start[1] = (c.rows + tile_rows - 1) / tile_rows;
-            first[0] = 0;
-            first[1] = c.rows;
-        }
-        __syncthreads();
-        return;
-    }
+    if (!c.offsets) return;
     bool bad = false;
     for (int e = threadIdx.x; e <= c.E; e += THREADS) {
         const int v = c.offsets[e], cut = min(max(v, 0), c.rows);
@@ -119,9 +111,17 @@ struct Unit {
     int row0, count;       // rows of y
 };
 
+__device__ __forceinline__ int unit_count(const Int4Call& c, int feature_tiles, int tile_rows, const int* start) {
+    return feature_tiles * (c.offsets ? start[c.E] : (int)(((int64_t)c.rows + tile_rows - 1) / tile_rows));
+}
+
 // Unit u: row tiles of one feature tile are neighbours, so that its weights are read once.
 __device__ __forceinline__ Unit unit_at(const Int4Call& c, int u, int feature_tiles, int tile_rows, const int* start,
                                         const int* first) {
+    if (!c.offsets) {
+        const int tiles = (int)(((int64_t)c.rows + tile_rows - 1) / tile_rows), tile = u / tiles, row0 = (u - tile * tiles) * tile_rows;
+        return {0, tile, row0, min(tile_rows, c.rows - row0)};
+    }
     const int v = u / feature_tiles;
     int lo = 0, hi = c.E - 1;              // last expert with start[e] <= v
     while (lo < hi) {

@@ -16,6 +16,7 @@
 // the weights; their sums meet in shared memory in the order of the warps.
 // CTAs are persistent; the ring is filled for the next unit while one ends.
 #include <algorithm>
+#include <cmath>
 #include <cstddef>
 
 #include "int4.cuh"
@@ -24,7 +25,6 @@ namespace moe {
 
 namespace {
 
-constexpr int THREADS = 256, WARPS = 8;
 constexpr int X_PITCH = 160;           // bytes between rows of a tile of x: the lanes' 8-byte reads fall into different banks
 
 // d (+)= a b; the first of a chain starts from zeros.
@@ -50,7 +50,7 @@ struct Slot {
     static_assert(!ZEROS || sizeof(z[0]) == RB * 32, "records");
 };
 
-template <int RB, int NB, int SUB, bool ZEROS, int DEPTH>
+template <int RB, int NB, int SUB, bool ZEROS, int DEPTH, int WARPS>
 struct Smem {
     Slot<RB, NB, SUB, ZEROS> ring[WARPS][DEPTH];
     float sums[WARPS][NB * 8][RB * I4_ROWS + 4];      // + 4: the lanes' rows fall into different banks
@@ -58,11 +58,12 @@ struct Smem {
 };
 
 // SUB: scales per tile and row (2 where a group may end inside a tile).
-template <int RB, int NB, int SUB, bool ZEROS, int DEPTH>
-__global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
+template <int RB, int NB, int SUB, bool ZEROS, int DEPTH, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) int4_few_kernel(const Int4Call c) {
+    constexpr int THREADS = WARPS * 32;
     using W = Slot<RB, NB, SUB, ZEROS>;
     extern __shared__ __align__(16) char smem_raw[];
-    auto& sm = *reinterpret_cast<Smem<RB, NB, SUB, ZEROS, DEPTH>*>(smem_raw);
+    auto& sm = *reinterpret_cast<Smem<RB, NB, SUB, ZEROS, DEPTH, WARPS>*>(smem_raw);
     int* start = sm.table;
     int* first = sm.table + c.E + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
     pdl_trigger();
     if (c.offsets) pdl_wait();
     i4::row_tiles<THREADS>(c, NB * 8, start, first);
-    const int units = start[c.E] * feature_tiles;
+    const int units = i4::unit_count(c, feature_tiles, NB * 8, start);
 
     // What is copied next, in addresses that advance with it.  p_x: where this lane's piece of its row of x lies, as
     // zeros, or nobody reads it.
@@ -268,36 +269,28 @@ __global__ void __launch_bounds__(THREADS) int4_few_kernel(const Int4Call c) {
     i4::copy_wait<0>();
 }
 
-template <int RB, int NB, int SUB, bool ZEROS>
+template <int RB, int NB, int SUB, bool ZEROS, int WARPS>
 cudaError_t launch(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
     constexpr int DEPTH = RB == 4 || NB == 4 ? 3 : 4;
-    using S = Smem<RB, NB, SUB, ZEROS, DEPTH>;
-    constexpr auto kernel = int4_few_kernel<RB, NB, SUB, ZEROS, DEPTH>;
+    using S = Smem<RB, NB, SUB, ZEROS, DEPTH, WARPS>;
+    constexpr auto kernel = int4_few_kernel<RB, NB, SUB, ZEROS, DEPTH, WARPS>;
     const int bytes = sizeof(S) + 2 * (c.E + 1) * (int)sizeof(int);
     constexpr int most = sizeof(S) + 2 * (MOE_DISPATCH_MAX_EXPERTS + 1) * (int)sizeof(int);
     static_assert(most <= 227 * 1024 - 1024, "shared memory");
     cudaError_t e = ensure_smem_limit<kernel>(most);
     if (e != cudaSuccess) return e;
-    const int per_sm = std::min(4, 227 * 1024 / (bytes + 1024));
+    const int per_sm = std::min(2048 / (WARPS * 32), 227 * 1024 / (bytes + 1024));
     const int64_t tiles = c.blocks / RB;
     // with offsets no more row tiles than full ones and one for each expert
-    const int64_t row_tiles = c.offsets ? std::min<int64_t>(c.rows, c.rows / (NB * 8) + c.E) : (c.rows + NB * 8 - 1) / (NB * 8);
+    const int64_t row_tiles = c.offsets ? std::min<int64_t>(c.rows, c.rows / (NB * 8) + c.E) : ((int64_t)c.rows + NB * 8 - 1) / (NB * 8);
     const int64_t grid = std::min<int64_t>(tiles * row_tiles, (int64_t)L->num_sms * per_sm);
-    return launch_pdl(kernel, dim3((unsigned)grid), dim3(THREADS), bytes, s, c);
+    return launch_pdl(kernel, dim3((unsigned)grid), dim3(WARPS * 32), bytes, s, c);
 }
 
-template <int RB, int NB>
+template <int RB, int NB, int WARPS>
 cudaError_t launch_sub(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
-    if (L->d.group % I4_K) return c.z ? launch<RB, NB, 2, true>(L, c, s) : launch<RB, NB, 2, false>(L, c, s);
-    return c.z ? launch<RB, NB, 1, true>(L, c, s) : launch<RB, NB, 1, false>(L, c, s);
-}
-
-template <int RB>
-cudaError_t launch_rows(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
-    const int64_t rows = c.offsets ? (int64_t)c.rows / c.E * 4 : c.rows;
-    if (rows <= 8) return launch_sub<RB, 1>(L, c, s);
-    if (rows <= 16) return launch_sub<RB, 2>(L, c, s);
-    return launch_sub<RB == 4 ? 2 : RB, 4>(L, c, s);
+    if (L->d.group % I4_K) return c.z ? launch<RB, NB, 2, true, WARPS>(L, c, s) : launch<RB, NB, 2, false, WARPS>(L, c, s);
+    return c.z ? launch<RB, NB, 1, true, WARPS>(L, c, s) : launch<RB, NB, 1, false, WARPS>(L, c, s);
 }
 
 // One thread per lane's 16 bytes.
@@ -379,10 +372,34 @@ cudaError_t launch_int4_repack(const moe_int4* L, const moe_int4_weights* w, cud
     return cudaGetLastError();
 }
 
+double int4_row_tiles(const Int4Call& c, int height) {
+    if (!c.offsets) return (double)(((int64_t)c.rows + height - 1) / height);
+    const double experts = c.E * (1 - std::exp(-(double)c.rows / c.E)), mean = c.rows / experts;
+    return experts * std::max(1.0, mean / height + 0.5);
+}
+
+// Measured: a tile of a block takes the GPU 0.15 ns with 8 rows of x, 0.30 with 16 and 0.56 with 32; over
+// that, 4 us.
+double int4_few_us(const moe_int4*, const Int4Call& c, int* row_groups) {
+    constexpr struct { int groups; double ns; } forms[] = {{1, 0.15}, {2, 0.30}, {4, 0.56}};
+    double best = 1e30;
+    for (const auto& f : forms) {
+        const double us = 4 + int4_row_tiles(c, 8 * f.groups) * c.blocks * c.kt * f.ns * 1e-3;
+        if (us < best) best = us, *row_groups = f.groups;
+    }
+    return best;
+}
+
 cudaError_t launch_int4_few(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
+    int groups = 1;
+    int4_few_us(L, c, &groups);
+    // Blocks of a unit: the more, the less often x is read; but where there are few blocks, more CTAs (1 x 2048 x
+    // 7168: 4.9 us with 2, 5.8 with 1, 6.1 with 4; 16 x 7168 x 2048 gated: 11.6 with 2, 13.3 with 1, 16.2 with 4).
     const int64_t blocks = (int64_t)c.blocks * (c.offsets ? std::min(c.E, c.rows) : 1);
-    if (blocks <= 4 * L->num_sms) return launch_rows<1>(L, c, s);
-    return launch_rows<4>(L, c, s);
+    const int rb = blocks <= L->num_sms ? 1 : blocks <= 4 * L->num_sms ? 2 : 4;
+    if (groups == 1) return rb == 1 ? launch_sub<1, 1, 8>(L, c, s) : rb == 2 ? launch_sub<2, 1, 8>(L, c, s) : launch_sub<4, 1, 8>(L, c, s);
+    if (groups == 2) return rb == 1 ? launch_sub<1, 2, 8>(L, c, s) : rb == 2 ? launch_sub<2, 2, 8>(L, c, s) : launch_sub<4, 2, 8>(L, c, s);
+    return rb == 1 ? launch_sub<1, 4, 8>(L, c, s) : launch_sub<2, 4, 8>(L, c, s);
 }
 
 }  // namespace moe

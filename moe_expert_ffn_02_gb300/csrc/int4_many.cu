@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
     if (c.offsets) pdl_wait();
     i4::row_tiles<THREADS>(c, bn, start, first);
     const uint32_t tmem = sm.tmem;
-    const int units = start[c.E] * c.strips;
+    const int units = i4::unit_count(c, c.strips, bn, start);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, c.wait_limit, c.status, nullptr));
     };
@@ -414,13 +414,22 @@ cudaError_t launch_mode(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
 
 }  // namespace
 
-bool int4_takes_many(const Int4Call& c) { return (c.offsets ? c.rows / c.E : c.rows) > 32; }
+namespace {
+int chunk_of(const moe_int4* L) { return L->d.group % 128 == 0 || L->groups == 1 ? 128 : L->d.group % 64 == 0 ? 64 : 32; }
+}  // namespace
+
+// Measured: a stage takes a CTA 0.93 us (1.0 with several chunks) however few there are, and an SM 0.47 us (0.67)
+// when it has as many as fit.
+double int4_many_us(const moe_int4* L, const Int4Call& c) {
+    const int chunk = chunk_of(L);
+    const double units = int4_row_tiles(c, chunk == 32 ? Shape<4>::BN : Shape<1>::BN) * c.strips;
+    return 4 + c.kt / TILES * std::max(chunk == 128 ? 0.93 : 1.0, units / L->num_sms * (chunk == 128 ? 0.47 : 0.67));
+}
 
 cudaError_t launch_int4_many(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
-    const int group = L->d.group;
-    const int chunk = group % 128 == 0 || L->groups == 1 ? 128 : group % 64 == 0 ? 64 : 32;
+    const int chunk = chunk_of(L);
     Int4Call call = c;
-    call.groups_are_chunks = group == chunk;
+    call.groups_are_chunks = L->d.group == chunk;
     return chunk == 128 ? launch_mode<1>(L, call, s) : chunk == 64 ? launch_mode<2>(L, call, s) : launch_mode<4>(L, call, s);
 }
 
