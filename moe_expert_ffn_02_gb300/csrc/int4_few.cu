@@ -378,10 +378,10 @@ double int4_row_tiles(const Int4Call& c, int height) {
     return experts * std::max(1.0, mean / height + 0.5);
 }
 
-// Measured: a tile of a block takes the GPU 0.15 ns with 8 rows of x, 0.30 with 16 and 0.56 with 32; over
+// Measured: a tile of a block takes the GPU 0.15 ns with 8 rows of x, 0.30 with 16 and 0.50 with 32; over
 // that, 4 us.
 double int4_few_us(const moe_int4*, const Int4Call& c, int* row_groups) {
-    constexpr struct { int groups; double ns; } forms[] = {{1, 0.15}, {2, 0.30}, {4, 0.56}};
+    constexpr struct { int groups; double ns; } forms[] = {{1, 0.15}, {2, 0.30}, {4, 0.50}};
     double best = 1e30;
     for (const auto& f : forms) {
         const double us = 4 + int4_row_tiles(c, 8 * f.groups) * c.blocks * c.kt * f.ns * 1e-3;

@@ -1,436 +1,30 @@
-// Products with 4-bit weights, many rows per matrix, on the 5th-generation
-// tensor cores (tcgen05, sm_103a).
-//
-// A tile is 128 weight rows (the MMA's M, tensor-memory lanes) by up to BN
-// rows of x (its N, columns), a stage 128 input channels.  Four warps widen the
-// codes of a stage, less their zero points, to bf16, exactly, and store them
-// straight into tensor memory as the MMA's first operand: through shared
-// memory each weight would be written and read there at two bytes, as long as
-// the MMAs of 64 columns take.  One of them issues the MMAs; all wait, scale
-// what came out and add it up in fp32 registers.
-//
-// The tensor core's running sum truncates, and scales are per 32 channels at
-// the finest: each stage goes into fresh accumulators, CHUNKS of them (1, 2 or
-// 4, of 128, 64 or 32 channels, as fine as the groups).  A lane is one weight
-// row, so a scale is one scalar per thread and chunk.
-//
-// What there is to overlap, CTAs overlap: four share an SM (two where CHUNKS is
-// more than one and the accumulators take more of the tensor memory).  Warps
-// with roles of their own, one CTA to the SM, were twice as slow: each hand-off
-// between roles costs its 100 to 300 clocks, each role's code its place in the
-// instruction cache, and the widening warps keep the others from issuing.
-#include <algorithm>
-
-#include "dense_internal.cuh"
-#include "int4.cuh"
-#include "tcgen05.cuh"
+// The forms of the 4-bit products for many rows: which chunk a call's groups ask for.  Each chunk's kernels are
+// compiled in a unit of their own.
+#include "experts_internal.cuh"
 
 namespace moe {
 
-namespace {
-
-constexpr int THREADS = 128;
-constexpr int TILES = 2, STAGE_K = TILES * I4_K, STEPS = STAGE_K / 32;     // of 64 and of 32 channels
-constexpr int A_COLS = STAGE_K / 2;              // operand columns: two bf16 channels each
-constexpr int X_SLOTS = 2;                       // stages of x
-
-enum XMode { X_TILE, X_GATHER, X_COPY };
-
-// Tensor memory: accumulators, then the operand.
-template <int CHUNKS>
-struct Shape {
-    static constexpr int BN = CHUNKS == 4 ? 48 : 64;
-    static constexpr int TMEM_COLS = CHUNKS == 1 ? 128 : 256;
-    static constexpr int CTAS = 512 / TMEM_COLS;             // per SM
-    static constexpr int CODE_SLOTS = CHUNKS == 1 ? 2 : 4;   // stages of codes
-    static constexpr int SCALE_SLOTS = 2 * CODE_SLOTS;       // of scales, which are read after the codes' slot is filled anew
-    static constexpr int BOX = BN % 32 ? 16 : 32;            // rows of x that one copy brings
-    static constexpr int PIECE = BN % 32 ? 16 : 32;          // columns that one load of accumulators brings
-    static_assert(CHUNKS * BN + A_COLS <= TMEM_COLS, "tensor memory");
-};
-
-template <int CHUNKS>
-struct Smem {
-    using Sh = Shape<CHUNKS>;
-    uint8_t x[X_SLOTS][TILES][Sh::BN * 128];     // 128-byte swizzle, 1024-byte aligned
-    uint4 codes[Sh::CODE_SLOTS][TILES][I4_STRIP][32];
-    uint32_t zeros[Sh::CODE_SLOTS][CHUNKS][I4_STRIP][8];
-    uint2 scales[Sh::SCALE_SLOTS][CHUNKS][I4_STRIP][8];      // fp32 pairs; bf16 pairs fill the first half of a stage's
-    uint64_t code_full[Sh::CODE_SLOTS], x_full[X_SLOTS], done;
-    uint32_t tmem;
-    int table[1];                                // start[E + 1], first[E + 1]
-};
-
-// 16 lanes by 32 columns, four 8-column groups: registers 4 i .. 4 i + 3 of lane 4 g + q are columns
-// 8 i + 2 q, + 1 of row g, then of row g + 8.
-__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Two K16 steps (32 channels), the first operand in tensor memory, by the elected lane.  b_lo: low word of
-// the second operand's descriptor, 2 more per step.  accumulate: whether the first adds to what is there.
-__device__ __forceinline__ void mma_ts2(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t elected, uint32_t accumulate) {
-    constexpr uint32_t HI = (uint32_t)(tc::DESC_HI >> 32);
-    asm volatile(
-        "{\n .reg .pred q, t;\n .reg .b64 b;\n .reg .b32 x, y;\n"
-        " setp.ne.b32 q, %5, 0;\n setp.ne.b32 t, %6, 0;\n"
-        " mov.b64 b, {%2, %4};\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, t;\n"
-        " setp.eq.b32 t, 0, 0;\n"
-        " add.u32 x, %1, 8;\n add.u32 y, %2, 2;\n mov.b64 b, {y, %4};\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n}" ::"r"(d),
-        "r"(a), "r"(b_lo), "r"(idesc), "n"(HI), "r"(elected), "r"(accumulate)
-        : "memory");
-}
-
-// True in one lane of a converged warp.
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t p;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-    return p;
-}
-
-__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int k, int row, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(k), "r"(row), "r"(bar)
-        : "memory");
-}
-// Four rows anywhere, one after the other at dst.
-__device__ __forceinline__ void tma_gather(uint32_t dst, const CUtensorMap* map, int k, const int (&row)[4], uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(k), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar)
-        : "memory");
-}
-
-// (a0, a1) += (p0, p1) * (s, s): two fp32 fused multiply-adds in one instruction.
-__device__ __forceinline__ void fma_pair(uint64_t& a, uint32_t p0, uint32_t p1, uint64_t ss) {
-    asm("{\n .reg .b64 t;\n mov.b64 t, {%1, %2};\n fma.rn.f32x2 %0, t, %3, %0;\n}" : "+l"(a) : "r"(p0), "r"(p1), "l"(ss));
-}
-
-// D f32, A = B = bf16, both K-major, M = 128.
-__device__ __forceinline__ uint32_t idesc_for(int n) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-}
-
-template <int CHUNKS, XMode MODE, bool ZEROS, bool GATED>
-__global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel(const __grid_constant__ CUtensorMap x_map, const Int4Call c, int bn) {
-    using Sh = Shape<CHUNKS>;
-    constexpr int BN = Sh::BN, CODE_SLOTS = Sh::CODE_SLOTS, SCALE_SLOTS = Sh::SCALE_SLOTS, CHUNK_STEPS = STEPS / CHUNKS;
-    constexpr uint32_t TILE_BYTES = BN * 128, A_AT = CHUNKS * BN;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    auto& sm = *reinterpret_cast<Smem<CHUNKS>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    int* start = sm.table;
-    int* first = sm.table + c.E + 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
-    const int stages = c.kt / TILES;             // per unit
-    const int s_rec = (c.s_f32 ? 8 : 4) * I4_STRIP * 8, z_rec = 4 * I4_STRIP * 8;    // bytes of a strip's group
-
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < CODE_SLOTS; ++s) mbar_init(&sm.code_full[s], 1);
-        for (int s = 0; s < X_SLOTS; ++s) mbar_init(&sm.x_full[s], 1);
-        mbar_init(&sm.done, 1);
-        fence_mbar_init();
-    }
-    if (warp == 0) tc::tmem_alloc(&sm.tmem, Sh::TMEM_COLS);
-    tc::tc_fence_before();
-    __syncthreads();
-    tc::tc_fence_after();
-    if (c.offsets) pdl_wait();
-    i4::row_tiles<THREADS>(c, bn, start, first);
-    const uint32_t tmem = sm.tmem;
-    const int units = i4::unit_count(c, c.strips, bn, start);
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, c.wait_limit, c.status, nullptr));
-    };
-
-    // ---- Copies.  Warp 3 requests codes, scales and zero points, warp 1 rows of x (MODE X_COPY: all warps bring them,
-    // stage by stage); both are ahead of the sums by as many stages as there are slots.
-    int p_unit = blockIdx.x, p_stage = 0;
-    uint32_t p_n = 0;
-    size_t p_strip = 0;
-    int p_row0 = 0, p_count = 0, p_row[4];
-    auto enter = [&]() {
-        const i4::Unit un = i4::unit_at(c, p_unit, c.strips, bn, start, first);
-        p_strip = (size_t)un.expert * c.strips + un.tile;
-        p_row0 = un.row0;
-        p_count = un.count;
-        if (MODE == X_GATHER && warp == 1) {     // lane i has rows 4 i to 4 i + 3; -1 reads as zeros
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p_row[i] = lane * 4 + i < un.count ? i4::source_row(c, un.row0 + lane * 4 + i) : -1;
-        }
-    };
-    auto advance = [&]() {
-        ++p_n;
-        if (++p_stage == stages) {
-            p_stage = 0;
-            p_unit += gridDim.x;
-            if (p_unit < units) enter();
-        }
-    };
-    auto copy_codes = [&]() {
-        if (p_unit >= units) return;
-        if (elect_one()) {
-            const uint32_t slot = p_n % CODE_SLOTS;
-            // a record for every chunk, whatever the groups: neighbours where groups are as long as chunks
-            const int pieces = CHUNKS == 1 || c.groups_are_chunks ? 1 : CHUNKS, records = CHUNKS / pieces, step = p_stage * STEPS;
-            uint64_t* bar = &sm.code_full[slot];
-            mbar_arrive_expect_tx(bar, TILES * (I4_STRIP * 512) + CHUNKS * (s_rec + (ZEROS ? z_rec : 0)));
-            bulk_g2s(sm.codes[slot], reinterpret_cast<const char*>(c.w) + (p_strip * c.kt + p_stage * TILES) * (I4_STRIP * 512),
-                     TILES * (I4_STRIP * 512), bar);
-#pragma unroll 1
-            for (int j = 0; j < pieces; ++j) {
-                const size_t from = p_strip * c.groups + i4::group_of(c, step + j * CHUNK_STEPS);
-                if (ZEROS)
-                    bulk_g2s(reinterpret_cast<char*>(sm.zeros[slot]) + j * z_rec, reinterpret_cast<const char*>(c.z) + from * z_rec, records * z_rec, bar);
-                bulk_g2s(reinterpret_cast<char*>(sm.scales[p_n % SCALE_SLOTS]) + j * s_rec, c.s + from * s_rec, records * s_rec, bar);
-            }
-        }
-        __syncwarp();
-        advance();
-    };
-    auto copy_x = [&]() {
-        if (p_unit >= units) return;
-        const uint32_t slot = p_n % X_SLOTS, bar = smem_addr(&sm.x_full[slot]), to = smem_addr(sm.x[slot][0]);
-        const int copies = MODE == X_TILE ? (p_count + Sh::BOX - 1) / Sh::BOX : (p_count + 3) / 4;
-        if (lane == 0) mbar_arrive_expect_tx(&sm.x_full[slot], copies * TILES * (MODE == X_TILE ? Sh::BOX : 4) * 128);
-        __syncwarp();
-        if (MODE == X_TILE) {
-            const int box = lane / TILES, tile = lane % TILES;
-            if (box < copies)
-                tma_rows(to + tile * TILE_BYTES + box * (Sh::BOX * 128), &x_map, p_stage * STAGE_K + tile * I4_K, p_row0 + box * Sh::BOX, bar);
-        } else if (lane < copies) {
-#pragma unroll
-            for (int tile = 0; tile < TILES; ++tile)
-                tma_gather(to + tile * TILE_BYTES + lane * 512, &x_map, p_stage * STAGE_K + tile * I4_K, p_row, bar);
-        }
-        advance();
-    };
-    // rows of x off the 16-byte grid: 8 rows by 4 of the 16 pieces of 8 channels a warp each time
-    auto copy_x_by_hand = [&](const i4::Unit& un, int st, uint8_t* slot) {
-#pragma unroll 1
-        for (int r = warp * 8 + g; r < un.count; r += THREADS / 4) {
-            const int from = i4::source_row(c, un.row0 + r);
-            const uint16_t* p = c.x + (from < 0 ? 0 : from) * c.ldx + st * STAGE_K;
-            uint4 v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = ((lane & 3) + 4 * i) * 8;
-                v[i] = i4::load8(p + k, from < 0 ? 0 : min(c.K - st * STAGE_K - k, 8));
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int piece = (lane & 3) + 4 * i;
-                *reinterpret_cast<uint4*>(slot + (piece >> 3) * TILE_BYTES + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) = v[i];
-            }
-        }
-        fence_async_proxy();
-        __syncwarp();
-    };
-    const bool copies_codes = warp == 3, copies_x = MODE != X_COPY && warp == 1;
-    if (p_unit < units) enter();
-    // The weights do not depend on the preceding kernel: the first of them are requested before the wait for it.
-    if (copies_codes)
-#pragma unroll 1
-        for (int i = 0; i < CODE_SLOTS; ++i) copy_codes();
-    if (!c.offsets) pdl_wait();
-    if (copies_x)
-#pragma unroll 1
-        for (int i = 0; i < X_SLOTS; ++i) copy_x();
-
-    // ---- Sums.
-    const int row = warp * 32 + lane, row_block = row >> 4, row_g = row & 7, upper = (row >> 3) & 1;
-    // where the row's scale lies in a record, in words, and which of its bytes make it an fp32
-    const int s_at = (row_block * 8 + row_g) * (c.s_f32 ? 2 : 1) + (c.s_f32 ? upper : 0), s_step = I4_STRIP * 8 * (c.s_f32 ? 2 : 1);
-    const uint32_t s_bytes = c.s_f32 ? 0x3210u : upper ? 0x3244u : 0x1044u;
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-    uint32_t n = 0;
-    bool ok = true, pending = false;             // pending: MMAs that nobody has seen complete
-    i4::Unit un = {};
-    if (blockIdx.x < units) un = i4::unit_at(c, blockIdx.x, c.strips, bn, start, first);
-    if (MODE == X_COPY && blockIdx.x < units) copy_x_by_hand(un, 0, sm.x[0][0]);
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-        i4::Unit next = un;
-        if (u + (int)gridDim.x < units) next = i4::unit_at(c, u + gridDim.x, c.strips, bn, start, first);
-        const uint32_t idesc = idesc_for((un.count + 15) / 16 * 16);
-        uint64_t acc[BN / 2];
-#pragma unroll
-        for (int i = 0; i < BN / 2; ++i) acc[i] = 0;
-        for (int st = 0; st < stages; ++st, ++n) {
-            const uint32_t slot = n % CODE_SLOTS;
-            ok = ok && wait(&sm.code_full[slot], n / CODE_SLOTS & 1u);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {        // the warp's blocks: 16 lanes of tensor memory each
-                const int block = 2 * warp + i;
-#pragma unroll
-                for (int tile = 0; tile < TILES; ++tile) {
-                    uint32_t r[16], v[4];
-                    const uint4 code = sm.codes[slot][tile][block][lane];
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t z = ZEROS ? sm.zeros[slot][(tile * 2 + half) / CHUNK_STEPS][block][g] : I4_ZERO;
-                        i4::widen(half ? code.y : code.x, ZEROS ? __byte_perm(z, 0, 0x1010) : z, v);
-                        r[8 * half] = v[0], r[8 * half + 1] = v[1], r[8 * half + 4] = v[2], r[8 * half + 5] = v[3];
-                        i4::widen(half ? code.w : code.z, ZEROS ? __byte_perm(z, 0, 0x3232) : z, v);
-                        r[8 * half + 2] = v[0], r[8 * half + 3] = v[1], r[8 * half + 6] = v[2], r[8 * half + 7] = v[3];
-                    }
-                    tmem_st_16x32(lanes + ((uint32_t)(i * 16) << 16) + A_AT + tile * (A_COLS / TILES), r);
-                }
-            }
-            tmem_wait_st();
-            tc::tc_fence_before();
-            // all of the operand is there, and everybody has read the accumulators; a wait that gave up ends it for all
-            ok = !__syncthreads_or(!ok);
-            if (!ok) break;
-            tc::tc_fence_after();
-            if (warp == 2) {
-                ok = MODE == X_COPY || wait(&sm.x_full[n % X_SLOTS], n / X_SLOTS & 1u);
-                if (ok) {
-                    const uint32_t el = elect_one(), b = (uint32_t)tc::sw128_desc(smem_addr(sm.x[n % X_SLOTS][0]));
-#pragma unroll
-                    for (int i = 0; i < STEPS; ++i)
-                        mma_ts2(tmem + i / CHUNK_STEPS * BN, tmem + A_AT + i * 16, b + (i >> 1) * (TILE_BYTES >> 4) + (i & 1) * 4, idesc, el,
-                                i % CHUNK_STEPS != 0);
-                    if (el) tc::mma_commit(&sm.done);
-                    __syncwarp();
-                    pending = true;
-                }
-            }
-            if (copies_codes) copy_codes();
-            // by hand the next stage's x, while the MMAs of this one run
-            if (MODE == X_COPY && (st + 1 < stages || u + (int)gridDim.x < units))
-                copy_x_by_hand(st + 1 < stages ? un : next, st + 1 < stages ? st + 1 : 0, sm.x[(n + 1) % X_SLOTS][0]);
-            uint64_t sc[CHUNKS];
-#pragma unroll
-            for (int j = 0; j < CHUNKS; ++j) {
-                uint32_t v = __byte_perm(reinterpret_cast<const uint32_t*>(sm.scales[n % SCALE_SLOTS])[s_at + j * s_step], 0, s_bytes);
-                sc[j] = (uint64_t)v << 32 | v;
-            }
-            ok = ok && wait(&sm.done, n & 1u);
-            if (ok) pending = false;
-            tc::tc_fence_after();
-            if (copies_x && ok) copy_x();
-#pragma unroll
-            for (int i = 0; i < CHUNKS * BN / Sh::PIECE; ++i) {
-                const int j = i * Sh::PIECE / BN, col = i * Sh::PIECE % BN;
-                if (ok && col < un.count) {
-                    uint32_t part[Sh::PIECE];
-                    if constexpr (Sh::PIECE == 32) tc::tmem_ld32u(lanes + j * BN + col, part);
-                    else tc::tmem_ld16u(lanes + j * BN + col, part);
-                    tc::tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < Sh::PIECE / 2; ++e) fma_pair(acc[col / 2 + e], part[2 * e], part[2 * e + 1], sc[j]);
-                }
-            }
-        }
-        ok = !__syncthreads_or(!ok);
-        if (!ok) break;
-        const int n0 = GATED ? (un.tile * I4_STRIP + row_block) * 8 + row_g : un.tile * 128 + row;
-        auto store = [&](auto* y) {
-            auto* at = y + (un.row0 + (GATED ? upper : 0)) * c.ldy + n0;
-#pragma unroll
-            for (int m = 0; m < BN; m += 2) {
-                if (m % 16 == 0 && m >= un.count) break;
-                const float even = __uint_as_float((uint32_t)acc[m / 2]), odd = __uint_as_float((uint32_t)(acc[m / 2] >> 32));
-                if (GATED) {
-                    // lanes of a gate row take the even rows of x, those of its up row, 8 lanes on, the odd ones
-                    const float got = __shfl_xor_sync(0xFFFFFFFFu, upper ? even : odd, 8);
-                    const float h = i4::gate(upper ? got : even, upper ? odd : got);
-                    if (n0 < c.N && m + upper < un.count) i4::put_y(at, h);
-                } else {
-                    if (n0 < c.N && m < un.count) i4::put_y(at, even);
-                    if (n0 < c.N && m + 1 < un.count) i4::put_y(at + c.ldy, odd);
-                }
-                at += 2 * c.ldy;
-            }
-        };
-        if (c.y_f32) store(static_cast<float*>(c.y));
-        else store(static_cast<__nv_bfloat16*>(c.y));
-        un = next;
-    }
-    // After an expired wait, MMAs and copies in flight get their time before the CTA leaves.
-    if (!ok) {
-        if (pending) mbar_wait_bounded(&sm.done, n & 1u, LANDING_LIMIT_US, c.status, nullptr);
-        if (copies_codes)
-            for (uint32_t i = p_n - min(p_n, (uint32_t)CODE_SLOTS); i < p_n; ++i)
-                mbar_wait_bounded(&sm.code_full[i % CODE_SLOTS], i / CODE_SLOTS & 1u, LANDING_LIMIT_US, c.status, nullptr);
-        if (copies_x)
-            for (uint32_t i = p_n - min(p_n, (uint32_t)X_SLOTS); i < p_n; ++i)
-                mbar_wait_bounded(&sm.x_full[i % X_SLOTS], i / X_SLOTS & 1u, LANDING_LIMIT_US, c.status, nullptr);
-    }
-    tc::tc_fence_before();
-    __syncthreads();
-    tc::tc_fence_after();
-    if (warp == 0) tc::tmem_dealloc(tmem, Sh::TMEM_COLS);
-}
-
-template <int CHUNKS, XMode MODE, bool ZEROS, bool GATED>
-cudaError_t launch(const moe_int4* L, const Int4Call& c, const CUtensorMap& map, cudaStream_t s) {
-    using Sh = Shape<CHUNKS>;
-    constexpr auto kernel = int4_many_kernel<CHUNKS, MODE, ZEROS, GATED>;
-    constexpr int fixed = sizeof(Smem<CHUNKS>) + 1024;
-    constexpr int most = fixed + 2 * (MOE_DISPATCH_MAX_EXPERTS + 1) * (int)sizeof(int);
-    cudaError_t e = ensure_smem_limit<kernel>(most);
-    if (e != cudaSuccess) return e;
-    // Rows per tile: as many as fit, or fewer while SMs would be left without work (a stage costs a CTA about as much
-    // whatever its rows: the weights are widened for it anyway).
-    auto units = [&](int bn) {
-        return (int64_t)c.strips * (c.offsets ? std::min<int64_t>(c.rows, c.rows / bn + c.E) : ((int64_t)c.rows + bn - 1) / bn);
-    };
-    int bn = Sh::BN;
-    while (bn > 16 && units(bn) * 2 <= (int64_t)L->num_sms * Sh::CTAS) bn = bn > 32 ? 32 : 16;
-    const int64_t grid = std::min<int64_t>(units(bn), (int64_t)L->num_sms * Sh::CTAS);
-    return launch_pdl(kernel, dim3((unsigned)grid), dim3(THREADS), fixed + 2 * (c.E + 1) * (int)sizeof(int), s, map, c, bn);
-}
-
-template <int CHUNKS, XMode MODE>
-cudaError_t launch_types(const moe_int4* L, const Int4Call& c, const CUtensorMap& map, cudaStream_t s) {
-    if (c.gated) return c.z ? launch<CHUNKS, MODE, true, true>(L, c, map, s) : launch<CHUNKS, MODE, false, true>(L, c, map, s);
-    return c.z ? launch<CHUNKS, MODE, true, false>(L, c, map, s) : launch<CHUNKS, MODE, false, false>(L, c, map, s);
-}
-
-template <int CHUNKS>
-cudaError_t launch_mode(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
-    CUtensorMap map = {};
-    if (c.x_grid < 16) return launch_types<CHUNKS, X_COPY>(L, c, map, s);
-    const EncodeTiledFn encode = tensor_map_encoder();
-    if (!encode) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {(cuuint64_t)c.K, (cuuint64_t)c.x_rows}, strides[1] = {(cuuint64_t)c.ldx * 2};
-    const cuuint32_t box[2] = {I4_K, c.token ? 1u : (cuuint32_t)Shape<CHUNKS>::BOX}, step[2] = {1, 1};
-    if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(c.x), dims, strides, box, step,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
-    return c.token ? launch_types<CHUNKS, X_GATHER>(L, c, map, s) : launch_types<CHUNKS, X_TILE>(L, c, map, s);
-}
-
-}  // namespace
+cudaError_t launch_int4_many_128(const moe_int4* L, const Int4Call& c, cudaStream_t s);
+cudaError_t launch_int4_many_64(const moe_int4* L, const Int4Call& c, cudaStream_t s);
+cudaError_t launch_int4_many_32(const moe_int4* L, const Int4Call& c, cudaStream_t s);
+double int4_many_us_128(const moe_int4* L, const Int4Call& c);
+double int4_many_us_64(const moe_int4* L, const Int4Call& c);
+double int4_many_us_32(const moe_int4* L, const Int4Call& c);
 
 namespace {
 int chunk_of(const moe_int4* L) { return L->d.group % 128 == 0 || L->groups == 1 ? 128 : L->d.group % 64 == 0 ? 64 : 32; }
 }  // namespace
 
-// Measured: a stage takes a CTA 0.93 us (1.0 with several chunks) however few there are, and an SM 0.47 us (0.67)
-// when it has as many as fit.
 double int4_many_us(const moe_int4* L, const Int4Call& c) {
     const int chunk = chunk_of(L);
-    const double units = int4_row_tiles(c, chunk == 32 ? Shape<4>::BN : Shape<1>::BN) * c.strips;
-    return 4 + c.kt / TILES * std::max(chunk == 128 ? 0.93 : 1.0, units / L->num_sms * (chunk == 128 ? 0.47 : 0.67));
+    return chunk == 128 ? int4_many_us_128(L, c) : chunk == 64 ? int4_many_us_64(L, c) : int4_many_us_32(L, c);
 }
 
 cudaError_t launch_int4_many(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
     const int chunk = chunk_of(L);
     Int4Call call = c;
     call.groups_are_chunks = L->d.group == chunk;
-    return chunk == 128 ? launch_mode<1>(L, call, s) : chunk == 64 ? launch_mode<2>(L, call, s) : launch_mode<4>(L, call, s);
+    return chunk == 128 ? launch_int4_many_128(L, call, s) : chunk == 64 ? launch_int4_many_64(L, call, s) : launch_int4_many_32(L, call, s);
 }
 
 }  // namespace moe
