@@ -84,6 +84,13 @@ __device__ __forceinline__ void put16(uint32_t dst, const uint4& v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// *p, or 0 without looking at it: a predicate, no branch, so that many such loads are in flight at once.
+__device__ __forceinline__ uint32_t load_if(const uint16_t* p, bool have) {
+    uint16_t v;
+    asm("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n mov.u16 %0, 0;\n @q ld.global.nc.u16 %0, [%1];\n}" : "=h"(v) : "l"(p), "r"((int)have));
+    return v;
+}
+
 // Eight channels of a row that starts on a 2-byte boundary, those from `have` on as zeros.  Words that
 // straddle the piece's ends are read as halves: nothing outside it is touched.
 __device__ __forceinline__ uint4 load8(const uint16_t* p, int have) {

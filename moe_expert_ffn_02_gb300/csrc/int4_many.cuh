@@ -256,8 +256,8 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
                 const uint16_t* p = c.x + (from < 0 ? 0 : from * c.ldx + k);
 #pragma unroll
                 for (int tile = 0; tile < TILES; ++tile) {
-                    const uint32_t lo = from >= 0 && k + tile * I4_K < c.K ? p[tile * I4_K] : 0u;
-                    const uint32_t hi = from >= 0 && k + tile * I4_K + 1 < c.K ? p[tile * I4_K + 1] : 0u;
+                    const uint32_t lo = i4::load_if(p + tile * I4_K, from >= 0 && k + tile * I4_K < c.K);
+                    const uint32_t hi = i4::load_if(p + tile * I4_K + 1, from >= 0 && k + tile * I4_K + 1 < c.K);
                     v[i][tile] = lo | hi << 16;
                 }
             }
