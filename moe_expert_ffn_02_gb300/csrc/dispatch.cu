@@ -261,10 +261,11 @@ cudaError_t launch_copy(DispatchCall& c, bool given, int row_bytes, cudaStream_t
 }
 
 // ---------------------------------------------------------------------------
-// Combine: a thread has 8 columns of one token (1 where rows are off the
-// 16-byte grid) and loads them from 8 rows at a time before it adds them up.
+// Combine: a thread has 8 columns of one token and loads them from 8 rows (fp32: 4) at a time before it adds
+// them up.  Rows off the 16-byte grid: four single columns, C_THREADS apart, of 8 rows.
 // ---------------------------------------------------------------------------
 constexpr int C_THREADS = 128;
+constexpr int c_parts(int n) { return n == 1 ? 4 : 1; }
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T v);
@@ -344,36 +345,46 @@ __global__ void __launch_bounds__(C_THREADS) combine_rows_kernel(const moe_combi
         wt[threadIdx.x] = a.w ? a.w[t * k + threadIdx.x] : 1.0f;
     }
     __syncthreads();
-    const int col = (blockIdx.x * C_THREADS + threadIdx.x) * N;
+    constexpr int C = c_parts(N), STEP = C_THREADS * N;      // parts of a thread, so many columns apart
+    const int col = (blockIdx.x * C * C_THREADS + threadIdx.x) * N;
     if (col >= a.cols) return;
     const TO* o = static_cast<const TO*>(a.o) + col;
-    float acc[N];
-    if (a.add) {
+    float acc[C][N];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
         Pack<TY, N> v;
-        v.load(static_cast<const TY*>(a.add) + t * a.ld_add + col);
+        const bool have = a.add && col + c * STEP < a.cols;
+        if (have) v.load(static_cast<const TY*>(a.add) + t * a.ld_add + col + c * STEP);
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = v.get(i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = 0.f;
+        for (int i = 0; i < N; ++i) acc[c][i] = have ? v.get(i) : 0.f;
     }
-    constexpr int J = sizeof(TO) == 2 ? 8 : 4;
+    constexpr int J = N == 1 || sizeof(TO) == 2 ? 8 : 4;
     for (int j0 = 0; j0 < k; j0 += J) {
-        Pack<TO, N> v[J];
+        Pack<TO, N> v[J][C];
 #pragma unroll
         for (int j = 0; j < J; ++j)
-            if (j0 + j < k && row[j0 + j] >= 0) v[j].load(o + row[j0 + j] * a.ldo);
+            if (j0 + j < k && row[j0 + j] >= 0) {
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (col + c * STEP < a.cols) v[j][c].load(o + row[j0 + j] * a.ldo + c * STEP);
+            }
 #pragma unroll
         for (int j = 0; j < J; ++j)
             if (j0 + j < k && row[j0 + j] >= 0) {
                 const float w = wt[j0 + j];
 #pragma unroll
-                for (int i = 0; i < N; ++i) acc[i] = __fmaf_rn(w, v[j].get(i), acc[i]);
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc[c][i] = __fmaf_rn(w, v[j][c].get(i), acc[c][i]);
             }
     }
-    Pack<TY, N> out;
-    put(out, acc);
-    out.store(static_cast<TY*>(a.y) + t * a.ldy + col);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        if (col + c * STEP < a.cols) {
+            Pack<TY, N> out;
+            put(out, acc[c]);
+            out.store(static_cast<TY*>(a.y) + t * a.ldy + col + c * STEP);
+        }
 }
 
 // ---------------------------------------------------------------------------
@@ -515,7 +526,7 @@ namespace {
 
 template <typename TO, typename TY>
 cudaError_t combine_typed(const moe_combine_args* a, bool vec, cudaStream_t s) {
-    const int cols = C_THREADS * (vec ? 8 : 1);
+    const int cols = C_THREADS * (vec ? 8 : c_parts(1));
     const dim3 grid((a->cols + cols - 1) / cols, std::min(a->tokens, 32768), (a->tokens - 1) / 32768 + 1);
     return vec ? launch_pdl(combine_rows_kernel<TO, TY, 8>, grid, dim3(C_THREADS), 0, s, *a)
                : launch_pdl(combine_rows_kernel<TO, TY, 1>, grid, dim3(C_THREADS), 0, s, *a);

@@ -91,26 +91,12 @@ __device__ __forceinline__ uint32_t load_if(const uint16_t* p, bool have) {
     return v;
 }
 
-// Eight channels of a row that starts on a 2-byte boundary, those from `have` on as zeros.  Words that
-// straddle the piece's ends are read as halves: nothing outside it is touched.
+// Eight channels of a row that starts on any 2-byte boundary, those from `have` on as zeros.
 __device__ __forceinline__ uint4 load8(const uint16_t* p, int have) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (have >= 8) {
-        if ((reinterpret_cast<uintptr_t>(p) & 2) == 0) {
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
-            v = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(p + 1);
-            const uint32_t a = p[0], b = w[0], c = w[1], d = w[2], e = p[7];
-            v = make_uint4(a | b << 16, __funnelshift_l(b, c, 16), __funnelshift_l(c, d, 16), d >> 16 | e << 16);
-        }
-    } else if (have > 0) {
-        uint32_t h[8];
+    uint32_t h[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = i < have ? p[i] : 0u;
-        v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-    }
-    return v;
+    for (int i = 0; i < 8; ++i) h[i] = load_if(p + i, i < have);
+    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
 }
 
 struct Unit {

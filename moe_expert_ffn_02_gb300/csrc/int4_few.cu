@@ -57,8 +57,8 @@ struct Smem {
     int table[1];                      // start[E + 1], first[E + 1]
 };
 
-// SUB: scales per tile and row (2 where a group may end inside a tile).
-template <int RB, int NB, int SUB, bool ZEROS, int DEPTH, int WARPS>
+// SUB: scales per tile and row (2 where a group may end inside a tile).  HAND: rows of x off the 16-byte grid.
+template <int RB, int NB, int SUB, bool ZEROS, bool HAND, int DEPTH, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32) int4_few_kernel(const Int4Call c) {
     constexpr int THREADS = WARPS * 32;
     using W = Slot<RB, NB, SUB, ZEROS>;
@@ -103,7 +103,25 @@ __global__ void __launch_bounds__(WARPS * 32) int4_few_kernel(const Int4Call c) 
             p_x[n] = c.x + (r < 0 ? 0 : r * c.ldx + t0 * I4_K + q * 8);
         }
     };
+    // Rows off the 16-byte grid cannot be copied asynchronously: they are loaded here and go into their slot when the
+    // next tile is copied, a tile's products later.
+    uint4 held[NB][2];
+    uint32_t held_at = 0, held_how = 0;          // held_how: bit n, nobody reads the lane's n-th row
+    auto put_held = [&]() {
+        if constexpr (HAND) {
+            if (!held_at) return;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                if (held_how & 1 << n) continue;
+                const uint32_t to = held_at + offsetof(W, x) + n * (8 * X_PITCH) + g * X_PITCH + q * 16;
+                i4::put16(to, held[n][0]);
+                i4::put16(to + 64, held[n][1]);
+            }
+            held_at = 0;
+        }
+    };
     auto copy = [&](bool weights, bool rows) {
+        if (rows) put_held();
         if (p_unit < units) {
             const int t = t0 + p_step;
             if (p_step == 0) {
@@ -127,10 +145,14 @@ __global__ void __launch_bounds__(WARPS * 32) int4_few_kernel(const Int4Call c) 
                 }
             }
             if (rows) {
-                const bool whole = (t + 1) * I4_K <= c.K && c.x_grid == 16;
+                held_how = 0;
+                const bool whole = !HAND && (t + 1) * I4_K <= c.K;
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    if (p_how[n] == NOBODY) continue;
+                    if (p_how[n] == NOBODY) {
+                        held_how |= 1 << n;
+                        continue;
+                    }
                     const uint32_t to = p_at + offsetof(W, x) + n * (8 * X_PITCH) + g * X_PITCH + q * 16;
                     if (whole && p_how[n] == READ) {
                         i4::copy16(to, p_x[n]);
@@ -139,13 +161,14 @@ __global__ void __launch_bounds__(WARPS * 32) int4_few_kernel(const Int4Call c) 
                         continue;
                     }
                     const int have = p_how[n] == ZERO ? 0 : c.K - t * I4_K - q * 8;      // channels from here on
-                    if (c.x_grid == 16) {
+                    if (!HAND) {
                         const int b0 = min(max(have, 0), 8) * 2, b1 = min(max(have - 32, 0), 8) * 2;
                         i4::copy16(to, b0 ? p_x[n] : c.x, b0);
                         i4::copy16(to + 64, b1 ? p_x[n] + 32 : c.x, b1);
                     } else {
-                        i4::put16(to, i4::load8(p_x[n], have));
-                        i4::put16(to + 64, i4::load8(p_x[n] + 32, have - 32));
+                        held[n][0] = i4::load8(p_x[n], have);
+                        held[n][1] = i4::load8(p_x[n] + 32, have - 32);
+                        held_at = p_at;
                     }
                     if (p_how[n] == READ) p_x[n] += I4_K;
                 }
@@ -269,11 +292,11 @@ __global__ void __launch_bounds__(WARPS * 32) int4_few_kernel(const Int4Call c) 
     i4::copy_wait<0>();
 }
 
-template <int RB, int NB, int SUB, bool ZEROS, int WARPS>
+template <int RB, int NB, int SUB, bool ZEROS, bool HAND>
 cudaError_t launch(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
-    constexpr int DEPTH = RB == 4 || NB == 4 ? 3 : 4;
+    constexpr int WARPS = 8, DEPTH = RB == 4 || NB == 4 ? 3 : 4;
     using S = Smem<RB, NB, SUB, ZEROS, DEPTH, WARPS>;
-    constexpr auto kernel = int4_few_kernel<RB, NB, SUB, ZEROS, DEPTH, WARPS>;
+    constexpr auto kernel = int4_few_kernel<RB, NB, SUB, ZEROS, HAND, DEPTH, WARPS>;
     const int bytes = sizeof(S) + 2 * (c.E + 1) * (int)sizeof(int);
     constexpr int most = sizeof(S) + 2 * (MOE_DISPATCH_MAX_EXPERTS + 1) * (int)sizeof(int);
     static_assert(most <= 227 * 1024 - 1024, "shared memory");
@@ -287,10 +310,10 @@ cudaError_t launch(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
     return launch_pdl(kernel, dim3((unsigned)grid), dim3(WARPS * 32), bytes, s, c);
 }
 
-template <int RB, int NB, int WARPS>
+template <int RB, int NB, bool HAND>
 cudaError_t launch_sub(const moe_int4* L, const Int4Call& c, cudaStream_t s) {
-    if (L->d.group % I4_K) return c.z ? launch<RB, NB, 2, true, WARPS>(L, c, s) : launch<RB, NB, 2, false, WARPS>(L, c, s);
-    return c.z ? launch<RB, NB, 1, true, WARPS>(L, c, s) : launch<RB, NB, 1, false, WARPS>(L, c, s);
+    if (L->d.group % I4_K) return c.z ? launch<RB, NB, 2, true, HAND>(L, c, s) : launch<RB, NB, 2, false, HAND>(L, c, s);
+    return c.z ? launch<RB, NB, 1, true, HAND>(L, c, s) : launch<RB, NB, 1, false, HAND>(L, c, s);
 }
 
 // One thread per lane's 16 bytes.
@@ -397,9 +420,11 @@ cudaError_t launch_int4_few(const moe_int4* L, const Int4Call& c, cudaStream_t s
     // 7168: 4.9 us with 2, 5.8 with 1, 6.1 with 4; 16 x 7168 x 2048 gated: 11.6 with 2, 13.3 with 1, 16.2 with 4).
     const int64_t blocks = (int64_t)c.blocks * (c.offsets ? std::min(c.E, c.rows) : 1);
     const int rb = blocks <= L->num_sms ? 1 : blocks <= 4 * L->num_sms ? 2 : 4;
-    if (groups == 1) return rb == 1 ? launch_sub<1, 1, 8>(L, c, s) : rb == 2 ? launch_sub<2, 1, 8>(L, c, s) : launch_sub<4, 1, 8>(L, c, s);
-    if (groups == 2) return rb == 1 ? launch_sub<1, 2, 8>(L, c, s) : rb == 2 ? launch_sub<2, 2, 8>(L, c, s) : launch_sub<4, 2, 8>(L, c, s);
-    return rb == 1 ? launch_sub<1, 4, 8>(L, c, s) : launch_sub<2, 4, 8>(L, c, s);
+    if (c.x_grid < 16)
+        return groups == 1 ? launch_sub<2, 1, true>(L, c, s) : groups == 2 ? launch_sub<2, 2, true>(L, c, s) : launch_sub<2, 4, true>(L, c, s);
+    if (groups == 1) return rb == 1 ? launch_sub<1, 1, false>(L, c, s) : rb == 2 ? launch_sub<2, 1, false>(L, c, s) : launch_sub<4, 1, false>(L, c, s);
+    if (groups == 2) return rb == 1 ? launch_sub<1, 2, false>(L, c, s) : rb == 2 ? launch_sub<2, 2, false>(L, c, s) : launch_sub<4, 2, false>(L, c, s);
+    return rb == 1 ? launch_sub<1, 4, false>(L, c, s) : launch_sub<2, 4, false>(L, c, s);
 }
 
 }  // namespace moe

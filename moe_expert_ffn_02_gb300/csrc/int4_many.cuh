@@ -33,20 +33,21 @@ namespace moe {
 
 namespace {
 
-constexpr int THREADS = 128;
+constexpr int SUM_WARPS = 4, COPY_WARPS = 4;     // COPY_WARPS: only where x is brought by hand
 constexpr int TILES = 2, STAGE_K = TILES * I4_K, STEPS = STAGE_K / 32;     // of 64 and of 32 channels
 constexpr int A_COLS = STAGE_K / 2;              // operand columns: two bf16 channels each
 constexpr int X_SLOTS = 2;                       // stages of x
 constexpr int MAX_SPLIT = 8;                     // CTAs of a cluster
 
 enum XMode { X_TILE, X_GATHER, X_COPY };
+__host__ __device__ constexpr int threads_of(XMode mode) { return (SUM_WARPS + (mode == X_COPY ? COPY_WARPS : 0)) * 32; }
 
 // Tensor memory: accumulators, then the operand.
 template <int CHUNKS>
 struct Shape {
     static constexpr int BN = CHUNKS == 4 ? 48 : 64;
     static constexpr int TMEM_COLS = CHUNKS == 1 ? 128 : 256;
-    static constexpr int CTAS = 512 / TMEM_COLS;             // per SM
+    static constexpr int CTAS = 512 / TMEM_COLS;             // per SM (with x by hand two: registers)
     static constexpr int CODE_SLOTS = CHUNKS == 1 ? 2 : 4;   // stages of codes
     static constexpr int SCALE_SLOTS = 2 * CODE_SLOTS;       // of scales, which are read after the codes' slot is filled anew
     static constexpr int BOX = BN % 32 ? 16 : 32;            // rows of x that one copy brings
@@ -148,8 +149,9 @@ __device__ __forceinline__ uint32_t in_peer(uint32_t addr, uint32_t rank) {
 }
 
 template <int CHUNKS, XMode MODE, bool ZEROS, bool GATED, bool SPLIT>
-__global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel(const __grid_constant__ CUtensorMap x_map, const Int4Call c) {
+__global__ void __launch_bounds__(threads_of(MODE), MODE == X_COPY ? 2 : Shape<CHUNKS>::CTAS) int4_many_kernel(const __grid_constant__ CUtensorMap x_map, const Int4Call c) {
     using Sh = Shape<CHUNKS>;
+    constexpr int THREADS = threads_of(MODE);
     constexpr int BN = Sh::BN, CODE_SLOTS = Sh::CODE_SLOTS, SCALE_SLOTS = Sh::SCALE_SLOTS, CHUNK_STEPS = STEPS / CHUNKS;
     constexpr uint32_t TILE_BYTES = BN * 128, A_AT = CHUNKS * BN;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -181,8 +183,8 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
         return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, c.wait_limit, c.status, nullptr));
     };
 
-    // ---- Copies.  Warp 3 requests codes, scales and zero points, warp 1 rows of x (MODE X_COPY: all warps bring them,
-    // stage by stage); both are ahead of the sums by as many stages as there are slots.
+    // ---- Copies.  Warp 3 requests codes, scales and zero points, warp 1 rows of x; both are ahead of the sums by as
+    // many stages as there are slots.  (MODE X_COPY: four warps bring x, one stage ahead, and do nothing else.)
     int p_unit = stages ? cluster : units, p_stage = 0;
     uint32_t p_n = 0;
     size_t p_strip = 0;
@@ -248,11 +250,11 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
         constexpr int BATCH = 8;
         const int k = (stage0 + st) * STAGE_K + lane * 2;
 #pragma unroll 1
-        for (int r0 = warp; r0 < un.count; r0 += BATCH * (THREADS / 32)) {
+        for (int r0 = warp - SUM_WARPS; r0 < un.count; r0 += BATCH * COPY_WARPS) {
             uint32_t v[BATCH][TILES];
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
-                const int r = r0 + i * (THREADS / 32), from = r < un.count ? i4::source_row(c, un.row0 + r) : -1;
+                const int r = r0 + i * COPY_WARPS, from = r < un.count ? i4::source_row(c, un.row0 + r) : -1;
                 const uint16_t* p = c.x + (from < 0 ? 0 : from * c.ldx + k);
 #pragma unroll
                 for (int tile = 0; tile < TILES; ++tile) {
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
             }
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
-                const int r = r0 + i * (THREADS / 32);
+                const int r = r0 + i * COPY_WARPS;
                 if (r >= un.count) break;
 #pragma unroll
                 for (int tile = 0; tile < TILES; ++tile)
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
         fence_async_proxy();
         __syncwarp();
     };
-    const bool copies_codes = warp == 3, copies_x = MODE != X_COPY && warp == 1;
+    const bool copies_codes = warp == 3, copies_x = MODE != X_COPY && warp == 1, sums = MODE != X_COPY || warp < SUM_WARPS;
     if (p_unit < units) enter();
     // The weights do not depend on the preceding kernel: the first of them are requested before the wait for it.
     if (copies_codes)
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
     bool ok = true, pending = false;             // pending: MMAs that nobody has seen complete
     i4::Unit un = {};
     if (cluster < units) un = i4::unit_at(c, cluster, c.strips, BN, start, first);
-    if (MODE == X_COPY && cluster < units && stages) copy_x_by_hand(un, 0, sm.x[0][0]);
+    if (!sums && cluster < units && stages) copy_x_by_hand(un, 0, sm.x[0][0]);
     for (int u = cluster; u < units; u += clusters) {
         i4::Unit next = un;
         if (u + clusters < units) next = i4::unit_at(c, u + clusters, c.strips, BN, start, first);
@@ -304,26 +306,28 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
         for (int i = 0; i < BN / 2; ++i) acc[i] = 0;
         for (int st = 0; st < stages; ++st, ++n) {
             const uint32_t slot = n % CODE_SLOTS;
-            ok = ok && wait(&sm.code_full[slot], n / CODE_SLOTS & 1u);
+            if (sums) {
+                ok = ok && wait(&sm.code_full[slot], n / CODE_SLOTS & 1u);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {        // the warp's blocks: 16 lanes of tensor memory each
-                const int block = 2 * warp + i;
+                for (int i = 0; i < 2; ++i) {        // the warp's blocks: 16 lanes of tensor memory each
+                    const int block = 2 * warp + i;
 #pragma unroll
-                for (int tile = 0; tile < TILES; ++tile) {
-                    uint32_t r[16], v[4];
-                    const uint4 code = sm.codes[slot][tile][block][lane];
+                    for (int tile = 0; tile < TILES; ++tile) {
+                        uint32_t r[16], v[4];
+                        const uint4 code = sm.codes[slot][tile][block][lane];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t z = ZEROS ? sm.zeros[slot][(tile * 2 + half) / CHUNK_STEPS][block][g] : I4_ZERO;
-                        i4::widen(half ? code.y : code.x, ZEROS ? __byte_perm(z, 0, 0x1010) : z, v);
-                        r[8 * half] = v[0], r[8 * half + 1] = v[1], r[8 * half + 4] = v[2], r[8 * half + 5] = v[3];
-                        i4::widen(half ? code.w : code.z, ZEROS ? __byte_perm(z, 0, 0x3232) : z, v);
-                        r[8 * half + 2] = v[0], r[8 * half + 3] = v[1], r[8 * half + 6] = v[2], r[8 * half + 7] = v[3];
+                        for (int half = 0; half < 2; ++half) {
+                            const uint32_t z = ZEROS ? sm.zeros[slot][(tile * 2 + half) / CHUNK_STEPS][block][g] : I4_ZERO;
+                            i4::widen(half ? code.y : code.x, ZEROS ? __byte_perm(z, 0, 0x1010) : z, v);
+                            r[8 * half] = v[0], r[8 * half + 1] = v[1], r[8 * half + 4] = v[2], r[8 * half + 5] = v[3];
+                            i4::widen(half ? code.w : code.z, ZEROS ? __byte_perm(z, 0, 0x3232) : z, v);
+                            r[8 * half + 2] = v[0], r[8 * half + 3] = v[1], r[8 * half + 6] = v[2], r[8 * half + 7] = v[3];
+                        }
+                        tmem_st_16x32(lanes + ((uint32_t)(i * 16) << 16) + A_AT + tile * (A_COLS / TILES), r);
                     }
-                    tmem_st_16x32(lanes + ((uint32_t)(i * 16) << 16) + A_AT + tile * (A_COLS / TILES), r);
                 }
+                tmem_wait_st();
             }
-            tmem_wait_st();
             tc::tc_fence_before();
             // all of the operand is there, and everybody has read the accumulators; a wait that gave up ends it for all
             ok = !__syncthreads_or(!ok);
@@ -343,9 +347,12 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
                 }
             }
             if (copies_codes) copy_codes();
-            // by hand the next stage's x, while the MMAs of this one run
-            if (MODE == X_COPY && (st + 1 < stages || u + clusters < units))
-                copy_x_by_hand(st + 1 < stages ? un : next, st + 1 < stages ? st + 1 : 0, sm.x[(n + 1) % X_SLOTS][0]);
+            if (!sums) {
+                // the next stage's x; the MMAs that read its slot were waited for before the barrier
+                if (st + 1 < stages || u + clusters < units)
+                    copy_x_by_hand(st + 1 < stages ? un : next, st + 1 < stages ? st + 1 : 0, sm.x[(n + 1) % X_SLOTS][0]);
+                continue;
+            }
             uint64_t sc[CHUNKS];
 #pragma unroll
             for (int j = 0; j < CHUNKS; ++j) {
@@ -389,6 +396,7 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
             cluster_sync();
             const int pairs = BN / 2 / split;
             const uint32_t in = smem_addr(sm.x), mine = in + (rank * pairs * 128 + row) * 8;
+            if (sums)
 #pragma unroll
             for (int i = 0; i < BN / 2; ++i) {
                 const int to = i / pairs;
@@ -399,8 +407,8 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
             cluster_sync();
             bool fine = true;
             for (int r = 0; r < split; ++r) fine &= !sm.peer_failed[r];
-            if (!fine) break;
-            const uint64_t* sums = reinterpret_cast<const uint64_t*>(sm.x) + row;
+            if (!fine || !sums) break;
+            const uint64_t* came = reinterpret_cast<const uint64_t*>(sm.x) + row;
             auto store = [&](auto* y) {
 #pragma unroll 1
                 for (int i = 0; i < pairs; ++i) {
@@ -408,7 +416,7 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
                     if (m >= un.count) break;
                     float even = 0.f, odd = 0.f;
                     for (int r = 0; r < split; ++r) {
-                        const uint64_t v = sums[(r * pairs + i) * 128];
+                        const uint64_t v = came[(r * pairs + i) * 128];
                         even += __uint_as_float((uint32_t)v);
                         odd += __uint_as_float((uint32_t)(v >> 32));
                     }
@@ -420,6 +428,10 @@ __global__ void __launch_bounds__(THREADS, Shape<CHUNKS>::CTAS) int4_many_kernel
             break;
         }
         if (!ok) break;
+        if (!sums) {
+            un = next;
+            continue;
+        }
         auto store = [&](auto* y) {
             auto* at = y + (un.row0 + (GATED ? upper : 0)) * c.ldy + n0;
 #pragma unroll
@@ -459,7 +471,7 @@ int64_t most_units(const Int4Call& c) {
 template <int CHUNKS>
 int split_of(const moe_int4* L, const Int4Call& c, double units) {
     int split = 1;
-    while (split < MAX_SPLIT && units * split * 2 <= (double)L->num_sms * Shape<CHUNKS>::CTAS && c.kt / TILES >= 4 * split) split *= 2;
+    while (split < MAX_SPLIT && units * split * 2 <= (double)L->num_sms * (c.x_grid < 16 ? 2 : Shape<CHUNKS>::CTAS) && c.kt / TILES >= 4 * split) split *= 2;
     return split;
 }
 
@@ -471,7 +483,7 @@ cudaError_t launch(const moe_int4* L, const Int4Call& c, const CUtensorMap& map,
     constexpr int most = fixed + 2 * (MOE_DISPATCH_MAX_EXPERTS + 1) * (int)sizeof(int);
     cudaError_t e = ensure_smem_limit<kernel>(most);
     if (e != cudaSuccess) return e;
-    const int64_t units = most_units<CHUNKS>(c), room = (int64_t)L->num_sms * Sh::CTAS;
+    const int64_t units = most_units<CHUNKS>(c), room = (int64_t)L->num_sms * (MODE == X_COPY ? 2 : Sh::CTAS);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -479,7 +491,7 @@ cudaError_t launch(const moe_int4* L, const Int4Call& c, const CUtensorMap& map,
     attr[1].val.clusterDim = {(unsigned)split, 1, 1};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(split > 1 ? units * split : std::min(units, room)));
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(threads_of(MODE));
     cfg.dynamicSmemBytes = fixed + 2 * (c.E + 1) * (int)sizeof(int);
     cfg.stream = s;
     cfg.attrs = attr;
