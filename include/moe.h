@@ -467,7 +467,8 @@ moe_status moe_linear_debug_timeout(moe_linear* linear);
 /* ids given: sorts the pairs and writes expert_offsets, sorted_token (-1 past
  * the last row) and inv_row (-1: no row).  ids NULL: inv_row is an input and
  * the other two are not used.  x given: rows[inv_row[t][j]] = x[t] for every
- * pair that has a row; rows behind the last stay as they were.  A row from
+ * pair that has a row; rows behind the last stay as they were, and rows must not
+ * overlap x.  A row from
  * n_rows on (and, with ids NULL, one below -1) sets MOE_DEV_BAD_ROW and is not
  * written.  Workspace (256-byte aligned): moe_dispatch_workspace_bytes, which
  * does not fall as tokens grows; small batches need none. */
@@ -579,6 +580,11 @@ moe_status moe_int4_forward(moe_int4* weights, const moe_int4_args* args, void* 
  * a call whose wait expired, an element of y is right or as it was. */
 moe_status moe_int4_device_status(moe_int4* weights, void* stream, uint32_t* flags);
 moe_status moe_int4_set_wait_limit(moe_int4* weights, uint32_t microseconds);
+
+/* Test hook: in the next forward call of these weights that takes the form for
+ * many rows (the other has no such waits) the first thread block leaves out the
+ * products of its first stage, so that the wait for them expires. */
+moe_status moe_int4_debug_timeout(moe_int4* weights);
 
 const char* moe_status_string(moe_status s);
 const char* moe_last_error(void);   /* thread-local; "" when none */

@@ -32,7 +32,7 @@ __all__ = [
     "MoeDispatchArgs", "MoeCombineArgs", "MoeCombineGradArgs", "moe_dispatch_workspace_bytes", "moe_dispatch", "moe_combine",
     "moe_combine_grad", "moe_dispatch_device_status", "ExpertPlan",
     "MoeInt4Desc", "MoeInt4Weights", "MoeInt4Args", "moe_int4_create", "moe_int4_destroy", "moe_int4_forward",
-    "moe_int4_device_status", "moe_int4_set_wait_limit", "Int4Linear", "Int4GatedLinear", "Int4ExpertFfn",
+    "moe_int4_device_status", "moe_int4_set_wait_limit", "moe_int4_debug_timeout", "Int4Linear", "Int4GatedLinear", "Int4ExpertFfn",
 ]
 
 MODE_ROUTE, MODE_PREFILL, MODE_DECODE = 0, 1, 2
@@ -193,6 +193,7 @@ def load(build_if_missing: bool = False):
             "moe_int4_forward": ([vp, ctypes.POINTER(MoeInt4Args), vp], st),
             "moe_int4_device_status": ([vp, vp, ctypes.POINTER(u32)], st),
             "moe_int4_set_wait_limit": ([vp, u32], st),
+            "moe_int4_debug_timeout": ([vp], st),
             "moe_status_string": ([st], ctypes.c_char_p),
             "moe_last_error": ([], ctypes.c_char_p),
             "moe_abi_version": ([], i32),
@@ -484,6 +485,11 @@ def moe_int4_device_status(weights: int, stream: int = 0):
 
 def moe_int4_set_wait_limit(weights: int, microseconds: int) -> None:
     _check(load().moe_int4_set_wait_limit(weights, microseconds))
+
+
+def moe_int4_debug_timeout(weights: int) -> None:
+    """In the next forward call of these weights with many rows the wait for the products of one stage expires."""
+    _check(load().moe_int4_debug_timeout(weights))
 
 
 # ---------------------------------------------------------------- torch convenience
@@ -941,8 +947,9 @@ class ExpertPlan:
     (device_status).
 
     The buffers serve batches of up to `tokens` tokens, are never remade and
-    belong to one stream at a time: a captured graph goes on using them, and
-    two graphs that may run side by side need a plan each."""
+    belong to one stream at a time: a captured graph goes on using them (and
+    needs the plan as long as it is replayed), and two graphs that may run side
+    by side need a plan each."""
 
     def __init__(self, tokens: int, top_k: int, n_experts: int, first_expert: int = 0, device=None):
         import torch
@@ -964,7 +971,20 @@ class ExpertPlan:
         self._dispatch = _packed_call("moe_dispatch", [vp, ctypes.c_size_t, vp])
         self._combine = _packed_call("moe_combine", [vp])
         self._grad = _packed_call("moe_combine_grad", [vp])
+        self._streams = {}
         self._bind(0)
+
+    def _stream(self):
+        """The current stream; seen for the first time, it is recorded with torch's allocator, so that dropping the plan
+        while its kernels are queued is safe."""
+        handle = _stream(self._dev)
+        if handle not in self._streams:
+            import torch
+            stream = torch.cuda.current_stream(self._dev)
+            for t in (self._ws, self.expert_offsets, self._token, self._inv):
+                t.record_stream(stream)
+            self._streams[handle] = True
+        return handle
 
     def _bind(self, tokens):
         self.tokens = tokens
@@ -981,11 +1001,18 @@ class ExpertPlan:
 
     def _matrix(self, t, what, cols=None, rows=None):
         """Type, pointer, row stride and shape of a matrix operand."""
-        kind = self._types.get(t.dtype)
-        if kind is None or t.dim() != 2:
+        kind, shape = self._types.get(t.dtype), t.shape
+        if kind is None or len(shape) != 2:
             _bad(f"{what} must be bfloat16 or float32 with two dimensions")
-        n, c = t.shape
-        return kind, t.data_ptr(), _rows_of(t, n if rows is None else rows, c if cols is None else cols, self._dev, what), n, c
+        n, c = shape
+        if (rows is not None and n != rows) or (cols is not None and c != cols):
+            _bad(f"{what} must be [{n if rows is None else rows}][{c if cols is None else cols}], not {list(shape)}")
+        if t.get_device() != self._dev:
+            _bad(f"{what} must be on CUDA device {self._dev}")
+        ld, inner = t.stride()
+        if inner != 1 and c > 1:
+            _bad(f"{what} must have contiguous rows")
+        return kind, t.data_ptr(), ld if n > 1 or ld >= c else c, n, c
 
     def _weight(self, w, what):
         if w.dtype is not self._f32 or w.shape != (self.tokens, self.top_k) or not w.is_contiguous() or w.get_device() != self._dev:
@@ -1010,7 +1037,7 @@ class ExpertPlan:
         elif rows is not None or ids is None:
             _bad("x is missing")
         o, tok, inv = self._ptrs
-        stream = _stream(self._dev)
+        stream = self._stream()
         # a tensor without elements has no address: with no tokens nothing is read there
         ip = 0 if ids is None else ids.data_ptr() or o
         st = self._dispatch(_DISPATCH_ARGS.pack(t, self.top_k, self.n_experts, self.first_expert, ip, o, tok, inv,
@@ -1032,7 +1059,7 @@ class ExpertPlan:
                 _bad("add must have y's type")
         wp = 0 if w is None else self._weight(w, "w")
         st = self._combine(_COMBINE_ARGS.pack(self.tokens, self.top_k, cols, n_rows, okind, ykind, self._ptrs[2], wp, op, ldo,
-                                              ap, lda, yp, ldy), _stream(self._dev))
+                                              ap, lda, yp, ldy), self._stream())
         if st != MOE_OK:
             _check(st)
         return y
@@ -1055,7 +1082,7 @@ class ExpertPlan:
         wp = 0 if w is None else self._weight(w, "w")
         dwp = 0 if d_w is None else self._weight(d_w, "d_w")
         st = self._grad(_COMBINE_GRAD_ARGS.pack(self.tokens, self.top_k, cols, n_rows, okind, ykind, self._ptrs[2], wp, gp, ldg,
-                                                op, ldo, dp, ldd, dwp), _stream(self._dev))
+                                                op, ldo, dp, ldd, dwp), self._stream())
         if st != MOE_OK:
             _check(st)
 
@@ -1199,8 +1226,8 @@ class Int4ExpertFfn:
         """The current stream, seen for the first time (or since the last buffers were made), uses all of them."""
         import torch
         stream = torch.cuda.current_stream(self.down._dev)
-        for plan, *mats in self._store.values():
-            for t in (plan._ws, plan.expert_offsets, plan._token, plan._inv, *mats):
+        for _, *mats in self._store.values():        # the plans record theirs
+            for t in mats:
                 t.record_stream(stream)
         self._streams[handle] = True
 

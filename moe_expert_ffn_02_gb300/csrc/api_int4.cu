@@ -141,6 +141,7 @@ MOE_EXPORT moe_status moe_int4_forward(moe_int4* L, const moe_int4_args* a, void
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int groups = 0;
     const bool many = moe::int4_many_us(L, c) < moe::int4_few_us(L, c, &groups);
+    c.plant = many && L->plant.load(std::memory_order_relaxed) && L->plant.exchange(false);     // threads may share the weights
     cudaError_t e = many ? moe::launch_int4_many(L, c, s) : moe::launch_int4_few(L, c, s);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "4-bit product");
 }
@@ -154,5 +155,11 @@ MOE_EXPORT moe_status moe_int4_set_wait_limit(moe_int4* L, uint32_t microseconds
     if (!L) return fail(MOE_ERR_INVALID_ARG, "weights is NULL");
     if (microseconds == 0) return fail(MOE_ERR_INVALID_ARG, "limit must be positive");
     L->wait_limit = microseconds;
+    return MOE_OK;
+}
+
+MOE_EXPORT moe_status moe_int4_debug_timeout(moe_int4* L) {
+    if (!L) return fail(MOE_ERR_INVALID_ARG, "weights is NULL");
+    L->plant = true;
     return MOE_OK;
 }

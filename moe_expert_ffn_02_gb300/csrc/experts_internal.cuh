@@ -34,6 +34,7 @@ struct moe_int4 {
     uint32_t* z;           // [expert][strip][groups][8][8] pairs of bf16, or NULL: 136
     uint32_t* dev_status;  // device status word
     uint32_t wait_limit;
+    std::atomic<bool> plant;  // moe_int4_debug_timeout, for the next call of the form for many rows
 };
 
 namespace moe {
@@ -58,6 +59,7 @@ struct Int4Call {
     int rows, x_rows;
     int N, K, E, blocks, strips, kt, groups;
     uint32_t wait_limit;
+    bool plant;            // the first CTA issues no MMAs in its first stage
     bool s_f32, y_f32, gated;
     bool groups_are_chunks;    // many rows: a group is what one accumulator sums up
     int x_grid;            // 16, 8 or 2: the bytes whose multiples all rows of x start on

@@ -276,15 +276,18 @@ __global__ void __launch_bounds__(threads_of(MODE), MODE == X_COPY ? 2 : Shape<C
         __syncwarp();
     };
     const bool copies_codes = warp == 3, copies_x = MODE != X_COPY && warp == 1, sums = MODE != X_COPY || warp < SUM_WARPS;
-    if (p_unit < units) enter();
     // The weights do not depend on the preceding kernel: the first of them are requested before the wait for it.
-    if (copies_codes)
+    if (copies_codes && p_unit < units) {
+        enter();
 #pragma unroll 1
         for (int i = 0; i < CODE_SLOTS; ++i) copy_codes();
+    }
     if (!c.offsets) pdl_wait();
-    if (copies_x)
+    if (copies_x && p_unit < units) {
+        enter();
 #pragma unroll 1
         for (int i = 0; i < X_SLOTS; ++i) copy_x();
+    }
 
     // ---- Sums.
     const int row = warp * 32 + lane, row_block = row >> 4, row_g = row & 7, upper = (row >> 3) & 1;
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(threads_of(MODE), MODE == X_COPY ? 2 : Shape<C
     const uint32_t s_bytes = c.s_f32 ? 0x3210u : upper ? 0x3244u : 0x1044u;
     const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
     uint32_t n = 0;
-    bool ok = true, pending = false;             // pending: MMAs that nobody has seen complete
+    bool ok = true, pending = false, freed = false;          // pending: MMAs that nobody has seen complete
     i4::Unit un = {};
     if (cluster < units) un = i4::unit_at(c, cluster, c.strips, BN, start, first);
     if (!sums && cluster < units && stages) copy_x_by_hand(un, 0, sm.x[0][0]);
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(threads_of(MODE), MODE == X_COPY ? 2 : Shape<C
             tc::tc_fence_after();
             if (warp == 2) {
                 ok = MODE == X_COPY || wait(&sm.x_full[n % X_SLOTS], n / X_SLOTS & 1u);
-                if (ok) {
+                if (ok && !(c.plant && blockIdx.x == 0 && n == 0)) {
                     const uint32_t el = elect_one(), b = (uint32_t)tc::sw128_desc(smem_addr(sm.x[n % X_SLOTS][0]));
 #pragma unroll
                     for (int i = 0; i < STEPS; ++i)
@@ -391,6 +394,17 @@ __global__ void __launch_bounds__(threads_of(MODE), MODE == X_COPY ? 2 : Shape<C
             }
         };
         if (SPLIT) {
+            // Tensor memory goes back before anything is waited for that a peer does: a peer may be waiting for tensor
+            // memory itself.
+            if (!ok && pending) {
+                mbar_wait_bounded(&sm.done, n & 1u, LANDING_LIMIT_US, c.status, nullptr);
+                pending = false;
+            }
+            tc::tc_fence_before();
+            __syncthreads();
+            tc::tc_fence_after();
+            if (warp == 0) tc::tmem_dealloc(tmem, Sh::TMEM_COLS);
+            freed = true;
             // every CTA's operands have been read: where x was, the peers' sums of this CTA's columns come in,
             // [rank][two columns][row]
             cluster_sync();
@@ -457,7 +471,7 @@ __global__ void __launch_bounds__(threads_of(MODE), MODE == X_COPY ? 2 : Shape<C
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    if (warp == 0) tc::tmem_dealloc(tmem, Sh::TMEM_COLS);
+    if (warp == 0 && !freed) tc::tmem_dealloc(tmem, Sh::TMEM_COLS);
 }
 
 // No call has more units; with offsets no more row tiles than full ones and one for each expert.

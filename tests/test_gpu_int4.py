@@ -109,6 +109,20 @@ def test_strides(moe, m, xpad, ypad):
     check(y, *expect(x2, mats))
 
 
+@pytest.mark.parametrize("m,n,k,group", [(70, 300, 4096, 128), (129, 1000, 2100, 64), (65, 64, 7000, 32), (1000, 4096, 1024, 128), (3000, 520, 640, 32),
+                                         (90, 7168, 4096, 128), (250, 2100, 4096, 64), (250, 2100, 4104, 32), (2000, 1000, 520, 64), (400, 2048, 4096, 96)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_many_rows(moe, m, n, k, group, gated):
+    """Tiles that 2, 4 or 8 CTAs share, several tiles per CTA, all three sizes of chunk."""
+    lin, mats = make(moe, (), n, k, gated, group, True, "bf16")
+    x = (torch.randn(m, k, generator=gen(5), device="cuda") * 0.05).bfloat16()
+    for yt in ("bf16", "f32"):
+        y = torch.full((m, n), 7.0, dtype=DT[yt], device="cuda")
+        lin(x, y)
+        check(y, *expect(x, mats))
+    assert lin.device_status() == (0, 0)
+
+
 def offsets_of(counts, start=0):
     return torch.tensor([start, *(start + torch.tensor(counts).cumsum(0)).tolist()], dtype=torch.int32, device="cuda")
 
@@ -221,6 +235,53 @@ def test_same_bits_each_time_and_captured(moe, m):
     x.copy_(torch.randn(m, k, generator=gen(2), device="cuda"))
     graph.replay()
     check(again, *expect(x, mats))
+
+
+@pytest.mark.parametrize("m,n,k", [(600, 2048, 2048), (1500, 7168, 256), (600, 2048, 2047), (600, 7168, 256)])
+def test_a_wait_that_expires_leaves_the_output_right_or_as_it_was(moe, m, n, k):
+    """Tiles that clusters share, tiles that they do not, rows off the 16-byte grid."""
+    lin, mats = make(moe, (), n, k, False, 128, False, "bf16")
+    x = torch.randn(m, k, generator=gen(1), device="cuda").bfloat16()
+    y = torch.full((m, n), 7.0, device="cuda")
+    want, slack = expect(x, mats)
+    moe.moe_int4_set_wait_limit(lin.handle, 2000)
+    moe.moe_int4_debug_timeout(lin.handle)
+    lin(x, y)
+    assert lin.device_status() == (6, moe.DEV_WAIT_TIMEOUT)
+    kept = y == 7
+    assert kept.any() and not kept.all()
+    assert (((y.double() - want).abs() <= slack + want.abs() * U * 1.01) | kept).all()
+    moe.moe_int4_set_wait_limit(lin.handle, 2_000_000)
+    lin(x, y)
+    check(y, want, slack)
+    assert lin.device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("m,n,k", [(100, 256, 1024), (100, 256, 1001)])
+def test_the_form_without_waits_leaves_the_hook_alone(moe, m, n, k):
+    lin, mats = make(moe, (), n, k, False, 128, False, "bf16")
+    x = torch.randn(m, k, generator=gen(1), device="cuda").bfloat16()
+    y = torch.full((m, n), 7.0, device="cuda")
+    moe.moe_int4_debug_timeout(lin.handle)
+    lin(x, y)
+    check(y, *expect(x, mats))
+    assert lin.device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("m", [2, 40, 300])
+@pytest.mark.parametrize("k", [64, 320, 1024])
+def test_largest_zero_points_and_scales_of_every_size(moe, m, k):
+    """Zero points of 127 and scales from 2^-120 to 2^100: products and scaled sums in fp32's range stay exact to the bound."""
+    n, group = 48, 64
+    q = torch.randint(0, 256, (n, k // 2), generator=gen(1), device="cuda", dtype=torch.uint8)
+    s = torch.exp2(torch.linspace(-120, 100, n, device="cuda").round())[:, None].expand(n, k // group).contiguous()
+    z = torch.full((n, k // group), 127, dtype=torch.uint8, device="cuda")
+    lin = moe.Int4Linear(q, s, z, group=group)
+    code = torch.stack((q & 15, q >> 4), -1).flatten(1).double()
+    x = torch.randn(m, k, generator=gen(2), device="cuda").bfloat16()
+    y = torch.empty(m, n, device="cuda")
+    lin(x, y)
+    check(y, *expect(x, [(code - 127) * s[:, :1].double()]))
 
 
 def test_no_rows(moe):

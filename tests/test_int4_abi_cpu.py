@@ -37,3 +37,4 @@ def test_null(lib):
     assert lib.moe_int4_destroy(None) == 1
     assert lib.moe_int4_device_status(None, None, None) == 1
     assert lib.moe_int4_set_wait_limit(None, 1000) == 1
+    assert lib.moe_int4_debug_timeout(None) == 1
