@@ -15,6 +15,9 @@
 // CTA share its input channels, so that each reads its own part of x and of
 // the weights; their sums meet in shared memory in the order of the warps.
 // CTAs are persistent; the ring is filled for the next unit while one ends.
+//
+// Bound: issue slots, about 97 instructions per 1024 codes (44 of them widening, 8 products).  16 tokens x 8 of
+// 256 experts, 7168 x 2048 gated, groups of 32: 356 us, 4.7 TB/s; 1 x 2048 x 7168: 4.7 us, most of it latency.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
