@@ -564,7 +564,8 @@ moe_status moe_int4_create(const moe_int4_desc* desc, const moe_int4_weights* w,
 moe_status moe_int4_destroy(moe_int4* weights);      /* synchronises the device first */
 
 /* Offsets that fall or leave [0, rows] and tokens outside [0, x_rows) set
- * MOE_DEV_BAD_ROW and are cut off (such a token reads as zeros).  y must not
+ * MOE_DEV_BAD_ROW; offsets are cut to [0, rows] and one that falls to the
+ * largest before it, and such a token reads as zeros.  y must not
  * overlap x.  rows = 0 is a valid no-op. */
 typedef struct {
     int32_t rows, x_rows;        /* of y and of x (the same without token)      */

@@ -40,7 +40,7 @@ __device__ __forceinline__ int group_of(const Int4Call& c, int step32) {
 }
 
 // Row tiles per expert as prefix sums: start[e] row tiles of `tile_rows` rows lie before expert e's, whose
-// first row is first[e].  Offsets are cut to [0, rows] and to rising ones.  Called by the whole CTA; without
+// first row is first[e].  Offsets are cut to [0, rows], and one that falls to the largest before it.  Called by the whole CTA; without
 // offsets there is nothing to make.
 template <int THREADS>
 __device__ void row_tiles(const Int4Call& c, int tile_rows, int* start, int* first) {
@@ -69,7 +69,24 @@ __device__ void row_tiles(const Int4Call& c, int tile_rows, int* start, int* fir
         if (lane >= off) incl += o;
     }
     if (lane == 31) sums[warp] = incl;
-    __syncthreads();
+    // Offsets that were cut or fall: one thread makes them rise, so that no row has two experts and there are never
+    // more tiles than rows / tile_rows + E, the number that grids and 32-bit counts are made for.
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) {
+            int at = 0, low = first[0];
+            for (int e = 0; e < c.E; ++e) {
+                const int next = max(low, first[e + 1]);
+                start[e] = at;
+                at += (next - low + tile_rows - 1) / tile_rows;
+                first[e] = low;
+                low = next;
+            }
+            start[c.E] = at;
+            first[c.E] = low;
+        }
+        __syncthreads();
+        return;
+    }
     int at = incl - mine;
     for (int i = 0; i < warp; ++i) at += sums[i];
     for (int e = e0; e < e1; ++e) {

@@ -203,6 +203,31 @@ def test_bad_offsets_and_tokens_stay_in_bounds_and_are_flagged(moe, rows):
     check(y[:1], *expect(x[:1], [mats[0][0]]))
 
 
+@pytest.mark.parametrize("rows", [4, 300, 3000])
+@pytest.mark.parametrize("gather", [False, True])
+def test_falling_offsets_give_each_row_one_expert(moe, rows, gather):
+    n, k = 64, 128
+    r = rows
+    for off in ([0, r, 0, r, 1, r, r], [2, 0, 3, 1, r - 1, r, 3], [r, 0, r, 0, r, 0, r], [r + 5, 1, 2, 3, 4, 5, 6], [0, r // 2, r // 4, r, -7, r, 2 * r],
+                [0] + [r, 0] * 400):
+        e = len(off) - 1
+        lin, mats = make(moe, (e,), n, k, False, 128, False, "bf16")
+        x = torch.randn(r, k, generator=gen(1), device="cuda").bfloat16()
+        token = torch.randperm(r, generator=gen(2), device="cuda").int() if gather else None
+        y = torch.full((r, n), 7.0, device="cuda")
+        lin(x, y, torch.tensor(off, dtype=torch.int32, device="cuda"), token)
+        assert lin.device_status() == (5, moe.DEV_BAD_ROW)
+        low, left = min(max(off[0], 0), r), torch.ones(r, dtype=torch.bool)
+        for i in range(e):
+            high = max(low, min(max(off[i + 1], 0), r))
+            if high > low:
+                xi = x[low:high] if token is None else x[token[low:high].long()]
+                check(y[low:high], *expect(xi, [m[i] for m in mats]))
+                left[low:high] = False
+            low = high
+        assert (y[left.cuda()] == 7).all()
+
+
 @pytest.mark.parametrize("m", [3, 100])
 def test_nan_and_infinity_stay_in_their_row(moe, m):
     n, k = 80, 200
