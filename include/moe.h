@@ -462,6 +462,7 @@ moe_status moe_linear_debug_timeout(moe_linear* linear);
  * CUDA graph. */
 #define MOE_DISPATCH_MAX_TOPK 32
 #define MOE_DISPATCH_MAX_EXPERTS 1024
+#define MOE_DISPATCH_MAX_PAIRS 0x7FFF0000    /* tokens * top_k */
 #define MOE_DISPATCH_MAX_COLS (1 << 20)
 
 /* ids given: sorts the pairs and writes expert_offsets, sorted_token (-1 past
@@ -539,8 +540,8 @@ moe_status moe_dispatch_device_status(void* stream, uint32_t* flags);
  * given: row r reads row token[r] of x (the sorted_token of those calls), so
  * that x need not be copied into the experts' order.
  * Accuracy: codes less zero points and their products with x are exact; they
- * are summed over 32 or 64 channels by the tensor cores, scaled in fp32 and
- * added in fp32: (in / 32 + 32) 2^-23 of the sum of the products' magnitudes,
+ * are summed over 32, 64 or 128 channels by the tensor cores, scaled in fp32
+ * and added in fp32: (in / 32 + 32) 2^-23 of the sum of the products' magnitudes,
  * before SiLU and the one rounding to y_type.  A group's sum before its scale
  * has to fit fp32.  Which form adds up a call follows from its sizes. */
 #define MOE_INT4_MAX_FEATURES (1 << 20)

@@ -18,7 +18,9 @@ moe_status check_type(int type, const char* what) {
 moe_status check_pairs(int tokens, int top_k) {
     if (tokens < 0 || top_k < 1) return fail(MOE_ERR_INVALID_ARG, "tokens = %d, top_k = %d", tokens, top_k);
     if (top_k > MOE_DISPATCH_MAX_TOPK) return fail(MOE_ERR_UNSUPPORTED, "top_k (%d) is over %d", top_k, MOE_DISPATCH_MAX_TOPK);
-    if ((int64_t)tokens * top_k > INT32_MAX) return fail(MOE_ERR_UNSUPPORTED, "tokens * top_k does not fit 32 bits");
+    // a grid has a block more than there are tokens, or 65535 planes of 32768
+    if ((int64_t)tokens * top_k > MOE_DISPATCH_MAX_PAIRS)
+        return fail(MOE_ERR_UNSUPPORTED, "tokens * top_k is over %d", MOE_DISPATCH_MAX_PAIRS);
     return MOE_OK;
 }
 

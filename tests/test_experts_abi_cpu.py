@@ -84,3 +84,11 @@ def test_null_and_no_tokens(lib):
     assert lib.moe_combine(ctypes.byref(with_(moe.MoeCombineArgs, COMBINE, dict(tokens=0, y=None))), None) == 0
     assert lib.moe_combine_grad(ctypes.byref(with_(moe.MoeCombineGradArgs, GRAD, dict(tokens=0, dy=None))), None) == 0
     assert lib.moe_dispatch(ctypes.byref(with_(moe.MoeDispatchArgs, DISPATCH, dict(tokens=0, ids=None))), None, 0, None) == 0
+
+
+def test_pairs_past_the_largest_grids_are_refused(lib):
+    need = ctypes.c_size_t()
+    for tokens, k, code in [(2 ** 31 - 65536, 1, 0), (2 ** 31 - 65535, 1, 2), (2 ** 31 - 1, 1, 2), ((2 ** 31 - 65536) // 8, 8, 0), ((2 ** 31 - 65536) // 8 + 1, 8, 2)]:
+        assert lib.moe_dispatch_workspace_bytes(tokens, k, 256, ctypes.byref(need)) == code
+    for call, cls, base in ((lib.moe_combine, moe.MoeCombineArgs, COMBINE), (lib.moe_combine_grad, moe.MoeCombineGradArgs, GRAD)):
+        assert call(ctypes.byref(with_(cls, base, dict(tokens=2 ** 31 - 1, top_k=1))), None) == 2
