@@ -108,8 +108,9 @@ MOE_EXPORT moe_status moe_int4_forward(moe_int4* L, const moe_int4_args* a, void
     if (!a->y || !aligned(a->y, a->y_type == MOE_F32 ? 4 : 2)) return fail(MOE_ERR_INVALID_ARG, "y is NULL or misaligned");
     if (a->ldx < L->d.in_features) return fail(MOE_ERR_INVALID_ARG, "ldx (%lld) is less than in_features (%d)", (long long)a->ldx, L->d.in_features);
     if (a->ldy < L->d.out_features) return fail(MOE_ERR_INVALID_ARG, "ldy (%lld) is less than out_features (%d)", (long long)a->ldy, L->d.out_features);
-    // units (8 rows by a block of 16 weight rows at the least) are numbered in 32 bits
-    if (((int64_t)a->rows / 8 + L->d.n_experts) * L->blocks > INT32_MAX)
+    if (a->x_rows == 0) return fail(MOE_ERR_INVALID_ARG, "x has no rows, y has %d", a->rows);
+    // units (8 rows by a block of 16 weight rows at the least) are numbered in 32 bits, the step to a CTA's next one included
+    if (((int64_t)a->rows / 8 + L->d.n_experts) * L->blocks > INT32_MAX - 65536 || a->rows > INT32_MAX - 65536)
         return fail(MOE_ERR_UNSUPPORTED, "%d rows of %d features are too many for one call", a->rows, L->d.out_features);
     moe::Int4Call c = {};
     c.w = L->w;

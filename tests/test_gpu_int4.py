@@ -309,6 +309,14 @@ def test_largest_zero_points_and_scales_of_every_size(moe, m, k):
     check(y, *expect(x, [(code - 127) * s[:, :1].double()]))
 
 
+def test_x_without_rows_is_refused(moe):
+    lin, _ = make(moe, (), 64, 128, False, 128, False, "bf16")
+    x, y, token = (torch.zeros(64, 128, dtype=t, device="cuda") for t in (torch.bfloat16, torch.float32, torch.int32))
+    args = moe.MoeInt4Args(rows=64, x_rows=0, x=x.data_ptr(), ldx=128, token=token.data_ptr(), y=y.data_ptr(), ldy=128, y_type=moe.F32)
+    with pytest.raises(moe.MoeError):
+        moe.moe_int4_forward(lin.handle, args)
+
+
 def test_no_rows(moe):
     lin, _ = make(moe, (), 64, 128, False, 64, False, "bf16")
     lin(torch.empty(0, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(0, 64, device="cuda"))
