@@ -202,6 +202,37 @@ def test_gradients_by_differences(moe):
     assert abs((rows.double() * step.double()).sum() - (x.double() * dx.double()).sum()) <= mag * 64 * U
 
 
+@pytest.mark.parametrize("cols", [64, 33])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_past_2_to_the_31(moe, cols, dtype):
+    """Every operand's last rows start behind 2^31 elements; weights are powers of two and the sums small integers, so
+    every result is exact."""
+    t, k, e = 60, 2, 8
+    far = lambda n: torch.empty((n - 1) * (2 ** 31 // (n - 10) // 8 * 8) + cols, dtype=dtype, device="cuda").as_strided(   # noqa: E731
+        (n, cols), (2 ** 31 // (n - 10) // 8 * 8, 1))
+    g = torch.Generator(device="cuda").manual_seed(5)
+    ids = torch.randint(0, e, (t, k), generator=g, device="cuda", dtype=torch.int32)
+    value = torch.randint(-4, 5, (t, cols), generator=g, device="cuda").to(dtype)
+    w = 2.0 ** torch.randint(-2, 1, (t, k), generator=g, device="cuda").float()
+    plan = moe.ExpertPlan(t, k, e)
+    x, rows = far(t), far(t * k)
+    x.copy_(value)
+    plan.dispatch(ids, x, rows)
+    inv = plan.inv_row.long()
+    assert torch.equal(rows[inv[:, 1]], value) and torch.equal(rows[plan.inv_row[:, 0].long()], value)
+    plan.combine(rows, w, x)
+    assert torch.equal(x, (value.float() * w.sum(1, keepdim=True)).to(dtype))
+    x.copy_(value)
+    d_w = torch.empty(t, k, device="cuda")
+    plan.combine_grad(x, rows, w, rows, d_w)
+    assert torch.equal(d_w, value.float().square().sum(1, keepdim=True).expand(t, k))
+    for j in range(k):
+        assert torch.equal(rows[inv[:, j]], (value.float() * w[:, j:j + 1]).to(dtype))
+    plan.dispatch_grad(rows, x)
+    assert torch.equal(x, (value.float() * w.sum(1, keepdim=True)).to(dtype))
+    assert plan.device_status() == (0, 0)
+
+
 def test_no_tokens_and_fewer_tokens(moe):
     plan = moe.ExpertPlan(3000, 2, 5)
     for t in (3000, 513, 700, 1, 0, 2999):

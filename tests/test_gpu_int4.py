@@ -184,6 +184,52 @@ def test_image_past_4_gib(moe):
         check(y, *expect(x, [(code - 8) * float(s[0, 0, 0])]))
 
 
+def far_rows(rows, cols, dtype, pad=0):
+    """Rows so far apart that the last start behind 2^31 elements."""
+    ld = 2 ** 31 // (rows - 40) + pad
+    ld -= 0 if pad else ld % 8
+    return torch.empty(ld * (rows - 1) + cols, dtype=dtype, device="cuda").as_strided((rows, cols), (ld, 1))
+
+
+@pytest.mark.parametrize("m", [50, 300])
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("gather", [False, True])
+def test_rows_past_2_to_the_31(moe, m, pad, gather):
+    n, k = 72, 200
+    lin, mats = make(moe, (), n, k, False, 64, True, "bf16")
+    x, y = far_rows(m, k, torch.bfloat16, pad), far_rows(m, n, torch.bfloat16)
+    x.copy_(torch.randn(m, k, generator=gen(1), device="cuda"))
+    y.fill_(7)
+    if gather:
+        token = torch.arange(m - 1, -1, -1, dtype=torch.int32, device="cuda")
+        lin(x, y, None, token)
+        check(y, *expect(x.flip(0), mats))
+    else:
+        lin(x, y)
+        check(y, *expect(x, mats))
+
+
+@pytest.mark.parametrize("m,n,k,gated,group", [(3, 700, 2048, True, 32), (64, 512, 4096, False, 128), (200, 1000, 1024, True, 64), (1200, 2048, 512, False, 32)])
+def test_two_streams_share_the_weights(moe, m, n, k, gated, group):
+    lin, mats = make(moe, (), n, k, gated, group, False, "bf16")
+    xs = [torch.randn(m, k, generator=gen(i), device="cuda").bfloat16() for i in range(2)]
+    want = [torch.empty(m, n, device="cuda") for _ in xs]
+    for x, y in zip(xs, want):
+        lin(x, y)
+        check(y, *expect(x, mats))
+    runs = 8
+    got = [[torch.empty(m, n, device="cuda") for _ in range(runs)] for _ in xs]
+    side = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for i in range(runs):
+        for j, st in enumerate(side):
+            with torch.cuda.stream(st):
+                lin(xs[j], got[j][i])
+    torch.cuda.synchronize()
+    assert lin.device_status() == (0, 0)
+    assert all(torch.equal(y, want[j]) for j in range(2) for y in got[j])
+
+
 @pytest.mark.parametrize("rows", [4, 300])
 def test_bad_offsets_and_tokens_stay_in_bounds_and_are_flagged(moe, rows):
     e, n, k = 4, 64, 128
